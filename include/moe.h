@@ -68,6 +68,8 @@ typedef enum {
 #define MOE_DEV_RANGE 32         /* a router partial sum of the persistent     */
                                  /* decode kernel beyond +-2^21 (clamped: that */
                                  /* token's routing is not exact)              */
+#define MOE_DEV_BAD_OFFSETS 64   /* segment offsets descending or outside [0, R]: */
+                                 /* those segments are left out                */
 
 /* activation dtypes */
 typedef enum { MOE_DT_F32 = 0, MOE_DT_BF16 = 1 } moe_dtype;
@@ -78,6 +80,7 @@ typedef enum { MOE_DT_F32 = 0, MOE_DT_BF16 = 1 } moe_dtype;
 #define MOE_MAX_B 1024
 #define MOE_MAX_DIM 16384
 #define MOE_MAX_LAYERS 64
+#define MOE_MAX_ROWS (1 << 22) /* rows of the grouped products and of a quantised matrix list */
 
 /* flags for moe_expert_forward / moe_layer_forward / moe_stack_forward */
 #define MOE_F_NO_DEDUP 1u   /* evaluate every route on its own (each route re-reads
@@ -307,6 +310,86 @@ int moe_stack_forward_nvfp4(int L, const uint16_t* const* w_router, const float*
                             const uint8_t* const* down_bs, const float* const* down_gs, int B, int H, int I, int E,
                             int top_k, float* x_inout, int32_t* expert_ids_out, uint32_t flags, void* workspace,
                             size_t workspace_bytes, int32_t* dev_status, void* stream);
+
+/*
+ * moe_grouped_gemm -- rows grouped by expert times their expert's matrix:
+ *   y[r, n] = sum_k w[e, n, k] x[r, k]   for offsets[e] <= r < offsets[e+1],
+ * the segments any number of rows each, none included.  The offsets are
+ * those of moe_group_by_expert (x holds the routes' rows in the order of
+ * route_idx) or any ascending ones; they are read on the device.
+ * In:  x [R, K] bf16, w [E, N, K] bf16, offsets [E+1] int32.
+ * Out: y [R, N] fp32 or bf16 (y_dtype), sums in fp32, one rounding to bf16.
+ *      Rows that no segment holds (before offsets[0], from offsets[E] on)
+ *      are left as they were.
+ * 0 <= R <= MOE_MAX_ROWS, 1 <= E <= MOE_MAX_E, K a multiple of 8 in
+ * [8, MOE_MAX_DIM], N one in [8, 2 MOE_MAX_DIM].  Offsets that descend or
+ * leave [0, R] set MOE_DEV_BAD_OFFSETS and their segment is left out.  A
+ * NaN or infinity reaches the outputs of its own row (in w: of its own
+ * expert) alone.  y must not overlap an input.  Needs no workspace.
+ */
+int moe_grouped_gemm(const uint16_t* x, const uint16_t* w, const int32_t* offsets, int R, int N, int K, int E, void* y,
+                     int y_dtype, int32_t* dev_status, void* stream);
+
+/*
+ * moe_grouped_gemm_dx -- the gradient of moe_grouped_gemm with respect to x:
+ *   dx[r, k] = sum_n w[e, n, k] dy[r, n]
+ * dy [R, N] bf16; dx [R, K] fp32 or bf16 (dx_dtype).  Otherwise as
+ * moe_grouped_gemm.
+ */
+int moe_grouped_gemm_dx(const uint16_t* dy, const uint16_t* w, const int32_t* offsets, int R, int N, int K, int E,
+                        void* dx, int dx_dtype, int32_t* dev_status, void* stream);
+
+/*
+ * moe_grouped_gemm_dw -- the gradient with respect to the weights:
+ *   dw[e, n, k] = sum over the segment's rows r of dy[r, n] x[r, k]
+ * dy [R, N] and x [R, K] bf16; dw [E, N, K] fp32 or bf16 (dw_dtype), every
+ * element written (zeros for an expert without rows).  Otherwise as
+ * moe_grouped_gemm.  The sums' order is fixed: no atomics.
+ */
+int moe_grouped_gemm_dw(const uint16_t* dy, const uint16_t* x, const int32_t* offsets, int R, int N, int K, int E,
+                        void* dw, int dw_dtype, int32_t* dev_status, void* stream);
+
+/*
+ * moe_quantize_nvfp4 -- matrices into the NVFP4 layout of
+ * moe_stack_forward_nvfp4: x [G, rows, cols] fp32 or bf16 (x_dtype) into
+ * q [G, rows, cols/2] (E2M1 codes two a byte, element 2i in the low nibble),
+ * bs [G, rows, cols/16] (E4M3) and gs [G] fp32, with a = max |x| of a matrix:
+ *   gs = a / 2688 rounded up to 8 significant bits, in [2^-100, 2688 gs finite]
+ *   bs = E4M3 nearest to (max |x| of the 16 elements) / (6 gs)
+ *   q  = E2M1 nearest to x / (bs gs), at most 6 in magnitude, x's sign kept
+ * both ties to even; the results are those of exact arithmetic.  rows = 1
+ * gives each row of an activation matrix [G, cols] a scale of its own.
+ * A block with a NaN or an infinity sets MOE_DEV_NONFINITE and decodes to
+ * NaN throughout; other blocks are not affected (such elements do not enter
+ * a).  cols a multiple of 32 in [32, MOE_MAX_DIM], rows <= 2 MOE_MAX_DIM;
+ * G <= MOE_MAX_ROWS for rows = 1, 65535 otherwise; x 32-byte aligned.
+ * workspace: moe_quantize_nvfp4_workspace_bytes() (0 for rows = 1).
+ */
+int moe_quantize_nvfp4_workspace_bytes(int G, int rows, int cols, size_t* bytes);
+int moe_quantize_nvfp4(const void* x, int x_dtype, int G, int rows, int cols, uint8_t* q, uint8_t* bs, float* gs,
+                       void* workspace, size_t workspace_bytes, int32_t* dev_status, void* stream);
+
+/*
+ * moe_dequantize_nvfp4 -- the values of NVFP4 matrices: x [G, rows, cols]
+ * fp32 or bf16 = (e2m1(q) e4m3(bs)) gs, the first product exact, the second
+ * rounded to fp32 and then to x's type.  Shapes as moe_quantize_nvfp4 (any
+ * codes and scales are taken); x 32-byte aligned.
+ */
+int moe_dequantize_nvfp4(const uint8_t* q, const uint8_t* bs, const float* gs, int G, int rows, int cols, void* x,
+                         int x_dtype, void* stream);
+
+/*
+ * moe_grouped_gemm_nvfp4 -- moe_grouped_gemm with both operands in NVFP4, on
+ * the block-scaled tensor cores:
+ *   y[r, n] = (sum_k (e2m1 e4m3)(x[r, k]) (e2m1 e4m3)(w[e, n, k])) xgs[r] wgs[e]
+ * xq [R, K/2], xbs [R, K/16], xgs [R]: activations with a scale a row;
+ * wq [E, N, K/2], wbs [E, N, K/16], wgs [E]: weights with a scale a matrix
+ * (block scales are taken as unsigned E4M3: the sign bit must be clear).
+ * K a multiple of 32.  Otherwise as moe_grouped_gemm; sums in fp32.
+ */
+int moe_grouped_gemm_nvfp4(const uint8_t* xq, const uint8_t* xbs, const float* xgs, const uint8_t* wq, const uint8_t* wbs,
+                           const float* wgs, const int32_t* offsets, int R, int N, int K, int E, void* y, int y_dtype,
+                           int32_t* dev_status, void* stream);
 
 /*
  * moe_workspace_grouping -- where a workspace holds the grouped route list

@@ -43,6 +43,13 @@ _lib.moe_stack_forward_nvfp4.argtypes = [_I, _P, _P, _P, _P, _P, _P, _P, _P, _I,
                                          _S, _P, _P]
 _lib.moe_stack_forward_norm.argtypes = [_I, _P, _P, _P, _P, _P, ctypes.c_float, _I, _I, _I, _I, _I, _P, _P, _U,
                                         _P, _S, _P, _P]
+_lib.moe_grouped_gemm.argtypes = [_P, _P, _P, _I, _I, _I, _I, _P, _I, _P, _P]
+_lib.moe_grouped_gemm_dx.argtypes = [_P, _P, _P, _I, _I, _I, _I, _P, _I, _P, _P]
+_lib.moe_grouped_gemm_dw.argtypes = [_P, _P, _P, _I, _I, _I, _I, _P, _I, _P, _P]
+_lib.moe_quantize_nvfp4_workspace_bytes.argtypes = [_I, _I, _I, ctypes.POINTER(_S)]
+_lib.moe_quantize_nvfp4.argtypes = [_P, _I, _I, _I, _I, _P, _P, _P, _P, _S, _P, _P]
+_lib.moe_dequantize_nvfp4.argtypes = [_P, _P, _P, _I, _I, _I, _P, _I, _P]
+_lib.moe_grouped_gemm_nvfp4.argtypes = [_P, _P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _P, _I, _P, _P]
 _lib.moe_workspace_grouping.argtypes = [_P, _S, _I, _I, _I, _I, _I, ctypes.POINTER(_P), ctypes.POINTER(_P),
                                         ctypes.POINTER(_P), ctypes.POINTER(_P)]
 _lib.moe_forward_path.argtypes = [_I, _I, _I, _I, _I, _I, _U, ctypes.POINTER(_I), ctypes.POINTER(_I)]
@@ -57,12 +64,16 @@ _lib.moe_status_string.argtypes = [_I]
 _lib.moe_status_string.restype = ctypes.c_char_p
 for _f in ("moe_workspace_bytes", "moe_route", "moe_group_by_expert", "moe_expert_forward",
            "moe_expert_forward_noalloc", "moe_layer_forward", "moe_stack_forward", "moe_stack_forward_norm",
-           "moe_stack_forward_fp8", "moe_stack_forward_nvfp4", "moe_workspace_grouping"):
+           "moe_stack_forward_fp8", "moe_stack_forward_nvfp4", "moe_workspace_grouping", "moe_grouped_gemm",
+           "moe_grouped_gemm_dx", "moe_grouped_gemm_dw", "moe_quantize_nvfp4_workspace_bytes", "moe_quantize_nvfp4",
+           "moe_dequantize_nvfp4", "moe_grouped_gemm_nvfp4"):
     getattr(_lib, _f).restype = ctypes.c_int
 
 EXPORTED = ("moe_workspace_bytes", "moe_route", "moe_group_by_expert", "moe_expert_forward",
             "moe_expert_forward_noalloc", "moe_layer_forward", "moe_stack_forward", "moe_stack_forward_norm",
             "moe_stack_forward_fp8", "moe_stack_forward_nvfp4", "moe_workspace_grouping",
+            "moe_grouped_gemm", "moe_grouped_gemm_dx", "moe_grouped_gemm_dw", "moe_quantize_nvfp4_workspace_bytes",
+            "moe_quantize_nvfp4", "moe_dequantize_nvfp4", "moe_grouped_gemm_nvfp4",
             "moe_launch_count", "moe_forward_path", "moe_set_trace_buffer",
             "moe_inject_barrier_stall", "moe_status_string")
 
@@ -77,6 +88,7 @@ MOE_DEV_DUP_EXPERT = 4
 MOE_DEV_NONFINITE = 8
 MOE_DEV_BAD_ROUTE = 16
 MOE_DEV_RANGE = 32
+MOE_DEV_BAD_OFFSETS = 64
 MOE_DT_F32 = 0
 MOE_DT_BF16 = 1
 MOE_F_NO_DEDUP = 1
@@ -88,6 +100,7 @@ MOE_F_HOT_L2 = 32
 MOE_F_SPLIT_TC = 64
 TC_MIN_ROUTES = 8
 MAX_E, MAX_TOPK, MAX_B, MAX_DIM, MAX_LAYERS = 256, 8, 1024, 16384, 64
+MAX_ROWS = 1 << 22
 NOALLOC_SCRATCH_BYTES = 16 << 20
 
 
@@ -589,3 +602,177 @@ def stack_forward(x, layers, top_k, flags=0, stream=None, status=None):
     ids = torch.empty((st.L, x.shape[0], top_k), dtype=torch.int32, device=x.device)
     stack_forward_(xo, st, top_k, flags=flags, ids_out=ids, status=status, stream=stream)
     return xo, ids
+
+
+# ------------------------------------------------- grouped products and NVFP4
+_OUT = {torch.float32: MOE_DT_F32, torch.bfloat16: MOE_DT_BF16}
+
+
+def _on(dev, stream):
+    """The context of an operator call: x's device current, and the stream the
+    kernels go to (torch allocates the outputs for it)."""
+    if stream is not None and stream.device != dev:
+        raise ValueError(f"stream is on {stream.device}, x on {dev}")
+    return torch.cuda.stream(stream if stream is not None else torch.cuda.current_stream(dev))
+
+
+def _need_2d(t, dtype, name, what):
+    if t.dim() != 2:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {what}")
+    _need(t, dtype, name)
+
+
+def _out(out, shape, out_dtype, dev):
+    """The output tensor of an operator call: `out`, or a new one."""
+    if out is None:
+        if out_dtype not in _OUT:
+            raise TypeError("out_dtype must be float32 or bfloat16")
+        return torch.empty(shape, dtype=out_dtype, device=dev)
+    _shape(out, shape, "out")
+    if out.dtype not in _OUT:
+        raise TypeError("out must be float32 or bfloat16")
+    _opt(out, None, "out", dev)
+    return out
+
+
+def _grouped(fn, a, b, offsets, R, N, K, E, shape, out_dtype, out, status, stream):
+    dev = a.device
+    _shape(offsets, (E + 1,), "offsets")
+    _shape(status, (1,), "status")
+    _opt(b, torch.bfloat16, "the second operand", dev)
+    _opt(offsets, torch.int32, "offsets", dev)
+    _opt(status, torch.int32, "status", dev)
+    with _on(dev, stream):
+        y = _out(out, shape, out_dtype, dev)
+        _check(getattr(_lib, fn)(_ptr(a), _ptr(b), _ptr(offsets), R, N, K, E, _ptr(y), _OUT[y.dtype], _ptr(status),
+                                 _stream(stream)), fn)
+    return y
+
+
+def grouped_gemm(x, w, offsets, out_dtype=torch.float32, out=None, status=None, stream=None):
+    """y [R,N]: row r of segment e (offsets[e] <= r < offsets[e+1]) is w[e] x[r].
+
+    x [R,K] bf16, w [E,N,K] bf16, offsets [E+1] int32 on the device (as
+    group_by_expert returns them).  Rows that no segment holds are left as
+    they were in `out`, and are undefined in a new tensor."""
+    _need_2d(x, torch.bfloat16, "x", "[R, K]")
+    R, K = x.shape
+    _shape(w, (None, None, K), "w")
+    E, N, _ = w.shape
+    return _grouped("moe_grouped_gemm", x, w, offsets, R, N, K, E, (R, N), out_dtype, out, status, stream)
+
+
+def grouped_gemm_dx(dy, w, offsets, out_dtype=torch.float32, out=None, status=None, stream=None):
+    """dx [R,K]: the gradient of grouped_gemm with respect to x, row r of
+    segment e being w[e]^T dy[r]; dy [R,N] bf16, w [E,N,K] bf16."""
+    _need_2d(dy, torch.bfloat16, "dy", "[R, N]")
+    R, N = dy.shape
+    _shape(w, (None, N, None), "w")
+    E, _, K = w.shape
+    return _grouped("moe_grouped_gemm_dx", dy, w, offsets, R, N, K, E, (R, K), out_dtype, out, status, stream)
+
+
+def grouped_gemm_dw(dy, x, offsets, out_dtype=torch.float32, out=None, status=None, stream=None):
+    """dw [E,N,K]: the gradient of grouped_gemm with respect to w, the sum of
+    dy[r] x[r]^T over segment e's rows (zeros where it has none); dy [R,N]
+    bf16, x [R,K] bf16, E = len(offsets) - 1."""
+    _need_2d(dy, torch.bfloat16, "dy", "[R, N]")
+    R, N = dy.shape
+    _shape(x, (R, None), "x")
+    K = x.shape[1]
+    E = offsets.numel() - 1
+    return _grouped("moe_grouped_gemm_dw", dy, x, offsets, R, N, K, E, (E, N, K), out_dtype, out, status, stream)
+
+
+def _nvfp4_shape(t):
+    if t.dim() not in (2, 3):
+        raise ValueError(f"x has shape {tuple(t.shape)}, expected [R, C] (a scale a row) or [G, R, C] (a scale a matrix)")
+    return (t.shape[0], 1, t.shape[1]) if t.dim() == 2 else tuple(t.shape)
+
+
+def quantize_nvfp4(x, out=None, workspace=None, status=None, stream=None):
+    """-> (q, bs, gs): x in NVFP4, E2M1 codes two a byte [..., C/2] uint8, an
+    E4M3 scale per 16 elements [..., C/16] uint8 and fp32 scales.
+
+    x fp32 or bf16: [G,R,C] matrices with one scale each (gs [G], the layout
+    of stack_forward_nvfp4_), or [R,C] rows with one scale each (gs [R]).
+    `out` is such a triple to be written."""
+    _x_dtype(x)
+    G, rows, cols = _nvfp4_shape(x)
+    if not x.is_cuda or not x.is_contiguous():
+        raise ValueError("x must be a contiguous CUDA tensor")
+    if cols % 32:
+        raise ValueError(f"NVFP4 rows need a multiple of 32 elements, x has {cols}")
+    dev, lead = x.device, tuple(x.shape[:-1])
+    _shape(status, (1,), "status")
+    _opt(status, torch.int32, "status", dev)
+    _opt(workspace, torch.uint8, "workspace", dev)
+    if out is not None:
+        for t, shp, dt, n in zip(out, ((*lead, cols // 2), (*lead, cols // 16), (G,)),
+                                 (torch.uint8, torch.uint8, torch.float32), ("out q", "out bs", "out gs")):
+            _shape(t, shp, n)
+            _opt(t, dt, n, dev)
+    with _on(dev, stream):
+        if out is None:
+            out = (torch.empty((*lead, cols // 2), dtype=torch.uint8, device=dev),
+                   torch.empty((*lead, cols // 16), dtype=torch.uint8, device=dev),
+                   torch.empty((G,), dtype=torch.float32, device=dev))
+        q, bs, gs = out
+        if workspace is None and rows > 1:
+            n = _S(0)
+            _check(_lib.moe_quantize_nvfp4_workspace_bytes(G, rows, cols, ctypes.byref(n)),
+                   "moe_quantize_nvfp4_workspace_bytes")
+            workspace = torch.empty(n.value, dtype=torch.uint8, device=dev)
+        _check(_lib.moe_quantize_nvfp4(_ptr(x), _x_dtype(x), G, rows, cols, _ptr(q), _ptr(bs), _ptr(gs),
+                                       _ptr(workspace), workspace.numel() if workspace is not None else 0,
+                                       _ptr(status), _stream(stream)), "moe_quantize_nvfp4")
+    return q, bs, gs
+
+
+def _need_nvfp4(q, bs, gs, name):
+    """Shape checks of an NVFP4 triple -> its elements a row."""
+    _need(q, torch.uint8, f"{name} codes")
+    cols = 2 * q.shape[-1]
+    if cols % 32:
+        raise ValueError(f"NVFP4 rows need a multiple of 32 elements, {name} has {cols}")
+    _shape(bs, (*q.shape[:-1], cols // 16), f"{name} block scales")
+    _shape(gs, (q.shape[0],), f"{name} scales")
+    _opt(bs, torch.uint8, f"{name} block scales", q.device)
+    _opt(gs, torch.float32, f"{name} scales", q.device)
+    return cols
+
+
+def dequantize_nvfp4(q, bs, gs, out_dtype=torch.float32, out=None, stream=None):
+    """The values of quantize_nvfp4's triple: (e2m1(q) * e4m3(bs)) * gs."""
+    G, rows, _ = _nvfp4_shape(q)
+    cols = _need_nvfp4(q, bs, gs, "x")
+    dev = q.device
+    with _on(dev, stream):
+        x = _out(out, (*q.shape[:-1], cols), out_dtype, dev)
+        _check(_lib.moe_dequantize_nvfp4(_ptr(q), _ptr(bs), _ptr(gs), G, rows, cols, _ptr(x), _OUT[x.dtype],
+                                         _stream(stream)), "moe_dequantize_nvfp4")
+    return x
+
+
+def grouped_gemm_nvfp4(xq, xbs, xgs, wq, wbs, wgs, offsets, out_dtype=torch.float32, out=None, status=None,
+                       stream=None):
+    """grouped_gemm with both operands in NVFP4: x as quantize_nvfp4 returns a
+    [R,K] tensor (a scale a row), w as it returns [E,N,K] (a scale a matrix)."""
+    if xq.dim() != 2 or wq.dim() != 3:
+        raise ValueError(f"xq {tuple(xq.shape)} and wq {tuple(wq.shape)} must be [R, K/2] and [E, N, K/2]")
+    _shape(wq, (None, None, xq.shape[1]), "wq")
+    K = _need_nvfp4(xq, xbs, xgs, "x")
+    _need_nvfp4(wq, wbs, wgs, "w")
+    R, (E, N, _) = xq.shape[0], wq.shape
+    dev = xq.device
+    _opt(wq, torch.uint8, "wq", dev)
+    _shape(offsets, (E + 1,), "offsets")
+    _shape(status, (1,), "status")
+    _opt(offsets, torch.int32, "offsets", dev)
+    _opt(status, torch.int32, "status", dev)
+    with _on(dev, stream):
+        y = _out(out, (R, N), out_dtype, dev)
+        _check(_lib.moe_grouped_gemm_nvfp4(_ptr(xq), _ptr(xbs), _ptr(xgs), _ptr(wq), _ptr(wbs), _ptr(wgs),
+                                           _ptr(offsets), R, N, K, E, _ptr(y), _OUT[y.dtype], _ptr(status),
+                                           _stream(stream)), "moe_grouped_gemm_nvfp4")
+    return y

@@ -1,10 +1,11 @@
-"""Build libmoe.so in-tree with nvcc for sm_103a (no cmake, one translation unit)."""
+"""Build libmoe.so in-tree with nvcc for sm_103a (no cmake; the translation units compile in parallel)."""
 from __future__ import annotations
 
 import glob
 import os
 import subprocess
 import sys
+import tempfile
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -35,16 +36,25 @@ def build(force: bool = False, verbose: bool = False) -> str:
     if not force and up_to_date():
         return LIB
     tmp = LIB + f".tmp{os.getpid()}"
-    cmd = [nvcc_path(), *ARCH, "-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-shared",
-           "-I" + INCLUDE, os.path.join(CSRC, "moe_api.cu"), "-o", tmp]
+    flags = [nvcc_path(), *ARCH, "-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-I" + INCLUDE]
     if verbose:
-        cmd.insert(1, "-Xptxas=-v")
-    r = subprocess.run(cmd, capture_output=True, text=True)
-    if r.returncode != 0:
-        sys.stderr.write(r.stdout + r.stderr)
-        raise RuntimeError("nvcc failed building libmoe.so")
+        flags.insert(1, "-Xptxas=-v")
+    with tempfile.TemporaryDirectory(dir=PKG, prefix="_build") as d:
+        units = [(src, os.path.join(d, os.path.basename(src)[:-3] + ".o"))
+                 for src in sorted(glob.glob(os.path.join(CSRC, "*.cu")))]
+        jobs = [subprocess.Popen([*flags, "-c", src, "-o", obj], stdout=subprocess.PIPE, stderr=subprocess.STDOUT,
+                                 text=True) for src, obj in units]
+        logs = [j.communicate()[0] for j in jobs]
+        if any(j.returncode for j in jobs):
+            sys.stderr.write("".join(logs))
+            raise RuntimeError("nvcc failed building libmoe.so")
+        r = subprocess.run([nvcc_path(), *ARCH, "-shared", *[obj for _, obj in units], "-o", tmp],
+                           capture_output=True, text=True)
+        if r.returncode != 0:
+            sys.stderr.write(r.stdout + r.stderr)
+            raise RuntimeError("nvcc failed linking libmoe.so")
     if verbose:
-        sys.stderr.write(r.stderr)
+        sys.stderr.write("".join(logs))
     os.replace(tmp, LIB)
     return LIB
 

@@ -10,11 +10,11 @@
 #include <stdint.h>
 #include <string.h>
 
-#include <atomic>
 #include <mutex>
 
 #include "moe.h"
 #include "moe_common.cuh"
+#include "moe_host.cuh"
 #include "moe_phases.cuh"
 #include "moe_decode.cuh"
 #include "moe_tc.cuh"
@@ -200,7 +200,6 @@ __global__ void __launch_bounds__(kThreads) fused_kernel(Ctx c, StackArgs sa, un
 }
 
 // -------------------------------------------------------------- host side
-static size_t align_up(size_t v, size_t a) { return (v + a - 1) / a * a; }
 
 constexpr unsigned kAllFlags =
     MOE_F_NO_DEDUP | MOE_F_UNFUSED | MOE_F_FORCE_TC | MOE_F_NO_TC | MOE_F_NO_PREFETCH | MOE_F_HOT_L2 | MOE_F_SPLIT_TC;
@@ -249,7 +248,6 @@ static WsLayout ws_layout(int B, int H, int I, int E, int k) {
     return L;
 }
 
-static bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
 static int check_dims(int B, int H, int I, int E, int k, bool need_I) {
     if (B < 0 || B > MOE_MAX_B) return MOE_ERR_INVALID_ARG;
@@ -259,15 +257,6 @@ static int check_dims(int B, int H, int I, int E, int k, bool need_I) {
     if (need_I && (I < 8 || I > MOE_MAX_DIM || (I & 7))) return MOE_ERR_INVALID_ARG;
     return MOE_OK;
 }
-
-#define MOE_REQ(p) \
-    do {           \
-        if (!(p) || !aligned16(p)) return MOE_ERR_INVALID_ARG; \
-    } while (0)
-#define MOE_OPT(p) \
-    do {           \
-        if ((p) && !aligned16(p)) return MOE_ERR_INVALID_ARG; \
-    } while (0)
 
 static int nt_max_for(int H, int I) {
     const int dim = H > I ? H : I;
@@ -287,48 +276,6 @@ static size_t fused_smem(int B, int H, int I, int E) {
     const size_t g = group_smem_bytes(B, E);
     if (g > s) s = g;
     return align_up(s, 16);
-}
-
-static int to_status(cudaError_t e) {
-    if (e == cudaSuccess) return MOE_OK;
-    return MOE_ERR_CUDA;
-}
-
-// Kernels this library has launched in the process (every launch site goes
-// through launch_ex or launch_pdl), for measurement: moe_launch_count().
-static std::atomic<unsigned long long> g_launches{0};
-
-template <typename K, typename... Args>
-static int launch_ex(const cudaLaunchConfig_t& cfg, K kernel, Args... args) {
-    g_launches.fetch_add(1, std::memory_order_relaxed);
-    return to_status(cudaLaunchKernelEx(&cfg, kernel, args...));
-}
-
-// A launch that may start while the kernel ahead of it on the stream is
-// finishing (programmatic stream serialization): the kernel's setup overlaps
-// the previous kernel's tail; its first read of earlier results waits in
-// grid_dep_wait().  Used for the chain of phase kernels of one layer.
-template <typename K, typename... Args>
-static int launch_pdl(K kernel, dim3 grid, dim3 block, size_t smem, cudaStream_t st, Args... args) {
-    cudaLaunchConfig_t cfg;
-    memset(&cfg, 0, sizeof cfg);
-    cfg.gridDim = grid;
-    cfg.blockDim = block;
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = st;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    return launch_ex(cfg, kernel, args...);
-}
-
-// dynamic shared memory above 48 KB needs an opt-in per kernel and device
-template <typename K>
-static int allow_smem(K kernel, size_t bytes) {
-    if (bytes <= 48 * 1024) return MOE_OK;
-    return to_status(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes));
 }
 
 static int tc_threshold_for(unsigned flags, int H, int I);
@@ -395,28 +342,6 @@ static int launch_group(const int32_t* ids, int B, int k, int E, int32_t* offset
                       status);
 }
 
-
-static int sm_count();
-
-// ------------------------------------------------------- tensor-core path
-typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
-                                  const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
-                                  CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-// The driver's tensor-map encoder, looked up once (a function-local static
-// is initialised exactly once even when several host threads call first).
-static EncodeTiledFn encode_fn() {
-    static const EncodeTiledFn fn = []() -> EncodeTiledFn {
-        void* f = nullptr;
-        cudaDriverEntryPointQueryResult q;
-        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &q) ==
-                cudaSuccess &&
-            q == cudaDriverEntryPointSuccess)
-            return reinterpret_cast<EncodeTiledFn>(f);
-        return nullptr;
-    }();
-    return fn;
-}
 
 // 2-D bf16 tensor [rows, inner] (row-major), 128-byte swizzled boxes of
 // {64, box_rows}; rows beyond the tensor read as zeros.
@@ -610,13 +535,6 @@ static int launch_unfused_layer(const Ctx& c, cudaStream_t st, char* ws, const W
     rc = launch_group(c.ids, c.B, c.k, c.E, c.offsets, c.route_idx, c.unique, c.num_unique, c.status, st);
     if (rc) return rc;
     return launch_experts(c, st, ws, &L);
-}
-
-static int sm_count() {
-    int dev = 0, n = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess) return 0;
-    if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 0;
-    return n;
 }
 
 static int launch_fused(const Ctx& c, const StackArgs& sa, unsigned* bar, cudaStream_t st) {
@@ -1324,6 +1242,7 @@ const char* moe_status_string(int code) {
         case MOE_DEV_NONFINITE: return "device: non-finite router logit";
         case MOE_DEV_BAD_ROUTE: return "device: route index outside [0, B*top_k)";
         case MOE_DEV_RANGE: return "device: router partial sum beyond the fixed-point range (+-2^21)";
+        case MOE_DEV_BAD_OFFSETS: return "device: segment offsets descending or outside [0, R]";
         default: return "unknown status";
     }
 }

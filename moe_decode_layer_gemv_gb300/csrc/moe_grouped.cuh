@@ -1,0 +1,582 @@
+// moe_grouped.cuh -- matrix products grouped by expert with ragged segments,
+// bf16 operands, fp32 accumulation (tcgen05, TMA, tensor memory).
+//
+// Segment e holds the rows offsets[e] .. offsets[e+1]-1 of x [R, K] and
+// dy [R, N]; w is [E, N, K].  Three products share one kernel:
+//   forward  y[r, n]     = sum_k w[e, n, k] x[r, k]
+//   dx       dx[r, k]    = sum_n w[e, n, k] dy[r, n]
+//   dw       dw[e, n, k] = sum_r dy[r, n] x[r, k]   (r over the segment)
+// Each is computed as tiles D[m, n] whose m (the tensor-memory lanes) is the
+// output's contiguous dimension, so that a warp's stores are contiguous, and
+// whose n is the segment's rows (forward, dx) or the weight's rows (dw):
+//   forward  A = w   (m = n-index of w; contraction k contiguous: K-major)
+//            B = x   (K-major)
+//   dx       A = w   (m = k; contraction over w's rows: MN-major), B = dy (K-major)
+//   dw       A = x   (m = k; contraction over rows: MN-major), B = dy (MN-major)
+// The segments are read on the device: no launch depends on their sizes.
+#pragma once
+
+#include "moe_common.cuh"
+#include "moe_ptx.cuh"
+#include "moe_umma.cuh"
+
+namespace moe {
+
+enum { kGgFwd = 0, kGgDx = 1, kGgDw = 2 };
+
+constexpr int kGgThreads = 192;      // warps 0-3 epilogue, warp 4 TMA producer, warp 5 MMA issuer
+constexpr int kGgMaxStages = 12;
+constexpr int kGgBoxN = 32;          // rows per TMA box of a K-major B operand
+constexpr int kGgTile = 128 * 128;   // bytes of one 128 x 64 bf16 operand tile
+constexpr int kGgSmem = 227 * 1024;
+constexpr uint32_t kGgWaitLimit = 1u << 22;
+constexpr uint32_t kGgTmemCols = 512;
+
+struct GgParams {
+    CUtensorMap ta, tb;
+    const int32_t* offsets;  // [E + 1]
+    int E, R;
+    int M;     // extent of the output's contiguous dimension
+    int C;     // contraction length (forward, dx)
+    int NW;    // dw: rows of a weight matrix
+    void* out;
+    int out_f32;
+    int32_t* status;
+};
+
+// CG CTAs (a cluster) work on one tile: with CG = 2 each holds 128 of the
+// tile's 256 m and half of its n, and one tcgen05.mma.cta_group::2 reads both
+// CTAs' shared memory.  KSUB 64-wide contraction steps fill one stage.
+template <int MODE, int CG>
+struct GgCfg {
+    static constexpr int BM = 128 * CG;
+    static constexpr int BN = 128 * CG;
+    static constexpr int KSUB = (CG == 1 && MODE != kGgDw) ? 2 : 1;
+};
+
+struct GgShared {
+    uint64_t full[kGgMaxStages];    // this CTA's tiles of a stage landed
+    uint64_t pfull[kGgMaxStages];   // CG = 2, leader: the other CTA's tiles landed
+    uint64_t empty[kGgMaxStages];   // the MMAs have read a stage
+    uint64_t acc_full[2];           // an accumulator's MMAs are complete
+    uint64_t acc_empty[2];          // leader: the epilogue warps (of both CTAs) have read an accumulator
+    uint64_t mma_done;
+    uint32_t tmem_slot;
+    int abort;                      // a bounded wait ran out
+    int nmax;                       // rows of the largest segment
+    int p0[MOE_MAX_E], cnt[MOE_MAX_E];
+    int start[MOE_MAX_E + 1];       // first tile of each segment (forward, dx)
+};
+static_assert(sizeof(GgShared) <= 4096, "control block");
+
+// ------------------------------------------------------------ PTX wrappers
+__device__ __forceinline__ void tma_load_3d(void* dst, const CUtensorMap* map, int c0, int c1, int c2, uint64_t* bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(
+            smem_u32(dst)),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(smem_u32(bar))
+        : "memory");
+}
+
+__device__ __forceinline__ uint32_t cluster_rank() {
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+
+__device__ __forceinline__ void cluster_sync() {
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
+// Arrive on the barrier at the same place in CTA `rank` of the cluster.
+__device__ __forceinline__ void mbar_arrive_cluster(uint64_t* bar, uint32_t rank) {
+    asm volatile(
+        "{\n\t.reg .b32 ra;\n\t"
+        "mapa.shared::cluster.u32 ra, %0, %1;\n\t"
+        "mbarrier.arrive.release.cluster.shared::cluster.b64 _, [ra];\n\t}" ::"r"(smem_u32(bar)),
+        "r"(rank)
+        : "memory");
+}
+
+__device__ __forceinline__ bool mbar_try_wait_cluster(uint64_t* bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(smem_u32(bar)), "r"(parity)
+        : "memory");
+    return ok != 0;
+}
+
+// MN-major operand, 128-byte swizzle: 64 elements (128 bytes) of the M or N
+// dimension per contraction row, 8-row groups 1024 bytes apart (stride byte
+// offset), 64-element blocks of M or N `lbo` bytes apart (leading byte offset).
+__device__ __forceinline__ uint64_t umma_sdesc_mn(uint32_t saddr, uint32_t lbo) {
+    uint64_t d = 0;
+    d |= (uint64_t)((saddr & 0x3FFFFu) >> 4);
+    d |= (uint64_t)(lbo >> 4) << 16;
+    d |= (uint64_t)(1024 >> 4) << 32;
+    d |= (uint64_t)1 << 46;
+    d |= (uint64_t)2 << 61;
+    return d;
+}
+
+template <int CG>
+__device__ __forceinline__ void gg_mma(uint32_t tmem_d, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
+                                       uint32_t accumulate) {
+    if (CG == 1)
+        umma_bf16(tmem_d, adesc, bdesc, idesc, accumulate);
+    else
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "setp.ne.b32 p, %4, 0;\n\t"
+            "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(tmem_d),
+            "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
+            : "memory");
+}
+
+// Arrive on `bar` (with CG = 2: at that place in both CTAs) when every MMA
+// issued so far is complete.
+template <int CG>
+__device__ __forceinline__ void gg_commit(uint64_t* bar) {
+    if (CG == 1)
+        umma_commit(bar);
+    else
+        asm volatile(
+            "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
+                smem_u32(bar)),
+            "h"((uint16_t)3)
+            : "memory");
+}
+
+// Arrive on this CTA's `bar` alone.
+template <int CG>
+__device__ __forceinline__ void gg_commit_own(uint64_t* bar) {
+    if (CG == 1)
+        umma_commit(bar);
+    else
+        asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(bar))
+                     : "memory");
+}
+
+template <int CG>
+__device__ __forceinline__ void gg_tmem_alloc(uint32_t* slot, uint32_t ncols) {
+    if (CG == 1) {
+        tmem_alloc(slot, ncols);
+    } else {
+        asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(slot)),
+                     "r"(ncols)
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+    }
+}
+
+template <int CG>
+__device__ __forceinline__ void gg_tmem_dealloc(uint32_t taddr, uint32_t ncols) {
+    if (CG == 1)
+        tmem_dealloc(taddr, ncols);
+    else
+        asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(ncols) : "memory");
+}
+
+// Bounded waits that also give up once another role of the CTA has raised the abort flag.
+__device__ __forceinline__ bool gg_wait(uint64_t* bar, uint32_t parity, int* abort) {
+    for (uint32_t i = 0; i < kGgWaitLimit; ++i) {
+        if (mbar_try_wait(bar, parity)) return true;
+        if ((i & 63u) == 63u && *(volatile int*)abort) return false;
+    }
+    *(volatile int*)abort = 1;
+    return false;
+}
+
+__device__ __forceinline__ bool gg_wait_cluster(uint64_t* bar, uint32_t parity, int* abort) {
+    for (uint32_t i = 0; i < kGgWaitLimit; ++i) {
+        if (mbar_try_wait_cluster(bar, parity)) return true;
+        if ((i & 63u) == 63u && *(volatile int*)abort) return false;
+    }
+    *(volatile int*)abort = 1;
+    return false;
+}
+
+// ------------------------------------------------------------- segments
+// The segments into shared memory.  Offsets outside [0, R] or descending
+// leave their segment out (and set MOE_DEV_BAD_OFFSETS): nothing is read or
+// written outside the tensors.  start[e] = tiles of the segments before e.
+__device__ __forceinline__ void gg_segments(GgShared* sh, const int32_t* offsets, int E, int R, int bn, int mt,
+                                            int32_t* status) {
+    const int tid = threadIdx.x;
+    if (tid == 0) sh->nmax = 0;
+    __syncthreads();
+    for (int e = tid; e < E; e += blockDim.x) {
+        const int a = __ldg(offsets + e), b = __ldg(offsets + e + 1);
+        const bool ok = a >= 0 && b >= a && b <= R;
+        if (!ok && blockIdx.x == 0) set_status(status, MOE_DEV_BAD_OFFSETS);
+        sh->p0[e] = ok ? a : 0;
+        sh->cnt[e] = ok ? b - a : 0;
+        if (ok && b > a) atomicMax(&sh->nmax, b - a);
+    }
+    __syncthreads();
+    if (tid < 32) {  // exclusive scan, 8 segments a lane
+        int c[MOE_MAX_E / 32], sum = 0;
+#pragma unroll
+        for (int j = 0; j < MOE_MAX_E / 32; ++j) {
+            const int e = tid * (MOE_MAX_E / 32) + j;
+            c[j] = sum;
+            sum += e < E ? (sh->cnt[e] + bn - 1) / bn * mt : 0;
+        }
+        int run = sum;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int v = __shfl_up_sync(0xffffffffu, run, o);
+            if (tid >= o) run += v;
+        }
+#pragma unroll
+        for (int j = 0; j < MOE_MAX_E / 32; ++j) {
+            const int e = tid * (MOE_MAX_E / 32) + j;
+            if (e < E) sh->start[e] = run - sum + c[j];
+        }
+        if (tid == 31) sh->start[E] = run;
+    }
+    __syncthreads();
+}
+
+// ------------------------------------------------------------- the kernel
+// Persistent: one CTA per SM (or one pair of CTAs per SM pair) walks the
+// tiles.  Three roles run through the same tile sequence, each at its own
+// pace: the producer fills the ring, the MMA issuer accumulates tile d into
+// tensor-memory buffer d mod 2, four warps read the other buffer out.
+template <int MODE, int CG>
+__global__ void __launch_bounds__(kGgThreads, 1) gg_kernel(const __grid_constant__ GgParams p) {
+    using Cfg = GgCfg<MODE, CG>;
+    extern __shared__ __align__(1024) unsigned char gg_smem_raw[];
+    unsigned char* base = reinterpret_cast<unsigned char*>(
+        (reinterpret_cast<uintptr_t>(gg_smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+    GgShared* sh = reinterpret_cast<GgShared*>(base);
+    unsigned char* ring = base + 4096;
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t rank = CG == 2 ? cluster_rank() : 0u;
+    const int unit = (int)blockIdx.x / CG, units = (int)gridDim.x / CG;
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < kGgMaxStages; ++s) {
+            mbar_init(&sh->full[s], 1);
+            mbar_init(&sh->pfull[s], 1);
+            mbar_init(&sh->empty[s], 1);
+        }
+        for (int a = 0; a < 2; ++a) {
+            mbar_init(&sh->acc_full[a], 1);
+            mbar_init(&sh->acc_empty[a], 4 * CG);
+        }
+        mbar_init(&sh->mma_done, 1);
+        sh->abort = 0;
+        fence_mbar_init();
+    }
+    if (warp == 5) gg_tmem_alloc<CG>(&sh->tmem_slot, kGgTmemCols);
+    grid_dep_wait();
+    const int mtiles = (p.M + Cfg::BM - 1) / Cfg::BM;
+    gg_segments(sh, p.offsets, p.E, p.R, Cfg::BN, mtiles, p.status);
+    tc_fence_before();
+    __syncthreads();
+    if (CG == 2) cluster_sync();
+    tc_fence_after();
+    const uint32_t tmem = sh->tmem_slot;
+
+    // Ring geometry.  A stage holds KSUB A tiles and KSUB B tiles; where the
+    // B operand is the segment's rows, its tiles are as high as the largest
+    // segment needs, so that few rows leave more bytes of weights in flight.
+    uint32_t b_tile = kGgTile;
+    if (MODE != kGgDw && CG == 1)
+        b_tile = (uint32_t)min(Cfg::BN, max(kGgBoxN, (sh->nmax + kGgBoxN - 1) / kGgBoxN * kGgBoxN)) * 128u;
+    const uint32_t stage_bytes = Cfg::KSUB * (kGgTile + b_tile);
+    const uint32_t b_off = Cfg::KSUB * kGgTile;
+    const uint32_t S = min((uint32_t)kGgMaxStages, ((uint32_t)kGgSmem - 1023u - 4096u) / stage_bytes);
+
+    const int ntiles_w = (p.NW + Cfg::BN - 1) / Cfg::BN;  // dw
+    const int items = MODE == kGgDw ? p.E * mtiles * ntiles_w : sh->start[p.E];
+
+    // f(e, q0, n, mt, nst): segment e; q0 = first row (forward, dx: of the
+    // tile, dw: of the segment); n = valid columns; m0; contraction steps of 64
+    auto walk = [&](auto f) {
+        int e = 0;
+        for (int it = unit; it < items; it += units) {
+            int q0, n, n0, m0, nk;
+            if (MODE == kGgDw) {
+                const int per = mtiles * ntiles_w;
+                e = it / per;
+                const int t = it - e * per;
+                m0 = (t % mtiles) * Cfg::BM;
+                n0 = (t / mtiles) * Cfg::BN;
+                n = min(Cfg::BN, p.NW - n0);
+                q0 = sh->p0[e];
+                nk = (sh->cnt[e] + 63) / 64;
+            } else {
+                while (sh->start[e + 1] <= it) ++e;
+                const int t = it - sh->start[e];
+                m0 = (t % mtiles) * Cfg::BM;
+                n0 = (t / mtiles) * Cfg::BN;
+                n = min(Cfg::BN, sh->cnt[e] - n0);
+                q0 = sh->p0[e] + n0;
+                nk = (p.C + 63) / 64;
+            }
+            if (!f(e, q0, n, n0, m0, nk)) break;
+        }
+    };
+
+    if (warp == 4) {
+        uint32_t g = 0, armed = 0;
+        if (lane == 0) {
+            walk([&](int e, int q0, int n, int n0, int m0, int nk) -> bool {
+                // rows of B that this CTA holds (forward, dx), in whole boxes
+                const int rows = MODE == kGgDw ? 128 : (n + kGgBoxN * CG - 1) / (kGgBoxN * CG) * kGgBoxN;
+                const uint32_t bytes = kGgTile + (uint32_t)rows * 128u;
+                const int am = m0 + (int)rank * 128, bn = (MODE == kGgDw ? n0 : q0) + (int)rank * rows;
+                for (int k0 = 0; k0 < nk; k0 += Cfg::KSUB, ++g) {
+                    const uint32_t s = g % S, ph = (g / S) & 1u;
+                    if (g >= S && !gg_wait(&sh->empty[s], ph ^ 1u, &sh->abort)) return false;
+                    unsigned char* st = ring + (size_t)s * stage_bytes;
+                    const int ke = min(Cfg::KSUB, nk - k0);
+                    mbar_arrive_expect_tx(&sh->full[s], (uint32_t)ke * bytes);
+                    armed = g + 1u;
+                    for (int u = 0; u < ke; ++u) {
+                        unsigned char* sa = st + (size_t)u * kGgTile;
+                        unsigned char* sb = st + b_off + (size_t)u * b_tile;
+                        const int c = (k0 + u) * 64;
+                        if (MODE == kGgFwd) {
+                            tma_load_3d(sa, &p.ta, c, am, e, &sh->full[s]);
+                        } else if (MODE == kGgDx) {
+                            tma_load_3d(sa, &p.ta, am, c, e, &sh->full[s]);
+                            tma_load_3d(sa + 8192, &p.ta, am + 64, c, e, &sh->full[s]);
+                        } else {
+                            tma_load_2d(sa, &p.ta, am, q0 + c, &sh->full[s]);
+                            tma_load_2d(sa + 8192, &p.ta, am + 64, q0 + c, &sh->full[s]);
+                        }
+                        if (MODE == kGgDw) {
+                            tma_load_2d(sb, &p.tb, bn, q0 + c, &sh->full[s]);
+                            tma_load_2d(sb + 8192, &p.tb, bn + 64, q0 + c, &sh->full[s]);
+                        } else {
+                            for (int r = 0; r < rows; r += kGgBoxN)
+                                tma_load_2d(sb + r * 128, &p.tb, c, bn + r, &sh->full[s]);
+                        }
+                    }
+                }
+                return true;
+            });
+            // teardown: no copy, and no release of a stage by the other CTA's
+            // MMAs, may be on its way when the CTA exits
+            for (uint32_t s = 0; s < S && s < armed; ++s) {
+                const uint32_t last = armed - 1u - ((armed - 1u - s) % S);
+                mbar_wait(&sh->full[s], (last / S) & 1u, kGgWaitLimit);
+                if (CG == 2) gg_wait(&sh->empty[s], (last / S) & 1u, &sh->abort);
+            }
+        }
+        __syncwarp();
+    } else if (warp == 5) {
+        uint32_t g = 0;
+        int d = 0;
+        walk([&](int e, int q0, int n, int n0, int m0, int nk) -> bool {
+            if (nk == 0) return true;
+            const int buf = d & 1, use = d >> 1;
+            ++d;
+            if (rank == 0 && use > 0 && !gg_wait_cluster(&sh->acc_empty[buf], (uint32_t)((use - 1) & 1), &sh->abort))
+                return false;
+            tc_fence_after();
+            const uint32_t tacc = tmem + (uint32_t)(buf * Cfg::BN);
+            const int npad = MODE == kGgDw ? Cfg::BN : (n + kGgBoxN * CG - 1) / (kGgBoxN * CG) * (kGgBoxN * CG);
+            const uint32_t idesc = umma_idesc_bf16(Cfg::BM, npad) | (MODE != kGgFwd ? 1u << 15 : 0u) |
+                                   (MODE == kGgDw ? 1u << 16 : 0u);
+            for (int k0 = 0; k0 < nk; k0 += Cfg::KSUB, ++g) {
+                const uint32_t s = g % S, ph = (g / S) & 1u;
+                if (!gg_wait(&sh->full[s], ph, &sh->abort)) return false;
+                unsigned char* st = ring + (size_t)s * stage_bytes;
+                const int ke = min(Cfg::KSUB, nk - k0);
+                int steps = 4;  // MMAs (16 deep) of a 64-wide step
+                if (MODE == kGgDw) {
+                    // the segment's end: rows behind it belong to the next
+                    // segment (or to no one), so both operands' rows up to the
+                    // last MMA's end are zeroed -- zeroing one would leave
+                    // 0 x infinity or 0 x NaN
+                    const int valid = sh->cnt[e] - k0 * 64;
+                    if (valid < 64) {
+                        steps = (valid + 15) / 16;
+                        const int first = valid, rows = steps * 16 - valid;
+                        for (int i = lane; i < rows * 32; i += 32) {
+                            const int blk = i & 3, ch = (i >> 2) & 7, row = first + (i >> 5);
+                            *reinterpret_cast<uint4*>(st + (blk >> 1) * b_off + (blk & 1) * 8192 + row * 128 + ch * 16) =
+                                make_uint4(0, 0, 0, 0);
+                        }
+                        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                        __syncwarp();
+                    }
+                }
+                if (rank != 0) {
+                    if (lane == 0) mbar_arrive_cluster(&sh->pfull[s], 0);
+                    continue;
+                }
+                if (CG == 2 && !gg_wait_cluster(&sh->pfull[s], ph, &sh->abort)) return false;
+                tc_fence_after();
+                if (lane == 0) {
+                    const uint32_t sta = smem_u32(st);
+                    for (int u = 0; u < ke; ++u) {
+                        const uint32_t aa = sta + (uint32_t)u * kGgTile, ba = sta + b_off + (uint32_t)u * b_tile;
+                        for (int kk = 0; kk < steps; ++kk) {
+                            const uint64_t ad = MODE == kGgFwd ? umma_sdesc(aa + kk * 32) : umma_sdesc_mn(aa + kk * 2048, 8192);
+                            const uint64_t bd = MODE == kGgDw ? umma_sdesc_mn(ba + kk * 2048, 8192) : umma_sdesc(ba + kk * 32);
+                            gg_mma<CG>(tacc, ad, bd, idesc, (k0 > 0 || u > 0 || kk > 0) ? 1u : 0u);
+                        }
+                    }
+                    gg_commit<CG>(&sh->empty[s]);
+                }
+                __syncwarp();
+            }
+            if (rank == 0 && lane == 0) gg_commit<CG>(&sh->acc_full[buf]);
+            __syncwarp();
+            return true;
+        });
+        if (rank == 0 && lane == 0) {
+            gg_commit_own<CG>(&sh->mma_done);
+            mbar_wait(&sh->mma_done, 0u, kGgWaitLimit);
+        }
+        __syncwarp();
+    } else {
+        int d = 0;
+        walk([&](int e, int q0, int n, int n0, int m0, int nk) -> bool {
+            const int m = m0 + (int)rank * 128 + (int)threadIdx.x;
+            const size_t row0 = MODE == kGgDw ? (size_t)e * p.NW + n0 : (size_t)q0;
+            const size_t at0 = row0 * (size_t)p.M + m;
+            const bool live = m < p.M;
+            int buf = 0;
+            if (nk > 0) {
+                buf = d & 1;
+                const int use = d >> 1;
+                ++d;
+                if (!gg_wait(&sh->acc_full[buf], (uint32_t)(use & 1), &sh->abort)) return false;
+                __syncwarp();
+                tc_fence_after();
+            }
+            const uint32_t row_addr = tmem + (uint32_t)(buf * Cfg::BN) + ((uint32_t)(warp * 32) << 16);
+            for (int c0 = 0; c0 < n; c0 += 16) {
+                float v[16];
+                if (nk > 0) {
+                    tmem_ld16(row_addr + c0, v);
+                    if (c0 + 16 >= n) {
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) {
+                            if (CG == 1)
+                                mbar_arrive(&sh->acc_empty[buf]);
+                            else
+                                mbar_arrive_cluster(&sh->acc_empty[buf], 0);
+                        }
+                    }
+                } else {
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) v[j] = 0.0f;
+                }
+                const int nc = min(16, n - c0);
+                if (live) {
+                    size_t at = at0 + (size_t)c0 * p.M;
+#pragma unroll
+                    for (int j = 0; j < 16; ++j, at += p.M) {
+                        if (j >= nc) break;
+                        if (p.out_f32)
+                            static_cast<float*>(p.out)[at] = v[j];
+                        else
+                            static_cast<uint16_t*>(p.out)[at] = f2bf_bits(v[j]);
+                    }
+                }
+            }
+            return true;
+        });
+    }
+    __syncthreads();
+    if (*(volatile int*)&sh->abort && threadIdx.x == 0) set_status(p.status, MOE_DEV_TIMEOUT);
+    if (CG == 2) cluster_sync();
+    if (warp == 5) {
+        tc_fence_after();
+        gg_tmem_dealloc<CG>(tmem, kGgTmemCols);
+    }
+}
+
+// ------------------------------------------------------- a few rows at once
+// Forward product for a handful of rows: a warp per weight row, up to
+// kGgvTok rows of one segment at a time.  Block (i, r) takes 8 weight rows
+// for the rows r .. of a segment when r starts a group of kGgvTok there.
+constexpr int kGgvTok = 4;
+
+__global__ void __launch_bounds__(256) gg_gemv_kernel(const uint16_t* __restrict__ x, const uint16_t* __restrict__ w,
+                                                      const int32_t* __restrict__ offsets, int R, int N, int K, int E,
+                                                      void* y, int out_f32, int32_t* status) {
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    grid_dep_wait();
+    const int r = blockIdx.y;
+    // the segment of row r: E <= blockDim.x, a thread per segment
+    bool mine = false, bad = false;
+    int a = 0, b = 0;
+    if ((int)threadIdx.x < E) {
+        a = __ldg(offsets + threadIdx.x);
+        b = __ldg(offsets + threadIdx.x + 1);
+        bad = a < 0 || b < a || b > R;
+        mine = !bad && a <= r && r < b;
+    }
+    __shared__ int s_e, s_p0, s_p1;
+    if (threadIdx.x == 0) s_e = -1;
+    __syncthreads();
+    if (bad && blockIdx.x == 0 && r == 0) set_status(status, MOE_DEV_BAD_OFFSETS);
+    if (mine) {
+        s_e = threadIdx.x;
+        s_p0 = a;
+        s_p1 = b;
+    }
+    __syncthreads();
+    const int e = s_e;
+    if (e < 0 || (r - s_p0) % kGgvTok) return;
+    const int nt = min(kGgvTok, s_p1 - r);
+    const int n = blockIdx.x * 8 + warp;
+    if (n >= N) return;
+    const uint16_t* wr = w + ((size_t)e * N + n) * K;
+    const uint16_t* xr = x + (size_t)r * K;
+    float acc[kGgvTok] = {};
+    const int chunks = K / 8;
+    for (int c0 = 0; c0 < chunks; c0 += 32 * 8) {
+        uint4 wv[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const int c = c0 + j * 32 + lane;
+            wv[j] = c < chunks ? ld_weight_v4(wr + (size_t)c * 8) : make_uint4(0, 0, 0, 0);
+        }
+#pragma unroll
+        for (int t = 0; t < kGgvTok; ++t) {
+            if (t >= nt) break;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const int c = c0 + j * 32 + lane;
+                if (c >= chunks) break;
+                const uint4 xv = __ldg(reinterpret_cast<const uint4*>(xr + (size_t)t * K + (size_t)c * 8));
+                const uint32_t ws[4] = {wv[j].x, wv[j].y, wv[j].z, wv[j].w}, xs[4] = {xv.x, xv.y, xv.z, xv.w};
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const float2 wf = bf16x2_to_f2(ws[i]), xf = bf16x2_to_f2(xs[i]);
+                    acc[t] = fmaf(wf.x, xf.x, acc[t]);
+                    acc[t] = fmaf(wf.y, xf.y, acc[t]);
+                }
+            }
+        }
+    }
+#pragma unroll
+    for (int t = 0; t < kGgvTok; ++t) {
+        if (t >= nt) break;
+        const float v = warp_sum(acc[t]);
+        if (lane == 0) {
+            const size_t at = (size_t)(r + t) * N + n;
+            if (out_f32)
+                static_cast<float*>(y)[at] = v;
+            else
+                static_cast<uint16_t*>(y)[at] = f2bf_bits(v);
+        }
+    }
+}
+
+}  // namespace moe

@@ -1,0 +1,511 @@
+// moe_nvfp4.cuh -- NVFP4 (E2M1 codes, an E4M3 scale per 16 elements of a
+// row, one fp32 scale a matrix or a row): quantisation, its inverse, and the
+// product of two NVFP4 operands grouped by expert.
+#pragma once
+
+#include "moe_grouped.cuh"
+
+namespace moe {
+
+// ------------------------------------------------------------ quantisation
+// For a group (a matrix, or one row) with the finite magnitudes' maximum a:
+//   gs = a / 2688 (448 * 6, the largest E4M3 times the largest E2M1),
+//        rounded up to 8 significant bits, at least 2^-100
+//   bs = E4M3 nearest to (block maximum) / (6 gs)
+//   q  = E2M1 nearest to x / (bs gs), both ties to even
+// With 8 bits in gs and 4 in bs the divisors 6 gs and bs gs are exact in
+// fp32, and a quotient of fp32 numbers by a divisor of at most 12 bits that
+// is not on a rounding border of the coarse formats does not round onto one:
+// the results are those of exact arithmetic.
+constexpr float kNv4Top = 2688.0f;
+constexpr float kNv4MinScale = 7.888609052210118e-31f;  // 2^-100
+constexpr uint32_t kNv4MaxScaleBits = 0x79c30000u;      // the largest 8-bit scale with 2688 gs finite
+
+__device__ __forceinline__ float nv4_scale(float amax) {
+    const float f = __fdiv_ru(amax, kNv4Top);
+    const uint32_t up = (__float_as_uint(f) + 0xffffu) & 0xffff0000u;
+    return fmaxf(__uint_as_float(min(up, kNv4MaxScaleBits)), kNv4MinScale);
+}
+
+// 32 bytes of global memory in one load or store (both 32-byte aligned).
+struct alignas(32) Words8 {
+    uint32_t w[8];
+};
+__device__ __forceinline__ Words8 ld_words8(const void* p) {
+    Words8 r;
+    asm volatile("ld.global.nc.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                 : "=r"(r.w[0]), "=r"(r.w[1]), "=r"(r.w[2]), "=r"(r.w[3]), "=r"(r.w[4]), "=r"(r.w[5]), "=r"(r.w[6]),
+                   "=r"(r.w[7])
+                 : "l"(p));
+    return r;
+}
+__device__ __forceinline__ void st_words8(void* p, const Words8& r) {
+    asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(r.w[0]), "r"(r.w[1]), "r"(r.w[2]),
+                 "r"(r.w[3]), "r"(r.w[4]), "r"(r.w[5]), "r"(r.w[6]), "r"(r.w[7])
+                 : "memory");
+}
+
+// One 16-element block as loaded: bf16 pairs (8 words) or fp32 (16 words).
+template <bool BF16>
+struct Nv4Block {
+    Words8 w[BF16 ? 1 : 2];
+
+    __device__ __forceinline__ void load(const void* x, size_t block) {
+        const char* p = static_cast<const char*>(x) + block * (BF16 ? 32 : 64);
+        w[0] = ld_words8(p);
+        if (!BF16) w[1] = ld_words8(p + 32);
+    }
+    __device__ __forceinline__ void clear() {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) w[0].w[i] = 0;
+        if (!BF16)
+#pragma unroll
+            for (int i = 0; i < 8; ++i) w[1].w[i] = 0;
+    }
+    // the largest magnitude among the finite elements; `bad` if any is not finite
+    __device__ __forceinline__ float amax(bool& bad) const {
+        if (BF16) {
+            // magnitudes of bf16 numbers order like their bits: two a word
+            uint32_t m = 0;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) m = __vmaxu2(m, w[0].w[i] & 0x7fff7fffu);
+            uint32_t t = max(m & 0xffffu, m >> 16);
+            bad = t >= 0x7f80u;
+            if (bad) {
+                t = 0;
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const uint32_t lo = w[0].w[i] & 0x7fffu, hi = (w[0].w[i] >> 16) & 0x7fffu;
+                    if (lo < 0x7f80u) t = max(t, lo);
+                    if (hi < 0x7f80u) t = max(t, hi);
+                }
+            }
+            return __uint_as_float(t << 16);
+        }
+        uint32_t t = 0;
+#pragma unroll
+        for (int j = 0; j < (BF16 ? 1 : 2); ++j)
+#pragma unroll
+            for (int i = 0; i < 8; ++i) t = max(t, w[j].w[i] & 0x7fffffffu);
+        bad = t >= 0x7f800000u;
+        if (bad) {
+            t = 0;
+#pragma unroll
+            for (int j = 0; j < (BF16 ? 1 : 2); ++j)
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const uint32_t b = w[j].w[i] & 0x7fffffffu;
+                    if (b < 0x7f800000u) t = max(t, b);
+                }
+        }
+        return __uint_as_float(t);
+    }
+    // elements 2i and 2i + 1
+    __device__ __forceinline__ float2 pair(int i) const {
+        if (BF16) return bf16x2_to_f2(w[0].w[i]);
+        const Words8& v = w[BF16 ? 0 : i >> 2];
+        return make_float2(__uint_as_float(v.w[(2 * i) & 7]), __uint_as_float(v.w[(2 * i + 1) & 7]));
+    }
+    // codes (8 bytes) and block scale (1 byte) under the group's scale; a
+    // block with an element that is not finite decodes to NaN throughout
+    __device__ __forceinline__ void encode(float gs, uint8_t* q, uint8_t* bs, size_t block) const {
+        bool bad;
+        const float m = amax(bad);
+        const uint32_t b = __nv_cvt_float_to_fp8(__fdiv_rn(m, 6.0f * gs), __NV_SATFINITE, __NV_E4M3);
+        const float s = f8_to_f(b) * gs;
+        const float inv = s > 0.0f && !bad ? __frcp_rn(s) : 0.0f;
+        uint32_t out[2] = {0, 0};
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            // x / s to nearest: the product with the reciprocal, corrected once
+            // by its exact remainder t s - x (written this way round a zero keeps its sign)
+            const float2 x = pair(i);
+            const float2 t = make_float2(x.x * inv, x.y * inv);
+            const float2 v = make_float2(fmaf(fmaf(t.x, s, -x.x), -inv, t.x), fmaf(fmaf(t.y, s, -x.y), -inv, t.y));
+            const uint32_t c = __nv_cvt_float2_to_fp4x2(v, __NV_E2M1, cudaRoundNearest);
+            out[i >> 2] |= c << (8 * (i & 3));
+        }
+        if (bad) out[0] = out[1] = 0;
+        *reinterpret_cast<uint2*>(q + block * 8) = make_uint2(out[0], out[1]);
+        bs[block] = (uint8_t)(bad ? 0x7fu : b);
+    }
+};
+
+// One scale a row: T threads hold a row's blocks in registers (up to BPT
+// each), find its maximum and write its codes -- x is read once.
+template <bool BF16, int T, int BPT>
+__global__ void __launch_bounds__(128) nv4_rows_kernel(const void* __restrict__ x, int G, int nb, uint8_t* q, uint8_t* bs,
+                                                       float* gs, int32_t* status) {
+    __shared__ float s_max[4];
+    grid_dep_wait();
+    const int sub = threadIdx.x / T, t = threadIdx.x % T;
+    const size_t row = (size_t)blockIdx.x * (128 / T) + sub;
+    const bool live = row < (size_t)G;
+    Nv4Block<BF16> blk[BPT];
+    float m = 0.0f;
+    bool any_bad = false;
+#pragma unroll
+    for (int j = 0; j < BPT; ++j) {
+        const int b = j * T + t;
+        if (live && b < nb)
+            blk[j].load(x, row * nb + b);
+        else
+            blk[j].clear();
+    }
+#pragma unroll
+    for (int j = 0; j < BPT; ++j) {
+        bool bad;
+        m = fmaxf(m, blk[j].amax(bad));
+        any_bad |= bad;
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    if (T > 32) {
+        if ((threadIdx.x & 31) == 0) s_max[threadIdx.x >> 5] = m;
+        __syncthreads();
+        m = fmaxf(fmaxf(s_max[0], s_max[1]), fmaxf(s_max[2], s_max[3]));
+    }
+    const float scale = nv4_scale(m);
+    if (any_bad) set_status(status, MOE_DEV_NONFINITE);
+#pragma unroll
+    for (int j = 0; j < BPT; ++j) {
+        const int b = j * T + t;
+        if (live && b < nb) blk[j].encode(scale, q, bs, row * nb + b);
+    }
+    if (live && t == 0) gs[row] = scale;
+}
+
+// One scale a matrix: its maximum first (as bits, in the workspace), then the codes.
+template <bool BF16>
+__global__ void __launch_bounds__(256) nv4_amax_kernel(const void* __restrict__ x, size_t per, unsigned* amax,
+                                                       int32_t* status) {
+    grid_dep_wait();
+    const size_t g = blockIdx.y;
+    float m = 0.0f;
+    bool any_bad = false;
+    for (size_t b = (size_t)blockIdx.x * blockDim.x + threadIdx.x; b < per; b += (size_t)gridDim.x * blockDim.x) {
+        Nv4Block<BF16> blk;
+        bool bad;
+        blk.load(x, g * per + b);
+        m = fmaxf(m, blk.amax(bad));
+        any_bad |= bad;
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    if ((threadIdx.x & 31) == 0) atomicMax(amax + g, __float_as_uint(m));
+    if (any_bad) set_status(status, MOE_DEV_NONFINITE);
+}
+
+template <bool BF16>
+__global__ void __launch_bounds__(256) nv4_encode_kernel(const void* __restrict__ x, size_t per, const unsigned* amax,
+                                                         uint8_t* q, uint8_t* bs, float* gs) {
+    grid_dep_wait();
+    const size_t g = blockIdx.y;
+    const float scale = nv4_scale(__uint_as_float(__ldcg(amax + g)));
+    for (size_t b = (size_t)blockIdx.x * blockDim.x + threadIdx.x; b < per; b += (size_t)gridDim.x * blockDim.x) {
+        Nv4Block<BF16> blk;
+        blk.load(x, g * per + b);
+        blk.encode(scale, q, bs, g * per + b);
+    }
+    if (blockIdx.x == 0 && threadIdx.x == 0) gs[g] = scale;
+}
+
+// Values e2m1(q) * e4m3(bs) * gs: a thread per block (the first two factors'
+// product is exact, the rounding is that of the last product, and of bf16).
+template <bool BF16>
+__global__ void __launch_bounds__(256) nv4_decode_kernel(const uint8_t* __restrict__ q, const uint8_t* __restrict__ bs,
+                                                         const float* __restrict__ gs, size_t per, size_t n, void* x) {
+    grid_dep_wait();
+    for (size_t b = (size_t)blockIdx.x * blockDim.x + threadIdx.x; b < n; b += (size_t)gridDim.x * blockDim.x) {
+        const uint2 c = __ldg(reinterpret_cast<const uint2*>(q) + b);
+        const float s = f8_to_f(bs[b]), g = __ldg(gs + b / per);
+        Words8 o[BF16 ? 1 : 2];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const float2 v = f4x2_to_f2(((i < 4 ? c.x : c.y) >> (8 * (i & 3))) & 0xffu);
+            const float lo = v.x * s * g, hi = v.y * s * g;
+            if (BF16) {
+                o[0].w[i] = (uint32_t)f2bf_bits(lo) | ((uint32_t)f2bf_bits(hi) << 16);
+            } else {
+                o[BF16 ? 0 : i >> 2].w[(2 * i) & 7] = __float_as_uint(lo);
+                o[BF16 ? 0 : i >> 2].w[(2 * i + 1) & 7] = __float_as_uint(hi);
+            }
+        }
+        char* at = static_cast<char*>(x) + b * (BF16 ? 32 : 64);
+        st_words8(at, o[0]);
+        if (!BF16) st_words8(at + 32, o[BF16 ? 0 : 1]);
+    }
+}
+
+// ------------------------------------------------------------- the product
+// y[r, n] = xgs[r] wgs[e] sum_k (xq bs)(wq bs): tcgen05.mma block-scaled
+// (kind::mxf4nvf4, one E4M3 scale per 16 elements), fp32 accumulation.  The
+// codes go to shared memory by TMA like the bf16 operands (a 128-byte row
+// holds 256 elements); the scales are read row by row (16 bytes = the 16
+// blocks of those 256 elements), rearranged in registers and copied to
+// tensor memory by tcgen05.cp: the MMA of 64 elements takes four scale bytes
+// a row as one 32-bit column word, rows 32 j + i at lane i of column j.  A
+// lane that loads rows i, i + 32, i + 64 and i + 96 holds exactly the 16
+// bytes that one lane of four columns wants for each 64-element step.
+constexpr int kG4Threads = 320;  // warps 0-3 epilogue, 4 TMA, 5 MMA, 6-9 scales
+constexpr int kG4ScaleWarps = 4;
+constexpr int kG4Bn = 128;
+constexpr int kG4A = 128 * 128;       // codes of 128 rows x 256 elements
+constexpr int kG4Sf = 2048;           // scales of 128 rows x 256 elements
+constexpr int kG4MaxStages = 9;
+constexpr uint32_t kG4SfCol = 256;    // tensor-memory column of the scales, behind two 128-column accumulators
+
+struct G4Params {
+    CUtensorMap ta, tb;  // wq [E, N, K/2], xq [R, K/2] bytes
+    const uint8_t *wbs, *xbs;
+    const float *wgs, *xgs;
+    const int32_t* offsets;
+    int E, R, M, K;
+    void* out;
+    int out_f32;
+    int32_t* status;
+};
+
+struct G4Shared {
+    GgShared g;
+    uint64_t sfull[kG4MaxStages];  // a stage's scales are in shared memory
+};
+static_assert(sizeof(G4Shared) <= 4096, "control block");
+
+// Copy 32 rows x 128 bits of shared memory (rows 16 bytes apart) to four
+// tensor-memory columns, repeated for the four lane quarters.
+__device__ __forceinline__ void umma_cp_scales(uint32_t taddr, uint32_t saddr) {
+    uint64_t d = 0;
+    d |= (uint64_t)((saddr & 0x3FFFFu) >> 4);
+    d |= (uint64_t)(128 >> 4) << 16;
+    d |= (uint64_t)(128 >> 4) << 32;  // 8-row groups 128 bytes apart
+    d |= (uint64_t)1 << 46;
+    asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(d) : "memory");
+}
+
+// Instruction descriptor, kind::mxf4nvf4: E2M1 A and B, E4M3 scales.
+__device__ __forceinline__ uint32_t umma_idesc_nvfp4(int M, int N) {
+    return (1u << 7) | (1u << 10) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
+}
+
+__device__ __forceinline__ void umma_nvfp4(uint32_t tmem_d, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
+                                           uint32_t sfa, uint32_t sfb, uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %6, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::mxf4nvf4.block_scale.scale_vec::4X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(
+            tmem_d),
+        "l"(adesc), "l"(bdesc), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
+        : "memory");
+}
+
+// The 16 scale bytes of a row from block k0 on; blocks from nb on read as 0.
+__device__ __forceinline__ uint4 g4_row_scales(const uint8_t* row, int k0, int nb, bool live) {
+    uint4 r = make_uint4(0, 0, 0, 0);
+    if (!live) return r;
+    const uint8_t* p = row + k0;
+    if ((nb & 15) == 0) return __ldg(reinterpret_cast<const uint4*>(p));
+    uint32_t w[4] = {0, 0, 0, 0};
+    if ((nb & 3) == 0) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (k0 + 4 * i < nb) w[i] = __ldg(reinterpret_cast<const uint32_t*>(p + 4 * i));
+    } else {  // nb is even: K % 32 == 0
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (k0 + 2 * i < nb)
+                w[i >> 1] |= (uint32_t)__ldg(reinterpret_cast<const uint16_t*>(p + 2 * i)) << (16 * (i & 1));
+    }
+    return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+__global__ void __launch_bounds__(kG4Threads, 1) g4_kernel(const __grid_constant__ G4Params p) {
+    extern __shared__ __align__(1024) unsigned char gg_smem_raw[];
+    unsigned char* base = reinterpret_cast<unsigned char*>(
+        (reinterpret_cast<uintptr_t>(gg_smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+    G4Shared* s4 = reinterpret_cast<G4Shared*>(base);
+    GgShared* sh = &s4->g;
+    unsigned char* ring = base + 4096;
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < kG4MaxStages; ++s) {
+            mbar_init(&sh->full[s], 1);
+            mbar_init(&sh->empty[s], 1);
+            mbar_init(&s4->sfull[s], 1);
+        }
+        for (int a = 0; a < 2; ++a) {
+            mbar_init(&sh->acc_full[a], 1);
+            mbar_init(&sh->acc_empty[a], 4);
+        }
+        mbar_init(&sh->mma_done, 1);
+        sh->abort = 0;
+        fence_mbar_init();
+    }
+    if (warp == 5) tmem_alloc(&sh->tmem_slot, kGgTmemCols);
+    grid_dep_wait();
+    const int mtiles = (p.M + 127) / 128;
+    gg_segments(sh, p.offsets, p.E, p.R, kG4Bn, mtiles, p.status);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = sh->tmem_slot;
+
+    // stage: weight codes, weight scales, row scales, row codes (as many rows
+    // as the largest segment needs)
+    const uint32_t b_tile = (uint32_t)min(kG4Bn, max(kGgBoxN, (sh->nmax + kGgBoxN - 1) / kGgBoxN * kGgBoxN)) * 128u;
+    const uint32_t b_off = kG4A + 2 * kG4Sf;
+    const uint32_t stage_bytes = b_off + b_tile;
+    const uint32_t S = min((uint32_t)kG4MaxStages, ((uint32_t)kGgSmem - 1023u - 4096u) / stage_bytes);
+    const int nk = (p.K + 255) / 256, nb = p.K / 16;
+
+    auto walk = [&](auto f) {
+        int e = 0;
+        for (int it = (int)blockIdx.x; it < sh->start[p.E]; it += (int)gridDim.x) {
+            while (sh->start[e + 1] <= it) ++e;
+            const int t = it - sh->start[e];
+            const int m0 = (t % mtiles) * 128, n0 = (t / mtiles) * kG4Bn;
+            if (!f(e, sh->p0[e] + n0, min(kG4Bn, sh->cnt[e] - n0), m0)) break;
+        }
+    };
+
+    if (warp == 4) {
+        uint32_t g = 0, armed = 0;
+        if (lane == 0) {
+            walk([&](int e, int q0, int n, int m0) -> bool {
+                const int rows = (n + kGgBoxN - 1) / kGgBoxN * kGgBoxN;
+                for (int k = 0; k < nk; ++k, ++g) {
+                    const uint32_t s = g % S, ph = (g / S) & 1u;
+                    if (g >= S && !gg_wait(&sh->empty[s], ph ^ 1u, &sh->abort)) return false;
+                    unsigned char* st = ring + (size_t)s * stage_bytes;
+                    mbar_arrive_expect_tx(&sh->full[s], kG4A + (uint32_t)rows * 128u);
+                    armed = g + 1u;
+                    tma_load_3d(st, &p.ta, k * 128, m0, e, &sh->full[s]);
+                    for (int r = 0; r < rows; r += kGgBoxN)
+                        tma_load_2d(st + b_off + r * 128, &p.tb, k * 128, q0 + r, &sh->full[s]);
+                }
+                return true;
+            });
+            for (uint32_t s = 0; s < S && s < armed; ++s) {
+                const uint32_t last = armed - 1u - ((armed - 1u - s) % S);
+                mbar_wait(&sh->full[s], (last / S) & 1u, kGgWaitLimit);
+            }
+        }
+        __syncwarp();
+    } else if (warp == 5) {
+        uint32_t g = 0;
+        int d = 0;
+        walk([&](int e, int q0, int n, int m0) -> bool {
+            const int buf = d & 1, use = d >> 1;
+            ++d;
+            if (use > 0 && !gg_wait(&sh->acc_empty[buf], (uint32_t)((use - 1) & 1), &sh->abort)) return false;
+            tc_fence_after();
+            const uint32_t tacc = tmem + (uint32_t)(buf * kG4Bn);
+            const uint32_t idesc = umma_idesc_nvfp4(128, (n + kGgBoxN - 1) / kGgBoxN * kGgBoxN);
+            for (int k = 0; k < nk; ++k, ++g) {
+                const uint32_t s = g % S, ph = (g / S) & 1u;
+                if (!gg_wait(&sh->full[s], ph, &sh->abort) || !gg_wait(&s4->sfull[s], ph, &sh->abort)) return false;
+                tc_fence_after();
+                if (lane == 0) {
+                    const uint32_t st = smem_u32(ring + (size_t)s * stage_bytes);
+                    // the scales' columns alternate between stages
+                    const uint32_t sfa = tmem + kG4SfCol + (g & 1u) * 32u, sfb = sfa + 16u;
+                    const int steps = min(4, (p.K - k * 256 + 63) / 64);
+                    for (int kk = 0; kk < steps; ++kk) {
+                        umma_cp_scales(sfa + kk * 4, st + kG4A + kk * 512);
+                        umma_cp_scales(sfb + kk * 4, st + kG4A + kG4Sf + kk * 512);
+                    }
+                    for (int kk = 0; kk < steps; ++kk)
+                        umma_nvfp4(tacc, umma_sdesc(st + kk * 32), umma_sdesc(st + b_off + kk * 32), idesc, sfa + kk * 4,
+                                   sfb + kk * 4, (k > 0 || kk > 0) ? 1u : 0u);
+                    umma_commit(&sh->empty[s]);
+                }
+                __syncwarp();
+            }
+            if (lane == 0) umma_commit(&sh->acc_full[buf]);
+            __syncwarp();
+            return true;
+        });
+        if (lane == 0) {
+            umma_commit(&sh->mma_done);
+            mbar_wait(&sh->mma_done, 0u, kGgWaitLimit);
+        }
+        __syncwarp();
+    } else if (warp >= 6) {
+        // ---------------- scales: warp 6 + i takes every fourth stage
+        uint32_t g = 0;
+        walk([&](int e, int q0, int n, int m0) -> bool {
+            for (int k = 0; k < nk; ++k, ++g) {
+                if ((int)(g % kG4ScaleWarps) != warp - 6) continue;
+                uint4 a[4], b[4];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const int m = m0 + 32 * j + lane, r = 32 * j + lane;
+                    a[j] = g4_row_scales(p.wbs + ((size_t)e * p.M + m) * nb, k * 16, nb, m < p.M);
+                    b[j] = g4_row_scales(p.xbs + (size_t)(q0 + r) * nb, k * 16, nb, r < n);
+                }
+                const uint32_t s = g % S, ph = (g / S) & 1u;
+                if (g >= S && !gg_wait(&sh->empty[s], ph ^ 1u, &sh->abort)) return false;
+                uint4* sa = reinterpret_cast<uint4*>(ring + (size_t)s * stage_bytes + kG4A);
+                uint4* sb = sa + kG4Sf / 16;
+                sa[lane] = make_uint4(a[0].x, a[1].x, a[2].x, a[3].x);
+                sa[32 + lane] = make_uint4(a[0].y, a[1].y, a[2].y, a[3].y);
+                sa[64 + lane] = make_uint4(a[0].z, a[1].z, a[2].z, a[3].z);
+                sa[96 + lane] = make_uint4(a[0].w, a[1].w, a[2].w, a[3].w);
+                sb[lane] = make_uint4(b[0].x, b[1].x, b[2].x, b[3].x);
+                sb[32 + lane] = make_uint4(b[0].y, b[1].y, b[2].y, b[3].y);
+                sb[64 + lane] = make_uint4(b[0].z, b[1].z, b[2].z, b[3].z);
+                sb[96 + lane] = make_uint4(b[0].w, b[1].w, b[2].w, b[3].w);
+                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&s4->sfull[s]);
+            }
+            return true;
+        });
+    } else {
+        int d = 0;
+        walk([&](int e, int q0, int n, int m0) -> bool {
+            const int m = m0 + (int)threadIdx.x;
+            const size_t at0 = (size_t)q0 * (size_t)p.M + m;
+            const bool live = m < p.M;
+            const float wg = __ldg(p.wgs + e);
+            const int buf = d & 1, use = d >> 1;
+            ++d;
+            if (!gg_wait(&sh->acc_full[buf], (uint32_t)(use & 1), &sh->abort)) return false;
+            __syncwarp();
+            tc_fence_after();
+            const uint32_t row_addr = tmem + (uint32_t)(buf * kG4Bn) + ((uint32_t)(warp * 32) << 16);
+            for (int c0 = 0; c0 < n; c0 += 16) {
+                float v[16];
+                tmem_ld16(row_addr + c0, v);
+                if (c0 + 16 >= n) {
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&sh->acc_empty[buf]);
+                }
+                const int nc = min(16, n - c0);
+                if (live) {
+                    size_t at = at0 + (size_t)c0 * p.M;
+#pragma unroll
+                    for (int j = 0; j < 16; ++j, at += p.M) {
+                        if (j >= nc) break;
+                        const float o = v[j] * __ldg(p.xgs + q0 + c0 + j) * wg;
+                        if (p.out_f32)
+                            static_cast<float*>(p.out)[at] = o;
+                        else
+                            static_cast<uint16_t*>(p.out)[at] = f2bf_bits(o);
+                    }
+                }
+            }
+            return true;
+        });
+    }
+    __syncthreads();
+    if (*(volatile int*)&sh->abort && threadIdx.x == 0) set_status(p.status, MOE_DEV_TIMEOUT);
+    if (warp == 5) {
+        tc_fence_after();
+        tmem_dealloc(tmem, kGgTmemCols);
+    }
+}
+
+}  // namespace moe

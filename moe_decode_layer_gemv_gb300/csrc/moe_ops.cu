@@ -1,0 +1,282 @@
+// moe_ops.cu -- the C ABI of the grouped products and the NVFP4 operators
+// (declared in include/moe.h): argument checks, the choice of a kernel and
+// its launch.  Kernels: moe_grouped.cuh and moe_nvfp4.cuh.
+#include <cuda_runtime.h>
+#include <stdint.h>
+#include <string.h>
+
+#include "moe.h"
+#include "moe_grouped.cuh"
+#include "moe_host.cuh"
+#include "moe_nvfp4.cuh"
+
+namespace moe {
+
+// A tensor map over a row-major tensor [outer2, outer1, inner] (outer2 = 0:
+// two dimensions) with 128-byte swizzled boxes of 128 bytes x box_rows;
+// elements outside the tensor read as zeros.
+static bool encode_map(CUtensorMap* map, const void* base, bool bytes, uint64_t inner, uint64_t outer1, uint64_t outer2,
+                       uint32_t box_rows) {
+    EncodeTiledFn fn = encode_fn();
+    if (!fn) return false;
+    const uint64_t pitch = inner * (bytes ? 1 : 2);
+    const cuuint64_t dims[3] = {inner, outer1, outer2};
+    const cuuint64_t strides[2] = {pitch, pitch * outer1};
+    const cuuint32_t box[3] = {bytes ? 128u : 64u, box_rows, 1};
+    const cuuint32_t estr[3] = {1, 1, 1};
+    return fn(map, bytes ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, outer2 ? 3 : 2,
+              const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+              CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+static int check_grouped(int R, int N, int K, int E, int dtype) {
+    if (R < 0 || R > MOE_MAX_ROWS || E < 1 || E > MOE_MAX_E) return MOE_ERR_INVALID_ARG;
+    if (N < 8 || N > 2 * MOE_MAX_DIM || (N & 7) || K < 8 || K > MOE_MAX_DIM || (K & 7)) return MOE_ERR_INVALID_ARG;
+    if (dtype != MOE_DT_F32 && dtype != MOE_DT_BF16) return MOE_ERR_INVALID_ARG;
+    return MOE_OK;
+}
+
+template <int MODE, int CG>
+static int launch_gg(const GgParams& p, int sms, cudaStream_t st) {
+    int rc = allow_smem(gg_kernel<MODE, CG>, kGgSmem);
+    if (rc) return rc;
+    cudaLaunchConfig_t cfg;
+    memset(&cfg, 0, sizeof cfg);
+    cfg.gridDim = dim3((unsigned)(sms / CG * CG));
+    cfg.blockDim = dim3(kGgThreads);
+    cfg.dynamicSmemBytes = kGgSmem;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = CG;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = CG > 1 ? 2 : 1;
+    return launch_ex(cfg, gg_kernel<MODE, CG>, p);
+}
+
+// The paired tile (256 x 256) from this many rows a segment on average.
+constexpr int kGgPairRows = 128;
+
+template <int MODE>
+static int run_gg(GgParams& p, const void* a, const void* b, int R, int N, int K, int E, cudaStream_t st) {
+    bool ok;
+    if (MODE == kGgFwd)
+        ok = encode_map(&p.ta, a, false, K, N, E, 128) && encode_map(&p.tb, b, false, K, R, 0, kGgBoxN);
+    else if (MODE == kGgDx)
+        ok = encode_map(&p.ta, a, false, K, N, E, 64) && encode_map(&p.tb, b, false, N, R, 0, kGgBoxN);
+    else
+        ok = encode_map(&p.ta, a, false, K, R, 0, 64) && encode_map(&p.tb, b, false, N, R, 0, 64);
+    if (!ok) return MOE_ERR_UNSUPPORTED;
+    p.E = E;
+    p.R = R;
+    p.M = MODE == kGgFwd ? N : K;
+    p.C = MODE == kGgFwd ? K : N;
+    p.NW = N;
+    const int sms = sm_count();
+    if (sms < 2) return MOE_ERR_CUDA;
+    const bool pair = (int64_t)R >= (int64_t)kGgPairRows * E;
+    return pair ? launch_gg<MODE, 2>(p, sms, st) : launch_gg<MODE, 1>(p, sms, st);
+}
+
+template <bool BF16, int T>
+static int launch_rows(const void* x, int G, int nb, uint8_t* q, uint8_t* bs, float* gs, int32_t* status, cudaStream_t st) {
+    const int per = 128 / T, bpt = (nb + T - 1) / T;
+    const unsigned grid = (unsigned)((G + per - 1) / per);
+    if (bpt <= 1) return launch_pdl(nv4_rows_kernel<BF16, T, 1>, grid, 128, 0, st, x, G, nb, q, bs, gs, status);
+    if (bpt <= 2) return launch_pdl(nv4_rows_kernel<BF16, T, 2>, grid, 128, 0, st, x, G, nb, q, bs, gs, status);
+    if (bpt <= 4) return launch_pdl(nv4_rows_kernel<BF16, T, 4>, grid, 128, 0, st, x, G, nb, q, bs, gs, status);
+    return launch_pdl(nv4_rows_kernel<BF16, T, 8>, grid, 128, 0, st, x, G, nb, q, bs, gs, status);
+}
+
+template <bool BF16>
+static int run_quantize(const void* x, int G, int rows, int cols, uint8_t* q, uint8_t* bs, float* gs, unsigned* amax,
+                        int32_t* status, cudaStream_t st) {
+    const int nb = cols / 16;
+    if (rows == 1)
+        return nb <= 32 ? launch_rows<BF16, 32>(x, G, nb, q, bs, gs, status, st)
+                        : launch_rows<BF16, 128>(x, G, nb, q, bs, gs, status, st);
+    const size_t per = (size_t)rows * nb;
+    int rc = to_status(cudaMemsetAsync(amax, 0, sizeof(unsigned) * (size_t)G, st));
+    if (rc) return rc;
+    size_t bx = (per + 255) / 256;
+    if (bx > 64) bx = 64;
+    const dim3 grid((unsigned)bx, (unsigned)G);
+    if ((rc = launch_pdl(nv4_amax_kernel<BF16>, grid, 256, 0, st, x, per, amax, status))) return rc;
+    return launch_pdl(nv4_encode_kernel<BF16>, grid, 256, 0, st, x, per, (const unsigned*)amax, q, bs, gs);
+}
+
+static int check_nvfp4(int G, int rows, int cols, int dtype) {
+    if (G < 0 || rows < 1 || cols < 32 || cols > MOE_MAX_DIM || (cols & 31)) return MOE_ERR_INVALID_ARG;
+    if (rows == 1 ? G > MOE_MAX_ROWS : G > 65535 || rows > 2 * MOE_MAX_DIM) return MOE_ERR_INVALID_ARG;
+    if (dtype != MOE_DT_F32 && dtype != MOE_DT_BF16) return MOE_ERR_INVALID_ARG;
+    return MOE_OK;
+}
+
+static bool aligned32(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 31u) == 0; }
+
+}  // namespace moe
+
+using namespace moe;
+
+extern "C" {
+
+int moe_grouped_gemm(const uint16_t* x, const uint16_t* w, const int32_t* offsets, int R, int N, int K, int E, void* y,
+                     int y_dtype, int32_t* dev_status, void* stream) {
+    int rc = check_grouped(R, N, K, E, y_dtype);
+    if (rc) return rc;
+    if (R == 0) return MOE_OK;
+    MOE_REQ(x);
+    MOE_REQ(w);
+    MOE_REQ(offsets);
+    MOE_REQ(y);
+    MOE_OPT(dev_status);
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    const int sms = sm_count();
+    // fewer tiles than SMs: the weights of a few rows stream faster through
+    // a warp per weight row on the whole GPU
+    if (R <= 32 && R * ceil_div(N, 128) < sms)
+        return launch_pdl(gg_gemv_kernel, dim3((unsigned)ceil_div(N, 8), (unsigned)R), 256, 0, st, x, w, offsets, R, N,
+                          K, E, y, (int)(y_dtype == MOE_DT_F32), dev_status);
+    GgParams p;
+    memset(&p, 0, sizeof p);
+    p.offsets = offsets;
+    p.out = y;
+    p.out_f32 = y_dtype == MOE_DT_F32;
+    p.status = dev_status;
+    return run_gg<kGgFwd>(p, w, x, R, N, K, E, st);
+}
+
+int moe_grouped_gemm_dx(const uint16_t* dy, const uint16_t* w, const int32_t* offsets, int R, int N, int K, int E,
+                        void* dx, int dx_dtype, int32_t* dev_status, void* stream) {
+    int rc = check_grouped(R, N, K, E, dx_dtype);
+    if (rc) return rc;
+    if (R == 0) return MOE_OK;
+    MOE_REQ(dy);
+    MOE_REQ(w);
+    MOE_REQ(offsets);
+    MOE_REQ(dx);
+    MOE_OPT(dev_status);
+    GgParams p;
+    memset(&p, 0, sizeof p);
+    p.offsets = offsets;
+    p.out = dx;
+    p.out_f32 = dx_dtype == MOE_DT_F32;
+    p.status = dev_status;
+    return run_gg<kGgDx>(p, w, dy, R, N, K, E, static_cast<cudaStream_t>(stream));
+}
+
+int moe_grouped_gemm_dw(const uint16_t* dy, const uint16_t* x, const int32_t* offsets, int R, int N, int K, int E,
+                        void* dw, int dw_dtype, int32_t* dev_status, void* stream) {
+    int rc = check_grouped(R, N, K, E, dw_dtype);
+    if (rc) return rc;
+    MOE_REQ(dw);
+    MOE_OPT(dev_status);
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    if (R == 0)
+        return to_status(cudaMemsetAsync(dw, 0, (size_t)E * N * K * (dw_dtype == MOE_DT_F32 ? 4 : 2), st));
+    MOE_REQ(dy);
+    MOE_REQ(x);
+    MOE_REQ(offsets);
+    GgParams p;
+    memset(&p, 0, sizeof p);
+    p.offsets = offsets;
+    p.out = dw;
+    p.out_f32 = dw_dtype == MOE_DT_F32;
+    p.status = dev_status;
+    return run_gg<kGgDw>(p, x, dy, R, N, K, E, st);
+}
+
+int moe_quantize_nvfp4_workspace_bytes(int G, int rows, int cols, size_t* bytes) {
+    const int rc = check_nvfp4(G, rows, cols, MOE_DT_F32);
+    if (rc) return rc;
+    if (!bytes) return MOE_ERR_INVALID_ARG;
+    *bytes = rows == 1 ? 0 : align_up(sizeof(unsigned) * (size_t)G, 256);
+    return MOE_OK;
+}
+
+int moe_quantize_nvfp4(const void* x, int x_dtype, int G, int rows, int cols, uint8_t* q, uint8_t* bs, float* gs,
+                       void* workspace, size_t workspace_bytes, int32_t* dev_status, void* stream) {
+    int rc = check_nvfp4(G, rows, cols, x_dtype);
+    if (rc) return rc;
+    if (G == 0) return MOE_OK;
+    MOE_REQ(x);
+    MOE_REQ(q);
+    MOE_REQ(bs);
+    MOE_REQ(gs);
+    MOE_OPT(dev_status);
+    if (!aligned32(x)) return MOE_ERR_INVALID_ARG;
+    size_t need = 0;
+    if ((rc = moe_quantize_nvfp4_workspace_bytes(G, rows, cols, &need))) return rc;
+    if (need > 0) {
+        if (!workspace || workspace_bytes < need) return MOE_ERR_WORKSPACE;
+        MOE_REQ(workspace);
+    }
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    unsigned* amax = static_cast<unsigned*>(workspace);
+    return x_dtype == MOE_DT_BF16 ? run_quantize<true>(x, G, rows, cols, q, bs, gs, amax, dev_status, st)
+                                  : run_quantize<false>(x, G, rows, cols, q, bs, gs, amax, dev_status, st);
+}
+
+int moe_dequantize_nvfp4(const uint8_t* q, const uint8_t* bs, const float* gs, int G, int rows, int cols, void* x,
+                         int x_dtype, void* stream) {
+    const int rc = check_nvfp4(G, rows, cols, x_dtype);
+    if (rc) return rc;
+    if (G == 0) return MOE_OK;
+    MOE_REQ(q);
+    MOE_REQ(bs);
+    MOE_REQ(gs);
+    MOE_REQ(x);
+    if (!aligned32(x)) return MOE_ERR_INVALID_ARG;
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    const size_t per = (size_t)rows * (cols / 16), n = per * G;
+    const int sms = sm_count();
+    size_t grid = (n + 255) / 256;
+    if (grid > (size_t)sms * 64) grid = (size_t)sms * 64;
+    return x_dtype == MOE_DT_BF16 ? launch_pdl(nv4_decode_kernel<true>, (unsigned)grid, 256, 0, st, q, bs, gs, per, n, x)
+                                  : launch_pdl(nv4_decode_kernel<false>, (unsigned)grid, 256, 0, st, q, bs, gs, per, n, x);
+}
+
+int moe_grouped_gemm_nvfp4(const uint8_t* xq, const uint8_t* xbs, const float* xgs, const uint8_t* wq, const uint8_t* wbs,
+                           const float* wgs, const int32_t* offsets, int R, int N, int K, int E, void* y, int y_dtype,
+                           int32_t* dev_status, void* stream) {
+    int rc = check_grouped(R, N, K, E, y_dtype);
+    if (rc) return rc;
+    if (K & 31) return MOE_ERR_INVALID_ARG;  // rows of codes in whole 16-byte pieces
+    if (R == 0) return MOE_OK;
+    MOE_REQ(xq);
+    MOE_REQ(xbs);
+    MOE_REQ(xgs);
+    MOE_REQ(wq);
+    MOE_REQ(wbs);
+    MOE_REQ(wgs);
+    MOE_REQ(offsets);
+    MOE_REQ(y);
+    MOE_OPT(dev_status);
+    G4Params p;
+    memset(&p, 0, sizeof p);
+    if (!encode_map(&p.ta, wq, true, K / 2, N, E, 128) || !encode_map(&p.tb, xq, true, K / 2, R, 0, kGgBoxN))
+        return MOE_ERR_UNSUPPORTED;
+    p.wbs = wbs;
+    p.xbs = xbs;
+    p.wgs = wgs;
+    p.xgs = xgs;
+    p.offsets = offsets;
+    p.E = E;
+    p.R = R;
+    p.M = N;
+    p.K = K;
+    p.out = y;
+    p.out_f32 = y_dtype == MOE_DT_F32;
+    p.status = dev_status;
+    const int sms = sm_count();
+    if (sms < 1) return MOE_ERR_CUDA;
+    if ((rc = allow_smem(g4_kernel, kGgSmem))) return rc;
+    return launch_pdl(g4_kernel, (unsigned)sms, kG4Threads, kGgSmem, static_cast<cudaStream_t>(stream), p);
+}
+
+}  // extern "C"
