@@ -88,26 +88,17 @@ __device__ __forceinline__ void cluster_sync() {
     asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
-// Arrive on the barrier at the same place in CTA `rank` of the cluster.
+// Arrive on the barrier at the same place in CTA `rank` of the cluster.  The
+// default semantics: what is handed over is asynchronous-proxy data (landed
+// TMA tiles, read tensor memory), and a cluster-scope release would make the
+// thread wait for its global stores.
 __device__ __forceinline__ void mbar_arrive_cluster(uint64_t* bar, uint32_t rank) {
     asm volatile(
         "{\n\t.reg .b32 ra;\n\t"
         "mapa.shared::cluster.u32 ra, %0, %1;\n\t"
-        "mbarrier.arrive.release.cluster.shared::cluster.b64 _, [ra];\n\t}" ::"r"(smem_u32(bar)),
+        "mbarrier.arrive.shared::cluster.b64 _, [ra];\n\t}" ::"r"(smem_u32(bar)),
         "r"(rank)
         : "memory");
-}
-
-__device__ __forceinline__ bool mbar_try_wait_cluster(uint64_t* bar, uint32_t parity) {
-    uint32_t ok;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(ok)
-        : "r"(smem_u32(bar)), "r"(parity)
-        : "memory");
-    return ok != 0;
 }
 
 // MN-major operand, 128-byte swizzle: 64 elements (128 bytes) of the M or N
@@ -185,15 +176,6 @@ __device__ __forceinline__ void gg_tmem_dealloc(uint32_t taddr, uint32_t ncols) 
 __device__ __forceinline__ bool gg_wait(uint64_t* bar, uint32_t parity, int* abort) {
     for (uint32_t i = 0; i < kGgWaitLimit; ++i) {
         if (mbar_try_wait(bar, parity)) return true;
-        if ((i & 63u) == 63u && *(volatile int*)abort) return false;
-    }
-    *(volatile int*)abort = 1;
-    return false;
-}
-
-__device__ __forceinline__ bool gg_wait_cluster(uint64_t* bar, uint32_t parity, int* abort) {
-    for (uint32_t i = 0; i < kGgWaitLimit; ++i) {
-        if (mbar_try_wait_cluster(bar, parity)) return true;
         if ((i & 63u) == 63u && *(volatile int*)abort) return false;
     }
     *(volatile int*)abort = 1;
@@ -380,7 +362,7 @@ __global__ void __launch_bounds__(kGgThreads, 1) gg_kernel(const __grid_constant
             if (nk == 0) return true;
             const int buf = d & 1, use = d >> 1;
             ++d;
-            if (rank == 0 && use > 0 && !gg_wait_cluster(&sh->acc_empty[buf], (uint32_t)((use - 1) & 1), &sh->abort))
+            if (rank == 0 && use > 0 && !gg_wait(&sh->acc_empty[buf], (uint32_t)((use - 1) & 1), &sh->abort))
                 return false;
             tc_fence_after();
             const uint32_t tacc = tmem + (uint32_t)(buf * Cfg::BN);
@@ -408,6 +390,7 @@ __global__ void __launch_bounds__(kGgThreads, 1) gg_kernel(const __grid_constant
                                 make_uint4(0, 0, 0, 0);
                         }
                         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                        if (rank != 0) asm volatile("fence.acq_rel.cluster;" ::: "memory");
                         __syncwarp();
                     }
                 }
@@ -415,7 +398,7 @@ __global__ void __launch_bounds__(kGgThreads, 1) gg_kernel(const __grid_constant
                     if (lane == 0) mbar_arrive_cluster(&sh->pfull[s], 0);
                     continue;
                 }
-                if (CG == 2 && !gg_wait_cluster(&sh->pfull[s], ph, &sh->abort)) return false;
+                if (CG == 2 && !gg_wait(&sh->pfull[s], ph, &sh->abort)) return false;
                 tc_fence_after();
                 if (lane == 0) {
                     const uint32_t sta = smem_u32(st);
