@@ -605,21 +605,38 @@ def stack_forward(x, layers, top_k, flags=0, stream=None, status=None):
 
 
 # ------------------------------------------------- grouped products and NVFP4
+# (checks and marshalling kept short: these calls serve single decoded tokens too)
 _OUT = {torch.float32: MOE_DT_F32, torch.bfloat16: MOE_DT_BF16}
 
 
-def _on(dev, stream):
-    """The context of an operator call: x's device current, and the stream the
-    kernels go to (torch allocates the outputs for it)."""
+def _is(t, name, dtype, shape, dev):
+    """t is a contiguous tensor of this type and shape on dev (an operator's x
+    sets dev)."""
+    if t.dtype is not dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if dev.type != "cuda" or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous CUDA tensor")
+    if t.device != dev:
+        raise ValueError(f"{name} is on {t.device}, x on {dev}")
+
+
+def _dims(t, name, what, *dims):
+    if t.dim() not in dims:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {what}")
+
+
+def _on(dev, stream, call):
+    """call(stream handle) with dev current and torch's allocations made for
+    the stream that the kernels go to."""
     if stream is not None and stream.device != dev:
         raise ValueError(f"stream is on {stream.device}, x on {dev}")
-    return torch.cuda.stream(stream if stream is not None else torch.cuda.current_stream(dev))
-
-
-def _need_2d(t, dtype, name, what):
-    if t.dim() != 2:
-        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {what}")
-    _need(t, dtype, name)
+    here = torch.cuda.current_stream(dev)
+    if (stream is None or stream == here) and torch.cuda.current_device() == dev.index:
+        return call(here.cuda_stream)
+    with torch.cuda.stream(here if stream is None else stream):
+        return call((here if stream is None else stream).cuda_stream)
 
 
 def _out(out, shape, out_dtype, dev):
@@ -628,25 +645,31 @@ def _out(out, shape, out_dtype, dev):
         if out_dtype not in _OUT:
             raise TypeError("out_dtype must be float32 or bfloat16")
         return torch.empty(shape, dtype=out_dtype, device=dev)
-    _shape(out, shape, "out")
     if out.dtype not in _OUT:
         raise TypeError("out must be float32 or bfloat16")
-    _opt(out, None, "out", dev)
+    _is(out, "out", out.dtype, shape, dev)
     return out
 
 
-def _grouped(fn, a, b, offsets, R, N, K, E, shape, out_dtype, out, status, stream):
+def _status_ptr(status, dev):
+    if status is None:
+        return None
+    _is(status, "status", torch.int32, (1,), dev)
+    return status.data_ptr()
+
+
+def _grouped(name, fn, a, b, offsets, R, N, K, E, shape, out_dtype, out, status, stream):
     dev = a.device
-    _shape(offsets, (E + 1,), "offsets")
-    _shape(status, (1,), "status")
-    _opt(b, torch.bfloat16, "the second operand", dev)
-    _opt(offsets, torch.int32, "offsets", dev)
-    _opt(status, torch.int32, "status", dev)
-    with _on(dev, stream):
+    _is(offsets, "offsets", torch.int32, (E + 1,), dev)
+    st = _status_ptr(status, dev)
+
+    def call(handle):
         y = _out(out, shape, out_dtype, dev)
-        _check(getattr(_lib, fn)(_ptr(a), _ptr(b), _ptr(offsets), R, N, K, E, _ptr(y), _OUT[y.dtype], _ptr(status),
-                                 _stream(stream)), fn)
-    return y
+        _check(fn(a.data_ptr(), b.data_ptr(), offsets.data_ptr(), R, N, K, E, y.data_ptr(), _OUT[y.dtype], st, handle),
+               name)
+        return y
+
+    return _on(dev, stream, call)
 
 
 def grouped_gemm(x, w, offsets, out_dtype=torch.float32, out=None, status=None, stream=None):
@@ -655,39 +678,55 @@ def grouped_gemm(x, w, offsets, out_dtype=torch.float32, out=None, status=None, 
     x [R,K] bf16, w [E,N,K] bf16, offsets [E+1] int32 on the device (as
     group_by_expert returns them).  Rows that no segment holds are left as
     they were in `out`, and are undefined in a new tensor."""
-    _need_2d(x, torch.bfloat16, "x", "[R, K]")
+    _dims(x, "x", "[R, K]", 2)
+    _dims(w, "w", "[E, N, K]", 3)
     R, K = x.shape
-    _shape(w, (None, None, K), "w")
     E, N, _ = w.shape
-    return _grouped("moe_grouped_gemm", x, w, offsets, R, N, K, E, (R, N), out_dtype, out, status, stream)
+    _is(x, "x", torch.bfloat16, (R, K), x.device)
+    _is(w, "w", torch.bfloat16, (E, N, K), x.device)
+    return _grouped("moe_grouped_gemm", _lib.moe_grouped_gemm, x, w, offsets, R, N, K, E, (R, N), out_dtype, out,
+                    status, stream)
 
 
 def grouped_gemm_dx(dy, w, offsets, out_dtype=torch.float32, out=None, status=None, stream=None):
     """dx [R,K]: the gradient of grouped_gemm with respect to x, row r of
     segment e being w[e]^T dy[r]; dy [R,N] bf16, w [E,N,K] bf16."""
-    _need_2d(dy, torch.bfloat16, "dy", "[R, N]")
+    _dims(dy, "dy", "[R, N]", 2)
+    _dims(w, "w", "[E, N, K]", 3)
     R, N = dy.shape
-    _shape(w, (None, N, None), "w")
     E, _, K = w.shape
-    return _grouped("moe_grouped_gemm_dx", dy, w, offsets, R, N, K, E, (R, K), out_dtype, out, status, stream)
+    _is(dy, "dy", torch.bfloat16, (R, N), dy.device)
+    _is(w, "w", torch.bfloat16, (E, N, K), dy.device)
+    return _grouped("moe_grouped_gemm_dx", _lib.moe_grouped_gemm_dx, dy, w, offsets, R, N, K, E, (R, K), out_dtype, out,
+                    status, stream)
 
 
 def grouped_gemm_dw(dy, x, offsets, out_dtype=torch.float32, out=None, status=None, stream=None):
     """dw [E,N,K]: the gradient of grouped_gemm with respect to w, the sum of
     dy[r] x[r]^T over segment e's rows (zeros where it has none); dy [R,N]
     bf16, x [R,K] bf16, E = len(offsets) - 1."""
-    _need_2d(dy, torch.bfloat16, "dy", "[R, N]")
+    _dims(dy, "dy", "[R, N]", 2)
+    _dims(x, "x", "[R, K]", 2)
+    _dims(offsets, "offsets", "[E + 1]", 1)
     R, N = dy.shape
-    _shape(x, (R, None), "x")
     K = x.shape[1]
-    E = offsets.numel() - 1
-    return _grouped("moe_grouped_gemm_dw", dy, x, offsets, R, N, K, E, (E, N, K), out_dtype, out, status, stream)
+    E = offsets.shape[0] - 1
+    _is(dy, "dy", torch.bfloat16, (R, N), dy.device)
+    _is(x, "x", torch.bfloat16, (R, K), dy.device)
+    return _grouped("moe_grouped_gemm_dw", _lib.moe_grouped_gemm_dw, dy, x, offsets, R, N, K, E, (E, N, K), out_dtype,
+                    out, status, stream)
 
 
-def _nvfp4_shape(t):
-    if t.dim() not in (2, 3):
-        raise ValueError(f"x has shape {tuple(t.shape)}, expected [R, C] (a scale a row) or [G, R, C] (a scale a matrix)")
+def _nvfp4_dims(t, name):
+    """-> (groups, rows a group, columns) of a [R,C] (a scale a row) or
+    [G,R,C] (a scale a matrix) tensor."""
+    _dims(t, name, "[R, C] (a scale a row) or [G, R, C] (a scale a matrix)", 2, 3)
     return (t.shape[0], 1, t.shape[1]) if t.dim() == 2 else tuple(t.shape)
+
+
+def _nvfp4_cols(cols, name):
+    if cols % 32:
+        raise ValueError(f"NVFP4 rows need a multiple of 32 elements, {name} has {cols}")
 
 
 def quantize_nvfp4(x, out=None, workspace=None, status=None, stream=None):
@@ -697,82 +736,79 @@ def quantize_nvfp4(x, out=None, workspace=None, status=None, stream=None):
     x fp32 or bf16: [G,R,C] matrices with one scale each (gs [G], the layout
     of stack_forward_nvfp4_), or [R,C] rows with one scale each (gs [R]).
     `out` is such a triple to be written."""
-    _x_dtype(x)
-    G, rows, cols = _nvfp4_shape(x)
-    if not x.is_cuda or not x.is_contiguous():
-        raise ValueError("x must be a contiguous CUDA tensor")
-    if cols % 32:
-        raise ValueError(f"NVFP4 rows need a multiple of 32 elements, x has {cols}")
-    dev, lead = x.device, tuple(x.shape[:-1])
-    _shape(status, (1,), "status")
-    _opt(status, torch.int32, "status", dev)
-    _opt(workspace, torch.uint8, "workspace", dev)
+    G, rows, cols = _nvfp4_dims(x, "x")
+    _nvfp4_cols(cols, "x")
+    dt = _x_dtype(x)
+    dev, lead = x.device, x.shape[:-1]
+    _is(x, "x", x.dtype, x.shape, dev)
+    st = _status_ptr(status, dev)
+    if workspace is not None:
+        _is(workspace, "workspace", torch.uint8, workspace.shape, dev)
     if out is not None:
-        for t, shp, dt, n in zip(out, ((*lead, cols // 2), (*lead, cols // 16), (G,)),
-                                 (torch.uint8, torch.uint8, torch.float32), ("out q", "out bs", "out gs")):
-            _shape(t, shp, n)
-            _opt(t, dt, n, dev)
-    with _on(dev, stream):
-        if out is None:
-            out = (torch.empty((*lead, cols // 2), dtype=torch.uint8, device=dev),
-                   torch.empty((*lead, cols // 16), dtype=torch.uint8, device=dev),
-                   torch.empty((G,), dtype=torch.float32, device=dev))
-        q, bs, gs = out
-        if workspace is None and rows > 1:
+        _is(out[0], "out q", torch.uint8, (*lead, cols // 2), dev)
+        _is(out[1], "out bs", torch.uint8, (*lead, cols // 16), dev)
+        _is(out[2], "out gs", torch.float32, (G,), dev)
+
+    def call(handle):
+        q, bs, gs = out if out is not None else (torch.empty((*lead, cols // 2), dtype=torch.uint8, device=dev),
+                                                 torch.empty((*lead, cols // 16), dtype=torch.uint8, device=dev),
+                                                 torch.empty((G,), dtype=torch.float32, device=dev))
+        ws = workspace
+        if ws is None and rows > 1:
             n = _S(0)
             _check(_lib.moe_quantize_nvfp4_workspace_bytes(G, rows, cols, ctypes.byref(n)),
                    "moe_quantize_nvfp4_workspace_bytes")
-            workspace = torch.empty(n.value, dtype=torch.uint8, device=dev)
-        _check(_lib.moe_quantize_nvfp4(_ptr(x), _x_dtype(x), G, rows, cols, _ptr(q), _ptr(bs), _ptr(gs),
-                                       _ptr(workspace), workspace.numel() if workspace is not None else 0,
-                                       _ptr(status), _stream(stream)), "moe_quantize_nvfp4")
-    return q, bs, gs
+            ws = torch.empty(n.value, dtype=torch.uint8, device=dev)
+        wp, wn = (None, 0) if ws is None else (ws.data_ptr(), ws.numel())
+        _check(_lib.moe_quantize_nvfp4(x.data_ptr(), dt, G, rows, cols, q.data_ptr(), bs.data_ptr(), gs.data_ptr(), wp,
+                                       wn, st, handle), "moe_quantize_nvfp4")
+        return q, bs, gs
 
-
-def _need_nvfp4(q, bs, gs, name):
-    """Shape checks of an NVFP4 triple -> its elements a row."""
-    _need(q, torch.uint8, f"{name} codes")
-    cols = 2 * q.shape[-1]
-    if cols % 32:
-        raise ValueError(f"NVFP4 rows need a multiple of 32 elements, {name} has {cols}")
-    _shape(bs, (*q.shape[:-1], cols // 16), f"{name} block scales")
-    _shape(gs, (q.shape[0],), f"{name} scales")
-    _opt(bs, torch.uint8, f"{name} block scales", q.device)
-    _opt(gs, torch.float32, f"{name} scales", q.device)
-    return cols
+    return _on(dev, stream, call)
 
 
 def dequantize_nvfp4(q, bs, gs, out_dtype=torch.float32, out=None, stream=None):
     """The values of quantize_nvfp4's triple: (e2m1(q) * e4m3(bs)) * gs."""
-    G, rows, _ = _nvfp4_shape(q)
-    cols = _need_nvfp4(q, bs, gs, "x")
-    dev = q.device
-    with _on(dev, stream):
-        x = _out(out, (*q.shape[:-1], cols), out_dtype, dev)
-        _check(_lib.moe_dequantize_nvfp4(_ptr(q), _ptr(bs), _ptr(gs), G, rows, cols, _ptr(x), _OUT[x.dtype],
-                                         _stream(stream)), "moe_dequantize_nvfp4")
-    return x
+    G, rows, half = _nvfp4_dims(q, "q")
+    cols, dev, lead = 2 * half, q.device, q.shape[:-1]
+    _nvfp4_cols(cols, "q")
+    _is(q, "q", torch.uint8, q.shape, dev)
+    _is(bs, "bs", torch.uint8, (*lead, cols // 16), dev)
+    _is(gs, "gs", torch.float32, (G,), dev)
+
+    def call(handle):
+        x = _out(out, (*lead, cols), out_dtype, dev)
+        _check(_lib.moe_dequantize_nvfp4(q.data_ptr(), bs.data_ptr(), gs.data_ptr(), G, rows, cols, x.data_ptr(),
+                                         _OUT[x.dtype], handle), "moe_dequantize_nvfp4")
+        return x
+
+    return _on(dev, stream, call)
 
 
 def grouped_gemm_nvfp4(xq, xbs, xgs, wq, wbs, wgs, offsets, out_dtype=torch.float32, out=None, status=None,
                        stream=None):
     """grouped_gemm with both operands in NVFP4: x as quantize_nvfp4 returns a
     [R,K] tensor (a scale a row), w as it returns [E,N,K] (a scale a matrix)."""
-    if xq.dim() != 2 or wq.dim() != 3:
-        raise ValueError(f"xq {tuple(xq.shape)} and wq {tuple(wq.shape)} must be [R, K/2] and [E, N, K/2]")
-    _shape(wq, (None, None, xq.shape[1]), "wq")
-    K = _need_nvfp4(xq, xbs, xgs, "x")
-    _need_nvfp4(wq, wbs, wgs, "w")
-    R, (E, N, _) = xq.shape[0], wq.shape
-    dev = xq.device
-    _opt(wq, torch.uint8, "wq", dev)
-    _shape(offsets, (E + 1,), "offsets")
-    _shape(status, (1,), "status")
-    _opt(offsets, torch.int32, "offsets", dev)
-    _opt(status, torch.int32, "status", dev)
-    with _on(dev, stream):
+    _dims(xq, "xq", "[R, K/2]", 2)
+    _dims(wq, "wq", "[E, N, K/2]", 3)
+    R, half = xq.shape
+    E, N, _ = wq.shape
+    K, dev = 2 * half, xq.device
+    _nvfp4_cols(K, "xq")
+    _is(xq, "xq", torch.uint8, (R, half), dev)
+    _is(xbs, "xbs", torch.uint8, (R, K // 16), dev)
+    _is(xgs, "xgs", torch.float32, (R,), dev)
+    _is(wq, "wq", torch.uint8, (E, N, half), dev)
+    _is(wbs, "wbs", torch.uint8, (E, N, K // 16), dev)
+    _is(wgs, "wgs", torch.float32, (E,), dev)
+    _is(offsets, "offsets", torch.int32, (E + 1,), dev)
+    st = _status_ptr(status, dev)
+
+    def call(handle):
         y = _out(out, (R, N), out_dtype, dev)
-        _check(_lib.moe_grouped_gemm_nvfp4(_ptr(xq), _ptr(xbs), _ptr(xgs), _ptr(wq), _ptr(wbs), _ptr(wgs),
-                                           _ptr(offsets), R, N, K, E, _ptr(y), _OUT[y.dtype], _ptr(status),
-                                           _stream(stream)), "moe_grouped_gemm_nvfp4")
-    return y
+        _check(_lib.moe_grouped_gemm_nvfp4(xq.data_ptr(), xbs.data_ptr(), xgs.data_ptr(), wq.data_ptr(), wbs.data_ptr(),
+                                           wgs.data_ptr(), offsets.data_ptr(), R, N, K, E, y.data_ptr(), _OUT[y.dtype],
+                                           st, handle), "moe_grouped_gemm_nvfp4")
+        return y
+
+    return _on(dev, stream, call)

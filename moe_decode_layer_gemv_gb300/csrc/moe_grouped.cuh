@@ -224,6 +224,101 @@ __device__ __forceinline__ void gg_segments(GgShared* sh, const int32_t* offsets
     __syncthreads();
 }
 
+// ------------------------------------------------------------- epilogue
+// 32 consecutive fp32 columns of this warp's 32 TMEM lanes; the registers are
+// valid after gg_ld_wait (which names them, so that no use moves above it).
+__device__ __forceinline__ void gg_ld32(uint32_t taddr, uint32_t (&r)[32]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,"
+        "%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
+          "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+          "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+        : "r"(taddr)
+        : "memory");
+}
+
+__device__ __forceinline__ void gg_ld_wait(uint32_t (&r)[32]) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
+                   "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]),
+                   "+r"(r[16]), "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]), "+r"(r[23]),
+                   "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]), "+r"(r[30]), "+r"(r[31])
+                 :
+                 : "memory");
+}
+
+// This lane's two neighbouring m of one row, in bf16, from the values of two
+// rows in lanes 2i and 2i + 1: the even lane keeps the first row, the odd the second.
+__device__ __forceinline__ uint32_t gg_pair(uint32_t first, uint32_t second, int odd) {
+    const uint32_t other = __shfl_xor_sync(0xffffffffu, odd ? first : second, 1);
+    const __nv_bfloat162 b =
+        __floats2bfloat162_rn(__uint_as_float(odd ? other : first), __uint_as_float(odd ? second : other));
+    return *reinterpret_cast<const uint32_t*>(&b);
+}
+
+// Store 32 columns (output rows row0 .. row0 + nc - 1) of this lane's m:
+// fp32 as they are, a warp writing 128 contiguous bytes a row; bf16 after
+// lanes 2i and 2i + 1 have exchanged a value per pair of rows, so that each
+// lane writes two neighbouring m (4 bytes) of one row.
+__device__ __forceinline__ void gg_store32(const uint32_t (&r)[32], void* out, int out_f32, size_t row0, int nc, int m,
+                                           int M) {
+    const bool whole = nc >= 32;
+    if (out_f32) {
+        uint32_t* o = static_cast<uint32_t*>(out) + row0 * (size_t)M + m;
+        if (m >= M) return;
+        if (whole) {
+#pragma unroll
+            for (int j = 0; j < 32; ++j, o += M) *o = r[j];
+        } else {
+#pragma unroll
+            for (int j = 0; j < 32; ++j, o += M)
+                if (j < nc) *o = r[j];
+        }
+        return;
+    }
+    const int odd = m & 1;
+    uint32_t* o = reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(out) + (row0 + odd) * (size_t)M + (m - odd));
+    const int last = m < M ? nc - odd : 0;  // rows row0 + odd + j, j < last
+    if (__all_sync(0xffffffffu, whole && m < M)) {
+#pragma unroll
+        for (int j = 0; j < 32; j += 2, o += M) *o = gg_pair(r[j], r[j + 1], odd);
+    } else {
+#pragma unroll
+        for (int j = 0; j < 32; j += 2, o += M) {
+            const uint32_t v = gg_pair(r[j], r[j + 1], odd);
+            if (j < last) *o = v;
+        }
+    }
+}
+
+// The columns of one accumulator, 32 at a time, the next 32 on their way
+// while these are stored; `done` runs once they are all in registers.
+template <typename Scale, typename Done>
+__device__ __forceinline__ void gg_epilogue(uint32_t taddr, void* out, int out_f32, size_t row0, int n, int m, int M,
+                                            Scale scale, Done done) {
+    uint32_t a[32], b[32];
+    gg_ld32(taddr, a);
+    for (int c = 0; c < n; c += 64) {
+        gg_ld_wait(a);
+        if (c + 32 < n)
+            gg_ld32(taddr + c + 32, b);
+        else
+            done();
+        scale(a, c);
+        gg_store32(a, out, out_f32, row0 + c, min(32, n - c), m, M);
+        if (c + 32 >= n) break;
+        gg_ld_wait(b);
+        if (c + 64 < n)
+            gg_ld32(taddr + c + 64, a);
+        else
+            done();
+        scale(b, c + 32);
+        gg_store32(b, out, out_f32, row0 + c + 32, min(32, n - c - 32), m, M);
+    }
+}
+
 // ------------------------------------------------------------- the kernel
 // Persistent: one CTA per SM (or one pair of CTAs per SM pair) walks the
 // tiles.  Three roles run through the same tile sequence, each at its own
@@ -428,49 +523,31 @@ __global__ void __launch_bounds__(kGgThreads, 1) gg_kernel(const __grid_constant
         walk([&](int e, int q0, int n, int n0, int m0, int nk) -> bool {
             const int m = m0 + (int)rank * 128 + (int)threadIdx.x;
             const size_t row0 = MODE == kGgDw ? (size_t)e * p.NW + n0 : (size_t)q0;
-            const size_t at0 = row0 * (size_t)p.M + m;
-            const bool live = m < p.M;
-            int buf = 0;
-            if (nk > 0) {
-                buf = d & 1;
-                const int use = d >> 1;
-                ++d;
-                if (!gg_wait(&sh->acc_full[buf], (uint32_t)(use & 1), &sh->abort)) return false;
-                __syncwarp();
-                tc_fence_after();
+            if (MODE == kGgDw && nk == 0) {  // no rows: zeros
+                uint32_t z[32];
+#pragma unroll
+                for (int j = 0; j < 32; ++j) z[j] = 0;
+                for (int c = 0; c < n; c += 32) gg_store32(z, p.out, p.out_f32, row0 + c, min(32, n - c), m, p.M);
+                return true;
             }
-            const uint32_t row_addr = tmem + (uint32_t)(buf * Cfg::BN) + ((uint32_t)(warp * 32) << 16);
-            for (int c0 = 0; c0 < n; c0 += 16) {
-                float v[16];
-                if (nk > 0) {
-                    tmem_ld16(row_addr + c0, v);
-                    if (c0 + 16 >= n) {
-                        tc_fence_before();
-                        __syncwarp();
-                        if (lane == 0) {
-                            if (CG == 1)
-                                mbar_arrive(&sh->acc_empty[buf]);
-                            else
-                                mbar_arrive_cluster(&sh->acc_empty[buf], 0);
-                        }
-                    }
-                } else {
-#pragma unroll
-                    for (int j = 0; j < 16; ++j) v[j] = 0.0f;
-                }
-                const int nc = min(16, n - c0);
-                if (live) {
-                    size_t at = at0 + (size_t)c0 * p.M;
-#pragma unroll
-                    for (int j = 0; j < 16; ++j, at += p.M) {
-                        if (j >= nc) break;
-                        if (p.out_f32)
-                            static_cast<float*>(p.out)[at] = v[j];
+            const int buf = d & 1, use = d >> 1;
+            ++d;
+            if (!gg_wait(&sh->acc_full[buf], (uint32_t)(use & 1), &sh->abort)) return false;
+            __syncwarp();
+            tc_fence_after();
+            gg_epilogue(
+                tmem + (uint32_t)(buf * Cfg::BN) + ((uint32_t)(warp * 32) << 16), p.out, p.out_f32, row0, n, m, p.M,
+                [](uint32_t(&)[32], int) {},
+                [&]() {
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) {
+                        if (CG == 1)
+                            mbar_arrive(&sh->acc_empty[buf]);
                         else
-                            static_cast<uint16_t*>(p.out)[at] = f2bf_bits(v[j]);
+                            mbar_arrive_cluster(&sh->acc_empty[buf], 0);
                     }
-                }
-            }
+                });
             return true;
         });
     }

@@ -255,6 +255,11 @@ constexpr int kG4Sf = 2048;           // scales of 128 rows x 256 elements
 constexpr int kG4MaxStages = 9;
 constexpr uint32_t kG4SfCol = 256;    // tensor-memory column of the scales, behind two 128-column accumulators
 
+template <int V>
+struct IntC {
+    static constexpr int value = V;
+};
+
 struct G4Params {
     CUtensorMap ta, tb;  // wq [E, N, K/2], xq [R, K/2] bytes
     const uint8_t *wbs, *xbs;
@@ -300,17 +305,17 @@ __device__ __forceinline__ void umma_nvfp4(uint32_t tmem_d, uint64_t adesc, uint
 }
 
 // The 16 scale bytes of a row from block k0 on; blocks from nb on read as 0.
-__device__ __forceinline__ uint4 g4_row_scales(const uint8_t* row, int k0, int nb, bool live) {
-    uint4 r = make_uint4(0, 0, 0, 0);
-    if (!live) return r;
+// VEC: bytes a load, by the alignment that nb gives every row (16, 4 or 2).
+template <int VEC>
+__device__ __forceinline__ uint4 g4_row_scales(const uint8_t* row, int k0, int nb) {
     const uint8_t* p = row + k0;
-    if ((nb & 15) == 0) return __ldg(reinterpret_cast<const uint4*>(p));
+    if (VEC == 16) return __ldg(reinterpret_cast<const uint4*>(p));
     uint32_t w[4] = {0, 0, 0, 0};
-    if ((nb & 3) == 0) {
+    if (VEC == 4) {
 #pragma unroll
         for (int i = 0; i < 4; ++i)
             if (k0 + 4 * i < nb) w[i] = __ldg(reinterpret_cast<const uint32_t*>(p + 4 * i));
-    } else {  // nb is even: K % 32 == 0
+    } else {
 #pragma unroll
         for (int i = 0; i < 8; ++i)
             if (k0 + 2 * i < nb)
@@ -432,20 +437,16 @@ __global__ void __launch_bounds__(kG4Threads, 1) g4_kernel(const __grid_constant
         }
         __syncwarp();
     } else if (warp >= 6) {
-        // ---------------- scales: warp 6 + i takes every fourth stage
-        uint32_t g = 0;
-        walk([&](int e, int q0, int n, int m0) -> bool {
-            for (int k = 0; k < nk; ++k, ++g) {
-                if ((int)(g % kG4ScaleWarps) != warp - 6) continue;
-                uint4 a[4], b[4];
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const int m = m0 + 32 * j + lane, r = 32 * j + lane;
-                    a[j] = g4_row_scales(p.wbs + ((size_t)e * p.M + m) * nb, k * 16, nb, m < p.M);
-                    b[j] = g4_row_scales(p.xbs + (size_t)(q0 + r) * nb, k * 16, nb, r < n);
-                }
-                const uint32_t s = g % S, ph = (g / S) & 1u;
-                if (g >= S && !gg_wait(&sh->empty[s], ph ^ 1u, &sh->abort)) return false;
+        // ---------------- scales: warp 6 + i takes every fourth stage, and
+        // has the next one's on their way while it waits to store these
+        auto scales = [&](auto vec) {
+            constexpr int VEC = decltype(vec)::value;
+            uint32_t g = 0, have = 0;  // stages walked; the stage in `a` and `b` (valid when any)
+            bool any = false;
+            uint4 a[4], b[4];
+            auto put = [&]() -> bool {
+                const uint32_t s = have % S, ph = (have / S) & 1u;
+                if (have >= S && !gg_wait(&sh->empty[s], ph ^ 1u, &sh->abort)) return false;
                 uint4* sa = reinterpret_cast<uint4*>(ring + (size_t)s * stage_bytes + kG4A);
                 uint4* sb = sa + kG4Sf / 16;
                 sa[lane] = make_uint4(a[0].x, a[1].x, a[2].x, a[3].x);
@@ -459,44 +460,72 @@ __global__ void __launch_bounds__(kG4Threads, 1) g4_kernel(const __grid_constant
                 asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&s4->sfull[s]);
-            }
-            return true;
-        });
+                return true;
+            };
+            walk([&](int e, int q0, int n, int m0) -> bool {
+                // rows beyond the tile's end take the last one's scales: what
+                // they scale is never stored
+                const uint8_t *ra[4], *rb[4];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    ra[j] = p.wbs + ((size_t)e * p.M + min(m0 + 32 * j + lane, p.M - 1)) * nb;
+                    rb[j] = p.xbs + (size_t)(q0 + min(32 * j + lane, n - 1)) * nb;
+                }
+                for (int k = 0; k < nk; ++k, ++g) {
+                    if ((int)(g % kG4ScaleWarps) != warp - 6) continue;
+                    uint4 na[4], nb4[4];
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        na[j] = g4_row_scales<VEC>(ra[j], k * 16, nb);
+                        nb4[j] = g4_row_scales<VEC>(rb[j], k * 16, nb);
+                    }
+                    if (any && !put()) return false;
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        a[j] = na[j];
+                        b[j] = nb4[j];
+                    }
+                    have = g;
+                    any = true;
+                }
+                return true;
+            });
+            if (any) put();
+        };
+        if ((nb & 15) == 0)
+            scales(IntC<16>{});
+        else if ((nb & 3) == 0)
+            scales(IntC<4>{});
+        else
+            scales(IntC<2>{});
     } else {
         int d = 0;
         walk([&](int e, int q0, int n, int m0) -> bool {
             const int m = m0 + (int)threadIdx.x;
-            const size_t at0 = (size_t)q0 * (size_t)p.M + m;
-            const bool live = m < p.M;
             const float wg = __ldg(p.wgs + e);
+            float xg[kG4Bn / 32];  // the scales of rows q0 + 32 i + lane
+#pragma unroll
+            for (int i = 0; i < kG4Bn / 32; ++i) xg[i] = 32 * i + lane < n ? __ldg(p.xgs + q0 + 32 * i + lane) : 0.0f;
             const int buf = d & 1, use = d >> 1;
             ++d;
             if (!gg_wait(&sh->acc_full[buf], (uint32_t)(use & 1), &sh->abort)) return false;
             __syncwarp();
             tc_fence_after();
-            const uint32_t row_addr = tmem + (uint32_t)(buf * kG4Bn) + ((uint32_t)(warp * 32) << 16);
-            for (int c0 = 0; c0 < n; c0 += 16) {
-                float v[16];
-                tmem_ld16(row_addr + c0, v);
-                if (c0 + 16 >= n) {
+            gg_epilogue(
+                tmem + (uint32_t)(buf * kG4Bn) + ((uint32_t)(warp * 32) << 16), p.out, p.out_f32, (size_t)q0, n, m, p.M,
+                [&](uint32_t(&v)[32], int c) {
+                    float mine = xg[0];
+#pragma unroll
+                    for (int i = 1; i < kG4Bn / 32; ++i) mine = c == 32 * i ? xg[i] : mine;
+#pragma unroll
+                    for (int j = 0; j < 32; ++j)
+                        v[j] = __float_as_uint(__uint_as_float(v[j]) * __shfl_sync(0xffffffffu, mine, j) * wg);
+                },
+                [&]() {
                     tc_fence_before();
                     __syncwarp();
                     if (lane == 0) mbar_arrive(&sh->acc_empty[buf]);
-                }
-                const int nc = min(16, n - c0);
-                if (live) {
-                    size_t at = at0 + (size_t)c0 * p.M;
-#pragma unroll
-                    for (int j = 0; j < 16; ++j, at += p.M) {
-                        if (j >= nc) break;
-                        const float o = v[j] * __ldg(p.xgs + q0 + c0 + j) * wg;
-                        if (p.out_f32)
-                            static_cast<float*>(p.out)[at] = o;
-                        else
-                            static_cast<uint16_t*>(p.out)[at] = f2bf_bits(o);
-                    }
-                }
-            }
+                });
             return true;
         });
     }
