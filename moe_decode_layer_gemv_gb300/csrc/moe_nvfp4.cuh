@@ -241,19 +241,32 @@ __global__ void __launch_bounds__(256) nv4_decode_kernel(const uint8_t* __restri
 // y[r, n] = xgs[r] wgs[e] sum_k (xq bs)(wq bs): tcgen05.mma block-scaled
 // (kind::mxf4nvf4, one E4M3 scale per 16 elements), fp32 accumulation.  The
 // codes go to shared memory by TMA like the bf16 operands (a 128-byte row
-// holds 256 elements); the scales are read row by row (16 bytes = the 16
-// blocks of those 256 elements), rearranged in registers and copied to
-// tensor memory by tcgen05.cp: the MMA of 64 elements takes four scale bytes
-// a row as one 32-bit column word, rows 32 j + i at lane i of column j.  A
-// lane that loads rows i, i + 32, i + 64 and i + 96 holds exactly the 16
-// bytes that one lane of four columns wants for each 64-element step.
-constexpr int kG4Threads = 320;  // warps 0-3 epilogue, 4 TMA, 5 MMA, 6-9 scales
-constexpr int kG4ScaleWarps = 4;
-constexpr int kG4Bn = 128;
-constexpr int kG4A = 128 * 128;       // codes of 128 rows x 256 elements
-constexpr int kG4Sf = 2048;           // scales of 128 rows x 256 elements
+// holds 256 elements, one stage).  An MMA of 64 elements takes a row's four
+// scale bytes as one 32-bit word of tensor memory, row 32 j + i at lane i of
+// column j, the same in all four lane quarters: four warps, one a quarter,
+// read 16 bytes a row (a stage's 16 blocks) from shared memory and write
+// tensor memory themselves.  A lane that reads rows i, i + 32, ... holds
+// exactly its column words of every 64-element step, so nothing is exchanged.
+// (tcgen05.cp does the same copy on the tensor pipe, in line with the MMAs:
+// it took 0.3 of the large product's time.)
+constexpr int kG4Epi = 8;                 // epilogue warps: lane quarter w & 3, half of the columns w >> 2
+constexpr int kG4Threads = 32 * (kG4Epi + 6);  // warp 8 TMA, 9 MMA, 10-13 scales
+constexpr int kG4A = 128 * 128;           // codes of 128 rows x 256 elements
+constexpr int kG4SfStages = 4;            // stages whose scales one copy brings: 64 bytes a row
 constexpr int kG4MaxStages = 9;
-constexpr uint32_t kG4SfCol = 256;    // tensor-memory column of the scales, behind two 128-column accumulators
+constexpr uint32_t kG4SfCol = 256;        // tensor-memory column of the scales, behind the accumulators
+
+// CG = 1: 128 x 128 tiles, two accumulators.  CG = 2 (a CTA pair): 256 x 256
+// tiles, one accumulator -- the other 256 columns hold scales; eight epilogue
+// warps take it to registers in two steps, so that the next tile's MMAs start
+// some hundred cycles later.
+template <int CG>
+struct G4Cfg {
+    static constexpr int BN = 128 * CG;
+    static constexpr int ACC = CG == 1 ? 2 : 1;
+    static constexpr int SFA = 16, SFB = BN / 32 * 4;        // columns a stage
+    static constexpr int F = 256 / (SFA + SFB);              // stages of scales in tensor memory (8, 5)
+};
 
 template <int V>
 struct IntC {
@@ -261,7 +274,8 @@ struct IntC {
 };
 
 struct G4Params {
-    CUtensorMap ta, tb;  // wq [E, N, K/2], xq [R, K/2] bytes
+    CUtensorMap ta, tb;    // wq [E, N, K/2], xq [R, K/2] bytes
+    CUtensorMap tsa, tsb;  // wbs [E, N, K/16], xbs [R, K/16] bytes (K % 256 == 0)
     const uint8_t *wbs, *xbs;
     const float *wgs, *xgs;
     const int32_t* offsets;
@@ -273,45 +287,53 @@ struct G4Params {
 
 struct G4Shared {
     GgShared g;
-    uint64_t sfull[kG4MaxStages];  // a stage's scales are in shared memory
+    uint64_t sfull[8], sempty[8];  // a stage's scales are in tensor memory (leader: of both CTAs); its MMAs are done
+    uint64_t cfull[2], cempty[2];  // a copy of scales is in shared memory; the scale warps have read it
 };
 static_assert(sizeof(G4Shared) <= 4096, "control block");
-
-// Copy 32 rows x 128 bits of shared memory (rows 16 bytes apart) to four
-// tensor-memory columns, repeated for the four lane quarters.
-__device__ __forceinline__ void umma_cp_scales(uint32_t taddr, uint32_t saddr) {
-    uint64_t d = 0;
-    d |= (uint64_t)((saddr & 0x3FFFFu) >> 4);
-    d |= (uint64_t)(128 >> 4) << 16;
-    d |= (uint64_t)(128 >> 4) << 32;  // 8-row groups 128 bytes apart
-    d |= (uint64_t)1 << 46;
-    asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(d) : "memory");
-}
 
 // Instruction descriptor, kind::mxf4nvf4: E2M1 A and B, E4M3 scales.
 __device__ __forceinline__ uint32_t umma_idesc_nvfp4(int M, int N) {
     return (1u << 7) | (1u << 10) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
 }
 
+template <int CG>
 __device__ __forceinline__ void umma_nvfp4(uint32_t tmem_d, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
                                            uint32_t sfa, uint32_t sfb, uint32_t accumulate) {
+    if (CG == 1)
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "setp.ne.b32 p, %6, 0;\n\t"
+            "tcgen05.mma.cta_group::1.kind::mxf4nvf4.block_scale.scale_vec::4X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(
+                tmem_d),
+            "l"(adesc), "l"(bdesc), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
+            : "memory");
+    else
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "setp.ne.b32 p, %6, 0;\n\t"
+            "tcgen05.mma.cta_group::2.kind::mxf4nvf4.block_scale.scale_vec::4X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(
+                tmem_d),
+            "l"(adesc), "l"(bdesc), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
+            : "memory");
+}
+
+// 16 words of this lane to 16 consecutive columns
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
     asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "setp.ne.b32 p, %6, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::mxf4nvf4.block_scale.scale_vec::4X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(
-            tmem_d),
-        "l"(adesc), "l"(bdesc), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(
+            taddr),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+        "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
         : "memory");
 }
 
-// The 16 scale bytes of a row from block k0 on; blocks from nb on read as 0.
-// VEC: bytes a load, by the alignment that nb gives every row (16, 4 or 2).
-template <int VEC>
+// The 16 scale bytes of a row from block k0 on, from global memory; blocks
+// from nb on read as 0 (nb is even: K % 32 == 0).
 __device__ __forceinline__ uint4 g4_row_scales(const uint8_t* row, int k0, int nb) {
     const uint8_t* p = row + k0;
-    if (VEC == 16) return __ldg(reinterpret_cast<const uint4*>(p));
     uint32_t w[4] = {0, 0, 0, 0};
-    if (VEC == 4) {
+    if ((nb & 3) == 0) {
 #pragma unroll
         for (int i = 0; i < 4; ++i)
             if (k0 + 4 * i < nb) w[i] = __ldg(reinterpret_cast<const uint32_t*>(p + 4 * i));
@@ -324,62 +346,90 @@ __device__ __forceinline__ uint4 g4_row_scales(const uint8_t* row, int k0, int n
     return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
+template <int CG>
 __global__ void __launch_bounds__(kG4Threads, 1) g4_kernel(const __grid_constant__ G4Params p) {
+    using Cfg = G4Cfg<CG>;
     extern __shared__ __align__(1024) unsigned char gg_smem_raw[];
     unsigned char* base = reinterpret_cast<unsigned char*>(
         (reinterpret_cast<uintptr_t>(gg_smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
     G4Shared* s4 = reinterpret_cast<G4Shared*>(base);
     GgShared* sh = &s4->g;
-    unsigned char* ring = base + 4096;
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t rank = CG == 2 ? cluster_rank() : 0u;
+    const int unit = (int)blockIdx.x / CG, units = (int)gridDim.x / CG;
     if (threadIdx.x == 0) {
         for (int s = 0; s < kG4MaxStages; ++s) {
             mbar_init(&sh->full[s], 1);
+            mbar_init(&sh->pfull[s], 1);
             mbar_init(&sh->empty[s], 1);
-            mbar_init(&s4->sfull[s], 1);
+        }
+        for (int f = 0; f < 8; ++f) {
+            mbar_init(&s4->sfull[f], 4 * CG);
+            mbar_init(&s4->sempty[f], 1);
         }
         for (int a = 0; a < 2; ++a) {
             mbar_init(&sh->acc_full[a], 1);
-            mbar_init(&sh->acc_empty[a], 4);
+            mbar_init(&sh->acc_empty[a], kG4Epi * CG);
+            mbar_init(&s4->cfull[a], 1);
+            mbar_init(&s4->cempty[a], 4);
         }
         mbar_init(&sh->mma_done, 1);
         sh->abort = 0;
         fence_mbar_init();
     }
-    if (warp == 5) tmem_alloc(&sh->tmem_slot, kGgTmemCols);
+    if (warp == 9) gg_tmem_alloc<CG>(&sh->tmem_slot, kGgTmemCols);
     grid_dep_wait();
-    const int mtiles = (p.M + 127) / 128;
-    gg_segments(sh, p.offsets, p.E, p.R, kG4Bn, mtiles, p.status);
+    const int mtiles = (p.M + 128 * CG - 1) / (128 * CG);
+    gg_segments(sh, p.offsets, p.E, p.R, Cfg::BN, mtiles, p.status);
     tc_fence_before();
     __syncthreads();
+    if (CG == 2) cluster_sync();
     tc_fence_after();
     const uint32_t tmem = sh->tmem_slot;
 
-    // stage: weight codes, weight scales, row scales, row codes (as many rows
-    // as the largest segment needs)
-    const uint32_t b_tile = (uint32_t)min(kG4Bn, max(kGgBoxN, (sh->nmax + kGgBoxN - 1) / kGgBoxN * kGgBoxN)) * 128u;
-    const uint32_t b_off = kG4A + 2 * kG4Sf;
-    const uint32_t stage_bytes = b_off + b_tile;
-    const uint32_t S = min((uint32_t)kG4MaxStages, ((uint32_t)kGgSmem - 1023u - 4096u) / stage_bytes);
+    // shared memory: two copies of scales (128 weight rows, then the tile's
+    // rows, 64 bytes each), then the ring of codes (128 weight rows, then this
+    // CTA's share of the tile's rows).  One CTA's tiles hold as many rows as
+    // the largest segment needs.
+    const int nrows = CG == 2 ? Cfg::BN : min(Cfg::BN, max(kGgBoxN, (sh->nmax + kGgBoxN - 1) / kGgBoxN * kGgBoxN));
+    const bool sf_tma = (p.K & 255) == 0;
+    const uint32_t sf_bytes = sf_tma ? (128u + (uint32_t)nrows) * 64u : 0u;
+    unsigned char* sfbuf = base + 4096;
+    unsigned char* ring = sfbuf + 2 * sf_bytes;
+    const uint32_t stage_bytes = kG4A + (uint32_t)(nrows / CG) * 128u;
+    const uint32_t S = min((uint32_t)kG4MaxStages, ((uint32_t)kGgSmem - 1023u - 4096u - 2u * sf_bytes) / stage_bytes);
     const int nk = (p.K + 255) / 256, nb = p.K / 16;
 
     auto walk = [&](auto f) {
         int e = 0;
-        for (int it = (int)blockIdx.x; it < sh->start[p.E]; it += (int)gridDim.x) {
+        for (int it = unit; it < sh->start[p.E]; it += units) {
             while (sh->start[e + 1] <= it) ++e;
             const int t = it - sh->start[e];
-            const int m0 = (t % mtiles) * 128, n0 = (t / mtiles) * kG4Bn;
-            if (!f(e, sh->p0[e] + n0, min(kG4Bn, sh->cnt[e] - n0), m0)) break;
+            const int m0 = (t % mtiles) * 128 * CG + (int)rank * 128, n0 = (t / mtiles) * Cfg::BN;
+            if (!f(e, sh->p0[e] + n0, min(Cfg::BN, sh->cnt[e] - n0), m0)) break;
         }
     };
+    // rows of the tile that each CTA holds, in whole boxes
+    auto share = [](int n) { return (n + kGgBoxN * CG - 1) / (kGgBoxN * CG) * kGgBoxN; };
 
-    if (warp == 4) {
-        uint32_t g = 0, armed = 0;
+    if (warp == 8) {
+        // ---------------- TMA producer
+        uint32_t g = 0, armed = 0, c = 0;
         if (lane == 0) {
             walk([&](int e, int q0, int n, int m0) -> bool {
-                const int rows = (n + kGgBoxN - 1) / kGgBoxN * kGgBoxN;
+                const int rows = share(n);
                 for (int k = 0; k < nk; ++k, ++g) {
+                    if (sf_tma && k % kG4SfStages == 0) {
+                        const uint32_t u = c & 1u;
+                        if (c >= 2 && !gg_wait(&s4->cempty[u], ((c >> 1) - 1u) & 1u, &sh->abort)) return false;
+                        unsigned char* sf = sfbuf + u * sf_bytes;
+                        mbar_arrive_expect_tx(&s4->cfull[u], (128u + (uint32_t)(rows * CG)) * 64u);
+                        ++c;
+                        tma_load_3d(sf, &p.tsa, k * 16, m0, e, &s4->cfull[u]);
+                        for (int r = 0; r < rows * CG; r += kGgBoxN)
+                            tma_load_2d(sf + 8192 + r * 64, &p.tsb, k * 16, q0 + r, &s4->cfull[u]);
+                    }
                     const uint32_t s = g % S, ph = (g / S) & 1u;
                     if (g >= S && !gg_wait(&sh->empty[s], ph ^ 1u, &sh->abort)) return false;
                     unsigned char* st = ring + (size_t)s * stage_bytes;
@@ -387,153 +437,203 @@ __global__ void __launch_bounds__(kG4Threads, 1) g4_kernel(const __grid_constant
                     armed = g + 1u;
                     tma_load_3d(st, &p.ta, k * 128, m0, e, &sh->full[s]);
                     for (int r = 0; r < rows; r += kGgBoxN)
-                        tma_load_2d(st + b_off + r * 128, &p.tb, k * 128, q0 + r, &sh->full[s]);
+                        tma_load_2d(st + kG4A + r * 128, &p.tb, k * 128, q0 + (int)rank * rows + r, &sh->full[s]);
                 }
                 return true;
             });
+            // teardown: no copy, and no release of a stage by the other CTA's
+            // MMAs, may be on its way when the CTA exits
             for (uint32_t s = 0; s < S && s < armed; ++s) {
                 const uint32_t last = armed - 1u - ((armed - 1u - s) % S);
                 mbar_wait(&sh->full[s], (last / S) & 1u, kGgWaitLimit);
+                if (CG == 2) gg_wait(&sh->empty[s], (last / S) & 1u, &sh->abort);
+            }
+            for (uint32_t u = 0; u < 2 && u < c; ++u) {
+                const uint32_t last = c - 1u - ((c - 1u - u) & 1u);
+                mbar_wait(&s4->cfull[u], (last >> 1) & 1u, kGgWaitLimit);
             }
         }
         __syncwarp();
-    } else if (warp == 5) {
+    } else if (warp == 9) {
+        // ---------------- MMA issuer (one thread of the leader; the other CTA's passes its tiles on)
         uint32_t g = 0;
         int d = 0;
         walk([&](int e, int q0, int n, int m0) -> bool {
-            const int buf = d & 1, use = d >> 1;
+            const int buf = d % Cfg::ACC, use = d / Cfg::ACC;
             ++d;
-            if (use > 0 && !gg_wait(&sh->acc_empty[buf], (uint32_t)((use - 1) & 1), &sh->abort)) return false;
+            if (rank == 0 && use > 0 && !gg_wait(&sh->acc_empty[buf], (uint32_t)((use - 1) & 1), &sh->abort)) return false;
             tc_fence_after();
-            const uint32_t tacc = tmem + (uint32_t)(buf * kG4Bn);
-            const uint32_t idesc = umma_idesc_nvfp4(128, (n + kGgBoxN - 1) / kGgBoxN * kGgBoxN);
+            const uint32_t tacc = tmem + (uint32_t)(buf * Cfg::BN);
+            const uint32_t idesc = umma_idesc_nvfp4(128 * CG, share(n) * CG);
             for (int k = 0; k < nk; ++k, ++g) {
-                const uint32_t s = g % S, ph = (g / S) & 1u;
-                if (!gg_wait(&sh->full[s], ph, &sh->abort) || !gg_wait(&s4->sfull[s], ph, &sh->abort)) return false;
+                const uint32_t s = g % S, f = g % (uint32_t)Cfg::F;
+                if (!gg_wait(&sh->full[s], (g / S) & 1u, &sh->abort)) return false;
+                if (rank != 0) {
+                    if (lane == 0) mbar_arrive_cluster(&sh->pfull[s], 0);
+                    continue;
+                }
+                if (CG == 2 && !gg_wait(&sh->pfull[s], (g / S) & 1u, &sh->abort)) return false;
+                if (!gg_wait(&s4->sfull[f], (g / (uint32_t)Cfg::F) & 1u, &sh->abort)) return false;
                 tc_fence_after();
                 if (lane == 0) {
                     const uint32_t st = smem_u32(ring + (size_t)s * stage_bytes);
-                    // the scales' columns alternate between stages
-                    const uint32_t sfa = tmem + kG4SfCol + (g & 1u) * 32u, sfb = sfa + 16u;
+                    const uint32_t sfa = tmem + kG4SfCol + f * (uint32_t)(Cfg::SFA + Cfg::SFB), sfb = sfa + Cfg::SFA;
                     const int steps = min(4, (p.K - k * 256 + 63) / 64);
-                    for (int kk = 0; kk < steps; ++kk) {
-                        umma_cp_scales(sfa + kk * 4, st + kG4A + kk * 512);
-                        umma_cp_scales(sfb + kk * 4, st + kG4A + kG4Sf + kk * 512);
-                    }
                     for (int kk = 0; kk < steps; ++kk)
-                        umma_nvfp4(tacc, umma_sdesc(st + kk * 32), umma_sdesc(st + b_off + kk * 32), idesc, sfa + kk * 4,
-                                   sfb + kk * 4, (k > 0 || kk > 0) ? 1u : 0u);
-                    umma_commit(&sh->empty[s]);
+                        umma_nvfp4<CG>(tacc, umma_sdesc(st + kk * 32), umma_sdesc(st + kG4A + kk * 32), idesc,
+                                       sfa + kk * (Cfg::SFA / 4), sfb + kk * (Cfg::SFB / 4), (k > 0 || kk > 0) ? 1u : 0u);
+                    gg_commit<CG>(&sh->empty[s]);
+                    gg_commit<CG>(&s4->sempty[f]);
                 }
                 __syncwarp();
             }
-            if (lane == 0) umma_commit(&sh->acc_full[buf]);
+            if (rank == 0 && lane == 0) gg_commit<CG>(&sh->acc_full[buf]);
             __syncwarp();
             return true;
         });
-        if (lane == 0) {
-            umma_commit(&sh->mma_done);
+        if (rank == 0 && lane == 0) {
+            gg_commit_own<CG>(&sh->mma_done);
             mbar_wait(&sh->mma_done, 0u, kGgWaitLimit);
         }
         __syncwarp();
-    } else if (warp >= 6) {
-        // ---------------- scales: warp 6 + i takes every fourth stage, and
-        // has the next one's on their way while it waits to store these
-        auto scales = [&](auto vec) {
-            constexpr int VEC = decltype(vec)::value;
-            uint32_t g = 0, have = 0;  // stages walked; the stage in `a` and `b` (valid when any)
-            bool any = false;
-            uint4 a[4], b[4];
-            auto put = [&]() -> bool {
-                const uint32_t s = have % S, ph = (have / S) & 1u;
-                if (have >= S && !gg_wait(&sh->empty[s], ph ^ 1u, &sh->abort)) return false;
-                uint4* sa = reinterpret_cast<uint4*>(ring + (size_t)s * stage_bytes + kG4A);
-                uint4* sb = sa + kG4Sf / 16;
-                sa[lane] = make_uint4(a[0].x, a[1].x, a[2].x, a[3].x);
-                sa[32 + lane] = make_uint4(a[0].y, a[1].y, a[2].y, a[3].y);
-                sa[64 + lane] = make_uint4(a[0].z, a[1].z, a[2].z, a[3].z);
-                sa[96 + lane] = make_uint4(a[0].w, a[1].w, a[2].w, a[3].w);
-                sb[lane] = make_uint4(b[0].x, b[1].x, b[2].x, b[3].x);
-                sb[32 + lane] = make_uint4(b[0].y, b[1].y, b[2].y, b[3].y);
-                sb[64 + lane] = make_uint4(b[0].z, b[1].z, b[2].z, b[3].z);
-                sb[96 + lane] = make_uint4(b[0].w, b[1].w, b[2].w, b[3].w);
-                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&s4->sfull[s]);
-                return true;
-            };
-            walk([&](int e, int q0, int n, int m0) -> bool {
-                // rows beyond the tile's end take the last one's scales: what
-                // they scale is never stored
-                const uint8_t *ra[4], *rb[4];
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    ra[j] = p.wbs + ((size_t)e * p.M + min(m0 + 32 * j + lane, p.M - 1)) * nb;
-                    rb[j] = p.xbs + (size_t)(q0 + min(32 * j + lane, n - 1)) * nb;
-                }
-                for (int k = 0; k < nk; ++k, ++g) {
-                    if ((int)(g % kG4ScaleWarps) != warp - 6) continue;
-                    uint4 na[4], nb4[4];
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        na[j] = g4_row_scales<VEC>(ra[j], k * 16, nb);
-                        nb4[j] = g4_row_scales<VEC>(rb[j], k * 16, nb);
-                    }
-                    if (any && !put()) return false;
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        a[j] = na[j];
-                        b[j] = nb4[j];
-                    }
-                    have = g;
-                    any = true;
-                }
-                return true;
-            });
-            if (any) put();
-        };
-        if ((nb & 15) == 0)
-            scales(IntC<16>{});
-        else if ((nb & 3) == 0)
-            scales(IntC<4>{});
-        else
-            scales(IntC<2>{});
-    } else {
-        int d = 0;
+    } else if (warp >= 10) {
+        // ---------------- scales into this warp's quarter of tensor memory
+        uint32_t g = 0, c = 0;
+        const uint32_t quarter = (uint32_t)((warp & 3) * 32) << 16;
+        constexpr int NB = Cfg::BN / 32;
         walk([&](int e, int q0, int n, int m0) -> bool {
-            const int m = m0 + (int)threadIdx.x;
-            const float wg = __ldg(p.wgs + e);
-            float xg[kG4Bn / 32];  // the scales of rows q0 + 32 i + lane
+            for (int k = 0; k < nk; ++k, ++g) {
+                uint4 a[4], b[NB];
+                const int kq = k % kG4SfStages;
+                if (sf_tma) {
+                    const uint32_t u = c & 1u;
+                    if (kq == 0 && !gg_wait(&s4->cfull[u], (c >> 1) & 1u, &sh->abort)) return false;
+                    const unsigned char* sf = sfbuf + u * sf_bytes;
+                    // 64-byte swizzle: 16-byte chunk kq of row r is at chunk kq ^ ((r >> 1) & 3)
+                    const int ch = (kq ^ ((lane >> 1) & 3)) * 16;
 #pragma unroll
-            for (int i = 0; i < kG4Bn / 32; ++i) xg[i] = 32 * i + lane < n ? __ldg(p.xgs + q0 + 32 * i + lane) : 0.0f;
-            const int buf = d & 1, use = d >> 1;
+                    for (int j = 0; j < 4; ++j) a[j] = *reinterpret_cast<const uint4*>(sf + (32 * j + lane) * 64 + ch);
+#pragma unroll
+                    for (int j = 0; j < NB; ++j)
+                        b[j] = 32 * j < n ? *reinterpret_cast<const uint4*>(sf + 8192 + (32 * j + lane) * 64 + ch)
+                                          : make_uint4(0, 0, 0, 0);
+                    if (kq == kG4SfStages - 1 || k == nk - 1) {
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(&s4->cempty[u]);
+                        ++c;
+                    }
+                } else {
+                    // rows beyond the tile's end take the last one's scales:
+                    // what they scale is zero or never stored
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        a[j] = g4_row_scales(p.wbs + ((size_t)e * p.M + min(m0 + 32 * j + lane, p.M - 1)) * nb, k * 16, nb);
+#pragma unroll
+                    for (int j = 0; j < NB; ++j)
+                        b[j] = 32 * j < n ? g4_row_scales(p.xbs + (size_t)(q0 + min(32 * j + lane, n - 1)) * nb, k * 16, nb)
+                                          : make_uint4(0, 0, 0, 0);
+                }
+                const uint32_t f = g % (uint32_t)Cfg::F, use = g / (uint32_t)Cfg::F;
+                if (use > 0 && !gg_wait(&s4->sempty[f], (use - 1u) & 1u, &sh->abort)) return false;
+                __syncwarp();
+                tc_fence_after();
+                const uint32_t at = tmem + quarter + kG4SfCol + f * (uint32_t)(Cfg::SFA + Cfg::SFB);
+                const uint32_t wa[16] = {a[0].x, a[1].x, a[2].x, a[3].x, a[0].y, a[1].y, a[2].y, a[3].y,
+                                         a[0].z, a[1].z, a[2].z, a[3].z, a[0].w, a[1].w, a[2].w, a[3].w};
+                tmem_st16(at, wa);
+                uint32_t wb[4 * NB];
+#pragma unroll
+                for (int j = 0; j < NB; ++j) {
+                    wb[j] = b[j].x;
+                    wb[NB + j] = b[j].y;
+                    wb[2 * NB + j] = b[j].z;
+                    wb[3 * NB + j] = b[j].w;
+                }
+#pragma unroll
+                for (int j = 0; j < 4 * NB; j += 16)
+                    tmem_st16(at + Cfg::SFA + j, *reinterpret_cast<const uint32_t(*)[16]>(wb + j));
+                asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) {
+                    if (CG == 1)
+                        mbar_arrive(&s4->sfull[f]);
+                    else
+                        mbar_arrive_cluster(&s4->sfull[f], 0);
+                }
+            }
+            return true;
+        });
+        // no release by the other CTA's MMAs may be on its way at exit
+        if (CG == 2)
+            for (uint32_t f = 0; f < (uint32_t)Cfg::F && f < g; ++f) {
+                const uint32_t last = g - 1u - ((g - 1u - f) % (uint32_t)Cfg::F);
+                gg_wait(&s4->sempty[f], (last / (uint32_t)Cfg::F) & 1u, &sh->abort);
+            }
+        __syncwarp();
+    } else {
+        // ---------------- epilogue: lane quarter warp & 3, half of the columns
+        int d = 0;
+        constexpr int COLS = Cfg::BN / 2;
+        const int c0 = (warp >> 2) * COLS;
+        walk([&](int e, int q0, int n, int m0) -> bool {
+            const int m = m0 + (warp & 3) * 32 + lane;
+            const int mine = min(COLS, n - c0);  // columns of this warp; none below 1
+            const float wg = __ldg(p.wgs + e);
+            float xg[COLS / 32];  // the scales of rows q0 + c0 + 32 i + lane
+#pragma unroll
+            for (int i = 0; i < COLS / 32; ++i)
+                xg[i] = 32 * i + lane < mine ? __ldg(p.xgs + q0 + c0 + 32 * i + lane) : 0.0f;
+            const int buf = d % Cfg::ACC, use = d / Cfg::ACC;
             ++d;
             if (!gg_wait(&sh->acc_full[buf], (uint32_t)(use & 1), &sh->abort)) return false;
             __syncwarp();
             tc_fence_after();
-            gg_epilogue(
-                tmem + (uint32_t)(buf * kG4Bn) + ((uint32_t)(warp * 32) << 16), p.out, p.out_f32, (size_t)q0, n, m, p.M,
-                [&](uint32_t(&v)[32], int c) {
-                    float mine = xg[0];
+            const uint32_t taddr = tmem + (uint32_t)(buf * Cfg::BN + c0) + ((uint32_t)((warp & 3) * 32) << 16);
+            auto release = [&]() {
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) {
+                    if (CG == 1)
+                        mbar_arrive(&sh->acc_empty[buf]);
+                    else
+                        mbar_arrive_cluster(&sh->acc_empty[buf], 0);
+                }
+            };
+            if (mine <= 0) {
+                release();
+                return true;
+            }
+            // 64 columns to registers at a time; the accumulator is free once the last are there
 #pragma unroll
-                    for (int i = 1; i < kG4Bn / 32; ++i) mine = c == 32 * i ? xg[i] : mine;
+            for (int h = 0; h < COLS / 64; ++h) {
+                if (64 * h >= mine) break;
+                uint32_t v[2][32];
+#pragma unroll
+                for (int i = 0; i < 2; ++i)
+                    if (64 * h + 32 * i < mine) gg_ld32(taddr + 64 * h + 32 * i, v[i]);
+#pragma unroll
+                for (int i = 0; i < 2; ++i) gg_ld_wait(v[i]);
+                if (64 * h + 64 >= mine) release();
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const int c = 64 * h + 32 * i;
+                    if (c >= mine) break;
 #pragma unroll
                     for (int j = 0; j < 32; ++j)
-                        v[j] = __float_as_uint(__uint_as_float(v[j]) * __shfl_sync(0xffffffffu, mine, j) * wg);
-                },
-                [&]() {
-                    tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(&sh->acc_empty[buf]);
-                });
+                        v[i][j] = __float_as_uint(__uint_as_float(v[i][j]) * __shfl_sync(0xffffffffu, xg[c / 32], j) * wg);
+                    gg_store32(v[i], p.out, p.out_f32, (size_t)q0 + c0 + c, min(32, mine - c), m, p.M);
+                }
+            }
             return true;
         });
     }
     __syncthreads();
     if (*(volatile int*)&sh->abort && threadIdx.x == 0) set_status(p.status, MOE_DEV_TIMEOUT);
-    if (warp == 5) {
+    if (CG == 2) cluster_sync();
+    if (warp == 9) {
         tc_fence_after();
-        tmem_dealloc(tmem, kGgTmemCols);
+        gg_tmem_dealloc<CG>(tmem, kGgTmemCols);
     }
 }
 

@@ -13,21 +13,21 @@
 namespace moe {
 
 // A tensor map over a row-major tensor [outer2, outer1, inner] (outer2 = 0:
-// two dimensions) with 128-byte swizzled boxes of 128 bytes x box_rows;
-// elements outside the tensor read as zeros.
-static bool encode_map(CUtensorMap* map, const void* base, bool bytes, uint64_t inner, uint64_t outer1, uint64_t outer2,
-                       uint32_t box_rows) {
+// two dimensions) with boxes of box_bytes x box_rows (128 or 64 bytes, the
+// swizzle of that width); elements outside the tensor read as zeros.
+static bool encode_map(CUtensorMap* map, const void* base, int elem, uint64_t inner, uint64_t outer1, uint64_t outer2,
+                       uint32_t box_rows, uint32_t box_bytes = 128) {
     EncodeTiledFn fn = encode_fn();
     if (!fn) return false;
-    const uint64_t pitch = inner * (bytes ? 1 : 2);
+    const uint64_t pitch = inner * elem;
     const cuuint64_t dims[3] = {inner, outer1, outer2};
     const cuuint64_t strides[2] = {pitch, pitch * outer1};
-    const cuuint32_t box[3] = {bytes ? 128u : 64u, box_rows, 1};
+    const cuuint32_t box[3] = {box_bytes / (uint32_t)elem, box_rows, 1};
     const cuuint32_t estr[3] = {1, 1, 1};
-    return fn(map, bytes ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, outer2 ? 3 : 2,
+    return fn(map, elem == 1 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, outer2 ? 3 : 2,
               const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-              CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+              box_bytes == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 static int check_grouped(int R, int N, int K, int E, int dtype) {
@@ -37,14 +37,15 @@ static int check_grouped(int R, int N, int K, int E, int dtype) {
     return MOE_OK;
 }
 
-template <int MODE, int CG>
-static int launch_gg(const GgParams& p, int sms, cudaStream_t st) {
-    int rc = allow_smem(gg_kernel<MODE, CG>, kGgSmem);
+// A persistent kernel on every SM, in clusters of CG CTAs.
+template <int CG, typename K, typename P>
+static int launch_persistent(K kernel, const P& p, int threads, int sms, cudaStream_t st) {
+    const int rc = allow_smem(kernel, kGgSmem);
     if (rc) return rc;
     cudaLaunchConfig_t cfg;
     memset(&cfg, 0, sizeof cfg);
     cfg.gridDim = dim3((unsigned)(sms / CG * CG));
-    cfg.blockDim = dim3(kGgThreads);
+    cfg.blockDim = dim3((unsigned)threads);
     cfg.dynamicSmemBytes = kGgSmem;
     cfg.stream = st;
     cudaLaunchAttribute attr[2];
@@ -56,7 +57,7 @@ static int launch_gg(const GgParams& p, int sms, cudaStream_t st) {
     attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = CG > 1 ? 2 : 1;
-    return launch_ex(cfg, gg_kernel<MODE, CG>, p);
+    return launch_ex(cfg, kernel, p);
 }
 
 // The paired tile (256 x 256) from this many rows a segment on average.
@@ -66,11 +67,11 @@ template <int MODE>
 static int run_gg(GgParams& p, const void* a, const void* b, int R, int N, int K, int E, cudaStream_t st) {
     bool ok;
     if (MODE == kGgFwd)
-        ok = encode_map(&p.ta, a, false, K, N, E, 128) && encode_map(&p.tb, b, false, K, R, 0, kGgBoxN);
+        ok = encode_map(&p.ta, a, 2, K, N, E, 128) && encode_map(&p.tb, b, 2, K, R, 0, kGgBoxN);
     else if (MODE == kGgDx)
-        ok = encode_map(&p.ta, a, false, K, N, E, 64) && encode_map(&p.tb, b, false, N, R, 0, kGgBoxN);
+        ok = encode_map(&p.ta, a, 2, K, N, E, 64) && encode_map(&p.tb, b, 2, N, R, 0, kGgBoxN);
     else
-        ok = encode_map(&p.ta, a, false, K, R, 0, 64) && encode_map(&p.tb, b, false, N, R, 0, 64);
+        ok = encode_map(&p.ta, a, 2, K, R, 0, 64) && encode_map(&p.tb, b, 2, N, R, 0, 64);
     if (!ok) return MOE_ERR_UNSUPPORTED;
     p.E = E;
     p.R = R;
@@ -80,7 +81,8 @@ static int run_gg(GgParams& p, const void* a, const void* b, int R, int N, int K
     const int sms = sm_count();
     if (sms < 2) return MOE_ERR_CUDA;
     const bool pair = (int64_t)R >= (int64_t)kGgPairRows * E;
-    return pair ? launch_gg<MODE, 2>(p, sms, st) : launch_gg<MODE, 1>(p, sms, st);
+    return pair ? launch_persistent<2>(gg_kernel<MODE, 2>, p, kGgThreads, sms, st)
+                : launch_persistent<1>(gg_kernel<MODE, 1>, p, kGgThreads, sms, st);
 }
 
 template <bool BF16, int T>
@@ -259,7 +261,10 @@ int moe_grouped_gemm_nvfp4(const uint8_t* xq, const uint8_t* xbs, const float* x
     MOE_OPT(dev_status);
     G4Params p;
     memset(&p, 0, sizeof p);
-    if (!encode_map(&p.ta, wq, true, K / 2, N, E, 128) || !encode_map(&p.tb, xq, true, K / 2, R, 0, kGgBoxN))
+    if (!encode_map(&p.ta, wq, 1, K / 2, N, E, 128) || !encode_map(&p.tb, xq, 1, K / 2, R, 0, kGgBoxN))
+        return MOE_ERR_UNSUPPORTED;
+    if (K % 256 == 0 && (!encode_map(&p.tsa, wbs, 1, K / 16, N, E, 128, 64) ||
+                         !encode_map(&p.tsb, xbs, 1, K / 16, R, 0, kGgBoxN, 64)))
         return MOE_ERR_UNSUPPORTED;
     p.wbs = wbs;
     p.xbs = xbs;
@@ -274,9 +279,10 @@ int moe_grouped_gemm_nvfp4(const uint8_t* xq, const uint8_t* xbs, const float* x
     p.out_f32 = y_dtype == MOE_DT_F32;
     p.status = dev_status;
     const int sms = sm_count();
-    if (sms < 1) return MOE_ERR_CUDA;
-    if ((rc = allow_smem(g4_kernel, kGgSmem))) return rc;
-    return launch_pdl(g4_kernel, (unsigned)sms, kG4Threads, kGgSmem, static_cast<cudaStream_t>(stream), p);
+    if (sms < 2) return MOE_ERR_CUDA;
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    return (int64_t)R >= (int64_t)kGgPairRows * E ? launch_persistent<2>(g4_kernel<2>, p, kG4Threads, sms, st)
+                                                  : launch_persistent<1>(g4_kernel<1>, p, kG4Threads, sms, st);
 }
 
 }  // extern "C"
