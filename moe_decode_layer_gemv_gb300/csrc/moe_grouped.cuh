@@ -55,8 +55,7 @@ struct GgCfg {
 };
 
 struct GgShared {
-    uint64_t full[kGgMaxStages];    // this CTA's tiles of a stage landed
-    uint64_t pfull[kGgMaxStages];   // CG = 2, leader: the other CTA's tiles landed
+    uint64_t full[kGgMaxStages];    // leader: a stage's tiles landed (in both CTAs)
     uint64_t empty[kGgMaxStages];   // the MMAs have read a stage
     uint64_t acc_full[2];           // an accumulator's MMAs are complete
     uint64_t acc_empty[2];          // leader: the epilogue warps (of both CTAs) have read an accumulator
@@ -86,6 +85,49 @@ __device__ __forceinline__ uint32_t cluster_rank() {
 
 __device__ __forceinline__ void cluster_sync() {
     asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
+// Tiled loads into this CTA whose bytes are counted on the pair leader's
+// barrier (an address of the cluster's shared memory), so that one barrier
+// says that both CTAs' tiles landed.
+__device__ __forceinline__ void tma_load_2d_pair(void* dst, const CUtensorMap* map, int c0, int c1, uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2 [%0], [%1, {%2, %3}], [%4];" ::"r"(
+            smem_u32(dst)),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(bar)
+        : "memory");
+}
+
+__device__ __forceinline__ void tma_load_3d_pair(void* dst, const CUtensorMap* map, int c0, int c1, int c2,
+                                                 uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2 [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(
+            smem_u32(dst)),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(bar)
+        : "memory");
+}
+
+// The address in CTA `rank` of the cluster of what is at p here.
+__device__ __forceinline__ uint32_t cluster_addr(const void* p, uint32_t rank) {
+    uint32_t a;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_u32(p)), "r"(rank));
+    return a;
+}
+
+// Loads of a stage's tiles: `bar` is this CTA's barrier, of a pair the leader's.
+template <int CG>
+__device__ __forceinline__ void gg_load2(void* dst, const CUtensorMap* map, int c0, int c1, uint64_t* bar) {
+    if (CG == 1)
+        tma_load_2d(dst, map, c0, c1, bar);
+    else
+        tma_load_2d_pair(dst, map, c0, c1, cluster_addr(bar, 0));
+}
+template <int CG>
+__device__ __forceinline__ void gg_load3(void* dst, const CUtensorMap* map, int c0, int c1, int c2, uint64_t* bar) {
+    if (CG == 1)
+        tma_load_3d(dst, map, c0, c1, c2, bar);
+    else
+        tma_load_3d_pair(dst, map, c0, c1, c2, cluster_addr(bar, 0));
 }
 
 // Arrive on the barrier at the same place in CTA `rank` of the cluster.  The
@@ -180,6 +222,21 @@ __device__ __forceinline__ bool gg_wait(uint64_t* bar, uint32_t parity, int* abo
     }
     *(volatile int*)abort = 1;
     return false;
+}
+
+// The producer's teardown: no copy, and no release of a stage by the
+// leader's MMAs, may be on its way when the CTA exits.  (A pair's copies are
+// counted on the leader's barriers; after an abort the other CTA, which
+// cannot wait on them, gives its own the time to land.)
+template <int CG>
+__device__ __forceinline__ void gg_drain(GgShared* sh, uint32_t S, uint32_t armed, uint32_t rank) {
+    for (uint32_t s = 0; s < S && s < armed; ++s) {
+        const uint32_t last = armed - 1u - ((armed - 1u - s) % S);
+        if (rank == 0) mbar_wait(&sh->full[s], (last / S) & 1u, kGgWaitLimit);
+        if (CG == 2) gg_wait(&sh->empty[s], (last / S) & 1u, &sh->abort);
+    }
+    if (rank != 0 && *(volatile int*)&sh->abort)
+        for (int i = 0; i < 1000; ++i) __nanosleep(1000);
 }
 
 // ------------------------------------------------------------- segments
@@ -340,7 +397,6 @@ __global__ void __launch_bounds__(kGgThreads, 1) gg_kernel(const __grid_constant
     if (threadIdx.x == 0) {
         for (int s = 0; s < kGgMaxStages; ++s) {
             mbar_init(&sh->full[s], 1);
-            mbar_init(&sh->pfull[s], 1);
             mbar_init(&sh->empty[s], 1);
         }
         for (int a = 0; a < 2; ++a) {
@@ -415,49 +471,43 @@ __global__ void __launch_bounds__(kGgThreads, 1) gg_kernel(const __grid_constant
                     if (g >= S && !gg_wait(&sh->empty[s], ph ^ 1u, &sh->abort)) return false;
                     unsigned char* st = ring + (size_t)s * stage_bytes;
                     const int ke = min(Cfg::KSUB, nk - k0);
-                    mbar_arrive_expect_tx(&sh->full[s], (uint32_t)ke * bytes);
+                    if (rank == 0) mbar_arrive_expect_tx(&sh->full[s], (uint32_t)(ke * CG) * bytes);
                     armed = g + 1u;
                     for (int u = 0; u < ke; ++u) {
                         unsigned char* sa = st + (size_t)u * kGgTile;
                         unsigned char* sb = st + b_off + (size_t)u * b_tile;
                         const int c = (k0 + u) * 64;
                         if (MODE == kGgFwd) {
-                            tma_load_3d(sa, &p.ta, c, am, e, &sh->full[s]);
+                            gg_load3<CG>(sa, &p.ta, c, am, e, &sh->full[s]);
                         } else if (MODE == kGgDx) {
-                            tma_load_3d(sa, &p.ta, am, c, e, &sh->full[s]);
-                            tma_load_3d(sa + 8192, &p.ta, am + 64, c, e, &sh->full[s]);
+                            gg_load3<CG>(sa, &p.ta, am, c, e, &sh->full[s]);
+                            gg_load3<CG>(sa + 8192, &p.ta, am + 64, c, e, &sh->full[s]);
                         } else {
-                            tma_load_2d(sa, &p.ta, am, q0 + c, &sh->full[s]);
-                            tma_load_2d(sa + 8192, &p.ta, am + 64, q0 + c, &sh->full[s]);
+                            gg_load2<CG>(sa, &p.ta, am, q0 + c, &sh->full[s]);
+                            gg_load2<CG>(sa + 8192, &p.ta, am + 64, q0 + c, &sh->full[s]);
                         }
                         if (MODE == kGgDw) {
-                            tma_load_2d(sb, &p.tb, bn, q0 + c, &sh->full[s]);
-                            tma_load_2d(sb + 8192, &p.tb, bn + 64, q0 + c, &sh->full[s]);
+                            gg_load2<CG>(sb, &p.tb, bn, q0 + c, &sh->full[s]);
+                            gg_load2<CG>(sb + 8192, &p.tb, bn + 64, q0 + c, &sh->full[s]);
                         } else {
                             for (int r = 0; r < rows; r += kGgBoxN)
-                                tma_load_2d(sb + r * 128, &p.tb, c, bn + r, &sh->full[s]);
+                                gg_load2<CG>(sb + r * 128, &p.tb, c, bn + r, &sh->full[s]);
                         }
                     }
                 }
                 return true;
             });
-            // teardown: no copy, and no release of a stage by the other CTA's
-            // MMAs, may be on its way when the CTA exits
-            for (uint32_t s = 0; s < S && s < armed; ++s) {
-                const uint32_t last = armed - 1u - ((armed - 1u - s) % S);
-                mbar_wait(&sh->full[s], (last / S) & 1u, kGgWaitLimit);
-                if (CG == 2) gg_wait(&sh->empty[s], (last / S) & 1u, &sh->abort);
-            }
+            gg_drain<CG>(sh, S, armed, rank);
         }
         __syncwarp();
     } else if (warp == 5) {
         uint32_t g = 0;
         int d = 0;
-        walk([&](int e, int q0, int n, int n0, int m0, int nk) -> bool {
+        if (rank == 0) walk([&](int e, int q0, int n, int n0, int m0, int nk) -> bool {
             if (nk == 0) return true;
             const int buf = d & 1, use = d >> 1;
             ++d;
-            if (rank == 0 && use > 0 && !gg_wait(&sh->acc_empty[buf], (uint32_t)((use - 1) & 1), &sh->abort))
+            if (use > 0 && !gg_wait(&sh->acc_empty[buf], (uint32_t)((use - 1) & 1), &sh->abort))
                 return false;
             tc_fence_after();
             const uint32_t tacc = tmem + (uint32_t)(buf * Cfg::BN);
@@ -478,22 +528,20 @@ __global__ void __launch_bounds__(kGgThreads, 1) gg_kernel(const __grid_constant
                     const int valid = sh->cnt[e] - k0 * 64;
                     if (valid < 64) {
                         steps = (valid + 15) / 16;
-                        const int first = valid, rows = steps * 16 - valid;
-                        for (int i = lane; i < rows * 32; i += 32) {
-                            const int blk = i & 3, ch = (i >> 2) & 7, row = first + (i >> 5);
-                            *reinterpret_cast<uint4*>(st + (blk >> 1) * b_off + (blk & 1) * 8192 + row * 128 + ch * 16) =
-                                make_uint4(0, 0, 0, 0);
+                        for (int i = lane; i < (steps * 16 - valid) * 32; i += 32) {
+                            const int blk = i & 3, ch = (i >> 2) & 7, row = valid + (i >> 5);
+                            unsigned char* at = st + (blk >> 1) * b_off + (blk & 1) * 8192 + row * 128 + ch * 16;
+                            *reinterpret_cast<uint4*>(at) = make_uint4(0, 0, 0, 0);
+                            if (CG == 2)
+                                asm volatile("st.shared::cluster.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(cluster_addr(at, 1)),
+                                             "r"(0)
+                                             : "memory");
                         }
-                        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-                        if (rank != 0) asm volatile("fence.acq_rel.cluster;" ::: "memory");
+                        if (CG == 2) asm volatile("fence.acq_rel.cluster;" ::: "memory");
+                        asm volatile("fence.proxy.async;" ::: "memory");
                         __syncwarp();
                     }
                 }
-                if (rank != 0) {
-                    if (lane == 0) mbar_arrive_cluster(&sh->pfull[s], 0);
-                    continue;
-                }
-                if (CG == 2 && !gg_wait(&sh->pfull[s], ph, &sh->abort)) return false;
                 tc_fence_after();
                 if (lane == 0) {
                     const uint32_t sta = smem_u32(st);
@@ -509,7 +557,7 @@ __global__ void __launch_bounds__(kGgThreads, 1) gg_kernel(const __grid_constant
                 }
                 __syncwarp();
             }
-            if (rank == 0 && lane == 0) gg_commit<CG>(&sh->acc_full[buf]);
+            if (lane == 0) gg_commit<CG>(&sh->acc_full[buf]);
             __syncwarp();
             return true;
         });

@@ -361,7 +361,6 @@ __global__ void __launch_bounds__(kG4Threads, 1) g4_kernel(const __grid_constant
     if (threadIdx.x == 0) {
         for (int s = 0; s < kG4MaxStages; ++s) {
             mbar_init(&sh->full[s], 1);
-            mbar_init(&sh->pfull[s], 1);
             mbar_init(&sh->empty[s], 1);
         }
         for (int f = 0; f < 8; ++f) {
@@ -433,21 +432,16 @@ __global__ void __launch_bounds__(kG4Threads, 1) g4_kernel(const __grid_constant
                     const uint32_t s = g % S, ph = (g / S) & 1u;
                     if (g >= S && !gg_wait(&sh->empty[s], ph ^ 1u, &sh->abort)) return false;
                     unsigned char* st = ring + (size_t)s * stage_bytes;
-                    mbar_arrive_expect_tx(&sh->full[s], kG4A + (uint32_t)rows * 128u);
+                    if (rank == 0) mbar_arrive_expect_tx(&sh->full[s], CG * (kG4A + (uint32_t)rows * 128u));
                     armed = g + 1u;
-                    tma_load_3d(st, &p.ta, k * 128, m0, e, &sh->full[s]);
+                    gg_load3<CG>(st, &p.ta, k * 128, m0, e, &sh->full[s]);
                     for (int r = 0; r < rows; r += kGgBoxN)
-                        tma_load_2d(st + kG4A + r * 128, &p.tb, k * 128, q0 + (int)rank * rows + r, &sh->full[s]);
+                        gg_load2<CG>(st + kG4A + r * 128, &p.tb, k * 128, q0 + (int)rank * rows + r, &sh->full[s]);
                 }
                 return true;
             });
-            // teardown: no copy, and no release of a stage by the other CTA's
-            // MMAs, may be on its way when the CTA exits
-            for (uint32_t s = 0; s < S && s < armed; ++s) {
-                const uint32_t last = armed - 1u - ((armed - 1u - s) % S);
-                mbar_wait(&sh->full[s], (last / S) & 1u, kGgWaitLimit);
-                if (CG == 2) gg_wait(&sh->empty[s], (last / S) & 1u, &sh->abort);
-            }
+            // teardown: also the copies of scales have landed
+            gg_drain<CG>(sh, S, armed, rank);
             for (uint32_t u = 0; u < 2 && u < c; ++u) {
                 const uint32_t last = c - 1u - ((c - 1u - u) & 1u);
                 mbar_wait(&s4->cfull[u], (last >> 1) & 1u, kGgWaitLimit);
@@ -455,24 +449,19 @@ __global__ void __launch_bounds__(kG4Threads, 1) g4_kernel(const __grid_constant
         }
         __syncwarp();
     } else if (warp == 9) {
-        // ---------------- MMA issuer (one thread of the leader; the other CTA's passes its tiles on)
+        // ---------------- MMA issuer (one thread of the leader)
         uint32_t g = 0;
         int d = 0;
-        walk([&](int e, int q0, int n, int m0) -> bool {
+        if (rank == 0) walk([&](int e, int q0, int n, int m0) -> bool {
             const int buf = d % Cfg::ACC, use = d / Cfg::ACC;
             ++d;
-            if (rank == 0 && use > 0 && !gg_wait(&sh->acc_empty[buf], (uint32_t)((use - 1) & 1), &sh->abort)) return false;
+            if (use > 0 && !gg_wait(&sh->acc_empty[buf], (uint32_t)((use - 1) & 1), &sh->abort)) return false;
             tc_fence_after();
             const uint32_t tacc = tmem + (uint32_t)(buf * Cfg::BN);
             const uint32_t idesc = umma_idesc_nvfp4(128 * CG, share(n) * CG);
             for (int k = 0; k < nk; ++k, ++g) {
                 const uint32_t s = g % S, f = g % (uint32_t)Cfg::F;
                 if (!gg_wait(&sh->full[s], (g / S) & 1u, &sh->abort)) return false;
-                if (rank != 0) {
-                    if (lane == 0) mbar_arrive_cluster(&sh->pfull[s], 0);
-                    continue;
-                }
-                if (CG == 2 && !gg_wait(&sh->pfull[s], (g / S) & 1u, &sh->abort)) return false;
                 if (!gg_wait(&s4->sfull[f], (g / (uint32_t)Cfg::F) & 1u, &sh->abort)) return false;
                 tc_fence_after();
                 if (lane == 0) {
@@ -487,7 +476,7 @@ __global__ void __launch_bounds__(kG4Threads, 1) g4_kernel(const __grid_constant
                 }
                 __syncwarp();
             }
-            if (rank == 0 && lane == 0) gg_commit<CG>(&sh->acc_full[buf]);
+            if (lane == 0) gg_commit<CG>(&sh->acc_full[buf]);
             __syncwarp();
             return true;
         });
