@@ -29,7 +29,8 @@ constexpr int kGgMaxStages = 12;
 constexpr int kGgBoxN = 32;          // rows per TMA box of a K-major B operand
 constexpr int kGgTile = 128 * 128;   // bytes of one 128 x 64 bf16 operand tile
 constexpr int kGgSmem = 227 * 1024;
-constexpr uint32_t kGgWaitLimit = 1u << 22;
+constexpr uint32_t kGgWaitNs = 20000;     // a wait sleeps this long at a time ...
+constexpr uint32_t kGgWaitLimit = 1u << 17;  // ... and gives up after so many times
 constexpr uint32_t kGgTmemCols = 512;
 
 struct GgParams {
@@ -214,14 +215,38 @@ __device__ __forceinline__ void gg_tmem_dealloc(uint32_t taddr, uint32_t ncols) 
         asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(ncols) : "memory");
 }
 
-// Bounded waits that also give up once another role of the CTA has raised the abort flag.
+// Bounded wait that also gives up once another role of the CTA has raised
+// the abort flag.  The thread sleeps in hardware: warps that poll take the
+// issue slots of the one that issues the MMAs (measured: a stage of the NVFP4
+// product took twice the time).
 __device__ __forceinline__ bool gg_wait(uint64_t* bar, uint32_t parity, int* abort) {
+    if (mbar_try_wait(bar, parity)) return true;
     for (uint32_t i = 0; i < kGgWaitLimit; ++i) {
-        if (mbar_try_wait(bar, parity)) return true;
-        if ((i & 63u) == 63u && *(volatile int*)abort) return false;
+        if (mbar_try_wait_sleep(bar, parity, kGgWaitNs)) return true;
+        if (*(volatile int*)abort) return false;
     }
     *(volatile int*)abort = 1;
     return false;
+}
+
+// The segment of tile `it`, which is not before segment e.
+__device__ __forceinline__ int gg_seek(const int* start, int E, int it, int e) {
+    if (it < start[e + 1]) return e;
+    int lo = e + 1, hi = E - 1;  // the last segment with start <= it
+    while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (start[mid] <= it)
+            lo = mid;
+        else
+            hi = mid - 1;
+    }
+    return lo;
+}
+
+// Bounded wait for what is certainly under way, abort or not.
+__device__ __forceinline__ void gg_settle(uint64_t* bar, uint32_t parity) {
+    for (uint32_t i = 0; i < kGgWaitLimit; ++i)
+        if (mbar_try_wait_sleep(bar, parity, kGgWaitNs)) return;
 }
 
 // The producer's teardown: no copy, and no release of a stage by the
@@ -232,7 +257,7 @@ template <int CG>
 __device__ __forceinline__ void gg_drain(GgShared* sh, uint32_t S, uint32_t armed, uint32_t rank) {
     for (uint32_t s = 0; s < S && s < armed; ++s) {
         const uint32_t last = armed - 1u - ((armed - 1u - s) % S);
-        if (rank == 0) mbar_wait(&sh->full[s], (last / S) & 1u, kGgWaitLimit);
+        if (rank == 0) gg_settle(&sh->full[s], (last / S) & 1u);
         if (CG == 2) gg_wait(&sh->empty[s], (last / S) & 1u, &sh->abort);
     }
     if (rank != 0 && *(volatile int*)&sh->abort)
@@ -446,7 +471,7 @@ __global__ void __launch_bounds__(kGgThreads, 1) gg_kernel(const __grid_constant
                 q0 = sh->p0[e];
                 nk = (sh->cnt[e] + 63) / 64;
             } else {
-                while (sh->start[e + 1] <= it) ++e;
+                e = gg_seek(sh->start, p.E, it, e);
                 const int t = it - sh->start[e];
                 m0 = (t % mtiles) * Cfg::BM;
                 n0 = (t / mtiles) * Cfg::BN;
@@ -546,12 +571,16 @@ __global__ void __launch_bounds__(kGgThreads, 1) gg_kernel(const __grid_constant
                 if (lane == 0) {
                     const uint32_t sta = smem_u32(st);
                     for (int u = 0; u < ke; ++u) {
+                        // the 16-deep steps of a tile: 32 bytes of a K-major row, 16 rows of an MN-major tile
                         const uint32_t aa = sta + (uint32_t)u * kGgTile, ba = sta + b_off + (uint32_t)u * b_tile;
-                        for (int kk = 0; kk < steps; ++kk) {
-                            const uint64_t ad = MODE == kGgFwd ? umma_sdesc(aa + kk * 32) : umma_sdesc_mn(aa + kk * 2048, 8192);
-                            const uint64_t bd = MODE == kGgDw ? umma_sdesc_mn(ba + kk * 2048, 8192) : umma_sdesc(ba + kk * 32);
-                            gg_mma<CG>(tacc, ad, bd, idesc, (k0 > 0 || u > 0 || kk > 0) ? 1u : 0u);
-                        }
+                        const uint64_t ad = MODE == kGgFwd ? umma_sdesc(aa) : umma_sdesc_mn(aa, 8192);
+                        const uint64_t bd = MODE == kGgDw ? umma_sdesc_mn(ba, 8192) : umma_sdesc(ba);
+#pragma unroll
+                        for (int kk = 0; kk < 4; ++kk)
+                            if (kk < steps)
+                                gg_mma<CG>(tacc, ad + (uint64_t)(kk * (MODE == kGgFwd ? 32 : 2048) / 16),
+                                           bd + (uint64_t)(kk * (MODE == kGgDw ? 2048 : 32) / 16), idesc,
+                                           (k0 > 0 || u > 0 || kk > 0) ? 1u : 0u);
                     }
                     gg_commit<CG>(&sh->empty[s]);
                 }
@@ -563,7 +592,7 @@ __global__ void __launch_bounds__(kGgThreads, 1) gg_kernel(const __grid_constant
         });
         if (rank == 0 && lane == 0) {
             gg_commit_own<CG>(&sh->mma_done);
-            mbar_wait(&sh->mma_done, 0u, kGgWaitLimit);
+            gg_settle(&sh->mma_done, 0u);
         }
         __syncwarp();
     } else {

@@ -403,7 +403,7 @@ __global__ void __launch_bounds__(kG4Threads, 1) g4_kernel(const __grid_constant
     auto walk = [&](auto f) {
         int e = 0;
         for (int it = unit; it < sh->start[p.E]; it += units) {
-            while (sh->start[e + 1] <= it) ++e;
+            e = gg_seek(sh->start, p.E, it, e);
             const int t = it - sh->start[e];
             const int m0 = (t % mtiles) * 128 * CG + (int)rank * 128, n0 = (t / mtiles) * Cfg::BN;
             if (!f(e, sh->p0[e] + n0, min(Cfg::BN, sh->cnt[e] - n0), m0)) break;
@@ -444,7 +444,7 @@ __global__ void __launch_bounds__(kG4Threads, 1) g4_kernel(const __grid_constant
             gg_drain<CG>(sh, S, armed, rank);
             for (uint32_t u = 0; u < 2 && u < c; ++u) {
                 const uint32_t last = c - 1u - ((c - 1u - u) & 1u);
-                mbar_wait(&s4->cfull[u], (last >> 1) & 1u, kGgWaitLimit);
+                gg_settle(&s4->cfull[u], (last >> 1) & 1u);
             }
         }
         __syncwarp();
@@ -468,9 +468,12 @@ __global__ void __launch_bounds__(kG4Threads, 1) g4_kernel(const __grid_constant
                     const uint32_t st = smem_u32(ring + (size_t)s * stage_bytes);
                     const uint32_t sfa = tmem + kG4SfCol + f * (uint32_t)(Cfg::SFA + Cfg::SFB), sfb = sfa + Cfg::SFA;
                     const int steps = min(4, (p.K - k * 256 + 63) / 64);
-                    for (int kk = 0; kk < steps; ++kk)
-                        umma_nvfp4<CG>(tacc, umma_sdesc(st + kk * 32), umma_sdesc(st + kG4A + kk * 32), idesc,
-                                       sfa + kk * (Cfg::SFA / 4), sfb + kk * (Cfg::SFB / 4), (k > 0 || kk > 0) ? 1u : 0u);
+                    const uint64_t ad = umma_sdesc(st), bd = umma_sdesc(st + kG4A);
+#pragma unroll
+                    for (int kk = 0; kk < 4; ++kk)
+                        if (kk < steps)
+                            umma_nvfp4<CG>(tacc, ad + (uint64_t)(kk * 2), bd + (uint64_t)(kk * 2), idesc,
+                                           sfa + kk * (Cfg::SFA / 4), sfb + kk * (Cfg::SFB / 4), (k > 0 || kk > 0) ? 1u : 0u);
                     gg_commit<CG>(&sh->empty[s]);
                     gg_commit<CG>(&s4->sempty[f]);
                 }
@@ -482,7 +485,7 @@ __global__ void __launch_bounds__(kG4Threads, 1) g4_kernel(const __grid_constant
         });
         if (rank == 0 && lane == 0) {
             gg_commit_own<CG>(&sh->mma_done);
-            mbar_wait(&sh->mma_done, 0u, kGgWaitLimit);
+            gg_settle(&sh->mma_done, 0u);
         }
         __syncwarp();
     } else if (warp >= 10) {
