@@ -35,6 +35,7 @@ constexpr uint32_t kGgTmemCols = 512;
 
 struct GgParams {
     CUtensorMap ta, tb;
+    CUtensorMap tb_all;  // forward, dx: tb with boxes of 128 rows
     const int32_t* offsets;  // [E + 1]
     int E, R;
     int M;     // extent of the output's contiguous dimension
@@ -70,12 +71,40 @@ struct GgShared {
 static_assert(sizeof(GgShared) <= 4096, "control block");
 
 // ------------------------------------------------------------ PTX wrappers
-__device__ __forceinline__ void tma_load_3d(void* dst, const CUtensorMap* map, int c0, int c1, int c2, uint64_t* bar) {
-    asm volatile(
-        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(
-            smem_u32(dst)),
-        "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(smem_u32(bar))
-        : "memory");
+// Tiled loads of a stage, from and to 32-bit shared-memory addresses.  Of a
+// pair (CG = 2) each CTA loads its own tiles, and `bar` is the leader's
+// barrier (an address of the cluster's shared memory): one barrier then says
+// that both CTAs' tiles landed.
+template <int CG>
+__device__ __forceinline__ void gg_load2(uint32_t dst, const CUtensorMap* map, int c0, int c1, uint32_t bar) {
+    if (CG == 1)
+        asm volatile(
+            "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(
+                dst),
+            "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(bar)
+            : "memory");
+    else
+        asm volatile(
+            "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2 [%0], [%1, {%2, %3}], [%4];" ::"r"(
+                dst),
+            "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(bar)
+            : "memory");
+}
+
+template <int CG>
+__device__ __forceinline__ void gg_load3(uint32_t dst, const CUtensorMap* map, int c0, int c1, int c2, uint32_t bar) {
+    if (CG == 1)
+        asm volatile(
+            "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(
+                dst),
+            "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(bar)
+            : "memory");
+    else
+        asm volatile(
+            "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2 [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(
+                dst),
+            "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(bar)
+            : "memory");
 }
 
 __device__ __forceinline__ uint32_t cluster_rank() {
@@ -88,47 +117,11 @@ __device__ __forceinline__ void cluster_sync() {
     asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
-// Tiled loads into this CTA whose bytes are counted on the pair leader's
-// barrier (an address of the cluster's shared memory), so that one barrier
-// says that both CTAs' tiles landed.
-__device__ __forceinline__ void tma_load_2d_pair(void* dst, const CUtensorMap* map, int c0, int c1, uint32_t bar) {
-    asm volatile(
-        "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2 [%0], [%1, {%2, %3}], [%4];" ::"r"(
-            smem_u32(dst)),
-        "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(bar)
-        : "memory");
-}
-
-__device__ __forceinline__ void tma_load_3d_pair(void* dst, const CUtensorMap* map, int c0, int c1, int c2,
-                                                 uint32_t bar) {
-    asm volatile(
-        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2 [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(
-            smem_u32(dst)),
-        "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(bar)
-        : "memory");
-}
-
 // The address in CTA `rank` of the cluster of what is at p here.
 __device__ __forceinline__ uint32_t cluster_addr(const void* p, uint32_t rank) {
     uint32_t a;
     asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_u32(p)), "r"(rank));
     return a;
-}
-
-// Loads of a stage's tiles: `bar` is this CTA's barrier, of a pair the leader's.
-template <int CG>
-__device__ __forceinline__ void gg_load2(void* dst, const CUtensorMap* map, int c0, int c1, uint64_t* bar) {
-    if (CG == 1)
-        tma_load_2d(dst, map, c0, c1, bar);
-    else
-        tma_load_2d_pair(dst, map, c0, c1, cluster_addr(bar, 0));
-}
-template <int CG>
-__device__ __forceinline__ void gg_load3(void* dst, const CUtensorMap* map, int c0, int c1, int c2, uint64_t* bar) {
-    if (CG == 1)
-        tma_load_3d(dst, map, c0, c1, c2, bar);
-    else
-        tma_load_3d_pair(dst, map, c0, c1, c2, cluster_addr(bar, 0));
 }
 
 // Arrive on the barrier at the same place in CTA `rank` of the cluster.  The
@@ -229,6 +222,20 @@ __device__ __forceinline__ bool gg_wait(uint64_t* bar, uint32_t parity, int* abo
     return false;
 }
 
+// A place in a ring of S stages and the parity of its current use: waits and
+// addresses without a division in the single-thread issue loops, whose time a
+// stage would otherwise be bound by.
+struct GgRing {
+    uint32_t s = 0, ph = 0, uses = 0;
+    __device__ __forceinline__ void next(uint32_t S) {
+        ++uses;
+        if (++s == S) {
+            s = 0;
+            ph ^= 1u;
+        }
+    }
+};
+
 // The segment of tile `it`, which is not before segment e.
 __device__ __forceinline__ int gg_seek(const int* start, int E, int it, int e) {
     if (it < start[e + 1]) return e;
@@ -254,11 +261,11 @@ __device__ __forceinline__ void gg_settle(uint64_t* bar, uint32_t parity) {
 // counted on the leader's barriers; after an abort the other CTA, which
 // cannot wait on them, gives its own the time to land.)
 template <int CG>
-__device__ __forceinline__ void gg_drain(GgShared* sh, uint32_t S, uint32_t armed, uint32_t rank) {
-    for (uint32_t s = 0; s < S && s < armed; ++s) {
-        const uint32_t last = armed - 1u - ((armed - 1u - s) % S);
-        if (rank == 0) gg_settle(&sh->full[s], (last / S) & 1u);
-        if (CG == 2) gg_wait(&sh->empty[s], (last / S) & 1u, &sh->abort);
+__device__ __forceinline__ void gg_drain(GgShared* sh, uint32_t S, const GgRing& r, uint32_t rank) {
+    for (uint32_t s = 0; s < S && s < r.uses; ++s) {
+        const uint32_t ph = s < r.s ? r.ph : r.ph ^ 1u;  // the parity of the stage's last use
+        if (rank == 0) gg_settle(&sh->full[s], ph);
+        if (CG == 2) gg_wait(&sh->empty[s], ph, &sh->abort);
     }
     if (rank != 0 && *(volatile int*)&sh->abort)
         for (int i = 0; i < 1000; ++i) __nanosleep(1000);
@@ -331,14 +338,16 @@ __device__ __forceinline__ void gg_ld_wait(uint32_t (&r)[32]) {
                  : "memory");
 }
 
-// This lane's two neighbouring m of one row, in bf16, from the values of two
-// rows in lanes 2i and 2i + 1: the even lane keeps the first row, the odd the second.
-__device__ __forceinline__ uint32_t gg_pair(uint32_t first, uint32_t second, int odd) {
-    const uint32_t other = __shfl_xor_sync(0xffffffffu, odd ? first : second, 1);
-    const __nv_bfloat162 b =
-        __floats2bfloat162_rn(__uint_as_float(odd ? other : first), __uint_as_float(odd ? second : other));
+// This lane's two neighbouring m of one row, in bf16, from two rows' values
+// in lanes 2i and 2i + 1: the even lane takes the first row, the odd the second.
+__device__ __forceinline__ uint32_t gg_pack(uint32_t first, uint32_t second) {
+    const __nv_bfloat162 b = __floats2bfloat162_rn(__uint_as_float(first), __uint_as_float(second));
     return *reinterpret_cast<const uint32_t*>(&b);
 }
+__device__ __forceinline__ uint32_t gg_pair(uint32_t packed, uint32_t select) {
+    return __byte_perm(packed, __shfl_xor_sync(0xffffffffu, packed, 1), select);
+}
+__device__ __forceinline__ uint32_t gg_pair_select(int odd) { return odd ? 0x3276u : 0x5410u; }
 
 // Store 32 columns (output rows row0 .. row0 + nc - 1) of this lane's m:
 // fp32 as they are, a warp writing 128 contiguous bytes a row; bf16 after
@@ -361,15 +370,16 @@ __device__ __forceinline__ void gg_store32(const uint32_t (&r)[32], void* out, i
         return;
     }
     const int odd = m & 1;
+    const uint32_t sel = gg_pair_select(odd);
     uint32_t* o = reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(out) + (row0 + odd) * (size_t)M + (m - odd));
     const int last = m < M ? nc - odd : 0;  // rows row0 + odd + j, j < last
     if (__all_sync(0xffffffffu, whole && m < M)) {
 #pragma unroll
-        for (int j = 0; j < 32; j += 2, o += M) *o = gg_pair(r[j], r[j + 1], odd);
+        for (int j = 0; j < 32; j += 2, o += M) *o = gg_pair(gg_pack(r[j], r[j + 1]), sel);
     } else {
 #pragma unroll
         for (int j = 0; j < 32; j += 2, o += M) {
-            const uint32_t v = gg_pair(r[j], r[j + 1], odd);
+            const uint32_t v = gg_pair(gg_pack(r[j], r[j + 1]), sel);
             if (j < last) *o = v;
         }
     }
@@ -484,66 +494,69 @@ __global__ void __launch_bounds__(kGgThreads, 1) gg_kernel(const __grid_constant
     };
 
     if (warp == 4) {
-        uint32_t g = 0, armed = 0;
+        // ---------------- TMA producer
+        GgRing r;
+        const uint32_t ring_at = smem_u32(ring);
+        const uint32_t bars = CG == 1 ? smem_u32(sh->full) : cluster_addr(sh->full, 0);
         if (lane == 0) {
             walk([&](int e, int q0, int n, int n0, int m0, int nk) -> bool {
                 // rows of B that this CTA holds (forward, dx), in whole boxes
                 const int rows = MODE == kGgDw ? 128 : (n + kGgBoxN * CG - 1) / (kGgBoxN * CG) * kGgBoxN;
-                const uint32_t bytes = kGgTile + (uint32_t)rows * 128u;
+                const uint32_t bytes = CG * (kGgTile + (uint32_t)rows * 128u);
                 const int am = m0 + (int)rank * 128, bn = (MODE == kGgDw ? n0 : q0) + (int)rank * rows;
-                for (int k0 = 0; k0 < nk; k0 += Cfg::KSUB, ++g) {
-                    const uint32_t s = g % S, ph = (g / S) & 1u;
-                    if (g >= S && !gg_wait(&sh->empty[s], ph ^ 1u, &sh->abort)) return false;
-                    unsigned char* st = ring + (size_t)s * stage_bytes;
+                for (int k0 = 0; k0 < nk; k0 += Cfg::KSUB) {
+                    if (!gg_wait(&sh->empty[r.s], r.ph ^ 1u, &sh->abort)) return false;
+                    const uint32_t st = ring_at + r.s * stage_bytes, bar = bars + r.s * 8u;
                     const int ke = min(Cfg::KSUB, nk - k0);
-                    if (rank == 0) mbar_arrive_expect_tx(&sh->full[s], (uint32_t)(ke * CG) * bytes);
-                    armed = g + 1u;
-                    for (int u = 0; u < ke; ++u) {
-                        unsigned char* sa = st + (size_t)u * kGgTile;
-                        unsigned char* sb = st + b_off + (size_t)u * b_tile;
+                    if (rank == 0) mbar_arrive_expect_tx(&sh->full[r.s], (uint32_t)ke * bytes);
+#pragma unroll
+                    for (int u = 0; u < Cfg::KSUB; ++u) {
+                        if (u >= ke) break;
+                        const uint32_t sa = st + u * kGgTile, sb = st + b_off + u * b_tile;
                         const int c = (k0 + u) * 64;
                         if (MODE == kGgFwd) {
-                            gg_load3<CG>(sa, &p.ta, c, am, e, &sh->full[s]);
+                            gg_load3<CG>(sa, &p.ta, c, am, e, bar);
                         } else if (MODE == kGgDx) {
-                            gg_load3<CG>(sa, &p.ta, am, c, e, &sh->full[s]);
-                            gg_load3<CG>(sa + 8192, &p.ta, am + 64, c, e, &sh->full[s]);
+                            gg_load3<CG>(sa, &p.ta, am, c, e, bar);
+                            gg_load3<CG>(sa + 8192, &p.ta, am + 64, c, e, bar);
                         } else {
-                            gg_load2<CG>(sa, &p.ta, am, q0 + c, &sh->full[s]);
-                            gg_load2<CG>(sa + 8192, &p.ta, am + 64, q0 + c, &sh->full[s]);
+                            gg_load2<CG>(sa, &p.ta, am, q0 + c, bar);
+                            gg_load2<CG>(sa + 8192, &p.ta, am + 64, q0 + c, bar);
                         }
                         if (MODE == kGgDw) {
-                            gg_load2<CG>(sb, &p.tb, bn, q0 + c, &sh->full[s]);
-                            gg_load2<CG>(sb + 8192, &p.tb, bn + 64, q0 + c, &sh->full[s]);
+                            gg_load2<CG>(sb, &p.tb, bn, q0 + c, bar);
+                            gg_load2<CG>(sb + 8192, &p.tb, bn + 64, q0 + c, bar);
+                        } else if (rows == 128) {
+                            gg_load2<CG>(sb, &p.tb_all, c, bn, bar);
                         } else {
-                            for (int r = 0; r < rows; r += kGgBoxN)
-                                gg_load2<CG>(sb + r * 128, &p.tb, c, bn + r, &sh->full[s]);
+                            for (int i = 0; i < rows; i += kGgBoxN) gg_load2<CG>(sb + i * 128, &p.tb, c, bn + i, bar);
                         }
                     }
+                    r.next(S);
                 }
                 return true;
             });
-            gg_drain<CG>(sh, S, armed, rank);
+            gg_drain<CG>(sh, S, r, rank);
         }
         __syncwarp();
     } else if (warp == 5) {
-        uint32_t g = 0;
-        int d = 0;
+        // ---------------- MMA issuer (one thread of the leader)
+        GgRing r;
+        int buf = 0;
+        uint32_t free_ph = 1;  // parity of acc_empty to wait for (at first: nothing)
+        const uint32_t ring_at = smem_u32(ring);
         if (rank == 0) walk([&](int e, int q0, int n, int n0, int m0, int nk) -> bool {
             if (nk == 0) return true;
-            const int buf = d & 1, use = d >> 1;
-            ++d;
-            if (use > 0 && !gg_wait(&sh->acc_empty[buf], (uint32_t)((use - 1) & 1), &sh->abort))
-                return false;
+            if (!gg_wait(&sh->acc_empty[buf], free_ph, &sh->abort)) return false;
             tc_fence_after();
             const uint32_t tacc = tmem + (uint32_t)(buf * Cfg::BN);
             const int npad = MODE == kGgDw ? Cfg::BN : (n + kGgBoxN * CG - 1) / (kGgBoxN * CG) * (kGgBoxN * CG);
             const uint32_t idesc = umma_idesc_bf16(Cfg::BM, npad) | (MODE != kGgFwd ? 1u << 15 : 0u) |
                                    (MODE == kGgDw ? 1u << 16 : 0u);
-            for (int k0 = 0; k0 < nk; k0 += Cfg::KSUB, ++g) {
-                const uint32_t s = g % S, ph = (g / S) & 1u;
-                if (!gg_wait(&sh->full[s], ph, &sh->abort)) return false;
-                unsigned char* st = ring + (size_t)s * stage_bytes;
-                const int ke = min(Cfg::KSUB, nk - k0);
+            uint32_t acc = 0;
+            for (int k0 = 0; k0 < nk; k0 += Cfg::KSUB) {
+                if (!gg_wait(&sh->full[r.s], r.ph, &sh->abort)) return false;
+                const uint32_t sta = ring_at + r.s * stage_bytes;
                 int steps = 4;  // MMAs (16 deep) of a 64-wide step
                 if (MODE == kGgDw) {
                     // the segment's end: rows behind it belong to the next
@@ -553,6 +566,7 @@ __global__ void __launch_bounds__(kGgThreads, 1) gg_kernel(const __grid_constant
                     const int valid = sh->cnt[e] - k0 * 64;
                     if (valid < 64) {
                         steps = (valid + 15) / 16;
+                        unsigned char* st = ring + (size_t)r.s * stage_bytes;
                         for (int i = lane; i < (steps * 16 - valid) * 32; i += 32) {
                             const int blk = i & 3, ch = (i >> 2) & 7, row = valid + (i >> 5);
                             unsigned char* at = st + (blk >> 1) * b_off + (blk & 1) * 8192 + row * 128 + ch * 16;
@@ -569,25 +583,31 @@ __global__ void __launch_bounds__(kGgThreads, 1) gg_kernel(const __grid_constant
                 }
                 tc_fence_after();
                 if (lane == 0) {
-                    const uint32_t sta = smem_u32(st);
-                    for (int u = 0; u < ke; ++u) {
+                    const int ke = min(Cfg::KSUB, nk - k0);
+#pragma unroll
+                    for (int u = 0; u < Cfg::KSUB; ++u) {
+                        if (u >= ke) break;
                         // the 16-deep steps of a tile: 32 bytes of a K-major row, 16 rows of an MN-major tile
-                        const uint32_t aa = sta + (uint32_t)u * kGgTile, ba = sta + b_off + (uint32_t)u * b_tile;
+                        const uint32_t aa = sta + u * kGgTile, ba = sta + b_off + u * b_tile;
                         const uint64_t ad = MODE == kGgFwd ? umma_sdesc(aa) : umma_sdesc_mn(aa, 8192);
                         const uint64_t bd = MODE == kGgDw ? umma_sdesc_mn(ba, 8192) : umma_sdesc(ba);
 #pragma unroll
-                        for (int kk = 0; kk < 4; ++kk)
-                            if (kk < steps)
-                                gg_mma<CG>(tacc, ad + (uint64_t)(kk * (MODE == kGgFwd ? 32 : 2048) / 16),
-                                           bd + (uint64_t)(kk * (MODE == kGgDw ? 2048 : 32) / 16), idesc,
-                                           (k0 > 0 || u > 0 || kk > 0) ? 1u : 0u);
+                        for (int kk = 0; kk < 4; ++kk) {
+                            if (MODE == kGgDw && kk >= steps) break;
+                            gg_mma<CG>(tacc, ad + (uint64_t)(kk * (MODE == kGgFwd ? 32 : 2048) / 16),
+                                       bd + (uint64_t)(kk * (MODE == kGgDw ? 2048 : 32) / 16), idesc, acc);
+                            acc = 1;
+                        }
                     }
-                    gg_commit<CG>(&sh->empty[s]);
+                    gg_commit<CG>(&sh->empty[r.s]);
                 }
                 __syncwarp();
+                r.next(S);
             }
             if (lane == 0) gg_commit<CG>(&sh->acc_full[buf]);
             __syncwarp();
+            buf ^= 1;
+            if (buf == 0) free_ph ^= 1u;
             return true;
         });
         if (rank == 0 && lane == 0) {

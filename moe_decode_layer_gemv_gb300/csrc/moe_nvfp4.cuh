@@ -253,7 +253,7 @@ constexpr int kG4Epi = 8;                 // epilogue warps: lane quarter w & 3,
 constexpr int kG4Threads = 32 * (kG4Epi + 6);  // warp 8 TMA, 9 MMA, 10-13 scales
 constexpr int kG4A = 128 * 128;           // codes of 128 rows x 256 elements
 constexpr int kG4SfStages = 4;            // stages whose scales one copy brings: 64 bytes a row
-constexpr int kG4MaxStages = 9;
+constexpr int kG4MaxStages = 8;
 constexpr uint32_t kG4SfCol = 256;        // tensor-memory column of the scales, behind the accumulators
 
 // CG = 1: 128 x 128 tiles, two accumulators.  CG = 2 (a CTA pair): 256 x 256
@@ -265,7 +265,7 @@ struct G4Cfg {
     static constexpr int BN = 128 * CG;
     static constexpr int ACC = CG == 1 ? 2 : 1;
     static constexpr int SFA = 16, SFB = BN / 32 * 4;        // columns a stage
-    static constexpr int F = 256 / (SFA + SFB);              // stages of scales in tensor memory (8, 5)
+    static constexpr int S = 256 / (SFA + SFB);              // stages whose scales tensor memory holds (8, 5)
 };
 
 template <int V>
@@ -275,6 +275,7 @@ struct IntC {
 
 struct G4Params {
     CUtensorMap ta, tb;    // wq [E, N, K/2], xq [R, K/2] bytes
+    CUtensorMap tb_all;    // tb with boxes of 128 rows
     CUtensorMap tsa, tsb;  // wbs [E, N, K/16], xbs [R, K/16] bytes (K % 256 == 0)
     const uint8_t *wbs, *xbs;
     const float *wgs, *xgs;
@@ -287,10 +288,12 @@ struct G4Params {
 
 struct G4Shared {
     GgShared g;
-    uint64_t sfull[8], sempty[8];  // a stage's scales are in tensor memory (leader: of both CTAs); its MMAs are done
+    uint64_t sfull[kG4MaxStages];  // leader: a stage's scales are in tensor memory (of both CTAs)
+    alignas(16) float xg[kG4Epi][128];  // the epilogue warps' row scales
     uint64_t cfull[2], cempty[2];  // a copy of scales is in shared memory; the scale warps have read it
 };
-static_assert(sizeof(G4Shared) <= 4096, "control block");
+constexpr int kG4Control = 8192;
+static_assert(sizeof(G4Shared) <= kG4Control, "control block");
 
 // Instruction descriptor, kind::mxf4nvf4: E2M1 A and B, E4M3 scales.
 __device__ __forceinline__ uint32_t umma_idesc_nvfp4(int M, int N) {
@@ -362,10 +365,7 @@ __global__ void __launch_bounds__(kG4Threads, 1) g4_kernel(const __grid_constant
         for (int s = 0; s < kG4MaxStages; ++s) {
             mbar_init(&sh->full[s], 1);
             mbar_init(&sh->empty[s], 1);
-        }
-        for (int f = 0; f < 8; ++f) {
-            mbar_init(&s4->sfull[f], 4 * CG);
-            mbar_init(&s4->sempty[f], 1);
+            mbar_init(&s4->sfull[s], 4 * CG);
         }
         for (int a = 0; a < 2; ++a) {
             mbar_init(&sh->acc_full[a], 1);
@@ -394,10 +394,10 @@ __global__ void __launch_bounds__(kG4Threads, 1) g4_kernel(const __grid_constant
     const int nrows = CG == 2 ? Cfg::BN : min(Cfg::BN, max(kGgBoxN, (sh->nmax + kGgBoxN - 1) / kGgBoxN * kGgBoxN));
     const bool sf_tma = (p.K & 255) == 0;
     const uint32_t sf_bytes = sf_tma ? (128u + (uint32_t)nrows) * 64u : 0u;
-    unsigned char* sfbuf = base + 4096;
+    unsigned char* sfbuf = base + kG4Control;
     unsigned char* ring = sfbuf + 2 * sf_bytes;
     const uint32_t stage_bytes = kG4A + (uint32_t)(nrows / CG) * 128u;
-    const uint32_t S = min((uint32_t)kG4MaxStages, ((uint32_t)kGgSmem - 1023u - 4096u - 2u * sf_bytes) / stage_bytes);
+    const uint32_t S = min((uint32_t)Cfg::S, ((uint32_t)kGgSmem - 1023u - (uint32_t)kG4Control - 2u * sf_bytes) / stage_bytes);
     const int nk = (p.K + 255) / 256, nb = p.K / 16;
 
     auto walk = [&](auto f) {
@@ -414,73 +414,78 @@ __global__ void __launch_bounds__(kG4Threads, 1) g4_kernel(const __grid_constant
 
     if (warp == 8) {
         // ---------------- TMA producer
-        uint32_t g = 0, armed = 0, c = 0;
+        GgRing r, c;
+        const uint32_t ring_at = smem_u32(ring), sf_at = smem_u32(sfbuf);
+        const uint32_t bars = CG == 1 ? smem_u32(sh->full) : cluster_addr(sh->full, 0);
         if (lane == 0) {
             walk([&](int e, int q0, int n, int m0) -> bool {
                 const int rows = share(n);
-                for (int k = 0; k < nk; ++k, ++g) {
+                for (int k = 0; k < nk; ++k) {
                     if (sf_tma && k % kG4SfStages == 0) {
-                        const uint32_t u = c & 1u;
-                        if (c >= 2 && !gg_wait(&s4->cempty[u], ((c >> 1) - 1u) & 1u, &sh->abort)) return false;
-                        unsigned char* sf = sfbuf + u * sf_bytes;
-                        mbar_arrive_expect_tx(&s4->cfull[u], (128u + (uint32_t)(rows * CG)) * 64u);
-                        ++c;
-                        tma_load_3d(sf, &p.tsa, k * 16, m0, e, &s4->cfull[u]);
-                        for (int r = 0; r < rows * CG; r += kGgBoxN)
-                            tma_load_2d(sf + 8192 + r * 64, &p.tsb, k * 16, q0 + r, &s4->cfull[u]);
+                        if (!gg_wait(&s4->cempty[c.s], c.ph ^ 1u, &sh->abort)) return false;
+                        const uint32_t sf = sf_at + c.s * sf_bytes, bar = smem_u32(&s4->cfull[c.s]);
+                        mbar_arrive_expect_tx(&s4->cfull[c.s], (128u + (uint32_t)(rows * CG)) * 64u);
+                        gg_load3<1>(sf, &p.tsa, k * 16, m0, e, bar);
+                        for (int i = 0; i < rows * CG; i += kGgBoxN)
+                            gg_load2<1>(sf + 8192 + i * 64, &p.tsb, k * 16, q0 + i, bar);
+                        c.next(2);
                     }
-                    const uint32_t s = g % S, ph = (g / S) & 1u;
-                    if (g >= S && !gg_wait(&sh->empty[s], ph ^ 1u, &sh->abort)) return false;
-                    unsigned char* st = ring + (size_t)s * stage_bytes;
-                    if (rank == 0) mbar_arrive_expect_tx(&sh->full[s], CG * (kG4A + (uint32_t)rows * 128u));
-                    armed = g + 1u;
-                    gg_load3<CG>(st, &p.ta, k * 128, m0, e, &sh->full[s]);
-                    for (int r = 0; r < rows; r += kGgBoxN)
-                        gg_load2<CG>(st + kG4A + r * 128, &p.tb, k * 128, q0 + (int)rank * rows + r, &sh->full[s]);
+                    if (!gg_wait(&sh->empty[r.s], r.ph ^ 1u, &sh->abort)) return false;
+                    const uint32_t st = ring_at + r.s * stage_bytes, bar = bars + r.s * 8u;
+                    if (rank == 0) mbar_arrive_expect_tx(&sh->full[r.s], CG * (kG4A + (uint32_t)rows * 128u));
+                    gg_load3<CG>(st, &p.ta, k * 128, m0, e, bar);
+                    if (rows == 128)
+                        gg_load2<CG>(st + kG4A, &p.tb_all, k * 128, q0 + (int)rank * 128, bar);
+                    else
+                        for (int i = 0; i < rows; i += kGgBoxN)
+                            gg_load2<CG>(st + kG4A + i * 128, &p.tb, k * 128, q0 + (int)rank * rows + i, bar);
+                    r.next(S);
                 }
                 return true;
             });
             // teardown: also the copies of scales have landed
-            gg_drain<CG>(sh, S, armed, rank);
-            for (uint32_t u = 0; u < 2 && u < c; ++u) {
-                const uint32_t last = c - 1u - ((c - 1u - u) & 1u);
-                gg_settle(&s4->cfull[u], (last >> 1) & 1u);
-            }
+            gg_drain<CG>(sh, S, r, rank);
+            for (uint32_t u = 0; u < 2 && u < c.uses; ++u) gg_settle(&s4->cfull[u], u < c.s ? c.ph : c.ph ^ 1u);
         }
         __syncwarp();
     } else if (warp == 9) {
         // ---------------- MMA issuer (one thread of the leader)
-        uint32_t g = 0;
-        int d = 0;
+        GgRing r;
+        int buf = 0;
+        uint32_t free_ph = 1;
+        const uint32_t ring_at = smem_u32(ring);
         if (rank == 0) walk([&](int e, int q0, int n, int m0) -> bool {
-            const int buf = d % Cfg::ACC, use = d / Cfg::ACC;
-            ++d;
-            if (use > 0 && !gg_wait(&sh->acc_empty[buf], (uint32_t)((use - 1) & 1), &sh->abort)) return false;
+            const uint32_t idesc = umma_idesc_nvfp4(128 * CG, share(n) * CG);
+            if (!gg_wait(&sh->acc_empty[buf], free_ph, &sh->abort)) return false;
             tc_fence_after();
             const uint32_t tacc = tmem + (uint32_t)(buf * Cfg::BN);
-            const uint32_t idesc = umma_idesc_nvfp4(128 * CG, share(n) * CG);
-            for (int k = 0; k < nk; ++k, ++g) {
-                const uint32_t s = g % S, f = g % (uint32_t)Cfg::F;
-                if (!gg_wait(&sh->full[s], (g / S) & 1u, &sh->abort)) return false;
-                if (!gg_wait(&s4->sfull[f], (g / (uint32_t)Cfg::F) & 1u, &sh->abort)) return false;
+            uint32_t acc = 0;
+            for (int k = 0; k < nk; ++k) {
+                if (!gg_wait(&sh->full[r.s], r.ph, &sh->abort) || !gg_wait(&s4->sfull[r.s], r.ph, &sh->abort)) return false;
                 tc_fence_after();
                 if (lane == 0) {
-                    const uint32_t st = smem_u32(ring + (size_t)s * stage_bytes);
-                    const uint32_t sfa = tmem + kG4SfCol + f * (uint32_t)(Cfg::SFA + Cfg::SFB), sfb = sfa + Cfg::SFA;
-                    const int steps = min(4, (p.K - k * 256 + 63) / 64);
+                    const uint32_t st = ring_at + r.s * stage_bytes;
+                    const uint32_t sfa = tmem + kG4SfCol + r.s * (uint32_t)(Cfg::SFA + Cfg::SFB), sfb = sfa + Cfg::SFA;
+                    const int left = p.K - k * 256;
                     const uint64_t ad = umma_sdesc(st), bd = umma_sdesc(st + kG4A);
 #pragma unroll
-                    for (int kk = 0; kk < 4; ++kk)
-                        if (kk < steps)
-                            umma_nvfp4<CG>(tacc, ad + (uint64_t)(kk * 2), bd + (uint64_t)(kk * 2), idesc,
-                                           sfa + kk * (Cfg::SFA / 4), sfb + kk * (Cfg::SFB / 4), (k > 0 || kk > 0) ? 1u : 0u);
-                    gg_commit<CG>(&sh->empty[s]);
-                    gg_commit<CG>(&s4->sempty[f]);
+                    for (int kk = 0; kk < 4; ++kk) {
+                        if (kk * 64 >= left) break;
+                        umma_nvfp4<CG>(tacc, ad + (uint64_t)(kk * 2), bd + (uint64_t)(kk * 2), idesc,
+                                       sfa + kk * (Cfg::SFA / 4), sfb + kk * (Cfg::SFB / 4), acc);
+                        acc = 1;
+                    }
+                    gg_commit<CG>(&sh->empty[r.s]);
                 }
                 __syncwarp();
+                r.next(S);
             }
             if (lane == 0) gg_commit<CG>(&sh->acc_full[buf]);
             __syncwarp();
+            if (++buf == Cfg::ACC) {
+                buf = 0;
+                free_ph ^= 1u;
+            }
             return true;
         });
         if (rank == 0 && lane == 0) {
@@ -490,17 +495,16 @@ __global__ void __launch_bounds__(kG4Threads, 1) g4_kernel(const __grid_constant
         __syncwarp();
     } else if (warp >= 10) {
         // ---------------- scales into this warp's quarter of tensor memory
-        uint32_t g = 0, c = 0;
+        GgRing r, c;
         const uint32_t quarter = (uint32_t)((warp & 3) * 32) << 16;
         constexpr int NB = Cfg::BN / 32;
         walk([&](int e, int q0, int n, int m0) -> bool {
-            for (int k = 0; k < nk; ++k, ++g) {
+            for (int k = 0; k < nk; ++k) {
                 uint4 a[4], b[NB];
                 const int kq = k % kG4SfStages;
                 if (sf_tma) {
-                    const uint32_t u = c & 1u;
-                    if (kq == 0 && !gg_wait(&s4->cfull[u], (c >> 1) & 1u, &sh->abort)) return false;
-                    const unsigned char* sf = sfbuf + u * sf_bytes;
+                    if (kq == 0 && !gg_wait(&s4->cfull[c.s], c.ph, &sh->abort)) return false;
+                    const unsigned char* sf = sfbuf + c.s * sf_bytes;
                     // 64-byte swizzle: 16-byte chunk kq of row r is at chunk kq ^ ((r >> 1) & 3)
                     const int ch = (kq ^ ((lane >> 1) & 3)) * 16;
 #pragma unroll
@@ -511,8 +515,8 @@ __global__ void __launch_bounds__(kG4Threads, 1) g4_kernel(const __grid_constant
                                           : make_uint4(0, 0, 0, 0);
                     if (kq == kG4SfStages - 1 || k == nk - 1) {
                         __syncwarp();
-                        if (lane == 0) mbar_arrive(&s4->cempty[u]);
-                        ++c;
+                        if (lane == 0) mbar_arrive(&s4->cempty[c.s]);
+                        c.next(2);
                     }
                 } else {
                     // rows beyond the tile's end take the last one's scales:
@@ -525,11 +529,10 @@ __global__ void __launch_bounds__(kG4Threads, 1) g4_kernel(const __grid_constant
                         b[j] = 32 * j < n ? g4_row_scales(p.xbs + (size_t)(q0 + min(32 * j + lane, n - 1)) * nb, k * 16, nb)
                                           : make_uint4(0, 0, 0, 0);
                 }
-                const uint32_t f = g % (uint32_t)Cfg::F, use = g / (uint32_t)Cfg::F;
-                if (use > 0 && !gg_wait(&s4->sempty[f], (use - 1u) & 1u, &sh->abort)) return false;
+                if (!gg_wait(&sh->empty[r.s], r.ph ^ 1u, &sh->abort)) return false;
                 __syncwarp();
                 tc_fence_after();
-                const uint32_t at = tmem + quarter + kG4SfCol + f * (uint32_t)(Cfg::SFA + Cfg::SFB);
+                const uint32_t at = tmem + quarter + kG4SfCol + r.s * (uint32_t)(Cfg::SFA + Cfg::SFB);
                 const uint32_t wa[16] = {a[0].x, a[1].x, a[2].x, a[3].x, a[0].y, a[1].y, a[2].y, a[3].y,
                                          a[0].z, a[1].z, a[2].z, a[3].z, a[0].w, a[1].w, a[2].w, a[3].w};
                 tmem_st16(at, wa);
@@ -549,36 +552,32 @@ __global__ void __launch_bounds__(kG4Threads, 1) g4_kernel(const __grid_constant
                 __syncwarp();
                 if (lane == 0) {
                     if (CG == 1)
-                        mbar_arrive(&s4->sfull[f]);
+                        mbar_arrive(&s4->sfull[r.s]);
                     else
-                        mbar_arrive_cluster(&s4->sfull[f], 0);
+                        mbar_arrive_cluster(&s4->sfull[r.s], 0);
                 }
+                r.next(S);
             }
             return true;
         });
-        // no release by the other CTA's MMAs may be on its way at exit
-        if (CG == 2)
-            for (uint32_t f = 0; f < (uint32_t)Cfg::F && f < g; ++f) {
-                const uint32_t last = g - 1u - ((g - 1u - f) % (uint32_t)Cfg::F);
-                gg_wait(&s4->sempty[f], (last / (uint32_t)Cfg::F) & 1u, &sh->abort);
-            }
         __syncwarp();
     } else {
         // ---------------- epilogue: lane quarter warp & 3, half of the columns
-        int d = 0;
+        int buf = 0;
+        uint32_t full_ph = 0;
         constexpr int COLS = Cfg::BN / 2;
         const int c0 = (warp >> 2) * COLS;
+        float* xg = s4->xg[warp];  // this warp's columns' scales
         walk([&](int e, int q0, int n, int m0) -> bool {
-            const int m = m0 + (warp & 3) * 32 + lane;
+            const int m = m0 + (warp & 3) * 32 + lane, odd = m & 1;
+            const uint32_t sel = gg_pair_select(odd);
             const int mine = min(COLS, n - c0);  // columns of this warp; none below 1
             const float wg = __ldg(p.wgs + e);
-            float xg[COLS / 32];  // the scales of rows q0 + c0 + 32 i + lane
+            __syncwarp();
 #pragma unroll
-            for (int i = 0; i < COLS / 32; ++i)
-                xg[i] = 32 * i + lane < mine ? __ldg(p.xgs + q0 + c0 + 32 * i + lane) : 0.0f;
-            const int buf = d % Cfg::ACC, use = d / Cfg::ACC;
-            ++d;
-            if (!gg_wait(&sh->acc_full[buf], (uint32_t)(use & 1), &sh->abort)) return false;
+            for (int i = 0; i < COLS; i += 32) xg[i + lane] = i + lane < mine ? __ldg(p.xgs + q0 + c0 + i + lane) : 0.0f;
+            __syncwarp();
+            if (!gg_wait(&sh->acc_full[buf], full_ph, &sh->abort)) return false;
             __syncwarp();
             tc_fence_after();
             const uint32_t taddr = tmem + (uint32_t)(buf * Cfg::BN + c0) + ((uint32_t)((warp & 3) * 32) << 16);
@@ -592,30 +591,59 @@ __global__ void __launch_bounds__(kG4Threads, 1) g4_kernel(const __grid_constant
                         mbar_arrive_cluster(&sh->acc_empty[buf], 0);
                 }
             };
+            auto scaled = [&](uint32_t(&v)[32], int c) {
+#pragma unroll
+                for (int j = 0; j < 32; j += 4) {
+                    const float4 x = *reinterpret_cast<const float4*>(xg + c + j);
+                    v[j] = __float_as_uint(__uint_as_float(v[j]) * x.x * wg);
+                    v[j + 1] = __float_as_uint(__uint_as_float(v[j + 1]) * x.y * wg);
+                    v[j + 2] = __float_as_uint(__uint_as_float(v[j + 2]) * x.z * wg);
+                    v[j + 3] = __float_as_uint(__uint_as_float(v[j + 3]) * x.w * wg);
+                }
+            };
             if (mine <= 0) {
                 release();
-                return true;
-            }
-            // 64 columns to registers at a time; the accumulator is free once the last are there
-#pragma unroll
-            for (int h = 0; h < COLS / 64; ++h) {
-                if (64 * h >= mine) break;
-                uint32_t v[2][32];
-#pragma unroll
-                for (int i = 0; i < 2; ++i)
-                    if (64 * h + 32 * i < mine) gg_ld32(taddr + 64 * h + 32 * i, v[i]);
-#pragma unroll
-                for (int i = 0; i < 2; ++i) gg_ld_wait(v[i]);
-                if (64 * h + 64 >= mine) release();
-#pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    const int c = 64 * h + 32 * i;
-                    if (c >= mine) break;
-#pragma unroll
-                    for (int j = 0; j < 32; ++j)
-                        v[i][j] = __float_as_uint(__uint_as_float(v[i][j]) * __shfl_sync(0xffffffffu, xg[c / 32], j) * wg);
-                    gg_store32(v[i], p.out, p.out_f32, (size_t)q0 + c0 + c, min(32, mine - c), m, p.M);
+            } else if (p.out_f32) {
+#pragma unroll 1
+                for (int c = 0; c < mine; c += 32) {
+                    uint32_t v[32];
+                    gg_ld32(taddr + c, v);
+                    gg_ld_wait(v);
+                    if (c + 32 >= mine) release();
+                    scaled(v, c);
+                    gg_store32(v, p.out, 1, (size_t)q0 + c0 + c, min(32, mine - c), m, p.M);
                 }
+            } else {
+                // everything into registers as bf16, then the release, then the stores
+                uint32_t h[COLS / 32][16];
+#pragma unroll
+                for (int i = 0; i < COLS / 32; ++i) {
+                    if (32 * i >= mine) break;
+                    uint32_t v[32];
+                    gg_ld32(taddr + 32 * i, v);
+                    gg_ld_wait(v);
+                    if (32 * i + 32 >= mine) release();
+                    scaled(v, 32 * i);
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) h[i][j] = gg_pack(v[2 * j], v[2 * j + 1]);
+                }
+                uint32_t* o = reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(p.out) +
+                                                          ((size_t)q0 + c0 + odd) * (size_t)p.M + (m - odd));
+                const int last = m < p.M ? mine - odd : 0;  // rows q0 + c0 + odd + 2 j, 2 j < last
+                if (__all_sync(0xffffffffu, mine == COLS && m < p.M)) {
+#pragma unroll
+                    for (int j = 0; j < COLS / 2; ++j, o += p.M) *o = gg_pair(h[j / 16][j % 16], sel);
+                } else {
+#pragma unroll
+                    for (int j = 0; j < COLS / 2; ++j, o += p.M) {
+                        const uint32_t v = gg_pair(h[j / 16][j % 16], sel);
+                        if (2 * j < last) *o = v;
+                    }
+                }
+            }
+            if (++buf == Cfg::ACC) {
+                buf = 0;
+                full_ph ^= 1u;
             }
             return true;
         });

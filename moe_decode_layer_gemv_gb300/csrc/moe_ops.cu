@@ -67,9 +67,11 @@ template <int MODE>
 static int run_gg(GgParams& p, const void* a, const void* b, int R, int N, int K, int E, cudaStream_t st) {
     bool ok;
     if (MODE == kGgFwd)
-        ok = encode_map(&p.ta, a, 2, K, N, E, 128) && encode_map(&p.tb, b, 2, K, R, 0, kGgBoxN);
+        ok = encode_map(&p.ta, a, 2, K, N, E, 128) && encode_map(&p.tb, b, 2, K, R, 0, kGgBoxN) &&
+             encode_map(&p.tb_all, b, 2, K, R, 0, 128);
     else if (MODE == kGgDx)
-        ok = encode_map(&p.ta, a, 2, K, N, E, 64) && encode_map(&p.tb, b, 2, N, R, 0, kGgBoxN);
+        ok = encode_map(&p.ta, a, 2, K, N, E, 64) && encode_map(&p.tb, b, 2, N, R, 0, kGgBoxN) &&
+             encode_map(&p.tb_all, b, 2, N, R, 0, 128);
     else
         ok = encode_map(&p.ta, a, 2, K, R, 0, 64) && encode_map(&p.tb, b, 2, N, R, 0, 64);
     if (!ok) return MOE_ERR_UNSUPPORTED;
@@ -261,7 +263,8 @@ int moe_grouped_gemm_nvfp4(const uint8_t* xq, const uint8_t* xbs, const float* x
     MOE_OPT(dev_status);
     G4Params p;
     memset(&p, 0, sizeof p);
-    if (!encode_map(&p.ta, wq, 1, K / 2, N, E, 128) || !encode_map(&p.tb, xq, 1, K / 2, R, 0, kGgBoxN))
+    if (!encode_map(&p.ta, wq, 1, K / 2, N, E, 128) || !encode_map(&p.tb, xq, 1, K / 2, R, 0, kGgBoxN) ||
+        !encode_map(&p.tb_all, xq, 1, K / 2, R, 0, 128))
         return MOE_ERR_UNSUPPORTED;
     if (K % 256 == 0 && (!encode_map(&p.tsa, wbs, 1, K / 16, N, E, 128, 64) ||
                          !encode_map(&p.tsb, xbs, 1, K / 16, R, 0, kGgBoxN, 64)))
