@@ -24,7 +24,8 @@ namespace moe {
 
 enum { kGgFwd = 0, kGgDx = 1, kGgDw = 2 };
 
-constexpr int kGgThreads = 192;      // warps 0-3 epilogue, warp 4 TMA producer, warp 5 MMA issuer
+constexpr int kGgThreads = 192;      // warps 0-3 epilogue, warp 4 TMA producer, warp 5 MMA issuer ...
+constexpr int kGgThreadsDw = 224;    // ... and for dw warp 6, which clears rows behind a segment
 constexpr int kGgMaxStages = 12;
 constexpr int kGgBoxN = 32;          // rows per TMA box of a K-major B operand
 constexpr int kGgTile = 128 * 128;   // bytes of one 128 x 64 bf16 operand tile
@@ -58,6 +59,7 @@ struct GgCfg {
 
 struct GgShared {
     uint64_t full[kGgMaxStages];    // leader: a stage's tiles landed (in both CTAs)
+    uint64_t clear[kGgMaxStages];   // dw, leader: a stage's rows behind its segment are zero
     uint64_t empty[kGgMaxStages];   // the MMAs have read a stage
     uint64_t acc_full[2];           // an accumulator's MMAs are complete
     uint64_t acc_empty[2];          // leader: the epilogue warps (of both CTAs) have read an accumulator
@@ -416,8 +418,13 @@ __device__ __forceinline__ void gg_epilogue(uint32_t taddr, void* out, int out_f
 // tiles.  Three roles run through the same tile sequence, each at its own
 // pace: the producer fills the ring, the MMA issuer accumulates tile d into
 // tensor-memory buffer d mod 2, four warps read the other buffer out.
+template <int MODE>
+constexpr int gg_threads() {
+    return MODE == kGgDw ? kGgThreadsDw : kGgThreads;
+}
+
 template <int MODE, int CG>
-__global__ void __launch_bounds__(kGgThreads, 1) gg_kernel(const __grid_constant__ GgParams p) {
+__global__ void __launch_bounds__(gg_threads<MODE>(), 1) gg_kernel(const __grid_constant__ GgParams p) {
     using Cfg = GgCfg<MODE, CG>;
     extern __shared__ __align__(1024) unsigned char gg_smem_raw[];
     unsigned char* base = reinterpret_cast<unsigned char*>(
@@ -432,6 +439,7 @@ __global__ void __launch_bounds__(kGgThreads, 1) gg_kernel(const __grid_constant
     if (threadIdx.x == 0) {
         for (int s = 0; s < kGgMaxStages; ++s) {
             mbar_init(&sh->full[s], 1);
+            mbar_init(&sh->clear[s], 1);
             mbar_init(&sh->empty[s], 1);
         }
         for (int a = 0; a < 2; ++a) {
@@ -559,26 +567,10 @@ __global__ void __launch_bounds__(kGgThreads, 1) gg_kernel(const __grid_constant
                 const uint32_t sta = ring_at + r.s * stage_bytes;
                 int steps = 4;  // MMAs (16 deep) of a 64-wide step
                 if (MODE == kGgDw) {
-                    // the segment's end: rows behind it belong to the next
-                    // segment (or to no one), so both operands' rows up to the
-                    // last MMA's end are zeroed -- zeroing one would leave
-                    // 0 x infinity or 0 x NaN
                     const int valid = sh->cnt[e] - k0 * 64;
                     if (valid < 64) {
                         steps = (valid + 15) / 16;
-                        unsigned char* st = ring + (size_t)r.s * stage_bytes;
-                        for (int i = lane; i < (steps * 16 - valid) * 32; i += 32) {
-                            const int blk = i & 3, ch = (i >> 2) & 7, row = valid + (i >> 5);
-                            unsigned char* at = st + (blk >> 1) * b_off + (blk & 1) * 8192 + row * 128 + ch * 16;
-                            *reinterpret_cast<uint4*>(at) = make_uint4(0, 0, 0, 0);
-                            if (CG == 2)
-                                asm volatile("st.shared::cluster.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(cluster_addr(at, 1)),
-                                             "r"(0)
-                                             : "memory");
-                        }
-                        if (CG == 2) asm volatile("fence.acq_rel.cluster;" ::: "memory");
-                        asm volatile("fence.proxy.async;" ::: "memory");
-                        __syncwarp();
+                        if (!gg_wait(&sh->clear[r.s], r.ph, &sh->abort)) return false;
                     }
                 }
                 tc_fence_after();
@@ -614,6 +606,38 @@ __global__ void __launch_bounds__(kGgThreads, 1) gg_kernel(const __grid_constant
             gg_commit_own<CG>(&sh->mma_done);
             gg_settle(&sh->mma_done, 0u);
         }
+        __syncwarp();
+    } else if (warp == 6) {
+        // ---------------- dw: the segment's end.  Rows behind it belong to
+        // the next segment (or to no one), so both operands' rows up to the
+        // last MMA's end are zeroed -- zeroing one would leave 0 x infinity or
+        // 0 x NaN.  A warp of its own does it as soon as the rows landed: in
+        // the MMA warp the fences held up every tile's end.
+        GgRing r;
+        if (rank == 0) walk([&](int e, int q0, int n, int n0, int m0, int nk) -> bool {
+            for (int k = 0; k < nk; ++k) {
+                if (!gg_wait(&sh->full[r.s], r.ph, &sh->abort)) return false;
+                const int valid = sh->cnt[e] - k * 64;
+                if (valid < 64 && (valid & 15)) {
+                    unsigned char* st = ring + (size_t)r.s * stage_bytes;
+                    for (int i = lane; i < (16 - (valid & 15)) * 32; i += 32) {
+                        const int blk = i & 3, ch = (i >> 2) & 7, row = valid + (i >> 5);
+                        unsigned char* at = st + (blk >> 1) * b_off + (blk & 1) * 8192 + row * 128 + ch * 16;
+                        *reinterpret_cast<uint4*>(at) = make_uint4(0, 0, 0, 0);
+                        if (CG == 2)
+                            asm volatile("st.shared::cluster.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(cluster_addr(at, 1)),
+                                         "r"(0)
+                                         : "memory");
+                    }
+                    if (CG == 2) asm volatile("fence.acq_rel.cluster;" ::: "memory");
+                    asm volatile("fence.proxy.async;" ::: "memory");
+                }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&sh->clear[r.s]);
+                r.next(S);
+            }
+            return true;
+        });
         __syncwarp();
     } else {
         int d = 0;

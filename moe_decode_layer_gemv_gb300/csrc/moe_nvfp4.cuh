@@ -175,39 +175,97 @@ __global__ void __launch_bounds__(128) nv4_rows_kernel(const void* __restrict__ 
     if (live && t == 0) gs[row] = scale;
 }
 
-// One scale a matrix: its maximum first (as bits, in the workspace), then the codes.
+// One scale a matrix.  The matrices are cut into chunks of 64 KB, numbered
+// through; step t reads chunk t for its matrix's maximum and writes the codes
+// of chunk t - lag, whose matrix is complete by then and which is still in L2
+// (lag: a matrix, and the steps in flight): x comes from HBM once.  Steps are
+// claimed in order, so that the chunks a step waits for belong to steps
+// claimed before it, whose maxima wait for nothing.
+// Workspace: claimed steps, then per matrix its maximum (as bits) and its
+// chunks done.
+constexpr int kNv4CtasPerSm = 4;
 template <bool BF16>
-__global__ void __launch_bounds__(256) nv4_amax_kernel(const void* __restrict__ x, size_t per, unsigned* amax,
-                                                       int32_t* status) {
-    grid_dep_wait();
-    const size_t g = blockIdx.y;
-    float m = 0.0f;
-    bool any_bad = false;
-    for (size_t b = (size_t)blockIdx.x * blockDim.x + threadIdx.x; b < per; b += (size_t)gridDim.x * blockDim.x) {
-        Nv4Block<BF16> blk;
-        bool bad;
-        blk.load(x, g * per + b);
-        m = fmaxf(m, blk.amax(bad));
-        any_bad |= bad;
-    }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-    if ((threadIdx.x & 31) == 0) atomicMax(amax + g, __float_as_uint(m));
-    if (any_bad) set_status(status, MOE_DEV_NONFINITE);
+__host__ __device__ constexpr int nv4_bpt() {  // blocks a thread
+    return BF16 ? 8 : 4;
 }
+template <bool BF16>
+__host__ __device__ constexpr int nv4_chunk() {
+    return 256 * nv4_bpt<BF16>();
+}
+static inline size_t nv4_workspace(int G) { return sizeof(unsigned) * (2 + 2 * (size_t)G); }
 
 template <bool BF16>
-__global__ void __launch_bounds__(256) nv4_encode_kernel(const void* __restrict__ x, size_t per, const unsigned* amax,
-                                                         uint8_t* q, uint8_t* bs, float* gs) {
+__global__ void __launch_bounds__(256, kNv4CtasPerSm) nv4_matrices_kernel(const void* __restrict__ x, size_t per,
+                                                                          unsigned cpm, unsigned chunks, uint8_t* q,
+                                                                          uint8_t* bs, float* gs, unsigned* ws,
+                                                                          int32_t* status) {
+    constexpr int BPT = nv4_bpt<BF16>();
+    __shared__ unsigned s_step, s_max[8], s_bits;
+    unsigned *amax = ws + 2, *done = amax + chunks / cpm;
     grid_dep_wait();
-    const size_t g = blockIdx.y;
-    const float scale = nv4_scale(__uint_as_float(__ldcg(amax + g)));
-    for (size_t b = (size_t)blockIdx.x * blockDim.x + threadIdx.x; b < per; b += (size_t)gridDim.x * blockDim.x) {
-        Nv4Block<BF16> blk;
-        blk.load(x, g * per + b);
-        blk.encode(scale, q, bs, g * per + b);
+    const unsigned lag = cpm + gridDim.x;
+    for (;;) {
+        __syncthreads();
+        if (threadIdx.x == 0) s_step = atomicAdd(ws, 1u);
+        __syncthreads();
+        const unsigned t = s_step;
+        if (t >= chunks + lag) return;
+        if (t < chunks) {
+            const unsigned g = t / cpm, c = t - g * cpm;
+            float m = 0.0f;
+            bool any_bad = false;
+            Nv4Block<BF16> blk[BPT];
+#pragma unroll
+            for (int j = 0; j < BPT; ++j) {
+                const size_t b = (size_t)c * nv4_chunk<BF16>() + j * 256 + threadIdx.x;
+                if (b < per)
+                    blk[j].load(x, g * per + b);
+                else
+                    blk[j].clear();
+            }
+#pragma unroll
+            for (int j = 0; j < BPT; ++j) {
+                bool bad;
+                m = fmaxf(m, blk[j].amax(bad));
+                any_bad |= bad;
+            }
+            const unsigned w = __reduce_max_sync(0xffffffffu, __float_as_uint(m));  // magnitudes order like their bits
+            if ((threadIdx.x & 31) == 0) s_max[threadIdx.x >> 5] = w;
+            if (any_bad) set_status(status, MOE_DEV_NONFINITE);
+            __syncthreads();
+            if (threadIdx.x == 0) {
+                unsigned v = s_max[0];
+#pragma unroll
+                for (int i = 1; i < 8; ++i) v = max(v, s_max[i]);
+                atomicMax(amax + g, v);
+                __threadfence();
+                red_release_gpu_add(done + g, 1u);
+            }
+        }
+        if (t >= lag) {
+            const unsigned g = (t - lag) / cpm, c = (t - lag) - g * cpm;
+            Nv4Block<BF16> blk[BPT];
+#pragma unroll
+            for (int j = 0; j < BPT; ++j) {
+                const size_t b = (size_t)c * nv4_chunk<BF16>() + j * 256 + threadIdx.x;
+                if (b < per) blk[j].load(x, g * per + b);
+            }
+            if (threadIdx.x == 0) {
+                unsigned i = 0;
+                while (ld_acquire_gpu(done + g) < cpm && ++i < (1u << 22)) __nanosleep(64);
+                if (i >= (1u << 22)) set_status(status, MOE_DEV_TIMEOUT);
+                s_bits = __ldcg(amax + g);
+            }
+            __syncthreads();
+            const float scale = nv4_scale(__uint_as_float(s_bits));
+#pragma unroll
+            for (int j = 0; j < BPT; ++j) {
+                const size_t b = (size_t)c * nv4_chunk<BF16>() + j * 256 + threadIdx.x;
+                if (b < per) blk[j].encode(scale, q, bs, g * per + b);
+            }
+            if (c == 0 && threadIdx.x == 0) gs[g] = scale;
+        }
     }
-    if (blockIdx.x == 0 && threadIdx.x == 0) gs[g] = scale;
 }
 
 // Values e2m1(q) * e4m3(bs) * gs: a thread per block (the first two factors'

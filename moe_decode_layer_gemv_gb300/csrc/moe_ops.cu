@@ -83,8 +83,8 @@ static int run_gg(GgParams& p, const void* a, const void* b, int R, int N, int K
     const int sms = sm_count();
     if (sms < 2) return MOE_ERR_CUDA;
     const bool pair = (int64_t)R >= (int64_t)kGgPairRows * E;
-    return pair ? launch_persistent<2>(gg_kernel<MODE, 2>, p, kGgThreads, sms, st)
-                : launch_persistent<1>(gg_kernel<MODE, 1>, p, kGgThreads, sms, st);
+    return pair ? launch_persistent<2>(gg_kernel<MODE, 2>, p, gg_threads<MODE>(), sms, st)
+                : launch_persistent<1>(gg_kernel<MODE, 1>, p, gg_threads<MODE>(), sms, st);
 }
 
 template <bool BF16, int T>
@@ -98,25 +98,28 @@ static int launch_rows(const void* x, int G, int nb, uint8_t* q, uint8_t* bs, fl
 }
 
 template <bool BF16>
-static int run_quantize(const void* x, int G, int rows, int cols, uint8_t* q, uint8_t* bs, float* gs, unsigned* amax,
+static int run_quantize(const void* x, int G, int rows, int cols, uint8_t* q, uint8_t* bs, float* gs, unsigned* ws,
                         int32_t* status, cudaStream_t st) {
     const int nb = cols / 16;
     if (rows == 1)
         return nb <= 32 ? launch_rows<BF16, 32>(x, G, nb, q, bs, gs, status, st)
                         : launch_rows<BF16, 128>(x, G, nb, q, bs, gs, status, st);
     const size_t per = (size_t)rows * nb;
-    int rc = to_status(cudaMemsetAsync(amax, 0, sizeof(unsigned) * (size_t)G, st));
+    const unsigned cpm = (unsigned)((per + nv4_chunk<BF16>() - 1) / nv4_chunk<BF16>());
+    const int sms = sm_count();
+    if (sms < 1) return MOE_ERR_CUDA;
+    const unsigned chunks = cpm * (unsigned)G;
+    unsigned grid = (unsigned)sms * kNv4CtasPerSm;
+    if (grid > chunks) grid = chunks;
+    int rc = to_status(cudaMemsetAsync(ws, 0, nv4_workspace(G), st));
     if (rc) return rc;
-    size_t bx = (per + 255) / 256;
-    if (bx > 64) bx = 64;
-    const dim3 grid((unsigned)bx, (unsigned)G);
-    if ((rc = launch_pdl(nv4_amax_kernel<BF16>, grid, 256, 0, st, x, per, amax, status))) return rc;
-    return launch_pdl(nv4_encode_kernel<BF16>, grid, 256, 0, st, x, per, (const unsigned*)amax, q, bs, gs);
+    return launch_pdl(nv4_matrices_kernel<BF16>, grid, 256, 0, st, x, per, cpm, chunks, q, bs, gs, ws, status);
 }
 
 static int check_nvfp4(int G, int rows, int cols, int dtype) {
     if (G < 0 || rows < 1 || cols < 32 || cols > MOE_MAX_DIM || (cols & 31)) return MOE_ERR_INVALID_ARG;
-    if (rows == 1 ? G > MOE_MAX_ROWS : G > 65535 || rows > 2 * MOE_MAX_DIM) return MOE_ERR_INVALID_ARG;
+    if (rows == 1 ? G > MOE_MAX_ROWS : (G > 65535 || rows > 2 * MOE_MAX_DIM)) return MOE_ERR_INVALID_ARG;
+    if (rows > 1 && (int64_t)G * rows * (cols / 16) > MOE_MAX_BLOCKS) return MOE_ERR_INVALID_ARG;
     if (dtype != MOE_DT_F32 && dtype != MOE_DT_BF16) return MOE_ERR_INVALID_ARG;
     return MOE_OK;
 }
@@ -199,7 +202,7 @@ int moe_quantize_nvfp4_workspace_bytes(int G, int rows, int cols, size_t* bytes)
     const int rc = check_nvfp4(G, rows, cols, MOE_DT_F32);
     if (rc) return rc;
     if (!bytes) return MOE_ERR_INVALID_ARG;
-    *bytes = rows == 1 ? 0 : align_up(sizeof(unsigned) * (size_t)G, 256);
+    *bytes = rows == 1 ? 0 : align_up(nv4_workspace(G), 256);
     return MOE_OK;
 }
 
@@ -221,9 +224,9 @@ int moe_quantize_nvfp4(const void* x, int x_dtype, int G, int rows, int cols, ui
         MOE_REQ(workspace);
     }
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    unsigned* amax = static_cast<unsigned*>(workspace);
-    return x_dtype == MOE_DT_BF16 ? run_quantize<true>(x, G, rows, cols, q, bs, gs, amax, dev_status, st)
-                                  : run_quantize<false>(x, G, rows, cols, q, bs, gs, amax, dev_status, st);
+    unsigned* ws = static_cast<unsigned*>(workspace);
+    return x_dtype == MOE_DT_BF16 ? run_quantize<true>(x, G, rows, cols, q, bs, gs, ws, dev_status, st)
+                                  : run_quantize<false>(x, G, rows, cols, q, bs, gs, ws, dev_status, st);
 }
 
 int moe_dequantize_nvfp4(const uint8_t* q, const uint8_t* bs, const float* gs, int G, int rows, int cols, void* x,
