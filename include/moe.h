@@ -81,7 +81,7 @@ typedef enum { MOE_DT_F32 = 0, MOE_DT_BF16 = 1 } moe_dtype;
 #define MOE_MAX_DIM 16384
 #define MOE_MAX_LAYERS 64
 #define MOE_MAX_ROWS (1 << 22)      /* rows of the grouped products, and of rows quantised each by itself */
-#define MOE_MAX_BLOCKS (1LL << 36)  /* 16-element blocks of the matrices quantised in one call */
+#define MOE_MAX_BLOCKS (1LL << 32)  /* 16-element blocks of the matrices quantised in one call */
 
 /* flags for moe_expert_forward / moe_layer_forward / moe_stack_forward */
 #define MOE_F_NO_DEDUP 1u   /* evaluate every route on its own (each route re-reads

@@ -27,6 +27,23 @@ __device__ __forceinline__ float nv4_scale(float amax) {
     return fmaxf(__uint_as_float(min(up, kNv4MaxScaleBits)), kNv4MinScale);
 }
 
+// A reciprocal to about one step (the quotients made with it are corrected
+// by their remainders; s is normal and so is 1 / s).
+__device__ __forceinline__ float nv4_rcp(float s) {
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(s));
+    return r;
+}
+
+struct Nv4Scale {
+    float gs, six, inv6;  // 6 gs and its reciprocal
+    __device__ __forceinline__ explicit Nv4Scale(float amax) {
+        gs = nv4_scale(amax);
+        six = 6.0f * gs;
+        inv6 = nv4_rcp(six);
+    }
+};
+
 // 32 bytes of global memory in one load or store (both 32-byte aligned).
 struct alignas(32) Words8 {
     uint32_t w[8];
@@ -106,24 +123,37 @@ struct Nv4Block {
         const Words8& v = w[BF16 ? 0 : i >> 2];
         return make_float2(__uint_as_float(v.w[(2 * i) & 7]), __uint_as_float(v.w[(2 * i + 1) & 7]));
     }
-    // codes (8 bytes) and block scale (1 byte) under the group's scale; a
-    // block with an element that is not finite decodes to NaN throughout
-    __device__ __forceinline__ void encode(float gs, uint8_t* q, uint8_t* bs, size_t block) const {
-        bool bad;
-        const float m = amax(bad);
-        const uint32_t b = __nv_cvt_float_to_fp8(__fdiv_rn(m, 6.0f * gs), __NV_SATFINITE, __NV_E4M3);
-        const float s = f8_to_f(b) * gs;
-        const float inv = s > 0.0f && !bad ? __frcp_rn(s) : 0.0f;
-        uint32_t out[2] = {0, 0};
+    // codes (8 bytes) and block scale (1 byte) under the group's scale, for a
+    // block whose finite maximum is m; a block with an element that is not
+    // finite (bad) decodes to NaN throughout
+    __device__ __forceinline__ void encode(float m, bool bad, const Nv4Scale& g, uint8_t* q, uint8_t* bs,
+                                           size_t block) const {
+        const float q0 = m * g.inv6;
+        const uint32_t b =
+            __nv_cvt_float_to_fp8(fmaf(fmaf(q0, g.six, -m), -g.inv6, q0), __NV_SATFINITE, __NV_E4M3);
+        const float s = f8_to_f(b) * g.gs;
+        const float inv = s > 0.0f && !bad ? nv4_rcp(s) : 0.0f;
+        const float2 s2 = make_float2(s, s), inv2 = make_float2(inv, inv), ninv2 = make_float2(-inv, -inv);
+        uint32_t out[2];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            // x / s to nearest: the product with the reciprocal, corrected once
-            // by its exact remainder t s - x (written this way round a zero keeps its sign)
-            const float2 x = pair(i);
-            const float2 t = make_float2(x.x * inv, x.y * inv);
-            const float2 v = make_float2(fmaf(fmaf(t.x, s, -x.x), -inv, t.x), fmaf(fmaf(t.y, s, -x.y), -inv, t.y));
-            const uint32_t c = __nv_cvt_float2_to_fp4x2(v, __NV_E2M1, cudaRoundNearest);
-            out[i >> 2] |= c << (8 * (i & 3));
+        for (int h = 0; h < 2; ++h) {
+            float2 v[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                // x / s to nearest: the product with the reciprocal, corrected
+                // once by its exact remainder t s - x (written this way round a
+                // zero keeps its sign)
+                const float2 x = pair(4 * h + i), t = __fmul2_rn(x, inv2);
+                v[i] = __ffma2_rn(__ffma2_rn(t, s2, make_float2(-x.x, -x.y)), ninv2, t);
+            }
+            asm("{\n\t.reg .b8 a, b, c, d;\n\t"
+                "cvt.rn.satfinite.e2m1x2.f32 a, %2, %1;\n\t"
+                "cvt.rn.satfinite.e2m1x2.f32 b, %4, %3;\n\t"
+                "cvt.rn.satfinite.e2m1x2.f32 c, %6, %5;\n\t"
+                "cvt.rn.satfinite.e2m1x2.f32 d, %8, %7;\n\t"
+                "mov.b32 %0, {a, b, c, d};\n\t}"
+                : "=r"(out[h])
+                : "f"(v[0].x), "f"(v[0].y), "f"(v[1].x), "f"(v[1].y), "f"(v[2].x), "f"(v[2].y), "f"(v[3].x), "f"(v[3].y));
         }
         if (bad) out[0] = out[1] = 0;
         *reinterpret_cast<uint2*>(q + block * 8) = make_uint2(out[0], out[1]);
@@ -142,8 +172,8 @@ __global__ void __launch_bounds__(128) nv4_rows_kernel(const void* __restrict__ 
     const size_t row = (size_t)blockIdx.x * (128 / T) + sub;
     const bool live = row < (size_t)G;
     Nv4Block<BF16> blk[BPT];
-    float m = 0.0f;
-    bool any_bad = false;
+    float m = 0.0f, mine[BPT];
+    bool any_bad = false, bad[BPT];
 #pragma unroll
     for (int j = 0; j < BPT; ++j) {
         const int b = j * T + t;
@@ -154,45 +184,56 @@ __global__ void __launch_bounds__(128) nv4_rows_kernel(const void* __restrict__ 
     }
 #pragma unroll
     for (int j = 0; j < BPT; ++j) {
-        bool bad;
-        m = fmaxf(m, blk[j].amax(bad));
-        any_bad |= bad;
+        mine[j] = blk[j].amax(bad[j]);
+        m = fmaxf(m, mine[j]);
+        any_bad |= bad[j];
     }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    m = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(m)));  // magnitudes order like their bits
     if (T > 32) {
         if ((threadIdx.x & 31) == 0) s_max[threadIdx.x >> 5] = m;
         __syncthreads();
         m = fmaxf(fmaxf(s_max[0], s_max[1]), fmaxf(s_max[2], s_max[3]));
     }
-    const float scale = nv4_scale(m);
+    const Nv4Scale scale(m);
     if (any_bad) set_status(status, MOE_DEV_NONFINITE);
 #pragma unroll
     for (int j = 0; j < BPT; ++j) {
         const int b = j * T + t;
-        if (live && b < nb) blk[j].encode(scale, q, bs, row * nb + b);
+        if (live && b < nb) blk[j].encode(mine[j], bad[j], scale, q, bs, row * nb + b);
     }
-    if (live && t == 0) gs[row] = scale;
+    if (live && t == 0) gs[row] = scale.gs;
 }
 
-// One scale a matrix.  The matrices are cut into chunks of 64 KB, numbered
-// through; step t reads chunk t for its matrix's maximum and writes the codes
-// of chunk t - lag, whose matrix is complete by then and which is still in L2
-// (lag: a matrix, and the steps in flight): x comes from HBM once.  Steps are
-// claimed in order, so that the chunks a step waits for belong to steps
-// claimed before it, whose maxima wait for nothing.
-// Workspace: claimed steps, then per matrix its maximum (as bits) and its
-// chunks done.
+// One scale a matrix.  The matrices are cut into chunks of 32 KB, numbered
+// through; step t reads chunk t for its maximum and writes the codes of chunk
+// t - lag, whose matrix's maxima are all known by then and which is still in
+// L2 (lag: a matrix, and the steps in flight): x comes from HBM once.  Steps
+// are claimed in order, so that the chunks a step waits for belong to steps
+// claimed before it, whose maxima wait for nothing.  Workspace (zeroed):
+// claimed steps, then per chunk its maximum's bits with the sign bit set --
+// the word is its own flag, no fence orders it.
 constexpr int kNv4CtasPerSm = 4;
 template <bool BF16>
 __host__ __device__ constexpr int nv4_bpt() {  // blocks a thread
-    return BF16 ? 8 : 4;
+    return BF16 ? 4 : 2;
 }
 template <bool BF16>
 __host__ __device__ constexpr int nv4_chunk() {
     return 256 * nv4_bpt<BF16>();
 }
-static inline size_t nv4_workspace(int G) { return sizeof(unsigned) * (2 + 2 * (size_t)G); }
+// words of workspace for G matrices of `per` blocks, whatever x's type
+static inline size_t nv4_workspace(int G, size_t per) {
+    return sizeof(unsigned) * (4 + (size_t)G * ((per + nv4_chunk<false>() - 1) / nv4_chunk<false>()));
+}
+
+__device__ __forceinline__ unsigned ld_relaxed_gpu(const unsigned* p) {
+    unsigned v;
+    asm volatile("ld.relaxed.gpu.global.u32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
+    return v;
+}
+__device__ __forceinline__ void st_relaxed_gpu(unsigned* p, unsigned v) {
+    asm volatile("st.relaxed.gpu.global.u32 [%0], %1;" ::"l"(p), "r"(v) : "memory");
+}
 
 template <bool BF16>
 __global__ void __launch_bounds__(256, kNv4CtasPerSm) nv4_matrices_kernel(const void* __restrict__ x, size_t per,
@@ -200,26 +241,28 @@ __global__ void __launch_bounds__(256, kNv4CtasPerSm) nv4_matrices_kernel(const 
                                                                           uint8_t* bs, float* gs, unsigned* ws,
                                                                           int32_t* status) {
     constexpr int BPT = nv4_bpt<BF16>();
-    __shared__ unsigned s_step, s_max[8], s_bits;
-    unsigned *amax = ws + 2, *done = amax + chunks / cpm;
+    constexpr unsigned kFlag = 0x80000000u;
+    __shared__ unsigned s_step, s_max[8], s_all[8];
+    unsigned* amax = ws + 4;
     grid_dep_wait();
     const unsigned lag = cpm + gridDim.x;
+    if (threadIdx.x == 0) s_step = atomicAdd(ws, 1u);
     for (;;) {
-        __syncthreads();
-        if (threadIdx.x == 0) s_step = atomicAdd(ws, 1u);
         __syncthreads();
         const unsigned t = s_step;
         if (t >= chunks + lag) return;
+        unsigned next = 0;
+        if (threadIdx.x == 0) next = atomicAdd(ws, 1u);  // on its way while this step runs
+        Nv4Block<BF16> blk[BPT];
         if (t < chunks) {
             const unsigned g = t / cpm, c = t - g * cpm;
+            const size_t b0 = (size_t)c * nv4_chunk<BF16>() + threadIdx.x;
             float m = 0.0f;
             bool any_bad = false;
-            Nv4Block<BF16> blk[BPT];
 #pragma unroll
             for (int j = 0; j < BPT; ++j) {
-                const size_t b = (size_t)c * nv4_chunk<BF16>() + j * 256 + threadIdx.x;
-                if (b < per)
-                    blk[j].load(x, g * per + b);
+                if (b0 + j * 256 < per)
+                    blk[j].load(x, g * per + b0 + j * 256);
                 else
                     blk[j].clear();
             }
@@ -232,39 +275,49 @@ __global__ void __launch_bounds__(256, kNv4CtasPerSm) nv4_matrices_kernel(const 
             const unsigned w = __reduce_max_sync(0xffffffffu, __float_as_uint(m));  // magnitudes order like their bits
             if ((threadIdx.x & 31) == 0) s_max[threadIdx.x >> 5] = w;
             if (any_bad) set_status(status, MOE_DEV_NONFINITE);
-            __syncthreads();
-            if (threadIdx.x == 0) {
-                unsigned v = s_max[0];
+        }
+        __syncthreads();
+        if (t < chunks && threadIdx.x == 0) {
+            unsigned v = s_max[0];
 #pragma unroll
-                for (int i = 1; i < 8; ++i) v = max(v, s_max[i]);
-                atomicMax(amax + g, v);
-                __threadfence();
-                red_release_gpu_add(done + g, 1u);
-            }
+            for (int i = 1; i < 8; ++i) v = max(v, s_max[i]);
+            st_relaxed_gpu(amax + t, v | kFlag);
         }
         if (t >= lag) {
-            const unsigned g = (t - lag) / cpm, c = (t - lag) - g * cpm;
-            Nv4Block<BF16> blk[BPT];
+            const unsigned u = t - lag, g = u / cpm, c = u - g * cpm;
+            const size_t b0 = (size_t)c * nv4_chunk<BF16>() + threadIdx.x;
 #pragma unroll
             for (int j = 0; j < BPT; ++j) {
-                const size_t b = (size_t)c * nv4_chunk<BF16>() + j * 256 + threadIdx.x;
-                if (b < per) blk[j].load(x, g * per + b);
+                if (b0 + j * 256 < per)
+                    blk[j].load(x, g * per + b0 + j * 256);
+                else
+                    blk[j].clear();
             }
-            if (threadIdx.x == 0) {
-                unsigned i = 0;
-                while (ld_acquire_gpu(done + g) < cpm && ++i < (1u << 22)) __nanosleep(64);
-                if (i >= (1u << 22)) set_status(status, MOE_DEV_TIMEOUT);
-                s_bits = __ldcg(amax + g);
+            unsigned top = 0;
+            for (unsigned i = threadIdx.x; i < cpm; i += 256) {
+                unsigned v = ld_relaxed_gpu(amax + (size_t)g * cpm + i);
+                for (unsigned n = 0; !(v & kFlag) && n < (1u << 22); ++n) {
+                    __nanosleep(64);
+                    v = ld_relaxed_gpu(amax + (size_t)g * cpm + i);
+                }
+                if (!(v & kFlag)) set_status(status, MOE_DEV_TIMEOUT);
+                top = max(top, v & ~kFlag);
             }
+            top = __reduce_max_sync(0xffffffffu, top);
+            if ((threadIdx.x & 31) == 0) s_all[threadIdx.x >> 5] = top;
             __syncthreads();
-            const float scale = nv4_scale(__uint_as_float(s_bits));
+#pragma unroll
+            for (int i = 0; i < 8; ++i) top = max(top, s_all[i]);
+            const Nv4Scale scale(__uint_as_float(top));
 #pragma unroll
             for (int j = 0; j < BPT; ++j) {
-                const size_t b = (size_t)c * nv4_chunk<BF16>() + j * 256 + threadIdx.x;
-                if (b < per) blk[j].encode(scale, q, bs, g * per + b);
+                bool bad;
+                const float m = blk[j].amax(bad);
+                if (b0 + j * 256 < per) blk[j].encode(m, bad, scale, q, bs, g * per + b0 + j * 256);
             }
-            if (c == 0 && threadIdx.x == 0) gs[g] = scale;
+            if (c == 0 && threadIdx.x == 0) gs[g] = scale.gs;
         }
+        if (threadIdx.x == 0) s_step = next;
     }
 }
 

@@ -111,7 +111,7 @@ static int run_quantize(const void* x, int G, int rows, int cols, uint8_t* q, ui
     const unsigned chunks = cpm * (unsigned)G;
     unsigned grid = (unsigned)sms * kNv4CtasPerSm;
     if (grid > chunks) grid = chunks;
-    int rc = to_status(cudaMemsetAsync(ws, 0, nv4_workspace(G), st));
+    int rc = to_status(cudaMemsetAsync(ws, 0, sizeof(unsigned) * (4 + (size_t)chunks), st));
     if (rc) return rc;
     return launch_pdl(nv4_matrices_kernel<BF16>, grid, 256, 0, st, x, per, cpm, chunks, q, bs, gs, ws, status);
 }
@@ -202,7 +202,7 @@ int moe_quantize_nvfp4_workspace_bytes(int G, int rows, int cols, size_t* bytes)
     const int rc = check_nvfp4(G, rows, cols, MOE_DT_F32);
     if (rc) return rc;
     if (!bytes) return MOE_ERR_INVALID_ARG;
-    *bytes = rows == 1 ? 0 : align_up(nv4_workspace(G), 256);
+    *bytes = rows == 1 ? 0 : align_up(nv4_workspace(G, (size_t)rows * (cols / 16)), 256);
     return MOE_OK;
 }
 
