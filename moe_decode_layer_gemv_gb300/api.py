@@ -630,13 +630,14 @@ def _dims(t, name, what, *dims):
 def _on(dev, stream, call):
     """call(stream handle) with dev current and torch's allocations made for
     the stream that the kernels go to."""
-    if stream is not None and stream.device != dev:
+    if stream is None and torch._C._cuda_getDevice() == dev.index:
+        return call(torch._C._cuda_getCurrentRawStream(dev.index))
+    if stream is None:
+        stream = torch.cuda.current_stream(dev)
+    elif stream.device != dev:
         raise ValueError(f"stream is on {stream.device}, x on {dev}")
-    here = torch.cuda.current_stream(dev)
-    if (stream is None or stream == here) and torch.cuda.current_device() == dev.index:
-        return call(here.cuda_stream)
-    with torch.cuda.stream(here if stream is None else stream):
-        return call((here if stream is None else stream).cuda_stream)
+    with torch.cuda.stream(stream):
+        return call(stream.cuda_stream)
 
 
 def _out(out, shape, out_dtype, dev):

@@ -119,6 +119,15 @@ __device__ __forceinline__ void cluster_sync() {
     asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
+// One lane of a converged warp.  Through elect.sync the compiler knows that a
+// single thread issues what follows; behind lane == 0 each MMA's and copy's
+// operands cost it some 200 cycles more.
+__device__ __forceinline__ bool gg_elect() {
+    uint32_t p;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+    return p != 0;
+}
+
 // The address in CTA `rank` of the cluster of what is at p here.
 __device__ __forceinline__ uint32_t cluster_addr(const void* p, uint32_t rank) {
     uint32_t a;
@@ -506,7 +515,7 @@ __global__ void __launch_bounds__(gg_threads<MODE>(), 1) gg_kernel(const __grid_
         GgRing r;
         const uint32_t ring_at = smem_u32(ring);
         const uint32_t bars = CG == 1 ? smem_u32(sh->full) : cluster_addr(sh->full, 0);
-        if (lane == 0) {
+        if (gg_elect()) {
             walk([&](int e, int q0, int n, int n0, int m0, int nk) -> bool {
                 // rows of B that this CTA holds (forward, dx), in whole boxes
                 const int rows = MODE == kGgDw ? 128 : (n + kGgBoxN * CG - 1) / (kGgBoxN * CG) * kGgBoxN;
@@ -574,7 +583,7 @@ __global__ void __launch_bounds__(gg_threads<MODE>(), 1) gg_kernel(const __grid_
                     }
                 }
                 tc_fence_after();
-                if (lane == 0) {
+                if (gg_elect()) {
                     const int ke = min(Cfg::KSUB, nk - k0);
 #pragma unroll
                     for (int u = 0; u < Cfg::KSUB; ++u) {
@@ -596,7 +605,7 @@ __global__ void __launch_bounds__(gg_threads<MODE>(), 1) gg_kernel(const __grid_
                 __syncwarp();
                 r.next(S);
             }
-            if (lane == 0) gg_commit<CG>(&sh->acc_full[buf]);
+            if (gg_elect()) gg_commit<CG>(&sh->acc_full[buf]);
             __syncwarp();
             buf ^= 1;
             if (buf == 0) free_ph ^= 1u;

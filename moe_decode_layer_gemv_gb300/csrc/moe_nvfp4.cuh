@@ -528,7 +528,7 @@ __global__ void __launch_bounds__(kG4Threads, 1) g4_kernel(const __grid_constant
         GgRing r, c;
         const uint32_t ring_at = smem_u32(ring), sf_at = smem_u32(sfbuf);
         const uint32_t bars = CG == 1 ? smem_u32(sh->full) : cluster_addr(sh->full, 0);
-        if (lane == 0) {
+        if (gg_elect()) {
             walk([&](int e, int q0, int n, int m0) -> bool {
                 const int rows = share(n);
                 for (int k = 0; k < nk; ++k) {
@@ -574,7 +574,7 @@ __global__ void __launch_bounds__(kG4Threads, 1) g4_kernel(const __grid_constant
             for (int k = 0; k < nk; ++k) {
                 if (!gg_wait(&sh->full[r.s], r.ph, &sh->abort) || !gg_wait(&s4->sfull[r.s], r.ph, &sh->abort)) return false;
                 tc_fence_after();
-                if (lane == 0) {
+                if (gg_elect()) {
                     const uint32_t st = ring_at + r.s * stage_bytes;
                     const uint32_t sfa = tmem + kG4SfCol + r.s * (uint32_t)(Cfg::SFA + Cfg::SFB), sfb = sfa + Cfg::SFA;
                     const int left = p.K - k * 256;
@@ -591,7 +591,7 @@ __global__ void __launch_bounds__(kG4Threads, 1) g4_kernel(const __grid_constant
                 __syncwarp();
                 r.next(S);
             }
-            if (lane == 0) gg_commit<CG>(&sh->acc_full[buf]);
+            if (gg_elect()) gg_commit<CG>(&sh->acc_full[buf]);
             __syncwarp();
             if (++buf == Cfg::ACC) {
                 buf = 0;
