@@ -44,6 +44,7 @@ struct GgParams {
     int NW;    // dw: rows of a weight matrix
     void* out;
     int out_f32;
+    int a_blocked, b_blocked;  // MN-major operands: the map has a 64-column block dimension
     int32_t* status;
 };
 
@@ -59,7 +60,8 @@ struct GgCfg {
 
 struct GgShared {
     uint64_t full[kGgMaxStages];    // leader: a stage's tiles landed (in both CTAs)
-    uint64_t clear[kGgMaxStages];   // dw, leader: a stage's rows behind its segment are zero
+    uint64_t tfull[kGgMaxStages];   // dw: the stage that a segment ends in landed in this CTA ...
+    uint64_t clear[kGgMaxStages];   // ... leader: and its rows behind the segment are zero (in both CTAs)
     uint64_t empty[kGgMaxStages];   // the MMAs have read a stage
     uint64_t acc_full[2];           // an accumulator's MMAs are complete
     uint64_t acc_empty[2];          // leader: the epilogue warps (of both CTAs) have read an accumulator
@@ -107,6 +109,37 @@ __device__ __forceinline__ void gg_load3(uint32_t dst, const CUtensorMap* map, i
                 dst),
             "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(bar)
             : "memory");
+}
+
+template <int CG>
+__device__ __forceinline__ void gg_load4(uint32_t dst, const CUtensorMap* map, int c0, int c1, int c2, int c3,
+                                         uint32_t bar) {
+    if (CG == 1)
+        asm volatile(
+            "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(
+                dst),
+            "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(bar)
+            : "memory");
+    else
+        asm volatile(
+            "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2 [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(
+                dst),
+            "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(bar)
+            : "memory");
+}
+
+// 64 rows x 128 columns of an MN-major operand: two 64-column blocks, one
+// copy where the tensor's rows are whole blocks (the map then has a block
+// dimension), else a copy each.
+template <int CG>
+__device__ __forceinline__ void gg_load_mn(uint32_t dst, const CUtensorMap* map, bool blocked, int col, int row,
+                                           uint32_t bar) {
+    if (blocked) {
+        gg_load3<CG>(dst, map, 0, row, col >> 6, bar);
+    } else {
+        gg_load2<CG>(dst, map, col, row, bar);
+        gg_load2<CG>(dst + 8192, map, col + 64, row, bar);
+    }
 }
 
 __device__ __forceinline__ uint32_t cluster_rank() {
@@ -282,6 +315,9 @@ __device__ __forceinline__ void gg_drain(GgShared* sh, uint32_t S, const GgRing&
         for (int i = 0; i < 1000; ++i) __nanosleep(1000);
 }
 
+// Whether a 64-row step with `left` rows to the segment's end needs clearing.
+__device__ __forceinline__ bool gg_ragged(int left) { return left < 64 && (left & 15); }
+
 // ------------------------------------------------------------- segments
 // The segments into shared memory.  Offsets outside [0, R] or descending
 // leave their segment out (and set MOE_DEV_BAD_OFFSETS): nothing is read or
@@ -448,7 +484,8 @@ __global__ void __launch_bounds__(gg_threads<MODE>(), 1) gg_kernel(const __grid_
     if (threadIdx.x == 0) {
         for (int s = 0; s < kGgMaxStages; ++s) {
             mbar_init(&sh->full[s], 1);
-            mbar_init(&sh->clear[s], 1);
+            mbar_init(&sh->tfull[s], 1);
+            mbar_init(&sh->clear[s], CG);
             mbar_init(&sh->empty[s], 1);
         }
         for (int a = 0; a < 2; ++a) {
@@ -525,7 +562,17 @@ __global__ void __launch_bounds__(gg_threads<MODE>(), 1) gg_kernel(const __grid_
                     if (!gg_wait(&sh->empty[r.s], r.ph ^ 1u, &sh->abort)) return false;
                     const uint32_t st = ring_at + r.s * stage_bytes, bar = bars + r.s * 8u;
                     const int ke = min(Cfg::KSUB, nk - k0);
-                    if (rank == 0) mbar_arrive_expect_tx(&sh->full[r.s], (uint32_t)ke * bytes);
+                    // dw: the stage that a segment ends in, if not with a whole MMA, lands on
+                    // each CTA's own barrier and is cleared there before it counts as full
+                    const bool tail = MODE == kGgDw && gg_ragged(sh->cnt[e] - k0 * 64);
+                    const uint32_t tbar = smem_u32(&sh->tfull[r.s]);
+                    if (tail) mbar_arrive_expect_tx(&sh->tfull[r.s], kGgTile + (uint32_t)rows * 128u);
+                    if (rank == 0) {
+                        if (tail)
+                            mbar_arrive(&sh->full[r.s]);
+                        else
+                            mbar_arrive_expect_tx(&sh->full[r.s], (uint32_t)ke * bytes);
+                    }
 #pragma unroll
                     for (int u = 0; u < Cfg::KSUB; ++u) {
                         if (u >= ke) break;
@@ -534,15 +581,20 @@ __global__ void __launch_bounds__(gg_threads<MODE>(), 1) gg_kernel(const __grid_
                         if (MODE == kGgFwd) {
                             gg_load3<CG>(sa, &p.ta, c, am, e, bar);
                         } else if (MODE == kGgDx) {
-                            gg_load3<CG>(sa, &p.ta, am, c, e, bar);
-                            gg_load3<CG>(sa + 8192, &p.ta, am + 64, c, e, bar);
+                            if (p.a_blocked) {
+                                gg_load4<CG>(sa, &p.ta, 0, c, am >> 6, e, bar);
+                            } else {
+                                gg_load3<CG>(sa, &p.ta, am, c, e, bar);
+                                gg_load3<CG>(sa + 8192, &p.ta, am + 64, c, e, bar);
+                            }
+                        } else if (tail) {
+                            gg_load_mn<1>(sa, &p.ta, p.a_blocked, am, q0 + c, tbar);
+                            gg_load_mn<1>(sb, &p.tb, p.b_blocked, bn, q0 + c, tbar);
                         } else {
-                            gg_load2<CG>(sa, &p.ta, am, q0 + c, bar);
-                            gg_load2<CG>(sa + 8192, &p.ta, am + 64, q0 + c, bar);
+                            gg_load_mn<CG>(sa, &p.ta, p.a_blocked, am, q0 + c, bar);
+                            gg_load_mn<CG>(sb, &p.tb, p.b_blocked, bn, q0 + c, bar);
                         }
                         if (MODE == kGgDw) {
-                            gg_load2<CG>(sb, &p.tb, bn, q0 + c, bar);
-                            gg_load2<CG>(sb + 8192, &p.tb, bn + 64, q0 + c, bar);
                         } else if (rows == 128) {
                             gg_load2<CG>(sb, &p.tb_all, c, bn, bar);
                         } else {
@@ -561,6 +613,7 @@ __global__ void __launch_bounds__(gg_threads<MODE>(), 1) gg_kernel(const __grid_
         GgRing r;
         int buf = 0;
         uint32_t free_ph = 1;  // parity of acc_empty to wait for (at first: nothing)
+        uint32_t tails = 0;    // parity of each stage's next use as a segment's end
         const uint32_t ring_at = smem_u32(ring);
         if (rank == 0) walk([&](int e, int q0, int n, int n0, int m0, int nk) -> bool {
             if (nk == 0) return true;
@@ -577,9 +630,10 @@ __global__ void __launch_bounds__(gg_threads<MODE>(), 1) gg_kernel(const __grid_
                 int steps = 4;  // MMAs (16 deep) of a 64-wide step
                 if (MODE == kGgDw) {
                     const int valid = sh->cnt[e] - k0 * 64;
-                    if (valid < 64) {
-                        steps = (valid + 15) / 16;
-                        if (!gg_wait(&sh->clear[r.s], r.ph, &sh->abort)) return false;
+                    if (valid < 64) steps = (valid + 15) / 16;
+                    if (gg_ragged(valid)) {
+                        if (!gg_wait(&sh->clear[r.s], (tails >> r.s) & 1u, &sh->abort)) return false;
+                        tails ^= 1u << r.s;
                     }
                 }
                 tc_fence_after();
@@ -620,29 +674,33 @@ __global__ void __launch_bounds__(gg_threads<MODE>(), 1) gg_kernel(const __grid_
         // ---------------- dw: the segment's end.  Rows behind it belong to
         // the next segment (or to no one), so both operands' rows up to the
         // last MMA's end are zeroed -- zeroing one would leave 0 x infinity or
-        // 0 x NaN.  A warp of its own does it as soon as the rows landed: in
-        // the MMA warp the fences held up every tile's end.
+        // 0 x NaN.  A warp of its own does it in each CTA as soon as the rows
+        // landed: in the MMA warp, or in both CTAs from the leader, the fences
+        // held up every tile's end (40 of 280 us of the training batch).
         GgRing r;
-        if (rank == 0) walk([&](int e, int q0, int n, int n0, int m0, int nk) -> bool {
-            for (int k = 0; k < nk; ++k) {
-                if (!gg_wait(&sh->full[r.s], r.ph, &sh->abort)) return false;
-                const int valid = sh->cnt[e] - k * 64;
-                if (valid < 64 && (valid & 15)) {
+        uint32_t tails = 0;
+        walk([&](int e, int q0, int n, int n0, int m0, int nk) -> bool {
+            const int left = sh->cnt[e] - (nk - 1) * 64;
+            for (int k = 0; k + 1 < nk; ++k) r.next(S);
+            if (nk > 0) {
+                if (gg_ragged(left)) {
+                    if (!gg_wait(&sh->tfull[r.s], (tails >> r.s) & 1u, &sh->abort)) return false;
+                    tails ^= 1u << r.s;
                     unsigned char* st = ring + (size_t)r.s * stage_bytes;
-                    for (int i = lane; i < (16 - (valid & 15)) * 32; i += 32) {
-                        const int blk = i & 3, ch = (i >> 2) & 7, row = valid + (i >> 5);
-                        unsigned char* at = st + (blk >> 1) * b_off + (blk & 1) * 8192 + row * 128 + ch * 16;
-                        *reinterpret_cast<uint4*>(at) = make_uint4(0, 0, 0, 0);
-                        if (CG == 2)
-                            asm volatile("st.shared::cluster.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(cluster_addr(at, 1)),
-                                         "r"(0)
-                                         : "memory");
+                    for (int i = lane; i < (16 - (left & 15)) * 32; i += 32) {
+                        const int blk = i & 3, ch = (i >> 2) & 7, row = left + (i >> 5);
+                        *reinterpret_cast<uint4*>(st + (blk >> 1) * b_off + (blk & 1) * 8192 + row * 128 + ch * 16) =
+                            make_uint4(0, 0, 0, 0);
                     }
-                    if (CG == 2) asm volatile("fence.acq_rel.cluster;" ::: "memory");
-                    asm volatile("fence.proxy.async;" ::: "memory");
+                    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                    __syncwarp();
+                    if (lane == 0) {
+                        if (CG == 1)
+                            mbar_arrive(&sh->clear[r.s]);
+                        else
+                            mbar_arrive_cluster(&sh->clear[r.s], 0);
+                    }
                 }
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&sh->clear[r.s]);
                 r.next(S);
             }
             return true;

@@ -399,7 +399,6 @@ struct G4Params {
 
 struct G4Shared {
     GgShared g;
-    uint64_t sfull[kG4MaxStages];  // leader: a stage's scales are in tensor memory (of both CTAs)
     alignas(16) float xg[kG4Epi][128];  // the epilogue warps' row scales
     uint64_t cfull[2], cempty[2];  // a copy of scales is in shared memory; the scale warps have read it
 };
@@ -474,9 +473,8 @@ __global__ void __launch_bounds__(kG4Threads, 1) g4_kernel(const __grid_constant
     const int unit = (int)blockIdx.x / CG, units = (int)gridDim.x / CG;
     if (threadIdx.x == 0) {
         for (int s = 0; s < kG4MaxStages; ++s) {
-            mbar_init(&sh->full[s], 1);
+            mbar_init(&sh->full[s], 1 + 4 * CG);  // the tiles, and the four scale warps (of both CTAs)
             mbar_init(&sh->empty[s], 1);
-            mbar_init(&s4->sfull[s], 4 * CG);
         }
         for (int a = 0; a < 2; ++a) {
             mbar_init(&sh->acc_full[a], 1);
@@ -572,7 +570,7 @@ __global__ void __launch_bounds__(kG4Threads, 1) g4_kernel(const __grid_constant
             const uint32_t tacc = tmem + (uint32_t)(buf * Cfg::BN);
             uint32_t acc = 0;
             for (int k = 0; k < nk; ++k) {
-                if (!gg_wait(&sh->full[r.s], r.ph, &sh->abort) || !gg_wait(&s4->sfull[r.s], r.ph, &sh->abort)) return false;
+                if (!gg_wait(&sh->full[r.s], r.ph, &sh->abort)) return false;
                 tc_fence_after();
                 if (gg_elect()) {
                     const uint32_t st = ring_at + r.s * stage_bytes;
@@ -663,9 +661,9 @@ __global__ void __launch_bounds__(kG4Threads, 1) g4_kernel(const __grid_constant
                 __syncwarp();
                 if (lane == 0) {
                     if (CG == 1)
-                        mbar_arrive(&s4->sfull[r.s]);
+                        mbar_arrive(&sh->full[r.s]);
                     else
-                        mbar_arrive_cluster(&s4->sfull[r.s], 0);
+                        mbar_arrive_cluster(&sh->full[r.s], 0);
                 }
                 r.next(S);
             }

@@ -30,6 +30,20 @@ static bool encode_map(CUtensorMap* map, const void* base, int elem, uint64_t in
               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// A map over bf16 [outer2, outer1, inner] (outer2 = 0: [outer1, inner]) whose
+// boxes are 64 rows x two 64-column blocks: inner % 64 == 0.
+static bool encode_blocked(CUtensorMap* map, const void* base, uint64_t inner, uint64_t outer1, uint64_t outer2) {
+    EncodeTiledFn fn = encode_fn();
+    if (!fn) return false;
+    const cuuint64_t dims[4] = {64, outer1, inner / 64, outer2};
+    const cuuint64_t strides[3] = {inner * 2, 128, inner * outer1 * 2};
+    const cuuint32_t box[4] = {64, 64, 2, 1};
+    const cuuint32_t estr[4] = {1, 1, 1, 1};
+    return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, outer2 ? 4 : 3, const_cast<void*>(base), dims, strides, box, estr,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 static int check_grouped(int R, int N, int K, int E, int dtype) {
     if (R < 0 || R > MOE_MAX_ROWS || E < 1 || E > MOE_MAX_E) return MOE_ERR_INVALID_ARG;
     if (N < 8 || N > 2 * MOE_MAX_DIM || (N & 7) || K < 8 || K > MOE_MAX_DIM || (K & 7)) return MOE_ERR_INVALID_ARG;
@@ -66,14 +80,18 @@ constexpr int kGgPairRows = 128;
 template <int MODE>
 static int run_gg(GgParams& p, const void* a, const void* b, int R, int N, int K, int E, cudaStream_t st) {
     bool ok;
+    p.a_blocked = K % 64 == 0;
+    p.b_blocked = N % 64 == 0;
     if (MODE == kGgFwd)
         ok = encode_map(&p.ta, a, 2, K, N, E, 128) && encode_map(&p.tb, b, 2, K, R, 0, kGgBoxN) &&
              encode_map(&p.tb_all, b, 2, K, R, 0, 128);
     else if (MODE == kGgDx)
-        ok = encode_map(&p.ta, a, 2, K, N, E, 64) && encode_map(&p.tb, b, 2, N, R, 0, kGgBoxN) &&
+        ok = (p.a_blocked ? encode_blocked(&p.ta, a, K, N, E) : encode_map(&p.ta, a, 2, K, N, E, 64)) &&
+             encode_map(&p.tb, b, 2, N, R, 0, kGgBoxN) &&
              encode_map(&p.tb_all, b, 2, N, R, 0, 128);
     else
-        ok = encode_map(&p.ta, a, 2, K, R, 0, 64) && encode_map(&p.tb, b, 2, N, R, 0, 64);
+        ok = (p.a_blocked ? encode_blocked(&p.ta, a, K, R, 0) : encode_map(&p.ta, a, 2, K, R, 0, 64)) &&
+             (p.b_blocked ? encode_blocked(&p.tb, b, N, R, 0) : encode_map(&p.tb, b, 2, N, R, 0, 64));
     if (!ok) return MOE_ERR_UNSUPPORTED;
     p.E = E;
     p.R = R;
