@@ -605,72 +605,67 @@ def stack_forward(x, layers, top_k, flags=0, stream=None, status=None):
 
 
 # ------------------------------------------------- grouped products and NVFP4
-# (checks and marshalling kept short: these calls serve single decoded tokens too)
+# (checks and marshalling kept short: these calls serve single decoded tokens,
+# whose kernels take less time than a careless call)
 _OUT = {torch.float32: MOE_DT_F32, torch.bfloat16: MOE_DT_BF16}
 
 
-def _is(t, name, dtype, shape, dev):
-    """t is a contiguous tensor of this type and shape on dev (an operator's x
-    sets dev)."""
+def _is(t, name, dtype, shape, index):
+    """t is a contiguous CUDA tensor of this type and shape on device `index`
+    (that of an operator's first tensor)."""
+    if t.dtype is dtype and t.shape == shape and t.get_device() == index and index >= 0 and t.is_contiguous():
+        return
     if t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
     if t.shape != shape:
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
-    if dev.type != "cuda" or not t.is_contiguous():
+    if not t.is_cuda or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous CUDA tensor")
-    if t.device != dev:
-        raise ValueError(f"{name} is on {t.device}, x on {dev}")
+    raise ValueError(f"{name} is on {t.device}, the first tensor on device {index}")
 
 
-def _dims(t, name, what, *dims):
-    if t.dim() not in dims:
-        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {what}")
+def _bad_dims(**tensors):
+    return ValueError(", ".join(f"{n} {tuple(t.shape)}" for n, t in tensors.items()) + ": wrong number of dimensions")
 
 
-def _on(dev, stream, call):
-    """call(stream handle) with dev current and torch's allocations made for
-    the stream that the kernels go to."""
-    if stream is None and torch._C._cuda_getDevice() == dev.index:
-        return call(torch._C._cuda_getCurrentRawStream(dev.index))
+def _on(index, stream, call, *args):
+    """call(stream handle, ...) with device `index` current and torch's
+    allocations made for the stream that the kernels go to."""
+    if stream is None and torch._C._cuda_getDevice() == index:
+        return call(torch._C._cuda_getCurrentRawStream(index), *args)
     if stream is None:
-        stream = torch.cuda.current_stream(dev)
-    elif stream.device != dev:
-        raise ValueError(f"stream is on {stream.device}, x on {dev}")
+        stream = torch.cuda.current_stream(index)
+    elif stream.device.index != index:
+        raise ValueError(f"stream is on {stream.device}, the tensors on device {index}")
     with torch.cuda.stream(stream):
-        return call(stream.cuda_stream)
+        return call(stream.cuda_stream, *args)
 
 
-def _out(out, shape, out_dtype, dev):
+def _out(out, shape, out_dtype, like):
     """The output tensor of an operator call: `out`, or a new one."""
     if out is None:
         if out_dtype not in _OUT:
             raise TypeError("out_dtype must be float32 or bfloat16")
-        return torch.empty(shape, dtype=out_dtype, device=dev)
+        return like.new_empty(shape, dtype=out_dtype)
     if out.dtype not in _OUT:
         raise TypeError("out must be float32 or bfloat16")
-    _is(out, "out", out.dtype, shape, dev)
+    _is(out, "out", out.dtype, shape, like.get_device())
     return out
 
 
-def _status_ptr(status, dev):
+def _status_ptr(status, index):
     if status is None:
         return None
-    _is(status, "status", torch.int32, (1,), dev)
+    _is(status, "status", torch.int32, (1,), index)
     return status.data_ptr()
 
 
-def _grouped(name, fn, a, b, offsets, R, N, K, E, shape, out_dtype, out, status, stream):
-    dev = a.device
-    _is(offsets, "offsets", torch.int32, (E + 1,), dev)
-    st = _status_ptr(status, dev)
-
-    def call(handle):
-        y = _out(out, shape, out_dtype, dev)
-        _check(fn(a.data_ptr(), b.data_ptr(), offsets.data_ptr(), R, N, K, E, y.data_ptr(), _OUT[y.dtype], st, handle),
-               name)
-        return y
-
-    return _on(dev, stream, call)
+def _grouped(handle, name, fn, a, b, offsets, R, N, K, E, shape, out_dtype, out, st):
+    y = _out(out, shape, out_dtype, a)
+    rc = fn(a.data_ptr(), b.data_ptr(), offsets.data_ptr(), R, N, K, E, y.data_ptr(), _OUT[y.dtype], st, handle)
+    if rc:
+        raise MoeError(name, rc)
+    return y
 
 
 def grouped_gemm(x, w, offsets, out_dtype=torch.float32, out=None, status=None, stream=None):
@@ -679,55 +674,88 @@ def grouped_gemm(x, w, offsets, out_dtype=torch.float32, out=None, status=None, 
     x [R,K] bf16, w [E,N,K] bf16, offsets [E+1] int32 on the device (as
     group_by_expert returns them).  Rows that no segment holds are left as
     they were in `out`, and are undefined in a new tensor."""
-    _dims(x, "x", "[R, K]", 2)
-    _dims(w, "w", "[E, N, K]", 3)
-    R, K = x.shape
-    E, N, _ = w.shape
-    _is(x, "x", torch.bfloat16, (R, K), x.device)
-    _is(w, "w", torch.bfloat16, (E, N, K), x.device)
-    return _grouped("moe_grouped_gemm", _lib.moe_grouped_gemm, x, w, offsets, R, N, K, E, (R, N), out_dtype, out,
-                    status, stream)
+    try:
+        R, K = x.shape
+        E, N, _ = w.shape
+    except ValueError:
+        raise _bad_dims(x=x, w=w) from None
+    i = x.get_device()
+    _is(x, "x", torch.bfloat16, (R, K), i)
+    _is(w, "w", torch.bfloat16, (E, N, K), i)
+    _is(offsets, "offsets", torch.int32, (E + 1,), i)
+    return _on(i, stream, _grouped, "moe_grouped_gemm", _lib.moe_grouped_gemm, x, w, offsets, R, N, K, E, (R, N),
+               out_dtype, out, _status_ptr(status, i))
 
 
 def grouped_gemm_dx(dy, w, offsets, out_dtype=torch.float32, out=None, status=None, stream=None):
     """dx [R,K]: the gradient of grouped_gemm with respect to x, row r of
     segment e being w[e]^T dy[r]; dy [R,N] bf16, w [E,N,K] bf16."""
-    _dims(dy, "dy", "[R, N]", 2)
-    _dims(w, "w", "[E, N, K]", 3)
-    R, N = dy.shape
-    E, _, K = w.shape
-    _is(dy, "dy", torch.bfloat16, (R, N), dy.device)
-    _is(w, "w", torch.bfloat16, (E, N, K), dy.device)
-    return _grouped("moe_grouped_gemm_dx", _lib.moe_grouped_gemm_dx, dy, w, offsets, R, N, K, E, (R, K), out_dtype, out,
-                    status, stream)
+    try:
+        R, N = dy.shape
+        E, _, K = w.shape
+    except ValueError:
+        raise _bad_dims(dy=dy, w=w) from None
+    i = dy.get_device()
+    _is(dy, "dy", torch.bfloat16, (R, N), i)
+    _is(w, "w", torch.bfloat16, (E, N, K), i)
+    _is(offsets, "offsets", torch.int32, (E + 1,), i)
+    return _on(i, stream, _grouped, "moe_grouped_gemm_dx", _lib.moe_grouped_gemm_dx, dy, w, offsets, R, N, K, E, (R, K),
+               out_dtype, out, _status_ptr(status, i))
 
 
 def grouped_gemm_dw(dy, x, offsets, out_dtype=torch.float32, out=None, status=None, stream=None):
     """dw [E,N,K]: the gradient of grouped_gemm with respect to w, the sum of
     dy[r] x[r]^T over segment e's rows (zeros where it has none); dy [R,N]
     bf16, x [R,K] bf16, E = len(offsets) - 1."""
-    _dims(dy, "dy", "[R, N]", 2)
-    _dims(x, "x", "[R, K]", 2)
-    _dims(offsets, "offsets", "[E + 1]", 1)
-    R, N = dy.shape
-    K = x.shape[1]
-    E = offsets.shape[0] - 1
-    _is(dy, "dy", torch.bfloat16, (R, N), dy.device)
-    _is(x, "x", torch.bfloat16, (R, K), dy.device)
-    return _grouped("moe_grouped_gemm_dw", _lib.moe_grouped_gemm_dw, dy, x, offsets, R, N, K, E, (E, N, K), out_dtype,
-                    out, status, stream)
+    try:
+        R, N = dy.shape
+        _, K = x.shape
+        E = offsets.shape[0] - 1
+    except (ValueError, IndexError):
+        raise _bad_dims(dy=dy, x=x, offsets=offsets) from None
+    i = dy.get_device()
+    _is(dy, "dy", torch.bfloat16, (R, N), i)
+    _is(x, "x", torch.bfloat16, (R, K), i)
+    _is(offsets, "offsets", torch.int32, (E + 1,), i)
+    return _on(i, stream, _grouped, "moe_grouped_gemm_dw", _lib.moe_grouped_gemm_dw, dy, x, offsets, R, N, K, E,
+               (E, N, K), out_dtype, out, _status_ptr(status, i))
 
 
 def _nvfp4_dims(t, name):
     """-> (groups, rows a group, columns) of a [R,C] (a scale a row) or
     [G,R,C] (a scale a matrix) tensor."""
-    _dims(t, name, "[R, C] (a scale a row) or [G, R, C] (a scale a matrix)", 2, 3)
-    return (t.shape[0], 1, t.shape[1]) if t.dim() == 2 else tuple(t.shape)
+    shape = t.shape
+    if len(shape) == 2:
+        return shape[0], 1, shape[1]
+    if len(shape) == 3:
+        return shape
+    raise ValueError(f"{name} has shape {tuple(shape)}, expected [R, C] (a scale a row) or [G, R, C] (a scale a matrix)")
 
 
 def _nvfp4_cols(cols, name):
     if cols % 32:
         raise ValueError(f"NVFP4 rows need a multiple of 32 elements, {name} has {cols}")
+
+
+def _quantize(handle, x, dt, G, rows, cols, out, workspace, st):
+    if out is None:
+        lead = x.shape[:-1]
+        q = x.new_empty((*lead, cols // 2), dtype=torch.uint8)
+        bs = x.new_empty((*lead, cols // 16), dtype=torch.uint8)
+        gs = x.new_empty((G,), dtype=torch.float32)
+    else:
+        q, bs, gs = out
+    wp, wn = None, 0
+    if rows > 1:
+        if workspace is None:
+            n = _S(0)
+            _check(_lib.moe_quantize_nvfp4_workspace_bytes(G, rows, cols, ctypes.byref(n)),
+                   "moe_quantize_nvfp4_workspace_bytes")
+            workspace = x.new_empty(n.value, dtype=torch.uint8)
+        wp, wn = workspace.data_ptr(), workspace.numel()
+    _check(_lib.moe_quantize_nvfp4(x.data_ptr(), dt, G, rows, cols, q.data_ptr(), bs.data_ptr(), gs.data_ptr(), wp, wn,
+                                   st, handle), "moe_quantize_nvfp4")
+    return q, bs, gs
 
 
 def quantize_nvfp4(x, out=None, workspace=None, status=None, stream=None):
@@ -736,80 +764,64 @@ def quantize_nvfp4(x, out=None, workspace=None, status=None, stream=None):
 
     x fp32 or bf16: [G,R,C] matrices with one scale each (gs [G], the layout
     of stack_forward_nvfp4_), or [R,C] rows with one scale each (gs [R]).
-    `out` is such a triple to be written."""
+    `out` is such a triple to be written; workspace is for matrices."""
     G, rows, cols = _nvfp4_dims(x, "x")
     _nvfp4_cols(cols, "x")
-    dt = _x_dtype(x)
-    dev, lead = x.device, x.shape[:-1]
-    _is(x, "x", x.dtype, x.shape, dev)
-    st = _status_ptr(status, dev)
+    dt, i = _x_dtype(x), x.get_device()
+    _is(x, "x", x.dtype, x.shape, i)
     if workspace is not None:
-        _is(workspace, "workspace", torch.uint8, workspace.shape, dev)
+        _is(workspace, "workspace", torch.uint8, workspace.shape, i)
     if out is not None:
-        _is(out[0], "out q", torch.uint8, (*lead, cols // 2), dev)
-        _is(out[1], "out bs", torch.uint8, (*lead, cols // 16), dev)
-        _is(out[2], "out gs", torch.float32, (G,), dev)
+        lead = x.shape[:-1]
+        _is(out[0], "out q", torch.uint8, (*lead, cols // 2), i)
+        _is(out[1], "out bs", torch.uint8, (*lead, cols // 16), i)
+        _is(out[2], "out gs", torch.float32, (G,), i)
+    return _on(i, stream, _quantize, x, dt, G, rows, cols, out, workspace, _status_ptr(status, i))
 
-    def call(handle):
-        q, bs, gs = out if out is not None else (torch.empty((*lead, cols // 2), dtype=torch.uint8, device=dev),
-                                                 torch.empty((*lead, cols // 16), dtype=torch.uint8, device=dev),
-                                                 torch.empty((G,), dtype=torch.float32, device=dev))
-        ws = workspace
-        if ws is None and rows > 1:
-            n = _S(0)
-            _check(_lib.moe_quantize_nvfp4_workspace_bytes(G, rows, cols, ctypes.byref(n)),
-                   "moe_quantize_nvfp4_workspace_bytes")
-            ws = torch.empty(n.value, dtype=torch.uint8, device=dev)
-        wp, wn = (None, 0) if ws is None else (ws.data_ptr(), ws.numel())
-        _check(_lib.moe_quantize_nvfp4(x.data_ptr(), dt, G, rows, cols, q.data_ptr(), bs.data_ptr(), gs.data_ptr(), wp,
-                                       wn, st, handle), "moe_quantize_nvfp4")
-        return q, bs, gs
 
-    return _on(dev, stream, call)
+def _dequantize(handle, q, bs, gs, G, rows, cols, out_dtype, out):
+    x = _out(out, (*q.shape[:-1], cols), out_dtype, q)
+    _check(_lib.moe_dequantize_nvfp4(q.data_ptr(), bs.data_ptr(), gs.data_ptr(), G, rows, cols, x.data_ptr(),
+                                     _OUT[x.dtype], handle), "moe_dequantize_nvfp4")
+    return x
 
 
 def dequantize_nvfp4(q, bs, gs, out_dtype=torch.float32, out=None, stream=None):
     """The values of quantize_nvfp4's triple: (e2m1(q) * e4m3(bs)) * gs."""
     G, rows, half = _nvfp4_dims(q, "q")
-    cols, dev, lead = 2 * half, q.device, q.shape[:-1]
+    cols, i = 2 * half, q.get_device()
     _nvfp4_cols(cols, "q")
-    _is(q, "q", torch.uint8, q.shape, dev)
-    _is(bs, "bs", torch.uint8, (*lead, cols // 16), dev)
-    _is(gs, "gs", torch.float32, (G,), dev)
+    _is(q, "q", torch.uint8, q.shape, i)
+    _is(bs, "bs", torch.uint8, (*q.shape[:-1], cols // 16), i)
+    _is(gs, "gs", torch.float32, (G,), i)
+    return _on(i, stream, _dequantize, q, bs, gs, G, rows, cols, out_dtype, out)
 
-    def call(handle):
-        x = _out(out, (*lead, cols), out_dtype, dev)
-        _check(_lib.moe_dequantize_nvfp4(q.data_ptr(), bs.data_ptr(), gs.data_ptr(), G, rows, cols, x.data_ptr(),
-                                         _OUT[x.dtype], handle), "moe_dequantize_nvfp4")
-        return x
 
-    return _on(dev, stream, call)
+def _grouped_nvfp4(handle, xq, xbs, xgs, wq, wbs, wgs, offsets, R, N, K, E, out_dtype, out, st):
+    y = _out(out, (R, N), out_dtype, xq)
+    _check(_lib.moe_grouped_gemm_nvfp4(xq.data_ptr(), xbs.data_ptr(), xgs.data_ptr(), wq.data_ptr(), wbs.data_ptr(),
+                                       wgs.data_ptr(), offsets.data_ptr(), R, N, K, E, y.data_ptr(), _OUT[y.dtype], st,
+                                       handle), "moe_grouped_gemm_nvfp4")
+    return y
 
 
 def grouped_gemm_nvfp4(xq, xbs, xgs, wq, wbs, wgs, offsets, out_dtype=torch.float32, out=None, status=None,
                        stream=None):
     """grouped_gemm with both operands in NVFP4: x as quantize_nvfp4 returns a
     [R,K] tensor (a scale a row), w as it returns [E,N,K] (a scale a matrix)."""
-    _dims(xq, "xq", "[R, K/2]", 2)
-    _dims(wq, "wq", "[E, N, K/2]", 3)
-    R, half = xq.shape
-    E, N, _ = wq.shape
-    K, dev = 2 * half, xq.device
+    try:
+        R, half = xq.shape
+        E, N, _ = wq.shape
+    except ValueError:
+        raise _bad_dims(xq=xq, wq=wq) from None
+    K, i = 2 * half, xq.get_device()
     _nvfp4_cols(K, "xq")
-    _is(xq, "xq", torch.uint8, (R, half), dev)
-    _is(xbs, "xbs", torch.uint8, (R, K // 16), dev)
-    _is(xgs, "xgs", torch.float32, (R,), dev)
-    _is(wq, "wq", torch.uint8, (E, N, half), dev)
-    _is(wbs, "wbs", torch.uint8, (E, N, K // 16), dev)
-    _is(wgs, "wgs", torch.float32, (E,), dev)
-    _is(offsets, "offsets", torch.int32, (E + 1,), dev)
-    st = _status_ptr(status, dev)
-
-    def call(handle):
-        y = _out(out, (R, N), out_dtype, dev)
-        _check(_lib.moe_grouped_gemm_nvfp4(xq.data_ptr(), xbs.data_ptr(), xgs.data_ptr(), wq.data_ptr(), wbs.data_ptr(),
-                                           wgs.data_ptr(), offsets.data_ptr(), R, N, K, E, y.data_ptr(), _OUT[y.dtype],
-                                           st, handle), "moe_grouped_gemm_nvfp4")
-        return y
-
-    return _on(dev, stream, call)
+    _is(xq, "xq", torch.uint8, (R, half), i)
+    _is(xbs, "xbs", torch.uint8, (R, K // 16), i)
+    _is(xgs, "xgs", torch.float32, (R,), i)
+    _is(wq, "wq", torch.uint8, (E, N, half), i)
+    _is(wbs, "wbs", torch.uint8, (E, N, K // 16), i)
+    _is(wgs, "wgs", torch.float32, (E,), i)
+    _is(offsets, "offsets", torch.int32, (E + 1,), i)
+    return _on(i, stream, _grouped_nvfp4, xq, xbs, xgs, wq, wbs, wgs, offsets, R, N, K, E, out_dtype, out,
+               _status_ptr(status, i))
