@@ -345,10 +345,18 @@ int moe_grouped_gemm_dx(const uint16_t* dy, const uint16_t* w, const int32_t* of
  *   dw[e, n, k] = sum over the segment's rows r of dy[r, n] x[r, k]
  * dy [R, N] and x [R, K] bf16; dw [E, N, K] fp32 or bf16 (dw_dtype), every
  * element written (zeros for an expert without rows).  Otherwise as
- * moe_grouped_gemm.  The sums' order is fixed: no atomics.
+ * moe_grouped_gemm, but with a workspace: where few experts of many rows
+ * leave fewer output tiles than the GPU has SMs, each segment's rows are cut
+ * into parts and the parts' fp32 sums are joined in a fixed order (no
+ * atomics: the same call gives the same bits).
+ * moe_grouped_gemm_dw_workspace_bytes (host-only, for the current device)
+ * receives its size, 0 where none is needed; the workspace is used by one
+ * call at a time.
  */
+int moe_grouped_gemm_dw_workspace_bytes(int R, int N, int K, int E, size_t* bytes);
 int moe_grouped_gemm_dw(const uint16_t* dy, const uint16_t* x, const int32_t* offsets, int R, int N, int K, int E,
-                        void* dw, int dw_dtype, int32_t* dev_status, void* stream);
+                        void* dw, int dw_dtype, void* workspace, size_t workspace_bytes, int32_t* dev_status,
+                        void* stream);
 
 /*
  * moe_quantize_nvfp4 -- matrices into the NVFP4 layout of

@@ -45,7 +45,8 @@ _lib.moe_stack_forward_norm.argtypes = [_I, _P, _P, _P, _P, _P, ctypes.c_float, 
                                         _P, _S, _P, _P]
 _lib.moe_grouped_gemm.argtypes = [_P, _P, _P, _I, _I, _I, _I, _P, _I, _P, _P]
 _lib.moe_grouped_gemm_dx.argtypes = [_P, _P, _P, _I, _I, _I, _I, _P, _I, _P, _P]
-_lib.moe_grouped_gemm_dw.argtypes = [_P, _P, _P, _I, _I, _I, _I, _P, _I, _P, _P]
+_lib.moe_grouped_gemm_dw_workspace_bytes.argtypes = [_I, _I, _I, _I, ctypes.POINTER(_S)]
+_lib.moe_grouped_gemm_dw.argtypes = [_P, _P, _P, _I, _I, _I, _I, _P, _I, _P, _S, _P, _P]
 _lib.moe_quantize_nvfp4_workspace_bytes.argtypes = [_I, _I, _I, ctypes.POINTER(_S)]
 _lib.moe_quantize_nvfp4.argtypes = [_P, _I, _I, _I, _I, _P, _P, _P, _P, _S, _P, _P]
 _lib.moe_dequantize_nvfp4.argtypes = [_P, _P, _P, _I, _I, _I, _P, _I, _P]
@@ -65,15 +66,15 @@ _lib.moe_status_string.restype = ctypes.c_char_p
 for _f in ("moe_workspace_bytes", "moe_route", "moe_group_by_expert", "moe_expert_forward",
            "moe_expert_forward_noalloc", "moe_layer_forward", "moe_stack_forward", "moe_stack_forward_norm",
            "moe_stack_forward_fp8", "moe_stack_forward_nvfp4", "moe_workspace_grouping", "moe_grouped_gemm",
-           "moe_grouped_gemm_dx", "moe_grouped_gemm_dw", "moe_quantize_nvfp4_workspace_bytes", "moe_quantize_nvfp4",
-           "moe_dequantize_nvfp4", "moe_grouped_gemm_nvfp4"):
+           "moe_grouped_gemm_dx", "moe_grouped_gemm_dw", "moe_grouped_gemm_dw_workspace_bytes",
+           "moe_quantize_nvfp4_workspace_bytes", "moe_quantize_nvfp4", "moe_dequantize_nvfp4", "moe_grouped_gemm_nvfp4"):
     getattr(_lib, _f).restype = ctypes.c_int
 
 EXPORTED = ("moe_workspace_bytes", "moe_route", "moe_group_by_expert", "moe_expert_forward",
             "moe_expert_forward_noalloc", "moe_layer_forward", "moe_stack_forward", "moe_stack_forward_norm",
             "moe_stack_forward_fp8", "moe_stack_forward_nvfp4", "moe_workspace_grouping",
-            "moe_grouped_gemm", "moe_grouped_gemm_dx", "moe_grouped_gemm_dw", "moe_quantize_nvfp4_workspace_bytes",
-            "moe_quantize_nvfp4", "moe_dequantize_nvfp4", "moe_grouped_gemm_nvfp4",
+            "moe_grouped_gemm", "moe_grouped_gemm_dx", "moe_grouped_gemm_dw", "moe_grouped_gemm_dw_workspace_bytes",
+            "moe_quantize_nvfp4_workspace_bytes", "moe_quantize_nvfp4", "moe_dequantize_nvfp4", "moe_grouped_gemm_nvfp4",
             "moe_launch_count", "moe_forward_path", "moe_set_trace_buffer",
             "moe_inject_barrier_stall", "moe_status_string")
 
@@ -703,10 +704,26 @@ def grouped_gemm_dx(dy, w, offsets, out_dtype=torch.float32, out=None, status=No
                out_dtype, out, _status_ptr(status, i))
 
 
-def grouped_gemm_dw(dy, x, offsets, out_dtype=torch.float32, out=None, status=None, stream=None):
+def _grouped_dw(handle, dy, x, offsets, R, N, K, E, out_dtype, out, workspace, st):
+    dw = _out(out, (E, N, K), out_dtype, dy)
+    n = _S(0)
+    _check(_lib.moe_grouped_gemm_dw_workspace_bytes(R, N, K, E, ctypes.byref(n)), "moe_grouped_gemm_dw_workspace_bytes")
+    wp, wn = None, 0
+    if n.value:
+        if workspace is None:
+            workspace = dy.new_empty(n.value, dtype=torch.uint8)
+        wp, wn = workspace.data_ptr(), workspace.numel()
+    _check(_lib.moe_grouped_gemm_dw(dy.data_ptr(), x.data_ptr(), offsets.data_ptr(), R, N, K, E, dw.data_ptr(),
+                                    _OUT[dw.dtype], wp, wn, st, handle), "moe_grouped_gemm_dw")
+    return dw
+
+
+def grouped_gemm_dw(dy, x, offsets, out_dtype=torch.float32, out=None, workspace=None, status=None, stream=None):
     """dw [E,N,K]: the gradient of grouped_gemm with respect to w, the sum of
     dy[r] x[r]^T over segment e's rows (zeros where it has none); dy [R,N]
-    bf16, x [R,K] bf16, E = len(offsets) - 1."""
+    bf16, x [R,K] bf16, E = len(offsets) - 1.  Few experts of many rows take a
+    workspace (uint8, moe_grouped_gemm_dw_workspace_bytes; allocated here by
+    default)."""
     try:
         R, N = dy.shape
         _, K = x.shape
@@ -717,8 +734,9 @@ def grouped_gemm_dw(dy, x, offsets, out_dtype=torch.float32, out=None, status=No
     _is(dy, "dy", torch.bfloat16, (R, N), i)
     _is(x, "x", torch.bfloat16, (R, K), i)
     _is(offsets, "offsets", torch.int32, (E + 1,), i)
-    return _on(i, stream, _grouped, "moe_grouped_gemm_dw", _lib.moe_grouped_gemm_dw, dy, x, offsets, R, N, K, E,
-               (E, N, K), out_dtype, out, _status_ptr(status, i))
+    if workspace is not None:
+        _is(workspace, "workspace", torch.uint8, workspace.shape, i)
+    return _on(i, stream, _grouped_dw, dy, x, offsets, R, N, K, E, out_dtype, out, workspace, _status_ptr(status, i))
 
 
 def _nvfp4_dims(t, name):

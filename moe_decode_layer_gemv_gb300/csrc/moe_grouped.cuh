@@ -33,6 +33,12 @@ constexpr int kGgSmem = 227 * 1024;
 constexpr uint32_t kGgWaitNs = 20000;     // a wait sleeps this long at a time ...
 constexpr uint32_t kGgWaitLimit = 1u << 17;  // ... and gives up after so many times
 constexpr uint32_t kGgTmemCols = 512;
+// The tensor cores add to an accumulator with truncation: an error that grows
+// with the number of additions (measured: 1.2e-8 of the result a 16-deep MMA).
+// fp32 results take at most so many 64-wide steps in one accumulator, 64
+// MMAs; the parts are added in fp32, rounded to nearest.  Beside a bf16
+// result's own rounding the error of one accumulator does not count.
+constexpr int kGgPartSteps = 16;
 
 struct GgParams {
     CUtensorMap ta, tb;
@@ -42,6 +48,7 @@ struct GgParams {
     int M;     // extent of the output's contiguous dimension
     int C;     // contraction length (forward, dx)
     int NW;    // dw: rows of a weight matrix
+    int split; // dw: parts that each segment's rows are cut into, part p's result at out + p E NW M
     void* out;
     int out_f32;
     int a_blocked, b_blocked;  // MN-major operands: the map has a 64-column block dimension
@@ -400,12 +407,19 @@ __device__ __forceinline__ uint32_t gg_pair_select(int odd) { return odd ? 0x327
 // fp32 as they are, a warp writing 128 contiguous bytes a row; bf16 after
 // lanes 2i and 2i + 1 have exchanged a value per pair of rows, so that each
 // lane writes two neighbouring m (4 bytes) of one row.
-__device__ __forceinline__ void gg_store32(const uint32_t (&r)[32], void* out, int out_f32, size_t row0, int nc, int m,
-                                           int M) {
+__device__ __forceinline__ void gg_store32(uint32_t (&r)[32], void* out, int out_f32, size_t row0, int nc, int m, int M,
+                                           bool add = false) {
     const bool whole = nc >= 32;
     if (out_f32) {
         uint32_t* o = static_cast<uint32_t*>(out) + row0 * (size_t)M + m;
         if (m >= M) return;
+        if (add) {  // to this thread's own earlier stores
+            float old[32];
+#pragma unroll
+            for (int j = 0; j < 32; ++j) old[j] = j < nc ? __ldcg(reinterpret_cast<const float*>(o + (size_t)j * M)) : 0.0f;
+#pragma unroll
+            for (int j = 0; j < 32; ++j) r[j] = __float_as_uint(old[j] + __uint_as_float(r[j]));
+        }
         if (whole) {
 #pragma unroll
             for (int j = 0; j < 32; ++j, o += M) *o = r[j];
@@ -434,9 +448,9 @@ __device__ __forceinline__ void gg_store32(const uint32_t (&r)[32], void* out, i
 
 // The columns of one accumulator, 32 at a time, the next 32 on their way
 // while these are stored; `done` runs once they are all in registers.
-template <typename Scale, typename Done>
+template <typename Done>
 __device__ __forceinline__ void gg_epilogue(uint32_t taddr, void* out, int out_f32, size_t row0, int n, int m, int M,
-                                            Scale scale, Done done) {
+                                            bool add, Done done) {
     uint32_t a[32], b[32];
     gg_ld32(taddr, a);
     for (int c = 0; c < n; c += 64) {
@@ -445,16 +459,14 @@ __device__ __forceinline__ void gg_epilogue(uint32_t taddr, void* out, int out_f
             gg_ld32(taddr + c + 32, b);
         else
             done();
-        scale(a, c);
-        gg_store32(a, out, out_f32, row0 + c, min(32, n - c), m, M);
+        gg_store32(a, out, out_f32, row0 + c, min(32, n - c), m, M, add);
         if (c + 32 >= n) break;
         gg_ld_wait(b);
         if (c + 64 < n)
             gg_ld32(taddr + c + 64, a);
         else
             done();
-        scale(b, c + 32);
-        gg_store32(b, out, out_f32, row0 + c + 32, min(32, n - c - 32), m, M);
+        gg_store32(b, out, out_f32, row0 + c + 32, min(32, n - c - 32), m, M, add);
     }
 }
 
@@ -517,14 +529,15 @@ __global__ void __launch_bounds__(gg_threads<MODE>(), 1) gg_kernel(const __grid_
     const uint32_t S = min((uint32_t)kGgMaxStages, ((uint32_t)kGgSmem - 1023u - 4096u) / stage_bytes);
 
     const int ntiles_w = (p.NW + Cfg::BN - 1) / Cfg::BN;  // dw
-    const int items = MODE == kGgDw ? p.E * mtiles * ntiles_w : sh->start[p.E];
+    const int items = MODE == kGgDw ? p.split * p.E * mtiles * ntiles_w : sh->start[p.E];
 
-    // f(e, q0, n, mt, nst): segment e; q0 = first row (forward, dx: of the
-    // tile, dw: of the segment); n = valid columns; m0; contraction steps of 64
+    // f(e, q0, n, n0, m0, len): segment e; first row q0 (forward, dx: of the
+    // tile; dw: of the segment's part); n valid columns from n0 on; m from m0
+    // on; contraction length.  (dw: e counts part after part, part * E + e)
     auto walk = [&](auto f) {
         int e = 0;
         for (int it = unit; it < items; it += units) {
-            int q0, n, n0, m0, nk;
+            int q0, n, n0, m0, len;
             if (MODE == kGgDw) {
                 const int per = mtiles * ntiles_w;
                 e = it / per;
@@ -532,8 +545,10 @@ __global__ void __launch_bounds__(gg_threads<MODE>(), 1) gg_kernel(const __grid_
                 m0 = (t % mtiles) * Cfg::BM;
                 n0 = (t / mtiles) * Cfg::BN;
                 n = min(Cfg::BN, p.NW - n0);
-                q0 = sh->p0[e];
-                nk = (sh->cnt[e] + 63) / 64;
+                const int seg = e % p.E, cnt = sh->cnt[seg];
+                const int part = ((cnt + p.split - 1) / p.split + 63) / 64 * 64, at = min(cnt, e / p.E * part);
+                q0 = sh->p0[seg] + at;
+                len = min(part, cnt - at);
             } else {
                 e = gg_seek(sh->start, p.E, it, e);
                 const int t = it - sh->start[e];
@@ -541,11 +556,13 @@ __global__ void __launch_bounds__(gg_threads<MODE>(), 1) gg_kernel(const __grid_
                 n0 = (t / mtiles) * Cfg::BN;
                 n = min(Cfg::BN, sh->cnt[e] - n0);
                 q0 = sh->p0[e] + n0;
-                nk = (p.C + 63) / 64;
+                len = p.C;
             }
-            if (!f(e, q0, n, n0, m0, nk)) break;
+            if (!f(e, q0, n, n0, m0, len)) break;
         }
     };
+    // 64-wide steps that one accumulator takes
+    const int part_steps = p.out_f32 ? kGgPartSteps : 1 << 30;
 
     if (warp == 4) {
         // ---------------- TMA producer
@@ -553,7 +570,8 @@ __global__ void __launch_bounds__(gg_threads<MODE>(), 1) gg_kernel(const __grid_
         const uint32_t ring_at = smem_u32(ring);
         const uint32_t bars = CG == 1 ? smem_u32(sh->full) : cluster_addr(sh->full, 0);
         if (gg_elect()) {
-            walk([&](int e, int q0, int n, int n0, int m0, int nk) -> bool {
+            walk([&](int e, int q0, int n, int n0, int m0, int len) -> bool {
+                const int nk = (len + 63) / 64;
                 // rows of B that this CTA holds (forward, dx), in whole boxes
                 const int rows = MODE == kGgDw ? 128 : (n + kGgBoxN * CG - 1) / (kGgBoxN * CG) * kGgBoxN;
                 const uint32_t bytes = CG * (kGgTile + (uint32_t)rows * 128u);
@@ -564,7 +582,7 @@ __global__ void __launch_bounds__(gg_threads<MODE>(), 1) gg_kernel(const __grid_
                     const int ke = min(Cfg::KSUB, nk - k0);
                     // dw: the stage that a segment ends in, if not with a whole MMA, lands on
                     // each CTA's own barrier and is cleared there before it counts as full
-                    const bool tail = MODE == kGgDw && gg_ragged(sh->cnt[e] - k0 * 64);
+                    const bool tail = MODE == kGgDw && gg_ragged(len - k0 * 64);
                     const uint32_t tbar = smem_u32(&sh->tfull[r.s]);
                     if (tail) mbar_arrive_expect_tx(&sh->tfull[r.s], kGgTile + (uint32_t)rows * 128u);
                     if (rank == 0) {
@@ -615,27 +633,33 @@ __global__ void __launch_bounds__(gg_threads<MODE>(), 1) gg_kernel(const __grid_
         uint32_t free_ph = 1;  // parity of acc_empty to wait for (at first: nothing)
         uint32_t tails = 0;    // parity of each stage's next use as a segment's end
         const uint32_t ring_at = smem_u32(ring);
-        if (rank == 0) walk([&](int e, int q0, int n, int n0, int m0, int nk) -> bool {
-            if (nk == 0) return true;
-            if (!gg_wait(&sh->acc_empty[buf], free_ph, &sh->abort)) return false;
-            tc_fence_after();
-            const uint32_t tacc = tmem + (uint32_t)(buf * Cfg::BN);
+        if (rank == 0) walk([&](int e, int q0, int n, int n0, int m0, int len) -> bool {
+            const int nk = (len + 63) / 64;
             const int npad = MODE == kGgDw ? Cfg::BN : (n + kGgBoxN * CG - 1) / (kGgBoxN * CG) * (kGgBoxN * CG);
             const uint32_t idesc = umma_idesc_bf16(Cfg::BM, npad) | (MODE != kGgFwd ? 1u << 15 : 0u) |
                                    (MODE == kGgDw ? 1u << 16 : 0u);
-            uint32_t acc = 0;
+            uint32_t acc = 0, tacc = 0;
+            int room = 0;  // steps that the accumulator still takes
             for (int k0 = 0; k0 < nk; k0 += Cfg::KSUB) {
+                if (room == 0) {
+                    if (!gg_wait(&sh->acc_empty[buf], free_ph, &sh->abort)) return false;
+                    tacc = tmem + (uint32_t)(buf * Cfg::BN);
+                    acc = 0;
+                    room = part_steps;
+                }
                 if (!gg_wait(&sh->full[r.s], r.ph, &sh->abort)) return false;
                 const uint32_t sta = ring_at + r.s * stage_bytes;
                 int steps = 4;  // MMAs (16 deep) of a 64-wide step
                 if (MODE == kGgDw) {
-                    const int valid = sh->cnt[e] - k0 * 64;
+                    const int valid = len - k0 * 64;
                     if (valid < 64) steps = (valid + 15) / 16;
                     if (gg_ragged(valid)) {
                         if (!gg_wait(&sh->clear[r.s], (tails >> r.s) & 1u, &sh->abort)) return false;
                         tails ^= 1u << r.s;
                     }
                 }
+                room -= Cfg::KSUB;  // (a whole number of stages)
+                const bool last = room == 0 || k0 + Cfg::KSUB >= nk;
                 tc_fence_after();
                 if (gg_elect()) {
                     const int ke = min(Cfg::KSUB, nk - k0);
@@ -650,19 +674,22 @@ __global__ void __launch_bounds__(gg_threads<MODE>(), 1) gg_kernel(const __grid_
                         for (int kk = 0; kk < 4; ++kk) {
                             if (MODE == kGgDw && kk >= steps) break;
                             gg_mma<CG>(tacc, ad + (uint64_t)(kk * (MODE == kGgFwd ? 32 : 2048) / 16),
-                                       bd + (uint64_t)(kk * (MODE == kGgDw ? 2048 : 32) / 16), idesc, acc);
-                            acc = 1;
+                                       bd + (uint64_t)(kk * (MODE == kGgDw ? 2048 : 32) / 16), idesc,
+                                       u == 0 && kk == 0 ? acc : 1u);
                         }
                     }
                     gg_commit<CG>(&sh->empty[r.s]);
+                    if (last) gg_commit<CG>(&sh->acc_full[buf]);
                 }
                 __syncwarp();
+                acc = 1;
+                if (last) {
+                    room = 0;
+                    buf ^= 1;
+                    if (buf == 0) free_ph ^= 1u;
+                }
                 r.next(S);
             }
-            if (gg_elect()) gg_commit<CG>(&sh->acc_full[buf]);
-            __syncwarp();
-            buf ^= 1;
-            if (buf == 0) free_ph ^= 1u;
             return true;
         });
         if (rank == 0 && lane == 0) {
@@ -679,8 +706,8 @@ __global__ void __launch_bounds__(gg_threads<MODE>(), 1) gg_kernel(const __grid_
         // held up every tile's end (40 of 280 us of the training batch).
         GgRing r;
         uint32_t tails = 0;
-        walk([&](int e, int q0, int n, int n0, int m0, int nk) -> bool {
-            const int left = sh->cnt[e] - (nk - 1) * 64;
+        walk([&](int e, int q0, int n, int n0, int m0, int len) -> bool {
+            const int nk = (len + 63) / 64, left = len - (nk - 1) * 64;
             for (int k = 0; k + 1 < nk; ++k) r.next(S);
             if (nk > 0) {
                 if (gg_ragged(left)) {
@@ -707,8 +734,10 @@ __global__ void __launch_bounds__(gg_threads<MODE>(), 1) gg_kernel(const __grid_
         });
         __syncwarp();
     } else {
-        int d = 0;
-        walk([&](int e, int q0, int n, int n0, int m0, int nk) -> bool {
+        int buf = 0;
+        uint32_t full_ph = 0;
+        walk([&](int e, int q0, int n, int n0, int m0, int len) -> bool {
+            const int nk = (len + 63) / 64;
             const int m = m0 + (int)rank * 128 + (int)threadIdx.x;
             const size_t row0 = MODE == kGgDw ? (size_t)e * p.NW + n0 : (size_t)q0;
             if (MODE == kGgDw && nk == 0) {  // no rows: zeros
@@ -718,24 +747,25 @@ __global__ void __launch_bounds__(gg_threads<MODE>(), 1) gg_kernel(const __grid_
                 for (int c = 0; c < n; c += 32) gg_store32(z, p.out, p.out_f32, row0 + c, min(32, n - c), m, p.M);
                 return true;
             }
-            const int buf = d & 1, use = d >> 1;
-            ++d;
-            if (!gg_wait(&sh->acc_full[buf], (uint32_t)(use & 1), &sh->abort)) return false;
-            __syncwarp();
-            tc_fence_after();
-            gg_epilogue(
-                tmem + (uint32_t)(buf * Cfg::BN) + ((uint32_t)(warp * 32) << 16), p.out, p.out_f32, row0, n, m, p.M,
-                [](uint32_t(&)[32], int) {},
-                [&]() {
-                    tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) {
-                        if (CG == 1)
-                            mbar_arrive(&sh->acc_empty[buf]);
-                        else
-                            mbar_arrive_cluster(&sh->acc_empty[buf], 0);
-                    }
-                });
+            for (int k = 0; k < nk; k += part_steps) {
+                if (!gg_wait(&sh->acc_full[buf], full_ph, &sh->abort)) return false;
+                __syncwarp();
+                tc_fence_after();
+                gg_epilogue(tmem + (uint32_t)(buf * Cfg::BN) + ((uint32_t)(warp * 32) << 16), p.out, p.out_f32, row0, n, m,
+                            p.M, k > 0, [&]() {
+                                tc_fence_before();
+                                __syncwarp();
+                                if (lane == 0) {
+                                    if (CG == 1)
+                                        mbar_arrive(&sh->acc_empty[buf]);
+                                    else
+                                        mbar_arrive_cluster(&sh->acc_empty[buf], 0);
+                                }
+                            });
+                buf ^= 1;
+                if (buf == 0) full_ph ^= 1u;
+                if (part_steps >= nk) break;
+            }
             return true;
         });
     }
@@ -745,6 +775,24 @@ __global__ void __launch_bounds__(gg_threads<MODE>(), 1) gg_kernel(const __grid_
     if (warp == 5) {
         tc_fence_after();
         gg_tmem_dealloc<CG>(tmem, kGgTmemCols);
+    }
+}
+
+// dw of a split launch: the parts' sums, part after part (a fixed order).
+__global__ void __launch_bounds__(256) gg_join_kernel(const float4* __restrict__ parts, size_t n4, int split, void* out,
+                                                      int out_f32) {
+    grid_dep_wait();
+    for (size_t i = (size_t)blockIdx.x * blockDim.x + threadIdx.x; i < n4; i += (size_t)gridDim.x * blockDim.x) {
+        float4 a = __ldcg(parts + i);
+        for (int k = 1; k < split; ++k) {
+            const float4 b = __ldcg(parts + (size_t)k * n4 + i);
+            a = make_float4(a.x + b.x, a.y + b.y, a.z + b.z, a.w + b.w);
+        }
+        if (out_f32)
+            static_cast<float4*>(out)[i] = a;
+        else
+            static_cast<uint2*>(out)[i] = make_uint2(gg_pack(__float_as_uint(a.x), __float_as_uint(a.y)),
+                                                     gg_pack(__float_as_uint(a.z), __float_as_uint(a.w)));
     }
 }
 

@@ -74,8 +74,21 @@ static int launch_persistent(K kernel, const P& p, int threads, int sms, cudaStr
     return launch_ex(cfg, kernel, p);
 }
 
-// The paired tile (256 x 256) from this many rows a segment on average.
+// The paired tile (256 x 256) from this many rows a segment on average, where
+// the output is wider than a single CTA's tile.
 constexpr int kGgPairRows = 128;
+
+static bool gg_pairs(int R, int M, int E) { return (int64_t)R >= (int64_t)kGgPairRows * E && M > 128; }
+
+// dw: with fewer tiles than CTAs (or pairs) the segments' rows are cut into
+// parts, of 512 rows on average at least, whose sums are joined afterwards.
+static int gg_split(int R, int N, int K, int E, int sms) {
+    const int cg = gg_pairs(R, K, E) ? 2 : 1;
+    const int64_t tiles = (int64_t)E * ceil_div(N, 128 * cg) * ceil_div(K, 128 * cg);
+    int64_t parts = sms / cg / tiles;
+    if (parts > (int64_t)R / E / 512) parts = (int64_t)R / E / 512;
+    return parts < 2 ? 1 : (int)parts;
+}
 
 template <int MODE>
 static int run_gg(GgParams& p, const void* a, const void* b, int R, int N, int K, int E, cudaStream_t st) {
@@ -100,8 +113,7 @@ static int run_gg(GgParams& p, const void* a, const void* b, int R, int N, int K
     p.NW = N;
     const int sms = sm_count();
     if (sms < 2) return MOE_ERR_CUDA;
-    const bool pair = (int64_t)R >= (int64_t)kGgPairRows * E;
-    return pair ? launch_persistent<2>(gg_kernel<MODE, 2>, p, gg_threads<MODE>(), sms, st)
+    return gg_pairs(R, p.M, E) ? launch_persistent<2>(gg_kernel<MODE, 2>, p, gg_threads<MODE>(), sms, st)
                 : launch_persistent<1>(gg_kernel<MODE, 1>, p, gg_threads<MODE>(), sms, st);
 }
 
@@ -141,6 +153,8 @@ static int check_nvfp4(int G, int rows, int cols, int dtype) {
     if (dtype != MOE_DT_F32 && dtype != MOE_DT_BF16) return MOE_ERR_INVALID_ARG;
     return MOE_OK;
 }
+
+constexpr int kMaxSms = 152;  // sizes a workspace where no device is visible
 
 static bool aligned32(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 31u) == 0; }
 
@@ -195,25 +209,48 @@ int moe_grouped_gemm_dx(const uint16_t* dy, const uint16_t* w, const int32_t* of
     return run_gg<kGgDx>(p, w, dy, R, N, K, E, static_cast<cudaStream_t>(stream));
 }
 
+int moe_grouped_gemm_dw_workspace_bytes(int R, int N, int K, int E, size_t* bytes) {
+    const int rc = check_grouped(R, N, K, E, MOE_DT_F32);
+    if (rc) return rc;
+    if (!bytes) return MOE_ERR_INVALID_ARG;
+    const int sms = sm_count();
+    const int split = gg_split(R, N, K, E, sms > 1 ? sms : kMaxSms);
+    *bytes = split > 1 ? sizeof(float) * (size_t)split * E * N * K : 0;
+    return MOE_OK;
+}
+
 int moe_grouped_gemm_dw(const uint16_t* dy, const uint16_t* x, const int32_t* offsets, int R, int N, int K, int E,
-                        void* dw, int dw_dtype, int32_t* dev_status, void* stream) {
+                        void* dw, int dw_dtype, void* workspace, size_t workspace_bytes, int32_t* dev_status,
+                        void* stream) {
     int rc = check_grouped(R, N, K, E, dw_dtype);
     if (rc) return rc;
     MOE_REQ(dw);
     MOE_OPT(dev_status);
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    if (R == 0)
-        return to_status(cudaMemsetAsync(dw, 0, (size_t)E * N * K * (dw_dtype == MOE_DT_F32 ? 4 : 2), st));
+    const size_t n = (size_t)E * N * K;
+    if (R == 0) return to_status(cudaMemsetAsync(dw, 0, n * (dw_dtype == MOE_DT_F32 ? 4 : 2), st));
     MOE_REQ(dy);
     MOE_REQ(x);
     MOE_REQ(offsets);
+    const int sms = sm_count();
+    const int split = gg_split(R, N, K, E, sms > 1 ? sms : kMaxSms);
+    if (split > 1) {
+        if (!workspace || workspace_bytes < sizeof(float) * split * n) return MOE_ERR_WORKSPACE;
+        MOE_REQ(workspace);
+    }
     GgParams p;
     memset(&p, 0, sizeof p);
     p.offsets = offsets;
-    p.out = dw;
-    p.out_f32 = dw_dtype == MOE_DT_F32;
+    p.out = split > 1 ? workspace : dw;
+    p.out_f32 = split > 1 || dw_dtype == MOE_DT_F32;
+    p.split = split;
     p.status = dev_status;
-    return run_gg<kGgDw>(p, x, dy, R, N, K, E, st);
+    if ((rc = run_gg<kGgDw>(p, x, dy, R, N, K, E, st))) return rc;
+    if (split == 1) return MOE_OK;
+    size_t grid = (n / 4 + 255) / 256;
+    if (grid > (size_t)sms * 8) grid = (size_t)sms * 8;
+    return launch_pdl(gg_join_kernel, (unsigned)grid, 256, 0, st, static_cast<const float4*>(workspace), n / 4, split, dw,
+                      (int)(dw_dtype == MOE_DT_F32));
 }
 
 int moe_quantize_nvfp4_workspace_bytes(int G, int rows, int cols, size_t* bytes) {

@@ -86,6 +86,28 @@ def test_matches_64_bit_loops(cuda_lib, op, counts, N, K, dtype):
     assert int(st.item()) == 0
 
 
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("op,counts,N,K", [
+    ("fwd", [3, 0, 200], 136, 4104), ("fwd", [300, 260], 264, 4104),   # several accumulators a sum
+    ("dx", [70, 5], 4104, 136), ("dx", [300, 260], 4104, 264),
+    ("dw", [5000], 264, 200), ("dw", [3000, 0, 2100], 136, 72),        # ... and segments cut into parts
+    ("dw", [12345, 1, 0, 4000], 64, 520), ("dw", [700, 33000], 72, 72),
+])
+def test_long_sums_stay_close(cuda_lib, op, counts, N, K, dtype):
+    """fp32 results of long contractions: parts of 1024 terms in the tensor
+    cores, whose additions may truncate (2^-23 of the part's magnitudes each
+    addition of 16 terms, 64 of them: 2^-17; the terms' own sum adds as much
+    at most), added with rounding to nearest (2^-24 of the sum's magnitudes
+    each).  Errors of a random sign's sum stay far below: what is held here is
+    2^-17 of the result's 2-norm, where one accumulator for 33000 terms is off by 2e-5."""
+    off, x, w, dy = _case(counts, N, K)
+    got = _call(cuda_lib, op, off, x, w, dy, out_dtype=dtype)
+    ref = _reference(op, off, x, w, dy)
+    _check(got, ref, dtype)
+    if dtype == torch.float32:
+        assert float((got.double() - ref[0]).norm() / ref[0].norm()) <= 2.0 ** -17
+
+
 @pytest.mark.parametrize("counts", [[2, 0, 3], [20, 0, 43, 1], [200, 0, 300]])
 @pytest.mark.parametrize("op", ["fwd", "dx"])
 def test_rows_of_no_segment_are_left_as_they_were(cuda_lib, op, counts):

@@ -22,7 +22,8 @@ def test_grouped_products_refuse_before_any_launch(api, fn):
     f = getattr(api._lib, fn)
 
     def call(a=GOOD, b=GOOD, off=GOOD, R=4, N=64, K=64, E=8, out=GOOD, dt=1, st=None):
-        return f(a, b, off, R, N, K, E, out, dt, st, None)
+        ws = (GOOD, 0) if fn == "moe_grouped_gemm_dw" else ()
+        return f(a, b, off, R, N, K, E, out, dt, *ws, st, None)
 
     inv = api.MOE_ERR_INVALID_ARG
     for kw in (dict(R=-1), dict(R=(1 << 22) + 1), dict(N=0), dict(N=12), dict(N=32776), dict(K=4), dict(K=20),
@@ -33,6 +34,21 @@ def test_grouped_products_refuse_before_any_launch(api, fn):
         assert call(R=0, a=None, b=None, off=None, out=None) == api.MOE_OK
     else:
         assert call(R=0, out=None) == inv
+
+
+def test_split_weight_gradients_need_their_workspace(api):
+    n = ctypes.c_size_t(0)
+    need = api._lib.moe_grouped_gemm_dw_workspace_bytes
+    assert need(1000, 64, 64, 8, ctypes.byref(n)) == 0 and n.value == 0
+    assert need(1 << 16, 64, 64, 1, ctypes.byref(n)) == 0 and n.value >= 2 * 64 * 64 * 4
+    assert need(1 << 16, 64, 60, 1, ctypes.byref(n)) == api.MOE_ERR_INVALID_ARG
+    assert need(1 << 16, 64, 64, 1, None) == api.MOE_ERR_INVALID_ARG
+
+    def dw(ws, nw):
+        return api._lib.moe_grouped_gemm_dw(GOOD, GOOD, GOOD, 1 << 16, 64, 64, 1, GOOD, 0, ws, nw, None, None)
+
+    assert dw(None, 1 << 30) == api.MOE_ERR_WORKSPACE and dw(GOOD, 64) == api.MOE_ERR_WORKSPACE
+    assert dw(ODD, 1 << 30) == api.MOE_ERR_INVALID_ARG
 
 
 def test_quantisation_refuses_before_any_launch(api):
