@@ -24,8 +24,6 @@ namespace moe {
 
 enum { kGgFwd = 0, kGgDx = 1, kGgDw = 2 };
 
-constexpr int kGgThreads = 192;      // warps 0-3 epilogue, warp 4 TMA producer, warp 5 MMA issuer ...
-constexpr int kGgThreadsDw = 224;    // ... and for dw warp 6, which clears rows behind a segment
 constexpr int kGgMaxStages = 12;
 constexpr int kGgBoxN = 32;          // rows per TMA box of a K-major B operand
 constexpr int kGgTile = 128 * 128;   // bytes of one 128 x 64 bf16 operand tile
@@ -58,8 +56,16 @@ struct GgParams {
 // CG CTAs (a cluster) work on one tile: with CG = 2 each holds 128 of the
 // tile's 256 m and half of its n, and one tcgen05.mma.cta_group::2 reads both
 // CTAs' shared memory.  KSUB 64-wide contraction steps fill one stage.
+// Warps: EPI epilogue warps (lane quarter w & 3, share of the columns w >> 2),
+// the TMA producer, the MMA issuer and for dw one that clears rows behind a
+// segment.  Four epilogue warps keep up with a long contraction and disturb
+// it least (forward of 65536 rows: 254 us, eight 264); the weight gradient of
+// few rows is all epilogue (0.4 GB in bf16: 126 us with four, 88 with eight).
 template <int MODE, int CG>
 struct GgCfg {
+    static constexpr int EPI = MODE == kGgDw ? 8 : 4;
+    static constexpr int kThreads = 32 * (EPI + (MODE == kGgDw ? 3 : 2));
+    static constexpr int COLS = 128 * CG / (EPI / 4);  // columns an epilogue warp takes
     static constexpr int BM = 128 * CG;
     static constexpr int BN = 128 * CG;
     static constexpr int KSUB = (CG == 1 && MODE != kGgDw) ? 2 : 1;
@@ -474,14 +480,9 @@ __device__ __forceinline__ void gg_epilogue(uint32_t taddr, void* out, int out_f
 // Persistent: one CTA per SM (or one pair of CTAs per SM pair) walks the
 // tiles.  Three roles run through the same tile sequence, each at its own
 // pace: the producer fills the ring, the MMA issuer accumulates tile d into
-// tensor-memory buffer d mod 2, four warps read the other buffer out.
-template <int MODE>
-constexpr int gg_threads() {
-    return MODE == kGgDw ? kGgThreadsDw : kGgThreads;
-}
-
+// tensor-memory buffer d mod 2, the epilogue warps read the other buffer out.
 template <int MODE, int CG>
-__global__ void __launch_bounds__(gg_threads<MODE>(), 1) gg_kernel(const __grid_constant__ GgParams p) {
+__global__ void __launch_bounds__((GgCfg<MODE, CG>::kThreads), 1) gg_kernel(const __grid_constant__ GgParams p) {
     using Cfg = GgCfg<MODE, CG>;
     extern __shared__ __align__(1024) unsigned char gg_smem_raw[];
     unsigned char* base = reinterpret_cast<unsigned char*>(
@@ -502,13 +503,13 @@ __global__ void __launch_bounds__(gg_threads<MODE>(), 1) gg_kernel(const __grid_
         }
         for (int a = 0; a < 2; ++a) {
             mbar_init(&sh->acc_full[a], 1);
-            mbar_init(&sh->acc_empty[a], 4 * CG);
+            mbar_init(&sh->acc_empty[a], Cfg::EPI * CG);
         }
         mbar_init(&sh->mma_done, 1);
         sh->abort = 0;
         fence_mbar_init();
     }
-    if (warp == 5) gg_tmem_alloc<CG>(&sh->tmem_slot, kGgTmemCols);
+    if (warp == Cfg::EPI + 1) gg_tmem_alloc<CG>(&sh->tmem_slot, kGgTmemCols);
     grid_dep_wait();
     const int mtiles = (p.M + Cfg::BM - 1) / Cfg::BM;
     gg_segments(sh, p.offsets, p.E, p.R, Cfg::BN, mtiles, p.status);
@@ -564,7 +565,7 @@ __global__ void __launch_bounds__(gg_threads<MODE>(), 1) gg_kernel(const __grid_
     // 64-wide steps that one accumulator takes
     const int part_steps = p.out_f32 ? kGgPartSteps : 1 << 30;
 
-    if (warp == 4) {
+    if (warp == Cfg::EPI) {
         // ---------------- TMA producer
         GgRing r;
         const uint32_t ring_at = smem_u32(ring);
@@ -626,7 +627,7 @@ __global__ void __launch_bounds__(gg_threads<MODE>(), 1) gg_kernel(const __grid_
             gg_drain<CG>(sh, S, r, rank);
         }
         __syncwarp();
-    } else if (warp == 5) {
+    } else if (warp == Cfg::EPI + 1) {
         // ---------------- MMA issuer (one thread of the leader)
         GgRing r;
         int buf = 0;
@@ -697,7 +698,7 @@ __global__ void __launch_bounds__(gg_threads<MODE>(), 1) gg_kernel(const __grid_
             gg_settle(&sh->mma_done, 0u);
         }
         __syncwarp();
-    } else if (warp == 6) {
+    } else if (warp == Cfg::EPI + 2) {
         // ---------------- dw: the segment's end.  Rows behind it belong to
         // the next segment (or to no one), so both operands' rows up to the
         // last MMA's end are zeroed -- zeroing one would leave 0 x infinity or
@@ -736,32 +737,38 @@ __global__ void __launch_bounds__(gg_threads<MODE>(), 1) gg_kernel(const __grid_
     } else {
         int buf = 0;
         uint32_t full_ph = 0;
+        const int c0 = (warp >> 2) * Cfg::COLS;
         walk([&](int e, int q0, int n, int n0, int m0, int len) -> bool {
             const int nk = (len + 63) / 64;
-            const int m = m0 + (int)rank * 128 + (int)threadIdx.x;
-            const size_t row0 = MODE == kGgDw ? (size_t)e * p.NW + n0 : (size_t)q0;
+            const int m = m0 + (int)rank * 128 + (warp & 3) * 32 + lane;
+            const int mine = min(Cfg::COLS, n - c0);  // columns of this warp; none below 1
+            const size_t row0 = (MODE == kGgDw ? (size_t)e * p.NW + n0 : (size_t)q0) + c0;
             if (MODE == kGgDw && nk == 0) {  // no rows: zeros
                 uint32_t z[32];
 #pragma unroll
                 for (int j = 0; j < 32; ++j) z[j] = 0;
-                for (int c = 0; c < n; c += 32) gg_store32(z, p.out, p.out_f32, row0 + c, min(32, n - c), m, p.M);
+                for (int c = 0; c < mine; c += 32) gg_store32(z, p.out, p.out_f32, row0 + c, min(32, mine - c), m, p.M);
                 return true;
             }
             for (int k = 0; k < nk; k += part_steps) {
                 if (!gg_wait(&sh->acc_full[buf], full_ph, &sh->abort)) return false;
                 __syncwarp();
                 tc_fence_after();
-                gg_epilogue(tmem + (uint32_t)(buf * Cfg::BN) + ((uint32_t)(warp * 32) << 16), p.out, p.out_f32, row0, n, m,
-                            p.M, k > 0, [&]() {
-                                tc_fence_before();
-                                __syncwarp();
-                                if (lane == 0) {
-                                    if (CG == 1)
-                                        mbar_arrive(&sh->acc_empty[buf]);
-                                    else
-                                        mbar_arrive_cluster(&sh->acc_empty[buf], 0);
-                                }
-                            });
+                auto release = [&]() {
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) {
+                        if (CG == 1)
+                            mbar_arrive(&sh->acc_empty[buf]);
+                        else
+                            mbar_arrive_cluster(&sh->acc_empty[buf], 0);
+                    }
+                };
+                if (mine > 0)
+                    gg_epilogue(tmem + (uint32_t)(buf * Cfg::BN + c0) + ((uint32_t)((warp & 3) * 32) << 16), p.out,
+                                p.out_f32, row0, mine, m, p.M, k > 0, release);
+                else
+                    release();
                 buf ^= 1;
                 if (buf == 0) full_ph ^= 1u;
                 if (part_steps >= nk) break;
@@ -772,7 +779,7 @@ __global__ void __launch_bounds__(gg_threads<MODE>(), 1) gg_kernel(const __grid_
     __syncthreads();
     if (*(volatile int*)&sh->abort && threadIdx.x == 0) set_status(p.status, MOE_DEV_TIMEOUT);
     if (CG == 2) cluster_sync();
-    if (warp == 5) {
+    if (warp == Cfg::EPI + 1) {
         tc_fence_after();
         gg_tmem_dealloc<CG>(tmem, kGgTmemCols);
     }

@@ -75,10 +75,15 @@ static int launch_persistent(K kernel, const P& p, int threads, int sms, cudaStr
 }
 
 // The paired tile (256 x 256) from this many rows a segment on average, where
-// the output is wider than a single CTA's tile.
+// the output is wider than a single CTA's tile.  Measured on 64 experts of
+// 1536 x 2048 at 96 / 128 / 256 rows, single and paired: forward 76 / 81 / 110
+// and 79 / 81 / 95 us.  A bf16 weight gradient is all stores at few rows, and
+// the pair's larger tiles are always ahead (16 rows: 100 and 88 us).
 constexpr int kGgPairRows = 128;
 
-static bool gg_pairs(int R, int M, int E) { return (int64_t)R >= (int64_t)kGgPairRows * E && M > 128; }
+static bool gg_pairs(int R, int M, int E, bool dw_bf16 = false) {
+    return M > 128 && (dw_bf16 || (int64_t)R >= (int64_t)kGgPairRows * E);
+}
 
 // dw: with fewer tiles than CTAs (or pairs) the segments' rows are cut into
 // parts, of 512 rows on average at least, whose sums are joined afterwards.
@@ -113,8 +118,8 @@ static int run_gg(GgParams& p, const void* a, const void* b, int R, int N, int K
     p.NW = N;
     const int sms = sm_count();
     if (sms < 2) return MOE_ERR_CUDA;
-    return gg_pairs(R, p.M, E) ? launch_persistent<2>(gg_kernel<MODE, 2>, p, gg_threads<MODE>(), sms, st)
-                : launch_persistent<1>(gg_kernel<MODE, 1>, p, gg_threads<MODE>(), sms, st);
+    return gg_pairs(R, p.M, E, MODE == kGgDw && !p.out_f32) ? launch_persistent<2>(gg_kernel<MODE, 2>, p, GgCfg<MODE, 2>::kThreads, sms, st)
+                : launch_persistent<1>(gg_kernel<MODE, 1>, p, GgCfg<MODE, 1>::kThreads, sms, st);
 }
 
 template <bool BF16, int T>
@@ -342,7 +347,7 @@ int moe_grouped_gemm_nvfp4(const uint8_t* xq, const uint8_t* xbs, const float* x
     const int sms = sm_count();
     if (sms < 2) return MOE_ERR_CUDA;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    return (int64_t)R >= (int64_t)kGgPairRows * E ? launch_persistent<2>(g4_kernel<2>, p, kG4Threads, sms, st)
+    return gg_pairs(R, N, E) ? launch_persistent<2>(g4_kernel<2>, p, kG4Threads, sms, st)
                                                   : launch_persistent<1>(g4_kernel<1>, p, kG4Threads, sms, st);
 }
 
