@@ -279,6 +279,11 @@ __device__ __forceinline__ bool gg_wait(uint64_t* bar, uint32_t parity, int* abo
     return false;
 }
 
+// The same for a whole warp, with one answer for its lanes.
+__device__ __forceinline__ bool gg_wait_warp(uint64_t* bar, uint32_t parity, int* abort) {
+    return __all_sync(0xffffffffu, gg_wait(bar, parity, abort));
+}
+
 // A place in a ring of S stages and the parity of its current use: waits and
 // addresses without a division in the single-thread issue loops, whose time a
 // stage would otherwise be bound by.
@@ -634,7 +639,7 @@ __global__ void __launch_bounds__((GgCfg<MODE, CG>::kThreads), 1) gg_kernel(cons
         uint32_t free_ph = 1;  // parity of acc_empty to wait for (at first: nothing)
         uint32_t tails = 0;    // parity of each stage's next use as a segment's end
         const uint32_t ring_at = smem_u32(ring);
-        if (rank == 0) walk([&](int e, int q0, int n, int n0, int m0, int len) -> bool {
+        if (rank == 0 && gg_elect()) walk([&](int e, int q0, int n, int n0, int m0, int len) -> bool {
             const int nk = (len + 63) / 64;
             const int npad = MODE == kGgDw ? Cfg::BN : (n + kGgBoxN * CG - 1) / (kGgBoxN * CG) * (kGgBoxN * CG);
             const uint32_t idesc = umma_idesc_bf16(Cfg::BM, npad) | (MODE != kGgFwd ? 1u << 15 : 0u) |
@@ -662,27 +667,24 @@ __global__ void __launch_bounds__((GgCfg<MODE, CG>::kThreads), 1) gg_kernel(cons
                 room -= Cfg::KSUB;  // (a whole number of stages)
                 const bool last = room == 0 || k0 + Cfg::KSUB >= nk;
                 tc_fence_after();
-                if (gg_elect()) {
-                    const int ke = min(Cfg::KSUB, nk - k0);
+                const int ke = min(Cfg::KSUB, nk - k0);
 #pragma unroll
-                    for (int u = 0; u < Cfg::KSUB; ++u) {
-                        if (u >= ke) break;
-                        // the 16-deep steps of a tile: 32 bytes of a K-major row, 16 rows of an MN-major tile
-                        const uint32_t aa = sta + u * kGgTile, ba = sta + b_off + u * b_tile;
-                        const uint64_t ad = MODE == kGgFwd ? umma_sdesc(aa) : umma_sdesc_mn(aa, 8192);
-                        const uint64_t bd = MODE == kGgDw ? umma_sdesc_mn(ba, 8192) : umma_sdesc(ba);
+                for (int u = 0; u < Cfg::KSUB; ++u) {
+                    if (u >= ke) break;
+                    // the 16-deep steps of a tile: 32 bytes of a K-major row, 16 rows of an MN-major tile
+                    const uint32_t aa = sta + u * kGgTile, ba = sta + b_off + u * b_tile;
+                    const uint64_t ad = MODE == kGgFwd ? umma_sdesc(aa) : umma_sdesc_mn(aa, 8192);
+                    const uint64_t bd = MODE == kGgDw ? umma_sdesc_mn(ba, 8192) : umma_sdesc(ba);
 #pragma unroll
-                        for (int kk = 0; kk < 4; ++kk) {
-                            if (MODE == kGgDw && kk >= steps) break;
-                            gg_mma<CG>(tacc, ad + (uint64_t)(kk * (MODE == kGgFwd ? 32 : 2048) / 16),
-                                       bd + (uint64_t)(kk * (MODE == kGgDw ? 2048 : 32) / 16), idesc,
-                                       u == 0 && kk == 0 ? acc : 1u);
-                        }
+                    for (int kk = 0; kk < 4; ++kk) {
+                        if (MODE == kGgDw && kk >= steps) break;
+                        gg_mma<CG>(tacc, ad + (uint64_t)(kk * (MODE == kGgFwd ? 32 : 2048) / 16),
+                                   bd + (uint64_t)(kk * (MODE == kGgDw ? 2048 : 32) / 16), idesc,
+                                   u == 0 && kk == 0 ? acc : 1u);
                     }
-                    gg_commit<CG>(&sh->empty[r.s]);
-                    if (last) gg_commit<CG>(&sh->acc_full[buf]);
                 }
-                __syncwarp();
+                gg_commit<CG>(&sh->empty[r.s]);
+                if (last) gg_commit<CG>(&sh->acc_full[buf]);
                 acc = 1;
                 if (last) {
                     room = 0;
@@ -693,7 +695,8 @@ __global__ void __launch_bounds__((GgCfg<MODE, CG>::kThreads), 1) gg_kernel(cons
             }
             return true;
         });
-        if (rank == 0 && lane == 0) {
+        __syncwarp();
+        if (rank == 0 && gg_elect()) {
             gg_commit_own<CG>(&sh->mma_done);
             gg_settle(&sh->mma_done, 0u);
         }
@@ -712,7 +715,7 @@ __global__ void __launch_bounds__((GgCfg<MODE, CG>::kThreads), 1) gg_kernel(cons
             for (int k = 0; k + 1 < nk; ++k) r.next(S);
             if (nk > 0) {
                 if (gg_ragged(left)) {
-                    if (!gg_wait(&sh->tfull[r.s], (tails >> r.s) & 1u, &sh->abort)) return false;
+                    if (!gg_wait_warp(&sh->tfull[r.s], (tails >> r.s) & 1u, &sh->abort)) return false;
                     tails ^= 1u << r.s;
                     unsigned char* st = ring + (size_t)r.s * stage_bytes;
                     for (int i = lane; i < (16 - (left & 15)) * 32; i += 32) {
@@ -751,8 +754,7 @@ __global__ void __launch_bounds__((GgCfg<MODE, CG>::kThreads), 1) gg_kernel(cons
                 return true;
             }
             for (int k = 0; k < nk; k += part_steps) {
-                if (!gg_wait(&sh->acc_full[buf], full_ph, &sh->abort)) return false;
-                __syncwarp();
+                if (!gg_wait_warp(&sh->acc_full[buf], full_ph, &sh->abort)) return false;
                 tc_fence_after();
                 auto release = [&]() {
                     tc_fence_before();

@@ -563,7 +563,7 @@ __global__ void __launch_bounds__(kG4Threads, 1) g4_kernel(const __grid_constant
         int buf = 0;
         uint32_t free_ph = 1;
         const uint32_t ring_at = smem_u32(ring);
-        if (rank == 0) walk([&](int e, int q0, int n, int m0) -> bool {
+        if (rank == 0 && gg_elect()) walk([&](int e, int q0, int n, int m0) -> bool {
             const uint32_t idesc = umma_idesc_nvfp4(128 * CG, share(n) * CG);
             if (!gg_wait(&sh->acc_empty[buf], free_ph, &sh->abort)) return false;
             tc_fence_after();
@@ -572,32 +572,29 @@ __global__ void __launch_bounds__(kG4Threads, 1) g4_kernel(const __grid_constant
             for (int k = 0; k < nk; ++k) {
                 if (!gg_wait(&sh->full[r.s], r.ph, &sh->abort)) return false;
                 tc_fence_after();
-                if (gg_elect()) {
-                    const uint32_t st = ring_at + r.s * stage_bytes;
-                    const uint32_t sfa = tmem + kG4SfCol + r.s * (uint32_t)(Cfg::SFA + Cfg::SFB), sfb = sfa + Cfg::SFA;
-                    const int left = p.K - k * 256;
-                    const uint64_t ad = umma_sdesc(st), bd = umma_sdesc(st + kG4A);
+                const uint32_t st = ring_at + r.s * stage_bytes;
+                const uint32_t sfa = tmem + kG4SfCol + r.s * (uint32_t)(Cfg::SFA + Cfg::SFB), sfb = sfa + Cfg::SFA;
+                const int left = p.K - k * 256;
+                const uint64_t ad = umma_sdesc(st), bd = umma_sdesc(st + kG4A);
 #pragma unroll
-                    for (int kk = 0; kk < 4; ++kk) {
-                        if (kk * 64 >= left) break;
-                        umma_nvfp4<CG>(tacc, ad + (uint64_t)(kk * 2), bd + (uint64_t)(kk * 2), idesc,
-                                       sfa + kk * (Cfg::SFA / 4), sfb + kk * (Cfg::SFB / 4), acc);
-                        acc = 1;
-                    }
-                    gg_commit<CG>(&sh->empty[r.s]);
+                for (int kk = 0; kk < 4; ++kk) {
+                    if (kk * 64 >= left) break;
+                    umma_nvfp4<CG>(tacc, ad + (uint64_t)(kk * 2), bd + (uint64_t)(kk * 2), idesc,
+                                   sfa + kk * (Cfg::SFA / 4), sfb + kk * (Cfg::SFB / 4), acc);
+                    acc = 1;
                 }
-                __syncwarp();
+                gg_commit<CG>(&sh->empty[r.s]);
                 r.next(S);
             }
-            if (gg_elect()) gg_commit<CG>(&sh->acc_full[buf]);
-            __syncwarp();
+            gg_commit<CG>(&sh->acc_full[buf]);
             if (++buf == Cfg::ACC) {
                 buf = 0;
                 free_ph ^= 1u;
             }
             return true;
         });
-        if (rank == 0 && lane == 0) {
+        __syncwarp();
+        if (rank == 0 && gg_elect()) {
             gg_commit_own<CG>(&sh->mma_done);
             gg_settle(&sh->mma_done, 0u);
         }
@@ -612,7 +609,7 @@ __global__ void __launch_bounds__(kG4Threads, 1) g4_kernel(const __grid_constant
                 uint4 a[4], b[NB];
                 const int kq = k % kG4SfStages;
                 if (sf_tma) {
-                    if (kq == 0 && !gg_wait(&s4->cfull[c.s], c.ph, &sh->abort)) return false;
+                    if (kq == 0 && !gg_wait_warp(&s4->cfull[c.s], c.ph, &sh->abort)) return false;
                     const unsigned char* sf = sfbuf + c.s * sf_bytes;
                     // 64-byte swizzle: 16-byte chunk kq of row r is at chunk kq ^ ((r >> 1) & 3)
                     const int ch = (kq ^ ((lane >> 1) & 3)) * 16;
@@ -638,8 +635,7 @@ __global__ void __launch_bounds__(kG4Threads, 1) g4_kernel(const __grid_constant
                         b[j] = 32 * j < n ? g4_row_scales(p.xbs + (size_t)(q0 + min(32 * j + lane, n - 1)) * nb, k * 16, nb)
                                           : make_uint4(0, 0, 0, 0);
                 }
-                if (!gg_wait(&sh->empty[r.s], r.ph ^ 1u, &sh->abort)) return false;
-                __syncwarp();
+                if (!gg_wait_warp(&sh->empty[r.s], r.ph ^ 1u, &sh->abort)) return false;
                 tc_fence_after();
                 const uint32_t at = tmem + quarter + kG4SfCol + r.s * (uint32_t)(Cfg::SFA + Cfg::SFB);
                 const uint32_t wa[16] = {a[0].x, a[1].x, a[2].x, a[3].x, a[0].y, a[1].y, a[2].y, a[3].y,
@@ -686,8 +682,7 @@ __global__ void __launch_bounds__(kG4Threads, 1) g4_kernel(const __grid_constant
 #pragma unroll
             for (int i = 0; i < COLS; i += 32) xg[i + lane] = i + lane < mine ? __ldg(p.xgs + q0 + c0 + i + lane) : 0.0f;
             __syncwarp();
-            if (!gg_wait(&sh->acc_full[buf], full_ph, &sh->abort)) return false;
-            __syncwarp();
+            if (!gg_wait_warp(&sh->acc_full[buf], full_ph, &sh->abort)) return false;
             tc_fence_after();
             const uint32_t taddr = tmem + (uint32_t)(buf * Cfg::BN + c0) + ((uint32_t)((warp & 3) * 32) << 16);
             auto release = [&]() {

@@ -153,6 +153,32 @@ def test_experts_without_rows_get_zero_gradients(cuda_lib):
 
 
 @pytest.mark.parametrize("rows", [6, 60, 600])
+@pytest.mark.parametrize("op", ["fwd", "dx"])
+def test_rows_without_any_segment(cuda_lib, op, rows):
+    _, x, w, dy = _case([rows, 0, 0], 40, 72)
+    out = torch.full((rows, 40 if op == "fwd" else 72), -7.0, device=DEV)
+    st = cuda_lib.new_status()
+    _call(cuda_lib, op, torch.full((4,), 5, dtype=torch.int32, device=DEV), x, w, dy, out=out, status=st)
+    assert bool((out == -7).all()) and int(st.item()) == 0
+
+
+def test_two_streams_at_once(cuda_lib):
+    """Calls of every kind in flight together: none shares state with another."""
+    cases = [_case(c, 264, 200, seed=i) for i, c in enumerate(([3, 1], [30, 50, 0, 11], [400, 0, 250], [9000]))]
+    want = [[_call(cuda_lib, op, *c) for op in ("fwd", "dx", "dw")] for c in cases]
+    streams = [torch.cuda.Stream() for _ in cases]
+    torch.cuda.synchronize()
+    got = [[] for _ in cases]
+    for _ in range(3):
+        for i, (c, s) in enumerate(zip(cases, streams)):
+            got[i] = [_call(cuda_lib, op, *c, stream=s) for op in ("fwd", "dx", "dw")]
+    torch.cuda.synchronize()
+    for g, w in zip(got, want):
+        for a, b in zip(g, w):
+            assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("rows", [6, 60, 600])
 @pytest.mark.parametrize("offsets", [[0, 4, 2, 6], [-1, 2, 3, 6], [0, 2, 3, 7], [0, 2 ** 31 - 1, 2, 6]])
 @pytest.mark.parametrize("op", ["fwd", "dx", "dw"])
 def test_bad_offsets_leave_their_segment_out(cuda_lib, op, offsets, rows):

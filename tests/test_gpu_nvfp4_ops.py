@@ -203,6 +203,9 @@ def test_product_edges(cuda_lib, counts):
     st = cuda_lib.new_status()
     cuda_lib.grouped_gemm_nvfp4(*xq, *wq, bad, out=out, status=st)
     assert int(st.item()) == cuda_lib.MOE_DEV_BAD_OFFSETS
+    out.fill_(-7.0)
+    cuda_lib.grouped_gemm_nvfp4(*xq, *wq, torch.full_like(off, 2), out=out)  # no segment holds a row
+    assert bool((out == -7).all())
     assert cuda_lib.grouped_gemm_nvfp4(*(t[:0] for t in xq), *wq, torch.zeros_like(off)).shape == (0, 72)
 
 
