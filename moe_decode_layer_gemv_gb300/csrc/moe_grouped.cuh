@@ -83,7 +83,7 @@ struct GgShared {
     int abort;                      // a bounded wait ran out
     int nmax;                       // rows of the largest segment
     int p0[MOE_MAX_E], cnt[MOE_MAX_E];
-    int start[MOE_MAX_E + 1];       // first tile of each segment (forward, dx)
+    int start[MOE_MAX_E + 1];       // tiles of rows before each segment (forward, dx)
 };
 static_assert(sizeof(GgShared) <= 4096, "control block");
 
@@ -298,7 +298,31 @@ struct GgRing {
     }
 };
 
-// The segment of tile `it`, which is not before segment e.
+// Tiles unit, unit + units, ... as (outer, inner) with inner < n, without a
+// division a tile.
+struct GgWalk {
+    int outer, inner, d_outer, d_inner, n;
+    __device__ __forceinline__ GgWalk(int unit, int units, int n_) : n(n_) {
+        outer = unit / n;
+        inner = unit - outer * n;
+        d_outer = units / n;
+        d_inner = units - d_outer * n;
+    }
+    __device__ __forceinline__ void next() {
+        outer += d_outer;
+        inner += d_inner;
+        if (inner >= n) {
+            inner -= n;
+            ++outer;
+        }
+    }
+};
+
+__device__ __forceinline__ void prefetch_map(const CUtensorMap* map) {
+    asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(map)) : "memory");
+}
+
+// The segment of row tile `it`, which is not before segment e.
 __device__ __forceinline__ int gg_seek(const int* start, int E, int it, int e) {
     if (it < start[e + 1]) return e;
     int lo = e + 1, hi = E - 1;  // the last segment with start <= it
@@ -339,8 +363,8 @@ __device__ __forceinline__ bool gg_ragged(int left) { return left < 64 && (left 
 // ------------------------------------------------------------- segments
 // The segments into shared memory.  Offsets outside [0, R] or descending
 // leave their segment out (and set MOE_DEV_BAD_OFFSETS): nothing is read or
-// written outside the tensors.  start[e] = tiles of the segments before e.
-__device__ __forceinline__ void gg_segments(GgShared* sh, const int32_t* offsets, int E, int R, int bn, int mt,
+// written outside the tensors.  start[e] = tiles of bn rows before segment e.
+__device__ __forceinline__ void gg_segments(GgShared* sh, const int32_t* offsets, int E, int R, int bn,
                                             int32_t* status) {
     const int tid = threadIdx.x;
     if (tid == 0) sh->nmax = 0;
@@ -360,7 +384,7 @@ __device__ __forceinline__ void gg_segments(GgShared* sh, const int32_t* offsets
         for (int j = 0; j < MOE_MAX_E / 32; ++j) {
             const int e = tid * (MOE_MAX_E / 32) + j;
             c[j] = sum;
-            sum += e < E ? (sh->cnt[e] + bn - 1) / bn * mt : 0;
+            sum += e < E ? (sh->cnt[e] + bn - 1) / bn : 0;
         }
         int run = sum;
 #pragma unroll
@@ -513,11 +537,14 @@ __global__ void __launch_bounds__((GgCfg<MODE, CG>::kThreads), 1) gg_kernel(cons
         mbar_init(&sh->mma_done, 1);
         sh->abort = 0;
         fence_mbar_init();
+        prefetch_map(&p.ta);
+        prefetch_map(&p.tb);
+        if (MODE != kGgDw) prefetch_map(&p.tb_all);
     }
     if (warp == Cfg::EPI + 1) gg_tmem_alloc<CG>(&sh->tmem_slot, kGgTmemCols);
     grid_dep_wait();
     const int mtiles = (p.M + Cfg::BM - 1) / Cfg::BM;
-    gg_segments(sh, p.offsets, p.E, p.R, Cfg::BN, mtiles, p.status);
+    gg_segments(sh, p.offsets, p.E, p.R, Cfg::BN, p.status);
     tc_fence_before();
     __syncthreads();
     if (CG == 2) cluster_sync();
@@ -535,31 +562,33 @@ __global__ void __launch_bounds__((GgCfg<MODE, CG>::kThreads), 1) gg_kernel(cons
     const uint32_t S = min((uint32_t)kGgMaxStages, ((uint32_t)kGgSmem - 1023u - 4096u) / stage_bytes);
 
     const int ntiles_w = (p.NW + Cfg::BN - 1) / Cfg::BN;  // dw
-    const int items = MODE == kGgDw ? p.split * p.E * mtiles * ntiles_w : sh->start[p.E];
+    const int outers = MODE == kGgDw ? p.split * p.E : sh->start[p.E];
 
     // f(e, q0, n, n0, m0, len): segment e; first row q0 (forward, dx: of the
     // tile; dw: of the segment's part); n valid columns from n0 on; m from m0
     // on; contraction length.  (dw: e counts part after part, part * E + e)
     auto walk = [&](auto f) {
         int e = 0;
-        for (int it = unit; it < items; it += units) {
+        for (GgWalk w(unit, units, MODE == kGgDw ? mtiles * ntiles_w : mtiles); w.outer < outers; w.next()) {
             int q0, n, n0, m0, len;
             if (MODE == kGgDw) {
-                const int per = mtiles * ntiles_w;
-                e = it / per;
-                const int t = it - e * per;
-                m0 = (t % mtiles) * Cfg::BM;
-                n0 = (t / mtiles) * Cfg::BN;
+                e = w.outer;
+                const int tn = w.inner / mtiles;
+                m0 = (w.inner - tn * mtiles) * Cfg::BM;
+                n0 = tn * Cfg::BN;
                 n = min(Cfg::BN, p.NW - n0);
-                const int seg = e % p.E, cnt = sh->cnt[seg];
-                const int part = ((cnt + p.split - 1) / p.split + 63) / 64 * 64, at = min(cnt, e / p.E * part);
+                const int seg = p.split == 1 ? e : e % p.E, cnt = sh->cnt[seg];
+                int part = cnt, at = 0;
+                if (p.split > 1) {
+                    part = ((cnt + p.split - 1) / p.split + 63) / 64 * 64;
+                    at = min(cnt, e / p.E * part);
+                }
                 q0 = sh->p0[seg] + at;
                 len = min(part, cnt - at);
             } else {
-                e = gg_seek(sh->start, p.E, it, e);
-                const int t = it - sh->start[e];
-                m0 = (t % mtiles) * Cfg::BM;
-                n0 = (t / mtiles) * Cfg::BN;
+                e = gg_seek(sh->start, p.E, w.outer, e);
+                m0 = w.inner * Cfg::BM;
+                n0 = (w.outer - sh->start[e]) * Cfg::BN;
                 n = min(Cfg::BN, sh->cnt[e] - n0);
                 q0 = sh->p0[e] + n0;
                 len = p.C;

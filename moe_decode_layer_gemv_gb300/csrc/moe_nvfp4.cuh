@@ -485,11 +485,18 @@ __global__ void __launch_bounds__(kG4Threads, 1) g4_kernel(const __grid_constant
         mbar_init(&sh->mma_done, 1);
         sh->abort = 0;
         fence_mbar_init();
+        prefetch_map(&p.ta);
+        prefetch_map(&p.tb);
+        prefetch_map(&p.tb_all);
+        if ((p.K & 255) == 0) {
+            prefetch_map(&p.tsa);
+            prefetch_map(&p.tsb);
+        }
     }
     if (warp == 9) gg_tmem_alloc<CG>(&sh->tmem_slot, kGgTmemCols);
     grid_dep_wait();
     const int mtiles = (p.M + 128 * CG - 1) / (128 * CG);
-    gg_segments(sh, p.offsets, p.E, p.R, Cfg::BN, mtiles, p.status);
+    gg_segments(sh, p.offsets, p.E, p.R, Cfg::BN, p.status);
     tc_fence_before();
     __syncthreads();
     if (CG == 2) cluster_sync();
@@ -511,10 +518,10 @@ __global__ void __launch_bounds__(kG4Threads, 1) g4_kernel(const __grid_constant
 
     auto walk = [&](auto f) {
         int e = 0;
-        for (int it = unit; it < sh->start[p.E]; it += units) {
-            e = gg_seek(sh->start, p.E, it, e);
-            const int t = it - sh->start[e];
-            const int m0 = (t % mtiles) * 128 * CG + (int)rank * 128, n0 = (t / mtiles) * Cfg::BN;
+        const int rows = sh->start[p.E];
+        for (GgWalk w(unit, units, mtiles); w.outer < rows; w.next()) {
+            e = gg_seek(sh->start, p.E, w.outer, e);
+            const int m0 = w.inner * 128 * CG + (int)rank * 128, n0 = (w.outer - sh->start[e]) * Cfg::BN;
             if (!f(e, sh->p0[e] + n0, min(Cfg::BN, sh->cnt[e] - n0), m0)) break;
         }
     };
@@ -604,29 +611,66 @@ __global__ void __launch_bounds__(kG4Threads, 1) g4_kernel(const __grid_constant
         GgRing r, c;
         const uint32_t quarter = (uint32_t)((warp & 3) * 32) << 16;
         constexpr int NB = Cfg::BN / 32;
-        walk([&](int e, int q0, int n, int m0) -> bool {
-            for (int k = 0; k < nk; ++k) {
-                uint4 a[4], b[NB];
-                const int kq = k % kG4SfStages;
-                if (sf_tma) {
-                    if (kq == 0 && !gg_wait_warp(&s4->cfull[c.s], c.ph, &sh->abort)) return false;
-                    const unsigned char* sf = sfbuf + c.s * sf_bytes;
-                    // 64-byte swizzle: 16-byte chunk kq of row r is at chunk kq ^ ((r >> 1) & 3)
-                    const int ch = (kq ^ ((lane >> 1) & 3)) * 16;
+        // one stage's words: rows 32 j + lane of the weights (a) and of the tile (b)
+        auto put = [&](const uint4(&a)[4], const uint4(&b)[NB]) -> bool {
+            if (!gg_wait_warp(&sh->empty[r.s], r.ph ^ 1u, &sh->abort)) return false;
+            tc_fence_after();
+            const uint32_t at = tmem + quarter + kG4SfCol + r.s * (uint32_t)(Cfg::SFA + Cfg::SFB);
+            const uint32_t wa[16] = {a[0].x, a[1].x, a[2].x, a[3].x, a[0].y, a[1].y, a[2].y, a[3].y,
+                                     a[0].z, a[1].z, a[2].z, a[3].z, a[0].w, a[1].w, a[2].w, a[3].w};
+            tmem_st16(at, wa);
+            uint32_t wb[4 * NB];
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) a[j] = *reinterpret_cast<const uint4*>(sf + (32 * j + lane) * 64 + ch);
+            for (int j = 0; j < NB; ++j) {
+                wb[j] = b[j].x;
+                wb[NB + j] = b[j].y;
+                wb[2 * NB + j] = b[j].z;
+                wb[3 * NB + j] = b[j].w;
+            }
+#pragma unroll
+            for (int j = 0; j < 4 * NB; j += 16)
+                tmem_st16(at + Cfg::SFA + j, *reinterpret_cast<const uint32_t(*)[16]>(wb + j));
+            asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) {
+                if (CG == 1)
+                    mbar_arrive(&sh->full[r.s]);
+                else
+                    mbar_arrive_cluster(&sh->full[r.s], 0);
+            }
+            r.next(S);
+            return true;
+        };
+        if (sf_tma) {
+            const unsigned char* sf0 = sfbuf + lane * 64;
+            walk([&](int e, int q0, int n, int m0) -> bool {
+                for (int k = 0; k < nk; ++k) {
+                    const int kq = k % kG4SfStages;
+                    if (kq == 0 && !gg_wait_warp(&s4->cfull[c.s], c.ph, &sh->abort)) return false;
+                    // 64-byte swizzle: 16-byte chunk kq of row r is at chunk kq ^ ((r >> 1) & 3)
+                    const unsigned char* sf = sf0 + c.s * sf_bytes + (kq ^ ((lane >> 1) & 3)) * 16;
+                    uint4 a[4], b[NB];
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) a[j] = *reinterpret_cast<const uint4*>(sf + j * 2048);
 #pragma unroll
                     for (int j = 0; j < NB; ++j)
-                        b[j] = 32 * j < n ? *reinterpret_cast<const uint4*>(sf + 8192 + (32 * j + lane) * 64 + ch)
-                                          : make_uint4(0, 0, 0, 0);
+                        b[j] = 32 * j < n ? *reinterpret_cast<const uint4*>(sf + 8192 + j * 2048) : make_uint4(0, 0, 0, 0);
                     if (kq == kG4SfStages - 1 || k == nk - 1) {
                         __syncwarp();
                         if (lane == 0) mbar_arrive(&s4->cempty[c.s]);
                         c.next(2);
                     }
-                } else {
+                    if (!put(a, b)) return false;
+                }
+                return true;
+            });
+        } else {
+            walk([&](int e, int q0, int n, int m0) -> bool {
+                for (int k = 0; k < nk; ++k) {
                     // rows beyond the tile's end take the last one's scales:
                     // what they scale is zero or never stored
+                    uint4 a[4], b[NB];
 #pragma unroll
                     for (int j = 0; j < 4; ++j)
                         a[j] = g4_row_scales(p.wbs + ((size_t)e * p.M + min(m0 + 32 * j + lane, p.M - 1)) * nb, k * 16, nb);
@@ -634,37 +678,11 @@ __global__ void __launch_bounds__(kG4Threads, 1) g4_kernel(const __grid_constant
                     for (int j = 0; j < NB; ++j)
                         b[j] = 32 * j < n ? g4_row_scales(p.xbs + (size_t)(q0 + min(32 * j + lane, n - 1)) * nb, k * 16, nb)
                                           : make_uint4(0, 0, 0, 0);
+                    if (!put(a, b)) return false;
                 }
-                if (!gg_wait_warp(&sh->empty[r.s], r.ph ^ 1u, &sh->abort)) return false;
-                tc_fence_after();
-                const uint32_t at = tmem + quarter + kG4SfCol + r.s * (uint32_t)(Cfg::SFA + Cfg::SFB);
-                const uint32_t wa[16] = {a[0].x, a[1].x, a[2].x, a[3].x, a[0].y, a[1].y, a[2].y, a[3].y,
-                                         a[0].z, a[1].z, a[2].z, a[3].z, a[0].w, a[1].w, a[2].w, a[3].w};
-                tmem_st16(at, wa);
-                uint32_t wb[4 * NB];
-#pragma unroll
-                for (int j = 0; j < NB; ++j) {
-                    wb[j] = b[j].x;
-                    wb[NB + j] = b[j].y;
-                    wb[2 * NB + j] = b[j].z;
-                    wb[3 * NB + j] = b[j].w;
-                }
-#pragma unroll
-                for (int j = 0; j < 4 * NB; j += 16)
-                    tmem_st16(at + Cfg::SFA + j, *reinterpret_cast<const uint32_t(*)[16]>(wb + j));
-                asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) {
-                    if (CG == 1)
-                        mbar_arrive(&sh->full[r.s]);
-                    else
-                        mbar_arrive_cluster(&sh->full[r.s], 0);
-                }
-                r.next(S);
-            }
-            return true;
-        });
+                return true;
+            });
+        }
         __syncwarp();
     } else {
         // ---------------- epilogue: lane quarter warp & 3, half of the columns
@@ -674,8 +692,7 @@ __global__ void __launch_bounds__(kG4Threads, 1) g4_kernel(const __grid_constant
         const int c0 = (warp >> 2) * COLS;
         float* xg = s4->xg[warp];  // this warp's columns' scales
         walk([&](int e, int q0, int n, int m0) -> bool {
-            const int m = m0 + (warp & 3) * 32 + lane, odd = m & 1;
-            const uint32_t sel = gg_pair_select(odd);
+            const int m = m0 + (warp & 3) * 32 + lane;
             const int mine = min(COLS, n - c0);  // columns of this warp; none below 1
             const float wg = __ldg(p.wgs + e);
             __syncwarp();
@@ -707,7 +724,7 @@ __global__ void __launch_bounds__(kG4Threads, 1) g4_kernel(const __grid_constant
             };
             if (mine <= 0) {
                 release();
-            } else if (p.out_f32) {
+            } else if (p.out_f32 || mine < COLS) {
 #pragma unroll 1
                 for (int c = 0; c < mine; c += 32) {
                     uint32_t v[32];
@@ -715,35 +732,35 @@ __global__ void __launch_bounds__(kG4Threads, 1) g4_kernel(const __grid_constant
                     gg_ld_wait(v);
                     if (c + 32 >= mine) release();
                     scaled(v, c);
-                    gg_store32(v, p.out, 1, (size_t)q0 + c0 + c, min(32, mine - c), m, p.M);
+                    gg_store32(v, p.out, p.out_f32, (size_t)q0 + c0 + c, min(32, mine - c), m, p.M);
                 }
             } else {
-                // everything into registers as bf16, then the release, then the stores
-                uint32_t h[COLS / 32][16];
+                // everything into registers, all but the last 32 columns as
+                // bf16; then the release, then the stores
+                uint32_t h[COLS / 32 - 1][16], v[32];
 #pragma unroll
-                for (int i = 0; i < COLS / 32; ++i) {
-                    if (32 * i >= mine) break;
-                    uint32_t v[32];
+                for (int i = 0; i < COLS / 32 - 1; ++i) {
                     gg_ld32(taddr + 32 * i, v);
                     gg_ld_wait(v);
-                    if (32 * i + 32 >= mine) release();
                     scaled(v, 32 * i);
 #pragma unroll
                     for (int j = 0; j < 16; ++j) h[i][j] = gg_pack(v[2 * j], v[2 * j + 1]);
                 }
+                gg_ld32(taddr + COLS - 32, v);
+                gg_ld_wait(v);
+                release();
+                const int odd = m & 1;
+                const uint32_t sel = gg_pair_select(odd);
+                const bool live = m < p.M;
                 uint32_t* o = reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(p.out) +
                                                           ((size_t)q0 + c0 + odd) * (size_t)p.M + (m - odd));
-                const int last = m < p.M ? mine - odd : 0;  // rows q0 + c0 + odd + 2 j, 2 j < last
-                if (__all_sync(0xffffffffu, mine == COLS && m < p.M)) {
 #pragma unroll
-                    for (int j = 0; j < COLS / 2; ++j, o += p.M) *o = gg_pair(h[j / 16][j % 16], sel);
-                } else {
-#pragma unroll
-                    for (int j = 0; j < COLS / 2; ++j, o += p.M) {
-                        const uint32_t v = gg_pair(h[j / 16][j % 16], sel);
-                        if (2 * j < last) *o = v;
-                    }
+                for (int j = 0; j < COLS / 2 - 16; ++j, o += p.M) {
+                    const uint32_t w = gg_pair(h[j / 16][j % 16], sel);
+                    if (live) *o = w;
                 }
+                scaled(v, COLS - 32);
+                gg_store32(v, p.out, 0, (size_t)q0 + c0 + COLS - 32, 32, m, p.M);
             }
             if (++buf == Cfg::ACC) {
                 buf = 0;
