@@ -835,18 +835,17 @@ __global__ void __launch_bounds__(256) gg_join_kernel(const float4* __restrict__
 }
 
 // ------------------------------------------------------- a few rows at once
-// Forward product for a handful of rows: a warp per weight row, up to
-// kGgvTok rows of one segment at a time.  Block (i, r) takes 8 weight rows
+// Forward product for a handful of rows: a warp per weight row (256 J elements
+// of it in flight at a time), up to kGgvTok rows of one segment at a time.
+// Two rows of 1536 x 2048, weights from HBM: 4.3 us, the tiles above 9.8.  Block (i, r) takes 8 weight rows
 // for the rows r .. of a segment when r starts a group of kGgvTok there.
 constexpr int kGgvTok = 4;
 
-__global__ void __launch_bounds__(256) gg_gemv_kernel(const uint16_t* __restrict__ x, const uint16_t* __restrict__ w,
-                                                      const int32_t* __restrict__ offsets, int R, int N, int K, int E,
-                                                      void* y, int out_f32, int32_t* status) {
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    grid_dep_wait();
-    const int r = blockIdx.y;
-    // the segment of row r: E <= blockDim.x, a thread per segment
+// The segment of row r, found by the whole block (a thread per segment:
+// E <= blockDim.x), and its rows p0 .. p1 - 1; -1 where no segment holds r.
+__device__ __forceinline__ int gg_row_segment(const int32_t* offsets, int E, int R, int r, int& p0, int& p1,
+                                              int32_t* status) {
+    __shared__ int s_e, s_p0, s_p1;
     bool mine = false, bad = false;
     int a = 0, b = 0;
     if ((int)threadIdx.x < E) {
@@ -855,7 +854,6 @@ __global__ void __launch_bounds__(256) gg_gemv_kernel(const uint16_t* __restrict
         bad = a < 0 || b < a || b > R;
         mine = !bad && a <= r && r < b;
     }
-    __shared__ int s_e, s_p0, s_p1;
     if (threadIdx.x == 0) s_e = -1;
     __syncthreads();
     if (bad && blockIdx.x == 0 && r == 0) set_status(status, MOE_DEV_BAD_OFFSETS);
@@ -865,31 +863,52 @@ __global__ void __launch_bounds__(256) gg_gemv_kernel(const uint16_t* __restrict
         s_p1 = b;
     }
     __syncthreads();
-    const int e = s_e;
-    if (e < 0 || (r - s_p0) % kGgvTok) return;
-    const int nt = min(kGgvTok, s_p1 - r);
+    p0 = s_p0;
+    p1 = s_p1;
+    return s_e;
+}
+
+template <int J>
+__global__ void __launch_bounds__(256) gg_gemv_kernel(const uint16_t* __restrict__ x, const uint16_t* __restrict__ w,
+                                                      const int32_t* __restrict__ offsets, int R, int N, int K, int E,
+                                                      void* y, int out_f32, int32_t* status) {
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    grid_dep_wait();
+    const int r = blockIdx.y;
+    int p0, p1;
+    const int e = gg_row_segment(offsets, E, R, r, p0, p1, status);
+    if (e < 0 || (r - p0) % kGgvTok) return;
+    const int nt = min(kGgvTok, p1 - r);
     const int n = blockIdx.x * 8 + warp;
     if (n >= N) return;
     const uint16_t* wr = w + ((size_t)e * N + n) * K;
     const uint16_t* xr = x + (size_t)r * K;
     float acc[kGgvTok] = {};
     const int chunks = K / 8;
-    for (int c0 = 0; c0 < chunks; c0 += 32 * 8) {
-        uint4 wv[8];
+    for (int c0 = 0; c0 < chunks; c0 += 32 * J) {
+        const int nj = min(J, (chunks - c0 + 31) / 32);
+        uint4 wv[J];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
+        for (int j = 0; j < J; ++j) {
+            if (j >= nj) break;
             const int c = c0 + j * 32 + lane;
             wv[j] = c < chunks ? ld_weight_v4(wr + (size_t)c * 8) : make_uint4(0, 0, 0, 0);
         }
 #pragma unroll
         for (int t = 0; t < kGgvTok; ++t) {
             if (t >= nt) break;
+            uint4 xv[J];  // the first row's are on their way with the weights
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
+            for (int j = 0; j < J; ++j) {
+                if (j >= nj) break;
                 const int c = c0 + j * 32 + lane;
-                if (c >= chunks) break;
-                const uint4 xv = __ldg(reinterpret_cast<const uint4*>(xr + (size_t)t * K + (size_t)c * 8));
-                const uint32_t ws[4] = {wv[j].x, wv[j].y, wv[j].z, wv[j].w}, xs[4] = {xv.x, xv.y, xv.z, xv.w};
+                xv[j] = c < chunks ? __ldg(reinterpret_cast<const uint4*>(xr + (size_t)t * K + (size_t)c * 8))
+                                   : make_uint4(0, 0, 0, 0);
+            }
+#pragma unroll
+            for (int j = 0; j < J; ++j) {
+                if (j >= nj) break;
+                const uint32_t ws[4] = {wv[j].x, wv[j].y, wv[j].z, wv[j].w}, xs[4] = {xv[j].x, xv[j].y, xv[j].z, xv[j].w};
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     const float2 wf = bf16x2_to_f2(ws[i]), xf = bf16x2_to_f2(xs[i]);

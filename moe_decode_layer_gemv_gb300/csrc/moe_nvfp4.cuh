@@ -778,4 +778,112 @@ __global__ void __launch_bounds__(kG4Threads, 1) g4_kernel(const __grid_constant
     }
 }
 
+// ------------------------------------------------------- a few rows at once
+// The NVFP4 product for a handful of rows, a warp per weight row as in
+// gg_gemv_kernel: 32 elements (16 bytes of codes, two block scales) a lane at
+// a time.  A block's products are summed in f16 pairs without rounding: eight
+// products of E2M1 values a lane half, multiples of 1/4 up to 288; the scales'
+// product is exact in fp32.
+constexpr int kG4vRows = 2;  // weight rows a warp: a decoded piece of x serves them all
+
+__device__ __forceinline__ __half2 g4_half2(uint32_t codes, int byte) {
+    const __half2_raw h = __nv_cvt_fp4x2_to_halfraw2((__nv_fp4x2_storage_t)((codes >> (8 * byte)) & 0xffu), __NV_E2M1);
+    return *reinterpret_cast<const __half2*>(&h);
+}
+
+// sum over a block: 16 codes of w, x decoded
+__device__ __forceinline__ float g4_block(uint32_t w0, uint32_t w1, const __half2* x) {
+    __half2 s = __hmul2(g4_half2(w0, 0), x[0]);
+#pragma unroll
+    for (int i = 1; i < 4; ++i) s = __hfma2(g4_half2(w0, i), x[i], s);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) s = __hfma2(g4_half2(w1, i), x[4 + i], s);
+    const float2 f = __half22float2(s);
+    return f.x + f.y;
+}
+
+template <int J>
+__global__ void __launch_bounds__(256) g4_gemv_kernel(const uint8_t* __restrict__ xq, const uint8_t* __restrict__ xbs,
+                                                      const float* __restrict__ xgs, const uint8_t* __restrict__ wq,
+                                                      const uint8_t* __restrict__ wbs, const float* __restrict__ wgs,
+                                                      const int32_t* __restrict__ offsets, int R, int N, int K, int E,
+                                                      void* y, int out_f32, int32_t* status) {
+    constexpr int RW = kG4vRows;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    grid_dep_wait();
+    const int r = blockIdx.y;
+    int p0, p1;
+    const int e = gg_row_segment(offsets, E, R, r, p0, p1, status);
+    if (e < 0 || (r - p0) % kGgvTok) return;
+    const int nt = min(kGgvTok, p1 - r);
+    const int n = (blockIdx.x * 8 + warp) * RW;  // N is a multiple of RW
+    if (n >= N) return;
+    const int chunks = K / 32;  // 16 bytes of codes, 2 bytes of scales each
+    const size_t wrow = ((size_t)e * N + n) * chunks, xrow = (size_t)r * chunks;
+    float acc[kGgvTok][RW] = {};
+    for (int c0 = 0; c0 < chunks; c0 += 32 * J) {
+        uint4 wv[J][RW];
+        uint32_t ws[J][RW];
+#pragma unroll
+        for (int j = 0; j < J; ++j) {
+            const int c = c0 + j * 32 + lane;
+#pragma unroll
+            for (int i = 0; i < RW; ++i) {
+                const size_t at = wrow + (size_t)i * chunks + c;
+                wv[j][i] = c < chunks ? ld_weight_v4(wq + at * 16) : make_uint4(0, 0, 0, 0);
+                ws[j][i] = c < chunks ? __ldg(reinterpret_cast<const uint16_t*>(wbs) + at) : 0;
+            }
+        }
+#pragma unroll
+        for (int t = 0; t < kGgvTok; ++t) {
+            if (t >= nt) break;
+            uint4 xv[J];
+            uint32_t xs[J];
+#pragma unroll
+            for (int j = 0; j < J; ++j) {
+                const int c = c0 + j * 32 + lane;
+                const size_t at = xrow + (size_t)t * chunks + c;
+                xv[j] = c < chunks ? __ldg(reinterpret_cast<const uint4*>(xq) + at) : make_uint4(0, 0, 0, 0);
+                xs[j] = c < chunks ? __ldg(reinterpret_cast<const uint16_t*>(xbs) + at) : 0;
+            }
+#pragma unroll
+            for (int j = 0; j < J; ++j) {
+                __half2 h[16];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    h[i] = g4_half2(xv[j].x, i);
+                    h[4 + i] = g4_half2(xv[j].y, i);
+                    h[8 + i] = g4_half2(xv[j].z, i);
+                    h[12 + i] = g4_half2(xv[j].w, i);
+                }
+                // the scales as unsigned E4M3, like the tensor cores
+                const float2 sx = f8x2_to_f2(xs[j] & 0x7f7fu);
+#pragma unroll
+                for (int i = 0; i < RW; ++i) {
+                    const float2 sw = f8x2_to_f2(ws[j][i] & 0x7f7fu);
+                    acc[t][i] = fmaf(g4_block(wv[j][i].x, wv[j][i].y, h), sw.x * sx.x, acc[t][i]);
+                    acc[t][i] = fmaf(g4_block(wv[j][i].z, wv[j][i].w, h + 8), sw.y * sx.y, acc[t][i]);
+                }
+            }
+        }
+    }
+    const float wg = __ldg(wgs + e);
+#pragma unroll
+    for (int t = 0; t < kGgvTok; ++t) {
+        if (t >= nt) break;
+        const float xg = __ldg(xgs + r + t);
+#pragma unroll
+        for (int i = 0; i < RW; ++i) {
+            const float v = warp_sum(acc[t][i]) * xg * wg;
+            if (lane == 0) {
+                const size_t at = (size_t)(r + t) * N + n + i;
+                if (out_f32)
+                    static_cast<float*>(y)[at] = v;
+                else
+                    static_cast<uint16_t*>(y)[at] = f2bf_bits(v);
+            }
+        }
+    }
+}
+
 }  // namespace moe

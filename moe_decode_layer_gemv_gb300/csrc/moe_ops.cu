@@ -181,11 +181,15 @@ int moe_grouped_gemm(const uint16_t* x, const uint16_t* w, const int32_t* offset
     MOE_OPT(dev_status);
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     const int sms = sm_count();
-    // fewer tiles than SMs: the weights of a few rows stream faster through
-    // a warp per weight row on the whole GPU
-    if (R <= 32 && R * ceil_div(N, 128) < sms)
-        return launch_pdl(gg_gemv_kernel, dim3((unsigned)ceil_div(N, 8), (unsigned)R), 256, 0, st, x, w, offsets, R, N,
-                          K, E, y, (int)(y_dtype == MOE_DT_F32), dev_status);
+    // fewer tiles than SMs: a few rows' weights stream faster through a warp
+    // per weight row on the whole GPU (1536 x 2048, a row an expert: 4 rows 7.1
+    // and 10.1 us, 12 rows 15 and 16; beyond, the tiles are ahead)
+    if (R <= 32 && R * ceil_div(N, 128) < sms) {
+        const dim3 grid((unsigned)ceil_div(N, 8), (unsigned)R);
+        const int f32 = y_dtype == MOE_DT_F32;
+        return K <= 1024 ? launch_pdl(gg_gemv_kernel<4>, grid, 256, 0, st, x, w, offsets, R, N, K, E, y, f32, dev_status)
+                         : launch_pdl(gg_gemv_kernel<8>, grid, 256, 0, st, x, w, offsets, R, N, K, E, y, f32, dev_status);
+    }
     GgParams p;
     memset(&p, 0, sizeof p);
     p.offsets = offsets;
@@ -324,6 +328,20 @@ int moe_grouped_gemm_nvfp4(const uint8_t* xq, const uint8_t* xbs, const float* x
     MOE_REQ(offsets);
     MOE_REQ(y);
     MOE_OPT(dev_status);
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    const int sms = sm_count();
+    if (sms < 2) return MOE_ERR_CUDA;
+    // a few rows: as in moe_grouped_gemm, but the codes cost more instructions
+    // than bf16 weights a byte, so the tiles are ahead earlier (1536 x 2048, a
+    // row an expert: 2 rows 3.1 and 6.7 us, 8 rows 6.9 and 7.3, 12 rows 9.4 and 7.7)
+    if (R <= 32 && 3 * R * ceil_div(N, 128) < 2 * sms) {
+        const dim3 grid((unsigned)ceil_div(N, 8 * kG4vRows), (unsigned)R);
+        const int f32 = y_dtype == MOE_DT_F32;
+        return K <= 1024 ? launch_pdl(g4_gemv_kernel<1>, grid, 256, 0, st, xq, xbs, xgs, wq, wbs, wgs, offsets, R, N, K, E,
+                                      y, f32, dev_status)
+                         : launch_pdl(g4_gemv_kernel<2>, grid, 256, 0, st, xq, xbs, xgs, wq, wbs, wgs, offsets, R, N, K, E,
+                                      y, f32, dev_status);
+    }
     G4Params p;
     memset(&p, 0, sizeof p);
     if (!encode_map(&p.ta, wq, 1, K / 2, N, E, 128) || !encode_map(&p.tb, xq, 1, K / 2, R, 0, kGgBoxN) ||
@@ -344,9 +362,6 @@ int moe_grouped_gemm_nvfp4(const uint8_t* xq, const uint8_t* xbs, const float* x
     p.out = y;
     p.out_f32 = y_dtype == MOE_DT_F32;
     p.status = dev_status;
-    const int sms = sm_count();
-    if (sms < 2) return MOE_ERR_CUDA;
-    cudaStream_t st = static_cast<cudaStream_t>(stream);
     return gg_pairs(R, N, E) ? launch_persistent<2>(g4_kernel<2>, p, kG4Threads, sms, st)
                                                   : launch_persistent<1>(g4_kernel<1>, p, kG4Threads, sms, st);
 }
