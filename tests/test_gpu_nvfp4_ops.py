@@ -263,3 +263,35 @@ def test_quantised_weights_run_in_the_stack_and_in_the_product(cuda_lib):
     # a code is off by at most a quarter of its magnitude (half a step of 0.5
     # at 1.0 is the coarsest); two quantised operands in a row stay below a half
     assert float((layer(product) - want).norm() / want.norm()) <= 0.5
+
+
+def test_quantisation_past_32_bits(cuda_lib):
+    """More than 2^31 elements: the last matrix, and the last row, against the definition."""
+    for shape in ((34, 8192, 8192), (140000, 16384)):
+        x = torch.empty(shape, dtype=torch.bfloat16, device=DEV)
+        x.fill_(0.5)
+        g = torch.Generator(device=DEV)
+        g.manual_seed(1)
+        last = x[-1:].reshape(-1, shape[-1])[:8]
+        last.copy_(torch.randn(last.shape, generator=g, device=DEV) * 3)
+        q, bs, gs = cuda_lib.quantize_nvfp4(x)
+        dq, dbs, dgs = _definition(last.float().cpu().numpy())
+        assert float(gs[-1]) == float(dgs)
+        np.testing.assert_array_equal(q[-1:].reshape(-1, shape[-1] // 2)[:8].cpu().numpy(), dq)
+        np.testing.assert_array_equal(bs[-1:].reshape(-1, shape[-1] // 16)[:8].cpu().numpy(), dbs)
+        v = cuda_lib.dequantize_nvfp4(q, bs, gs, out_dtype=torch.bfloat16)
+        want = oracle.dequant_nvfp4(dq, dbs, float(dgs))
+        assert torch.equal(v[-1:].reshape(-1, shape[-1])[:8].cpu(), torch.from_numpy(want).to(torch.bfloat16))
+        del x, q, bs, gs, v
+        torch.cuda.empty_cache()
+
+
+@pytest.mark.parametrize("rows", [3, 60, 400])
+def test_product_of_the_largest_matrices(cuda_lib, rows):
+    off, x, w = _product_case([rows], 2 * cuda_lib.MAX_DIM, cuda_lib.MAX_DIM)
+    xq, wq = cuda_lib.quantize_nvfp4(x), cuda_lib.quantize_nvfp4(w)
+    del x, w
+    y = cuda_lib.grouped_gemm_nvfp4(*xq, *wq, off)
+    _check_product(cuda_lib, off, xq, wq, y)
+    del y, xq, wq
+    torch.cuda.empty_cache()
