@@ -53,7 +53,6 @@ struct GgParams {
     int NW;    // dw: rows of a weight matrix
     int split; // dw: parts that each segment's rows are cut into, part p's result at out + p E NW M
     void* out;
-    int out_f32;
     int a_blocked, b_blocked;  // MN-major operands: the map has a 64-column block dimension
     int32_t* status;
 };
@@ -66,11 +65,13 @@ struct GgParams {
 // Warps: EPI epilogue warps (lane quarter w & 3, share of the columns w >> 2),
 // the TMA producer, the MMA issuer and for dw one that clears rows behind a
 // segment.  Four epilogue warps keep up with a long contraction and disturb
-// it least (forward of 65536 rows: 254 us, eight 264); the weight gradient of
-// few rows is all epilogue (0.4 GB in bf16: 126 us with four, 88 with eight).
-template <int MODE, int CG>
+// it least (forward of 65536 rows to bf16: 250 us, eight 264); the weight
+// gradient of few rows is all epilogue (0.4 GB in bf16: 126 us with four, 88
+// with eight).  fp32 results, whose parts are summed in registers, take eight
+// (summed in the output, by four, they cost 330 us instead of 270).
+template <int MODE, int CG, bool F32>
 struct GgCfg {
-    static constexpr int EPI = MODE == kGgDw ? 8 : 4;
+    static constexpr int EPI = MODE == kGgDw || F32 ? 8 : 4;
     static constexpr int kThreads = 32 * (EPI + (MODE == kGgDw ? 3 : 2));
     static constexpr int COLS = 128 * CG / (EPI / 4);  // columns an epilogue warp takes
     static constexpr int BM = 128 * CG;
@@ -449,19 +450,12 @@ __device__ __forceinline__ uint32_t gg_pair_select(int odd) { return odd ? 0x327
 // fp32 as they are, a warp writing 128 contiguous bytes a row; bf16 after
 // lanes 2i and 2i + 1 have exchanged a value per pair of rows, so that each
 // lane writes two neighbouring m (4 bytes) of one row.
-__device__ __forceinline__ void gg_store32(uint32_t (&r)[32], void* out, int out_f32, size_t row0, int nc, int m, int M,
-                                           bool add = false) {
+__device__ __forceinline__ void gg_store32(const uint32_t (&r)[32], void* out, int out_f32, size_t row0, int nc, int m,
+                                           int M) {
     const bool whole = nc >= 32;
     if (out_f32) {
         uint32_t* o = static_cast<uint32_t*>(out) + row0 * (size_t)M + m;
         if (m >= M) return;
-        if (add) {  // to this thread's own earlier stores
-            float old[32];
-#pragma unroll
-            for (int j = 0; j < 32; ++j) old[j] = j < nc ? __ldcg(reinterpret_cast<const float*>(o + (size_t)j * M)) : 0.0f;
-#pragma unroll
-            for (int j = 0; j < 32; ++j) r[j] = __float_as_uint(old[j] + __uint_as_float(r[j]));
-        }
         if (whole) {
 #pragma unroll
             for (int j = 0; j < 32; ++j, o += M) *o = r[j];
@@ -488,11 +482,10 @@ __device__ __forceinline__ void gg_store32(uint32_t (&r)[32], void* out, int out
     }
 }
 
-// The columns of one accumulator, 32 at a time, the next 32 on their way
-// while these are stored; `done` runs once they are all in registers.
+// The columns of one accumulator to bf16, 32 at a time, the next 32 on their
+// way while these are stored; `done` runs once they are all in registers.
 template <typename Done>
-__device__ __forceinline__ void gg_epilogue(uint32_t taddr, void* out, int out_f32, size_t row0, int n, int m, int M,
-                                            bool add, Done done) {
+__device__ __forceinline__ void gg_epilogue(uint32_t taddr, void* out, size_t row0, int n, int m, int M, Done done) {
     uint32_t a[32], b[32];
     gg_ld32(taddr, a);
     for (int c = 0; c < n; c += 64) {
@@ -501,14 +494,38 @@ __device__ __forceinline__ void gg_epilogue(uint32_t taddr, void* out, int out_f
             gg_ld32(taddr + c + 32, b);
         else
             done();
-        gg_store32(a, out, out_f32, row0 + c, min(32, n - c), m, M, add);
+        gg_store32(a, out, 0, row0 + c, min(32, n - c), m, M);
         if (c + 32 >= n) break;
         gg_ld_wait(b);
         if (c + 64 < n)
             gg_ld32(taddr + c + 64, a);
         else
             done();
-        gg_store32(b, out, out_f32, row0 + c + 32, min(32, n - c - 32), m, M, add);
+        gg_store32(b, out, 0, row0 + c + 32, min(32, n - c - 32), m, M);
+    }
+}
+
+// fp32: an accumulator's COLS columns into `sum` (the first part), or added to it.
+template <int COLS>
+__device__ __forceinline__ void gg_gather(uint32_t taddr, uint32_t (&sum)[COLS / 32][32], int n, bool first) {
+    if (first) {
+#pragma unroll
+        for (int i = 0; i < COLS / 32; ++i)
+            if (32 * i < n) gg_ld32(taddr + 32 * i, sum[i]);
+#pragma unroll
+        for (int i = 0; i < COLS / 32; ++i) gg_ld_wait(sum[i]);
+    } else {
+#pragma unroll
+        for (int i = 0; i < COLS / 16; ++i) {
+            if (16 * i >= n) break;
+            float v[16];
+            tmem_ld16(taddr + 16 * i, v);
+#pragma unroll
+            for (int j = 0; j < 16; ++j) {
+                uint32_t& t = sum[i / 2][i % 2 * 16 + j];
+                t = __float_as_uint(__uint_as_float(t) + v[j]);
+            }
+        }
     }
 }
 
@@ -517,9 +534,9 @@ __device__ __forceinline__ void gg_epilogue(uint32_t taddr, void* out, int out_f
 // tiles.  Three roles run through the same tile sequence, each at its own
 // pace: the producer fills the ring, the MMA issuer accumulates tile d into
 // tensor-memory buffer d mod 2, the epilogue warps read the other buffer out.
-template <int MODE, int CG>
-__global__ void __launch_bounds__((GgCfg<MODE, CG>::kThreads), 1) gg_kernel(const __grid_constant__ GgParams p) {
-    using Cfg = GgCfg<MODE, CG>;
+template <int MODE, int CG, bool F32>
+__global__ void __launch_bounds__((GgCfg<MODE, CG, F32>::kThreads), 1) gg_kernel(const __grid_constant__ GgParams p) {
+    using Cfg = GgCfg<MODE, CG, F32>;
     extern __shared__ __align__(1024) unsigned char gg_smem_raw[];
     unsigned char* base = reinterpret_cast<unsigned char*>(
         (reinterpret_cast<uintptr_t>(gg_smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
@@ -604,7 +621,7 @@ __global__ void __launch_bounds__((GgCfg<MODE, CG>::kThreads), 1) gg_kernel(cons
         }
     };
     // 64-wide steps that one accumulator takes
-    const int part_steps = p.out_f32 ? kGgPartSteps : 1 << 30;
+    constexpr int part_steps = F32 ? kGgPartSteps : 1 << 30;
 
     if (warp == Cfg::EPI) {
         // ---------------- TMA producer
@@ -786,9 +803,10 @@ __global__ void __launch_bounds__((GgCfg<MODE, CG>::kThreads), 1) gg_kernel(cons
                 uint32_t z[32];
 #pragma unroll
                 for (int j = 0; j < 32; ++j) z[j] = 0;
-                for (int c = 0; c < mine; c += 32) gg_store32(z, p.out, p.out_f32, row0 + c, min(32, mine - c), m, p.M);
+                for (int c = 0; c < mine; c += 32) gg_store32(z, p.out, F32, row0 + c, min(32, mine - c), m, p.M);
                 return true;
             }
+            uint32_t sum[F32 ? Cfg::COLS / 32 : 1][32];  // fp32: the parts' sum
             for (int k = 0; k < nk; k += part_steps) {
                 if (!gg_wait_warp(&sh->acc_full[buf], full_ph, &sh->abort)) return false;
                 tc_fence_after();
@@ -802,14 +820,23 @@ __global__ void __launch_bounds__((GgCfg<MODE, CG>::kThreads), 1) gg_kernel(cons
                             mbar_arrive_cluster(&sh->acc_empty[buf], 0);
                     }
                 };
-                if (mine > 0)
-                    gg_epilogue(tmem + (uint32_t)(buf * Cfg::BN + c0) + ((uint32_t)((warp & 3) * 32) << 16), p.out,
-                                p.out_f32, row0, mine, m, p.M, k > 0, release);
-                else
+                const uint32_t taddr = tmem + (uint32_t)(buf * Cfg::BN + c0) + ((uint32_t)((warp & 3) * 32) << 16);
+                if constexpr (F32) {
+                    if (mine > 0) gg_gather<Cfg::COLS>(taddr, sum, mine, k == 0);
                     release();
+                } else if (mine > 0) {
+                    gg_epilogue(taddr, p.out, row0, mine, m, p.M, release);
+                } else {
+                    release();
+                }
                 buf ^= 1;
                 if (buf == 0) full_ph ^= 1u;
                 if (part_steps >= nk) break;
+            }
+            if constexpr (F32) {
+#pragma unroll
+                for (int i = 0; i < Cfg::COLS / 32; ++i)
+                    if (32 * i < mine) gg_store32(sum[i], p.out, 1, row0 + 32 * i, min(32, mine - 32 * i), m, p.M);
             }
             return true;
         });

@@ -74,28 +74,28 @@ static int launch_persistent(K kernel, const P& p, int threads, int sms, cudaStr
     return launch_ex(cfg, kernel, p);
 }
 
-// The paired tile (256 x 256) from this many rows a segment on average, where
+// The paired tile (256 x 256) from so many rows a segment on average, where
 // the output is wider than a single CTA's tile.  Measured on 64 experts of
-// 1536 x 2048 at 96 / 128 / 256 rows, single and paired: forward 76 / 81 / 110
-// and 79 / 81 / 95 us.  A bf16 weight gradient is all stores at few rows, and
-// the pair's larger tiles are always ahead (16 rows: 100 and 88 us).
-constexpr int kGgPairRows = 128;
+// 1536 x 2048, single and paired, at 96 / 128 / 256 rows: forward to bf16 76 /
+// 81 / 110 and 79 / 81 / 95 us, to fp32 78 / 84 / 118 and 81 / 84 / 101.
+// Weight gradients of few rows are all stores: in bf16 the pair's larger tiles
+// are always ahead (16 rows: 100 and 88 us), in fp32 late (256 rows: 170 and
+// 175; 1024: 426 and 295).
+constexpr int kGgPairRows = 128, kGgPairRowsDw = 0, kGgPairRowsDwF32 = 384;
 
-static bool gg_pairs(int R, int M, int E, bool dw_bf16 = false) {
-    return M > 128 && (dw_bf16 || (int64_t)R >= (int64_t)kGgPairRows * E);
-}
+static bool gg_pairs(int R, int M, int E, int rows = kGgPairRows) { return M > 128 && (int64_t)R >= (int64_t)rows * E; }
 
 // dw: with fewer tiles than CTAs (or pairs) the segments' rows are cut into
 // parts, of 512 rows on average at least, whose sums are joined afterwards.
 static int gg_split(int R, int N, int K, int E, int sms) {
-    const int cg = gg_pairs(R, K, E) ? 2 : 1;
+    const int cg = gg_pairs(R, K, E, kGgPairRowsDwF32) ? 2 : 1;
     const int64_t tiles = (int64_t)E * ceil_div(N, 128 * cg) * ceil_div(K, 128 * cg);
     int64_t parts = sms / cg / tiles;
     if (parts > (int64_t)R / E / 512) parts = (int64_t)R / E / 512;
     return parts < 2 ? 1 : (int)parts;
 }
 
-template <int MODE>
+template <int MODE, bool F32>
 static int run_gg(GgParams& p, const void* a, const void* b, int R, int N, int K, int E, cudaStream_t st) {
     bool ok;
     p.a_blocked = K % 64 == 0;
@@ -118,8 +118,9 @@ static int run_gg(GgParams& p, const void* a, const void* b, int R, int N, int K
     p.NW = N;
     const int sms = sm_count();
     if (sms < 2) return MOE_ERR_CUDA;
-    return gg_pairs(R, p.M, E, MODE == kGgDw && !p.out_f32) ? launch_persistent<2>(gg_kernel<MODE, 2>, p, GgCfg<MODE, 2>::kThreads, sms, st)
-                : launch_persistent<1>(gg_kernel<MODE, 1>, p, GgCfg<MODE, 1>::kThreads, sms, st);
+    return gg_pairs(R, p.M, E, MODE != kGgDw ? kGgPairRows : F32 ? kGgPairRowsDwF32 : kGgPairRowsDw)
+               ? launch_persistent<2>(gg_kernel<MODE, 2, F32>, p, GgCfg<MODE, 2, F32>::kThreads, sms, st)
+               : launch_persistent<1>(gg_kernel<MODE, 1, F32>, p, GgCfg<MODE, 1, F32>::kThreads, sms, st);
 }
 
 template <bool BF16, int T>
@@ -194,9 +195,9 @@ int moe_grouped_gemm(const uint16_t* x, const uint16_t* w, const int32_t* offset
     memset(&p, 0, sizeof p);
     p.offsets = offsets;
     p.out = y;
-    p.out_f32 = y_dtype == MOE_DT_F32;
     p.status = dev_status;
-    return run_gg<kGgFwd>(p, w, x, R, N, K, E, st);
+    return y_dtype == MOE_DT_F32 ? run_gg<kGgFwd, true>(p, w, x, R, N, K, E, st)
+                                 : run_gg<kGgFwd, false>(p, w, x, R, N, K, E, st);
 }
 
 int moe_grouped_gemm_dx(const uint16_t* dy, const uint16_t* w, const int32_t* offsets, int R, int N, int K, int E,
@@ -213,9 +214,10 @@ int moe_grouped_gemm_dx(const uint16_t* dy, const uint16_t* w, const int32_t* of
     memset(&p, 0, sizeof p);
     p.offsets = offsets;
     p.out = dx;
-    p.out_f32 = dx_dtype == MOE_DT_F32;
     p.status = dev_status;
-    return run_gg<kGgDx>(p, w, dy, R, N, K, E, static_cast<cudaStream_t>(stream));
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    return dx_dtype == MOE_DT_F32 ? run_gg<kGgDx, true>(p, w, dy, R, N, K, E, st)
+                                  : run_gg<kGgDx, false>(p, w, dy, R, N, K, E, st);
 }
 
 int moe_grouped_gemm_dw_workspace_bytes(int R, int N, int K, int E, size_t* bytes) {
@@ -251,10 +253,11 @@ int moe_grouped_gemm_dw(const uint16_t* dy, const uint16_t* x, const int32_t* of
     memset(&p, 0, sizeof p);
     p.offsets = offsets;
     p.out = split > 1 ? workspace : dw;
-    p.out_f32 = split > 1 || dw_dtype == MOE_DT_F32;
     p.split = split;
     p.status = dev_status;
-    if ((rc = run_gg<kGgDw>(p, x, dy, R, N, K, E, st))) return rc;
+    rc = split > 1 || dw_dtype == MOE_DT_F32 ? run_gg<kGgDw, true>(p, x, dy, R, N, K, E, st)
+                                             : run_gg<kGgDw, false>(p, x, dy, R, N, K, E, st);
+    if (rc) return rc;
     if (split == 1) return MOE_OK;
     size_t grid = (n / 4 + 255) / 256;
     if (grid > (size_t)sms * 8) grid = (size_t)sms * 8;
