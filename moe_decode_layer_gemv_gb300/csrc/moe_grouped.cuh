@@ -351,9 +351,9 @@ __device__ __forceinline__ void gg_settle(uint64_t* bar, uint32_t parity) {
 }
 
 // The producer's teardown: no copy, and no release of a stage by the
-// leader's MMAs, may be on its way when the CTA exits.  (A pair's copies are
-// counted on the leader's barriers; after an abort the other CTA, which
-// cannot wait on them, gives its own the time to land.)
+// leader's MMAs, may be on its way when the CTA exits.  (After an abort some
+// copies cannot be waited for here, those of a pair's other CTA and of a
+// segment's end: they are given the time to land.)
 template <int CG>
 __device__ __forceinline__ void gg_drain(GgShared* sh, uint32_t S, const GgRing& r, uint32_t rank) {
     for (uint32_t s = 0; s < S && s < r.uses; ++s) {
@@ -361,12 +361,32 @@ __device__ __forceinline__ void gg_drain(GgShared* sh, uint32_t S, const GgRing&
         if (rank == 0) gg_settle(&sh->full[s], ph);
         if (CG == 2) gg_wait(&sh->empty[s], ph, &sh->abort);
     }
-    if (rank != 0 && *(volatile int*)&sh->abort)
+    if (*(volatile int*)&sh->abort)
         for (int i = 0; i < 1000; ++i) __nanosleep(1000);
 }
 
 // Whether a 64-row step with `left` rows to the segment's end needs clearing.
 __device__ __forceinline__ bool gg_ragged(int left) { return left < 64 && (left & 15); }
+
+// ---------------------------------------------------------------- loads
+// Every input may come from the kernel ahead on the stream, which may still
+// run when this one is launched (grid_dep_wait): none is read-only for this
+// kernel's whole life, so none is read through the non-coherent path (no
+// ld.global.nc, no __restrict__).  Volatile, so that a few rows' products
+// issue them with the weights' loads (4.3 us for 5.2).
+__device__ __forceinline__ uint4 ld_input_v4(const void* p) {
+    uint4 r;
+    asm volatile("ld.global.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w) : "l"(p));
+    return r;
+}
+// What is read once:
+__device__ __forceinline__ uint4 ld_stream_v4(const void* p) {
+    uint4 r;
+    asm volatile("ld.global.L1::no_allocate.L2::256B.v4.u32 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w)
+                 : "l"(p));
+    return r;
+}
 
 // ------------------------------------------------------------- segments
 // The segments into shared memory.  Offsets outside [0, R] or descending
@@ -378,7 +398,7 @@ __device__ __forceinline__ void gg_segments(GgShared* sh, const int32_t* offsets
     if (tid == 0) sh->nmax = 0;
     __syncthreads();
     for (int e = tid; e < E; e += blockDim.x) {
-        const int a = __ldg(offsets + e), b = __ldg(offsets + e + 1);
+        const int a = offsets[e], b = offsets[e + 1];
         const bool ok = a >= 0 && b >= a && b <= R;
         if (!ok && blockIdx.x == 0) set_status(status, MOE_DEV_BAD_OFFSETS);
         sh->p0[e] = ok ? a : 0;
@@ -850,21 +870,34 @@ __global__ void __launch_bounds__((GgCfg<MODE, CG, F32>::kThreads), 1) gg_kernel
     }
 }
 
-// dw of a split launch: the parts' sums, part after part (a fixed order).
-__global__ void __launch_bounds__(256) gg_join_kernel(const float4* __restrict__ parts, size_t n4, int split, void* out,
+// dw of a split launch: the parts' sums in a fixed order.  A block takes 32
+// pieces of four values; its eight warps sum every eighth part, and the first
+// adds their sums.
+__global__ void __launch_bounds__(256) gg_join_kernel(const float4* parts, size_t n4, int split, void* out,
                                                       int out_f32) {
+    __shared__ float4 s_sum[8][32];
     grid_dep_wait();
-    for (size_t i = (size_t)blockIdx.x * blockDim.x + threadIdx.x; i < n4; i += (size_t)gridDim.x * blockDim.x) {
-        float4 a = __ldcg(parts + i);
-        for (int k = 1; k < split; ++k) {
-            const float4 b = __ldcg(parts + (size_t)k * n4 + i);
-            a = make_float4(a.x + b.x, a.y + b.y, a.z + b.z, a.w + b.w);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    auto add = [](float4 a, float4 b) { return make_float4(a.x + b.x, a.y + b.y, a.z + b.z, a.w + b.w); };
+    for (size_t i0 = (size_t)blockIdx.x * 32; i0 < n4; i0 += (size_t)gridDim.x * 32) {
+        const size_t i = i0 + lane;
+        float4 a = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        if (i < n4) {
+#pragma unroll 4
+            for (int k = warp; k < split; k += 8) a = add(a, __ldcg(parts + (size_t)k * n4 + i));
         }
-        if (out_f32)
-            static_cast<float4*>(out)[i] = a;
-        else
-            static_cast<uint2*>(out)[i] = make_uint2(gg_pack(__float_as_uint(a.x), __float_as_uint(a.y)),
-                                                     gg_pack(__float_as_uint(a.z), __float_as_uint(a.w)));
+        s_sum[warp][lane] = a;
+        __syncthreads();
+        if (warp == 0 && i < n4) {
+#pragma unroll
+            for (int w = 1; w < 8; ++w) a = add(a, s_sum[w][lane]);
+            if (out_f32)
+                static_cast<float4*>(out)[i] = a;
+            else
+                static_cast<uint2*>(out)[i] = make_uint2(gg_pack(__float_as_uint(a.x), __float_as_uint(a.y)),
+                                                         gg_pack(__float_as_uint(a.z), __float_as_uint(a.w)));
+        }
+        __syncthreads();
     }
 }
 
@@ -883,8 +916,8 @@ __device__ __forceinline__ int gg_row_segment(const int32_t* offsets, int E, int
     bool mine = false, bad = false;
     int a = 0, b = 0;
     if ((int)threadIdx.x < E) {
-        a = __ldg(offsets + threadIdx.x);
-        b = __ldg(offsets + threadIdx.x + 1);
+        a = offsets[threadIdx.x];
+        b = offsets[threadIdx.x + 1];
         bad = a < 0 || b < a || b > R;
         mine = !bad && a <= r && r < b;
     }
@@ -903,8 +936,7 @@ __device__ __forceinline__ int gg_row_segment(const int32_t* offsets, int E, int
 }
 
 template <int J>
-__global__ void __launch_bounds__(256) gg_gemv_kernel(const uint16_t* __restrict__ x, const uint16_t* __restrict__ w,
-                                                      const int32_t* __restrict__ offsets, int R, int N, int K, int E,
+__global__ void __launch_bounds__(256) gg_gemv_kernel(const uint16_t* x, const uint16_t* w, const int32_t* offsets, int R, int N, int K, int E,
                                                       void* y, int out_f32, int32_t* status) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     grid_dep_wait();
@@ -926,7 +958,7 @@ __global__ void __launch_bounds__(256) gg_gemv_kernel(const uint16_t* __restrict
         for (int j = 0; j < J; ++j) {
             if (j >= nj) break;
             const int c = c0 + j * 32 + lane;
-            wv[j] = c < chunks ? ld_weight_v4(wr + (size_t)c * 8) : make_uint4(0, 0, 0, 0);
+            wv[j] = c < chunks ? ld_stream_v4(wr + (size_t)c * 8) : make_uint4(0, 0, 0, 0);
         }
 #pragma unroll
         for (int t = 0; t < kGgvTok; ++t) {
@@ -936,7 +968,7 @@ __global__ void __launch_bounds__(256) gg_gemv_kernel(const uint16_t* __restrict
             for (int j = 0; j < J; ++j) {
                 if (j >= nj) break;
                 const int c = c0 + j * 32 + lane;
-                xv[j] = c < chunks ? __ldg(reinterpret_cast<const uint4*>(xr + (size_t)t * K + (size_t)c * 8))
+                xv[j] = c < chunks ? ld_input_v4(xr + (size_t)t * K + (size_t)c * 8)
                                    : make_uint4(0, 0, 0, 0);
             }
 #pragma unroll

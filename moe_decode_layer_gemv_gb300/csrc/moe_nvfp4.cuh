@@ -50,7 +50,7 @@ struct alignas(32) Words8 {
 };
 __device__ __forceinline__ Words8 ld_words8(const void* p) {
     Words8 r;
-    asm volatile("ld.global.nc.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+    asm volatile("ld.global.L1::no_allocate.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
                  : "=r"(r.w[0]), "=r"(r.w[1]), "=r"(r.w[2]), "=r"(r.w[3]), "=r"(r.w[4]), "=r"(r.w[5]), "=r"(r.w[6]),
                    "=r"(r.w[7])
                  : "l"(p));
@@ -165,7 +165,7 @@ struct Nv4Block {
 // One scale a row: T threads hold a row's blocks in registers (up to BPT
 // each), find its maximum and write its codes -- x is read once.
 template <bool BF16, int T, int BPT>
-__global__ void __launch_bounds__(128) nv4_rows_kernel(const void* __restrict__ x, int G, int nb, uint8_t* q, uint8_t* bs,
+__global__ void __launch_bounds__(128) nv4_rows_kernel(const void* x, int G, int nb, uint8_t* q, uint8_t* bs,
                                                        float* gs, int32_t* status) {
     __shared__ float s_max[4];
     grid_dep_wait();
@@ -240,7 +240,7 @@ __device__ __forceinline__ void st_relaxed_gpu(unsigned* p, unsigned v) {
 }
 
 template <bool BF16>
-__global__ void __launch_bounds__(256, kNv4CtasPerSm) nv4_matrices_kernel(const void* __restrict__ x, size_t per,
+__global__ void __launch_bounds__(256, kNv4CtasPerSm) nv4_matrices_kernel(const void* x, size_t per,
                                                                           unsigned cpm, unsigned chunks, uint8_t* q,
                                                                           uint8_t* bs, float* gs, unsigned* ws,
                                                                           int32_t* status) {
@@ -329,12 +329,12 @@ __global__ void __launch_bounds__(256, kNv4CtasPerSm) nv4_matrices_kernel(const 
 // product is exact, the rounding is that of the last product, and of bf16).
 // 6.7 TB/s: HBM.
 template <bool BF16>
-__global__ void __launch_bounds__(256) nv4_decode_kernel(const uint8_t* __restrict__ q, const uint8_t* __restrict__ bs,
-                                                         const float* __restrict__ gs, size_t per, size_t n, void* x) {
+__global__ void __launch_bounds__(256) nv4_decode_kernel(const uint8_t* q, const uint8_t* bs,
+                                                         const float* gs, size_t per, size_t n, void* x) {
     grid_dep_wait();
     for (size_t b = (size_t)blockIdx.x * blockDim.x + threadIdx.x; b < n; b += (size_t)gridDim.x * blockDim.x) {
-        const uint2 c = __ldg(reinterpret_cast<const uint2*>(q) + b);
-        const float s = f8_to_f(bs[b]), g = __ldg(gs + b / per);
+        const uint2 c = reinterpret_cast<const uint2*>(q)[b];
+        const float s = f8_to_f(bs[b]), g = gs[b / per];
         Words8 o[BF16 ? 1 : 2];
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
@@ -458,12 +458,12 @@ __device__ __forceinline__ uint4 g4_row_scales(const uint8_t* row, int k0, int n
     if ((nb & 3) == 0) {
 #pragma unroll
         for (int i = 0; i < 4; ++i)
-            if (k0 + 4 * i < nb) w[i] = __ldg(reinterpret_cast<const uint32_t*>(p + 4 * i));
+            if (k0 + 4 * i < nb) w[i] = *reinterpret_cast<const uint32_t*>(p + 4 * i);
     } else {
 #pragma unroll
         for (int i = 0; i < 8; ++i)
             if (k0 + 2 * i < nb)
-                w[i >> 1] |= (uint32_t)__ldg(reinterpret_cast<const uint16_t*>(p + 2 * i)) << (16 * (i & 1));
+                w[i >> 1] |= (uint32_t)*reinterpret_cast<const uint16_t*>(p + 2 * i) << (16 * (i & 1));
     }
     return make_uint4(w[0], w[1], w[2], w[3]);
 }
@@ -703,10 +703,10 @@ __global__ void __launch_bounds__(kG4Threads, 1) g4_kernel(const __grid_constant
         walk([&](int e, int q0, int n, int m0) -> bool {
             const int m = m0 + (warp & 3) * 32 + lane;
             const int mine = min(COLS, n - c0);  // columns of this warp; none below 1
-            const float wg = __ldg(p.wgs + e);
+            const float wg = p.wgs[e];
             __syncwarp();
 #pragma unroll
-            for (int i = 0; i < COLS; i += 32) xg[i + lane] = i + lane < mine ? __ldg(p.xgs + q0 + c0 + i + lane) : 0.0f;
+            for (int i = 0; i < COLS; i += 32) xg[i + lane] = i + lane < mine ? p.xgs[q0 + c0 + i + lane] : 0.0f;
             __syncwarp();
             if (!gg_wait_warp(&sh->acc_full[buf], full_ph, &sh->abort)) return false;
             tc_fence_after();
@@ -812,10 +812,10 @@ __device__ __forceinline__ float g4_block(uint32_t w0, uint32_t w1, const __half
 }
 
 template <int J>
-__global__ void __launch_bounds__(256) g4_gemv_kernel(const uint8_t* __restrict__ xq, const uint8_t* __restrict__ xbs,
-                                                      const float* __restrict__ xgs, const uint8_t* __restrict__ wq,
-                                                      const uint8_t* __restrict__ wbs, const float* __restrict__ wgs,
-                                                      const int32_t* __restrict__ offsets, int R, int N, int K, int E,
+__global__ void __launch_bounds__(256) g4_gemv_kernel(const uint8_t* xq, const uint8_t* xbs,
+                                                      const float* xgs, const uint8_t* wq,
+                                                      const uint8_t* wbs, const float* wgs,
+                                                      const int32_t* offsets, int R, int N, int K, int E,
                                                       void* y, int out_f32, int32_t* status) {
     constexpr int RW = kG4vRows;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -839,8 +839,8 @@ __global__ void __launch_bounds__(256) g4_gemv_kernel(const uint8_t* __restrict_
 #pragma unroll
             for (int i = 0; i < RW; ++i) {
                 const size_t at = wrow + (size_t)i * chunks + c;
-                wv[j][i] = c < chunks ? ld_weight_v4(wq + at * 16) : make_uint4(0, 0, 0, 0);
-                ws[j][i] = c < chunks ? __ldg(reinterpret_cast<const uint16_t*>(wbs) + at) : 0;
+                wv[j][i] = c < chunks ? ld_stream_v4(wq + at * 16) : make_uint4(0, 0, 0, 0);
+                ws[j][i] = c < chunks ? reinterpret_cast<const uint16_t*>(wbs)[at] : 0;
             }
         }
 #pragma unroll
@@ -852,8 +852,8 @@ __global__ void __launch_bounds__(256) g4_gemv_kernel(const uint8_t* __restrict_
             for (int j = 0; j < J; ++j) {
                 const int c = c0 + j * 32 + lane;
                 const size_t at = xrow + (size_t)t * chunks + c;
-                xv[j] = c < chunks ? __ldg(reinterpret_cast<const uint4*>(xq) + at) : make_uint4(0, 0, 0, 0);
-                xs[j] = c < chunks ? __ldg(reinterpret_cast<const uint16_t*>(xbs) + at) : 0;
+                xv[j] = c < chunks ? *reinterpret_cast<const uint4*>(xq + at * 16) : make_uint4(0, 0, 0, 0);
+                xs[j] = c < chunks ? reinterpret_cast<const uint16_t*>(xbs)[at] : 0;
             }
 #pragma unroll
             for (int j = 0; j < J; ++j) {
@@ -876,11 +876,11 @@ __global__ void __launch_bounds__(256) g4_gemv_kernel(const uint8_t* __restrict_
             }
         }
     }
-    const float wg = __ldg(wgs + e);
+    const float wg = wgs[e];
 #pragma unroll
     for (int t = 0; t < kGgvTok; ++t) {
         if (t >= nt) break;
-        const float xg = __ldg(xgs + r + t);
+        const float xg = xgs[r + t];
 #pragma unroll
         for (int i = 0; i < RW; ++i) {
             const float v = warp_sum(acc[t][i]) * xg * wg;

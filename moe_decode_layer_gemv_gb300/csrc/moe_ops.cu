@@ -259,7 +259,7 @@ int moe_grouped_gemm_dw(const uint16_t* dy, const uint16_t* x, const int32_t* of
                                              : run_gg<kGgDw, false>(p, x, dy, R, N, K, E, st);
     if (rc) return rc;
     if (split == 1) return MOE_OK;
-    size_t grid = (n / 4 + 255) / 256;
+    size_t grid = (n / 4 + 31) / 32;
     if (grid > (size_t)sms * 8) grid = (size_t)sms * 8;
     return launch_pdl(gg_join_kernel, (unsigned)grid, 256, 0, st, static_cast<const float4*>(workspace), n / 4, split, dw,
                       (int)(dw_dtype == MOE_DT_F32));

@@ -178,6 +178,41 @@ def test_two_streams_at_once(cuda_lib):
             assert torch.equal(a, b)
 
 
+@pytest.mark.parametrize("B,k,E", [(4, 2, 40), (100, 4, 24), (700, 2, 6)])
+def test_inputs_written_by_the_call_before(cuda_lib, B, k, E):
+    """Each call's inputs are written right before it on the stream (launches
+    overlap the end of the kernel ahead): rows, weights and the grouping
+    change every time, in the same buffers."""
+    N, K, g = 72, 136, torch.Generator(device=DEV)
+    g.manual_seed(0)
+    x = torch.empty((B * k, K), dtype=torch.bfloat16, device=DEV)
+    w = torch.empty((E, N, K), dtype=torch.bfloat16, device=DEV)
+    off = torch.empty(E + 1, dtype=torch.int32, device=DEV)
+    seen = []
+    for _ in range(20):
+        ids = torch.rand((B, E), generator=g, device=DEV).topk(k, dim=1).indices.to(torch.int32)
+        nx, nw = torch.randn_like(x), torch.randn_like(w)
+        x.copy_(nx), w.copy_(nw)
+        off.copy_(cuda_lib.group_by_expert(ids, E)[0])
+        y = cuda_lib.grouped_gemm(x, w, off)
+        dx = cuda_lib.grouped_gemm_dx(y.to(torch.bfloat16), w, off)
+        q = cuda_lib.grouped_gemm_nvfp4(*cuda_lib.quantize_nvfp4(torch.nn.functional.pad(x, (0, 24))),
+                                        *cuda_lib.quantize_nvfp4(torch.nn.functional.pad(w, (0, 24))), off)
+        seen.append((nx, nw, off.clone(), y, dx, q))
+    torch.cuda.synchronize()
+    for nx, nw, o, y, dx, q in seen:
+        x.copy_(nx), w.copy_(nw), off.copy_(o)
+        torch.cuda.synchronize()
+        assert torch.equal(y, cuda_lib.grouped_gemm(x, w, off))
+        yb = y.to(torch.bfloat16)
+        torch.cuda.synchronize()
+        assert torch.equal(dx, cuda_lib.grouped_gemm_dx(yb, w, off))
+        xq = cuda_lib.quantize_nvfp4(torch.nn.functional.pad(x, (0, 24)))
+        wq = cuda_lib.quantize_nvfp4(torch.nn.functional.pad(w, (0, 24)))
+        torch.cuda.synchronize()
+        assert torch.equal(q, cuda_lib.grouped_gemm_nvfp4(*xq, *wq, off))
+
+
 @pytest.mark.parametrize("rows", [6, 60, 600])
 @pytest.mark.parametrize("offsets", [[0, 4, 2, 6], [-1, 2, 3, 6], [0, 2, 3, 7], [0, 2 ** 31 - 1, 2, 6]])
 @pytest.mark.parametrize("op", ["fwd", "dx", "dw"])
