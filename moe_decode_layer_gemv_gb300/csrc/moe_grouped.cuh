@@ -379,6 +379,11 @@ __device__ __forceinline__ uint4 ld_input_v4(const void* p) {
     asm volatile("ld.global.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w) : "l"(p));
     return r;
 }
+__device__ __forceinline__ float ld_input_f(const float* p) {
+    float r;
+    asm volatile("ld.global.f32 %0, [%1];" : "=f"(r) : "l"(p));
+    return r;
+}
 // What is read once:
 __device__ __forceinline__ uint4 ld_stream_v4(const void* p) {
     uint4 r;

@@ -703,12 +703,14 @@ __global__ void __launch_bounds__(kG4Threads, 1) g4_kernel(const __grid_constant
         walk([&](int e, int q0, int n, int m0) -> bool {
             const int m = m0 + (warp & 3) * 32 + lane;
             const int mine = min(COLS, n - c0);  // columns of this warp; none below 1
-            const float wg = p.wgs[e];
-            __syncwarp();
+            const float wg = ld_input_f(p.wgs + e);
+            float mg[COLS / 32];
 #pragma unroll
-            for (int i = 0; i < COLS; i += 32) xg[i + lane] = i + lane < mine ? p.xgs[q0 + c0 + i + lane] : 0.0f;
-            __syncwarp();
+            for (int i = 0; i < COLS / 32; ++i) mg[i] = 32 * i + lane < mine ? ld_input_f(p.xgs + q0 + c0 + 32 * i + lane) : 0.0f;
             if (!gg_wait_warp(&sh->acc_full[buf], full_ph, &sh->abort)) return false;
+#pragma unroll
+            for (int i = 0; i < COLS / 32; ++i) xg[32 * i + lane] = mg[i];
+            __syncwarp();
             tc_fence_after();
             const uint32_t taddr = tmem + (uint32_t)(buf * Cfg::BN + c0) + ((uint32_t)((warp & 3) * 32) << 16);
             auto release = [&]() {
