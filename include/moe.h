@@ -324,7 +324,8 @@ int moe_stack_forward_nvfp4(int L, const uint16_t* const* w_router, const float*
  *      are left as they were.
  * 0 <= R <= MOE_MAX_ROWS, 1 <= E <= MOE_MAX_E, K a multiple of 8 in
  * [8, MOE_MAX_DIM], N one in [8, 2 MOE_MAX_DIM].  Offsets that descend or
- * leave [0, R] set MOE_DEV_BAD_OFFSETS and their segment is left out.  A
+ * leave [0, R] set MOE_DEV_BAD_OFFSETS and their segment is left out (where
+ * good segments then overlap, their rows are not valid).  A
  * NaN or infinity reaches the outputs of its own row (in w: of its own
  * expert) alone.  y must not overlap an input.  Needs no workspace.
  */
@@ -372,7 +373,9 @@ int moe_grouped_gemm_dw(const uint16_t* dy, const uint16_t* x, const int32_t* of
  * NaN throughout; other blocks are not affected (such elements do not enter
  * a).  cols a multiple of 32 in [32, MOE_MAX_DIM], rows <= 2 MOE_MAX_DIM;
  * G <= MOE_MAX_ROWS for rows = 1, 65535 otherwise; x 32-byte aligned.
- * workspace: moe_quantize_nvfp4_workspace_bytes() (0 for rows = 1).
+ * At most MOE_MAX_BLOCKS blocks of 16 elements for rows > 1.
+ * workspace: moe_quantize_nvfp4_workspace_bytes() (0 for rows = 1), used by
+ * one call at a time.
  */
 int moe_quantize_nvfp4_workspace_bytes(int G, int rows, int cols, size_t* bytes);
 int moe_quantize_nvfp4(const void* x, int x_dtype, int G, int rows, int cols, uint8_t* q, uint8_t* bs, float* gs,

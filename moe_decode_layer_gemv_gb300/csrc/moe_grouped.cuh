@@ -15,10 +15,12 @@
 //   dw       A = x   (m = k; contraction over rows: MN-major), B = dy (MN-major)
 // The segments are read on the device: no launch depends on their sizes.
 //
-// Measured (cold L2): 65536 rows over 64 experts of 1536 x 2048, paired tiles:
-// forward 248 us (1664 TFLOP/s, tensor pipe 77 % busy, 12 TB/s from L2), dx and
-// dw 250; with few rows the weights' (dw: the gradients') bytes bound it: 512
-// rows over 256 experts 217 us, 0.95 of the copy bandwidth.
+// Measured (L2 flushed): 65536 rows over 64 experts of 1536 x 2048, paired
+// tiles: forward 247 us (1670 TFLOP/s, tensor pipe 77 % busy, 12 TB/s from L2),
+// dx 249, dw 248; 19 even segments of 4096 rows: 1870 TFLOP/s and more, the
+// ragged ends and the last round cost the rest.  With few rows the weights'
+// (dw: the gradients') bytes bound it: 512 rows over 256 experts 202 us, the
+// copy bandwidth.
 #pragma once
 
 #include "moe_common.cuh"

@@ -365,10 +365,10 @@ __global__ void __launch_bounds__(256) nv4_decode_kernel(const uint8_t* q, const
 // exactly its column words of every 64-element step, so nothing is exchanged.
 // (tcgen05.cp does the same copy on the tensor pipe, in line with the MMAs:
 // it took 0.3 of the large product's time.)
-// Measured: 65536 rows over 64 experts of 1536 x 2048, 106 us (3.9 PFLOP/s);
-// the MMAs alone are about 32 us of it, the rest is a stage's chain of
-// barriers and single-thread issue (8 stages a tile) and the accumulator's
-// drain.  32 rows over 256 experts: 20 us, 8 of them the bytes.
+// Measured: 65536 rows over 64 experts of 1536 x 2048, 104 us (4.0 PFLOP/s);
+// the MMAs alone are about 32 us of it, the rest is a stage's hand-overs (8
+// stages a tile) and the accumulator's drain.  32 rows over 256 experts: 16.5
+// us, 8 of them the bytes.
 constexpr int kG4Epi = 8;                 // epilogue warps: lane quarter w & 3, half of the columns w >> 2
 constexpr int kG4Threads = 32 * (kG4Epi + 6);  // warp 8 TMA, 9 MMA, 10-13 scales
 constexpr int kG4A = 128 * 128;           // codes of 128 rows x 256 elements
