@@ -647,7 +647,7 @@ def _out(out, shape, out_dtype, like):
     if out is None:
         if out_dtype not in _OUT:
             raise TypeError("out_dtype must be float32 or bfloat16")
-        return like.new_empty(shape, dtype=out_dtype)
+        return torch.empty(shape, dtype=out_dtype, device=like.device)
     if out.dtype not in _OUT:
         raise TypeError("out must be float32 or bfloat16")
     _is(out, "out", out.dtype, shape, like.get_device())
@@ -711,7 +711,7 @@ def _grouped_dw(handle, dy, x, offsets, R, N, K, E, out_dtype, out, workspace, s
     wp, wn = None, 0
     if n.value:
         if workspace is None:
-            workspace = dy.new_empty(n.value, dtype=torch.uint8)
+            workspace = torch.empty(n.value, dtype=torch.uint8, device=dy.device)
         wp, wn = workspace.data_ptr(), workspace.numel()
     _check(_lib.moe_grouped_gemm_dw(dy.data_ptr(), x.data_ptr(), offsets.data_ptr(), R, N, K, E, dw.data_ptr(),
                                     _OUT[dw.dtype], wp, wn, st, handle), "moe_grouped_gemm_dw")
@@ -757,10 +757,10 @@ def _nvfp4_cols(cols, name):
 
 def _quantize(handle, x, dt, G, rows, cols, out, workspace, st):
     if out is None:
-        lead = x.shape[:-1]
-        q = x.new_empty((*lead, cols // 2), dtype=torch.uint8)
-        bs = x.new_empty((*lead, cols // 16), dtype=torch.uint8)
-        gs = x.new_empty((G,), dtype=torch.float32)
+        lead, dev = x.shape[:-1], x.device
+        q = torch.empty((*lead, cols // 2), dtype=torch.uint8, device=dev)
+        bs = torch.empty((*lead, cols // 16), dtype=torch.uint8, device=dev)
+        gs = torch.empty((G,), dtype=torch.float32, device=dev)
     else:
         q, bs, gs = out
     wp, wn = None, 0
@@ -769,7 +769,7 @@ def _quantize(handle, x, dt, G, rows, cols, out, workspace, st):
             n = _S(0)
             _check(_lib.moe_quantize_nvfp4_workspace_bytes(G, rows, cols, ctypes.byref(n)),
                    "moe_quantize_nvfp4_workspace_bytes")
-            workspace = x.new_empty(n.value, dtype=torch.uint8)
+            workspace = torch.empty(n.value, dtype=torch.uint8, device=x.device)
         wp, wn = workspace.data_ptr(), workspace.numel()
     _check(_lib.moe_quantize_nvfp4(x.data_ptr(), dt, G, rows, cols, q.data_ptr(), bs.data_ptr(), gs.data_ptr(), wp, wn,
                                    st, handle), "moe_quantize_nvfp4")
