@@ -38,11 +38,11 @@ constexpr int kGgSmem = 227 * 1024;
 constexpr uint32_t kGgWaitNs = 20000;     // a wait sleeps this long at a time ...
 constexpr uint32_t kGgWaitLimit = 1u << 17;  // ... and gives up after so many times
 constexpr uint32_t kGgTmemCols = 512;
-// The tensor cores add to an accumulator with truncation: an error that grows
-// with the number of additions (measured: 1.2e-8 of the result a 16-deep MMA).
-// fp32 results take at most so many 64-wide steps in one accumulator, 64
-// MMAs; the parts are added in fp32, rounded to nearest.  Beside a bf16
-// result's own rounding the error of one accumulator does not count.
+// The tensor cores add to an accumulator with truncation, which makes a sum
+// smaller with every addition: sums of one sign by 1.0e-6 in 64 MMAs (16 deep),
+// by 7.4e-5 in 1024 and by 1.6e-3 in 16384, most of half a bf16 step.  So an
+// accumulator takes at most so many 64-wide steps, 64 MMAs, whatever the
+// result's type; the parts are added in fp32, rounded to nearest.
 constexpr int kGgPartSteps = 16;
 
 struct GgParams {
@@ -66,14 +66,13 @@ struct GgParams {
 // the training batch is bound by the copies from L2 (340 us).
 // Warps: EPI epilogue warps (lane quarter w & 3, share of the columns w >> 2),
 // the TMA producer, the MMA issuer and for dw one that clears rows behind a
-// segment.  Four epilogue warps keep up with a long contraction and disturb
-// it least (forward of 65536 rows to bf16: 250 us, eight 264); the weight
-// gradient of few rows is all epilogue (0.4 GB in bf16: 126 us with four, 88
-// with eight).  fp32 results, whose parts are summed in registers, take eight
-// (summed in the output, by four, they cost 330 us instead of 270).
+// segment.  Eight epilogue warps, since the parts of a sum are added in their
+// registers (added in the output, by four, fp32 results of 65536 rows cost
+// 330 us instead of 270), and since the weight gradient of few rows is all
+// epilogue (0.4 GB in bf16: 126 us with four, 88 with eight, 72 by now).
 template <int MODE, int CG, bool F32>
 struct GgCfg {
-    static constexpr int EPI = MODE == kGgDw || F32 ? 8 : 4;
+    static constexpr int EPI = 8;
     static constexpr int kThreads = 32 * (EPI + (MODE == kGgDw ? 3 : 2));
     static constexpr int COLS = 128 * CG / (EPI / 4);  // columns an epilogue warp takes
     static constexpr int BM = 128 * CG;
@@ -509,30 +508,7 @@ __device__ __forceinline__ void gg_store32(const uint32_t (&r)[32], void* out, i
     }
 }
 
-// The columns of one accumulator to bf16, 32 at a time, the next 32 on their
-// way while these are stored; `done` runs once they are all in registers.
-template <typename Done>
-__device__ __forceinline__ void gg_epilogue(uint32_t taddr, void* out, size_t row0, int n, int m, int M, Done done) {
-    uint32_t a[32], b[32];
-    gg_ld32(taddr, a);
-    for (int c = 0; c < n; c += 64) {
-        gg_ld_wait(a);
-        if (c + 32 < n)
-            gg_ld32(taddr + c + 32, b);
-        else
-            done();
-        gg_store32(a, out, 0, row0 + c, min(32, n - c), m, M);
-        if (c + 32 >= n) break;
-        gg_ld_wait(b);
-        if (c + 64 < n)
-            gg_ld32(taddr + c + 64, a);
-        else
-            done();
-        gg_store32(b, out, 0, row0 + c + 32, min(32, n - c - 32), m, M);
-    }
-}
-
-// fp32: an accumulator's COLS columns into `sum` (the first part), or added to it.
+// An accumulator's COLS columns into `sum` (the first part), or added to it.
 template <int COLS>
 __device__ __forceinline__ void gg_gather(uint32_t taddr, uint32_t (&sum)[COLS / 32][32], int n, bool first) {
     if (first) {
@@ -647,9 +623,6 @@ __global__ void __launch_bounds__((GgCfg<MODE, CG, F32>::kThreads), 1) gg_kernel
             if (!f(e, q0, n, n0, m0, len)) break;
         }
     };
-    // 64-wide steps that one accumulator takes
-    constexpr int part_steps = F32 ? kGgPartSteps : 1 << 30;
-
     if (warp == Cfg::EPI) {
         // ---------------- TMA producer
         GgRing r;
@@ -731,7 +704,7 @@ __global__ void __launch_bounds__((GgCfg<MODE, CG, F32>::kThreads), 1) gg_kernel
                     if (!gg_wait(&sh->acc_empty[buf], free_ph, &sh->abort)) return false;
                     tacc = tmem + (uint32_t)(buf * Cfg::BN);
                     acc = 0;
-                    room = part_steps;
+                    room = kGgPartSteps;
                 }
                 if (!gg_wait(&sh->full[r.s], r.ph, &sh->abort)) return false;
                 const uint32_t sta = ring_at + r.s * stage_bytes;
@@ -833,38 +806,26 @@ __global__ void __launch_bounds__((GgCfg<MODE, CG, F32>::kThreads), 1) gg_kernel
                 for (int c = 0; c < mine; c += 32) gg_store32(z, p.out, F32, row0 + c, min(32, mine - c), m, p.M);
                 return true;
             }
-            uint32_t sum[F32 ? Cfg::COLS / 32 : 1][32];  // fp32: the parts' sum
-            for (int k = 0; k < nk; k += part_steps) {
+            uint32_t sum[Cfg::COLS / 32][32];  // the parts' sum
+            for (int k = 0; k < nk; k += kGgPartSteps) {
                 if (!gg_wait_warp(&sh->acc_full[buf], full_ph, &sh->abort)) return false;
                 tc_fence_after();
-                auto release = [&]() {
-                    tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) {
-                        if (CG == 1)
-                            mbar_arrive(&sh->acc_empty[buf]);
-                        else
-                            mbar_arrive_cluster(&sh->acc_empty[buf], 0);
-                    }
-                };
                 const uint32_t taddr = tmem + (uint32_t)(buf * Cfg::BN + c0) + ((uint32_t)((warp & 3) * 32) << 16);
-                if constexpr (F32) {
-                    if (mine > 0) gg_gather<Cfg::COLS>(taddr, sum, mine, k == 0);
-                    release();
-                } else if (mine > 0) {
-                    gg_epilogue(taddr, p.out, row0, mine, m, p.M, release);
-                } else {
-                    release();
+                if (mine > 0) gg_gather<Cfg::COLS>(taddr, sum, mine, k == 0);
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) {
+                    if (CG == 1)
+                        mbar_arrive(&sh->acc_empty[buf]);
+                    else
+                        mbar_arrive_cluster(&sh->acc_empty[buf], 0);
                 }
                 buf ^= 1;
                 if (buf == 0) full_ph ^= 1u;
-                if (part_steps >= nk) break;
             }
-            if constexpr (F32) {
 #pragma unroll
-                for (int i = 0; i < Cfg::COLS / 32; ++i)
-                    if (32 * i < mine) gg_store32(sum[i], p.out, 1, row0 + 32 * i, min(32, mine - 32 * i), m, p.M);
-            }
+            for (int i = 0; i < Cfg::COLS / 32; ++i)
+                if (32 * i < mine) gg_store32(sum[i], p.out, F32, row0 + 32 * i, min(32, mine - 32 * i), m, p.M);
             return true;
         });
     }
