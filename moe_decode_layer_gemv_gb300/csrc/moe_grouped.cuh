@@ -56,6 +56,7 @@ struct GgParams {
     int split; // dw: parts that each segment's rows are cut into, part p's result at out + p E NW M
     void* out;
     int a_blocked, b_blocked;  // MN-major operands: the map has a 64-column block dimension
+    CUtensorMap zero[4];  // dw: boxes of 64 columns x 8, 4, 2 and 1 rows, for rows of zeros from behind x's end
     int32_t* status;
 };
 
@@ -190,10 +191,13 @@ __device__ __forceinline__ uint32_t cluster_addr(const void* p, uint32_t rank) {
     return a;
 }
 
-// Arrive on the barrier at the same place in CTA `rank` of the cluster.  The
-// default semantics: what is handed over is asynchronous-proxy data (landed
-// TMA tiles, read tensor memory), and a cluster-scope release would make the
-// thread wait for its global stores.
+// Arrive on the barrier at the same place in CTA `rank` of the cluster, for
+// tensor memory that has been read or written: tcgen05.wait has completed the
+// accesses, no memory that a cache may hold is handed over, and the default
+// scope is enough (a cluster-scope release waits for every outstanding store:
+// it doubled the time of the NVFP4 product).  What one CTA of a pair puts into
+// shared memory for the leader's MMAs comes by copies that count on the
+// leader's barrier, never by stores.
 __device__ __forceinline__ void mbar_arrive_cluster(uint64_t* bar, uint32_t rank) {
     asm volatile(
         "{\n\t.reg .b32 ra;\n\t"
@@ -554,7 +558,7 @@ __global__ void __launch_bounds__((GgCfg<MODE, CG, F32>::kThreads), 1) gg_kernel
         for (int s = 0; s < kGgMaxStages; ++s) {
             mbar_init(&sh->full[s], 1);
             mbar_init(&sh->tfull[s], 1);
-            mbar_init(&sh->clear[s], CG);
+            mbar_init(&sh->clear[s], 1);
             mbar_init(&sh->empty[s], 1);
         }
         for (int a = 0; a < 2; ++a) {
@@ -759,8 +763,12 @@ __global__ void __launch_bounds__((GgCfg<MODE, CG, F32>::kThreads), 1) gg_kernel
         // the next segment (or to no one), so both operands' rows up to the
         // last MMA's end are zeroed -- zeroing one would leave 0 x infinity or
         // 0 x NaN.  A warp of its own does it in each CTA as soon as the rows
-        // landed: in the MMA warp, or in both CTAs from the leader, the fences
-        // held up every tile's end (40 of 280 us of the training batch).
+        // landed, with copies of rows behind the tensor's end, which read as
+        // zeros and count on the leader's barrier as the tiles do: nothing
+        // written by a thread passes from one CTA to the other's MMAs.
+        // (Stores of zeros handed over by a release at cluster scope take the
+        // training batch from 254 to 280 us, loading a segment's last rows
+        // piecemeal instead 258.)
         GgRing r;
         uint32_t tails = 0;
         walk([&](int e, int q0, int n, int n0, int m0, int len) -> bool {
@@ -770,20 +778,20 @@ __global__ void __launch_bounds__((GgCfg<MODE, CG, F32>::kThreads), 1) gg_kernel
                 if (gg_ragged(left)) {
                     if (!gg_wait_warp(&sh->tfull[r.s], (tails >> r.s) & 1u, &sh->abort)) return false;
                     tails ^= 1u << r.s;
-                    unsigned char* st = ring + (size_t)r.s * stage_bytes;
-                    for (int i = lane; i < (16 - (left & 15)) * 32; i += 32) {
-                        const int blk = i & 3, ch = (i >> 2) & 7, row = left + (i >> 5);
-                        *reinterpret_cast<uint4*>(st + (blk >> 1) * b_off + (blk & 1) * 8192 + row * 128 + ch * 16) =
-                            make_uint4(0, 0, 0, 0);
+                    if (gg_elect()) {
+                        // (two boxes of the largest height that fits, overlapping)
+                        const int rows = 16 - (left & 15), i = rows >= 8 ? 0 : rows >= 4 ? 1 : rows >= 2 ? 2 : 3, h = 8 >> i;
+                        const uint32_t at = smem_u32(ring) + r.s * stage_bytes + left * 128;
+                        const uint32_t bar = CG == 1 ? smem_u32(&sh->clear[r.s]) : cluster_addr(&sh->clear[r.s], 0);
+                        if (rank == 0) mbar_arrive_expect_tx(&sh->clear[r.s], CG * (rows > h ? 2 : 1) * h * 512u);
+#pragma unroll
+                        for (int o = 0; o < 4; ++o) {
+                            const uint32_t to = at + (o >> 1) * b_off + (o & 1) * 8192;
+                            gg_load2<CG>(to, &p.zero[i], 0, p.R, bar);
+                            if (rows > h) gg_load2<CG>(to + (rows - h) * 128, &p.zero[i], 0, p.R, bar);
+                        }
                     }
-                    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                     __syncwarp();
-                    if (lane == 0) {
-                        if (CG == 1)
-                            mbar_arrive(&sh->clear[r.s]);
-                        else
-                            mbar_arrive_cluster(&sh->clear[r.s], 0);
-                    }
                 }
                 r.next(S);
             }

@@ -110,6 +110,7 @@ static int run_gg(GgParams& p, const void* a, const void* b, int R, int N, int K
     else
         ok = (p.a_blocked ? encode_blocked(&p.ta, a, K, R, 0) : encode_map(&p.ta, a, 2, K, R, 0, 64)) &&
              (p.b_blocked ? encode_blocked(&p.tb, b, N, R, 0) : encode_map(&p.tb, b, 2, N, R, 0, 64));
+    for (int i = 0; MODE == kGgDw && ok && i < 4; ++i) ok = encode_map(&p.zero[i], a, 2, K, R, 0, 8 >> i);
     if (!ok) return MOE_ERR_UNSUPPORTED;
     p.E = E;
     p.R = R;
