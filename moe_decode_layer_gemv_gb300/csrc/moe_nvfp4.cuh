@@ -365,6 +365,13 @@ __global__ void __launch_bounds__(256) nv4_decode_kernel(const uint8_t* q, const
 // exactly its column words of every 64-element step, so nothing is exchanged.
 // (tcgen05.cp does the same copy on the tensor pipe, in line with the MMAs:
 // it took 0.3 of the large product's time.)
+// A sum is not cut into parts as those of bf16 operands are: K <= MOE_MAX_DIM
+// is at most 256 additions, and what they truncate is bounded.  Sums of one
+// sign lose up to 1.3e-6 at K = 4096 and 5.3e-6 at 16384, the most where the
+// block scales differ widely (2.4e-6 at 16384 where they do not).  Parts of
+// 4096 terms take that to 1.2e-6, but beside the scales there is room for one
+// accumulator and the sums of a pair's tile spill: 16384 rows of K = 8192 to
+// fp32 took 125 us instead of 92.
 // Measured: 65536 rows over 64 experts of 1536 x 2048, 104 us (4.0 PFLOP/s);
 // the MMAs alone are about 32 us of it, the rest is a stage's hand-overs (8
 // stages a tile) and the accumulator's drain.  32 rows over 256 experts: 16.5
