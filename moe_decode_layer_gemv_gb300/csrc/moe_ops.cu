@@ -76,12 +76,14 @@ static int launch_persistent(K kernel, const P& p, int threads, int sms, cudaStr
 
 // The paired tile (256 x 256) from so many rows a segment on average, where
 // the output is wider than a single CTA's tile.  Measured on 64 experts of
-// 1536 x 2048, single and paired, at 96 / 128 / 256 rows: forward to bf16 76 /
-// 81 / 110 and 79 / 81 / 95 us, to fp32 78 / 84 / 118 and 81 / 84 / 101.
+// 1536 x 2048, single and paired, at 96 / 128 / 256 rows: forward to bf16 80 /
+// 85 / 113 and 82 / 85 / 98 us, to fp32 82 / 88 / 120 and 83 / 86 / 106, dx to
+// bf16 72 / 82 / 116 and 73 / 75 / 99.
 // Weight gradients of few rows are all stores: in bf16 the pair's larger tiles
-// are always ahead (16 rows: 100 and 88 us), in fp32 late (256 rows: 170 and
-// 175; 1024: 426 and 295).
-constexpr int kGgPairRows = 128, kGgPairRowsDw = 0, kGgPairRowsDwF32 = 384;
+// are always ahead (16 rows: 101 and 96 us), in fp32 late (192 rows: 157 and
+// 161; 256: 180 and 159; 1024: 425 and 300; of 2048 x 768, 192 rows: 82 and 88,
+// 256: 94 and 89).
+constexpr int kGgPairRows = 128, kGgPairRowsDw = 0, kGgPairRowsDwF32 = 256;
 
 static bool gg_pairs(int R, int M, int E, int rows = kGgPairRows) { return M > 128 && (int64_t)R >= (int64_t)rows * E; }
 
