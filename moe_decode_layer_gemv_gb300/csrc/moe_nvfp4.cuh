@@ -372,9 +372,11 @@ __global__ void __launch_bounds__(256) nv4_decode_kernel(const uint8_t* q, const
 // 4096 terms take that to 1.2e-6, but beside the scales there is room for one
 // accumulator and the sums of a pair's tile spill: 16384 rows of K = 8192 to
 // fp32 took 125 us instead of 92.
-// Measured: 65536 rows over 64 experts of 1536 x 2048, 104 us (4.0 PFLOP/s);
-// the MMAs alone are about 32 us of it, the rest is a stage's hand-overs (8
-// stages a tile) and the accumulator's drain.  32 rows over 256 experts: 16.5
+// Measured: 65536 rows over 64 experts of 1536 x 2048, 104 us (4.0 PFLOP/s).
+// At the nominal 4-bit rate its operations are 31 us (not measured; the tensor
+// pipe is active 36 % of the time).  Without the copies, scale reads and
+// stores, the MMAs and a stage's hand-overs (8 stages a tile) still took 86 of
+// 108 us: the hand-overs bound it, then the accumulator's drain.  32 rows over 256 experts: 16.5
 // us, 8 of them the bytes.
 constexpr int kG4Epi = 8;                 // epilogue warps: lane quarter w & 3, half of the columns w >> 2
 constexpr int kG4Threads = 32 * (kG4Epi + 6);  // warp 8 TMA, 9 MMA, 10-13 scales
