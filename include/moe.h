@@ -317,7 +317,8 @@ int moe_stack_forward_nvfp4(int L, const uint16_t* const* w_router, const float*
  *   y[r, n] = sum_k w[e, n, k] x[r, k]   for offsets[e] <= r < offsets[e+1],
  * the segments any number of rows each, none included.  The offsets are
  * those of moe_group_by_expert (x holds the routes' rows in the order of
- * route_idx) or any ascending ones; they are read on the device.
+ * route_idx; it takes at most MOE_MAX_B tokens) or any ascending ones; they
+ * are read on the device.
  * In:  x [R, K] bf16, w [E, N, K] bf16, offsets [E+1] int32.
  * Out: y [R, N] fp32 or bf16 (y_dtype), sums in fp32, one rounding to bf16.
  *      The tensor cores' additions truncate: up to 2^-18 of the sum of

@@ -607,7 +607,12 @@ def stack_forward(x, layers, top_k, flags=0, stream=None, status=None):
 
 # ------------------------------------------------- grouped products and NVFP4
 # (checks and marshalling kept short: these calls serve single decoded tokens,
-# whose kernels take less time than a careless call)
+# whose kernels take less time than a careless call; the stream's handle comes
+# from torch's private getter, 0.1 us, where the public one makes an object, 1.1)
+#
+# None of them records an autograd graph: results are detached, whatever the
+# inputs require.  A training step calls grouped_gemm, grouped_gemm_dx and
+# grouped_gemm_dw itself, for instance in a torch.autograd.Function.
 _OUT = {torch.float32: MOE_DT_F32, torch.bfloat16: MOE_DT_BF16}
 
 
@@ -673,8 +678,10 @@ def grouped_gemm(x, w, offsets, out_dtype=torch.float32, out=None, status=None, 
     """y [R,N]: row r of segment e (offsets[e] <= r < offsets[e+1]) is w[e] x[r].
 
     x [R,K] bf16, w [E,N,K] bf16, offsets [E+1] int32 on the device (as
-    group_by_expert returns them).  Rows that no segment holds are left as
-    they were in `out`, and are undefined in a new tensor."""
+    group_by_expert returns them; beyond its MAX_B tokens, any ascending ones).
+    Rows that no segment holds are left as they were in `out`, and are
+    undefined in a new tensor.  The result is detached: gradients come from
+    grouped_gemm_dx and grouped_gemm_dw, called by the user."""
     try:
         R, K = x.shape
         E, N, _ = w.shape
@@ -826,7 +833,8 @@ def _grouped_nvfp4(handle, xq, xbs, xgs, wq, wbs, wgs, offsets, R, N, K, E, out_
 def grouped_gemm_nvfp4(xq, xbs, xgs, wq, wbs, wgs, offsets, out_dtype=torch.float32, out=None, status=None,
                        stream=None):
     """grouped_gemm with both operands in NVFP4: x as quantize_nvfp4 returns a
-    [R,K] tensor (a scale a row), w as it returns [E,N,K] (a scale a matrix)."""
+    [R,K] tensor (a scale a row), w as it returns [E,N,K] (a scale a matrix).
+    Detached, and without gradients."""
     try:
         R, half = xq.shape
         E, N, _ = wq.shape
