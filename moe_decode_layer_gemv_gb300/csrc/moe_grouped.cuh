@@ -16,11 +16,12 @@
 // The segments are read on the device: no launch depends on their sizes.
 //
 // Measured (L2 flushed): 65536 rows over 64 experts of 1536 x 2048, paired
-// tiles: forward 247 us (1670 TFLOP/s, tensor pipe 77 % busy, 12 TB/s from L2),
-// dx 249, dw 248; 19 even segments of 4096 rows: 1870 TFLOP/s and more, the
-// ragged ends and the last round cost the rest.  With few rows the weights'
-// (dw: the gradients') bytes bound it: 512 rows over 256 experts 202 us, the
-// copy bandwidth.
+// tiles: forward 249 us (1655 TFLOP/s, tensor pipe 78 % busy, 12 TB/s from L2),
+// dx 254, dw 254 (call after call without a pause, at the power limit: 289,
+// 288, 287); 19 even segments of 4096 rows: 1830 to 1865 TFLOP/s, the ragged
+// ends and the last round cost the rest.  With few rows the weights' (dw: the
+// gradients') bytes bound it: 512 rows over 256 experts 206 us, the copy
+// bandwidth.
 #pragma once
 
 #include "moe_common.cuh"
