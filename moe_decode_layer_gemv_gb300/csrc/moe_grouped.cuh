@@ -41,7 +41,7 @@ constexpr uint32_t kGgWaitLimit = 1u << 17;  // ... and gives up after so many t
 constexpr uint32_t kGgTmemCols = 512;
 // The tensor cores add to an accumulator with truncation, which makes a sum
 // smaller with every addition: sums of one sign by 1.0e-6 in 64 MMAs (16 deep),
-// by 7.4e-5 in 1024 and by 1.6e-3 in 16384, most of half a bf16 step.  So an
+// by 7.4e-5 in 1024 and by 1.5e-3 in 16384, most of half a bf16 step.  So an
 // accumulator takes at most so many 64-wide steps, 64 MMAs, whatever the
 // result's type; the parts are added in fp32, rounded to nearest.
 constexpr int kGgPartSteps = 16;
