@@ -74,6 +74,10 @@ typedef enum {
 /* activation dtypes */
 typedef enum { MOE_DT_F32 = 0, MOE_DT_BF16 = 1 } moe_dtype;
 
+/* activations of the gated unit */
+#define MOE_ACT_SILU 0  /* g / (1 + exp(-g)) */
+#define MOE_ACT_GELU 1  /* the tanh form: g (1 + tanh(sqrt(2/pi) (g + 0.044715 g^3))) / 2 */
+
 /* limits */
 #define MOE_MAX_E 256
 #define MOE_MAX_TOPK 8
@@ -361,6 +365,36 @@ int moe_grouped_gemm_dw_workspace_bytes(int R, int N, int K, int E, size_t* byte
 int moe_grouped_gemm_dw(const uint16_t* dy, const uint16_t* x, const int32_t* offsets, int R, int N, int K, int E,
                         void* dw, int dw_dtype, void* workspace, size_t workspace_bytes, int32_t* dev_status,
                         void* stream);
+
+/*
+ * moe_grouped_glu -- the experts' gated unit: both projections, the
+ * activation and the product in one kernel.  For row r of segment e
+ *   g = gate_up[e, i, :] . x[r, :],  u = gate_up[e, I + i, :] . x[r, :]
+ *   h[r, i] = act(g) u          (act: MOE_ACT_*)
+ * x [R, H] bf16, gate_up [E, 2I, H] bf16 (rows [0, I) gate, [I, 2I) up),
+ * h [R, I] fp32 or bf16 (h_dtype); gu [R, 2I] bf16 or NULL receives (g, u),
+ * which moe_grouped_glu_backward starts from.  g and u are fp32 sums; h is
+ * made from them before they are rounded.  moe_grouped_gemm with w = down
+ * completes the block.  R, offsets, segments and dev_status as in
+ * moe_grouped_gemm; H and I multiples of 8 in [8, MOE_MAX_DIM].  An infinite
+ * g gives what the formula gives (NaN at -infinity).
+ */
+int moe_grouped_glu(const uint16_t* x, const uint16_t* gate_up, const int32_t* offsets, int R, int H, int I, int E, int act,
+                    void* h, int h_dtype, uint16_t* gu, int32_t* dev_status, void* stream);
+
+/*
+ * moe_grouped_glu_backward -- the gradient of moe_grouped_gemm(h, down) after
+ * moe_grouped_glu with respect to (g, u), in one kernel: with
+ *   dh[r, i] = sum_n down[e, n, i] dy[r, n]      (fp32, never stored)
+ *   dgu[r, i] = dh u act'(g),  dgu[r, I + i] = dh act(g),  h[r, i] = act(g) u
+ * dy [R, H], down [E, H, I], gu [R, 2I] bf16 (as moe_grouped_glu left it);
+ * dgu [R, 2I] and h [R, I] bf16.  The rest of the block's backward pass is
+ * moe_grouped_gemm_dx(dgu, gate_up), moe_grouped_gemm_dw(dgu, x) and
+ * moe_grouped_gemm_dw(dy, h): h is made again here, so that the forward pass
+ * need not keep it.  dgu may not overlap gu.  Otherwise as moe_grouped_glu.
+ */
+int moe_grouped_glu_backward(const uint16_t* dy, const uint16_t* down, const uint16_t* gu, const int32_t* offsets, int R,
+                             int H, int I, int E, int act, uint16_t* dgu, uint16_t* h, int32_t* dev_status, void* stream);
 
 /*
  * moe_quantize_nvfp4 -- matrices into the NVFP4 layout of

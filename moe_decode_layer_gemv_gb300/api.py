@@ -51,6 +51,8 @@ _lib.moe_quantize_nvfp4_workspace_bytes.argtypes = [_I, _I, _I, ctypes.POINTER(_
 _lib.moe_quantize_nvfp4.argtypes = [_P, _I, _I, _I, _I, _P, _P, _P, _P, _S, _P, _P]
 _lib.moe_dequantize_nvfp4.argtypes = [_P, _P, _P, _I, _I, _I, _P, _I, _P]
 _lib.moe_grouped_gemm_nvfp4.argtypes = [_P, _P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _P, _I, _P, _P]
+_lib.moe_grouped_glu.argtypes = [_P, _P, _P, _I, _I, _I, _I, _I, _P, _I, _P, _P, _P]
+_lib.moe_grouped_glu_backward.argtypes = [_P, _P, _P, _P, _I, _I, _I, _I, _I, _P, _P, _P, _P]
 _lib.moe_workspace_grouping.argtypes = [_P, _S, _I, _I, _I, _I, _I, ctypes.POINTER(_P), ctypes.POINTER(_P),
                                         ctypes.POINTER(_P), ctypes.POINTER(_P)]
 _lib.moe_forward_path.argtypes = [_I, _I, _I, _I, _I, _I, _U, ctypes.POINTER(_I), ctypes.POINTER(_I)]
@@ -67,7 +69,8 @@ for _f in ("moe_workspace_bytes", "moe_route", "moe_group_by_expert", "moe_exper
            "moe_expert_forward_noalloc", "moe_layer_forward", "moe_stack_forward", "moe_stack_forward_norm",
            "moe_stack_forward_fp8", "moe_stack_forward_nvfp4", "moe_workspace_grouping", "moe_grouped_gemm",
            "moe_grouped_gemm_dx", "moe_grouped_gemm_dw", "moe_grouped_gemm_dw_workspace_bytes",
-           "moe_quantize_nvfp4_workspace_bytes", "moe_quantize_nvfp4", "moe_dequantize_nvfp4", "moe_grouped_gemm_nvfp4"):
+           "moe_quantize_nvfp4_workspace_bytes", "moe_quantize_nvfp4", "moe_dequantize_nvfp4", "moe_grouped_gemm_nvfp4",
+           "moe_grouped_glu", "moe_grouped_glu_backward"):
     getattr(_lib, _f).restype = ctypes.c_int
 
 EXPORTED = ("moe_workspace_bytes", "moe_route", "moe_group_by_expert", "moe_expert_forward",
@@ -75,6 +78,7 @@ EXPORTED = ("moe_workspace_bytes", "moe_route", "moe_group_by_expert", "moe_expe
             "moe_stack_forward_fp8", "moe_stack_forward_nvfp4", "moe_workspace_grouping",
             "moe_grouped_gemm", "moe_grouped_gemm_dx", "moe_grouped_gemm_dw", "moe_grouped_gemm_dw_workspace_bytes",
             "moe_quantize_nvfp4_workspace_bytes", "moe_quantize_nvfp4", "moe_dequantize_nvfp4", "moe_grouped_gemm_nvfp4",
+            "moe_grouped_glu", "moe_grouped_glu_backward",
             "moe_launch_count", "moe_forward_path", "moe_set_trace_buffer",
             "moe_inject_barrier_stall", "moe_status_string")
 
@@ -99,6 +103,8 @@ MOE_F_NO_TC = 8
 MOE_F_NO_PREFETCH = 16
 MOE_F_HOT_L2 = 32
 MOE_F_SPLIT_TC = 64
+MOE_ACT_SILU = 0
+MOE_ACT_GELU = 1
 TC_MIN_ROUTES = 8
 MAX_E, MAX_TOPK, MAX_B, MAX_DIM, MAX_LAYERS = 256, 8, 1024, 16384, 64
 MAX_ROWS = 1 << 22
@@ -851,3 +857,87 @@ def grouped_gemm_nvfp4(xq, xbs, xgs, wq, wbs, wgs, offsets, out_dtype=torch.floa
     _is(offsets, "offsets", torch.int32, (E + 1,), i)
     return _on(i, stream, _grouped_nvfp4, xq, xbs, xgs, wq, wbs, wgs, offsets, R, N, K, E, out_dtype, out,
                _status_ptr(status, i))
+
+
+# ------------------------------------------- around the grouped products
+# (as above: short checks, no autograd graph)
+_ACT = {"silu": MOE_ACT_SILU, "gelu": MOE_ACT_GELU}
+
+
+def _act(act):
+    if act not in _ACT:
+        raise ValueError(f"act must be one of {', '.join(_ACT)}, got {act!r}")
+    return _ACT[act]
+
+
+def _glu(handle, x, gate_up, offsets, R, H, I, E, act, keep, out_dtype, out, gu, st):
+    h = _out(out, (R, I), out_dtype, x)
+    if keep and gu is None:
+        gu = torch.empty((R, 2 * I), dtype=torch.bfloat16, device=x.device)
+    rc = _lib.moe_grouped_glu(x.data_ptr(), gate_up.data_ptr(), offsets.data_ptr(), R, H, I, E, act, h.data_ptr(),
+                              _OUT[h.dtype], None if gu is None else gu.data_ptr(), st, handle)
+    if rc:
+        raise MoeError("moe_grouped_glu", rc)
+    return h if gu is None else (h, gu)
+
+
+def grouped_glu(x, gate_up, offsets, act="silu", keep=False, out_dtype=torch.bfloat16, out=None, gu=None, status=None,
+                stream=None):
+    """h [R,I]: the experts' gated unit, act(g) u with g and u the halves of
+    gate_up[e] x[r] for row r of segment e; or (h, gu) with keep (or a gu to
+    be written): gu [R,2I] bf16 is what grouped_glu_backward starts from.
+
+    x [R,H] bf16, gate_up [E,2I,H] bf16 (gate rows, then up rows), offsets as
+    in grouped_gemm, which takes h on to the down projection.  act: "silu" or
+    "gelu" (its tanh form).  Rows that no segment holds are left as they were
+    in `out` and `gu`, and are undefined in new tensors.  Detached."""
+    try:
+        R, H = x.shape
+        E, I2, _ = gate_up.shape
+    except ValueError:
+        raise _bad_dims(x=x, gate_up=gate_up) from None
+    if I2 % 2:
+        raise ValueError(f"gate_up has shape {tuple(gate_up.shape)}, expected [E, 2I, {H}]")
+    i, I, code = x.get_device(), I2 // 2, _act(act)
+    _is(x, "x", torch.bfloat16, (R, H), i)
+    _is(gate_up, "gate_up", torch.bfloat16, (E, I2, H), i)
+    _is(offsets, "offsets", torch.int32, (E + 1,), i)
+    if gu is not None:
+        _is(gu, "gu", torch.bfloat16, (R, I2), i)
+    return _on(i, stream, _glu, x, gate_up, offsets, R, H, I, E, code, keep, out_dtype, out, gu, _status_ptr(status, i))
+
+
+def _glu_backward(handle, dy, down, gu, offsets, R, H, I, E, act, dgu, h, st):
+    if dgu is None:
+        dgu = torch.empty((R, 2 * I), dtype=torch.bfloat16, device=dy.device)
+    if h is None:
+        h = torch.empty((R, I), dtype=torch.bfloat16, device=dy.device)
+    rc = _lib.moe_grouped_glu_backward(dy.data_ptr(), down.data_ptr(), gu.data_ptr(), offsets.data_ptr(), R, H, I, E, act,
+                                       dgu.data_ptr(), h.data_ptr(), st, handle)
+    if rc:
+        raise MoeError("moe_grouped_glu_backward", rc)
+    return dgu, h
+
+
+def grouped_glu_backward(dy, down, gu, offsets, act="silu", dgu=None, h=None, status=None, stream=None):
+    """(dgu [R,2I], h [R,I]) bf16: from dy [R,H], the gradient of
+    grouped_gemm(h, down, offsets), that of gu, and h once more.
+
+    down [E,H,I] bf16, gu as grouped_glu kept it.  The block's other gradients
+    are grouped_gemm_dx(dgu, gate_up, offsets), grouped_gemm_dw(dgu, x,
+    offsets) and grouped_gemm_dw(dy, h, offsets).  `dgu` may not overlap gu."""
+    try:
+        R, H = dy.shape
+        E, _, I = down.shape
+    except ValueError:
+        raise _bad_dims(dy=dy, down=down) from None
+    i, code = dy.get_device(), _act(act)
+    _is(dy, "dy", torch.bfloat16, (R, H), i)
+    _is(down, "down", torch.bfloat16, (E, H, I), i)
+    _is(gu, "gu", torch.bfloat16, (R, 2 * I), i)
+    _is(offsets, "offsets", torch.int32, (E + 1,), i)
+    if dgu is not None:
+        _is(dgu, "dgu", torch.bfloat16, (R, 2 * I), i)
+    if h is not None:
+        _is(h, "h", torch.bfloat16, (R, I), i)
+    return _on(i, stream, _glu_backward, dy, down, gu, offsets, R, H, I, E, code, dgu, h, _status_ptr(status, i))

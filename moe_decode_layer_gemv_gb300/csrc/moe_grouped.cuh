@@ -32,6 +32,11 @@ namespace moe {
 
 enum { kGgFwd = 0, kGgDx = 1, kGgDw = 2 };
 
+// What the epilogue makes of a tile: the product itself; a gated unit of a
+// forward product's gate and up rows; the gated unit's gradient of a dx
+// product.
+enum { kGgStore = 0, kGgGlu = 1, kGgGluBack = 2 };
+
 constexpr int kGgMaxStages = 12;
 constexpr int kGgBoxN = 32;          // rows per TMA box of a K-major B operand
 constexpr int kGgTile = 128 * 128;   // bytes of one 128 x 64 bf16 operand tile
@@ -57,6 +62,10 @@ struct GgParams {
     int split; // dw: parts that each segment's rows are cut into, part p's result at out + p E NW M
     void* out;
     int a_blocked, b_blocked;  // MN-major operands: the map has a 64-column block dimension
+    // gated units
+    void* out2;      // forward: gu [R, 2 M] bf16, or nullptr; backward: h [R, M] bf16
+    const void* in;  // backward: gu
+    float c0, c1;    // the activation's coefficients
     CUtensorMap zero[4];  // dw: boxes of 64 columns x 8, 4, 2 and 1 rows, for rows of zeros from behind x's end
     int32_t* status;
 };
@@ -149,6 +158,23 @@ __device__ __forceinline__ void gg_load4(uint32_t dst, const CUtensorMap* map, i
             "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2 [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(
                 dst),
             "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(bar)
+            : "memory");
+}
+
+template <int CG>
+__device__ __forceinline__ void gg_load5(uint32_t dst, const CUtensorMap* map, int c0, int c1, int c2, int c3, int c4,
+                                         uint32_t bar) {
+    if (CG == 1)
+        asm volatile(
+            "cp.async.bulk.tensor.5d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5, %6}], [%7];" ::"r"(
+                dst),
+            "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(c4), "r"(bar)
+            : "memory");
+    else
+        asm volatile(
+            "cp.async.bulk.tensor.5d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2 [%0], [%1, {%2, %3, %4, %5, %6}], [%7];" ::"r"(
+                dst),
+            "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(c4), "r"(bar)
             : "memory");
 }
 
@@ -537,12 +563,121 @@ __device__ __forceinline__ void gg_gather(uint32_t taddr, uint32_t (&sum)[COLS /
     }
 }
 
+// ------------------------------------------------------------- gated units
+// act(g) = g s(q), s the logistic function and q = g (c0 + c1 g^2): SiLU with
+// c0 = 1, c1 = 0, GELU's tanh form with c0 = 2 sqrt(2 / pi), c1 = 0.044715 c0
+// (g (1 + tanh(q / 2)) / 2 = g s(q)).
+//   act'(g) = s + g s (1 - s) q',   q' = c0 + 3 c1 g^2
+// g^2 is kept finite, so that c1 = 0 and s = 0 or 1 count for what they are.
+__device__ __forceinline__ float glu_act(float g, float c0, float c1, float& grad) {
+    const float gg = fminf(g * g, 1e30f);
+    const float s = __fdividef(1.0f, 1.0f + expf(-g * fmaf(c1, gg, c0)));
+    const float a = g * s;
+    grad = fmaf(a * (1.0f - s), fmaf(3.0f * c1, gg, c0), s);
+    return a;
+}
+
+// The gated unit of a forward tile.  A CTA's 128 rows are gate rows and up
+// rows in alternating groups of eight (one five-dimensional copy brings them
+// so), which leaves g and u of one output eight lanes apart: each lane of the
+// pair gives the other one of two rows' values and makes one row's result.  i0:
+// the first of this warp's 16 outputs.  (Gate and up rows in halves of the
+// tile, exchanged through shared memory, would need barriers between warps;
+// two accumulators with g and u in one lane 5/4 of the copies from L2.)
+template <int COLS, bool F32, typename P>
+__device__ __forceinline__ void glu_store(const P& p, uint32_t (&sum)[COLS / 32][32], size_t row0, int mine, int i0,
+                                          int lane) {
+    const int up = (lane >> 3) & 1, i = i0 + ((lane >> 4) << 3) + (lane & 7), I = p.M;
+    const int col = i < I ? i + (up ? I : 0) : 2 * I;
+#pragma unroll
+    for (int k = 0; k < COLS / 32; ++k) {
+        const int nc = mine - 32 * k;
+        if (nc <= 0) break;
+        uint32_t(&r)[32] = sum[k];
+        if (p.out2) gg_store32(r, p.out2, 0, row0 + 32 * k, min(32, nc), col, 2 * I);
+        const size_t at = (row0 + 32 * k + up) * (size_t)I + i;
+        const int last = i < I ? nc - up : 0;
+#pragma unroll
+        for (int j = 0; j < 32; j += 2) {
+            const uint32_t got = __shfl_xor_sync(0xffffffffu, up ? r[j] : r[j + 1], 8);
+            const float g = __uint_as_float(up ? got : r[j]), u = __uint_as_float(up ? r[j + 1] : got);
+            float grad;
+            const float h = glu_act(g, p.c0, p.c1, grad) * u;
+            if (j < last) {
+                if (F32)
+                    static_cast<float*>(p.out)[at + (size_t)j * I] = h;
+                else
+                    static_cast<uint16_t*>(p.out)[at + (size_t)j * I] = f2bf_bits(h);
+            }
+        }
+    }
+}
+
+__device__ __forceinline__ uint32_t ld_input_u32(const void* p) {
+    uint32_t r;
+    asm volatile("ld.global.u32 %0, [%1];" : "=r"(r) : "l"(p));
+    return r;
+}
+
+// The gated unit's gradient of a dx tile (dh), this lane's m of rows row0 on:
+//   dg = dh u act'(g),  du = dh act(g),  h = act(g) u
+// g and u come as gg_store32 leaves them, two neighbouring m of one row in
+// each lane, and the results go the same way.
+template <int COLS, typename P>
+__device__ __forceinline__ void glu_back_store(const P& p, const uint32_t (&sum)[COLS / 32][32], size_t row0, int mine,
+                                               int m) {
+    const int I = p.M, odd = m & 1;
+    const uint32_t sel = gg_pair_select(odd);
+    const int last = m < I ? mine - odd : 0;  // rows row0 + odd + j, j < last
+    const uint16_t* in = static_cast<const uint16_t*>(p.in) + (row0 + odd) * 2 * (size_t)I + (m - odd);
+    uint16_t* dgu = static_cast<uint16_t*>(p.out) + (row0 + odd) * 2 * (size_t)I + (m - odd);
+    uint16_t* hp = static_cast<uint16_t*>(p.out2) + (row0 + odd) * (size_t)I + (m - odd);
+    constexpr int B = 16;  // rows whose g and u are loaded ahead of the ones at work
+    uint32_t g[B / 2], u[B / 2];
+    auto fetch = [&](int c) {
+#pragma unroll
+        for (int j = 0; j < B; j += 2) {
+            g[j / 2] = u[j / 2] = 0;
+            if (c + j < last) {
+                g[j / 2] = ld_input_u32(in + (size_t)(c + j) * 2 * I);
+                u[j / 2] = ld_input_u32(in + (size_t)(c + j) * 2 * I + I);
+            }
+        }
+    };
+    fetch(0);
+#pragma unroll
+    for (int c = 0; c < COLS; c += B) {
+        if (c >= mine) break;
+        uint32_t gc[B / 2], uc[B / 2];
+#pragma unroll
+        for (int j = 0; j < B / 2; ++j) gc[j] = g[j], uc[j] = u[j];
+        if (c + B < COLS) fetch(c + B);
+#pragma unroll
+        for (int j = 0; j < B; j += 2) {
+            // rows j (low halves) and j + 1 (high halves) of this lane's m
+            const uint32_t gp = gg_pair(gc[j / 2], sel), up = gg_pair(uc[j / 2], sel);
+            const float2 gf = bf16x2_to_f2(gp), uf = bf16x2_to_f2(up);
+            const float d0 = __uint_as_float(sum[(c + j) / 32][(c + j) % 32]);
+            const float d1 = __uint_as_float(sum[(c + j) / 32][(c + j) % 32 + 1]);
+            float e0, e1;
+            const float a0 = glu_act(gf.x, p.c0, p.c1, e0), a1 = glu_act(gf.y, p.c0, p.c1, e1);
+            auto put = [&](uint16_t* to, float v0, float v1) {
+                const uint32_t v = gg_pair(gg_pack(__float_as_uint(v0), __float_as_uint(v1)), sel);
+                if (c + j < last) *reinterpret_cast<uint32_t*>(to) = v;
+            };
+            put(dgu + (size_t)(c + j) * 2 * I, d0 * uf.x * e0, d1 * uf.y * e1);
+            put(dgu + (size_t)(c + j) * 2 * I + I, d0 * a0, d1 * a1);
+            put(hp + (size_t)(c + j) * I, a0 * uf.x, a1 * uf.y);
+        }
+    }
+}
+
 // ------------------------------------------------------------- the kernel
 // Persistent: one CTA per SM (or one pair of CTAs per SM pair) walks the
 // tiles.  Three roles run through the same tile sequence, each at its own
 // pace: the producer fills the ring, the MMA issuer accumulates tile d into
 // tensor-memory buffer d mod 2, the epilogue warps read the other buffer out.
-template <int MODE, int CG, bool F32>
+template <int MODE, int CG, bool F32, int EP = kGgStore>
 __global__ void __launch_bounds__((GgCfg<MODE, CG, F32>::kThreads), 1) gg_kernel(const __grid_constant__ GgParams p) {
     using Cfg = GgCfg<MODE, CG, F32>;
     extern __shared__ __align__(1024) unsigned char gg_smem_raw[];
@@ -575,7 +710,8 @@ __global__ void __launch_bounds__((GgCfg<MODE, CG, F32>::kThreads), 1) gg_kernel
     }
     if (warp == Cfg::EPI + 1) gg_tmem_alloc<CG>(&sh->tmem_slot, kGgTmemCols);
     grid_dep_wait();
-    const int mtiles = (p.M + Cfg::BM - 1) / Cfg::BM;
+    constexpr int MW = EP == kGgGlu ? 64 : 128, BMW = MW * CG;  // outputs that a CTA's 128 rows and a tile give
+    const int mtiles = (p.M + BMW - 1) / BMW;
     gg_segments(sh, p.offsets, p.E, p.R, Cfg::BN, p.status);
     tc_fence_before();
     __syncthreads();
@@ -606,7 +742,7 @@ __global__ void __launch_bounds__((GgCfg<MODE, CG, F32>::kThreads), 1) gg_kernel
             if (MODE == kGgDw) {
                 e = w.outer;
                 const int tn = w.inner / mtiles;
-                m0 = (w.inner - tn * mtiles) * Cfg::BM;
+                m0 = (w.inner - tn * mtiles) * BMW;
                 n0 = tn * Cfg::BN;
                 n = min(Cfg::BN, p.NW - n0);
                 const int seg = p.split == 1 ? e : e % p.E, cnt = sh->cnt[seg];
@@ -619,7 +755,7 @@ __global__ void __launch_bounds__((GgCfg<MODE, CG, F32>::kThreads), 1) gg_kernel
                 len = min(part, cnt - at);
             } else {
                 e = gg_seek(sh->start, p.E, w.outer, e);
-                m0 = w.inner * Cfg::BM;
+                m0 = w.inner * BMW;
                 n0 = (w.outer - sh->start[e]) * Cfg::BN;
                 n = min(Cfg::BN, sh->cnt[e] - n0);
                 q0 = sh->p0[e] + n0;
@@ -639,7 +775,7 @@ __global__ void __launch_bounds__((GgCfg<MODE, CG, F32>::kThreads), 1) gg_kernel
                 // rows of B that this CTA holds (forward, dx), in whole boxes
                 const int rows = MODE == kGgDw ? 128 : (n + kGgBoxN * CG - 1) / (kGgBoxN * CG) * kGgBoxN;
                 const uint32_t bytes = CG * (kGgTile + (uint32_t)rows * 128u);
-                const int am = m0 + (int)rank * 128, bn = (MODE == kGgDw ? n0 : q0) + (int)rank * rows;
+                const int am = m0 + (int)rank * MW, bn = (MODE == kGgDw ? n0 : q0) + (int)rank * rows;
                 for (int k0 = 0; k0 < nk; k0 += Cfg::KSUB) {
                     if (!gg_wait(&sh->empty[r.s], r.ph ^ 1u, &sh->abort)) return false;
                     const uint32_t st = ring_at + r.s * stage_bytes, bar = bars + r.s * 8u;
@@ -660,7 +796,9 @@ __global__ void __launch_bounds__((GgCfg<MODE, CG, F32>::kThreads), 1) gg_kernel
                         if (u >= ke) break;
                         const uint32_t sa = st + u * kGgTile, sb = st + b_off + u * b_tile;
                         const int c = (k0 + u) * 64;
-                        if (MODE == kGgFwd) {
+                        if (EP == kGgGlu) {
+                            gg_load5<CG>(sa, &p.ta, c, 0, 0, am >> 3, e, bar);
+                        } else if (MODE == kGgFwd) {
                             gg_load3<CG>(sa, &p.ta, c, am, e, bar);
                         } else if (MODE == kGgDx) {
                             if (p.a_blocked) {
@@ -832,6 +970,14 @@ __global__ void __launch_bounds__((GgCfg<MODE, CG, F32>::kThreads), 1) gg_kernel
                 buf ^= 1;
                 if (buf == 0) full_ph ^= 1u;
             }
+            if constexpr (EP == kGgGlu) {
+                glu_store<Cfg::COLS, F32>(p, sum, row0, mine, m0 + (int)rank * MW + (warp & 3) * 16, lane);
+                return true;
+            }
+            if constexpr (EP == kGgGluBack) {
+                glu_back_store<Cfg::COLS>(p, sum, row0, mine, m);
+                return true;
+            }
 #pragma unroll
             for (int i = 0; i < Cfg::COLS / 32; ++i)
                 if (32 * i < mine) gg_store32(sum[i], p.out, F32, row0 + 32 * i, min(32, mine - 32 * i), m, p.M);
@@ -850,7 +996,7 @@ __global__ void __launch_bounds__((GgCfg<MODE, CG, F32>::kThreads), 1) gg_kernel
 // dw of a split launch: the parts' sums in a fixed order.  A block takes 32
 // pieces of four values; its eight warps sum every eighth part, and the first
 // adds their sums.
-__global__ void __launch_bounds__(256) gg_join_kernel(const float4* parts, size_t n4, int split, void* out,
+static __global__ void __launch_bounds__(256) gg_join_kernel(const float4* parts, size_t n4, int split, void* out,
                                                       int out_f32) {
     __shared__ float4 s_sum[8][32];
     grid_dep_wait();

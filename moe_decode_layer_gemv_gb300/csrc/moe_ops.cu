@@ -8,84 +8,10 @@
 #include "moe.h"
 #include "moe_grouped.cuh"
 #include "moe_host.cuh"
+#include "moe_launch.cuh"
 #include "moe_nvfp4.cuh"
 
 namespace moe {
-
-// A tensor map over a row-major tensor [outer2, outer1, inner] (outer2 = 0:
-// two dimensions) with boxes of box_bytes x box_rows (128 or 64 bytes, the
-// swizzle of that width); elements outside the tensor read as zeros.
-static bool encode_map(CUtensorMap* map, const void* base, int elem, uint64_t inner, uint64_t outer1, uint64_t outer2,
-                       uint32_t box_rows, uint32_t box_bytes = 128) {
-    EncodeTiledFn fn = encode_fn();
-    if (!fn) return false;
-    const uint64_t pitch = inner * elem;
-    const cuuint64_t dims[3] = {inner, outer1, outer2};
-    const cuuint64_t strides[2] = {pitch, pitch * outer1};
-    const cuuint32_t box[3] = {box_bytes / (uint32_t)elem, box_rows, 1};
-    const cuuint32_t estr[3] = {1, 1, 1};
-    return fn(map, elem == 1 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, outer2 ? 3 : 2,
-              const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-              box_bytes == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
-              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
-// A map over bf16 [outer2, outer1, inner] (outer2 = 0: [outer1, inner]) whose
-// boxes are 64 rows x two 64-column blocks: inner % 64 == 0.
-static bool encode_blocked(CUtensorMap* map, const void* base, uint64_t inner, uint64_t outer1, uint64_t outer2) {
-    EncodeTiledFn fn = encode_fn();
-    if (!fn) return false;
-    const cuuint64_t dims[4] = {64, outer1, inner / 64, outer2};
-    const cuuint64_t strides[3] = {inner * 2, 128, inner * outer1 * 2};
-    const cuuint32_t box[4] = {64, 64, 2, 1};
-    const cuuint32_t estr[4] = {1, 1, 1, 1};
-    return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, outer2 ? 4 : 3, const_cast<void*>(base), dims, strides, box, estr,
-              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
-static int check_grouped(int R, int N, int K, int E, int dtype) {
-    if (R < 0 || R > MOE_MAX_ROWS || E < 1 || E > MOE_MAX_E) return MOE_ERR_INVALID_ARG;
-    if (N < 8 || N > 2 * MOE_MAX_DIM || (N & 7) || K < 8 || K > MOE_MAX_DIM || (K & 7)) return MOE_ERR_INVALID_ARG;
-    if (dtype != MOE_DT_F32 && dtype != MOE_DT_BF16) return MOE_ERR_INVALID_ARG;
-    return MOE_OK;
-}
-
-// A persistent kernel on every SM, in clusters of CG CTAs.
-template <int CG, typename K, typename P>
-static int launch_persistent(K kernel, const P& p, int threads, int sms, cudaStream_t st) {
-    const int rc = allow_smem(kernel, kGgSmem);
-    if (rc) return rc;
-    cudaLaunchConfig_t cfg;
-    memset(&cfg, 0, sizeof cfg);
-    cfg.gridDim = dim3((unsigned)(sms / CG * CG));
-    cfg.blockDim = dim3((unsigned)threads);
-    cfg.dynamicSmemBytes = kGgSmem;
-    cfg.stream = st;
-    cudaLaunchAttribute attr[2];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    attr[1].id = cudaLaunchAttributeClusterDimension;
-    attr[1].val.clusterDim.x = CG;
-    attr[1].val.clusterDim.y = 1;
-    attr[1].val.clusterDim.z = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = CG > 1 ? 2 : 1;
-    return launch_ex(cfg, kernel, p);
-}
-
-// The paired tile (256 x 256) from so many rows a segment on average, where
-// the output is wider than a single CTA's tile.  Measured on 64 experts of
-// 1536 x 2048, single and paired, at 96 / 128 / 256 rows: forward to bf16 80 /
-// 85 / 113 and 82 / 85 / 98 us, to fp32 82 / 88 / 120 and 83 / 86 / 106, dx to
-// bf16 72 / 82 / 116 and 73 / 75 / 99.
-// Weight gradients of few rows are all stores: in bf16 the pair's larger tiles
-// are always ahead (16 rows: 101 and 96 us), in fp32 late (192 rows: 157 and
-// 161; 256: 180 and 159; 1024: 425 and 300; of 2048 x 768, 192 rows: 82 and 88,
-// 256: 94 and 89).
-constexpr int kGgPairRows = 128, kGgPairRowsDw = 0, kGgPairRowsDwF32 = 256;
-
-static bool gg_pairs(int R, int M, int E, int rows = kGgPairRows) { return M > 128 && (int64_t)R >= (int64_t)rows * E; }
 
 // dw: with fewer tiles than CTAs (or pairs) the segments' rows are cut into
 // parts, of 512 rows on average at least, whose sums are joined afterwards.
