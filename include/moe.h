@@ -397,6 +397,51 @@ int moe_grouped_glu_backward(const uint16_t* dy, const uint16_t* down, const uin
                              int H, int I, int E, int act, uint16_t* dgu, uint16_t* h, int32_t* dev_status, void* stream);
 
 /*
+ * moe_combine_norm -- what joins a block to the residual stream, in one
+ * kernel: the weighted sum of a token's rows, a norm behind the block, the
+ * residual add with its scale, and the norm before the next block
+ * ("TEXT Generation Optimization Report", Fused Operations:
+ * fused_rms_norm_residual; RMSNorm as in moe_stack_forward_norm).
+ *   z[t] = sum_j w[t, j] o[pos[t, j]]
+ *   b    = z / sqrt(mean(z^2) + eps) post     (post NULL: b = z)
+ *   y    = x + scale b
+ *   n    = y / sqrt(mean(y^2) + eps) pre      (pre NULL: no n)
+ * x [T, H] (x_dtype), o [R, H] (o_dtype) the block's rows, grouped as
+ * moe_group_by_expert sorts them; pos [T, k] int32 the row of each route
+ * (pos[route_idx[i]] = i), -1 for one that was dropped; NULL: row t k + j.  w
+ * [T, k] fp32 (NULL: ones), k <= MOE_MAX_TOPK; post, scale, pre [H] fp32
+ * (scale NULL: the number scale_all); eps in [0, 1].  y [T, H] of x's type
+ * (may alias x), n [T, H] (n_dtype).  o NULL: the norm of x alone (no y).
+ * Sums in fp32; n is made from y before it is rounded.  A row outside
+ * [-1, R) counts as dropped and sets MOE_DEV_BAD_ROUTE.  H a multiple of 8 in
+ * [8, MOE_MAX_DIM], T and R at most MOE_MAX_ROWS.
+ */
+int moe_combine_norm(const void* x, int x_dtype, const void* o, int o_dtype, const int32_t* pos, const float* w, int T, int H,
+                     int R, int k, const float* post, const float* scale, float scale_all, const float* pre, float eps,
+                     void* y, void* n, int n_dtype, int32_t* dev_status, void* stream);
+
+/*
+ * moe_combine_norm_backward -- its gradients.  dy [T, H] (of y's type; NULL:
+ * zeros) and dn [T, H] (n_dtype; only with pre) are the gradients of y and n;
+ * y is what the forward pass left (read only with pre), the other inputs are
+ * its own.  dx [T, H] of y's type, d_o [R, H] of o's type, dw [T, k] fp32
+ * (NULL: not wanted), dpost, dscale, dpre [H] fp32, each for the vector that
+ * is given.  pos must name each row at most once, as a grouping's inverse
+ * does; rows that it does not name are left as they were in d_o, and dw is 0
+ * for dropped routes.  dx may alias dy, d_o may not alias o.  The column sums
+ * are joined in a fixed order (the same call gives the same bits) through the
+ * workspace, of moe_combine_norm_backward_workspace_bytes() (host-only, for
+ * the current device; sums: how many of post, scale and pre are given), used
+ * by one call at a time.
+ */
+int moe_combine_norm_backward_workspace_bytes(int T, int H, int sums, size_t* bytes);
+int moe_combine_norm_backward(const void* dy, const void* dn, int n_dtype, const void* y, int y_dtype, const void* o,
+                              int o_dtype, const int32_t* pos, const float* w, int T, int H, int R, int k, const float* post,
+                              const float* scale, float scale_all, const float* pre, float eps, void* dx, void* d_o, float* dw,
+                              float* dpost, float* dscale, float* dpre, void* workspace, size_t workspace_bytes,
+                              int32_t* dev_status, void* stream);
+
+/*
  * moe_quantize_nvfp4 -- matrices into the NVFP4 layout of
  * moe_stack_forward_nvfp4: x [G, rows, cols] fp32 or bf16 (x_dtype) into
  * q [G, rows, cols/2] (E2M1 codes two a byte, element 2i in the low nibble),

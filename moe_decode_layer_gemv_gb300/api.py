@@ -53,6 +53,11 @@ _lib.moe_dequantize_nvfp4.argtypes = [_P, _P, _P, _I, _I, _I, _P, _I, _P]
 _lib.moe_grouped_gemm_nvfp4.argtypes = [_P, _P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _P, _I, _P, _P]
 _lib.moe_grouped_glu.argtypes = [_P, _P, _P, _I, _I, _I, _I, _I, _P, _I, _P, _P, _P]
 _lib.moe_grouped_glu_backward.argtypes = [_P, _P, _P, _P, _I, _I, _I, _I, _I, _P, _P, _P, _P]
+_F = ctypes.c_float
+_lib.moe_combine_norm.argtypes = [_P, _I, _P, _I, _P, _P, _I, _I, _I, _I, _P, _P, _F, _P, _F, _P, _P, _I, _P, _P]
+_lib.moe_combine_norm_backward_workspace_bytes.argtypes = [_I, _I, _I, ctypes.POINTER(_S)]
+_lib.moe_combine_norm_backward.argtypes = [_P, _P, _I, _P, _I, _P, _I, _P, _P, _I, _I, _I, _I, _P, _P, _F, _P, _F, _P, _P, _P,
+                                           _P, _P, _P, _P, _S, _P, _P]
 _lib.moe_workspace_grouping.argtypes = [_P, _S, _I, _I, _I, _I, _I, ctypes.POINTER(_P), ctypes.POINTER(_P),
                                         ctypes.POINTER(_P), ctypes.POINTER(_P)]
 _lib.moe_forward_path.argtypes = [_I, _I, _I, _I, _I, _I, _U, ctypes.POINTER(_I), ctypes.POINTER(_I)]
@@ -70,7 +75,8 @@ for _f in ("moe_workspace_bytes", "moe_route", "moe_group_by_expert", "moe_exper
            "moe_stack_forward_fp8", "moe_stack_forward_nvfp4", "moe_workspace_grouping", "moe_grouped_gemm",
            "moe_grouped_gemm_dx", "moe_grouped_gemm_dw", "moe_grouped_gemm_dw_workspace_bytes",
            "moe_quantize_nvfp4_workspace_bytes", "moe_quantize_nvfp4", "moe_dequantize_nvfp4", "moe_grouped_gemm_nvfp4",
-           "moe_grouped_glu", "moe_grouped_glu_backward"):
+           "moe_grouped_glu", "moe_grouped_glu_backward", "moe_combine_norm", "moe_combine_norm_backward",
+           "moe_combine_norm_backward_workspace_bytes"):
     getattr(_lib, _f).restype = ctypes.c_int
 
 EXPORTED = ("moe_workspace_bytes", "moe_route", "moe_group_by_expert", "moe_expert_forward",
@@ -78,7 +84,8 @@ EXPORTED = ("moe_workspace_bytes", "moe_route", "moe_group_by_expert", "moe_expe
             "moe_stack_forward_fp8", "moe_stack_forward_nvfp4", "moe_workspace_grouping",
             "moe_grouped_gemm", "moe_grouped_gemm_dx", "moe_grouped_gemm_dw", "moe_grouped_gemm_dw_workspace_bytes",
             "moe_quantize_nvfp4_workspace_bytes", "moe_quantize_nvfp4", "moe_dequantize_nvfp4", "moe_grouped_gemm_nvfp4",
-            "moe_grouped_glu", "moe_grouped_glu_backward",
+            "moe_grouped_glu", "moe_grouped_glu_backward", "moe_combine_norm", "moe_combine_norm_backward",
+            "moe_combine_norm_backward_workspace_bytes",
             "moe_launch_count", "moe_forward_path", "moe_set_trace_buffer",
             "moe_inject_barrier_stall", "moe_status_string")
 
@@ -941,3 +948,149 @@ def grouped_glu_backward(dy, down, gu, offsets, act="silu", dgu=None, h=None, st
     if h is not None:
         _is(h, "h", torch.bfloat16, (R, I), i)
     return _on(i, stream, _glu_backward, dy, down, gu, offsets, R, H, I, E, code, dgu, h, _status_ptr(status, i))
+
+
+def _join_args(x, o, pos, w, post, scale, pre):
+    """The arguments that combine_norm and its gradients share, checked
+    -> (device, T, H, R, k, scale vector or None, scale number)."""
+    try:
+        T, H = x.shape
+        R, k = (0, 0) if o is None else (o.shape[0], 1)
+        if o is not None and o.dim() != 2:
+            raise ValueError
+        for t in (pos, w):
+            if t is not None:
+                _, k = t.shape
+    except ValueError:
+        raise _bad_dims(**{n: t for n, t in (("x", x), ("o", o), ("pos", pos), ("w", w)) if t is not None}) from None
+    i = x.get_device()
+    if o is None:
+        if pre is None:
+            raise ValueError("combine_norm needs rows (o), a norm (pre), or both")
+        if pos is not None or w is not None or post is not None:
+            raise ValueError("pos, w and post belong to rows: o is missing")
+        scale = 1.0
+    else:
+        if o.dtype not in _OUT:
+            raise TypeError("o must be float32 or bfloat16")
+        _is(o, "o", o.dtype, (R, H), i)
+        if pos is not None:
+            _is(pos, "pos", torch.int32, (T, k), i)
+        elif R < T * k:
+            raise ValueError(f"o has {R} rows, {T} tokens of {k} need {T * k}")
+        if w is not None:
+            _is(w, "w", torch.float32, (T, k), i)
+        if post is not None:
+            _is(post, "post", torch.float32, (H,), i)
+    if pre is not None:
+        _is(pre, "pre", torch.float32, (H,), i)
+    vector = None
+    if isinstance(scale, torch.Tensor):
+        vector, scale = scale, 1.0
+        _is(vector, "scale", torch.float32, (H,), i)
+    return i, T, H, R, k, vector, float(scale)
+
+
+def _opt_ptr(t):
+    # (an empty tensor has no address; to the library NULL means "not given", so any aligned one stands for it)
+    return None if t is None else t.data_ptr() or 16
+
+
+def _combine(handle, x, o, pos, w, T, H, R, k, post, vector, scale, pre, eps, n_dtype, y, n, st):
+    if o is None:
+        y = x
+    elif y is None:
+        y = torch.empty_like(x)
+    if pre is not None:
+        n = _out(n, (T, H), n_dtype, x)
+    rc = _lib.moe_combine_norm(x.data_ptr(), _OUT[x.dtype], _opt_ptr(o), _OUT[(x if o is None else o).dtype], _opt_ptr(pos),
+                               _opt_ptr(w), T, H, R, k, _opt_ptr(post), _opt_ptr(vector), scale, _opt_ptr(pre), eps,
+                               y.data_ptr(), _opt_ptr(n), MOE_DT_F32 if n is None else _OUT[n.dtype], st, handle)
+    if rc:
+        raise MoeError("moe_combine_norm", rc)
+    return y, n
+
+
+def combine_norm(x, o=None, pos=None, w=None, post=None, scale=1.0, pre=None, eps=1e-6, n_dtype=torch.bfloat16, y=None,
+                 n=None, status=None, stream=None):
+    """(y, n): a block's rows joined to the residual stream x [T,H], and the
+    next block's normed input,
+      z[t] = sum_j w[t,j] o[pos[t,j]],  b = rmsnorm(z) post (or z),
+      y = x + scale b,  n = rmsnorm(y) pre.
+
+    x fp32 or bf16; o [R,H] fp32 or bf16, the rows as grouped_gemm leaves
+    them; pos [T,k] int32, where the grouping put each route (route_idx's
+    inverse), -1 for a dropped one, by default row t k + j; w [T,k] fp32,
+    post and pre [H] fp32; scale a number or [H] fp32.  y and n are buffers to
+    be written (y may be x).  Without pre there is no n (None); without o it
+    is x's norm alone, and y is x.  Detached."""
+    _x_dtype(x)
+    i, T, H, R, k, vector, scale = _join_args(x, o, pos, w, post, scale, pre)
+    _is(x, "x", x.dtype, (T, H), i)
+    if y is not None:
+        if o is None:
+            raise ValueError("y is x where there are no rows (o)")
+        _is(y, "y", x.dtype, (T, H), i)
+    if n is not None and pre is None:
+        raise ValueError("n needs its norm's weights (pre)")
+    return _on(i, stream, _combine, x, o, pos, w, T, H, R, k, post, vector, scale, pre, eps, n_dtype, y, n,
+               _status_ptr(status, i))
+
+
+def _combine_backward(handle, dy, dn, y, o, pos, w, T, H, R, k, post, vector, scale, pre, eps, dx, do, workspace, st):
+    if dx is None:
+        dx = torch.empty_like(y)
+    f32 = lambda *shape: torch.empty(shape, dtype=torch.float32, device=y.device)  # noqa: E731
+    if o is not None and do is None:
+        do = torch.empty_like(o)
+    dw = f32(T, k) if w is not None else None
+    dpost, dscale, dpre = (f32(H) if t is not None else None for t in (post, vector, pre))
+    wp, wn = None, 0
+    if post is not None or vector is not None or pre is not None:
+        if workspace is None:
+            size = _S(0)
+            _check(_lib.moe_combine_norm_backward_workspace_bytes(
+                T, H, (post is not None) + (vector is not None) + (pre is not None), ctypes.byref(size)),
+                "moe_combine_norm_backward_workspace_bytes")
+            workspace = torch.empty(size.value, dtype=torch.uint8, device=y.device)
+        wp, wn = workspace.data_ptr(), workspace.numel()
+    _check(_lib.moe_combine_norm_backward(
+        _opt_ptr(dy), _opt_ptr(dn), MOE_DT_F32 if dn is None else _OUT[dn.dtype], y.data_ptr(), _OUT[y.dtype], _opt_ptr(o),
+        _OUT[(y if o is None else o).dtype], _opt_ptr(pos), _opt_ptr(w), T, H, R, k, _opt_ptr(post), _opt_ptr(vector), scale,
+        _opt_ptr(pre), eps, dx.data_ptr(), _opt_ptr(do), _opt_ptr(dw), _opt_ptr(dpost), _opt_ptr(dscale), _opt_ptr(dpre), wp,
+        wn, st, handle), "moe_combine_norm_backward")
+    return dx, do, dw, dpost, dscale, dpre
+
+
+def combine_norm_backward(dy, dn, y, o=None, pos=None, w=None, post=None, scale=1.0, pre=None, eps=1e-6, dx=None, do=None,
+                          workspace=None, status=None, stream=None):
+    """(dx, do, dw, dpost, dscale, dpre): combine_norm's gradients from dy
+    [T,H] (of y's type, or None) and dn [T,H] (fp32 or bf16; only with pre),
+    None for what is not there (dw, dpost, dscale and dpre are fp32; dscale
+    for a vector).
+
+    y is what combine_norm returned (x, without rows); the rest are its own
+    arguments.  pos must name each row at most once, as a grouping's inverse
+    does; rows it does not name are left as they were in `do` (undefined in a
+    new tensor).  dx may be dy.  workspace: uint8, allocated here by default."""
+    _x_dtype(y)
+    i, T, H, R, k, vector, scale = _join_args(y, o, pos, w, post, scale, pre)
+    _is(y, "y", y.dtype, (T, H), i)
+    if dy is not None:
+        _is(dy, "dy", y.dtype, (T, H), i)
+    if (dn is None) != (pre is None):
+        raise ValueError("dn and pre belong together")
+    if dn is not None:
+        if dn.dtype not in _OUT:
+            raise TypeError("dn must be float32 or bfloat16")
+        _is(dn, "dn", dn.dtype, (T, H), i)
+    if dx is not None:
+        _is(dx, "dx", y.dtype, (T, H), i)
+    if do is not None:
+        if o is None:
+            raise ValueError("do belongs to rows: o is missing")
+        _is(do, "do", o.dtype, (R, H), i)
+    if workspace is not None:
+        _is(workspace, "workspace", torch.uint8, workspace.shape, i)
+    return _on(i, stream, _combine_backward, dy, dn, y, o, pos, w, T, H, R, k, post, vector, scale, pre, eps, dx, do,
+               workspace, _status_ptr(status, i))

@@ -1,6 +1,7 @@
 // moe_block.cu -- the C ABI of the operators around the grouped products
-// (declared in include/moe.h): the experts' gated unit and its gradient.
-// Argument checks, the choice of a kernel and its launch.
+// (declared in include/moe.h): the experts' gated unit and its gradient,
+// what joins a block to the residual stream and its gradients.  Argument
+// checks, the choice of a kernel and its launch.
 #include <cuda_runtime.h>
 #include <stdint.h>
 #include <string.h>
@@ -9,6 +10,7 @@
 #include "moe_glu.cuh"
 #include "moe_grouped.cuh"
 #include "moe_host.cuh"
+#include "moe_join.cuh"
 #include "moe_launch.cuh"
 
 namespace moe {
@@ -49,6 +51,71 @@ static int run_glu(GgParams& p, const void* gate_up, const void* x, int R, int I
     return gg_pairs(R, 2 * I, E)
                ? launch_persistent<2>(gg_kernel<kGgFwd, 2, F32, kGgGlu>, p, GgCfg<kGgFwd, 2, F32>::kThreads, sms, st)
                : launch_persistent<1>(gg_kernel<kGgFwd, 1, F32, kGgGlu>, p, GgCfg<kGgFwd, 1, F32>::kThreads, sms, st);
+}
+
+static int check_join(int T, int H, int R, int k, bool o, bool pre, int x_dtype, int o_dtype, int n_dtype, float eps) {
+    if (T < 0 || T > MOE_MAX_ROWS || H < 8 || H > MOE_MAX_DIM || (H & 7)) return MOE_ERR_INVALID_ARG;
+    if (!o && !pre) return MOE_ERR_INVALID_ARG;
+    if (o && (R < 0 || R > MOE_MAX_ROWS || k < 1 || k > MOE_MAX_TOPK)) return MOE_ERR_INVALID_ARG;
+    for (const int dt : {x_dtype, o_dtype, n_dtype})
+        if (dt != MOE_DT_F32 && dt != MOE_DT_BF16) return MOE_ERR_INVALID_ARG;
+    if (!(eps >= 0.0f && eps <= 1.0f)) return MOE_ERR_INVALID_ARG;
+    return MOE_OK;
+}
+
+// Vectors of eight columns that a thread holds, given the threads a token may take.
+static int join_vectors(int H, int threads) {
+    int nv = 1;
+    while (H / 8 > nv * threads) nv *= 2;
+    return nv;
+}
+static unsigned join_threads(int H, int nv) { return (unsigned)ceil_div(ceil_div(H / 8, nv), 32) * 32; }
+
+template <bool OF32, int MT>
+static int run_join(const JoinParams& p, unsigned tokens, cudaStream_t st) {
+    const int nv = join_vectors(p.H, MT);
+    const unsigned x = join_threads(p.H, nv), y = tokens * x > MT ? MT / x : tokens;
+    const dim3 block(x, y), grid((unsigned)ceil_div(p.T, (int)y));
+    switch (nv) {
+        case 1: return launch_pdl(join_kernel<OF32, 1, MT>, grid, block, 0, st, p);
+        case 2: return launch_pdl(join_kernel<OF32, 2, MT>, grid, block, 0, st, p);
+        case 4: return launch_pdl(join_kernel<OF32, 4, MT>, grid, block, 0, st, p);
+        default: return launch_pdl(join_kernel<OF32, MOE_MAX_DIM / 8 / MT, MT>, grid, block, 0, st, p);
+    }
+}
+
+// Few tokens: a block each, of as many threads as help; many: several a block.
+template <bool OF32>
+static int run_join(const JoinParams& p, int sms, cudaStream_t st) {
+    return p.T < 2 * sms ? run_join<OF32, 512>(p, 1, st) : run_join<OF32, 256>(p, 8, st);
+}
+
+// Blocks of the backward pass: what an SM's shared memory holds, four at most.
+static int join_back_grid(int T, int H, int sums, int sms) {
+    const size_t each = (size_t)sums * H * 4 + 4096;
+    int per = (int)((200 * 1024) / each);
+    per = per < 1 ? 1 : per > 4 ? 4 : per;
+    return T < per * sms ? T : per * sms;
+}
+
+template <bool OF32, int NV>
+static int launch_join_back(const JoinParams& p, int grid, cudaStream_t st) {
+    const size_t smem = (size_t)p.sums * p.H * 4;
+    // (with the kernel's static part 48 KB are passed earlier)
+    const int rc = smem > 32 * 1024 ? to_status(cudaFuncSetAttribute(
+                                          join_back_kernel<OF32, NV>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem))
+                                    : MOE_OK;
+    return rc ? rc : launch_pdl(join_back_kernel<OF32, NV>, (unsigned)grid, join_threads(p.H, NV), smem, st, p);
+}
+
+template <bool OF32>
+static int run_join_back(const JoinParams& p, int grid, cudaStream_t st) {
+    switch (join_vectors(p.H, 256)) {
+        case 1: return launch_join_back<OF32, 1>(p, grid, st);
+        case 2: return launch_join_back<OF32, 2>(p, grid, st);
+        case 4: return launch_join_back<OF32, 4>(p, grid, st);
+        default: return launch_join_back<OF32, 8>(p, grid, st);
+    }
 }
 
 }  // namespace moe
@@ -129,6 +196,134 @@ int moe_grouped_glu_backward(const uint16_t* dy, const uint16_t* down, const uin
     return gg_pairs(R, I, E)
                ? launch_persistent<2>(gg_kernel<kGgDx, 2, false, kGgGluBack>, p, GgCfg<kGgDx, 2, false>::kThreads, sms, st)
                : launch_persistent<1>(gg_kernel<kGgDx, 1, false, kGgGluBack>, p, GgCfg<kGgDx, 1, false>::kThreads, sms, st);
+}
+
+int moe_combine_norm(const void* x, int x_dtype, const void* o, int o_dtype, const int32_t* pos, const float* w, int T, int H,
+                     int R, int k, const float* post, const float* scale, float scale_all, const float* pre, float eps,
+                     void* y, void* n, int n_dtype, int32_t* dev_status, void* stream) {
+    const int rc = check_join(T, H, R, k, o != nullptr, pre != nullptr, x_dtype, o_dtype, n_dtype, eps);
+    if (rc) return rc;
+    if (o && !pos && (int64_t)T * k > R) return MOE_ERR_INVALID_ARG;
+    if (T == 0) return MOE_OK;
+    MOE_REQ(x);
+    MOE_OPT(o);
+    MOE_OPT(pos);
+    MOE_OPT(w);
+    MOE_OPT(post);
+    MOE_OPT(scale);
+    MOE_OPT(pre);
+    if (o) MOE_REQ(y);
+    if (pre) MOE_REQ(n);
+    MOE_OPT(dev_status);
+    const int sms = sm_count();
+    if (sms < 1) return MOE_ERR_CUDA;
+    JoinParams p;
+    memset(&p, 0, sizeof p);
+    p.x = x;
+    p.o = o;
+    p.pos = pos;
+    p.w = w;
+    p.post = o ? post : nullptr;
+    p.scale = o ? scale : nullptr;
+    p.pre = pre;
+    p.y = o ? y : nullptr;
+    p.n = n;
+    p.x_f32 = x_dtype == MOE_DT_F32;
+    p.n_f32 = n_dtype == MOE_DT_F32;
+    p.T = T;
+    p.H = H;
+    p.R = R;
+    p.k = o ? k : 0;
+    p.scale_all = scale_all;
+    p.eps = eps;
+    p.status = dev_status;
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    return o_dtype == MOE_DT_F32 ? run_join<true>(p, sms, st) : run_join<false>(p, sms, st);
+}
+
+int moe_combine_norm_backward_workspace_bytes(int T, int H, int sums, size_t* bytes) {
+    if (T < 0 || T > MOE_MAX_ROWS || H < 8 || H > MOE_MAX_DIM || (H & 7) || sums < 0 || sums > 3 || !bytes)
+        return MOE_ERR_INVALID_ARG;
+    const int sms = sm_count();
+    *bytes = sizeof(float) * (size_t)join_back_grid(T, H, sums, sms > 0 ? sms : kMaxSms) * sums * H;
+    return MOE_OK;
+}
+
+int moe_combine_norm_backward(const void* dy, const void* dn, int n_dtype, const void* y, int y_dtype, const void* o,
+                              int o_dtype, const int32_t* pos, const float* w, int T, int H, int R, int k, const float* post,
+                              const float* scale, float scale_all, const float* pre, float eps, void* dx, void* d_o, float* dw,
+                              float* dpost, float* dscale, float* dpre, void* workspace, size_t workspace_bytes,
+                              int32_t* dev_status, void* stream) {
+    const int rc = check_join(T, H, R, k, o != nullptr, pre != nullptr, y_dtype, o_dtype, n_dtype, eps);
+    if (rc) return rc;
+    if (o && !pos && (int64_t)T * k > R) return MOE_ERR_INVALID_ARG;
+    if (!o) post = scale = nullptr;
+    MOE_OPT(post);
+    MOE_OPT(scale);
+    MOE_OPT(pre);
+    if (post) MOE_REQ(dpost);
+    if (scale) MOE_REQ(dscale);
+    if (pre) MOE_REQ(dpre);
+    MOE_OPT(dev_status);
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    const int sums = (post != nullptr) + (scale != nullptr) + (pre != nullptr);
+    float* to[3];
+    int i = 0;
+    if (post) to[i++] = dpost;
+    if (scale) to[i++] = dscale;
+    if (pre) to[i++] = dpre;
+    while (i < 3) to[i++] = nullptr;
+    if (T == 0) {
+        int bad = MOE_OK;
+        for (i = 0; i < sums && !bad; ++i) bad = to_status(cudaMemsetAsync(to[i], 0, sizeof(float) * (size_t)H, st));
+        return bad;
+    }
+    MOE_OPT(dy);
+    if (pre) MOE_REQ(dn);
+    if (pre) MOE_REQ(y);
+    MOE_REQ(dx);
+    MOE_OPT(o);
+    if (o) MOE_REQ(d_o);
+    MOE_OPT(pos);
+    MOE_OPT(w);
+    MOE_OPT(dw);
+    const int sms = sm_count();
+    const int grid = join_back_grid(T, H, sums, sms > 0 ? sms : kMaxSms);
+    if (sums) {
+        if (!workspace || workspace_bytes < sizeof(float) * (size_t)grid * sums * H) return MOE_ERR_WORKSPACE;
+        MOE_REQ(workspace);
+    }
+    JoinParams p;
+    memset(&p, 0, sizeof p);
+    p.x = y;
+    p.o = o;
+    p.pos = pos;
+    p.w = w;
+    p.post = post;
+    p.scale = scale;
+    p.want_scale = scale != nullptr;
+    p.pre = pre;
+    p.y = dx;
+    p.x_f32 = y_dtype == MOE_DT_F32;
+    p.n_f32 = n_dtype == MOE_DT_F32;
+    p.T = T;
+    p.H = H;
+    p.R = R;
+    p.k = o ? k : 0;
+    p.scale_all = scale_all;
+    p.eps = eps;
+    p.dy = dy;
+    p.dn = dn;
+    p.d_o = d_o;
+    p.dw = w && o ? dw : nullptr;
+    p.parts = static_cast<float*>(workspace);
+    p.sums = sums;
+    p.status = dev_status;
+    const int bad = o_dtype == MOE_DT_F32 ? run_join_back<true>(p, grid, st) : run_join_back<false>(p, grid, st);
+    if (bad || !sums) return bad;
+    const int n = sums * H;
+    return launch_pdl(join_sums_kernel, (unsigned)ceil_div(n, 32), 256, 0, st, (const float*)workspace, grid, n, H, to[0],
+                      to[1], to[2]);
 }
 
 }  // extern "C"

@@ -88,6 +88,8 @@ inline EncodeTiledFn encode_fn() {
     return fn;
 }
 
+constexpr int kMaxSms = 152;  // sizes a workspace where no device is visible
+
 inline int sm_count() {
     int dev = 0, n = 0;
     if (cudaGetDevice(&dev) != cudaSuccess) return 0;

@@ -1,0 +1,397 @@
+// moe_join.cuh -- what joins a routed (or dense) block to the residual stream:
+// the weighted sum of a token's rows, a norm behind the block, the residual
+// add with its scale and the norm before the next block, in one kernel, and
+// the gradients of all of it in another.
+//
+//   z[t] = sum_j w[t, j] o[pos[t, j]]           b = rms(z) z post, or z
+//   y[t] = x[t] + scale b                       n = rms(y) y pre
+//   rms(v) = 1 / sqrt(mean(v^2) + eps)
+#pragma once
+
+#include "moe_common.cuh"
+#include "moe_grouped.cuh"
+#include "moe_ptx.cuh"
+
+namespace moe {
+
+struct JoinParams {
+    const void *x, *o;      // x: y in the backward pass
+    const int32_t* pos;     // [T, k], or nullptr: row t k + j
+    const float *w, *post, *scale, *pre;
+    void *y, *n;            // y: dx in the backward pass
+    int x_f32, n_f32;
+    int T, H, R, k;
+    float scale_all, eps;
+    // backward
+    const void *dy, *dn;
+    void* d_o;
+    float* dw;
+    float* parts;           // [gridDim.x][sums][H] column sums: of those wanted, dpost, dscale, dpre
+    int sums, want_scale;
+    int32_t* status;
+};
+
+// ---------------------------------------------------------------- eight values
+// Inputs may come from the kernel ahead on the stream: coherent loads, past L1
+// where a value is read once.
+struct Raw8 {
+    uint4 a, b;
+};
+__device__ __forceinline__ uint4 ld_once_v4(const void* p) {
+    uint4 r;
+    asm volatile("ld.global.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w)
+                 : "l"(p));
+    return r;
+}
+// elements 8 v .. 8 v + 7 of row `row` of a [.., H] tensor
+__device__ __forceinline__ Raw8 raw8(const void* p, bool f32, size_t row, int H, int v) {
+    Raw8 r;
+    const size_t at = row * (size_t)H + 8 * (size_t)v;
+    if (f32) {
+        r.a = ld_once_v4(static_cast<const float*>(p) + at);
+        r.b = ld_once_v4(static_cast<const float*>(p) + at + 4);
+    } else {
+        r.a = ld_once_v4(static_cast<const uint16_t*>(p) + at);
+        r.b = make_uint4(0, 0, 0, 0);
+    }
+    return r;
+}
+__device__ __forceinline__ void values8(const Raw8& r, bool f32, float (&v)[8]) {
+    const uint32_t a[8] = {r.a.x, r.a.y, r.a.z, r.a.w, r.b.x, r.b.y, r.b.z, r.b.w};
+    if (f32) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(a[i]);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const float2 f = bf16x2_to_f2(a[i]);
+            v[2 * i] = f.x;
+            v[2 * i + 1] = f.y;
+        }
+    }
+}
+__device__ __forceinline__ void put8(void* p, bool f32, size_t row, int H, int v, const float (&f)[8]) {
+    const size_t at = row * (size_t)H + 8 * (size_t)v;
+    if (f32) {
+        float4* o = reinterpret_cast<float4*>(static_cast<float*>(p) + at);
+        o[0] = make_float4(f[0], f[1], f[2], f[3]);
+        o[1] = make_float4(f[4], f[5], f[6], f[7]);
+    } else {
+        uint32_t u[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) u[i] = gg_pack(__float_as_uint(f[2 * i]), __float_as_uint(f[2 * i + 1]));
+        *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p) + at) = make_uint4(u[0], u[1], u[2], u[3]);
+    }
+}
+__device__ __forceinline__ void vector8(const float* p, int v, float (&f)[8]) {
+    const float4 a = *reinterpret_cast<const float4*>(p + 8 * v), b = *reinterpret_cast<const float4*>(p + 8 * v + 4);
+    f[0] = a.x, f[1] = a.y, f[2] = a.z, f[3] = a.w, f[4] = b.x, f[5] = b.y, f[6] = b.z, f[7] = b.w;
+}
+
+// Eight columns' sums in shared memory, owned by one thread: the first and the
+// last four of each vector in two arrays, so that a warp's accesses are dense.
+__device__ __forceinline__ void add8(float* sums, int nvec, int v, const float (&f)[8]) {
+    float4* s = reinterpret_cast<float4*>(sums);
+    float4 a = s[v], b = s[nvec + v];
+    s[v] = make_float4(a.x + f[0], a.y + f[1], a.z + f[2], a.w + f[3]);
+    s[nvec + v] = make_float4(b.x + f[4], b.y + f[5], b.z + f[6], b.w + f[7]);
+}
+
+// ---------------------------------------------------------------- reductions
+// Sums over the threads of one token (blockDim.x, whole warps) of N values;
+// every thread of the block takes part.  `buf`: blockDim.y * 32 * N floats,
+// free again after the next barrier of the block.
+template <int N>
+__device__ __forceinline__ void token_sum(float (&v)[N], float* buf) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) v[i] = warp_sum(v[i]);
+    if (blockDim.x == 32) return;
+    const int warps = blockDim.x >> 5, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    float* mine = buf + threadIdx.y * 32 * N;
+    if (lane == 0) {
+#pragma unroll
+        for (int i = 0; i < N; ++i) mine[i * 32 + warp] = v[i];
+    }
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < N; ++i) v[i] = warp_sum(lane < warps ? mine[i * 32 + lane] : 0.0f);
+}
+
+// The rows and weights of a token's routes; a row of -1 is none.
+__device__ __forceinline__ void token_routes(const JoinParams& p, int t, bool valid, int (&row)[MOE_MAX_TOPK],
+                                             float (&w)[MOE_MAX_TOPK]) {
+#pragma unroll
+    for (int j = 0; j < MOE_MAX_TOPK; ++j) {
+        row[j] = -1;
+        w[j] = 0.0f;
+        if (j < p.k && valid && p.o) {
+            const size_t at = (size_t)t * p.k + j;
+            row[j] = p.pos ? p.pos[at] : (int)at;
+            w[j] = p.w ? p.w[at] : 1.0f;
+            if (row[j] < -1 || row[j] >= p.R) {
+                set_status(p.status, MOE_DEV_BAD_ROUTE);
+                row[j] = -1;
+            }
+        }
+    }
+}
+
+// z of eight columns
+template <bool OF32>
+__device__ __forceinline__ void gather8(const JoinParams& p, const int (&row)[MOE_MAX_TOPK], const float (&w)[MOE_MAX_TOPK],
+                                        int v, float (&z)[8]) {
+    Raw8 r[MOE_MAX_TOPK];
+#pragma unroll
+    for (int j = 0; j < MOE_MAX_TOPK; ++j)
+        if (row[j] >= 0) r[j] = raw8(p.o, OF32, row[j], p.H, v);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) z[i] = 0.0f;
+#pragma unroll
+    for (int j = 0; j < MOE_MAX_TOPK; ++j)
+        if (row[j] >= 0) {
+            float f[8];
+            values8(r[j], OF32, f);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) z[i] = fmaf(w[j], f[i], z[i]);
+        }
+}
+
+// ---------------------------------------------------------------- forward
+// A token per row of threads (blockDim.y tokens a block of up to MT threads); a
+// thread holds the columns of NV vectors of eight.
+template <bool OF32, int NV, int MT>
+__global__ void __launch_bounds__(MT) join_kernel(JoinParams p) {
+    __shared__ float buf[2][MT];
+    grid_dep_wait();
+    const int t = blockIdx.x * blockDim.y + threadIdx.y, nvec = p.H / 8;
+    const bool valid = t < p.T;
+    int row[MOE_MAX_TOPK];
+    float w[MOE_MAX_TOPK], s[1] = {0.0f}, b[NV][8];
+    token_routes(p, t, valid, row, w);
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        const int v = threadIdx.x + i * blockDim.x;
+        if (!valid || v >= nvec) continue;
+        gather8<OF32>(p, row, w, v, b[i]);
+#pragma unroll
+        for (int c = 0; c < 8; ++c) s[0] = fmaf(b[i][c], b[i][c], s[0]);
+    }
+    float r = 1.0f;
+    if (p.post) {
+        token_sum(s, buf[0]);
+        r = 1.0f / sqrtf(s[0] / (float)p.H + p.eps);
+    }
+    s[0] = 0.0f;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        const int v = threadIdx.x + i * blockDim.x;
+        if (!valid || v >= nvec) continue;
+        float f[8], x[8];
+        if (p.post) {
+            vector8(p.post, v, f);
+#pragma unroll
+            for (int c = 0; c < 8; ++c) b[i][c] *= r * f[c];
+        }
+        values8(raw8(p.x, p.x_f32, t, p.H, v), p.x_f32, x);
+        if (p.scale) {
+            vector8(p.scale, v, f);
+#pragma unroll
+            for (int c = 0; c < 8; ++c) b[i][c] = fmaf(f[c], b[i][c], x[c]);
+        } else {
+#pragma unroll
+            for (int c = 0; c < 8; ++c) b[i][c] = fmaf(p.scale_all, b[i][c], x[c]);
+        }
+        if (p.y) put8(p.y, p.x_f32, t, p.H, v, b[i]);
+#pragma unroll
+        for (int c = 0; c < 8; ++c) s[0] = fmaf(b[i][c], b[i][c], s[0]);
+    }
+    if (!p.pre) return;
+    token_sum(s, buf[1]);
+    r = 1.0f / sqrtf(s[0] / (float)p.H + p.eps);
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        const int v = threadIdx.x + i * blockDim.x;
+        if (!valid || v >= nvec) continue;
+        float f[8];
+        vector8(p.pre, v, f);
+#pragma unroll
+        for (int c = 0; c < 8; ++c) f[c] *= b[i][c] * r;
+        put8(p.n, p.n_f32, t, p.H, v, f);
+    }
+}
+
+// ---------------------------------------------------------------- backward
+// With d the gradient of y (a = dn pre):
+//   d  = dy + rms(y) a - y rms(y)^3 mean(a y)        dx = d
+//   g  = scale d (the gradient of b);  with a norm behind the block, c = g post:
+//   dz = rms(z) c - z rms(z)^3 mean(c z), else g
+//   do[pos_j] = w_j dz,  dw_j = <dz, o[pos_j]>
+//   dpre = sum_t dn y rms(y),  dscale = sum_t d b,  dpost = sum_t g z rms(z)
+// A block walks tokens and keeps the column sums in shared memory, each column
+// by the thread that owns it; the blocks' sums are joined in a fixed order.
+template <bool OF32, int NV>
+__global__ void __launch_bounds__(256) join_back_kernel(JoinParams p) {
+    extern __shared__ __align__(16) float cols[];  // [sums][H]
+    __shared__ float buf[3][32 * MOE_MAX_TOPK];
+    const int nvec = p.H / 8;
+    for (int i = threadIdx.x; i < p.sums * p.H; i += blockDim.x) cols[i] = 0.0f;
+    float* at = cols;
+    float* c_post = p.post ? at : nullptr;
+    at += p.post ? p.H : 0;
+    float* c_scale = p.want_scale ? at : nullptr;
+    at += p.want_scale ? p.H : 0;
+    float* c_pre = at;
+    grid_dep_wait();
+    __syncthreads();
+    for (int t = blockIdx.x; t < p.T; t += gridDim.x) {
+        int row[MOE_MAX_TOPK];
+        float w[MOE_MAX_TOPK], s[3] = {0.0f, 0.0f, 0.0f}, z[NV][8], d[NV][8];
+        token_routes(p, t, true, row, w);
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const int v = threadIdx.x + i * blockDim.x;
+            if (v >= nvec) continue;
+            if (p.o) gather8<OF32>(p, row, w, v, z[i]);
+            if (p.pre) {
+                float y[8], a[8], f[8];
+                values8(raw8(p.x, p.x_f32, t, p.H, v), p.x_f32, y);
+                values8(raw8(p.dn, p.n_f32, t, p.H, v), p.n_f32, a);
+                vector8(p.pre, v, f);
+#pragma unroll
+                for (int c = 0; c < 8; ++c) {
+                    s[0] = fmaf(y[c], y[c], s[0]);
+                    s[1] = fmaf(a[c] * f[c], y[c], s[1]);
+                }
+            }
+            if (p.post) {
+#pragma unroll
+                for (int c = 0; c < 8; ++c) s[2] = fmaf(z[i][c], z[i][c], s[2]);
+            }
+        }
+        token_sum(s, buf[0]);
+        const float ry = 1.0f / sqrtf(s[0] / (float)p.H + p.eps), my = ry * ry * ry * (s[1] / (float)p.H);
+        const float rz = 1.0f / sqrtf(s[2] / (float)p.H + p.eps);
+        float cz[1] = {0.0f};
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const int v = threadIdx.x + i * blockDim.x;
+            if (v >= nvec) continue;
+            if (p.dy) {
+                values8(raw8(p.dy, p.x_f32, t, p.H, v), p.x_f32, d[i]);
+            } else {
+#pragma unroll
+                for (int c = 0; c < 8; ++c) d[i][c] = 0.0f;
+            }
+            if (p.pre) {
+                float y[8], a[8], f[8];
+                values8(raw8(p.x, p.x_f32, t, p.H, v), p.x_f32, y);
+                values8(raw8(p.dn, p.n_f32, t, p.H, v), p.n_f32, a);
+                vector8(p.pre, v, f);
+#pragma unroll
+                for (int c = 0; c < 8; ++c) {
+                    d[i][c] += ry * (a[c] * f[c]) - y[c] * my;
+                    f[c] = a[c] * y[c] * ry;
+                }
+                add8(c_pre, nvec, v, f);
+            }
+            put8(p.y, p.x_f32, t, p.H, v, d[i]);
+            if (!p.o) continue;
+            float f[8], q[8];
+            if (p.post) vector8(p.post, v, q);
+            if (c_scale) {
+#pragma unroll
+                for (int c = 0; c < 8; ++c) f[c] = d[i][c] * (p.post ? z[i][c] * rz * q[c] : z[i][c]);
+                add8(c_scale, nvec, v, f);
+            }
+            if (p.scale) {
+                vector8(p.scale, v, f);
+#pragma unroll
+                for (int c = 0; c < 8; ++c) d[i][c] *= f[c];
+            } else {
+#pragma unroll
+                for (int c = 0; c < 8; ++c) d[i][c] *= p.scale_all;
+            }
+            if (p.post) {
+#pragma unroll
+                for (int c = 0; c < 8; ++c) f[c] = d[i][c] * (z[i][c] * rz);
+                add8(c_post, nvec, v, f);
+#pragma unroll
+                for (int c = 0; c < 8; ++c) {
+                    d[i][c] *= q[c];
+                    cz[0] = fmaf(d[i][c], z[i][c], cz[0]);
+                }
+            }
+        }
+        if (!p.o) {
+            __syncthreads();  // (buf is used again)
+            continue;
+        }
+        float mz = 0.0f;
+        if (p.post) {
+            token_sum(cz, buf[1]);
+            mz = rz * rz * rz * (cz[0] / (float)p.H);
+        }
+        float dots[MOE_MAX_TOPK] = {};
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const int v = threadIdx.x + i * blockDim.x;
+            if (v >= nvec) continue;
+            if (p.post) {
+#pragma unroll
+                for (int c = 0; c < 8; ++c) d[i][c] = rz * d[i][c] - z[i][c] * mz;
+            }
+#pragma unroll
+            for (int j = 0; j < MOE_MAX_TOPK; ++j)
+                if (row[j] >= 0) {
+                    float f[8];
+                    if (p.dw) {
+                        values8(raw8(p.o, OF32, row[j], p.H, v), OF32, f);
+#pragma unroll
+                        for (int c = 0; c < 8; ++c) dots[j] = fmaf(d[i][c], f[c], dots[j]);
+                    }
+#pragma unroll
+                    for (int c = 0; c < 8; ++c) f[c] = w[j] * d[i][c];
+                    put8(p.d_o, OF32, row[j], p.H, v, f);
+                }
+        }
+        if (p.dw) {
+            token_sum(dots, buf[2]);
+#pragma unroll
+            for (int j = 0; j < MOE_MAX_TOPK; ++j)
+                if (j < p.k && threadIdx.x == j) p.dw[(size_t)t * p.k + j] = dots[j];
+        }
+        __syncthreads();
+    }
+    float4* out = reinterpret_cast<float4*>(p.parts + (size_t)blockIdx.x * p.sums * p.H);
+    const float4* in = reinterpret_cast<const float4*>(cols);
+    for (int s = 0; s < p.sums; ++s)
+        for (int v = threadIdx.x; v < nvec; v += blockDim.x) {
+            out[2 * (s * nvec + v)] = in[2 * s * nvec + v];
+            out[2 * (s * nvec + v) + 1] = in[2 * s * nvec + nvec + v];
+        }
+}
+
+// The blocks' column sums in a fixed order: a block takes 32 columns, its
+// eight warps every eighth part.
+static __global__ void __launch_bounds__(256) join_sums_kernel(const float* parts, int grid, int n, int H, float* a, float* b,
+                                                               float* c) {
+    __shared__ float s_sum[8][32];
+    grid_dep_wait();
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, i = blockIdx.x * 32 + lane;
+    float s = 0.0f;
+    if (i < n) {
+#pragma unroll 8
+        for (int k = warp; k < grid; k += 8) s += __ldcg(parts + (size_t)k * n + i);
+    }
+    s_sum[warp][lane] = s;
+    __syncthreads();
+    if (warp == 0 && i < n) {
+#pragma unroll
+        for (int k = 1; k < 8; ++k) s += s_sum[k][lane];
+        float* const to[3] = {a, b, c};
+        to[i / H][i % H] = s;
+    }
+}
+
+}  // namespace moe

@@ -55,3 +55,47 @@ def test_the_binding_checks_the_gated_unit(api):
         api.grouped_glu_backward(_z(4, 64), _z(8, 64, 16), _z(4, 32), off, act="tanh")
     with pytest.raises(ValueError):
         api.grouped_glu_backward(_z(4, 64, 1), _z(8, 64, 16), _z(4, 32), off)
+
+
+def test_the_join_refuses_before_any_launch(api):
+    def fwd(x=GOOD, xd=0, o=GOOD, od=1, pos=GOOD, w=GOOD, T=4, H=64, R=8, k=2, post=GOOD, scale=GOOD, pre=GOOD, eps=1e-6,
+            y=GOOD, n=GOOD, nd=1, st=None):
+        return api._lib.moe_combine_norm(x, xd, o, od, pos, w, T, H, R, k, post, scale, 1.0, pre, eps, y, n, nd, st, None)
+
+    def back(x=GOOD, xd=0, o=GOOD, od=1, pos=GOOD, w=GOOD, T=4, H=64, R=8, k=2, post=GOOD, scale=GOOD, pre=GOOD, eps=1e-6,
+             y=GOOD, n=GOOD, nd=1, st=None, do=GOOD, dw=GOOD, dpost=GOOD, dscale=GOOD, dpre=GOOD, dy=GOOD, ws=GOOD,
+             nw=1 << 30):
+        return api._lib.moe_combine_norm_backward(dy, n, nd, x, xd, o, od, pos, w, T, H, R, k, post, scale, 1.0, pre, eps, y,
+                                                  do, dw, dpost, dscale, dpre, ws, nw, st, None)
+
+    inv = api.MOE_ERR_INVALID_ARG
+    for kw in (dict(T=-1), dict(T=(1 << 22) + 1), dict(H=0), dict(H=12), dict(H=16392), dict(R=-1), dict(R=(1 << 22) + 1),
+               dict(k=0), dict(k=9), dict(xd=2), dict(od=-1), dict(nd=5), dict(eps=-1e-3), dict(eps=1.5),
+               dict(eps=float("nan")), dict(o=None, pre=None), dict(pos=None, R=7), dict(x=None), dict(y=None), dict(n=None),
+               *[{v: ODD} for v in ("x", "o", "pos", "w", "post", "scale", "pre", "y", "n", "st")]):
+        assert fwd(**kw) == inv, kw
+        assert back(**kw) == inv, kw
+    for kw in ({v: ODD} for v in ("do", "dw", "dpost", "dscale", "dpre", "dy", "ws")):
+        assert back(**kw) == inv, kw
+    for kw in ({v: None} for v in ("do", "dpost", "dscale", "dpre")):
+        assert back(**kw) == inv, kw
+    assert back(ws=None) == api.MOE_ERR_WORKSPACE and back(nw=64) == api.MOE_ERR_WORKSPACE
+    assert fwd(T=0, x=None) == api.MOE_OK
+
+
+def test_the_binding_checks_the_join(api):
+    f = lambda *s: _z(*s, dt=torch.float32)  # noqa: E731
+    x, o, pos, w = f(4, 64), _z(8, 64), _z(4, 2, dt=torch.int32), f(4, 2)
+    for bad in (lambda: api.combine_norm(x, o, pos, w),  # host tensors
+                lambda: api.combine_norm(x),
+                lambda: api.combine_norm(x, pos=pos, pre=f(64)),
+                lambda: api.combine_norm(f(64), o, pos, w),
+                lambda: api.combine_norm(x, o, pos.flatten(), w),
+                lambda: api.combine_norm_backward(x, None, x, o, pos, w, pre=f(64)),
+                lambda: api.combine_norm_backward(x, x, x, o, pos, w)):
+        with pytest.raises(ValueError):
+            bad()
+    with pytest.raises(TypeError):
+        api.combine_norm(x.half(), o, pos, w)
+    with pytest.raises(TypeError):
+        api.combine_norm(x, o.half(), pos, w)
