@@ -85,6 +85,7 @@ typedef enum { MOE_DT_F32 = 0, MOE_DT_BF16 = 1 } moe_dtype;
 #define MOE_MAX_DIM 16384
 #define MOE_MAX_LAYERS 64
 #define MOE_MAX_ROWS (1 << 22)      /* rows of the grouped products, and of rows quantised each by itself */
+#define MOE_MAX_NS_STEPS 16         /* Newton-Schulz steps of moe_orthogonalize */
 #define MOE_MAX_BLOCKS (1LL << 32)  /* 16-element blocks of the matrices quantised in one call */
 
 /* flags for moe_expert_forward / moe_layer_forward / moe_stack_forward */
@@ -440,6 +441,27 @@ int moe_combine_norm_backward(const void* dy, const void* dn, int n_dtype, const
                               const float* scale, float scale_all, const float* pre, float eps, void* dx, void* d_o, float* dw,
                               float* dpost, float* dscale, float* dpre, void* workspace, size_t workspace_bytes,
                               int32_t* dev_status, void* stream);
+
+/*
+ * moe_orthogonalize -- matrices brought near the closest ones with orthonormal
+ * rows (or columns) by Newton-Schulz products, as the Muon optimiser does with
+ * the momentum of a weight's gradient:
+ *   X = G / (|G|_F + eps);  steps times:  A = X X^T,  X <- a X + (b A + c A A) X
+ * for each of E matrices g [E, N, K] fp32 or bf16 (g_dtype), on the shorter
+ * side; out [E, N, K] bf16 (may alias a bf16 g).  Products of fp16 values with
+ * fp32 sums: A (in the last two steps A - 1/2, with what follows from it) and b
+ * A + c A A are rounded to fp16 in between, within half a step, 2^-12, of each
+ * value; X is carried in 22 bits and rounded to fp16 for the products.  The norm of any finite matrix is exact to
+ * fp32's rounding, without overflow.  Values of X below 2^-33 are lost
+ * (a matrix far smaller than eps).  A matrix with a NaN or an infinity becomes
+ * NaN, the others are not affected; a zero matrix stays zero (with eps > 0).  The coefficients lie in [-16, 16]; such as let X grow past
+ * fp16's range overflow to infinities.  1 <= steps <= MOE_MAX_NS_STEPS, N and
+ * K in [1, MOE_MAX_DIM], E <= MOE_MAX_E, eps in [0, 1].  workspace:
+ * moe_orthogonalize_workspace_bytes() (host-only), used by one call at a time.
+ */
+int moe_orthogonalize_workspace_bytes(int E, int N, int K, size_t* bytes);
+int moe_orthogonalize(const void* g, int g_dtype, int E, int N, int K, int steps, float a, float b, float c, float eps,
+                      uint16_t* out, void* workspace, size_t workspace_bytes, int32_t* dev_status, void* stream);
 
 /*
  * moe_quantize_nvfp4 -- matrices into the NVFP4 layout of

@@ -58,6 +58,8 @@ _lib.moe_combine_norm.argtypes = [_P, _I, _P, _I, _P, _P, _I, _I, _I, _I, _P, _P
 _lib.moe_combine_norm_backward_workspace_bytes.argtypes = [_I, _I, _I, ctypes.POINTER(_S)]
 _lib.moe_combine_norm_backward.argtypes = [_P, _P, _I, _P, _I, _P, _I, _P, _P, _I, _I, _I, _I, _P, _P, _F, _P, _F, _P, _P, _P,
                                            _P, _P, _P, _P, _S, _P, _P]
+_lib.moe_orthogonalize_workspace_bytes.argtypes = [_I, _I, _I, ctypes.POINTER(_S)]
+_lib.moe_orthogonalize.argtypes = [_P, _I, _I, _I, _I, _I, _F, _F, _F, _F, _P, _P, _S, _P, _P]
 _lib.moe_workspace_grouping.argtypes = [_P, _S, _I, _I, _I, _I, _I, ctypes.POINTER(_P), ctypes.POINTER(_P),
                                         ctypes.POINTER(_P), ctypes.POINTER(_P)]
 _lib.moe_forward_path.argtypes = [_I, _I, _I, _I, _I, _I, _U, ctypes.POINTER(_I), ctypes.POINTER(_I)]
@@ -76,7 +78,7 @@ for _f in ("moe_workspace_bytes", "moe_route", "moe_group_by_expert", "moe_exper
            "moe_grouped_gemm_dx", "moe_grouped_gemm_dw", "moe_grouped_gemm_dw_workspace_bytes",
            "moe_quantize_nvfp4_workspace_bytes", "moe_quantize_nvfp4", "moe_dequantize_nvfp4", "moe_grouped_gemm_nvfp4",
            "moe_grouped_glu", "moe_grouped_glu_backward", "moe_combine_norm", "moe_combine_norm_backward",
-           "moe_combine_norm_backward_workspace_bytes"):
+           "moe_combine_norm_backward_workspace_bytes", "moe_orthogonalize_workspace_bytes", "moe_orthogonalize"):
     getattr(_lib, _f).restype = ctypes.c_int
 
 EXPORTED = ("moe_workspace_bytes", "moe_route", "moe_group_by_expert", "moe_expert_forward",
@@ -85,7 +87,7 @@ EXPORTED = ("moe_workspace_bytes", "moe_route", "moe_group_by_expert", "moe_expe
             "moe_grouped_gemm", "moe_grouped_gemm_dx", "moe_grouped_gemm_dw", "moe_grouped_gemm_dw_workspace_bytes",
             "moe_quantize_nvfp4_workspace_bytes", "moe_quantize_nvfp4", "moe_dequantize_nvfp4", "moe_grouped_gemm_nvfp4",
             "moe_grouped_glu", "moe_grouped_glu_backward", "moe_combine_norm", "moe_combine_norm_backward",
-            "moe_combine_norm_backward_workspace_bytes",
+            "moe_combine_norm_backward_workspace_bytes", "moe_orthogonalize_workspace_bytes", "moe_orthogonalize",
             "moe_launch_count", "moe_forward_path", "moe_set_trace_buffer",
             "moe_inject_barrier_stall", "moe_status_string")
 
@@ -1094,3 +1096,40 @@ def combine_norm_backward(dy, dn, y, o=None, pos=None, w=None, post=None, scale=
         _is(workspace, "workspace", torch.uint8, workspace.shape, i)
     return _on(i, stream, _combine_backward, dy, dn, y, o, pos, w, T, H, R, k, post, vector, scale, pre, eps, dx, do,
                workspace, _status_ptr(status, i))
+
+
+def _orthogonalize(handle, g, dt, E, N, K, steps, coeffs, eps, out, workspace, st):
+    if out is None:
+        out = torch.empty(g.shape, dtype=torch.bfloat16, device=g.device)
+    if workspace is None:
+        n = _S(0)
+        _check(_lib.moe_orthogonalize_workspace_bytes(E, N, K, ctypes.byref(n)), "moe_orthogonalize_workspace_bytes")
+        workspace = torch.empty(n.value, dtype=torch.uint8, device=g.device)
+    _check(_lib.moe_orthogonalize(g.data_ptr(), dt, E, N, K, steps, *coeffs, eps, out.data_ptr(), workspace.data_ptr(),
+                                  workspace.numel(), st, handle), "moe_orthogonalize")
+    return out
+
+
+def orthogonalize(g, steps=5, coeffs=(3.4445, -4.7750, 2.0315), eps=1e-7, out=None, workspace=None, status=None, stream=None):
+    """bf16 of g's shape: each matrix of g ([N,K] or [E,N,K], fp32 or bf16)
+    near the closest one with orthonormal rows or columns, by `steps`
+    Newton-Schulz products X <- a X + (b A + c A A) X, A = X X^T, from X =
+    g / (|g|_F + eps) on; coeffs = (a, b, c).  What the Muon optimiser makes of
+    a momentum, grouped_gemm_dw's for instance.  `out` may be g.  workspace
+    (uint8, moe_orthogonalize_workspace_bytes) is allocated here by default."""
+    if g.dim() not in (2, 3):
+        raise ValueError(f"g has shape {tuple(g.shape)}, expected [N, K] or [E, N, K]")
+    E, N, K = (1, *g.shape) if g.dim() == 2 else g.shape
+    if g.dtype not in _OUT:
+        raise TypeError("g must be float32 or bfloat16")
+    coeffs = tuple(float(c) for c in coeffs)
+    if len(coeffs) != 3:
+        raise ValueError(f"coeffs must be three numbers, got {len(coeffs)}")
+    i = g.get_device()
+    _is(g, "g", g.dtype, g.shape, i)
+    if out is not None:
+        _is(out, "out", torch.bfloat16, g.shape, i)
+    if workspace is not None:
+        _is(workspace, "workspace", torch.uint8, workspace.shape, i)
+    return _on(i, stream, _orthogonalize, g, _OUT[g.dtype], E, N, K, int(steps), coeffs, eps, out, workspace,
+               _status_ptr(status, i))

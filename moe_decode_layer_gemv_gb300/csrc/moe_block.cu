@@ -1,7 +1,7 @@
 // moe_block.cu -- the C ABI of the operators around the grouped products
 // (declared in include/moe.h): the experts' gated unit and its gradient,
-// what joins a block to the residual stream and its gradients.  Argument
-// checks, the choice of a kernel and its launch.
+// what joins a block to the residual stream and its gradients, and the
+// orthogonalised update.  Argument checks, the choice of a kernel, its launch.
 #include <cuda_runtime.h>
 #include <stdint.h>
 #include <string.h>
@@ -12,6 +12,7 @@
 #include "moe_host.cuh"
 #include "moe_join.cuh"
 #include "moe_launch.cuh"
+#include "moe_ortho.cuh"
 
 namespace moe {
 
@@ -116,6 +117,72 @@ static int run_join_back(const JoinParams& p, int grid, cudaStream_t st) {
         case 4: return launch_join_back<OF32, 4>(p, grid, st);
         default: return launch_join_back<OF32, 8>(p, grid, st);
     }
+}
+
+// ---------------------------------------------------------- orthogonalisation
+struct NsPlan {
+    int m, n;        // rows and columns of X, padded
+    int parts;       // blocks that sum a matrix's squares
+    size_t x, a, p;  // bytes of X, of A, of the sums
+    size_t bytes;
+};
+
+static int ns_plan(int E, int N, int K, NsPlan* q) {
+    if (E < 1 || E > MOE_MAX_E || N < 1 || N > MOE_MAX_DIM || K < 1 || K > MOE_MAX_DIM) return MOE_ERR_INVALID_ARG;
+    q->m = ceil_div(N < K ? N : K, 8) * 8;
+    q->n = ceil_div(N < K ? K : N, 64) * 64;
+    q->parts = ceil_div(4 * kMaxSms, E);
+    const int most = (int)(((size_t)N * K + 2047) / 2048);
+    if (q->parts > most) q->parts = most;
+    if (q->parts > kNsParts) q->parts = kNsParts;
+    q->x = align_up(sizeof(uint16_t) * (size_t)E * q->m * q->n, 256);
+    q->a = align_up(sizeof(uint16_t) * (size_t)E * q->m * q->m, 256);
+    q->p = align_up(sizeof(float) * 3 * (size_t)E * q->parts, 256);
+    q->bytes = 3 * q->x + 2 * q->a + q->p;
+    return MOE_OK;
+}
+
+// One product: X X^T or A A (symmetric), or B X.
+template <int EP>
+static int run_ns(const NsPlan& q, int E, const void* w, const void* x, int cols, float alpha, float beta, const void* in,
+                  void* low, void* out, const int* res, float shift, int32_t* status, int sms, cudaStream_t st) {
+    constexpr int MODE = EP == kGgSym ? kGgFwd : kGgDx;
+    GgParams p;
+    memset(&p, 0, sizeof p);
+    p.E = E;
+    p.rows = q.m;
+    p.R = E * q.m;
+    p.in = in;
+    p.low = low;
+    p.out = out;
+    p.alpha = alpha;
+    p.beta = beta;
+    p.shift = shift;
+    p.status = status;
+    bool ok;
+    if (EP == kGgSym) {  // x [E m, cols] times its own rows
+        p.M = q.m;
+        p.C = cols;
+        ok = encode_map(&p.ta, w, 2, cols, q.m, E, 128);
+    } else {  // x = B [E m, m], w = X [E, m, n]
+        p.M = q.n;
+        p.C = q.m;
+        p.a_blocked = 1;
+        ok = encode_blocked(&p.ta, w, q.n, q.m, E);
+    }
+    if (!ok || !encode_map(&p.tb, x, 2, p.C, p.R, 0, kGgBoxN) || !encode_map(&p.tb_all, x, 2, p.C, p.R, 0, 128))
+        return MOE_ERR_UNSUPPORTED;
+    if (res) {
+        p.res_rows = res[0];
+        p.res_cols = res[1];
+        p.res_trans = res[2];
+    }
+    // pairs of CTAs where their larger tiles still give every pair work
+    const int t = ceil_div(q.m, 256);
+    const int64_t tiles = (int64_t)E * (EP == kGgSym ? t * (t + 1) / 2 : t * ceil_div(q.n, 256));
+    return tiles >= sms / 2
+               ? launch_persistent<2>(gg_kernel<MODE, 2, false, EP>, p, GgCfg<MODE, 2, false>::kThreads, sms, st)
+               : launch_persistent<1>(gg_kernel<MODE, 1, false, EP>, p, GgCfg<MODE, 1, false>::kThreads, sms, st);
 }
 
 }  // namespace moe
@@ -324,6 +391,62 @@ int moe_combine_norm_backward(const void* dy, const void* dn, int n_dtype, const
     const int n = sums * H;
     return launch_pdl(join_sums_kernel, (unsigned)ceil_div(n, 32), 256, 0, st, (const float*)workspace, grid, n, H, to[0],
                       to[1], to[2]);
+}
+
+int moe_orthogonalize_workspace_bytes(int E, int N, int K, size_t* bytes) {
+    NsPlan q;
+    const int rc = ns_plan(E, N, K, &q);
+    if (rc) return rc;
+    if (!bytes) return MOE_ERR_INVALID_ARG;
+    *bytes = q.bytes;
+    return MOE_OK;
+}
+
+int moe_orthogonalize(const void* g, int g_dtype, int E, int N, int K, int steps, float a, float b, float c, float eps,
+                      uint16_t* out, void* workspace, size_t workspace_bytes, int32_t* dev_status, void* stream) {
+    NsPlan q;
+    int rc = ns_plan(E, N, K, &q);
+    if (rc) return rc;
+    if (g_dtype != MOE_DT_F32 && g_dtype != MOE_DT_BF16) return MOE_ERR_INVALID_ARG;
+    if (steps < 1 || steps > MOE_MAX_NS_STEPS || !(eps >= 0.0f && eps <= 1.0f)) return MOE_ERR_INVALID_ARG;
+    for (const float v : {a, b, c})
+        if (!(v >= -16.0f && v <= 16.0f)) return MOE_ERR_INVALID_ARG;
+    MOE_REQ(g);
+    MOE_REQ(out);
+    MOE_OPT(dev_status);
+    if (!workspace || workspace_bytes < q.bytes) return MOE_ERR_WORKSPACE;
+    MOE_REQ(workspace);
+    const int sms = sm_count();
+    if (sms < 2) return MOE_ERR_CUDA;
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    unsigned char* ws = static_cast<unsigned char*>(workspace);
+    void* x[2] = {ws, ws + q.x};
+    void *low = ws + 2 * q.x, *A = ws + 3 * q.x, *B = ws + 3 * q.x + q.a;
+    float* parts = reinterpret_cast<float*>(ws + 3 * q.x + 2 * q.a);
+    const int f32 = g_dtype == MOE_DT_F32, trans = N > K;
+    rc = launch_pdl(ns_norm_kernel, dim3((unsigned)q.parts, (unsigned)E), 256, 0, st, g, f32, (size_t)N * K, parts);
+    if (rc) return rc;
+    // (the blocks cover the padded X: its rows are G's columns where G is tall)
+    const int rows = trans ? q.n : q.m, cols = trans ? q.m : q.n;
+    rc = launch_pdl(ns_convert_kernel, dim3((unsigned)ceil_div(cols, 64), (unsigned)ceil_div(rows, 64), (unsigned)E), 256, 0, st,
+                    g, f32, N, K, (const float*)parts, q.parts, eps, trans, static_cast<uint16_t*>(x[0]),
+                    static_cast<uint16_t*>(low), q.m, q.n);
+    if (rc) return rc;
+    const float up = (float)(1 << kNsScaleLog2), down = 1.0f / up;
+    const int res[3] = {N, K, trans};
+    for (int s = 0; s < steps; ++s) {
+        void *from = x[s & 1], *to = x[(s & 1) ^ 1];
+        // a + b A + c A A of A = S + A': one + lin A' + c A' A'
+        const float S = steps - s <= kNsShifted ? kNsShift : 0.0f, lin = b + 2.0f * c * S, one = a + b * S + c * S * S;
+        rc = run_ns<kGgSym>(q, E, from, from, q.n, down * down, 0.0f, nullptr, nullptr, A, nullptr, S, dev_status, sms, st);
+        if (rc) return rc;
+        rc = run_ns<kGgSym>(q, E, A, A, q.m, c, lin, A, nullptr, B, nullptr, 0.0f, dev_status, sms, st);
+        if (rc) return rc;
+        rc = s + 1 < steps ? run_ns<kGgAxpy>(q, E, from, B, 0, 1.0f, one, from, low, to, nullptr, 0.0f, dev_status, sms, st)
+                           : run_ns<kGgResult>(q, E, from, B, 0, down, one * down, from, low, out, res, 0.0f, dev_status, sms, st);
+        if (rc) return rc;
+    }
+    return MOE_OK;
 }
 
 }  // extern "C"

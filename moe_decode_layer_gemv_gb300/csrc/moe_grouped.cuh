@@ -34,8 +34,10 @@ enum { kGgFwd = 0, kGgDx = 1, kGgDw = 2 };
 
 // What the epilogue makes of a tile: the product itself; a gated unit of a
 // forward product's gate and up rows; the gated unit's gradient of a dx
-// product.
-enum { kGgStore = 0, kGgGlu = 1, kGgGluBack = 2 };
+// product; and, with fp16 operands and segments of one length, the products of
+// orthogonalisation (moe_ortho.cuh): a symmetric one, of which half the tiles
+// are computed and stored twice, a general one, and one into the bf16 result.
+enum { kGgStore = 0, kGgGlu = 1, kGgGluBack = 2, kGgSym = 3, kGgAxpy = 4, kGgResult = 5 };
 
 constexpr int kGgMaxStages = 12;
 constexpr int kGgBoxN = 32;          // rows per TMA box of a K-major B operand
@@ -66,6 +68,11 @@ struct GgParams {
     void* out2;      // forward: gu [R, 2 M] bf16, or nullptr; backward: h [R, M] bf16
     const void* in;  // backward: gu
     float c0, c1;    // the activation's coefficients
+    // orthogonalisation: out = alpha product + beta in - shift 1 (in's and out's rows as the product's; nullptr: none)
+    float alpha, beta, shift;
+    void* low;       // B X: what fp16 leaves of in, added to it, and replaced by what it leaves of out
+    int rows;        // of every segment (offsets is then not read)
+    int res_rows, res_cols, res_trans;  // the result's matrices: [E, res_rows, res_cols], transposed or not
     CUtensorMap zero[4];  // dw: boxes of 64 columns x 8, 4, 2 and 1 rows, for rows of zeros from behind x's end
     int32_t* status;
 };
@@ -429,13 +436,13 @@ __device__ __forceinline__ uint4 ld_stream_v4(const void* p) {
 // The segments into shared memory.  Offsets outside [0, R] or descending
 // leave their segment out (and set MOE_DEV_BAD_OFFSETS): nothing is read or
 // written outside the tensors.  start[e] = tiles of bn rows before segment e.
-__device__ __forceinline__ void gg_segments(GgShared* sh, const int32_t* offsets, int E, int R, int bn,
+__device__ __forceinline__ void gg_segments(GgShared* sh, const int32_t* offsets, int rows, int E, int R, int bn,
                                             int32_t* status) {
     const int tid = threadIdx.x;
     if (tid == 0) sh->nmax = 0;
     __syncthreads();
     for (int e = tid; e < E; e += blockDim.x) {
-        const int a = offsets[e], b = offsets[e + 1];
+        const int a = rows ? e * rows : offsets[e], b = rows ? a + rows : offsets[e + 1];
         const bool ok = a >= 0 && b >= a && b <= R;
         if (!ok && blockIdx.x == 0) set_status(status, MOE_DEV_BAD_OFFSETS);
         sh->p0[e] = ok ? a : 0;
@@ -672,6 +679,119 @@ __device__ __forceinline__ void glu_back_store(const P& p, const uint32_t (&sum)
     }
 }
 
+// ------------------------------------------------------- orthogonalisation
+__device__ __forceinline__ uint32_t gg_pack_f16(float first, float second) {
+    const __half2 h = __floats2half2_rn(first, second);
+    return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+// out = alpha product + beta in (- shift on the diagonal of a symmetric one)
+// for this lane's m, rows r0 on of segment e.  Symmetric: rows of p.M values in fp16, of a tile below the diagonal also
+// into its mirror image, a lane's values then lying side by side.  General:
+// without the mirror, in and out in two fp16 values each.  Result: bf16 into
+// matrices of any size, as they are or transposed.
+template <int COLS, int EP, typename P>
+__device__ __forceinline__ void ns_store(const P& p, const uint32_t (&sum)[COLS / 32][32], int e, int r0, int mine, int m,
+                                         bool mirror) {
+    const int M = p.M, odd = m & 1;
+    const uint32_t sel = gg_pair_select(odd);
+    const int last = m < M ? mine - odd : 0;  // rows r0 + odd + j, j < last
+    const size_t pair = ((size_t)e * p.rows + r0 + odd) * M + (m - odd);
+    const uint16_t* in = static_cast<const uint16_t*>(p.in) + pair;
+    uint16_t* out = static_cast<uint16_t*>(p.out);
+    uint16_t* low = static_cast<uint16_t*>(p.low) + pair;
+    constexpr int B = 16;
+    uint32_t next[B / 2], lnext[B / 2];
+    auto fetch = [&](int c) {
+#pragma unroll
+        for (int j = 0; j < B; j += 2) {
+            next[j / 2] = p.in && c + j < last ? ld_input_u32(in + (size_t)(c + j) * M) : 0u;
+            if (EP != kGgSym) lnext[j / 2] = c + j < last ? ld_input_u32(low + (size_t)(c + j) * M) : 0u;
+        }
+    };
+    fetch(0);
+#pragma unroll
+    for (int c = 0; c < COLS; c += B) {
+        if (c >= mine) break;
+        uint32_t w[B / 2], l[B / 2];  // rows c + j and c + j + 1 of this lane's m
+#pragma unroll
+        for (int j = 0; j < B / 2; ++j) {
+            w[j] = next[j];
+            if (EP != kGgSym) l[j] = lnext[j];
+        }
+        if (c + B < COLS) fetch(c + B);
+#pragma unroll
+        for (int j = 0; j < B; j += 2) {
+            const uint32_t h = gg_pair(w[j / 2], sel);
+            float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h));
+            if (EP != kGgSym) {
+                const uint32_t hl = gg_pair(l[j / 2], sel);
+                const float2 fl = __half22float2(*reinterpret_cast<const __half2*>(&hl));
+                f.x += fl.x;
+                f.y += fl.y;
+            }
+            float v0 = fmaf(p.beta, f.x, p.alpha * __uint_as_float(sum[(c + j) / 32][(c + j) % 32]));
+            float v1 = fmaf(p.beta, f.y, p.alpha * __uint_as_float(sum[(c + j) / 32][(c + j) % 32 + 1]));
+            if (EP == kGgSym) {
+                v0 -= r0 + c + j == m ? p.shift : 0.0f;
+                v1 -= r0 + c + j + 1 == m ? p.shift : 0.0f;
+            }
+            w[j / 2] = EP == kGgResult ? gg_pack(__float_as_uint(v0), __float_as_uint(v1)) : gg_pack_f16(v0, v1);
+            if (EP == kGgAxpy) {
+                const float2 t = __half22float2(*reinterpret_cast<const __half2*>(&w[j / 2]));
+                l[j / 2] = gg_pack_f16(v0 - t.x, v1 - t.y);
+            }
+        }
+        if (EP != kGgResult) {
+#pragma unroll
+            for (int j = 0; j < B; j += 2) {
+                const uint32_t v = gg_pair(w[j / 2], sel);
+                const uint32_t vl = EP == kGgAxpy ? gg_pair(l[j / 2], sel) : 0u;
+                if (c + j < last) {
+                    *reinterpret_cast<uint32_t*>(out + pair + (size_t)(c + j) * M) = v;
+                    if (EP == kGgAxpy) *reinterpret_cast<uint32_t*>(low + (size_t)(c + j) * M) = vl;
+                }
+            }
+            if (EP == kGgSym && mirror && m < M) {
+                // (rows come in eights, so do the tile's: whole pieces of 16 bytes)
+                uint4* to = reinterpret_cast<uint4*>(out + ((size_t)e * p.rows + m) * M + r0 + c);
+                to[0] = make_uint4(w[0], w[1], w[2], w[3]);
+                if (c + 8 < mine) to[1] = make_uint4(w[4], w[5], w[6], w[7]);
+            }
+        } else if (p.res_trans) {
+            if (m < p.res_rows) {
+                uint16_t* to = out + ((size_t)e * p.res_rows + m) * p.res_cols + r0 + c;
+                const int n = min(mine - c, p.res_cols - (r0 + c));
+#pragma unroll
+                for (int j = 0; j < B; j += 8) {
+                    if (j + 8 <= n && p.res_cols % 8 == 0) {
+                        *reinterpret_cast<uint4*>(to + j) = make_uint4(w[j / 2], w[j / 2 + 1], w[j / 2 + 2], w[j / 2 + 3]);
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < 8; ++i)
+                            if (j + i < n) to[j + i] = (uint16_t)(w[(j + i) / 2] >> (i & 1) * 16);
+                    }
+                }
+            }
+        } else {
+            const int rows = p.res_rows - (r0 + c);  // left of the matrix
+            uint16_t* to = out + ((size_t)e * p.res_rows + r0 + c) * p.res_cols + m;
+            const bool even = p.res_cols % 2 == 0;
+#pragma unroll
+            for (int j = 0; j < B; j += 2) {
+                const uint32_t v = gg_pair(w[j / 2], sel);
+                if (even) {
+                    if (m < p.res_cols && c + j < last && j + odd < rows)
+                        *reinterpret_cast<uint32_t*>(to + (size_t)(j + odd) * p.res_cols - odd) = v;
+                } else if (m < p.res_cols) {
+                    if (c + j < mine && j < rows) to[(size_t)j * p.res_cols] = (uint16_t)w[j / 2];
+                    if (c + j + 1 < mine && j + 1 < rows) to[(size_t)(j + 1) * p.res_cols] = (uint16_t)(w[j / 2] >> 16);
+                }
+            }
+        }
+    }
+}
+
 // ------------------------------------------------------------- the kernel
 // Persistent: one CTA per SM (or one pair of CTAs per SM pair) walks the
 // tiles.  Three roles run through the same tile sequence, each at its own
@@ -712,7 +832,7 @@ __global__ void __launch_bounds__((GgCfg<MODE, CG, F32>::kThreads), 1) gg_kernel
     grid_dep_wait();
     constexpr int MW = EP == kGgGlu ? 64 : 128, BMW = MW * CG;  // outputs that a CTA's 128 rows and a tile give
     const int mtiles = (p.M + BMW - 1) / BMW;
-    gg_segments(sh, p.offsets, p.E, p.R, Cfg::BN, p.status);
+    gg_segments(sh, p.offsets, EP >= kGgSym ? p.rows : 0, p.E, p.R, Cfg::BN, p.status);
     tc_fence_before();
     __syncthreads();
     if (CG == 2) cluster_sync();
@@ -730,16 +850,26 @@ __global__ void __launch_bounds__((GgCfg<MODE, CG, F32>::kThreads), 1) gg_kernel
     const uint32_t S = min((uint32_t)kGgMaxStages, ((uint32_t)kGgSmem - 1023u - 4096u) / stage_bytes);
 
     const int ntiles_w = (p.NW + Cfg::BN - 1) / Cfg::BN;  // dw
-    const int outers = MODE == kGgDw ? p.split * p.E : sh->start[p.E];
+    const int tri = EP == kGgSym ? mtiles * (mtiles + 1) / 2 : 0;  // tiles on and below the diagonal
+    const int outers = EP == kGgSym ? p.E : MODE == kGgDw ? p.split * p.E : sh->start[p.E];
 
     // f(e, q0, n, n0, m0, len): segment e; first row q0 (forward, dx: of the
     // tile; dw: of the segment's part); n valid columns from n0 on; m from m0
     // on; contraction length.  (dw: e counts part after part, part * E + e)
     auto walk = [&](auto f) {
         int e = 0;
-        for (GgWalk w(unit, units, MODE == kGgDw ? mtiles * ntiles_w : mtiles); w.outer < outers; w.next()) {
+        for (GgWalk w(unit, units, EP == kGgSym ? tri : MODE == kGgDw ? mtiles * ntiles_w : mtiles); w.outer < outers; w.next()) {
             int q0, n, n0, m0, len;
-            if (MODE == kGgDw) {
+            if (EP == kGgSym) {
+                e = w.outer;
+                int i = 0, j = w.inner;  // row i of the triangle holds i + 1 tiles
+                while (j > i) j -= ++i;
+                m0 = j * BMW;
+                n0 = i * Cfg::BN;
+                n = min(Cfg::BN, p.rows - n0);
+                q0 = e * p.rows + n0;
+                len = p.C;
+            } else if (MODE == kGgDw) {
                 e = w.outer;
                 const int tn = w.inner / mtiles;
                 m0 = (w.inner - tn * mtiles) * BMW;
@@ -838,7 +968,7 @@ __global__ void __launch_bounds__((GgCfg<MODE, CG, F32>::kThreads), 1) gg_kernel
         if (rank == 0 && gg_elect()) walk([&](int e, int q0, int n, int n0, int m0, int len) -> bool {
             const int nk = (len + 63) / 64;
             const int npad = MODE == kGgDw ? Cfg::BN : (n + kGgBoxN * CG - 1) / (kGgBoxN * CG) * (kGgBoxN * CG);
-            const uint32_t idesc = umma_idesc_bf16(Cfg::BM, npad) | (MODE != kGgFwd ? 1u << 15 : 0u) |
+            const uint32_t idesc = (EP >= kGgSym ? umma_idesc_f16(Cfg::BM, npad) : umma_idesc_bf16(Cfg::BM, npad)) | (MODE != kGgFwd ? 1u << 15 : 0u) |
                                    (MODE == kGgDw ? 1u << 16 : 0u);
             uint32_t acc = 0, tacc = 0;
             int room = 0;  // steps that the accumulator still takes
@@ -976,6 +1106,10 @@ __global__ void __launch_bounds__((GgCfg<MODE, CG, F32>::kThreads), 1) gg_kernel
             }
             if constexpr (EP == kGgGluBack) {
                 glu_back_store<Cfg::COLS>(p, sum, row0, mine, m);
+                return true;
+            }
+            if constexpr (EP >= kGgSym) {
+                ns_store<Cfg::COLS, EP>(p, sum, e, n0 + c0, mine, m, EP == kGgSym && n0 > m0);
                 return true;
             }
 #pragma unroll

@@ -514,7 +514,7 @@ __global__ void __launch_bounds__(kG4Threads, 1) g4_kernel(const __grid_constant
     if (warp == 9) gg_tmem_alloc<CG>(&sh->tmem_slot, kGgTmemCols);
     grid_dep_wait();
     const int mtiles = (p.M + 128 * CG - 1) / (128 * CG);
-    gg_segments(sh, p.offsets, p.E, p.R, Cfg::BN, p.status);
+    gg_segments(sh, p.offsets, 0, p.E, p.R, Cfg::BN, p.status);
     tc_fence_before();
     __syncthreads();
     if (CG == 2) cluster_sync();

@@ -1,0 +1,149 @@
+// moe_ortho.cuh -- orthogonalising matrices by Newton-Schulz products: the
+// norm and the conversion ahead of them (the products: gg_kernel with the
+// kGgSym, kGgAxpy and kGgResult epilogues, moe_grouped.cuh).
+//
+//   X = G / (|G|_F + eps);  A = X X^T;  X <- a X + (b A + c A A) X
+//
+// on the shorter side: a tall G is transposed as it is converted, and the last
+// product stores its transpose.  What the products read is held in fp16, with
+// |X|_2 near 1, so that nothing overflows (bf16 operands would be off by 8
+// times as much).  X itself is carried in two fp16 values, 22 bits, from step
+// to step: whatever is rounded off it in directions that G does not have grows
+// by a factor of a in each step, and a gradient of few tokens has few
+// directions (256 x 256 of rank 24: 3.1e-2 of the result with X in fp16 alone,
+// 1.5e-3 so).  In the last two steps A' = A - 1/2 takes A's place,
+//   a + b A + c A A = (a + b/2 + c/4) + (b + c) A' + c A' A',
+// since most eigenvalues of A are near 1 by then and b A + c A A several times
+// as large as what is left of it, and its roundings too (random 300 x 900
+// matrices: 1.7e-3 without, 1.0e-3 so; earlier it would undo the above).  The
+// bf16 result's own rounding is 1.7e-3.  X carries a factor of 2^8, which keeps the
+// entries of the largest matrices (2^-14 on average at 16384 x 16384) out of
+// fp16's subnormals; a single entry of 1 is still far from 65504.
+#pragma once
+
+#include <math_constants.h>
+
+#include "moe_common.cuh"
+#include "moe_grouped.cuh"
+#include "moe_ptx.cuh"
+
+namespace moe {
+
+constexpr int kNsScaleLog2 = 8;
+constexpr float kNsShift = 0.5f;
+constexpr int kNsShifted = 2;  // last steps with the shift
+constexpr int kNsParts = 64;  // blocks that sum one matrix's squares, at most
+
+__device__ __forceinline__ float ns_value(const void* g, bool f32, size_t i) {
+    return f32 ? __ldcg(static_cast<const float*>(g) + i)
+               : __uint_as_float((uint32_t)__ldcg(static_cast<const unsigned short*>(g) + i) << 16);
+}
+
+// Sums of squares that neither overflow nor underflow (Blue 1978): values
+// beyond 2^48 are summed times 2^-80, those below 2^-48 times 2^80.
+// parts [E, gridDim.x, 3].
+__global__ void __launch_bounds__(256) ns_norm_kernel(const void* g, int f32, size_t n, float* parts) {
+    __shared__ float s_sum[3][8];
+    grid_dep_wait();
+    const size_t base = blockIdx.y * n;
+    float s[3] = {0.0f, 0.0f, 0.0f};
+    auto add = [&](float x) {
+        const float a = fabsf(x);
+        const float big = a > 0x1p48f ? x * 0x1p-80f : 0.0f, tiny = a < 0x1p-48f ? x * 0x1p80f : 0.0f;
+        const float mid = a > 0x1p48f || a < 0x1p-48f ? 0.0f : x;  // (a NaN goes here)
+        s[0] = fmaf(big, big, s[0]);
+        s[1] = fmaf(mid, mid, s[1]);
+        s[2] = fmaf(tiny, tiny, s[2]);
+    };
+    const size_t step = (size_t)gridDim.x * 256, first = (size_t)blockIdx.x * 256 + threadIdx.x;
+    if (n % 8 == 0) {
+        for (size_t i = first; i < n / 8; i += step) {
+            if (f32) {
+                const uint4 a = ld_input_v4(static_cast<const float*>(g) + base + 8 * i);
+                const uint4 b = ld_input_v4(static_cast<const float*>(g) + base + 8 * i + 4);
+                const uint32_t u[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+#pragma unroll
+                for (int j = 0; j < 8; ++j) add(__uint_as_float(u[j]));
+            } else {
+                const uint4 a = ld_input_v4(static_cast<const uint16_t*>(g) + base + 8 * i);
+                const uint32_t u[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const float2 f = bf16x2_to_f2(u[j]);
+                    add(f.x);
+                    add(f.y);
+                }
+            }
+        }
+    } else {
+        for (size_t i = first; i < n; i += step) add(ns_value(g, f32, base + i));
+    }
+#pragma unroll
+    for (int j = 0; j < 3; ++j) {
+        s[j] = warp_sum(s[j]);
+        if ((threadIdx.x & 31) == 0) s_sum[j][threadIdx.x >> 5] = s[j];
+    }
+    __syncthreads();
+    if (threadIdx.x < 3) {
+        float t = 0.0f;
+#pragma unroll
+        for (int w = 0; w < 8; ++w) t += s_sum[threadIdx.x][w];
+        parts[((size_t)blockIdx.y * gridDim.x + blockIdx.x) * 3 + threadIdx.x] = t;
+    }
+}
+
+// X [E, rows, cols] = 2^8 G / (|G|_F + eps), or its transpose, in fp16, and in
+// `low` what that leaves; zeros beyond G's N x K.  A block takes 64 x 64 values of G.  A matrix with a NaN or
+// an infinity becomes NaN throughout.
+__global__ void __launch_bounds__(256) ns_convert_kernel(const void* g, int f32, int N, int K, const float* parts, int nparts,
+                                                         float eps, int trans, uint16_t* x, uint16_t* low, int rows,
+                                                         int cols) {
+    __shared__ uint16_t tile[2][64][66];
+    __shared__ float s_scale[2];
+    grid_dep_wait();
+    const int e = blockIdx.z, r0 = blockIdx.y * 64, c0 = blockIdx.x * 64, tid = threadIdx.x;
+    if (tid < 32) {
+        double s[3] = {0.0, 0.0, 0.0};
+        for (int i = tid; i < nparts; i += 32)
+            for (int j = 0; j < 3; ++j) s[j] += (double)__ldcg(parts + ((size_t)e * nparts + i) * 3 + j);
+#pragma unroll
+        for (int j = 0; j < 3; ++j)
+            for (int o = 16; o > 0; o >>= 1) s[j] += __shfl_xor_sync(0xffffffffu, s[j], o);
+        if (tid == 0) {
+            const double sum = s[0] * 0x1p160 + s[1] + s[2] * 0x1p-160;
+            const double scale = ldexp(1.0, kNsScaleLog2) / (sqrt(sum) + (double)eps);
+            // in two factors, since the whole may lie outside fp32's range
+            int ex = 0;
+            const double f = frexp(scale, &ex);
+            const bool ok = isfinite(sum) && isfinite(scale);
+            s_scale[0] = ok ? ldexpf(1.0f, ex / 2) : CUDART_NAN_F;
+            s_scale[1] = ok ? (float)ldexp(f, ex - ex / 2) : CUDART_NAN_F;
+        }
+    }
+    __syncthreads();
+    const float s0 = s_scale[0], s1 = s_scale[1];
+    for (int i = tid; i < 64 * 64; i += 256) {
+        const int r = i >> 6, c = i & 63;
+        float v = 0.0f;
+        if (r0 + r < N && c0 + c < K) v = ns_value(g, f32, ((size_t)e * N + r0 + r) * K + c0 + c) * s0 * s1;
+        const __half h = __float2half_rn(v);
+        const __half l = __float2half_rn(v - __half2float(h));
+        tile[0][r][c] = *reinterpret_cast<const uint16_t*>(&h);
+        tile[1][r][c] = *reinterpret_cast<const uint16_t*>(&l);
+    }
+    __syncthreads();
+    // rows of X: G's rows, or its columns
+    const int x0 = trans ? c0 : r0, y0 = trans ? r0 : c0;
+    for (int i = tid; i < 64 * 32; i += 256) {
+        const int r = i >> 5, c = (i & 31) * 2;
+        if (x0 + r >= rows || y0 + c >= cols) continue;
+        const size_t at = ((size_t)e * rows + x0 + r) * cols + y0 + c;
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            const uint32_t a = trans ? tile[j][c][r] : tile[j][r][c], b = trans ? tile[j][c + 1][r] : tile[j][r][c + 1];
+            *reinterpret_cast<uint32_t*>((j ? low : x) + at) = a | b << 16;
+        }
+    }
+}
+
+}  // namespace moe

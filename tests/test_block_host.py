@@ -99,3 +99,29 @@ def test_the_binding_checks_the_join(api):
         api.combine_norm(x.half(), o, pos, w)
     with pytest.raises(TypeError):
         api.combine_norm(x, o.half(), pos, w)
+
+
+def test_orthogonalisation_refuses_before_any_launch(api):
+    import ctypes
+    n = ctypes.c_size_t(0)
+    need = api._lib.moe_orthogonalize_workspace_bytes
+    inv = api.MOE_ERR_INVALID_ARG
+    assert need(3, 72, 40, ctypes.byref(n)) == 0 and n.value >= 3 * (2 * 40 * 72 + 2 * 40 * 40) * 2
+    assert need(3, 72, 40, None) == inv
+
+    def call(g=GOOD, dt=0, E=3, N=72, K=40, steps=5, a=3.0, b=-4.0, c=2.0, eps=1e-7, out=GOOD, ws=GOOD, nw=1 << 30, st=None):
+        return api._lib.moe_orthogonalize(g, dt, E, N, K, steps, a, b, c, eps, out, ws, nw, st, None)
+
+    for kw in (dict(E=0), dict(E=257), dict(N=0), dict(K=0), dict(N=16385), dict(K=16385), dict(dt=2), dict(steps=0),
+               dict(steps=17), dict(a=17.0), dict(b=-17.0), dict(c=float("nan")), dict(eps=-1.0), dict(eps=2.0),
+               dict(eps=float("nan")), *[{p: v} for p in ("g", "out") for v in (None, ODD)], dict(st=ODD), dict(ws=ODD)):
+        assert call(**kw) == inv, kw
+        if kw.keys() & {"E", "N", "K"}:
+            assert need(kw.get("E", 3), kw.get("N", 72), kw.get("K", 40), ctypes.byref(n)) == inv
+    assert call(ws=None) == api.MOE_ERR_WORKSPACE and call(nw=100) == api.MOE_ERR_WORKSPACE
+    for bad in (lambda: api.orthogonalize(_z(4, 8)), lambda: api.orthogonalize(_z(4)),
+                lambda: api.orthogonalize(_z(4, 8), coeffs=(1.0, 2.0))):
+        with pytest.raises(ValueError):
+            bad()
+    with pytest.raises(TypeError):
+        api.orthogonalize(_z(4, 8, dt=torch.float16))
