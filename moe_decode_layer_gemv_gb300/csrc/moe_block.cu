@@ -152,7 +152,6 @@ static int run_ns(const NsPlan& q, int E, const void* w, const void* x, int cols
     p.E = E;
     p.rows = q.m;
     p.R = E * q.m;
-    p.in = in;
     p.low = low;
     p.out = out;
     p.alpha = alpha;
@@ -172,6 +171,10 @@ static int run_ns(const NsPlan& q, int E, const void* w, const void* x, int cols
     }
     if (!ok || !encode_map(&p.tb, x, 2, p.C, p.R, 0, kGgBoxN) || !encode_map(&p.tb_all, x, 2, p.C, p.R, 0, 128))
         return MOE_ERR_UNSUPPORTED;
+    if (in) {
+        if (!encode_input(&p.tin[0], in, p.M, p.R) || (low && !encode_input(&p.tin[1], low, p.M, p.R))) return MOE_ERR_UNSUPPORTED;
+        p.planes = low ? 2 : 1;
+    }
     if (res) {
         p.res_rows = res[0];
         p.res_cols = res[1];
@@ -181,8 +184,8 @@ static int run_ns(const NsPlan& q, int E, const void* w, const void* x, int cols
     const int t = ceil_div(q.m, 256);
     const int64_t tiles = (int64_t)E * (EP == kGgSym ? t * (t + 1) / 2 : t * ceil_div(q.n, 256));
     return tiles >= sms / 2
-               ? launch_persistent<2>(gg_kernel<MODE, 2, false, EP>, p, GgCfg<MODE, 2, false>::kThreads, sms, st)
-               : launch_persistent<1>(gg_kernel<MODE, 1, false, EP>, p, GgCfg<MODE, 1, false>::kThreads, sms, st);
+               ? launch_persistent<2>(gg_kernel<MODE, 2, false, EP>, p, GgCfg<MODE, 2, false>::kThreads + 32, sms, st)
+               : launch_persistent<1>(gg_kernel<MODE, 1, false, EP>, p, GgCfg<MODE, 1, false>::kThreads + 32, sms, st);
 }
 
 }  // namespace moe
@@ -249,8 +252,12 @@ int moe_grouped_glu_backward(const uint16_t* dy, const uint16_t* down, const uin
     if (sms < 2) return MOE_ERR_CUDA;
     p.a_blocked = I % 64 == 0;
     if (!(p.a_blocked ? encode_blocked(&p.ta, down, I, H, E) : encode_map(&p.ta, down, 2, I, H, E, 64)) ||
-        !encode_map(&p.tb, dy, 2, H, R, 0, kGgBoxN) || !encode_map(&p.tb_all, dy, 2, H, R, 0, 128))
+        !encode_map(&p.tb, dy, 2, H, R, 0, kGgBoxN) || !encode_map(&p.tb_all, dy, 2, H, R, 0, 128) ||
+        !encode_input(&p.tin[0], gu, 2 * I, R))
         return MOE_ERR_UNSUPPORTED;
+    p.tin[1] = p.tin[0];
+    p.planes = 2;
+    p.tin_at[1] = I;
     p.offsets = offsets;
     p.E = E;
     p.R = R;
@@ -258,11 +265,10 @@ int moe_grouped_glu_backward(const uint16_t* dy, const uint16_t* down, const uin
     p.C = H;
     p.out = dgu;
     p.out2 = h;
-    p.in = gu;
     p.status = dev_status;
     return gg_pairs(R, I, E)
-               ? launch_persistent<2>(gg_kernel<kGgDx, 2, false, kGgGluBack>, p, GgCfg<kGgDx, 2, false>::kThreads, sms, st)
-               : launch_persistent<1>(gg_kernel<kGgDx, 1, false, kGgGluBack>, p, GgCfg<kGgDx, 1, false>::kThreads, sms, st);
+               ? launch_persistent<2>(gg_kernel<kGgDx, 2, false, kGgGluBack>, p, GgCfg<kGgDx, 2, false>::kThreads + 32, sms, st)
+               : launch_persistent<1>(gg_kernel<kGgDx, 1, false, kGgGluBack>, p, GgCfg<kGgDx, 1, false>::kThreads + 32, sms, st);
 }
 
 int moe_combine_norm(const void* x, int x_dtype, const void* o, int o_dtype, const int32_t* pos, const float* w, int T, int H,

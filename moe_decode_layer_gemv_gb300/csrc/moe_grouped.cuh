@@ -66,11 +66,14 @@ struct GgParams {
     int a_blocked, b_blocked;  // MN-major operands: the map has a 64-column block dimension
     // gated units
     void* out2;      // forward: gu [R, 2 M] bf16, or nullptr; backward: h [R, M] bf16
-    const void* in;  // backward: gu
     float c0, c1;    // the activation's coefficients
-    // orthogonalisation: out = alpha product + beta in - shift 1 (in's and out's rows as the product's; nullptr: none)
+    // inputs of the epilogue, maps of 16 rows x 128 columns of [R, ..] (kGgGluBack: g and u, of one tensor;
+    // orthogonalisation: in and what fp16 left of it), how many, the columns at which their m = 0 lies
+    CUtensorMap tin[2];
+    int planes, tin_at[2];
+    // orthogonalisation: out = alpha product + beta in - shift 1
     float alpha, beta, shift;
-    void* low;       // B X: what fp16 leaves of in, added to it, and replaced by what it leaves of out
+    void* low;       // B X: replaced by what fp16 leaves of out
     int rows;        // of every segment (offsets is then not read)
     int res_rows, res_cols, res_trans;  // the result's matrices: [E, res_rows, res_cols], transposed or not
     CUtensorMap zero[4];  // dw: boxes of 64 columns x 8, 4, 2 and 1 rows, for rows of zeros from behind x's end
@@ -98,7 +101,28 @@ struct GgCfg {
     static constexpr int KSUB = (CG == 1 && MODE != kGgDw) ? 2 : 1;
 };
 
+// The epilogues that read inputs (kGgGluBack and later ones) get them by
+// copies, 16 rows of both planes for each half of the columns at a time, so
+// many of them ahead.  (Loads into registers ahead of their use, beside 128
+// registers of sums, were spilled as they arrived: 683 us for the training
+// batch's backward pass.)  They read their tile out of tensor memory as they
+// go, from one accumulator for the whole sum: a loop of few registers and
+// little code.  Its truncated additions (kGgPartSteps) cost a sum of one sign
+// up to 7.4e-5 of 16384 terms, 2 % of half a step of the bf16 or a third of
+// one of the fp16 results.
+constexpr int kGgInRows = 16, kGgInSlots = 2;
+constexpr int kGgInPlane = kGgInRows * 256;                // bytes
+constexpr int kGgInBytes = 2 * kGgInSlots * 2 * kGgInPlane;  // halves x slots x planes
+
+template <int EP>
+struct GgIn {
+    static constexpr bool kOn = EP >= kGgGluBack;
+    static constexpr int kBytes = kOn ? kGgInBytes : 0, kWarps = kOn ? 1 : 0;
+    static constexpr int kPart = kOn ? 1 << 30 : kGgPartSteps;  // steps an accumulator takes
+};
+
 struct GgShared {
+    uint64_t in_full[2][kGgInSlots], in_empty[2][kGgInSlots];
     uint64_t full[kGgMaxStages];    // leader: a stage's tiles landed (in both CTAs)
     uint64_t tfull[kGgMaxStages];   // dw: the stage that a segment ends in landed in this CTA ...
     uint64_t clear[kGgMaxStages];   // ... leader: and its rows behind the segment are zero (in both CTAs)
@@ -620,62 +644,50 @@ __device__ __forceinline__ void glu_store(const P& p, uint32_t (&sum)[COLS / 32]
     }
 }
 
-__device__ __forceinline__ uint32_t ld_input_u32(const void* p) {
-    uint32_t r;
-    asm volatile("ld.global.u32 %0, [%1];" : "=r"(r) : "l"(p));
-    return r;
+// A place in the ring of a half's epilogue inputs.
+struct GgInRing {
+    uint32_t s = 0, ph = 0, uses = 0;
+    __device__ __forceinline__ void next() {
+        ++uses;
+        if (++s == kGgInSlots) {
+            s = 0;
+            ph ^= 1u;
+        }
+    }
+};
+
+__device__ __forceinline__ float in_bf16(const uint16_t* at, int row) { return bf_bits2f(at[row * 128]); }
+__device__ __forceinline__ float in_f16(const uint16_t* at, int row) {
+    return __half2float(*reinterpret_cast<const __half*>(at + row * 128));
 }
 
-// The gated unit's gradient of a dx tile (dh), this lane's m of rows row0 on:
+// Two rows' values of this lane's m into two neighbouring m of one row each
+// (gg_pair) and from there into 4 bytes of `to`.
+__device__ __forceinline__ void gg_put(uint16_t* to, uint32_t packed, uint32_t sel, bool there) {
+    const uint32_t v = gg_pair(packed, sel);
+    if (there) *reinterpret_cast<uint32_t*>(to) = v;
+}
+
+// The gated unit's gradient of 16 rows of a dx tile (dh, d), this lane's m:
 //   dg = dh u act'(g),  du = dh act(g),  h = act(g) u
-// g and u come as gg_store32 leaves them, two neighbouring m of one row in
-// each lane, and the results go the same way.
-template <int COLS, typename P>
-__device__ __forceinline__ void glu_back_store(const P& p, const uint32_t (&sum)[COLS / 32][32], size_t row0, int mine,
-                                               int m) {
+// row: the first of them; n: how many are there; g, u: this lane's column of the inputs.
+template <typename P>
+__device__ __forceinline__ void glu_back_rows(const P& p, const float (&d)[16], const uint16_t* g, const uint16_t* u,
+                                              size_t row, int n, int m) {
     const int I = p.M, odd = m & 1;
     const uint32_t sel = gg_pair_select(odd);
-    const int last = m < I ? mine - odd : 0;  // rows row0 + odd + j, j < last
-    const uint16_t* in = static_cast<const uint16_t*>(p.in) + (row0 + odd) * 2 * (size_t)I + (m - odd);
-    uint16_t* dgu = static_cast<uint16_t*>(p.out) + (row0 + odd) * 2 * (size_t)I + (m - odd);
-    uint16_t* hp = static_cast<uint16_t*>(p.out2) + (row0 + odd) * (size_t)I + (m - odd);
-    constexpr int B = 16;  // rows whose g and u are loaded ahead of the ones at work
-    uint32_t g[B / 2], u[B / 2];
-    auto fetch = [&](int c) {
+    const int last = m < I ? n - odd : 0;  // rows row + odd + j, j < last
+    uint16_t* dg = static_cast<uint16_t*>(p.out) + (row + odd) * 2 * (size_t)I + (m - odd);
+    uint16_t* hp = static_cast<uint16_t*>(p.out2) + (row + odd) * (size_t)I + (m - odd);
 #pragma unroll
-        for (int j = 0; j < B; j += 2) {
-            g[j / 2] = u[j / 2] = 0;
-            if (c + j < last) {
-                g[j / 2] = ld_input_u32(in + (size_t)(c + j) * 2 * I);
-                u[j / 2] = ld_input_u32(in + (size_t)(c + j) * 2 * I + I);
-            }
-        }
-    };
-    fetch(0);
-#pragma unroll
-    for (int c = 0; c < COLS; c += B) {
-        if (c >= mine) break;
-        uint32_t gc[B / 2], uc[B / 2];
-#pragma unroll
-        for (int j = 0; j < B / 2; ++j) gc[j] = g[j], uc[j] = u[j];
-        if (c + B < COLS) fetch(c + B);
-#pragma unroll
-        for (int j = 0; j < B; j += 2) {
-            // rows j (low halves) and j + 1 (high halves) of this lane's m
-            const uint32_t gp = gg_pair(gc[j / 2], sel), up = gg_pair(uc[j / 2], sel);
-            const float2 gf = bf16x2_to_f2(gp), uf = bf16x2_to_f2(up);
-            const float d0 = __uint_as_float(sum[(c + j) / 32][(c + j) % 32]);
-            const float d1 = __uint_as_float(sum[(c + j) / 32][(c + j) % 32 + 1]);
-            float e0, e1;
-            const float a0 = glu_act(gf.x, p.c0, p.c1, e0), a1 = glu_act(gf.y, p.c0, p.c1, e1);
-            auto put = [&](uint16_t* to, float v0, float v1) {
-                const uint32_t v = gg_pair(gg_pack(__float_as_uint(v0), __float_as_uint(v1)), sel);
-                if (c + j < last) *reinterpret_cast<uint32_t*>(to) = v;
-            };
-            put(dgu + (size_t)(c + j) * 2 * I, d0 * uf.x * e0, d1 * uf.y * e1);
-            put(dgu + (size_t)(c + j) * 2 * I + I, d0 * a0, d1 * a1);
-            put(hp + (size_t)(c + j) * I, a0 * uf.x, a1 * uf.y);
-        }
+    for (int j = 0; j < 16; j += 2, dg += 4 * (size_t)I, hp += 2 * (size_t)I) {
+        const float u0 = in_bf16(u, j), u1 = in_bf16(u, j + 1);
+        float e0, e1;
+        const float a0 = glu_act(in_bf16(g, j), p.c0, p.c1, e0), a1 = glu_act(in_bf16(g, j + 1), p.c0, p.c1, e1);
+        auto pack = [](float v0, float v1) { return gg_pack(__float_as_uint(v0), __float_as_uint(v1)); };
+        gg_put(dg, pack(d[j] * u0 * e0, d[j + 1] * u1 * e1), sel, j < last);
+        gg_put(dg + I, pack(d[j] * a0, d[j + 1] * a1), sel, j < last);
+        gg_put(hp, pack(a0 * u0, a1 * u1), sel, j < last);
     }
 }
 
@@ -686,107 +698,79 @@ __device__ __forceinline__ uint32_t gg_pack_f16(float first, float second) {
 }
 
 // out = alpha product + beta in (- shift on the diagonal of a symmetric one)
-// for this lane's m, rows r0 on of segment e.  Symmetric: rows of p.M values in fp16, of a tile below the diagonal also
+// for 16 rows of this lane's m, from row r of segment e on, n of them there.
+// Symmetric: rows of p.M values in fp16, of a tile below the diagonal also
 // into its mirror image, a lane's values then lying side by side.  General:
 // without the mirror, in and out in two fp16 values each.  Result: bf16 into
 // matrices of any size, as they are or transposed.
-template <int COLS, int EP, typename P>
-__device__ __forceinline__ void ns_store(const P& p, const uint32_t (&sum)[COLS / 32][32], int e, int r0, int mine, int m,
-                                         bool mirror) {
+template <int EP, typename P>
+__device__ __forceinline__ void ns_rows(const P& p, const float (&d)[16], const uint16_t* in, const uint16_t* lo, int e, int r,
+                                        int n, int m, bool mirror) {
     const int M = p.M, odd = m & 1;
     const uint32_t sel = gg_pair_select(odd);
-    const int last = m < M ? mine - odd : 0;  // rows r0 + odd + j, j < last
-    const size_t pair = ((size_t)e * p.rows + r0 + odd) * M + (m - odd);
-    const uint16_t* in = static_cast<const uint16_t*>(p.in) + pair;
+    const int last = m < M ? n - odd : 0;  // rows r + odd + j, j < last
+    const size_t pair = ((size_t)e * p.rows + r + odd) * M + (m - odd);
     uint16_t* out = static_cast<uint16_t*>(p.out);
-    uint16_t* low = static_cast<uint16_t*>(p.low) + pair;
-    constexpr int B = 16;
-    uint32_t next[B / 2], lnext[B / 2];
-    auto fetch = [&](int c) {
+    uint32_t w[8], l[8];  // rows j and j + 1 of this lane's m
 #pragma unroll
-        for (int j = 0; j < B; j += 2) {
-            next[j / 2] = p.in && c + j < last ? ld_input_u32(in + (size_t)(c + j) * M) : 0u;
-            if (EP != kGgSym) lnext[j / 2] = c + j < last ? ld_input_u32(low + (size_t)(c + j) * M) : 0u;
+    for (int j = 0; j < 16; j += 2) {
+        float v0 = p.alpha * d[j], v1 = p.alpha * d[j + 1];
+        if (p.planes) {
+            float f0 = in_f16(in, j), f1 = in_f16(in, j + 1);
+            if (EP != kGgSym) f0 += in_f16(lo, j), f1 += in_f16(lo, j + 1);
+            v0 = fmaf(p.beta, f0, v0);
+            v1 = fmaf(p.beta, f1, v1);
         }
-    };
-    fetch(0);
-#pragma unroll
-    for (int c = 0; c < COLS; c += B) {
-        if (c >= mine) break;
-        uint32_t w[B / 2], l[B / 2];  // rows c + j and c + j + 1 of this lane's m
-#pragma unroll
-        for (int j = 0; j < B / 2; ++j) {
-            w[j] = next[j];
-            if (EP != kGgSym) l[j] = lnext[j];
+        if (EP == kGgSym) {
+            v0 -= r + j == m ? p.shift : 0.0f;
+            v1 -= r + j + 1 == m ? p.shift : 0.0f;
         }
-        if (c + B < COLS) fetch(c + B);
+        w[j / 2] = EP == kGgResult ? gg_pack(__float_as_uint(v0), __float_as_uint(v1)) : gg_pack_f16(v0, v1);
+        if (EP == kGgAxpy) {
+            const float2 t = __half22float2(*reinterpret_cast<const __half2*>(&w[j / 2]));
+            l[j / 2] = gg_pack_f16(v0 - t.x, v1 - t.y);
+        }
+    }
+    if (EP != kGgResult) {
+        uint16_t *to = out + pair, *tl = static_cast<uint16_t*>(p.low) + pair;
 #pragma unroll
-        for (int j = 0; j < B; j += 2) {
-            const uint32_t h = gg_pair(w[j / 2], sel);
-            float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h));
-            if (EP != kGgSym) {
-                const uint32_t hl = gg_pair(l[j / 2], sel);
-                const float2 fl = __half22float2(*reinterpret_cast<const __half2*>(&hl));
-                f.x += fl.x;
-                f.y += fl.y;
-            }
-            float v0 = fmaf(p.beta, f.x, p.alpha * __uint_as_float(sum[(c + j) / 32][(c + j) % 32]));
-            float v1 = fmaf(p.beta, f.y, p.alpha * __uint_as_float(sum[(c + j) / 32][(c + j) % 32 + 1]));
-            if (EP == kGgSym) {
-                v0 -= r0 + c + j == m ? p.shift : 0.0f;
-                v1 -= r0 + c + j + 1 == m ? p.shift : 0.0f;
-            }
-            w[j / 2] = EP == kGgResult ? gg_pack(__float_as_uint(v0), __float_as_uint(v1)) : gg_pack_f16(v0, v1);
-            if (EP == kGgAxpy) {
-                const float2 t = __half22float2(*reinterpret_cast<const __half2*>(&w[j / 2]));
-                l[j / 2] = gg_pack_f16(v0 - t.x, v1 - t.y);
+        for (int j = 0; j < 16; j += 2, to += 2 * (size_t)M, tl += 2 * (size_t)M) {
+            gg_put(to, w[j / 2], sel, j < last);
+            if (EP == kGgAxpy) gg_put(tl, l[j / 2], sel, j < last);
+        }
+        if (EP == kGgSym && mirror && m < M) {
+            // (rows come in eights, so do the tile's: whole pieces of 16 bytes)
+            uint4* at = reinterpret_cast<uint4*>(out + ((size_t)e * p.rows + m) * M + r);
+            at[0] = make_uint4(w[0], w[1], w[2], w[3]);
+            if (n > 8) at[1] = make_uint4(w[4], w[5], w[6], w[7]);
+        }
+    } else if (p.res_trans) {
+        if (m >= p.res_rows) return;
+        uint16_t* to = out + ((size_t)e * p.res_rows + m) * p.res_cols + r;
+        const int k = min(n, p.res_cols - r);
+#pragma unroll
+        for (int j = 0; j < 16; j += 8) {
+            if (j + 8 <= k && p.res_cols % 8 == 0) {
+                *reinterpret_cast<uint4*>(to + j) = make_uint4(w[j / 2], w[j / 2 + 1], w[j / 2 + 2], w[j / 2 + 3]);
+            } else {
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    if (j + i < k) to[j + i] = (uint16_t)(w[(j + i) / 2] >> (i & 1) * 16);
             }
         }
-        if (EP != kGgResult) {
+    } else {
+        const int rows = min(n, p.res_rows - r);
+        uint16_t* to = out + ((size_t)e * p.res_rows + r) * p.res_cols + m;
+        const bool even = p.res_cols % 2 == 0;
 #pragma unroll
-            for (int j = 0; j < B; j += 2) {
-                const uint32_t v = gg_pair(w[j / 2], sel);
-                const uint32_t vl = EP == kGgAxpy ? gg_pair(l[j / 2], sel) : 0u;
-                if (c + j < last) {
-                    *reinterpret_cast<uint32_t*>(out + pair + (size_t)(c + j) * M) = v;
-                    if (EP == kGgAxpy) *reinterpret_cast<uint32_t*>(low + (size_t)(c + j) * M) = vl;
-                }
-            }
-            if (EP == kGgSym && mirror && m < M) {
-                // (rows come in eights, so do the tile's: whole pieces of 16 bytes)
-                uint4* to = reinterpret_cast<uint4*>(out + ((size_t)e * p.rows + m) * M + r0 + c);
-                to[0] = make_uint4(w[0], w[1], w[2], w[3]);
-                if (c + 8 < mine) to[1] = make_uint4(w[4], w[5], w[6], w[7]);
-            }
-        } else if (p.res_trans) {
-            if (m < p.res_rows) {
-                uint16_t* to = out + ((size_t)e * p.res_rows + m) * p.res_cols + r0 + c;
-                const int n = min(mine - c, p.res_cols - (r0 + c));
-#pragma unroll
-                for (int j = 0; j < B; j += 8) {
-                    if (j + 8 <= n && p.res_cols % 8 == 0) {
-                        *reinterpret_cast<uint4*>(to + j) = make_uint4(w[j / 2], w[j / 2 + 1], w[j / 2 + 2], w[j / 2 + 3]);
-                    } else {
-#pragma unroll
-                        for (int i = 0; i < 8; ++i)
-                            if (j + i < n) to[j + i] = (uint16_t)(w[(j + i) / 2] >> (i & 1) * 16);
-                    }
-                }
-            }
-        } else {
-            const int rows = p.res_rows - (r0 + c);  // left of the matrix
-            uint16_t* to = out + ((size_t)e * p.res_rows + r0 + c) * p.res_cols + m;
-            const bool even = p.res_cols % 2 == 0;
-#pragma unroll
-            for (int j = 0; j < B; j += 2) {
-                const uint32_t v = gg_pair(w[j / 2], sel);
-                if (even) {
-                    if (m < p.res_cols && c + j < last && j + odd < rows)
-                        *reinterpret_cast<uint32_t*>(to + (size_t)(j + odd) * p.res_cols - odd) = v;
-                } else if (m < p.res_cols) {
-                    if (c + j < mine && j < rows) to[(size_t)j * p.res_cols] = (uint16_t)w[j / 2];
-                    if (c + j + 1 < mine && j + 1 < rows) to[(size_t)(j + 1) * p.res_cols] = (uint16_t)(w[j / 2] >> 16);
-                }
+        for (int j = 0; j < 16; j += 2, to += 2 * (size_t)p.res_cols) {
+            const uint32_t v = gg_pair(w[j / 2], sel);
+            if (m >= p.res_cols) continue;
+            if (even) {
+                if (j + odd < rows) *reinterpret_cast<uint32_t*>(to + (size_t)odd * p.res_cols - odd) = v;
+            } else {
+                if (j < rows) to[0] = (uint16_t)w[j / 2];
+                if (j + 1 < rows) to[p.res_cols] = (uint16_t)(w[j / 2] >> 16);
             }
         }
     }
@@ -798,19 +782,27 @@ __device__ __forceinline__ void ns_store(const P& p, const uint32_t (&sum)[COLS 
 // pace: the producer fills the ring, the MMA issuer accumulates tile d into
 // tensor-memory buffer d mod 2, the epilogue warps read the other buffer out.
 template <int MODE, int CG, bool F32, int EP = kGgStore>
-__global__ void __launch_bounds__((GgCfg<MODE, CG, F32>::kThreads), 1) gg_kernel(const __grid_constant__ GgParams p) {
+__global__ void __launch_bounds__((GgCfg<MODE, CG, F32>::kThreads + 32 * GgIn<EP>::kWarps), 1) gg_kernel(const __grid_constant__ GgParams p) {
     using Cfg = GgCfg<MODE, CG, F32>;
     extern __shared__ __align__(1024) unsigned char gg_smem_raw[];
     unsigned char* base = reinterpret_cast<unsigned char*>(
         (reinterpret_cast<uintptr_t>(gg_smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
     GgShared* sh = reinterpret_cast<GgShared*>(base);
-    unsigned char* ring = base + 4096;
+    using In = GgIn<EP>;
+    // (beside the inputs two steps a stage would leave room for two stages)
+    constexpr int KSUB = In::kOn ? 1 : Cfg::KSUB;
+    unsigned char* ins = base + 4096;
+    unsigned char* ring = ins + In::kBytes;
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t rank = CG == 2 ? cluster_rank() : 0u;
     const int unit = (int)blockIdx.x / CG, units = (int)gridDim.x / CG;
 
     if (threadIdx.x == 0) {
+        for (int s = 0; In::kOn && s < 2 * kGgInSlots; ++s) {
+            mbar_init(&sh->in_full[s & 1][s >> 1], 1);
+            mbar_init(&sh->in_empty[s & 1][s >> 1], 4);
+        }
         for (int s = 0; s < kGgMaxStages; ++s) {
             mbar_init(&sh->full[s], 1);
             mbar_init(&sh->tfull[s], 1);
@@ -845,9 +837,9 @@ __global__ void __launch_bounds__((GgCfg<MODE, CG, F32>::kThreads), 1) gg_kernel
     uint32_t b_tile = kGgTile;
     if (MODE != kGgDw && CG == 1)
         b_tile = (uint32_t)min(Cfg::BN, max(kGgBoxN, (sh->nmax + kGgBoxN - 1) / kGgBoxN * kGgBoxN)) * 128u;
-    const uint32_t stage_bytes = Cfg::KSUB * (kGgTile + b_tile);
-    const uint32_t b_off = Cfg::KSUB * kGgTile;
-    const uint32_t S = min((uint32_t)kGgMaxStages, ((uint32_t)kGgSmem - 1023u - 4096u) / stage_bytes);
+    const uint32_t stage_bytes = KSUB * (kGgTile + b_tile);
+    const uint32_t b_off = KSUB * kGgTile;
+    const uint32_t S = min((uint32_t)kGgMaxStages, ((uint32_t)kGgSmem - 1023u - 4096u - In::kBytes) / stage_bytes);
 
     const int ntiles_w = (p.NW + Cfg::BN - 1) / Cfg::BN;  // dw
     const int tri = EP == kGgSym ? mtiles * (mtiles + 1) / 2 : 0;  // tiles on and below the diagonal
@@ -906,10 +898,10 @@ __global__ void __launch_bounds__((GgCfg<MODE, CG, F32>::kThreads), 1) gg_kernel
                 const int rows = MODE == kGgDw ? 128 : (n + kGgBoxN * CG - 1) / (kGgBoxN * CG) * kGgBoxN;
                 const uint32_t bytes = CG * (kGgTile + (uint32_t)rows * 128u);
                 const int am = m0 + (int)rank * MW, bn = (MODE == kGgDw ? n0 : q0) + (int)rank * rows;
-                for (int k0 = 0; k0 < nk; k0 += Cfg::KSUB) {
+                for (int k0 = 0; k0 < nk; k0 += KSUB) {
                     if (!gg_wait(&sh->empty[r.s], r.ph ^ 1u, &sh->abort)) return false;
                     const uint32_t st = ring_at + r.s * stage_bytes, bar = bars + r.s * 8u;
-                    const int ke = min(Cfg::KSUB, nk - k0);
+                    const int ke = min(KSUB, nk - k0);
                     // dw: the stage that a segment ends in, if not with a whole MMA, lands on
                     // each CTA's own barrier and is cleared there before it counts as full
                     const bool tail = MODE == kGgDw && gg_ragged(len - k0 * 64);
@@ -922,7 +914,7 @@ __global__ void __launch_bounds__((GgCfg<MODE, CG, F32>::kThreads), 1) gg_kernel
                             mbar_arrive_expect_tx(&sh->full[r.s], (uint32_t)ke * bytes);
                     }
 #pragma unroll
-                    for (int u = 0; u < Cfg::KSUB; ++u) {
+                    for (int u = 0; u < KSUB; ++u) {
                         if (u >= ke) break;
                         const uint32_t sa = st + u * kGgTile, sb = st + b_off + u * b_tile;
                         const int c = (k0 + u) * 64;
@@ -972,12 +964,12 @@ __global__ void __launch_bounds__((GgCfg<MODE, CG, F32>::kThreads), 1) gg_kernel
                                    (MODE == kGgDw ? 1u << 16 : 0u);
             uint32_t acc = 0, tacc = 0;
             int room = 0;  // steps that the accumulator still takes
-            for (int k0 = 0; k0 < nk; k0 += Cfg::KSUB) {
+            for (int k0 = 0; k0 < nk; k0 += KSUB) {
                 if (room == 0) {
                     if (!gg_wait(&sh->acc_empty[buf], free_ph, &sh->abort)) return false;
                     tacc = tmem + (uint32_t)(buf * Cfg::BN);
                     acc = 0;
-                    room = kGgPartSteps;
+                    room = In::kPart;
                 }
                 if (!gg_wait(&sh->full[r.s], r.ph, &sh->abort)) return false;
                 const uint32_t sta = ring_at + r.s * stage_bytes;
@@ -990,12 +982,12 @@ __global__ void __launch_bounds__((GgCfg<MODE, CG, F32>::kThreads), 1) gg_kernel
                         tails ^= 1u << r.s;
                     }
                 }
-                room -= Cfg::KSUB;  // (a whole number of stages)
-                const bool last = room == 0 || k0 + Cfg::KSUB >= nk;
+                room -= KSUB;  // (a whole number of stages)
+                const bool last = room == 0 || k0 + KSUB >= nk;
                 tc_fence_after();
-                const int ke = min(Cfg::KSUB, nk - k0);
+                const int ke = min(KSUB, nk - k0);
 #pragma unroll
-                for (int u = 0; u < Cfg::KSUB; ++u) {
+                for (int u = 0; u < KSUB; ++u) {
                     if (u >= ke) break;
                     // the 16-deep steps of a tile: 32 bytes of a K-major row, 16 rows of an MN-major tile
                     const uint32_t aa = sta + u * kGgTile, ba = sta + b_off + u * b_tile;
@@ -1027,7 +1019,33 @@ __global__ void __launch_bounds__((GgCfg<MODE, CG, F32>::kThreads), 1) gg_kernel
             gg_settle(&sh->mma_done, 0u);
         }
         __syncwarp();
-    } else if (warp == Cfg::EPI + 2) {
+    } else if (In::kOn && warp == Cfg::EPI + 2) {
+        // ---------------- inputs of the epilogue
+        GgInRing r[2];
+        if (p.planes && gg_elect()) {
+            walk([&](int e, int q0, int n, int n0, int m0, int len) -> bool {
+                const int m = m0 + (int)rank * MW;
+                for (int c = 0; c < Cfg::COLS; c += kGgInRows)
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        if (h * Cfg::COLS + c >= n) continue;
+                        if (!gg_wait(&sh->in_empty[h][r[h].s], r[h].ph ^ 1u, &sh->abort)) return false;
+                        uint64_t* bar = &sh->in_full[h][r[h].s];
+                        const uint32_t to = smem_u32(ins) + (h * kGgInSlots + r[h].s) * 2 * kGgInPlane;
+                        mbar_arrive_expect_tx(bar, p.planes * kGgInPlane);
+                        for (int i = 0; i < p.planes; ++i)
+                            gg_load2<1>(to + i * kGgInPlane, &p.tin[i], p.tin_at[i] + m, q0 + h * Cfg::COLS + c, smem_u32(bar));
+                        r[h].next();
+                    }
+                return true;
+            });
+            // no copy may be on its way when the CTA exits
+            for (int h = 0; h < 2; ++h)
+                for (uint32_t s = 0; s < kGgInSlots && s < r[h].uses; ++s)
+                    gg_settle(&sh->in_full[h][s], s < r[h].s ? r[h].ph : r[h].ph ^ 1u);
+        }
+        __syncwarp();
+    } else if (MODE == kGgDw && warp == Cfg::EPI + 2) {
         // ---------------- dw: the segment's end.  Rows behind it belong to
         // the next segment (or to no one), so both operands' rows up to the
         // last MMA's end are zeroed -- zeroing one would leave 0 x infinity or
@@ -1071,6 +1089,7 @@ __global__ void __launch_bounds__((GgCfg<MODE, CG, F32>::kThreads), 1) gg_kernel
         int buf = 0;
         uint32_t full_ph = 0;
         const int c0 = (warp >> 2) * Cfg::COLS;
+        GgInRing in;
         walk([&](int e, int q0, int n, int n0, int m0, int len) -> bool {
             const int nk = (len + 63) / 64;
             const int m = m0 + (int)rank * 128 + (warp & 3) * 32 + lane;
@@ -1081,6 +1100,40 @@ __global__ void __launch_bounds__((GgCfg<MODE, CG, F32>::kThreads), 1) gg_kernel
 #pragma unroll
                 for (int j = 0; j < 32; ++j) z[j] = 0;
                 for (int c = 0; c < mine; c += 32) gg_store32(z, p.out, F32, row0 + c, min(32, mine - c), m, p.M);
+                return true;
+            }
+            if constexpr (In::kOn) {
+                const uint32_t taddr = tmem + (uint32_t)(buf * Cfg::BN + c0) + ((uint32_t)((warp & 3) * 32) << 16);
+                const int h = warp >> 2;
+                if (!gg_wait_warp(&sh->acc_full[buf], full_ph, &sh->abort)) return false;
+                tc_fence_after();
+                for (int c = 0; c < mine; c += kGgInRows) {
+                    const uint16_t* at = reinterpret_cast<const uint16_t*>(ins + (h * kGgInSlots + in.s) * 2 * kGgInPlane) +
+                                         (warp & 3) * 32 + lane;
+                    if (p.planes && !gg_wait_warp(&sh->in_full[h][in.s], in.ph, &sh->abort)) return false;
+                    float d[16];
+                    tmem_ld16(taddr + c, d);
+                    if constexpr (EP == kGgGluBack)
+                        glu_back_rows(p, d, at, at + kGgInPlane / 2, row0 + c, min(16, mine - c), m);
+                    else
+                        ns_rows<EP>(p, d, at, at + kGgInPlane / 2, e, n0 + c0 + c, min(16, mine - c), m,
+                                    EP == kGgSym && n0 > m0);
+                    if (p.planes) {
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(&sh->in_empty[h][in.s]);
+                        in.next();
+                    }
+                }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) {
+                    if (CG == 1)
+                        mbar_arrive(&sh->acc_empty[buf]);
+                    else
+                        mbar_arrive_cluster(&sh->acc_empty[buf], 0);
+                }
+                buf ^= 1;
+                if (buf == 0) full_ph ^= 1u;
                 return true;
             }
             uint32_t sum[Cfg::COLS / 32][32];  // the parts' sum
@@ -1102,14 +1155,6 @@ __global__ void __launch_bounds__((GgCfg<MODE, CG, F32>::kThreads), 1) gg_kernel
             }
             if constexpr (EP == kGgGlu) {
                 glu_store<Cfg::COLS, F32>(p, sum, row0, mine, m0 + (int)rank * MW + (warp & 3) * 16, lane);
-                return true;
-            }
-            if constexpr (EP == kGgGluBack) {
-                glu_back_store<Cfg::COLS>(p, sum, row0, mine, m);
-                return true;
-            }
-            if constexpr (EP >= kGgSym) {
-                ns_store<Cfg::COLS, EP>(p, sum, e, n0 + c0, mine, m, EP == kGgSym && n0 > m0);
                 return true;
             }
 #pragma unroll
