@@ -110,7 +110,7 @@ struct GgCfg {
 // little code.  Its truncated additions (kGgPartSteps) cost a sum of one sign
 // up to 7.4e-5 of 16384 terms, 2 % of half a step of the bf16 or a third of
 // one of the fp16 results.
-constexpr int kGgInRows = 16, kGgInSlots = 2;
+constexpr int kGgInRows = 16, kGgInSlots = 3;
 constexpr int kGgInPlane = kGgInRows * 256;                // bytes
 constexpr int kGgInBytes = 2 * kGgInSlots * 2 * kGgInPlane;  // halves x slots x planes
 
