@@ -91,11 +91,16 @@ static int run_join(const JoinParams& p, int sms, cudaStream_t st) {
     return p.T < 2 * sms ? run_join<OF32, 512>(p, 1, st) : run_join<OF32, 256>(p, 8, st);
 }
 
-// Blocks of the backward pass: what an SM's shared memory holds, four at most.
+// The backward pass: up to 512 threads a token of one vector each, beyond of
+// several; as many blocks an SM as its registers (128 a thread) and shared
+// memory hold.
+static int join_back_vectors(int H) { return join_vectors(H, 512); }
 static int join_back_grid(int T, int H, int sums, int sms) {
-    const size_t each = (size_t)sums * H * 4 + 4096;
-    int per = (int)((200 * 1024) / each);
-    per = per < 1 ? 1 : per > 4 ? 4 : per;
+    const int threads = (int)join_threads(H, join_back_vectors(H));
+    int per = 512 / threads;
+    const int fit = (int)((200 * 1024) / ((size_t)sums * H * 4 + 4096));
+    if (per > fit) per = fit;
+    per = per < 1 ? 1 : per > 16 ? 16 : per;
     return T < per * sms ? T : per * sms;
 }
 
@@ -104,18 +109,17 @@ static int launch_join_back(const JoinParams& p, int grid, cudaStream_t st) {
     const size_t smem = (size_t)p.sums * p.H * 4;
     // (with the kernel's static part 48 KB are passed earlier)
     const int rc = smem > 32 * 1024 ? to_status(cudaFuncSetAttribute(
-                                          join_back_kernel<OF32, NV>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem))
+                                          join_back_kernel<OF32, NV, 512>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem))
                                     : MOE_OK;
-    return rc ? rc : launch_pdl(join_back_kernel<OF32, NV>, (unsigned)grid, join_threads(p.H, NV), smem, st, p);
+    return rc ? rc : launch_pdl(join_back_kernel<OF32, NV, 512>, (unsigned)grid, join_threads(p.H, NV), smem, st, p);
 }
 
 template <bool OF32>
 static int run_join_back(const JoinParams& p, int grid, cudaStream_t st) {
-    switch (join_vectors(p.H, 256)) {
+    switch (join_back_vectors(p.H)) {
         case 1: return launch_join_back<OF32, 1>(p, grid, st);
         case 2: return launch_join_back<OF32, 2>(p, grid, st);
-        case 4: return launch_join_back<OF32, 4>(p, grid, st);
-        default: return launch_join_back<OF32, 8>(p, grid, st);
+        default: return launch_join_back<OF32, 4>(p, grid, st);
     }
 }
 

@@ -99,6 +99,21 @@ __device__ __forceinline__ void add8(float* sums, int nvec, int v, const float (
 }
 
 // ---------------------------------------------------------------- reductions
+// Eight values' sums over a warp: lanes take over half of the values at each of
+// three steps, so that nine shuffles do instead of forty; lane 4 v + .. ends
+// with value v's sum.
+__device__ __forceinline__ float warp_sum8(const float (&v)[8], int lane) {
+    float a[4], b[2], c;
+    const bool h16 = lane & 16, h8 = lane & 8, h4 = lane & 4;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) a[i] = (h16 ? v[i + 4] : v[i]) + __shfl_xor_sync(0xffffffffu, h16 ? v[i] : v[i + 4], 16);
+#pragma unroll
+    for (int i = 0; i < 2; ++i) b[i] = (h8 ? a[i + 2] : a[i]) + __shfl_xor_sync(0xffffffffu, h8 ? a[i] : a[i + 2], 8);
+    c = (h4 ? b[1] : b[0]) + __shfl_xor_sync(0xffffffffu, h4 ? b[0] : b[1], 4);
+    c += __shfl_xor_sync(0xffffffffu, c, 2);
+    return c + __shfl_xor_sync(0xffffffffu, c, 1);
+}
+
 // Sums over the threads of one token (blockDim.x, whole warps) of N values;
 // every thread of the block takes part.  `buf`: blockDim.y * 32 * N floats,
 // free again after the next barrier of the block.
@@ -137,24 +152,27 @@ __device__ __forceinline__ void token_routes(const JoinParams& p, int t, bool va
     }
 }
 
-// z of eight columns
-template <bool OF32>
+// z of eight columns, G rows on their way at a time
+template <bool OF32, int G>
 __device__ __forceinline__ void gather8(const JoinParams& p, const int (&row)[MOE_MAX_TOPK], const float (&w)[MOE_MAX_TOPK],
                                         int v, float (&z)[8]) {
-    Raw8 r[MOE_MAX_TOPK];
-#pragma unroll
-    for (int j = 0; j < MOE_MAX_TOPK; ++j)
-        if (row[j] >= 0) r[j] = raw8(p.o, OF32, row[j], p.H, v);
 #pragma unroll
     for (int i = 0; i < 8; ++i) z[i] = 0.0f;
 #pragma unroll
-    for (int j = 0; j < MOE_MAX_TOPK; ++j)
-        if (row[j] >= 0) {
-            float f[8];
-            values8(r[j], OF32, f);
+    for (int g = 0; g < MOE_MAX_TOPK; g += G) {
+        Raw8 r[G];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) z[i] = fmaf(w[j], f[i], z[i]);
-        }
+        for (int j = 0; j < G; ++j)
+            if (row[g + j] >= 0) r[j] = raw8(p.o, OF32, row[g + j], p.H, v);
+#pragma unroll
+        for (int j = 0; j < G; ++j)
+            if (row[g + j] >= 0) {
+                float f[8];
+                values8(r[j], OF32, f);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) z[i] = fmaf(w[g + j], f[i], z[i]);
+            }
+    }
 }
 
 // ---------------------------------------------------------------- forward
@@ -168,12 +186,15 @@ __global__ void __launch_bounds__(MT) join_kernel(JoinParams p) {
     const bool valid = t < p.T;
     int row[MOE_MAX_TOPK];
     float w[MOE_MAX_TOPK], s[1] = {0.0f}, b[NV][8];
+    Raw8 rx;  // (NV = 1: the stream's columns are on their way with the rows)
+    const bool ahead = NV == 1 && valid && (int)threadIdx.x < nvec;
+    if (ahead) rx = raw8(p.x, p.x_f32, t, p.H, threadIdx.x);
     token_routes(p, t, valid, row, w);
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
         const int v = threadIdx.x + i * blockDim.x;
         if (!valid || v >= nvec) continue;
-        gather8<OF32>(p, row, w, v, b[i]);
+        gather8<OF32, 8>(p, row, w, v, b[i]);
 #pragma unroll
         for (int c = 0; c < 8; ++c) s[0] = fmaf(b[i][c], b[i][c], s[0]);
     }
@@ -193,7 +214,7 @@ __global__ void __launch_bounds__(MT) join_kernel(JoinParams p) {
 #pragma unroll
             for (int c = 0; c < 8; ++c) b[i][c] *= r * f[c];
         }
-        values8(raw8(p.x, p.x_f32, t, p.H, v), p.x_f32, x);
+        values8(NV == 1 ? rx : raw8(p.x, p.x_f32, t, p.H, v), p.x_f32, x);
         if (p.scale) {
             vector8(p.scale, v, f);
 #pragma unroll
@@ -230,11 +251,18 @@ __global__ void __launch_bounds__(MT) join_kernel(JoinParams p) {
 //   dpre = sum_t dn y rms(y),  dscale = sum_t d b,  dpost = sum_t g z rms(z)
 // A block walks tokens and keeps the column sums in shared memory, each column
 // by the thread that owns it; the blocks' sums are joined in a fixed order.
-template <bool OF32, int NV>
-__global__ void __launch_bounds__(256) join_back_kernel(JoinParams p) {
+//
+// Bound by HBM: every input is read once.  With NV = 1 a thread keeps what it
+// read of a token (its row of o, two of the stream, dn) in registers to the
+// token's end, all loads in flight at once, and the next token's rows are
+// known by then.  Wider rows are read again, from L2.
+template <bool OF32, int NV, int MT>
+__global__ void __launch_bounds__(MT) join_back_kernel(JoinParams p) {
     extern __shared__ __align__(16) float cols[];  // [sums][H]
-    __shared__ float buf[3][32 * MOE_MAX_TOPK];
-    const int nvec = p.H / 8;
+    __shared__ float buf[2][32 * 3];
+    __shared__ float dbuf[32][MOE_MAX_TOPK];
+    constexpr bool HOLD = NV == 1;
+    const int nvec = p.H / 8, lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
     for (int i = threadIdx.x; i < p.sums * p.H; i += blockDim.x) cols[i] = 0.0f;
     float* at = cols;
     float* c_post = p.post ? at : nullptr;
@@ -244,19 +272,66 @@ __global__ void __launch_bounds__(256) join_back_kernel(JoinParams p) {
     float* c_pre = at;
     grid_dep_wait();
     __syncthreads();
+    // the routes of a token, lane j the j-th
+    int r_next = -1;
+    float w_next = 0.0f;
+    auto routes = [&](int t) {
+        r_next = -1;
+        w_next = 0.0f;
+        if (p.o && lane < p.k && t < p.T) {
+            const size_t i = (size_t)t * p.k + lane;
+            r_next = p.pos ? p.pos[i] : (int)i;
+            w_next = p.w ? p.w[i] : 1.0f;
+        }
+    };
+    routes(blockIdx.x);
     for (int t = blockIdx.x; t < p.T; t += gridDim.x) {
+        if (r_next < -1 || r_next >= p.R) {
+            set_status(p.status, MOE_DEV_BAD_ROUTE);
+            r_next = -1;
+        }
         int row[MOE_MAX_TOPK];
         float w[MOE_MAX_TOPK], s[3] = {0.0f, 0.0f, 0.0f}, z[NV][8], d[NV][8];
-        token_routes(p, t, true, row, w);
+#pragma unroll
+        for (int j = 0; j < MOE_MAX_TOPK; ++j) {
+            row[j] = __shfl_sync(0xffffffffu, r_next, j);
+            w[j] = __shfl_sync(0xffffffffu, w_next, j);
+        }
+        Raw8 ro[HOLD ? MOE_MAX_TOPK : 1], ry, rn, rd;
+        const bool mine = (int)threadIdx.x < nvec;
+        if (HOLD && mine) {
+            if (p.pre) {
+                ry = raw8(p.x, p.x_f32, t, p.H, threadIdx.x);
+                rn = raw8(p.dn, p.n_f32, t, p.H, threadIdx.x);
+            }
+            if (p.dy) rd = raw8(p.dy, p.x_f32, t, p.H, threadIdx.x);
+#pragma unroll
+            for (int j = 0; j < MOE_MAX_TOPK; ++j)
+                if (row[j] >= 0) ro[HOLD ? j : 0] = raw8(p.o, OF32, row[j], p.H, threadIdx.x);
+        }
+        routes(t + gridDim.x);
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             const int v = threadIdx.x + i * blockDim.x;
             if (v >= nvec) continue;
-            if (p.o) gather8<OF32>(p, row, w, v, z[i]);
+            if (HOLD) {
+#pragma unroll
+                for (int c = 0; c < 8; ++c) z[i][c] = 0.0f;
+#pragma unroll
+                for (int j = 0; j < MOE_MAX_TOPK; ++j)
+                    if (row[j] >= 0) {
+                        float f[8];
+                        values8(ro[HOLD ? j : 0], OF32, f);
+#pragma unroll
+                        for (int c = 0; c < 8; ++c) z[i][c] = fmaf(w[j], f[c], z[i][c]);
+                    }
+            } else if (p.o) {
+                gather8<OF32, OF32 ? 2 : 4>(p, row, w, v, z[i]);
+            }
             if (p.pre) {
                 float y[8], a[8], f[8];
-                values8(raw8(p.x, p.x_f32, t, p.H, v), p.x_f32, y);
-                values8(raw8(p.dn, p.n_f32, t, p.H, v), p.n_f32, a);
+                values8(HOLD ? ry : raw8(p.x, p.x_f32, t, p.H, v), p.x_f32, y);
+                values8(HOLD ? rn : raw8(p.dn, p.n_f32, t, p.H, v), p.n_f32, a);
                 vector8(p.pre, v, f);
 #pragma unroll
                 for (int c = 0; c < 8; ++c) {
@@ -269,29 +344,29 @@ __global__ void __launch_bounds__(256) join_back_kernel(JoinParams p) {
                 for (int c = 0; c < 8; ++c) s[2] = fmaf(z[i][c], z[i][c], s[2]);
             }
         }
-        token_sum(s, buf[0]);
-        const float ry = 1.0f / sqrtf(s[0] / (float)p.H + p.eps), my = ry * ry * ry * (s[1] / (float)p.H);
-        const float rz = 1.0f / sqrtf(s[2] / (float)p.H + p.eps);
+        if (p.pre || p.post) token_sum(s, buf[0]);
+        const float ny = 1.0f / sqrtf(s[0] / (float)p.H + p.eps), my = ny * ny * ny * (s[1] / (float)p.H);
+        const float nz = 1.0f / sqrtf(s[2] / (float)p.H + p.eps);
         float cz[1] = {0.0f};
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             const int v = threadIdx.x + i * blockDim.x;
             if (v >= nvec) continue;
             if (p.dy) {
-                values8(raw8(p.dy, p.x_f32, t, p.H, v), p.x_f32, d[i]);
+                values8(HOLD ? rd : raw8(p.dy, p.x_f32, t, p.H, v), p.x_f32, d[i]);
             } else {
 #pragma unroll
                 for (int c = 0; c < 8; ++c) d[i][c] = 0.0f;
             }
             if (p.pre) {
                 float y[8], a[8], f[8];
-                values8(raw8(p.x, p.x_f32, t, p.H, v), p.x_f32, y);
-                values8(raw8(p.dn, p.n_f32, t, p.H, v), p.n_f32, a);
+                values8(HOLD ? ry : raw8(p.x, p.x_f32, t, p.H, v), p.x_f32, y);
+                values8(HOLD ? rn : raw8(p.dn, p.n_f32, t, p.H, v), p.n_f32, a);
                 vector8(p.pre, v, f);
 #pragma unroll
                 for (int c = 0; c < 8; ++c) {
-                    d[i][c] += ry * (a[c] * f[c]) - y[c] * my;
-                    f[c] = a[c] * y[c] * ry;
+                    d[i][c] += ny * (a[c] * f[c]) - y[c] * my;
+                    f[c] = a[c] * y[c] * ny;
                 }
                 add8(c_pre, nvec, v, f);
             }
@@ -301,7 +376,7 @@ __global__ void __launch_bounds__(256) join_back_kernel(JoinParams p) {
             if (p.post) vector8(p.post, v, q);
             if (c_scale) {
 #pragma unroll
-                for (int c = 0; c < 8; ++c) f[c] = d[i][c] * (p.post ? z[i][c] * rz * q[c] : z[i][c]);
+                for (int c = 0; c < 8; ++c) f[c] = d[i][c] * (p.post ? z[i][c] * nz * q[c] : z[i][c]);
                 add8(c_scale, nvec, v, f);
             }
             if (p.scale) {
@@ -314,7 +389,7 @@ __global__ void __launch_bounds__(256) join_back_kernel(JoinParams p) {
             }
             if (p.post) {
 #pragma unroll
-                for (int c = 0; c < 8; ++c) f[c] = d[i][c] * (z[i][c] * rz);
+                for (int c = 0; c < 8; ++c) f[c] = d[i][c] * (z[i][c] * nz);
                 add8(c_post, nvec, v, f);
 #pragma unroll
                 for (int c = 0; c < 8; ++c) {
@@ -330,7 +405,7 @@ __global__ void __launch_bounds__(256) join_back_kernel(JoinParams p) {
         float mz = 0.0f;
         if (p.post) {
             token_sum(cz, buf[1]);
-            mz = rz * rz * rz * (cz[0] / (float)p.H);
+            mz = nz * nz * nz * (cz[0] / (float)p.H);
         }
         float dots[MOE_MAX_TOPK] = {};
 #pragma unroll
@@ -339,14 +414,14 @@ __global__ void __launch_bounds__(256) join_back_kernel(JoinParams p) {
             if (v >= nvec) continue;
             if (p.post) {
 #pragma unroll
-                for (int c = 0; c < 8; ++c) d[i][c] = rz * d[i][c] - z[i][c] * mz;
+                for (int c = 0; c < 8; ++c) d[i][c] = nz * d[i][c] - z[i][c] * mz;
             }
 #pragma unroll
             for (int j = 0; j < MOE_MAX_TOPK; ++j)
                 if (row[j] >= 0) {
                     float f[8];
                     if (p.dw) {
-                        values8(raw8(p.o, OF32, row[j], p.H, v), OF32, f);
+                        values8(HOLD ? ro[HOLD ? j : 0] : raw8(p.o, OF32, row[j], p.H, v), OF32, f);
 #pragma unroll
                         for (int c = 0; c < 8; ++c) dots[j] = fmaf(d[i][c], f[c], dots[j]);
                     }
@@ -356,12 +431,17 @@ __global__ void __launch_bounds__(256) join_back_kernel(JoinParams p) {
                 }
         }
         if (p.dw) {
-            token_sum(dots, buf[2]);
-#pragma unroll
-            for (int j = 0; j < MOE_MAX_TOPK; ++j)
-                if (j < p.k && threadIdx.x == j) p.dw[(size_t)t * p.k + j] = dots[j];
+            const float one = warp_sum8(dots, lane);
+            if ((lane & 3) == 0) dbuf[warp][lane >> 2] = one;
         }
-        __syncthreads();
+        __syncthreads();  // (buf is used again behind it)
+        if (p.dw && threadIdx.x < p.k) {
+            float sum = 0.0f;
+            for (int i = 0; i < warps; ++i) sum += dbuf[i][threadIdx.x];
+            p.dw[(size_t)t * p.k + threadIdx.x] = sum;
+        }
+        // (dbuf is written again only behind the next token's sums; without any there is one more barrier)
+        if (p.dw && !p.pre && !p.post) __syncthreads();
     }
     float4* out = reinterpret_cast<float4*>(p.parts + (size_t)blockIdx.x * p.sums * p.H);
     const float4* in = reinterpret_cast<const float4*>(cols);
