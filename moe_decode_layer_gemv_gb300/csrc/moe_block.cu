@@ -133,7 +133,7 @@ struct NsPlan {
 
 static int ns_plan(int E, int N, int K, NsPlan* q) {
     if (E < 1 || E > MOE_MAX_E || N < 1 || N > MOE_MAX_DIM || K < 1 || K > MOE_MAX_DIM) return MOE_ERR_INVALID_ARG;
-    q->m = ceil_div(N < K ? N : K, 8) * 8;
+    q->m = ceil_div(N < K ? N : K, 16) * 16;
     q->n = ceil_div(N < K ? K : N, 64) * 64;
     q->parts = ceil_div(4 * kMaxSms, E);
     const int most = (int)(((size_t)N * K + 2047) / 2048);

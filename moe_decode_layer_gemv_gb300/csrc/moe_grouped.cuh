@@ -656,13 +656,23 @@ struct GgInRing {
     }
 };
 
-__device__ __forceinline__ float in_bf16(const uint16_t* at, int row) { return bf_bits2f(at[row * 128]); }
 __device__ __forceinline__ float in_f16(const uint16_t* at, int row) {
     return __half2float(*reinterpret_cast<const __half*>(at + row * 128));
 }
+__device__ __forceinline__ uint32_t in_pair(const uint16_t* at, int row) {
+    return *reinterpret_cast<const uint32_t*>(at + row * 128);
+}
 
-// Two rows' values of this lane's m into two neighbouring m of one row each
-// (gg_pair) and from there into 4 bytes of `to`.
+// Two rows' sums of this lane's m (d0, d1) into two neighbouring m, m - odd and
+// m - odd + 1, of row `odd` of the two: the lanes of a pair swap one each, and
+// what is read and written beside them then comes in 4-byte pieces as it lies
+// in memory.
+__device__ __forceinline__ float2 gg_swap(float d0, float d1, int odd) {
+    const float got = __shfl_xor_sync(0xffffffffu, odd ? d0 : d1, 1);
+    return odd ? make_float2(got, d1) : make_float2(d0, got);
+}
+
+// Two rows' values of this lane's m, packed, the same way into 4 bytes of `to`.
 __device__ __forceinline__ void gg_put(uint16_t* to, uint32_t packed, uint32_t sel, bool there) {
     const uint32_t v = gg_pair(packed, sel);
     if (there) *reinterpret_cast<uint32_t*>(to) = v;
@@ -670,24 +680,26 @@ __device__ __forceinline__ void gg_put(uint16_t* to, uint32_t packed, uint32_t s
 
 // The gated unit's gradient of 16 rows of a dx tile (dh, d), this lane's m:
 //   dg = dh u act'(g),  du = dh act(g),  h = act(g) u
-// row: the first of them; n: how many are there; g, u: this lane's column of the inputs.
+// row: the first of them; n: how many are there; ins: the inputs at m = 0 of this warp's 32.
 template <typename P>
-__device__ __forceinline__ void glu_back_rows(const P& p, const float (&d)[16], const uint16_t* g, const uint16_t* u,
-                                              size_t row, int n, int m) {
-    const int I = p.M, odd = m & 1;
-    const uint32_t sel = gg_pair_select(odd);
+__device__ __forceinline__ void glu_back_rows(const P& p, const float* d, const uint16_t* ins, size_t row, int n, int m,
+                                              int lane) {
+    const int I = p.M, odd = lane & 1;
     const int last = m < I ? n - odd : 0;  // rows row + odd + j, j < last
+    const uint16_t *g = ins + (lane - odd) + odd * 128, *u = g + kGgInPlane / 2;
     uint16_t* dg = static_cast<uint16_t*>(p.out) + (row + odd) * 2 * (size_t)I + (m - odd);
     uint16_t* hp = static_cast<uint16_t*>(p.out2) + (row + odd) * (size_t)I + (m - odd);
 #pragma unroll
     for (int j = 0; j < 16; j += 2, dg += 4 * (size_t)I, hp += 2 * (size_t)I) {
-        const float u0 = in_bf16(u, j), u1 = in_bf16(u, j + 1);
+        const float2 dh = gg_swap(d[j], d[j + 1], odd), gf = bf16x2_to_f2(in_pair(g, j)), uf = bf16x2_to_f2(in_pair(u, j));
         float e0, e1;
-        const float a0 = glu_act(in_bf16(g, j), p.c0, p.c1, e0), a1 = glu_act(in_bf16(g, j + 1), p.c0, p.c1, e1);
+        const float a0 = glu_act(gf.x, p.c0, p.c1, e0), a1 = glu_act(gf.y, p.c0, p.c1, e1);
         auto pack = [](float v0, float v1) { return gg_pack(__float_as_uint(v0), __float_as_uint(v1)); };
-        gg_put(dg, pack(d[j] * u0 * e0, d[j + 1] * u1 * e1), sel, j < last);
-        gg_put(dg + I, pack(d[j] * a0, d[j + 1] * a1), sel, j < last);
-        gg_put(hp, pack(a0 * u0, a1 * u1), sel, j < last);
+        if (j < last) {
+            *reinterpret_cast<uint32_t*>(dg) = pack(dh.x * uf.x * e0, dh.y * uf.y * e1);
+            *reinterpret_cast<uint32_t*>(dg + I) = pack(dh.x * a0, dh.y * a1);
+            *reinterpret_cast<uint32_t*>(hp) = pack(a0 * uf.x, a1 * uf.y);
+        }
     }
 }
 
@@ -697,54 +709,83 @@ __device__ __forceinline__ uint32_t gg_pack_f16(float first, float second) {
     return *reinterpret_cast<const uint32_t*>(&h);
 }
 
-// out = alpha product + beta in (- shift on the diagonal of a symmetric one)
-// for 16 rows of this lane's m, from row r of segment e on, n of them there.
-// Symmetric: rows of p.M values in fp16, of a tile below the diagonal also
-// into its mirror image, a lane's values then lying side by side.  General:
-// without the mirror, in and out in two fp16 values each.  Result: bf16 into
-// matrices of any size, as they are or transposed.
-template <int EP, typename P>
-__device__ __forceinline__ void ns_rows(const P& p, const float (&d)[16], const uint16_t* in, const uint16_t* lo, int e, int r,
-                                        int n, int m, bool mirror) {
-    const int M = p.M, odd = m & 1;
-    const uint32_t sel = gg_pair_select(odd);
+__device__ __forceinline__ float2 f16x2_to_f2(uint32_t u) { return __half22float2(*reinterpret_cast<const __half2*>(&u)); }
+
+// out = alpha product + beta in for 16 rows of this lane's m, from row r of
+// segment e on, n of them there; in and out in two fp16 values each.
+template <typename P>
+__device__ __forceinline__ void ns_axpy_rows(const P& p, const float* d, const uint16_t* ins, int e, int r, int n, int m,
+                                             int lane) {
+    const int M = p.M, odd = lane & 1;
     const int last = m < M ? n - odd : 0;  // rows r + odd + j, j < last
+    const uint16_t *in = ins + (lane - odd) + odd * 128, *lo = in + kGgInPlane / 2;
     const size_t pair = ((size_t)e * p.rows + r + odd) * M + (m - odd);
-    uint16_t* out = static_cast<uint16_t*>(p.out);
-    uint32_t w[8], l[8];  // rows j and j + 1 of this lane's m
+    uint16_t *to = static_cast<uint16_t*>(p.out) + pair, *tl = static_cast<uint16_t*>(p.low) + pair;
 #pragma unroll
-    for (int j = 0; j < 16; j += 2) {
+    for (int j = 0; j < 16; j += 2, to += 2 * (size_t)M, tl += 2 * (size_t)M) {
+        const float2 v = gg_swap(d[j], d[j + 1], odd), f = f16x2_to_f2(in_pair(in, j)), l = f16x2_to_f2(in_pair(lo, j));
+        const float v0 = fmaf(p.beta, f.x + l.x, p.alpha * v.x), v1 = fmaf(p.beta, f.y + l.y, p.alpha * v.y);
+        const uint32_t w = gg_pack_f16(v0, v1);
+        const float2 t = f16x2_to_f2(w);
+        const uint32_t x = gg_pack_f16(v0 - t.x, v1 - t.y);
+        if (j < last) {
+            *reinterpret_cast<uint32_t*>(to) = w;
+            *reinterpret_cast<uint32_t*>(tl) = x;
+        }
+    }
+}
+
+// The same without the low parts of a symmetric product, less shift on the
+// diagonal, into rows of p.M fp16 values (a multiple of 16, as are the rows);
+// of a tile below the diagonal also into its mirror image, where a lane's
+// values lie side by side: 32 bytes, a whole sector.
+template <typename P>
+__device__ __forceinline__ void ns_sym_rows(const P& p, const float* d, const uint16_t* ins, int e, int r, int m, int lane,
+                                            bool mirror) {
+    const int M = p.M, odd = lane & 1;
+    const uint32_t sel = gg_pair_select(odd);
+    const bool there = m < M;
+    uint16_t* out = static_cast<uint16_t*>(p.out);
+    uint16_t* to = out + ((size_t)e * p.rows + r + odd) * M + (m - odd);
+    uint32_t w[8];  // rows j and j + 1 of this lane's m
+#pragma unroll
+    for (int j = 0; j < 16; j += 2, to += 2 * (size_t)M) {
         float v0 = p.alpha * d[j], v1 = p.alpha * d[j + 1];
         if (p.planes) {
-            float f0 = in_f16(in, j), f1 = in_f16(in, j + 1);
-            if (EP != kGgSym) f0 += in_f16(lo, j), f1 += in_f16(lo, j + 1);
-            v0 = fmaf(p.beta, f0, v0);
-            v1 = fmaf(p.beta, f1, v1);
+            v0 = fmaf(p.beta, in_f16(ins + lane, j), v0);
+            v1 = fmaf(p.beta, in_f16(ins + lane, j + 1), v1);
         }
-        if (EP == kGgSym) {
+        if (!mirror) {
             v0 -= r + j == m ? p.shift : 0.0f;
             v1 -= r + j + 1 == m ? p.shift : 0.0f;
         }
-        w[j / 2] = EP == kGgResult ? gg_pack(__float_as_uint(v0), __float_as_uint(v1)) : gg_pack_f16(v0, v1);
-        if (EP == kGgAxpy) {
-            const float2 t = __half22float2(*reinterpret_cast<const __half2*>(&w[j / 2]));
-            l[j / 2] = gg_pack_f16(v0 - t.x, v1 - t.y);
-        }
+        w[j / 2] = gg_pack_f16(v0, v1);
+        gg_put(to, w[j / 2], sel, there);
     }
-    if (EP != kGgResult) {
-        uint16_t *to = out + pair, *tl = static_cast<uint16_t*>(p.low) + pair;
+    if (mirror && there) {
+        uint16_t* at = out + ((size_t)e * p.rows + m) * M + r;
+        asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(at), "r"(w[0]), "r"(w[1]), "r"(w[2]),
+                     "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+                     : "memory");
+    }
+}
+
+// The last product: bf16 into matrices of any size, as they are or transposed.
+template <typename P>
+__device__ __forceinline__ void ns_result_rows(const P& p, const float* d, const uint16_t* ins, int e, int r, int n, int m,
+                                               int lane) {
+    const int odd = lane & 1;
+    const uint32_t sel = gg_pair_select(odd);
+    const uint16_t *in = ins + lane, *lo = in + kGgInPlane / 2;
+    uint16_t* out = static_cast<uint16_t*>(p.out);
+    uint32_t w[8];  // rows j and j + 1 of this lane's m
 #pragma unroll
-        for (int j = 0; j < 16; j += 2, to += 2 * (size_t)M, tl += 2 * (size_t)M) {
-            gg_put(to, w[j / 2], sel, j < last);
-            if (EP == kGgAxpy) gg_put(tl, l[j / 2], sel, j < last);
-        }
-        if (EP == kGgSym && mirror && m < M) {
-            // (rows come in eights, so do the tile's: whole pieces of 16 bytes)
-            uint4* at = reinterpret_cast<uint4*>(out + ((size_t)e * p.rows + m) * M + r);
-            at[0] = make_uint4(w[0], w[1], w[2], w[3]);
-            if (n > 8) at[1] = make_uint4(w[4], w[5], w[6], w[7]);
-        }
-    } else if (p.res_trans) {
+    for (int j = 0; j < 16; j += 2) {
+        const float v0 = fmaf(p.beta, in_f16(in, j) + in_f16(lo, j), p.alpha * d[j]);
+        const float v1 = fmaf(p.beta, in_f16(in, j + 1) + in_f16(lo, j + 1), p.alpha * d[j + 1]);
+        w[j / 2] = gg_pack(__float_as_uint(v0), __float_as_uint(v1));
+    }
+    if (p.res_trans) {
         if (m >= p.res_rows) return;
         uint16_t* to = out + ((size_t)e * p.res_rows + m) * p.res_cols + r;
         const int k = min(n, p.res_cols - r);
@@ -1107,21 +1148,29 @@ __global__ void __launch_bounds__((GgCfg<MODE, CG, F32>::kThreads + 32 * GgIn<EP
                 const int h = warp >> 2;
                 if (!gg_wait_warp(&sh->acc_full[buf], full_ph, &sh->abort)) return false;
                 tc_fence_after();
-                for (int c = 0; c < mine; c += kGgInRows) {
-                    const uint16_t* at = reinterpret_cast<const uint16_t*>(ins + (h * kGgInSlots + in.s) * 2 * kGgInPlane) +
-                                         (warp & 3) * 32 + lane;
-                    if (p.planes && !gg_wait_warp(&sh->in_full[h][in.s], in.ph, &sh->abort)) return false;
-                    float d[16];
-                    tmem_ld16(taddr + c, d);
-                    if constexpr (EP == kGgGluBack)
-                        glu_back_rows(p, d, at, at + kGgInPlane / 2, row0 + c, min(16, mine - c), m);
-                    else
-                        ns_rows<EP>(p, d, at, at + kGgInPlane / 2, e, n0 + c0 + c, min(16, mine - c), m,
-                                    EP == kGgSym && n0 > m0);
-                    if (p.planes) {
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive(&sh->in_empty[h][in.s]);
-                        in.next();
+                for (int c = 0; c < mine; c += 2 * kGgInRows) {
+                    uint32_t r[32];
+                    float d[32];
+                    gg_ld32(taddr + c, r);
+                    gg_ld_wait(r);
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) d[j] = __uint_as_float(r[j]);
+#pragma unroll
+                    for (int i = 0; i < 2 * kGgInRows; i += kGgInRows) {
+                        if (c + i >= mine) break;
+                        const uint16_t* at =
+                            reinterpret_cast<const uint16_t*>(ins + (h * kGgInSlots + in.s) * 2 * kGgInPlane) + (warp & 3) * 32;
+                        if (p.planes && !gg_wait_warp(&sh->in_full[h][in.s], in.ph, &sh->abort)) return false;
+                        const int rows = min(kGgInRows, mine - c - i), r0 = n0 + c0 + c + i;
+                        if constexpr (EP == kGgGluBack) glu_back_rows(p, d + i, at, row0 + c + i, rows, m, lane);
+                        if constexpr (EP == kGgSym) ns_sym_rows(p, d + i, at, e, r0, m, lane, n0 > m0);
+                        if constexpr (EP == kGgAxpy) ns_axpy_rows(p, d + i, at, e, r0, rows, m, lane);
+                        if constexpr (EP == kGgResult) ns_result_rows(p, d + i, at, e, r0, rows, m, lane);
+                        if (p.planes) {
+                            __syncwarp();
+                            if (lane == 0) mbar_arrive(&sh->in_empty[h][in.s]);
+                            in.next();
+                        }
                     }
                 }
                 tc_fence_before();
