@@ -126,70 +126,101 @@ static int run_join_back(const JoinParams& p, int grid, cudaStream_t st) {
 // ---------------------------------------------------------- orthogonalisation
 struct NsPlan {
     int m, n;        // rows and columns of X, padded
+    int group;       // matrices that go through all steps together
     int parts;       // blocks that sum a matrix's squares
-    size_t x, a, p;  // bytes of X, of A, of the sums
+    bool pairs;      // tiles of CTA pairs
+    size_t x, a, p;  // bytes of a group's X, of its A, of the sums
     size_t bytes;
 };
 
-static int ns_plan(int E, int N, int K, NsPlan* q) {
+static int ns_plan(int E, int N, int K, int sms, NsPlan* q) {
     if (E < 1 || E > MOE_MAX_E || N < 1 || N > MOE_MAX_DIM || K < 1 || K > MOE_MAX_DIM) return MOE_ERR_INVALID_ARG;
     q->m = ceil_div(N < K ? N : K, 16) * 16;
     q->n = ceil_div(N < K ? K : N, 64) * 64;
-    q->parts = ceil_div(4 * kMaxSms, E);
+    // pairs of CTAs where their larger tiles still give every pair work
+    const int t = ceil_div(q->m, 256);
+    const int tri = t * (t + 1) / 2;
+    q->pairs = (int64_t)E * tri >= sms / 2;
+    q->group = E;
+    q->parts = ceil_div(4 * sms, q->group);
     const int most = (int)(((size_t)N * K + 2047) / 2048);
     if (q->parts > most) q->parts = most;
     if (q->parts > kNsParts) q->parts = kNsParts;
-    q->x = align_up(sizeof(uint16_t) * (size_t)E * q->m * q->n, 256);
-    q->a = align_up(sizeof(uint16_t) * (size_t)E * q->m * q->m, 256);
-    q->p = align_up(sizeof(float) * 3 * (size_t)E * q->parts, 256);
+    q->x = align_up(sizeof(uint16_t) * (size_t)q->group * q->m * q->n, 256);
+    q->a = align_up(sizeof(uint16_t) * (size_t)q->group * q->m * q->m, 256);
+    q->p = align_up(sizeof(float) * 3 * (size_t)q->group * q->parts, 256);
     q->bytes = 3 * q->x + 2 * q->a + q->p;
     return MOE_OK;
 }
 
-// One product: X X^T or A A (symmetric), or B X.
-template <int EP>
-static int run_ns(const NsPlan& q, int E, const void* w, const void* x, int cols, float alpha, float beta, const void* in,
-                  void* low, void* out, const int* res, float shift, int32_t* status, int sms, cudaStream_t st) {
+// Every product's parameters, with the tensor maps encoded once: X X^T and B X
+// from either copy of X, A A, and the last B X.
+struct NsProducts {
+    GgParams xx[2], aa, bx[2], last[2];
+};
+
+static bool ns_params(const NsPlan& q, const void* w, const void* x, int cols, const void* in, void* low, void* out,
+                      bool sym, GgParams* p) {
+    memset(p, 0, sizeof *p);
+    p->rows = q.m;
+    p->low = low;
+    p->out = out;
+    const uint64_t G = (uint64_t)q.group, R = G * q.m;
+    bool ok;
+    if (sym) {  // x [G m, cols] times its own rows
+        p->M = q.m;
+        p->C = cols;
+        ok = encode_map(&p->ta, w, 2, cols, q.m, G, 128);
+    } else {  // x = B [G m, m], w = X [G, m, n]
+        p->M = q.n;
+        p->C = q.m;
+        p->a_blocked = 1;
+        ok = encode_blocked(&p->ta, w, q.n, q.m, G);
+    }
+    ok = ok && encode_map(&p->tb, x, 2, p->C, R, 0, kGgBoxN) && encode_map(&p->tb_all, x, 2, p->C, R, 0, 128);
+    if (in) {
+        ok = ok && encode_input(&p->tin[0], in, p->M, R) && (!low || encode_input(&p->tin[1], low, p->M, R));
+        p->planes = low ? 2 : 1;
+    }
+    return ok;
+}
+
+template <int CG>
+static int ns_allow() {
+    int rc = allow_smem(gg_kernel<kGgFwd, CG, false, kGgSym>, kGgSmem);
+    if (!rc) rc = allow_smem(gg_kernel<kGgDx, CG, false, kGgAxpy>, kGgSmem);
+    return rc ? rc : allow_smem(gg_kernel<kGgDx, CG, false, kGgResult>, kGgSmem);
+}
+
+// One product of E matrices, on no more SMs than it has tiles.
+template <int EP, int CG>
+static int run_ns(GgParams& p, int E, float alpha, float beta, float shift, bool early, int sms, cudaStream_t st) {
     constexpr int MODE = EP == kGgSym ? kGgFwd : kGgDx;
-    GgParams p;
-    memset(&p, 0, sizeof p);
     p.E = E;
-    p.rows = q.m;
-    p.R = E * q.m;
-    p.low = low;
-    p.out = out;
+    p.R = E * p.rows;
     p.alpha = alpha;
     p.beta = beta;
     p.shift = shift;
-    p.status = status;
-    bool ok;
-    if (EP == kGgSym) {  // x [E m, cols] times its own rows
-        p.M = q.m;
-        p.C = cols;
-        ok = encode_map(&p.ta, w, 2, cols, q.m, E, 128);
-    } else {  // x = B [E m, m], w = X [E, m, n]
-        p.M = q.n;
-        p.C = q.m;
-        p.a_blocked = 1;
-        ok = encode_blocked(&p.ta, w, q.n, q.m, E);
+    p.early = early;
+    const int64_t t = ceil_div(p.rows, 128 * CG), tiles = E * (EP == kGgSym ? t * (t + 1) / 2 : t * ceil_div(p.M, 128 * CG));
+    return launch_clusters<CG>(gg_kernel<MODE, CG, false, EP>, p, GgCfg<MODE, CG, false>::kThreads + 32,
+                               tiles * CG < sms ? (int)tiles * CG : sms, st);
+}
+
+template <int CG>
+static int run_ns_steps(NsProducts& s, int E, int steps, float a, float b, float c, bool more, int sms, cudaStream_t st) {
+    const float up = (float)(1 << kNsScaleLog2), down = 1.0f / up;
+    for (int i = 0; i < steps; ++i) {
+        // a + b A + c A A of A = S + A': one + lin A' + c A' A'
+        const float S = steps - i <= kNsShifted ? kNsShift : 0.0f, lin = b + 2.0f * c * S, one = a + b * S + c * S * S;
+        int rc = run_ns<kGgSym, CG>(s.xx[i & 1], E, down * down, 0.0f, S, true, sms, st);
+        if (!rc) rc = run_ns<kGgSym, CG>(s.aa, E, c, lin, 0.0f, true, sms, st);
+        if (!rc)
+            rc = i + 1 < steps ? run_ns<kGgAxpy, CG>(s.bx[i & 1], E, 1.0f, one, 0.0f, true, sms, st)
+                               : run_ns<kGgResult, CG>(s.last[i & 1], E, down, one * down, 0.0f, more, sms, st);
+        if (rc) return rc;
     }
-    if (!ok || !encode_map(&p.tb, x, 2, p.C, p.R, 0, kGgBoxN) || !encode_map(&p.tb_all, x, 2, p.C, p.R, 0, 128))
-        return MOE_ERR_UNSUPPORTED;
-    if (in) {
-        if (!encode_input(&p.tin[0], in, p.M, p.R) || (low && !encode_input(&p.tin[1], low, p.M, p.R))) return MOE_ERR_UNSUPPORTED;
-        p.planes = low ? 2 : 1;
-    }
-    if (res) {
-        p.res_rows = res[0];
-        p.res_cols = res[1];
-        p.res_trans = res[2];
-    }
-    // pairs of CTAs where their larger tiles still give every pair work
-    const int t = ceil_div(q.m, 256);
-    const int64_t tiles = (int64_t)E * (EP == kGgSym ? t * (t + 1) / 2 : t * ceil_div(q.n, 256));
-    return tiles >= sms / 2
-               ? launch_persistent<2>(gg_kernel<MODE, 2, false, EP>, p, GgCfg<MODE, 2, false>::kThreads + 32, sms, st)
-               : launch_persistent<1>(gg_kernel<MODE, 1, false, EP>, p, GgCfg<MODE, 1, false>::kThreads + 32, sms, st);
+    return MOE_OK;
 }
 
 }  // namespace moe
@@ -405,7 +436,8 @@ int moe_combine_norm_backward(const void* dy, const void* dn, int n_dtype, const
 
 int moe_orthogonalize_workspace_bytes(int E, int N, int K, size_t* bytes) {
     NsPlan q;
-    const int rc = ns_plan(E, N, K, &q);
+    const int sms = sm_count();
+    const int rc = ns_plan(E, N, K, sms > 1 ? sms : kMaxSms, &q);
     if (rc) return rc;
     if (!bytes) return MOE_ERR_INVALID_ARG;
     *bytes = q.bytes;
@@ -415,7 +447,8 @@ int moe_orthogonalize_workspace_bytes(int E, int N, int K, size_t* bytes) {
 int moe_orthogonalize(const void* g, int g_dtype, int E, int N, int K, int steps, float a, float b, float c, float eps,
                       uint16_t* out, void* workspace, size_t workspace_bytes, int32_t* dev_status, void* stream) {
     NsPlan q;
-    int rc = ns_plan(E, N, K, &q);
+    const int sms = sm_count();
+    int rc = ns_plan(E, N, K, sms > 1 ? sms : kMaxSms, &q);
     if (rc) return rc;
     if (g_dtype != MOE_DT_F32 && g_dtype != MOE_DT_BF16) return MOE_ERR_INVALID_ARG;
     if (steps < 1 || steps > MOE_MAX_NS_STEPS || !(eps >= 0.0f && eps <= 1.0f)) return MOE_ERR_INVALID_ARG;
@@ -426,34 +459,42 @@ int moe_orthogonalize(const void* g, int g_dtype, int E, int N, int K, int steps
     MOE_OPT(dev_status);
     if (!workspace || workspace_bytes < q.bytes) return MOE_ERR_WORKSPACE;
     MOE_REQ(workspace);
-    const int sms = sm_count();
     if (sms < 2) return MOE_ERR_CUDA;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     unsigned char* ws = static_cast<unsigned char*>(workspace);
-    void* x[2] = {ws, ws + q.x};
-    void *low = ws + 2 * q.x, *A = ws + 3 * q.x, *B = ws + 3 * q.x + q.a;
+    uint16_t* x[2] = {reinterpret_cast<uint16_t*>(ws), reinterpret_cast<uint16_t*>(ws + q.x)};
+    uint16_t* low = reinterpret_cast<uint16_t*>(ws + 2 * q.x);
+    void *A = ws + 3 * q.x, *B = ws + 3 * q.x + q.a;
     float* parts = reinterpret_cast<float*>(ws + 3 * q.x + 2 * q.a);
     const int f32 = g_dtype == MOE_DT_F32, trans = N > K;
-    rc = launch_pdl(ns_norm_kernel, dim3((unsigned)q.parts, (unsigned)E), 256, 0, st, g, f32, (size_t)N * K, parts);
-    if (rc) return rc;
-    // (the blocks cover the padded X: its rows are G's columns where G is tall)
-    const int rows = trans ? q.n : q.m, cols = trans ? q.m : q.n;
-    rc = launch_pdl(ns_convert_kernel, dim3((unsigned)ceil_div(cols, 64), (unsigned)ceil_div(rows, 64), (unsigned)E), 256, 0, st,
-                    g, f32, N, K, (const float*)parts, q.parts, eps, trans, static_cast<uint16_t*>(x[0]),
-                    static_cast<uint16_t*>(low), q.m, q.n);
-    if (rc) return rc;
-    const float up = (float)(1 << kNsScaleLog2), down = 1.0f / up;
-    const int res[3] = {N, K, trans};
-    for (int s = 0; s < steps; ++s) {
-        void *from = x[s & 1], *to = x[(s & 1) ^ 1];
-        // a + b A + c A A of A = S + A': one + lin A' + c A' A'
-        const float S = steps - s <= kNsShifted ? kNsShift : 0.0f, lin = b + 2.0f * c * S, one = a + b * S + c * S * S;
-        rc = run_ns<kGgSym>(q, E, from, from, q.n, down * down, 0.0f, nullptr, nullptr, A, nullptr, S, dev_status, sms, st);
+    NsProducts s;
+    bool ok = ns_params(q, A, A, q.m, A, nullptr, B, true, &s.aa);
+    for (int i = 0; i < 2 && ok; ++i) {
+        ok = ns_params(q, x[i], x[i], q.n, nullptr, nullptr, A, true, &s.xx[i]) &&
+             ns_params(q, x[i], B, 0, x[i], low, x[i ^ 1], false, &s.bx[i]);
+        s.xx[i].status = s.bx[i].status = dev_status;
+        s.last[i] = s.bx[i];
+        s.last[i].res_rows = N;
+        s.last[i].res_cols = K;
+        s.last[i].res_trans = trans;
+    }
+    if (!ok) return MOE_ERR_UNSUPPORTED;
+    s.aa.status = dev_status;
+    if ((rc = q.pairs ? ns_allow<2>() : ns_allow<1>())) return rc;
+    const size_t each = (size_t)N * K;
+    for (int e = 0; e < E; e += q.group) {
+        const int G = E - e < q.group ? E - e : q.group;
+        const void* from = static_cast<const unsigned char*>(g) + each * e * (f32 ? 4 : 2);
+        rc = launch_pdl(ns_norm_kernel, dim3((unsigned)q.parts, (unsigned)G), 256, 0, st, from, f32, each, parts);
         if (rc) return rc;
-        rc = run_ns<kGgSym>(q, E, A, A, q.m, c, lin, A, nullptr, B, nullptr, 0.0f, dev_status, sms, st);
+        // (the blocks cover the padded X: its rows are G's columns where G is tall)
+        const int rows = trans ? q.n : q.m, cols = trans ? q.m : q.n;
+        rc = launch_pdl(ns_convert_kernel, dim3((unsigned)ceil_div(cols, 256), (unsigned)ceil_div(rows, 64), (unsigned)G), 256, 0,
+                        st, from, f32, N, K, (const float*)parts, q.parts, eps, trans, x[0], low, q.m, q.n);
         if (rc) return rc;
-        rc = s + 1 < steps ? run_ns<kGgAxpy>(q, E, from, B, 0, 1.0f, one, from, low, to, nullptr, 0.0f, dev_status, sms, st)
-                           : run_ns<kGgResult>(q, E, from, B, 0, down, one * down, from, low, out, res, 0.0f, dev_status, sms, st);
+        s.last[(steps - 1) & 1].out = out + each * e;
+        const bool more = e + G < E;
+        rc = q.pairs ? run_ns_steps<2>(s, G, steps, a, b, c, more, sms, st) : run_ns_steps<1>(s, G, steps, a, b, c, more, sms, st);
         if (rc) return rc;
     }
     return MOE_OK;

@@ -74,6 +74,7 @@ struct GgParams {
     // orthogonalisation: out = alpha product + beta in - shift 1
     float alpha, beta, shift;
     void* low;       // B X: replaced by what fp16 leaves of out
+    int early;       // the kernel behind this one touches nothing before its grid_dep_wait
     int rows;        // of every segment (offsets is then not read)
     int res_rows, res_cols, res_trans;  // the result's matrices: [E, res_rows, res_cols], transposed or not
     CUtensorMap zero[4];  // dw: boxes of 64 columns x 8, 4, 2 and 1 rows, for rows of zeros from behind x's end
@@ -862,6 +863,7 @@ __global__ void __launch_bounds__((GgCfg<MODE, CG, F32>::kThreads + 32 * GgIn<EP
         if (MODE != kGgDw) prefetch_map(&p.tb_all);
     }
     if (warp == Cfg::EPI + 1) gg_tmem_alloc<CG>(&sh->tmem_slot, kGgTmemCols);
+    if (EP >= kGgSym && p.early) grid_dep_launch();
     grid_dep_wait();
     constexpr int MW = EP == kGgGlu ? 64 : 128, BMW = MW * CG;  // outputs that a CTA's 128 rows and a tile give
     const int mtiles = (p.M + BMW - 1) / BMW;

@@ -66,11 +66,9 @@ inline int check_grouped(int R, int N, int K, int E, int dtype) {
     return MOE_OK;
 }
 
-// A persistent kernel on every SM, in clusters of CG CTAs.
+// The launch itself, of a kernel whose shared memory is allowed already.
 template <int CG, typename K, typename P>
-inline int launch_persistent(K kernel, const P& p, int threads, int sms, cudaStream_t st) {
-    const int rc = allow_smem(kernel, kGgSmem);
-    if (rc) return rc;
+inline int launch_clusters(K kernel, const P& p, int threads, int sms, cudaStream_t st) {
     cudaLaunchConfig_t cfg;
     memset(&cfg, 0, sizeof cfg);
     cfg.gridDim = dim3((unsigned)(sms / CG * CG));
@@ -87,6 +85,13 @@ inline int launch_persistent(K kernel, const P& p, int threads, int sms, cudaStr
     cfg.attrs = attr;
     cfg.numAttrs = CG > 1 ? 2 : 1;
     return launch_ex(cfg, kernel, p);
+}
+
+// A persistent kernel on `sms` SMs, in clusters of CG CTAs.
+template <int CG, typename K, typename P>
+inline int launch_persistent(K kernel, const P& p, int threads, int sms, cudaStream_t st) {
+    const int rc = allow_smem(kernel, kGgSmem);
+    return rc ? rc : launch_clusters<CG>(kernel, p, threads, sms, st);
 }
 
 // The paired tile (256 x 256) from so many rows a segment on average, where

@@ -44,6 +44,7 @@ __device__ __forceinline__ float ns_value(const void* g, bool f32, size_t i) {
 // parts [E, gridDim.x, 3].
 __global__ void __launch_bounds__(256) ns_norm_kernel(const void* g, int f32, size_t n, float* parts) {
     __shared__ float s_sum[3][8];
+    grid_dep_launch();
     grid_dep_wait();
     const size_t base = blockIdx.y * n;
     float s[3] = {0.0f, 0.0f, 0.0f};
@@ -93,15 +94,20 @@ __global__ void __launch_bounds__(256) ns_norm_kernel(const void* g, int f32, si
 }
 
 // X [E, rows, cols] = 2^8 G / (|G|_F + eps), or its transpose, in fp16, and in
-// `low` what that leaves; zeros beyond G's N x K.  A block takes 64 x 64 values of G.  A matrix with a NaN or
-// an infinity becomes NaN throughout.
+// `low` what that leaves; zeros beyond G's N x K.  A block takes 64 rows of G
+// and four times 64 columns; eight values of a row a thread, transposed
+// through shared memory where G is tall.  A matrix with a NaN or an infinity
+// becomes NaN throughout.
+constexpr int kNsPitch = 72;  // of a transposed tile in shared memory: rows of whole 16-byte pieces
+
 __global__ void __launch_bounds__(256) ns_convert_kernel(const void* g, int f32, int N, int K, const float* parts, int nparts,
                                                          float eps, int trans, uint16_t* x, uint16_t* low, int rows,
                                                          int cols) {
-    __shared__ uint16_t tile[2][64][66];
+    __shared__ __align__(16) uint16_t tile[2][64][kNsPitch];
     __shared__ float s_scale[2];
+    grid_dep_launch();
     grid_dep_wait();
-    const int e = blockIdx.z, r0 = blockIdx.y * 64, c0 = blockIdx.x * 64, tid = threadIdx.x;
+    const int e = blockIdx.z, r0 = blockIdx.y * 64, tid = threadIdx.x;
     if (tid < 32) {
         double s[3] = {0.0, 0.0, 0.0};
         for (int i = tid; i < nparts; i += 32)
@@ -122,27 +128,68 @@ __global__ void __launch_bounds__(256) ns_convert_kernel(const void* g, int f32,
     }
     __syncthreads();
     const float s0 = s_scale[0], s1 = s_scale[1];
-    for (int i = tid; i < 64 * 64; i += 256) {
-        const int r = i >> 6, c = i & 63;
-        float v = 0.0f;
-        if (r0 + r < N && c0 + c < K) v = ns_value(g, f32, ((size_t)e * N + r0 + r) * K + c0 + c) * s0 * s1;
-        const __half h = __float2half_rn(v);
-        const __half l = __float2half_rn(v - __half2float(h));
-        tile[0][r][c] = *reinterpret_cast<const uint16_t*>(&h);
-        tile[1][r][c] = *reinterpret_cast<const uint16_t*>(&l);
-    }
-    __syncthreads();
-    // rows of X: G's rows, or its columns
-    const int x0 = trans ? c0 : r0, y0 = trans ? r0 : c0;
-    for (int i = tid; i < 64 * 32; i += 256) {
-        const int r = i >> 5, c = (i & 31) * 2;
-        if (x0 + r >= rows || y0 + c >= cols) continue;
-        const size_t at = ((size_t)e * rows + x0 + r) * cols + y0 + c;
+    const bool whole = K % 8 == 0;
+    for (int c0 = blockIdx.x * 256; c0 < blockIdx.x * 256 + 256 && c0 < (trans ? rows : cols); c0 += 64) {
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-            const uint32_t a = trans ? tile[j][c][r] : tile[j][r][c], b = trans ? tile[j][c + 1][r] : tile[j][r][c + 1];
-            *reinterpret_cast<uint32_t*>((j ? low : x) + at) = a | b << 16;
+        for (int i = tid; i < 64 * 8; i += 256) {
+            const int r = r0 + (i >> 3), c = c0 + (i & 7) * 8;
+            const size_t at = ((size_t)e * N + r) * K + c;
+            float v[8];
+            if (r < N && whole && c < K) {
+                if (f32) {
+                    const uint4 a = ld_input_v4(static_cast<const float*>(g) + at);
+                    const uint4 b = ld_input_v4(static_cast<const float*>(g) + at + 4);
+                    const uint32_t u[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) v[j] = __uint_as_float(u[j]);
+                } else {
+                    const uint4 a = ld_input_v4(static_cast<const uint16_t*>(g) + at);
+                    const uint32_t u[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const float2 f = bf16x2_to_f2(u[j]);
+                        v[2 * j] = f.x;
+                        v[2 * j + 1] = f.y;
+                    }
+                }
+            } else {
+#pragma unroll
+                for (int j = 0; j < 8; ++j) v[j] = r < N && c + j < K ? ns_value(g, f32, at + j) : 0.0f;
+            }
+            uint32_t hi[4], lo[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const float a = v[2 * j] * s0 * s1, b = v[2 * j + 1] * s0 * s1;
+                hi[j] = gg_pack_f16(a, b);
+                const float2 h = f16x2_to_f2(hi[j]);
+                lo[j] = gg_pack_f16(a - h.x, b - h.y);
+            }
+            if (!trans) {
+                if (r < rows && c < cols) {  // (cols is a multiple of 64)
+                    const size_t to = ((size_t)e * rows + r) * cols + c;
+                    *reinterpret_cast<uint4*>(x + to) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+                    *reinterpret_cast<uint4*>(low + to) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+                }
+            } else {
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    tile[0][(i & 7) * 8 + j][i >> 3] = (uint16_t)(hi[j / 2] >> (j & 1) * 16);
+                    tile[1][(i & 7) * 8 + j][i >> 3] = (uint16_t)(lo[j / 2] >> (j & 1) * 16);
+                }
+            }
         }
+        if (!trans) continue;
+        __syncthreads();
+#pragma unroll
+        for (int i = tid; i < 64 * 8; i += 256) {
+            const int r = i >> 3, c = (i & 7) * 8;  // X's row c0 + r, columns r0 + c on
+            if (c0 + r < rows && r0 + c < cols) {
+                const size_t to = ((size_t)e * rows + c0 + r) * cols + r0 + c;
+                *reinterpret_cast<uint4*>(x + to) = *reinterpret_cast<const uint4*>(&tile[0][r][c]);
+                *reinterpret_cast<uint4*>(low + to) = *reinterpret_cast<const uint4*>(&tile[1][r][c]);
+            }
+        }
+        __syncthreads();
     }
 }
 

@@ -121,6 +121,11 @@ __device__ __forceinline__ void cp_async_wait_all() { asm volatile("cp.async.wai
 // kernel calls it before it reads anything an earlier kernel wrote.
 __device__ __forceinline__ void grid_dep_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
+// Lets the kernel behind this one on the stream be launched as soon as all of
+// this one's blocks have come here, to wait in grid_dep_wait for its end: only
+// where that kernel is known to touch no memory before.
+__device__ __forceinline__ void grid_dep_launch() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
 // ---------------------------------------------------------- named barriers
 // The non-aligned form: threads of one warp may reach it at different times
 // (bar.sync is the .aligned form, which requires a converged warp -- a warp
