@@ -955,22 +955,23 @@ def grouped_glu_backward(dy, down, gu, offsets, act="silu", dgu=None, h=None, st
 def _join_args(x, o, pos, w, post, scale, pre):
     """The arguments that combine_norm and its gradients share, checked
     -> (device, T, H, R, k, scale vector or None, scale number)."""
+    i, k = x.get_device(), 1
     try:
         T, H = x.shape
-        R, k = (0, 0) if o is None else (o.shape[0], 1)
-        if o is not None and o.dim() != 2:
-            raise ValueError
-        for t in (pos, w):
-            if t is not None:
-                _, k = t.shape
+        if o is not None:
+            R, _ = o.shape
+        if pos is not None:
+            _, k = pos.shape
+        elif w is not None:
+            _, k = w.shape
     except ValueError:
         raise _bad_dims(**{n: t for n, t in (("x", x), ("o", o), ("pos", pos), ("w", w)) if t is not None}) from None
-    i = x.get_device()
     if o is None:
         if pre is None:
             raise ValueError("combine_norm needs rows (o), a norm (pre), or both")
         if pos is not None or w is not None or post is not None:
             raise ValueError("pos, w and post belong to rows: o is missing")
+        R = k = 0
         scale = 1.0
     else:
         if o.dtype not in _OUT:
@@ -986,11 +987,12 @@ def _join_args(x, o, pos, w, post, scale, pre):
             _is(post, "post", torch.float32, (H,), i)
     if pre is not None:
         _is(pre, "pre", torch.float32, (H,), i)
-    vector = None
+    if type(scale) is float:
+        return i, T, H, R, k, None, scale
     if isinstance(scale, torch.Tensor):
-        vector, scale = scale, 1.0
-        _is(vector, "scale", torch.float32, (H,), i)
-    return i, T, H, R, k, vector, float(scale)
+        _is(scale, "scale", torch.float32, (H,), i)
+        return i, T, H, R, k, scale, 1.0
+    return i, T, H, R, k, None, float(scale)
 
 
 def _opt_ptr(t):
@@ -998,16 +1000,25 @@ def _opt_ptr(t):
     return None if t is None else t.data_ptr() or 16
 
 
-def _combine(handle, x, o, pos, w, T, H, R, k, post, vector, scale, pre, eps, n_dtype, y, n, st):
+def _combine(handle, x, xd, o, pos, w, T, H, R, k, post, vector, scale, pre, eps, n_dtype, y, n, st):
     if o is None:
-        y = x
-    elif y is None:
-        y = torch.empty_like(x)
+        y, op, od = x, None, xd
+    else:
+        op, od = o.data_ptr() or 16, _OUT[o.dtype]
+        if y is None:
+            y = torch.empty_like(x)
+    np, nd = None, MOE_DT_F32
     if pre is not None:
-        n = _out(n, (T, H), n_dtype, x)
-    rc = _lib.moe_combine_norm(x.data_ptr(), _OUT[x.dtype], _opt_ptr(o), _OUT[(x if o is None else o).dtype], _opt_ptr(pos),
-                               _opt_ptr(w), T, H, R, k, _opt_ptr(post), _opt_ptr(vector), scale, _opt_ptr(pre), eps,
-                               y.data_ptr(), _opt_ptr(n), MOE_DT_F32 if n is None else _OUT[n.dtype], st, handle)
+        if n is not None or n_dtype is not x.dtype:
+            n = _out(n, (T, H), n_dtype, x)
+            nd = _OUT[n.dtype]
+        else:
+            n, nd = torch.empty_like(x), xd
+        np = n.data_ptr()
+    rc = _lib.moe_combine_norm(x.data_ptr(), xd, op, od, None if pos is None else pos.data_ptr(),
+                               None if w is None else w.data_ptr(), T, H, R, k, None if post is None else post.data_ptr(),
+                               None if vector is None else vector.data_ptr(), scale,
+                               None if pre is None else pre.data_ptr(), eps, y.data_ptr(), np, nd, st, handle)
     if rc:
         raise MoeError("moe_combine_norm", rc)
     return y, n
@@ -1026,7 +1037,7 @@ def combine_norm(x, o=None, pos=None, w=None, post=None, scale=1.0, pre=None, ep
     post and pre [H] fp32; scale a number or [H] fp32.  y and n are buffers to
     be written (y may be x).  Without pre there is no n (None); without o it
     is x's norm alone, and y is x.  Detached."""
-    _x_dtype(x)
+    xd = _x_dtype(x)
     i, T, H, R, k, vector, scale = _join_args(x, o, pos, w, post, scale, pre)
     _is(x, "x", x.dtype, (T, H), i)
     if y is not None:
@@ -1035,8 +1046,8 @@ def combine_norm(x, o=None, pos=None, w=None, post=None, scale=1.0, pre=None, ep
         _is(y, "y", x.dtype, (T, H), i)
     if n is not None and pre is None:
         raise ValueError("n needs its norm's weights (pre)")
-    return _on(i, stream, _combine, x, o, pos, w, T, H, R, k, post, vector, scale, pre, eps, n_dtype, y, n,
-               _status_ptr(status, i))
+    return _on(i, stream, _combine, x, xd, o, pos, w, T, H, R, k, post, vector, scale, pre, eps, n_dtype, y, n,
+               None if status is None else _status_ptr(status, i))
 
 
 def _combine_backward(handle, dy, dn, y, o, pos, w, T, H, R, k, post, vector, scale, pre, eps, dx, do, workspace, st):

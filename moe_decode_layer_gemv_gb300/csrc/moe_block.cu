@@ -142,7 +142,7 @@ static int ns_plan(int E, int N, int K, int sms, NsPlan* q) {
     const int tri = t * (t + 1) / 2;
     q->pairs = (int64_t)E * tri >= sms / 2;
     q->group = E;
-    q->parts = ceil_div(4 * sms, q->group);
+    q->parts = ceil_div(8 * sms, q->group);
     const int most = (int)(((size_t)N * K + 2047) / 2048);
     if (q->parts > most) q->parts = most;
     if (q->parts > kNsParts) q->parts = kNsParts;
@@ -179,7 +179,8 @@ static bool ns_params(const NsPlan& q, const void* w, const void* x, int cols, c
     }
     ok = ok && encode_map(&p->tb, x, 2, p->C, R, 0, kGgBoxN) && encode_map(&p->tb_all, x, 2, p->C, R, 0, 128);
     if (in) {
-        ok = ok && encode_input(&p->tin[0], in, p->M, R) && (!low || encode_input(&p->tin[1], low, p->M, R));
+        constexpr int rows = GgIn<kGgSym>::kRows;  // (the other products' as well)
+        ok = ok && encode_input(&p->tin[0], in, p->M, R, rows) && (!low || encode_input(&p->tin[1], low, p->M, R, rows));
         p->planes = low ? 2 : 1;
     }
     return ok;
@@ -203,7 +204,7 @@ static int run_ns(GgParams& p, int E, float alpha, float beta, float shift, bool
     p.shift = shift;
     p.early = early;
     const int64_t t = ceil_div(p.rows, 128 * CG), tiles = E * (EP == kGgSym ? t * (t + 1) / 2 : t * ceil_div(p.M, 128 * CG));
-    return launch_clusters<CG>(gg_kernel<MODE, CG, false, EP>, p, GgCfg<MODE, CG, false>::kThreads + 32,
+    return launch_clusters<CG>(gg_kernel<MODE, CG, false, EP>, p, GgRole<MODE, CG, false, EP>::kThreads,
                                tiles * CG < sms ? (int)tiles * CG : sms, st);
 }
 
@@ -288,7 +289,7 @@ int moe_grouped_glu_backward(const uint16_t* dy, const uint16_t* down, const uin
     p.a_blocked = I % 64 == 0;
     if (!(p.a_blocked ? encode_blocked(&p.ta, down, I, H, E) : encode_map(&p.ta, down, 2, I, H, E, 64)) ||
         !encode_map(&p.tb, dy, 2, H, R, 0, kGgBoxN) || !encode_map(&p.tb_all, dy, 2, H, R, 0, 128) ||
-        !encode_input(&p.tin[0], gu, 2 * I, R))
+        !encode_input(&p.tin[0], gu, 2 * I, R, GgIn<kGgGluBack>::kRows))
         return MOE_ERR_UNSUPPORTED;
     p.tin[1] = p.tin[0];
     p.planes = 2;
@@ -302,8 +303,8 @@ int moe_grouped_glu_backward(const uint16_t* dy, const uint16_t* down, const uin
     p.out2 = h;
     p.status = dev_status;
     return gg_pairs(R, I, E)
-               ? launch_persistent<2>(gg_kernel<kGgDx, 2, false, kGgGluBack>, p, GgCfg<kGgDx, 2, false>::kThreads + 32, sms, st)
-               : launch_persistent<1>(gg_kernel<kGgDx, 1, false, kGgGluBack>, p, GgCfg<kGgDx, 1, false>::kThreads + 32, sms, st);
+               ? launch_persistent<2>(gg_kernel<kGgDx, 2, false, kGgGluBack>, p, GgRole<kGgDx, 2, false, kGgGluBack>::kThreads, sms, st)
+               : launch_persistent<1>(gg_kernel<kGgDx, 1, false, kGgGluBack>, p, GgRole<kGgDx, 1, false, kGgGluBack>::kThreads, sms, st);
 }
 
 int moe_combine_norm(const void* x, int x_dtype, const void* o, int o_dtype, const int32_t* pos, const float* w, int T, int H,

@@ -67,7 +67,7 @@ struct GgParams {
     // gated units
     void* out2;      // forward: gu [R, 2 M] bf16, or nullptr; backward: h [R, M] bf16
     float c0, c1;    // the activation's coefficients
-    // inputs of the epilogue, maps of 16 rows x 128 columns of [R, ..] (kGgGluBack: g and u, of one tensor;
+    // inputs of the epilogue, maps of GgIn's rows x 128 columns of [R, ..] (kGgGluBack: g and u, of one tensor;
     // orthogonalisation: in and what fp16 left of it), how many, the columns at which their m = 0 lies
     CUtensorMap tin[2];
     int planes, tin_at[2];
@@ -103,7 +103,7 @@ struct GgCfg {
 };
 
 // The epilogues that read inputs (kGgGluBack and later ones) get them by
-// copies, 16 rows of both planes for each half of the columns at a time, so
+// copies, a few rows of both planes for each part of the columns at a time, so
 // many of them ahead.  (Loads into registers ahead of their use, beside 128
 // registers of sums, were spilled as they arrived: 683 us for the training
 // batch's backward pass.)  They read their tile out of tensor memory as they
@@ -111,19 +111,36 @@ struct GgCfg {
 // little code.  Its truncated additions (kGgPartSteps) cost a sum of one sign
 // up to 7.4e-5 of 16384 terms, 2 % of half a step of the bf16 or a third of
 // one of the fp16 results.
-constexpr int kGgInRows = 16, kGgInSlots = 3;
-constexpr int kGgInPlane = kGgInRows * 256;                // bytes
-constexpr int kGgInBytes = 2 * kGgInSlots * 2 * kGgInPlane;  // halves x slots x planes
+constexpr int kGgInMax = 4;  // parts of the columns, and slots each, at most
 
+// The inputs' geometry: parts of a tile's columns (with four epilogue warps
+// each), rows a slot, slots a part.  What they take is lost to the ring of the
+// operands: the gated unit's gradient of 65536 rows takes 205 us with 24 KB of
+// them, 188 with 32 and 48, 205 with 64, 225 with 96; eight or sixteen
+// epilogue warps make no difference there, as it waits for L2 by then.
 template <int EP>
 struct GgIn {
     static constexpr bool kOn = EP >= kGgGluBack;
-    static constexpr int kBytes = kOn ? kGgInBytes : 0, kWarps = kOn ? 1 : 0;
-    static constexpr int kPart = kOn ? 1 << 30 : kGgPartSteps;  // steps an accumulator takes
+    static constexpr int kParts = EP == kGgGluBack ? 2 : 4, kRows = 16, kSlots = EP == kGgGluBack ? 3 : 2;
+    static constexpr int kPlane = kRows * 256;  // bytes
+    static constexpr int kBytes = kOn ? kParts * kSlots * 2 * kPlane : 0;
+};
+
+// Roles and limits by epilogue, over GgCfg's.
+template <int MODE, int CG, bool F32, int EP>
+struct GgRole {
+    static constexpr bool kIn = GgIn<EP>::kOn;
+    static constexpr int kInBytes = GgIn<EP>::kBytes;
+    static constexpr int EPI = kIn ? 4 * GgIn<EP>::kParts : GgCfg<MODE, CG, F32>::EPI;  // epilogue warps
+    static constexpr int COLS = 128 * CG / (EPI / 4);
+    static constexpr int kThreads = kIn ? 32 * (EPI + 3) : GgCfg<MODE, CG, F32>::kThreads;
+    static constexpr int kPart = kIn ? 1 << 30 : kGgPartSteps;  // steps an accumulator takes
+    // (beside the inputs two steps a stage would leave room for two stages)
+    static constexpr int KSUB = kIn ? 1 : GgCfg<MODE, CG, F32>::KSUB;
 };
 
 struct GgShared {
-    uint64_t in_full[2][kGgInSlots], in_empty[2][kGgInSlots];
+    uint64_t in_full[kGgInMax][kGgInMax], in_empty[kGgInMax][kGgInMax];
     uint64_t full[kGgMaxStages];    // leader: a stage's tiles landed (in both CTAs)
     uint64_t tfull[kGgMaxStages];   // dw: the stage that a segment ends in landed in this CTA ...
     uint64_t clear[kGgMaxStages];   // ... leader: and its rows behind the segment are zero (in both CTAs)
@@ -645,12 +662,13 @@ __device__ __forceinline__ void glu_store(const P& p, uint32_t (&sum)[COLS / 32]
     }
 }
 
-// A place in the ring of a half's epilogue inputs.
+// A place in the ring of a part's epilogue inputs.
+template <int SLOTS>
 struct GgInRing {
     uint32_t s = 0, ph = 0, uses = 0;
     __device__ __forceinline__ void next() {
         ++uses;
-        if (++s == kGgInSlots) {
+        if (++s == SLOTS) {
             s = 0;
             ph ^= 1u;
         }
@@ -679,19 +697,19 @@ __device__ __forceinline__ void gg_put(uint16_t* to, uint32_t packed, uint32_t s
     if (there) *reinterpret_cast<uint32_t*>(to) = v;
 }
 
-// The gated unit's gradient of 16 rows of a dx tile (dh, d), this lane's m:
+// The gated unit's gradient of ROWS rows of a dx tile (dh, d), this lane's m:
 //   dg = dh u act'(g),  du = dh act(g),  h = act(g) u
 // row: the first of them; n: how many are there; ins: the inputs at m = 0 of this warp's 32.
-template <typename P>
+template <int ROWS, typename P>
 __device__ __forceinline__ void glu_back_rows(const P& p, const float* d, const uint16_t* ins, size_t row, int n, int m,
                                               int lane) {
     const int I = p.M, odd = lane & 1;
     const int last = m < I ? n - odd : 0;  // rows row + odd + j, j < last
-    const uint16_t *g = ins + (lane - odd) + odd * 128, *u = g + kGgInPlane / 2;
+    const uint16_t *g = ins + (lane - odd) + odd * 128, *u = g + ROWS * 128;
     uint16_t* dg = static_cast<uint16_t*>(p.out) + (row + odd) * 2 * (size_t)I + (m - odd);
     uint16_t* hp = static_cast<uint16_t*>(p.out2) + (row + odd) * (size_t)I + (m - odd);
 #pragma unroll
-    for (int j = 0; j < 16; j += 2, dg += 4 * (size_t)I, hp += 2 * (size_t)I) {
+    for (int j = 0; j < ROWS; j += 2, dg += 4 * (size_t)I, hp += 2 * (size_t)I) {
         const float2 dh = gg_swap(d[j], d[j + 1], odd), gf = bf16x2_to_f2(in_pair(g, j)), uf = bf16x2_to_f2(in_pair(u, j));
         float e0, e1;
         const float a0 = glu_act(gf.x, p.c0, p.c1, e0), a1 = glu_act(gf.y, p.c0, p.c1, e1);
@@ -712,18 +730,18 @@ __device__ __forceinline__ uint32_t gg_pack_f16(float first, float second) {
 
 __device__ __forceinline__ float2 f16x2_to_f2(uint32_t u) { return __half22float2(*reinterpret_cast<const __half2*>(&u)); }
 
-// out = alpha product + beta in for 16 rows of this lane's m, from row r of
+// out = alpha product + beta in for ROWS rows of this lane's m, from row r of
 // segment e on, n of them there; in and out in two fp16 values each.
-template <typename P>
+template <int ROWS, typename P>
 __device__ __forceinline__ void ns_axpy_rows(const P& p, const float* d, const uint16_t* ins, int e, int r, int n, int m,
                                              int lane) {
     const int M = p.M, odd = lane & 1;
     const int last = m < M ? n - odd : 0;  // rows r + odd + j, j < last
-    const uint16_t *in = ins + (lane - odd) + odd * 128, *lo = in + kGgInPlane / 2;
+    const uint16_t *in = ins + (lane - odd) + odd * 128, *lo = in + ROWS * 128;
     const size_t pair = ((size_t)e * p.rows + r + odd) * M + (m - odd);
     uint16_t *to = static_cast<uint16_t*>(p.out) + pair, *tl = static_cast<uint16_t*>(p.low) + pair;
 #pragma unroll
-    for (int j = 0; j < 16; j += 2, to += 2 * (size_t)M, tl += 2 * (size_t)M) {
+    for (int j = 0; j < ROWS; j += 2, to += 2 * (size_t)M, tl += 2 * (size_t)M) {
         const float2 v = gg_swap(d[j], d[j + 1], odd), f = f16x2_to_f2(in_pair(in, j)), l = f16x2_to_f2(in_pair(lo, j));
         const float v0 = fmaf(p.beta, f.x + l.x, p.alpha * v.x), v1 = fmaf(p.beta, f.y + l.y, p.alpha * v.y);
         const uint32_t w = gg_pack_f16(v0, v1);
@@ -739,8 +757,8 @@ __device__ __forceinline__ void ns_axpy_rows(const P& p, const float* d, const u
 // The same without the low parts of a symmetric product, less shift on the
 // diagonal, into rows of p.M fp16 values (a multiple of 16, as are the rows);
 // of a tile below the diagonal also into its mirror image, where a lane's
-// values lie side by side: 32 bytes, a whole sector.
-template <typename P>
+// values lie side by side.
+template <int ROWS, typename P>
 __device__ __forceinline__ void ns_sym_rows(const P& p, const float* d, const uint16_t* ins, int e, int r, int m, int lane,
                                             bool mirror) {
     const int M = p.M, odd = lane & 1;
@@ -748,9 +766,9 @@ __device__ __forceinline__ void ns_sym_rows(const P& p, const float* d, const ui
     const bool there = m < M;
     uint16_t* out = static_cast<uint16_t*>(p.out);
     uint16_t* to = out + ((size_t)e * p.rows + r + odd) * M + (m - odd);
-    uint32_t w[8];  // rows j and j + 1 of this lane's m
+    uint32_t w[ROWS / 2];  // rows j and j + 1 of this lane's m
 #pragma unroll
-    for (int j = 0; j < 16; j += 2, to += 2 * (size_t)M) {
+    for (int j = 0; j < ROWS; j += 2, to += 2 * (size_t)M) {
         float v0 = p.alpha * d[j], v1 = p.alpha * d[j + 1];
         if (p.planes) {
             v0 = fmaf(p.beta, in_f16(ins + lane, j), v0);
@@ -764,24 +782,23 @@ __device__ __forceinline__ void ns_sym_rows(const P& p, const float* d, const ui
         gg_put(to, w[j / 2], sel, there);
     }
     if (mirror && there) {
-        uint16_t* at = out + ((size_t)e * p.rows + m) * M + r;
-        asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(at), "r"(w[0]), "r"(w[1]), "r"(w[2]),
-                     "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
-                     : "memory");
+        uint4* at = reinterpret_cast<uint4*>(out + ((size_t)e * p.rows + m) * M + r);
+#pragma unroll
+        for (int j = 0; j < ROWS / 8; ++j) at[j] = make_uint4(w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]);
     }
 }
 
 // The last product: bf16 into matrices of any size, as they are or transposed.
-template <typename P>
+template <int ROWS, typename P>
 __device__ __forceinline__ void ns_result_rows(const P& p, const float* d, const uint16_t* ins, int e, int r, int n, int m,
                                                int lane) {
     const int odd = lane & 1;
     const uint32_t sel = gg_pair_select(odd);
-    const uint16_t *in = ins + lane, *lo = in + kGgInPlane / 2;
+    const uint16_t *in = ins + lane, *lo = in + ROWS * 128;
     uint16_t* out = static_cast<uint16_t*>(p.out);
-    uint32_t w[8];  // rows j and j + 1 of this lane's m
+    uint32_t w[ROWS / 2];  // rows j and j + 1 of this lane's m
 #pragma unroll
-    for (int j = 0; j < 16; j += 2) {
+    for (int j = 0; j < ROWS; j += 2) {
         const float v0 = fmaf(p.beta, in_f16(in, j) + in_f16(lo, j), p.alpha * d[j]);
         const float v1 = fmaf(p.beta, in_f16(in, j + 1) + in_f16(lo, j + 1), p.alpha * d[j + 1]);
         w[j / 2] = gg_pack(__float_as_uint(v0), __float_as_uint(v1));
@@ -791,7 +808,7 @@ __device__ __forceinline__ void ns_result_rows(const P& p, const float* d, const
         uint16_t* to = out + ((size_t)e * p.res_rows + m) * p.res_cols + r;
         const int k = min(n, p.res_cols - r);
 #pragma unroll
-        for (int j = 0; j < 16; j += 8) {
+        for (int j = 0; j < ROWS; j += 8) {
             if (j + 8 <= k && p.res_cols % 8 == 0) {
                 *reinterpret_cast<uint4*>(to + j) = make_uint4(w[j / 2], w[j / 2 + 1], w[j / 2 + 2], w[j / 2 + 3]);
             } else {
@@ -805,7 +822,7 @@ __device__ __forceinline__ void ns_result_rows(const P& p, const float* d, const
         uint16_t* to = out + ((size_t)e * p.res_rows + r) * p.res_cols + m;
         const bool even = p.res_cols % 2 == 0;
 #pragma unroll
-        for (int j = 0; j < 16; j += 2, to += 2 * (size_t)p.res_cols) {
+        for (int j = 0; j < ROWS; j += 2, to += 2 * (size_t)p.res_cols) {
             const uint32_t v = gg_pair(w[j / 2], sel);
             if (m >= p.res_cols) continue;
             if (even) {
@@ -824,26 +841,25 @@ __device__ __forceinline__ void ns_result_rows(const P& p, const float* d, const
 // pace: the producer fills the ring, the MMA issuer accumulates tile d into
 // tensor-memory buffer d mod 2, the epilogue warps read the other buffer out.
 template <int MODE, int CG, bool F32, int EP = kGgStore>
-__global__ void __launch_bounds__((GgCfg<MODE, CG, F32>::kThreads + 32 * GgIn<EP>::kWarps), 1) gg_kernel(const __grid_constant__ GgParams p) {
+__global__ void __launch_bounds__((GgRole<MODE, CG, F32, EP>::kThreads), 1) gg_kernel(const __grid_constant__ GgParams p) {
     using Cfg = GgCfg<MODE, CG, F32>;
     extern __shared__ __align__(1024) unsigned char gg_smem_raw[];
     unsigned char* base = reinterpret_cast<unsigned char*>(
         (reinterpret_cast<uintptr_t>(gg_smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
     GgShared* sh = reinterpret_cast<GgShared*>(base);
+    using Role = GgRole<MODE, CG, F32, EP>;
     using In = GgIn<EP>;
-    // (beside the inputs two steps a stage would leave room for two stages)
-    constexpr int KSUB = In::kOn ? 1 : Cfg::KSUB;
     unsigned char* ins = base + 4096;
-    unsigned char* ring = ins + In::kBytes;
+    unsigned char* ring = ins + Role::kInBytes;
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t rank = CG == 2 ? cluster_rank() : 0u;
     const int unit = (int)blockIdx.x / CG, units = (int)gridDim.x / CG;
 
     if (threadIdx.x == 0) {
-        for (int s = 0; In::kOn && s < 2 * kGgInSlots; ++s) {
-            mbar_init(&sh->in_full[s & 1][s >> 1], 1);
-            mbar_init(&sh->in_empty[s & 1][s >> 1], 4);
+        for (int s = 0; Role::kIn && s < kGgInMax * kGgInMax; ++s) {
+            mbar_init(&sh->in_full[0][s], 1);
+            mbar_init(&sh->in_empty[0][s], 4);
         }
         for (int s = 0; s < kGgMaxStages; ++s) {
             mbar_init(&sh->full[s], 1);
@@ -853,7 +869,7 @@ __global__ void __launch_bounds__((GgCfg<MODE, CG, F32>::kThreads + 32 * GgIn<EP
         }
         for (int a = 0; a < 2; ++a) {
             mbar_init(&sh->acc_full[a], 1);
-            mbar_init(&sh->acc_empty[a], Cfg::EPI * CG);
+            mbar_init(&sh->acc_empty[a], Role::EPI * CG);
         }
         mbar_init(&sh->mma_done, 1);
         sh->abort = 0;
@@ -862,9 +878,9 @@ __global__ void __launch_bounds__((GgCfg<MODE, CG, F32>::kThreads + 32 * GgIn<EP
         prefetch_map(&p.tb);
         if (MODE != kGgDw) prefetch_map(&p.tb_all);
     }
-    if (warp == Cfg::EPI + 1) gg_tmem_alloc<CG>(&sh->tmem_slot, kGgTmemCols);
+    if (warp == Role::EPI + 1) gg_tmem_alloc<CG>(&sh->tmem_slot, kGgTmemCols);
     if (EP >= kGgSym && p.early) grid_dep_launch();
-    grid_dep_wait();
+    if (EP < kGgSym) grid_dep_wait();
     constexpr int MW = EP == kGgGlu ? 64 : 128, BMW = MW * CG;  // outputs that a CTA's 128 rows and a tile give
     const int mtiles = (p.M + BMW - 1) / BMW;
     gg_segments(sh, p.offsets, EP >= kGgSym ? p.rows : 0, p.E, p.R, Cfg::BN, p.status);
@@ -873,16 +889,17 @@ __global__ void __launch_bounds__((GgCfg<MODE, CG, F32>::kThreads + 32 * GgIn<EP
     if (CG == 2) cluster_sync();
     tc_fence_after();
     const uint32_t tmem = sh->tmem_slot;
+    if (EP >= kGgSym) grid_dep_wait();  // (the segments came from no memory)
 
-    // Ring geometry.  A stage holds KSUB A tiles and KSUB B tiles; where the
+    // Ring geometry.  A stage holds Role::KSUB A tiles and Role::KSUB B tiles; where the
     // B operand is the segment's rows, its tiles are as high as the largest
     // segment needs, so that few rows leave more bytes of weights in flight.
     uint32_t b_tile = kGgTile;
     if (MODE != kGgDw && CG == 1)
         b_tile = (uint32_t)min(Cfg::BN, max(kGgBoxN, (sh->nmax + kGgBoxN - 1) / kGgBoxN * kGgBoxN)) * 128u;
-    const uint32_t stage_bytes = KSUB * (kGgTile + b_tile);
-    const uint32_t b_off = KSUB * kGgTile;
-    const uint32_t S = min((uint32_t)kGgMaxStages, ((uint32_t)kGgSmem - 1023u - 4096u - In::kBytes) / stage_bytes);
+    const uint32_t stage_bytes = Role::KSUB * (kGgTile + b_tile);
+    const uint32_t b_off = Role::KSUB * kGgTile;
+    const uint32_t S = min((uint32_t)kGgMaxStages, ((uint32_t)kGgSmem - 1023u - 4096u - Role::kInBytes) / stage_bytes);
 
     const int ntiles_w = (p.NW + Cfg::BN - 1) / Cfg::BN;  // dw
     const int tri = EP == kGgSym ? mtiles * (mtiles + 1) / 2 : 0;  // tiles on and below the diagonal
@@ -929,7 +946,7 @@ __global__ void __launch_bounds__((GgCfg<MODE, CG, F32>::kThreads + 32 * GgIn<EP
             if (!f(e, q0, n, n0, m0, len)) break;
         }
     };
-    if (warp == Cfg::EPI) {
+    if (warp == Role::EPI) {
         // ---------------- TMA producer
         GgRing r;
         const uint32_t ring_at = smem_u32(ring);
@@ -941,10 +958,10 @@ __global__ void __launch_bounds__((GgCfg<MODE, CG, F32>::kThreads + 32 * GgIn<EP
                 const int rows = MODE == kGgDw ? 128 : (n + kGgBoxN * CG - 1) / (kGgBoxN * CG) * kGgBoxN;
                 const uint32_t bytes = CG * (kGgTile + (uint32_t)rows * 128u);
                 const int am = m0 + (int)rank * MW, bn = (MODE == kGgDw ? n0 : q0) + (int)rank * rows;
-                for (int k0 = 0; k0 < nk; k0 += KSUB) {
+                for (int k0 = 0; k0 < nk; k0 += Role::KSUB) {
                     if (!gg_wait(&sh->empty[r.s], r.ph ^ 1u, &sh->abort)) return false;
                     const uint32_t st = ring_at + r.s * stage_bytes, bar = bars + r.s * 8u;
-                    const int ke = min(KSUB, nk - k0);
+                    const int ke = min(Role::KSUB, nk - k0);
                     // dw: the stage that a segment ends in, if not with a whole MMA, lands on
                     // each CTA's own barrier and is cleared there before it counts as full
                     const bool tail = MODE == kGgDw && gg_ragged(len - k0 * 64);
@@ -957,7 +974,7 @@ __global__ void __launch_bounds__((GgCfg<MODE, CG, F32>::kThreads + 32 * GgIn<EP
                             mbar_arrive_expect_tx(&sh->full[r.s], (uint32_t)ke * bytes);
                     }
 #pragma unroll
-                    for (int u = 0; u < KSUB; ++u) {
+                    for (int u = 0; u < Role::KSUB; ++u) {
                         if (u >= ke) break;
                         const uint32_t sa = st + u * kGgTile, sb = st + b_off + u * b_tile;
                         const int c = (k0 + u) * 64;
@@ -993,7 +1010,7 @@ __global__ void __launch_bounds__((GgCfg<MODE, CG, F32>::kThreads + 32 * GgIn<EP
             gg_drain<CG>(sh, S, r, rank);
         }
         __syncwarp();
-    } else if (warp == Cfg::EPI + 1) {
+    } else if (warp == Role::EPI + 1) {
         // ---------------- MMA issuer (one thread of the leader)
         GgRing r;
         int buf = 0;
@@ -1007,12 +1024,12 @@ __global__ void __launch_bounds__((GgCfg<MODE, CG, F32>::kThreads + 32 * GgIn<EP
                                    (MODE == kGgDw ? 1u << 16 : 0u);
             uint32_t acc = 0, tacc = 0;
             int room = 0;  // steps that the accumulator still takes
-            for (int k0 = 0; k0 < nk; k0 += KSUB) {
+            for (int k0 = 0; k0 < nk; k0 += Role::KSUB) {
                 if (room == 0) {
                     if (!gg_wait(&sh->acc_empty[buf], free_ph, &sh->abort)) return false;
                     tacc = tmem + (uint32_t)(buf * Cfg::BN);
                     acc = 0;
-                    room = In::kPart;
+                    room = Role::kPart;
                 }
                 if (!gg_wait(&sh->full[r.s], r.ph, &sh->abort)) return false;
                 const uint32_t sta = ring_at + r.s * stage_bytes;
@@ -1025,12 +1042,12 @@ __global__ void __launch_bounds__((GgCfg<MODE, CG, F32>::kThreads + 32 * GgIn<EP
                         tails ^= 1u << r.s;
                     }
                 }
-                room -= KSUB;  // (a whole number of stages)
-                const bool last = room == 0 || k0 + KSUB >= nk;
+                room -= Role::KSUB;  // (a whole number of stages)
+                const bool last = room == 0 || k0 + Role::KSUB >= nk;
                 tc_fence_after();
-                const int ke = min(KSUB, nk - k0);
+                const int ke = min(Role::KSUB, nk - k0);
 #pragma unroll
-                for (int u = 0; u < KSUB; ++u) {
+                for (int u = 0; u < Role::KSUB; ++u) {
                     if (u >= ke) break;
                     // the 16-deep steps of a tile: 32 bytes of a K-major row, 16 rows of an MN-major tile
                     const uint32_t aa = sta + u * kGgTile, ba = sta + b_off + u * b_tile;
@@ -1062,33 +1079,35 @@ __global__ void __launch_bounds__((GgCfg<MODE, CG, F32>::kThreads + 32 * GgIn<EP
             gg_settle(&sh->mma_done, 0u);
         }
         __syncwarp();
-    } else if (In::kOn && warp == Cfg::EPI + 2) {
+    } else if (Role::kIn && warp == Role::EPI + 2) {
         // ---------------- inputs of the epilogue
-        GgInRing r[2];
+        GgInRing<In::kSlots> r[In::kParts];
         if (p.planes && gg_elect()) {
             walk([&](int e, int q0, int n, int n0, int m0, int len) -> bool {
                 const int m = m0 + (int)rank * MW;
-                for (int c = 0; c < Cfg::COLS; c += kGgInRows)
+                for (int c = 0; c < Role::COLS; c += In::kRows)
 #pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        if (h * Cfg::COLS + c >= n) continue;
+                    for (int h = 0; h < In::kParts; ++h) {
+                        const int row = h * Role::COLS + c;
+                        if (row >= n) break;
                         if (!gg_wait(&sh->in_empty[h][r[h].s], r[h].ph ^ 1u, &sh->abort)) return false;
                         uint64_t* bar = &sh->in_full[h][r[h].s];
-                        const uint32_t to = smem_u32(ins) + (h * kGgInSlots + r[h].s) * 2 * kGgInPlane;
-                        mbar_arrive_expect_tx(bar, p.planes * kGgInPlane);
+                        const uint32_t to = smem_u32(ins) + (h * In::kSlots + r[h].s) * 2 * In::kPlane;
+                        mbar_arrive_expect_tx(bar, p.planes * In::kPlane);
                         for (int i = 0; i < p.planes; ++i)
-                            gg_load2<1>(to + i * kGgInPlane, &p.tin[i], p.tin_at[i] + m, q0 + h * Cfg::COLS + c, smem_u32(bar));
+                            gg_load2<1>(to + i * In::kPlane, &p.tin[i], p.tin_at[i] + m, q0 + row, smem_u32(bar));
                         r[h].next();
                     }
                 return true;
             });
             // no copy may be on its way when the CTA exits
-            for (int h = 0; h < 2; ++h)
-                for (uint32_t s = 0; s < kGgInSlots && s < r[h].uses; ++s)
+#pragma unroll
+            for (int h = 0; h < In::kParts; ++h)
+                for (uint32_t s = 0; s < In::kSlots && s < r[h].uses; ++s)
                     gg_settle(&sh->in_full[h][s], s < r[h].s ? r[h].ph : r[h].ph ^ 1u);
         }
         __syncwarp();
-    } else if (MODE == kGgDw && warp == Cfg::EPI + 2) {
+    } else if (MODE == kGgDw && warp == Role::EPI + 2) {
         // ---------------- dw: the segment's end.  Rows behind it belong to
         // the next segment (or to no one), so both operands' rows up to the
         // last MMA's end are zeroed -- zeroing one would leave 0 x infinity or
@@ -1131,12 +1150,12 @@ __global__ void __launch_bounds__((GgCfg<MODE, CG, F32>::kThreads + 32 * GgIn<EP
     } else {
         int buf = 0;
         uint32_t full_ph = 0;
-        const int c0 = (warp >> 2) * Cfg::COLS;
-        GgInRing in;
+        const int c0 = (warp >> 2) * Role::COLS;
+        GgInRing<In::kSlots> in;
         walk([&](int e, int q0, int n, int n0, int m0, int len) -> bool {
             const int nk = (len + 63) / 64;
             const int m = m0 + (int)rank * 128 + (warp & 3) * 32 + lane;
-            const int mine = min(Cfg::COLS, n - c0);  // columns of this warp; none below 1
+            const int mine = min(Role::COLS, n - c0);  // columns of this warp; none below 1
             const size_t row0 = (MODE == kGgDw ? (size_t)e * p.NW + n0 : (size_t)q0) + c0;
             if (MODE == kGgDw && nk == 0) {  // no rows: zeros
                 uint32_t z[32];
@@ -1145,34 +1164,35 @@ __global__ void __launch_bounds__((GgCfg<MODE, CG, F32>::kThreads + 32 * GgIn<EP
                 for (int c = 0; c < mine; c += 32) gg_store32(z, p.out, F32, row0 + c, min(32, mine - c), m, p.M);
                 return true;
             }
-            if constexpr (In::kOn) {
+            if constexpr (Role::kIn) {
                 const uint32_t taddr = tmem + (uint32_t)(buf * Cfg::BN + c0) + ((uint32_t)((warp & 3) * 32) << 16);
                 const int h = warp >> 2;
                 if (!gg_wait_warp(&sh->acc_full[buf], full_ph, &sh->abort)) return false;
                 tc_fence_after();
-                for (int c = 0; c < mine; c += 2 * kGgInRows) {
-                    uint32_t r[32];
-                    float d[32];
-                    gg_ld32(taddr + c, r);
-                    gg_ld_wait(r);
+                for (int c = 0; c < mine; c += 16) {
+                    float d[16];
+                    tmem_ld16(taddr + c, d);
+                    auto wait = [&]() -> bool { return !p.planes || gg_wait_warp(&sh->in_full[h][in.s], in.ph, &sh->abort); };
+                    auto at = [&]() {
+                        return reinterpret_cast<const uint16_t*>(ins + (h * In::kSlots + in.s) * 2 * In::kPlane) + (warp & 3) * 32;
+                    };
+                    auto done = [&]() {
+                        if (!p.planes) return;
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(&sh->in_empty[h][in.s]);
+                        in.next();
+                    };
+                    const int r0 = n0 + c0 + c;
 #pragma unroll
-                    for (int j = 0; j < 32; ++j) d[j] = __uint_as_float(r[j]);
-#pragma unroll
-                    for (int i = 0; i < 2 * kGgInRows; i += kGgInRows) {
+                    for (int i = 0; i < 16; i += In::kRows) {
                         if (c + i >= mine) break;
-                        const uint16_t* at =
-                            reinterpret_cast<const uint16_t*>(ins + (h * kGgInSlots + in.s) * 2 * kGgInPlane) + (warp & 3) * 32;
-                        if (p.planes && !gg_wait_warp(&sh->in_full[h][in.s], in.ph, &sh->abort)) return false;
-                        const int rows = min(kGgInRows, mine - c - i), r0 = n0 + c0 + c + i;
-                        if constexpr (EP == kGgGluBack) glu_back_rows(p, d + i, at, row0 + c + i, rows, m, lane);
-                        if constexpr (EP == kGgSym) ns_sym_rows(p, d + i, at, e, r0, m, lane, n0 > m0);
-                        if constexpr (EP == kGgAxpy) ns_axpy_rows(p, d + i, at, e, r0, rows, m, lane);
-                        if constexpr (EP == kGgResult) ns_result_rows(p, d + i, at, e, r0, rows, m, lane);
-                        if (p.planes) {
-                            __syncwarp();
-                            if (lane == 0) mbar_arrive(&sh->in_empty[h][in.s]);
-                            in.next();
-                        }
+                        if (!wait()) return false;
+                        const int rows = min(In::kRows, mine - c - i);
+                        if constexpr (EP == kGgGluBack) glu_back_rows<In::kRows>(p, d + i, at(), row0 + c + i, rows, m, lane);
+                        if constexpr (EP == kGgSym) ns_sym_rows<In::kRows>(p, d + i, at(), e, r0 + i, m, lane, n0 > m0);
+                        if constexpr (EP == kGgAxpy) ns_axpy_rows<In::kRows>(p, d + i, at(), e, r0 + i, rows, m, lane);
+                        if constexpr (EP == kGgResult) ns_result_rows<In::kRows>(p, d + i, at(), e, r0 + i, rows, m, lane);
+                        done();
                     }
                 }
                 tc_fence_before();
@@ -1187,12 +1207,12 @@ __global__ void __launch_bounds__((GgCfg<MODE, CG, F32>::kThreads + 32 * GgIn<EP
                 if (buf == 0) full_ph ^= 1u;
                 return true;
             }
-            uint32_t sum[Cfg::COLS / 32][32];  // the parts' sum
+            uint32_t sum[Role::COLS / 32][32];  // the parts' sum
             for (int k = 0; k < nk; k += kGgPartSteps) {
                 if (!gg_wait_warp(&sh->acc_full[buf], full_ph, &sh->abort)) return false;
                 tc_fence_after();
                 const uint32_t taddr = tmem + (uint32_t)(buf * Cfg::BN + c0) + ((uint32_t)((warp & 3) * 32) << 16);
-                if (mine > 0) gg_gather<Cfg::COLS>(taddr, sum, mine, k == 0);
+                if (mine > 0) gg_gather<Role::COLS>(taddr, sum, mine, k == 0);
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) {
@@ -1205,11 +1225,11 @@ __global__ void __launch_bounds__((GgCfg<MODE, CG, F32>::kThreads + 32 * GgIn<EP
                 if (buf == 0) full_ph ^= 1u;
             }
             if constexpr (EP == kGgGlu) {
-                glu_store<Cfg::COLS, F32>(p, sum, row0, mine, m0 + (int)rank * MW + (warp & 3) * 16, lane);
+                glu_store<Role::COLS, F32>(p, sum, row0, mine, m0 + (int)rank * MW + (warp & 3) * 16, lane);
                 return true;
             }
 #pragma unroll
-            for (int i = 0; i < Cfg::COLS / 32; ++i)
+            for (int i = 0; i < Role::COLS / 32; ++i)
                 if (32 * i < mine) gg_store32(sum[i], p.out, F32, row0 + 32 * i, min(32, mine - 32 * i), m, p.M);
             return true;
         });
@@ -1217,7 +1237,7 @@ __global__ void __launch_bounds__((GgCfg<MODE, CG, F32>::kThreads + 32 * GgIn<EP
     __syncthreads();
     if (*(volatile int*)&sh->abort && threadIdx.x == 0) set_status(p.status, MOE_DEV_TIMEOUT);
     if (CG == 2) cluster_sync();
-    if (warp == Cfg::EPI + 1) {
+    if (warp == Role::EPI + 1) {
         tc_fence_after();
         gg_tmem_dealloc<CG>(tmem, kGgTmemCols);
     }

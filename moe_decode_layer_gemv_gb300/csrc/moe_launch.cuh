@@ -46,13 +46,13 @@ inline bool encode_blocked(CUtensorMap* map, const void* base, uint64_t inner, u
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// A 16-bit tensor [rows, cols] in boxes of 16 rows x 128 columns: inputs of an epilogue.
-inline bool encode_input(CUtensorMap* map, const void* base, uint64_t cols, uint64_t rows) {
+// A 16-bit tensor [rows, cols] in boxes of box_rows x 128 columns: inputs of an epilogue.
+inline bool encode_input(CUtensorMap* map, const void* base, uint64_t cols, uint64_t rows, uint32_t box_rows) {
     EncodeTiledFn fn = encode_fn();
     if (!fn) return false;
     const cuuint64_t dims[2] = {cols, rows};
     const cuuint64_t strides[1] = {cols * 2};
-    const cuuint32_t box[2] = {128, kGgInRows};
+    const cuuint32_t box[2] = {128, box_rows};
     const cuuint32_t estr[2] = {1, 1};
     return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims, strides, box, estr,
               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,

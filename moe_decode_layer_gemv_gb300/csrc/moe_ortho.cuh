@@ -58,25 +58,30 @@ __global__ void __launch_bounds__(256) ns_norm_kernel(const void* g, int f32, si
     };
     const size_t step = (size_t)gridDim.x * 256, first = (size_t)blockIdx.x * 256 + threadIdx.x;
     if (n % 8 == 0) {
-        for (size_t i = first; i < n / 8; i += step) {
-            if (f32) {
-                const uint4 a = ld_input_v4(static_cast<const float*>(g) + base + 8 * i);
-                const uint4 b = ld_input_v4(static_cast<const float*>(g) + base + 8 * i + 4);
-                const uint32_t u[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+        const size_t pieces = f32 ? n / 4 : n / 8;  // of 16 bytes, four in flight a thread
+        const unsigned char* from = static_cast<const unsigned char*>(g) + base * (f32 ? 4 : 2);
+        for (size_t i = first; i < pieces; i += 4 * step) {
+            uint4 v[4];
 #pragma unroll
-                for (int j = 0; j < 8; ++j) add(__uint_as_float(u[j]));
-            } else {
-                const uint4 a = ld_input_v4(static_cast<const uint16_t*>(g) + base + 8 * i);
-                const uint32_t u[4] = {a.x, a.y, a.z, a.w};
+            for (int k = 0; k < 4; ++k)
+                v[k] = i + k * step < pieces ? ld_input_v4(from + 16 * (i + k * step)) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const uint32_t u[4] = {v[k].x, v[k].y, v[k].z, v[k].w};
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
-                    const float2 f = bf16x2_to_f2(u[j]);
-                    add(f.x);
-                    add(f.y);
+                    if (f32) {
+                        add(__uint_as_float(u[j]));
+                    } else {
+                        const float2 f = bf16x2_to_f2(u[j]);
+                        add(f.x);
+                        add(f.y);
+                    }
                 }
             }
         }
     } else {
+#pragma unroll 4
         for (size_t i = first; i < n; i += step) add(ns_value(g, f32, base + i));
     }
 #pragma unroll
@@ -95,15 +100,14 @@ __global__ void __launch_bounds__(256) ns_norm_kernel(const void* g, int f32, si
 
 // X [E, rows, cols] = 2^8 G / (|G|_F + eps), or its transpose, in fp16, and in
 // `low` what that leaves; zeros beyond G's N x K.  A block takes 64 rows of G
-// and four times 64 columns; eight values of a row a thread, transposed
-// through shared memory where G is tall.  A matrix with a NaN or an infinity
-// becomes NaN throughout.
-constexpr int kNsPitch = 72;  // of a transposed tile in shared memory: rows of whole 16-byte pieces
-
+// and four times 64 columns, a thread eight values of two rows; a tall G's
+// tiles are transposed through shared memory, two rows' values a word (an odd
+// pitch: two lanes a bank).  A matrix with a NaN or an infinity becomes NaN
+// throughout.
 __global__ void __launch_bounds__(256) ns_convert_kernel(const void* g, int f32, int N, int K, const float* parts, int nparts,
                                                          float eps, int trans, uint16_t* x, uint16_t* low, int rows,
                                                          int cols) {
-    __shared__ __align__(16) uint16_t tile[2][64][kNsPitch];
+    __shared__ uint32_t tile[2][64][33];
     __shared__ float s_scale[2];
     grid_dep_launch();
     grid_dep_wait();
@@ -130,9 +134,11 @@ __global__ void __launch_bounds__(256) ns_convert_kernel(const void* g, int f32,
     const float s0 = s_scale[0], s1 = s_scale[1];
     const bool whole = K % 8 == 0;
     for (int c0 = blockIdx.x * 256; c0 < blockIdx.x * 256 + 256 && c0 < (trans ? rows : cols); c0 += 64) {
+        const int c = c0 + (tid & 7) * 8;
+        uint32_t hi[2][4], lo[2][4];  // two rows' eight values, in pairs
 #pragma unroll
-        for (int i = tid; i < 64 * 8; i += 256) {
-            const int r = r0 + (i >> 3), c = c0 + (i & 7) * 8;
+        for (int k = 0; k < 2; ++k) {
+            const int r = r0 + (tid >> 3) * 2 + k;
             const size_t at = ((size_t)e * N + r) * K + c;
             float v[8];
             if (r < N && whole && c < K) {
@@ -156,38 +162,37 @@ __global__ void __launch_bounds__(256) ns_convert_kernel(const void* g, int f32,
 #pragma unroll
                 for (int j = 0; j < 8; ++j) v[j] = r < N && c + j < K ? ns_value(g, f32, at + j) : 0.0f;
             }
-            uint32_t hi[4], lo[4];
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 const float a = v[2 * j] * s0 * s1, b = v[2 * j + 1] * s0 * s1;
-                hi[j] = gg_pack_f16(a, b);
-                const float2 h = f16x2_to_f2(hi[j]);
-                lo[j] = gg_pack_f16(a - h.x, b - h.y);
+                hi[k][j] = gg_pack_f16(a, b);
+                const float2 h = f16x2_to_f2(hi[k][j]);
+                lo[k][j] = gg_pack_f16(a - h.x, b - h.y);
             }
-            if (!trans) {
-                if (r < rows && c < cols) {  // (cols is a multiple of 64)
-                    const size_t to = ((size_t)e * rows + r) * cols + c;
-                    *reinterpret_cast<uint4*>(x + to) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-                    *reinterpret_cast<uint4*>(low + to) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
-                }
-            } else {
-#pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    tile[0][(i & 7) * 8 + j][i >> 3] = (uint16_t)(hi[j / 2] >> (j & 1) * 16);
-                    tile[1][(i & 7) * 8 + j][i >> 3] = (uint16_t)(lo[j / 2] >> (j & 1) * 16);
-                }
+            if (!trans && r < rows && c < cols) {  // (cols is a multiple of 64)
+                const size_t to = ((size_t)e * rows + r) * cols + c;
+                *reinterpret_cast<uint4*>(x + to) = make_uint4(hi[k][0], hi[k][1], hi[k][2], hi[k][3]);
+                *reinterpret_cast<uint4*>(low + to) = make_uint4(lo[k][0], lo[k][1], lo[k][2], lo[k][3]);
             }
         }
         if (!trans) continue;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            uint32_t* to = &tile[0][(tid & 7) * 8 + 2 * j][tid >> 3];
+            to[0] = __byte_perm(hi[0][j], hi[1][j], 0x5410);
+            to[33] = __byte_perm(hi[0][j], hi[1][j], 0x7632);
+            to += 64 * 33;
+            to[0] = __byte_perm(lo[0][j], lo[1][j], 0x5410);
+            to[33] = __byte_perm(lo[0][j], lo[1][j], 0x7632);
+        }
         __syncthreads();
 #pragma unroll
-        for (int i = tid; i < 64 * 8; i += 256) {
-            const int r = i >> 3, c = (i & 7) * 8;  // X's row c0 + r, columns r0 + c on
-            if (c0 + r < rows && r0 + c < cols) {
-                const size_t to = ((size_t)e * rows + c0 + r) * cols + r0 + c;
-                *reinterpret_cast<uint4*>(x + to) = *reinterpret_cast<const uint4*>(&tile[0][r][c]);
-                *reinterpret_cast<uint4*>(low + to) = *reinterpret_cast<const uint4*>(&tile[1][r][c]);
-            }
+        for (int k = tid >> 5; k < 64; k += 8) {  // X's row c0 + k, a warp a row
+            const int lane = tid & 31;
+            if (c0 + k >= rows || r0 + 2 * lane >= cols) continue;
+            const size_t to = ((size_t)e * rows + c0 + k) * cols + r0 + 2 * lane;
+            *reinterpret_cast<uint32_t*>(x + to) = tile[0][k][lane];
+            *reinterpret_cast<uint32_t*>(low + to) = tile[1][k][lane];
         }
         __syncthreads();
     }
