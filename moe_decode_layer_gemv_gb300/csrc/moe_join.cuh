@@ -249,6 +249,10 @@ __global__ void __launch_bounds__(MT) join_kernel(JoinParams p) {
 //   dz = rms(z) c - z rms(z)^3 mean(c z), else g
 //   do[pos_j] = w_j dz,  dw_j = <dz, o[pos_j]>
 //   dpre = sum_t dn y rms(y),  dscale = sum_t d b,  dpost = sum_t g z rms(z)
+// With f = scale post, the sums of c z come from those of dy f z, a f z and y f z:
+// all that depends on a whole row is summed in one pass over it, with one
+// barrier of the block a token, and the token's dw is written behind the next
+// token's barrier.
 // A block walks tokens and keeps the column sums in shared memory, each column
 // by the thread that owns it; the blocks' sums are joined in a fixed order.
 //
@@ -259,8 +263,8 @@ __global__ void __launch_bounds__(MT) join_kernel(JoinParams p) {
 template <bool OF32, int NV, int MT>
 __global__ void __launch_bounds__(MT) join_back_kernel(JoinParams p) {
     extern __shared__ __align__(16) float cols[];  // [sums][H]
-    __shared__ float buf[2][32 * 3];
-    __shared__ float dbuf[32][MOE_MAX_TOPK];
+    __shared__ float buf[2][16][8];                // by the token's parity: the warps' sums ...
+    __shared__ float dbuf[2][16][MOE_MAX_TOPK];    // ... and dw
     constexpr bool HOLD = NV == 1;
     const int nvec = p.H / 8, lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
     for (int i = threadIdx.x; i < p.sums * p.H; i += blockDim.x) cols[i] = 0.0f;
@@ -284,14 +288,21 @@ __global__ void __launch_bounds__(MT) join_back_kernel(JoinParams p) {
             w_next = p.w ? p.w[i] : 1.0f;
         }
     };
+    auto write_dw = [&](int t, int parity) {
+        if (!p.dw || (int)threadIdx.x >= p.k) return;
+        float sum = 0.0f;
+        for (int i = 0; i < warps; ++i) sum += dbuf[parity][i][threadIdx.x];
+        p.dw[(size_t)t * p.k + threadIdx.x] = sum;
+    };
     routes(blockIdx.x);
-    for (int t = blockIdx.x; t < p.T; t += gridDim.x) {
+    int parity = 0, t = blockIdx.x;
+    for (; t < p.T; t += gridDim.x, parity ^= 1) {
         if (r_next < -1 || r_next >= p.R) {
             set_status(p.status, MOE_DEV_BAD_ROUTE);
             r_next = -1;
         }
         int row[MOE_MAX_TOPK];
-        float w[MOE_MAX_TOPK], s[3] = {0.0f, 0.0f, 0.0f}, z[NV][8], d[NV][8];
+        float w[MOE_MAX_TOPK], s[8] = {}, z[NV][8];
 #pragma unroll
         for (int j = 0; j < MOE_MAX_TOPK; ++j) {
             row[j] = __shfl_sync(0xffffffffu, r_next, j);
@@ -328,6 +339,22 @@ __global__ void __launch_bounds__(MT) join_back_kernel(JoinParams p) {
             } else if (p.o) {
                 gather8<OF32, OF32 ? 2 : 4>(p, row, w, v, z[i]);
             }
+            float fz[8];  // f z
+            if (p.post) {
+                float f[8];
+                vector8(p.post, v, fz);
+                if (p.scale) vector8(p.scale, v, f);
+#pragma unroll
+                for (int c = 0; c < 8; ++c) {
+                    s[2] = fmaf(z[i][c], z[i][c], s[2]);
+                    fz[c] *= (p.scale ? f[c] : p.scale_all) * z[i][c];
+                }
+                if (p.dy) {
+                    values8(HOLD ? rd : raw8(p.dy, p.x_f32, t, p.H, v), p.x_f32, f);
+#pragma unroll
+                    for (int c = 0; c < 8; ++c) s[3] = fmaf(f[c], fz[c], s[3]);
+                }
+            }
             if (p.pre) {
                 float y[8], a[8], f[8];
                 values8(HOLD ? ry : raw8(p.x, p.x_f32, t, p.H, v), p.x_f32, y);
@@ -335,114 +362,105 @@ __global__ void __launch_bounds__(MT) join_back_kernel(JoinParams p) {
                 vector8(p.pre, v, f);
 #pragma unroll
                 for (int c = 0; c < 8; ++c) {
+                    a[c] *= f[c];
                     s[0] = fmaf(y[c], y[c], s[0]);
-                    s[1] = fmaf(a[c] * f[c], y[c], s[1]);
+                    s[1] = fmaf(a[c], y[c], s[1]);
                 }
-            }
-            if (p.post) {
+                if (p.post) {
 #pragma unroll
-                for (int c = 0; c < 8; ++c) s[2] = fmaf(z[i][c], z[i][c], s[2]);
-            }
-        }
-        if (p.pre || p.post) token_sum(s, buf[0]);
-        const float ny = 1.0f / sqrtf(s[0] / (float)p.H + p.eps), my = ny * ny * ny * (s[1] / (float)p.H);
-        const float nz = 1.0f / sqrtf(s[2] / (float)p.H + p.eps);
-        float cz[1] = {0.0f};
-#pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            const int v = threadIdx.x + i * blockDim.x;
-            if (v >= nvec) continue;
-            if (p.dy) {
-                values8(HOLD ? rd : raw8(p.dy, p.x_f32, t, p.H, v), p.x_f32, d[i]);
-            } else {
-#pragma unroll
-                for (int c = 0; c < 8; ++c) d[i][c] = 0.0f;
-            }
-            if (p.pre) {
-                float y[8], a[8], f[8];
-                values8(HOLD ? ry : raw8(p.x, p.x_f32, t, p.H, v), p.x_f32, y);
-                values8(HOLD ? rn : raw8(p.dn, p.n_f32, t, p.H, v), p.n_f32, a);
-                vector8(p.pre, v, f);
-#pragma unroll
-                for (int c = 0; c < 8; ++c) {
-                    d[i][c] += ny * (a[c] * f[c]) - y[c] * my;
-                    f[c] = a[c] * y[c] * ny;
-                }
-                add8(c_pre, nvec, v, f);
-            }
-            put8(p.y, p.x_f32, t, p.H, v, d[i]);
-            if (!p.o) continue;
-            float f[8], q[8];
-            if (p.post) vector8(p.post, v, q);
-            if (c_scale) {
-#pragma unroll
-                for (int c = 0; c < 8; ++c) f[c] = d[i][c] * (p.post ? z[i][c] * nz * q[c] : z[i][c]);
-                add8(c_scale, nvec, v, f);
-            }
-            if (p.scale) {
-                vector8(p.scale, v, f);
-#pragma unroll
-                for (int c = 0; c < 8; ++c) d[i][c] *= f[c];
-            } else {
-#pragma unroll
-                for (int c = 0; c < 8; ++c) d[i][c] *= p.scale_all;
-            }
-            if (p.post) {
-#pragma unroll
-                for (int c = 0; c < 8; ++c) f[c] = d[i][c] * (z[i][c] * nz);
-                add8(c_post, nvec, v, f);
-#pragma unroll
-                for (int c = 0; c < 8; ++c) {
-                    d[i][c] *= q[c];
-                    cz[0] = fmaf(d[i][c], z[i][c], cz[0]);
+                    for (int c = 0; c < 8; ++c) {
+                        s[4] = fmaf(a[c], fz[c], s[4]);
+                        s[5] = fmaf(y[c], fz[c], s[5]);
+                    }
                 }
             }
         }
-        if (!p.o) {
-            __syncthreads();  // (buf is used again)
-            continue;
+        // every thread's totals: lane 4 v + k adds a quarter of the warps' sums of value v
+        {
+            const float one = warp_sum8(s, lane);
+            if ((lane & 3) == 0) buf[parity][warp][lane >> 2] = one;
+            __syncthreads();
+            float sum = 0.0f;
+            for (int i = lane & 3; i < warps; i += 4) sum += buf[parity][i][lane >> 2];
+            sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+            sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+#pragma unroll
+            for (int j = 0; j < 6; ++j) s[j] = __shfl_sync(0xffffffffu, sum, 4 * j);
         }
-        float mz = 0.0f;
-        if (p.post) {
-            token_sum(cz, buf[1]);
-            mz = nz * nz * nz * (cz[0] / (float)p.H);
-        }
+        if (t != (int)blockIdx.x) write_dw(t - gridDim.x, parity ^ 1);
+        const float n = 1.0f / (float)p.H;
+        const float ny = 1.0f / sqrtf(s[0] * n + p.eps), my = ny * ny * ny * (s[1] * n);
+        const float nz = 1.0f / sqrtf(s[2] * n + p.eps);
+        const float mz = nz * nz * nz * ((s[3] + (p.pre ? ny * s[4] - my * s[5] : 0.0f)) * n);
         float dots[MOE_MAX_TOPK] = {};
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             const int v = threadIdx.x + i * blockDim.x;
             if (v >= nvec) continue;
+            float d[8], f[8];
+            if (p.dy) {
+                values8(HOLD ? rd : raw8(p.dy, p.x_f32, t, p.H, v), p.x_f32, d);
+            } else {
+#pragma unroll
+                for (int c = 0; c < 8; ++c) d[c] = 0.0f;
+            }
+            if (p.pre) {
+                float y[8], a[8];
+                values8(HOLD ? ry : raw8(p.x, p.x_f32, t, p.H, v), p.x_f32, y);
+                values8(HOLD ? rn : raw8(p.dn, p.n_f32, t, p.H, v), p.n_f32, a);
+                vector8(p.pre, v, f);
+#pragma unroll
+                for (int c = 0; c < 8; ++c) {
+                    d[c] += ny * (a[c] * f[c]) - y[c] * my;
+                    f[c] = a[c] * y[c] * ny;
+                }
+                add8(c_pre, nvec, v, f);
+            }
+            put8(p.y, p.x_f32, t, p.H, v, d);
+            if (!p.o) continue;
+            float q[8];
+            if (p.post) vector8(p.post, v, q);
+            if (c_scale) {
+#pragma unroll
+                for (int c = 0; c < 8; ++c) f[c] = d[c] * (p.post ? z[i][c] * nz * q[c] : z[i][c]);
+                add8(c_scale, nvec, v, f);
+            }
+            if (p.scale) {
+                vector8(p.scale, v, f);
+#pragma unroll
+                for (int c = 0; c < 8; ++c) d[c] *= f[c];
+            } else {
+#pragma unroll
+                for (int c = 0; c < 8; ++c) d[c] *= p.scale_all;
+            }
             if (p.post) {
 #pragma unroll
-                for (int c = 0; c < 8; ++c) d[i][c] = nz * d[i][c] - z[i][c] * mz;
+                for (int c = 0; c < 8; ++c) {
+                    f[c] = d[c] * (z[i][c] * nz);
+                    d[c] = nz * (d[c] * q[c]) - z[i][c] * mz;
+                }
+                add8(c_post, nvec, v, f);
             }
 #pragma unroll
             for (int j = 0; j < MOE_MAX_TOPK; ++j)
                 if (row[j] >= 0) {
-                    float f[8];
                     if (p.dw) {
                         values8(HOLD ? ro[HOLD ? j : 0] : raw8(p.o, OF32, row[j], p.H, v), OF32, f);
 #pragma unroll
-                        for (int c = 0; c < 8; ++c) dots[j] = fmaf(d[i][c], f[c], dots[j]);
+                        for (int c = 0; c < 8; ++c) dots[j] = fmaf(d[c], f[c], dots[j]);
                     }
 #pragma unroll
-                    for (int c = 0; c < 8; ++c) f[c] = w[j] * d[i][c];
+                    for (int c = 0; c < 8; ++c) f[c] = w[j] * d[c];
                     put8(p.d_o, OF32, row[j], p.H, v, f);
                 }
         }
         if (p.dw) {
             const float one = warp_sum8(dots, lane);
-            if ((lane & 3) == 0) dbuf[warp][lane >> 2] = one;
+            if ((lane & 3) == 0) dbuf[parity][warp][lane >> 2] = one;
         }
-        __syncthreads();  // (buf is used again behind it)
-        if (p.dw && threadIdx.x < p.k) {
-            float sum = 0.0f;
-            for (int i = 0; i < warps; ++i) sum += dbuf[i][threadIdx.x];
-            p.dw[(size_t)t * p.k + threadIdx.x] = sum;
-        }
-        // (dbuf is written again only behind the next token's sums; without any there is one more barrier)
-        if (p.dw && !p.pre && !p.post) __syncthreads();
     }
+    __syncthreads();
+    write_dw(t - gridDim.x, parity ^ 1);
     float4* out = reinterpret_cast<float4*>(p.parts + (size_t)blockIdx.x * p.sums * p.H);
     const float4* in = reinterpret_cast<const float4*>(cols);
     for (int s = 0; s < p.sums; ++s)
