@@ -644,19 +644,24 @@ __device__ __forceinline__ void glu_store(const P& p, uint32_t (&sum)[COLS / 32]
         if (nc <= 0) break;
         uint32_t(&r)[32] = sum[k];
         if (p.out2) gg_store32(r, p.out2, 0, row0 + 32 * k, min(32, nc), col, 2 * I);
-        const size_t at = (row0 + 32 * k + up) * (size_t)I + i;
-        const int last = i < I ? nc - up : 0;
+        // bf16: lanes 2 l and 2 l + 1 swap once more, so that each writes two neighbouring outputs (4 bytes) of one row
+        const int odd = i & 1;
+        const size_t at = (row0 + 32 * k + up + (F32 ? 0 : 2 * odd)) * (size_t)I + (F32 ? i : i - odd);
+        const int last = i < I ? nc - up - (F32 ? 0 : 2 * odd) : 0;
+        float before = 0.0f;
 #pragma unroll
         for (int j = 0; j < 32; j += 2) {
             const uint32_t got = __shfl_xor_sync(0xffffffffu, up ? r[j] : r[j + 1], 8);
             const float g = __uint_as_float(up ? got : r[j]), u = __uint_as_float(up ? r[j + 1] : got);
             float grad;
             const float h = glu_act(g, p.c0, p.c1, grad) * u;
-            if (j < last) {
-                if (F32)
-                    static_cast<float*>(p.out)[at + (size_t)j * I] = h;
-                else
-                    static_cast<uint16_t*>(p.out)[at + (size_t)j * I] = f2bf_bits(h);
+            if (F32) {
+                if (j < last) static_cast<float*>(p.out)[at + (size_t)j * I] = h;
+            } else if (j % 4 == 0) {
+                before = h;
+            } else {
+                const uint32_t v = gg_pair(gg_pack(__float_as_uint(before), __float_as_uint(h)), gg_pair_select(odd));
+                if (j - 2 < last) *reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(p.out) + at + (size_t)(j - 2) * I) = v;
             }
         }
     }
