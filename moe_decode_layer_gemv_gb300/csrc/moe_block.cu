@@ -490,8 +490,11 @@ int moe_orthogonalize(const void* g, int g_dtype, int E, int N, int K, int steps
         if (rc) return rc;
         // (the blocks cover the padded X: its rows are G's columns where G is tall)
         const int rows = trans ? q.n : q.m, cols = trans ? q.m : q.n;
-        rc = launch_pdl(ns_convert_kernel, dim3((unsigned)ceil_div(cols, 256), (unsigned)ceil_div(rows, 64), (unsigned)G), 256, 0,
-                        st, from, f32, N, K, (const float*)parts, q.parts, eps, trans, x[0], low, q.m, q.n);
+        // (a block finds the norm first: with many blocks one serves four tiles)
+        const int64_t tiles = (int64_t)G * ceil_div(cols, 64) * ceil_div(rows, 64);
+        const int strip = tiles >= 16 * sms ? 256 : 64;
+        rc = launch_pdl(ns_convert_kernel, dim3((unsigned)ceil_div(cols, strip), (unsigned)ceil_div(rows, 64), (unsigned)G), 256,
+                        0, st, from, f32, N, K, (const float*)parts, q.parts, eps, trans, x[0], low, q.m, q.n, strip);
         if (rc) return rc;
         s.last[(steps - 1) & 1].out = out + each * e;
         const bool more = e + G < E;

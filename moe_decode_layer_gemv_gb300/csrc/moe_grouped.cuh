@@ -817,9 +817,17 @@ __device__ __forceinline__ void ns_result_rows(const P& p, const float* d, const
             if (j + 8 <= k && p.res_cols % 8 == 0) {
                 *reinterpret_cast<uint4*>(to + j) = make_uint4(w[j / 2], w[j / 2 + 1], w[j / 2 + 2], w[j / 2 + 3]);
             } else {
+                const bool even = p.res_cols % 2 == 0;  // (pairs then lie on 4 bytes, and k is even)
 #pragma unroll
-                for (int i = 0; i < 8; ++i)
-                    if (j + i < k) to[j + i] = (uint16_t)(w[(j + i) / 2] >> (i & 1) * 16);
+                for (int i = 0; i < 8; i += 2) {
+                    if (j + i >= k) break;
+                    if (even) {
+                        *reinterpret_cast<uint32_t*>(to + j + i) = w[(j + i) / 2];
+                    } else {
+                        to[j + i] = (uint16_t)w[(j + i) / 2];
+                        if (j + i + 1 < k) to[j + i + 1] = (uint16_t)(w[(j + i) / 2] >> 16);
+                    }
+                }
             }
         }
     } else {

@@ -100,13 +100,13 @@ __global__ void __launch_bounds__(256) ns_norm_kernel(const void* g, int f32, si
 
 // X [E, rows, cols] = 2^8 G / (|G|_F + eps), or its transpose, in fp16, and in
 // `low` what that leaves; zeros beyond G's N x K.  A block takes 64 rows of G
-// and four times 64 columns, a thread eight values of two rows; a tall G's
+// and `strip` columns, 64 at a time, a thread eight values of two rows; a tall G's
 // tiles are transposed through shared memory, two rows' values a word (an odd
 // pitch: two lanes a bank).  A matrix with a NaN or an infinity becomes NaN
 // throughout.
 __global__ void __launch_bounds__(256) ns_convert_kernel(const void* g, int f32, int N, int K, const float* parts, int nparts,
                                                          float eps, int trans, uint16_t* x, uint16_t* low, int rows,
-                                                         int cols) {
+                                                         int cols, int strip) {
     __shared__ uint32_t tile[2][64][33];
     __shared__ float s_scale[2];
     grid_dep_launch();
@@ -133,7 +133,7 @@ __global__ void __launch_bounds__(256) ns_convert_kernel(const void* g, int f32,
     __syncthreads();
     const float s0 = s_scale[0], s1 = s_scale[1];
     const bool whole = K % 8 == 0;
-    for (int c0 = blockIdx.x * 256; c0 < blockIdx.x * 256 + 256 && c0 < (trans ? rows : cols); c0 += 64) {
+    for (int c0 = blockIdx.x * strip; c0 < (blockIdx.x + 1) * strip && c0 < (trans ? rows : cols); c0 += 64) {
         const int c = c0 + (tid & 7) * 8;
         uint32_t hi[2][4], lo[2][4];  // two rows' eight values, in pairs
 #pragma unroll
@@ -160,7 +160,7 @@ __global__ void __launch_bounds__(256) ns_convert_kernel(const void* g, int f32,
                 }
             } else {
 #pragma unroll
-                for (int j = 0; j < 8; ++j) v[j] = r < N && c + j < K ? ns_value(g, f32, at + j) : 0.0f;
+                for (int j = 0; j < 8; ++j) v[j] = r < N && c + j < K ? ns_value(g, f32, at + j) : 0.0f;  // (all in flight)
             }
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
