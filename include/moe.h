@@ -392,7 +392,10 @@ int moe_grouped_glu(const uint16_t* x, const uint16_t* gate_up, const int32_t* o
  * dgu [R, 2I] and h [R, I] bf16.  The rest of the block's backward pass is
  * moe_grouped_gemm_dx(dgu, gate_up), moe_grouped_gemm_dw(dgu, x) and
  * moe_grouped_gemm_dw(dy, h): h is made again here, so that the forward pass
- * need not keep it.  dgu may not overlap gu.  Otherwise as moe_grouped_glu.
+ * need not keep it.  dgu may not overlap gu (the same address is refused).  dh
+ * is one fp32 sum, whose additions (one for 16 terms) truncate: a sum of one
+ * sign loses up to 7.4e-5 at H = 16384, 2 % of a bf16 result's half step.
+ * Otherwise as moe_grouped_glu.
  */
 int moe_grouped_glu_backward(const uint16_t* dy, const uint16_t* down, const uint16_t* gu, const int32_t* offsets, int R,
                              int H, int I, int E, int act, uint16_t* dgu, uint16_t* h, int32_t* dev_status, void* stream);
@@ -429,7 +432,8 @@ int moe_combine_norm(const void* x, int x_dtype, const void* o, int o_dtype, con
  * (NULL: not wanted), dpost, dscale, dpre [H] fp32, each for the vector that
  * is given.  pos must name each row at most once, as a grouping's inverse
  * does; rows that it does not name are left as they were in d_o, and dw is 0
- * for dropped routes.  dx may alias dy, d_o may not alias o.  The column sums
+ * for dropped routes.  dx may alias dy; d_o may not overlap o (the same address
+ * is refused).  The column sums
  * are joined in a fixed order (the same call gives the same bits) through the
  * workspace, of moe_combine_norm_backward_workspace_bytes() (host-only, for
  * the current device; sums: how many of post, scale and pre are given), used

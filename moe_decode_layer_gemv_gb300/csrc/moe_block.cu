@@ -282,6 +282,7 @@ int moe_grouped_glu_backward(const uint16_t* dy, const uint16_t* down, const uin
     MOE_REQ(offsets);
     MOE_REQ(dgu);
     MOE_REQ(h);
+    if (dgu == gu) return MOE_ERR_INVALID_ARG;  // (gu is read ahead of what is written)
     MOE_OPT(dev_status);
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     const int sms = sm_count();
@@ -393,6 +394,7 @@ int moe_combine_norm_backward(const void* dy, const void* dn, int n_dtype, const
     MOE_REQ(dx);
     MOE_OPT(o);
     if (o) MOE_REQ(d_o);
+    if (o && d_o == o && R > 0) return MOE_ERR_INVALID_ARG;  // (wide rows are read again behind the first writes)
     MOE_OPT(pos);
     MOE_OPT(w);
     MOE_OPT(dw);

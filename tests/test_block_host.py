@@ -23,7 +23,7 @@ def test_gated_unit_refuses_before_any_launch(api):
     def fwd(x=GOOD, w=GOOD, off=GOOD, R=4, H=64, I=64, E=8, act=0, h=GOOD, dt=1, gu=GOOD, st=None):
         return api._lib.moe_grouped_glu(x, w, off, R, H, I, E, act, h, dt, gu, st, None)
 
-    def back(x=GOOD, w=GOOD, off=GOOD, R=4, H=64, I=64, E=8, act=0, h=GOOD, gu=GOOD, dgu=GOOD, st=None):
+    def back(x=GOOD, w=GOOD, off=GOOD, R=4, H=64, I=64, E=8, act=0, h=GOOD, gu=GOOD, dgu=GOOD + 4096, st=None):
         return api._lib.moe_grouped_glu_backward(x, w, gu, off, R, H, I, E, act, dgu, h, st, None)
 
     inv = api.MOE_ERR_INVALID_ARG
@@ -33,6 +33,7 @@ def test_gated_unit_refuses_before_any_launch(api):
     for kw in both:
         assert fwd(**kw) == inv, kw
         assert back(**kw) == inv, kw
+    assert back(dgu=GOOD) == inv  # gu itself
     assert fwd(dt=2) == inv and back(gu=None) == inv and back(dgu=None) == inv and back(dgu=ODD) == inv
     assert fwd(R=0, x=None, h=None) == api.MOE_OK and back(R=0, x=None, dgu=None) == api.MOE_OK
 
@@ -63,7 +64,7 @@ def test_the_join_refuses_before_any_launch(api):
         return api._lib.moe_combine_norm(x, xd, o, od, pos, w, T, H, R, k, post, scale, 1.0, pre, eps, y, n, nd, st, None)
 
     def back(x=GOOD, xd=0, o=GOOD, od=1, pos=GOOD, w=GOOD, T=4, H=64, R=8, k=2, post=GOOD, scale=GOOD, pre=GOOD, eps=1e-6,
-             y=GOOD, n=GOOD, nd=1, st=None, do=GOOD, dw=GOOD, dpost=GOOD, dscale=GOOD, dpre=GOOD, dy=GOOD, ws=GOOD,
+             y=GOOD, n=GOOD, nd=1, st=None, do=GOOD + 4096, dw=GOOD, dpost=GOOD, dscale=GOOD, dpre=GOOD, dy=GOOD, ws=GOOD,
              nw=1 << 30):
         return api._lib.moe_combine_norm_backward(dy, n, nd, x, xd, o, od, pos, w, T, H, R, k, post, scale, 1.0, pre, eps, y,
                                                   do, dw, dpost, dscale, dpre, ws, nw, st, None)
@@ -79,6 +80,7 @@ def test_the_join_refuses_before_any_launch(api):
         assert back(**kw) == inv, kw
     for kw in ({v: None} for v in ("do", "dpost", "dscale", "dpre")):
         assert back(**kw) == inv, kw
+    assert back(do=GOOD) == inv  # o itself
     assert back(ws=None) == api.MOE_ERR_WORKSPACE and back(nw=64) == api.MOE_ERR_WORKSPACE
     assert fwd(T=0, x=None) == api.MOE_OK
 
