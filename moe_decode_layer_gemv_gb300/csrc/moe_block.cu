@@ -128,7 +128,7 @@ struct NsPlan {
     int m, n;        // rows and columns of X, padded
     int group;       // matrices that go through all steps together
     int parts;       // blocks that sum a matrix's squares
-    bool pairs;      // tiles of CTA pairs
+    bool pairs, narrow;  // tiles of CTA pairs, tiles of 32 columns
     size_t x, a, p;  // bytes of a group's X, of its A, of the sums
     size_t bytes;
 };
@@ -141,6 +141,10 @@ static int ns_plan(int E, int N, int K, int sms, NsPlan* q) {
     const int t = ceil_div(q->m, 256);
     const int tri = t * (t + 1) / 2;
     q->pairs = (int64_t)E * tri >= sms / 2;
+    // narrow tiles while they leave no SM a second one of the symmetric products.  Measured, a product of the
+    // chain with tiles of 128 and of 32 columns: one matrix of 390 x 515 6.7 and 4.6 us, 512 x 2048 8.8 and 7.3,
+    // 768 x 2048 9.8 and 9.2, 1024 x 1024 8.9 and 10.2; four of 390 x 515 6.8 and 6.6, eight 7.8 and 9.5
+    q->narrow = (int64_t)E * ceil_div(q->m, 32) * ceil_div(q->m, 128) <= sms;
     q->group = E;
     q->parts = ceil_div(8 * sms, q->group);
     const int most = (int)(((size_t)N * K + 2047) / 2048);
@@ -186,15 +190,15 @@ static bool ns_params(const NsPlan& q, const void* w, const void* x, int cols, c
     return ok;
 }
 
-template <int CG>
+template <int CG, bool NARROW>
 static int ns_allow() {
-    int rc = allow_smem(gg_kernel<kGgFwd, CG, false, kGgSym>, kGgSmem);
-    if (!rc) rc = allow_smem(gg_kernel<kGgDx, CG, false, kGgAxpy>, kGgSmem);
-    return rc ? rc : allow_smem(gg_kernel<kGgDx, CG, false, kGgResult>, kGgSmem);
+    int rc = allow_smem(gg_kernel<kGgFwd, CG, false, kGgSym, NARROW>, kGgSmem);
+    if (!rc) rc = allow_smem(gg_kernel<kGgDx, CG, false, kGgAxpy, NARROW>, kGgSmem);
+    return rc ? rc : allow_smem(gg_kernel<kGgDx, CG, false, kGgResult, NARROW>, kGgSmem);
 }
 
 // One product of E matrices, on no more SMs than it has tiles.
-template <int EP, int CG>
+template <int EP, int CG, bool NARROW>
 static int run_ns(GgParams& p, int E, float alpha, float beta, float shift, bool early, int sms, cudaStream_t st) {
     constexpr int MODE = EP == kGgSym ? kGgFwd : kGgDx;
     p.E = E;
@@ -203,22 +207,23 @@ static int run_ns(GgParams& p, int E, float alpha, float beta, float shift, bool
     p.beta = beta;
     p.shift = shift;
     p.early = early;
-    const int64_t t = ceil_div(p.rows, 128 * CG), tiles = E * (EP == kGgSym ? t * (t + 1) / 2 : t * ceil_div(p.M, 128 * CG));
-    return launch_clusters<CG>(gg_kernel<MODE, CG, false, EP>, p, GgRole<MODE, CG, false, EP>::kThreads,
+    const int64_t t = ceil_div(p.rows, NARROW ? 32 : 128 * CG);
+    const int64_t tiles = E * (EP == kGgSym && !NARROW ? t * (t + 1) / 2 : t * ceil_div(p.M, 128 * CG));
+    return launch_clusters<CG>(gg_kernel<MODE, CG, false, EP, NARROW>, p, GgRole<MODE, CG, false, EP, NARROW>::kThreads,
                                tiles * CG < sms ? (int)tiles * CG : sms, st);
 }
 
-template <int CG>
+template <int CG, bool NARROW>
 static int run_ns_steps(NsProducts& s, int E, int steps, float a, float b, float c, bool more, int sms, cudaStream_t st) {
     const float up = (float)(1 << kNsScaleLog2), down = 1.0f / up;
     for (int i = 0; i < steps; ++i) {
         // a + b A + c A A of A = S + A': one + lin A' + c A' A'
         const float S = steps - i <= kNsShifted ? kNsShift : 0.0f, lin = b + 2.0f * c * S, one = a + b * S + c * S * S;
-        int rc = run_ns<kGgSym, CG>(s.xx[i & 1], E, down * down, 0.0f, S, true, sms, st);
-        if (!rc) rc = run_ns<kGgSym, CG>(s.aa, E, c, lin, 0.0f, true, sms, st);
+        int rc = run_ns<kGgSym, CG, NARROW>(s.xx[i & 1], E, down * down, 0.0f, S, true, sms, st);
+        if (!rc) rc = run_ns<kGgSym, CG, NARROW>(s.aa, E, c, lin, 0.0f, true, sms, st);
         if (!rc)
-            rc = i + 1 < steps ? run_ns<kGgAxpy, CG>(s.bx[i & 1], E, 1.0f, one, 0.0f, true, sms, st)
-                               : run_ns<kGgResult, CG>(s.last[i & 1], E, down, one * down, 0.0f, more, sms, st);
+            rc = i + 1 < steps ? run_ns<kGgAxpy, CG, NARROW>(s.bx[i & 1], E, 1.0f, one, 0.0f, true, sms, st)
+                               : run_ns<kGgResult, CG, NARROW>(s.last[i & 1], E, down, one * down, 0.0f, more, sms, st);
         if (rc) return rc;
     }
     return MOE_OK;
@@ -483,7 +488,7 @@ int moe_orthogonalize(const void* g, int g_dtype, int E, int N, int K, int steps
     }
     if (!ok) return MOE_ERR_UNSUPPORTED;
     s.aa.status = dev_status;
-    if ((rc = q.pairs ? ns_allow<2>() : ns_allow<1>())) return rc;
+    if ((rc = q.narrow ? ns_allow<1, true>() : q.pairs ? ns_allow<2, false>() : ns_allow<1, false>())) return rc;
     const size_t each = (size_t)N * K;
     for (int e = 0; e < E; e += q.group) {
         const int G = E - e < q.group ? E - e : q.group;
@@ -500,7 +505,9 @@ int moe_orthogonalize(const void* g, int g_dtype, int E, int N, int K, int steps
         if (rc) return rc;
         s.last[(steps - 1) & 1].out = out + each * e;
         const bool more = e + G < E;
-        rc = q.pairs ? run_ns_steps<2>(s, G, steps, a, b, c, more, sms, st) : run_ns_steps<1>(s, G, steps, a, b, c, more, sms, st);
+        rc = q.narrow  ? run_ns_steps<1, true>(s, G, steps, a, b, c, more, sms, st)
+             : q.pairs ? run_ns_steps<2, false>(s, G, steps, a, b, c, more, sms, st)
+                       : run_ns_steps<1, false>(s, G, steps, a, b, c, more, sms, st);
         if (rc) return rc;
     }
     return MOE_OK;

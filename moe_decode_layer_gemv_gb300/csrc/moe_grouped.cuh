@@ -118,21 +118,24 @@ constexpr int kGgInMax = 4;  // parts of the columns, and slots each, at most
 // operands: the gated unit's gradient of 65536 rows takes 205 us with 24 KB of
 // them, 188 with 32 and 48, 205 with 64, 225 with 96; eight or sixteen
 // epilogue warps make no difference there, as it waits for L2 by then.
-template <int EP>
+template <int EP, bool NARROW = false>
 struct GgIn {
     static constexpr bool kOn = EP >= kGgGluBack;
-    static constexpr int kParts = EP == kGgGluBack ? 2 : 4, kRows = 16, kSlots = EP == kGgGluBack ? 3 : 2;
+    static constexpr int kParts = EP == kGgGluBack || NARROW ? 2 : 4, kRows = 16, kSlots = EP == kGgGluBack ? 3 : 2;
     static constexpr int kPlane = kRows * 256;  // bytes
     static constexpr int kBytes = kOn ? kParts * kSlots * 2 * kPlane : 0;
 };
 
-// Roles and limits by epilogue, over GgCfg's.
-template <int MODE, int CG, bool F32, int EP>
+// Roles and limits by epilogue, over GgCfg's.  NARROW tiles of 32 columns are
+// for products too small to fill the GPU: an SM takes in some 100 GB/s of
+// operands, so that it is the number of SMs that counts (orthogonalisation).
+template <int MODE, int CG, bool F32, int EP, bool NARROW = false>
 struct GgRole {
-    static constexpr bool kIn = GgIn<EP>::kOn;
-    static constexpr int kInBytes = GgIn<EP>::kBytes;
-    static constexpr int EPI = kIn ? 4 * GgIn<EP>::kParts : GgCfg<MODE, CG, F32>::EPI;  // epilogue warps
-    static constexpr int COLS = 128 * CG / (EPI / 4);
+    static constexpr bool kIn = GgIn<EP, NARROW>::kOn;
+    static constexpr int kInBytes = GgIn<EP, NARROW>::kBytes;
+    static constexpr int EPI = kIn ? 4 * GgIn<EP, NARROW>::kParts : GgCfg<MODE, CG, F32>::EPI;  // epilogue warps
+    static constexpr int BN = NARROW ? 32 : GgCfg<MODE, CG, F32>::BN;
+    static constexpr int COLS = BN / (EPI / 4);
     static constexpr int kThreads = kIn ? 32 * (EPI + 3) : GgCfg<MODE, CG, F32>::kThreads;
     static constexpr int kPart = kIn ? 1 << 30 : kGgPartSteps;  // steps an accumulator takes
     // (beside the inputs two steps a stage would leave room for two stages)
@@ -853,15 +856,16 @@ __device__ __forceinline__ void ns_result_rows(const P& p, const float* d, const
 // tiles.  Three roles run through the same tile sequence, each at its own
 // pace: the producer fills the ring, the MMA issuer accumulates tile d into
 // tensor-memory buffer d mod 2, the epilogue warps read the other buffer out.
-template <int MODE, int CG, bool F32, int EP = kGgStore>
-__global__ void __launch_bounds__((GgRole<MODE, CG, F32, EP>::kThreads), 1) gg_kernel(const __grid_constant__ GgParams p) {
+template <int MODE, int CG, bool F32, int EP = kGgStore, bool NARROW = false>
+__global__ void __launch_bounds__((GgRole<MODE, CG, F32, EP, NARROW>::kThreads), 1) gg_kernel(const __grid_constant__ GgParams p) {
     using Cfg = GgCfg<MODE, CG, F32>;
     extern __shared__ __align__(1024) unsigned char gg_smem_raw[];
     unsigned char* base = reinterpret_cast<unsigned char*>(
         (reinterpret_cast<uintptr_t>(gg_smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
     GgShared* sh = reinterpret_cast<GgShared*>(base);
-    using Role = GgRole<MODE, CG, F32, EP>;
-    using In = GgIn<EP>;
+    using Role = GgRole<MODE, CG, F32, EP, NARROW>;
+    using In = GgIn<EP, NARROW>;
+    constexpr bool kMirror = EP == kGgSym && !NARROW;  // half the tiles, stored twice
     unsigned char* ins = base + 4096;
     unsigned char* ring = ins + Role::kInBytes;
 
@@ -896,7 +900,7 @@ __global__ void __launch_bounds__((GgRole<MODE, CG, F32, EP>::kThreads), 1) gg_k
     if (EP < kGgSym) grid_dep_wait();
     constexpr int MW = EP == kGgGlu ? 64 : 128, BMW = MW * CG;  // outputs that a CTA's 128 rows and a tile give
     const int mtiles = (p.M + BMW - 1) / BMW;
-    gg_segments(sh, p.offsets, EP >= kGgSym ? p.rows : 0, p.E, p.R, Cfg::BN, p.status);
+    gg_segments(sh, p.offsets, EP >= kGgSym ? p.rows : 0, p.E, p.R, Role::BN, p.status);
     tc_fence_before();
     __syncthreads();
     if (CG == 2) cluster_sync();
@@ -909,37 +913,37 @@ __global__ void __launch_bounds__((GgRole<MODE, CG, F32, EP>::kThreads), 1) gg_k
     // segment needs, so that few rows leave more bytes of weights in flight.
     uint32_t b_tile = kGgTile;
     if (MODE != kGgDw && CG == 1)
-        b_tile = (uint32_t)min(Cfg::BN, max(kGgBoxN, (sh->nmax + kGgBoxN - 1) / kGgBoxN * kGgBoxN)) * 128u;
+        b_tile = (uint32_t)min(Role::BN, max(kGgBoxN, (sh->nmax + kGgBoxN - 1) / kGgBoxN * kGgBoxN)) * 128u;
     const uint32_t stage_bytes = Role::KSUB * (kGgTile + b_tile);
     const uint32_t b_off = Role::KSUB * kGgTile;
     const uint32_t S = min((uint32_t)kGgMaxStages, ((uint32_t)kGgSmem - 1023u - 4096u - Role::kInBytes) / stage_bytes);
 
-    const int ntiles_w = (p.NW + Cfg::BN - 1) / Cfg::BN;  // dw
-    const int tri = EP == kGgSym ? mtiles * (mtiles + 1) / 2 : 0;  // tiles on and below the diagonal
-    const int outers = EP == kGgSym ? p.E : MODE == kGgDw ? p.split * p.E : sh->start[p.E];
+    const int ntiles_w = (p.NW + Role::BN - 1) / Role::BN;  // dw
+    const int tri = kMirror ? mtiles * (mtiles + 1) / 2 : 0;  // tiles on and below the diagonal
+    const int outers = kMirror ? p.E : MODE == kGgDw ? p.split * p.E : sh->start[p.E];
 
     // f(e, q0, n, n0, m0, len): segment e; first row q0 (forward, dx: of the
     // tile; dw: of the segment's part); n valid columns from n0 on; m from m0
     // on; contraction length.  (dw: e counts part after part, part * E + e)
     auto walk = [&](auto f) {
         int e = 0;
-        for (GgWalk w(unit, units, EP == kGgSym ? tri : MODE == kGgDw ? mtiles * ntiles_w : mtiles); w.outer < outers; w.next()) {
+        for (GgWalk w(unit, units, kMirror ? tri : MODE == kGgDw ? mtiles * ntiles_w : mtiles); w.outer < outers; w.next()) {
             int q0, n, n0, m0, len;
-            if (EP == kGgSym) {
+            if (kMirror) {
                 e = w.outer;
                 int i = 0, j = w.inner;  // row i of the triangle holds i + 1 tiles
                 while (j > i) j -= ++i;
                 m0 = j * BMW;
-                n0 = i * Cfg::BN;
-                n = min(Cfg::BN, p.rows - n0);
+                n0 = i * Role::BN;
+                n = min(Role::BN, p.rows - n0);
                 q0 = e * p.rows + n0;
                 len = p.C;
             } else if (MODE == kGgDw) {
                 e = w.outer;
                 const int tn = w.inner / mtiles;
                 m0 = (w.inner - tn * mtiles) * BMW;
-                n0 = tn * Cfg::BN;
-                n = min(Cfg::BN, p.NW - n0);
+                n0 = tn * Role::BN;
+                n = min(Role::BN, p.NW - n0);
                 const int seg = p.split == 1 ? e : e % p.E, cnt = sh->cnt[seg];
                 int part = cnt, at = 0;
                 if (p.split > 1) {
@@ -951,8 +955,8 @@ __global__ void __launch_bounds__((GgRole<MODE, CG, F32, EP>::kThreads), 1) gg_k
             } else {
                 e = gg_seek(sh->start, p.E, w.outer, e);
                 m0 = w.inner * BMW;
-                n0 = (w.outer - sh->start[e]) * Cfg::BN;
-                n = min(Cfg::BN, sh->cnt[e] - n0);
+                n0 = (w.outer - sh->start[e]) * Role::BN;
+                n = min(Role::BN, sh->cnt[e] - n0);
                 q0 = sh->p0[e] + n0;
                 len = p.C;
             }
@@ -1032,7 +1036,7 @@ __global__ void __launch_bounds__((GgRole<MODE, CG, F32, EP>::kThreads), 1) gg_k
         const uint32_t ring_at = smem_u32(ring);
         if (rank == 0 && gg_elect()) walk([&](int e, int q0, int n, int n0, int m0, int len) -> bool {
             const int nk = (len + 63) / 64;
-            const int npad = MODE == kGgDw ? Cfg::BN : (n + kGgBoxN * CG - 1) / (kGgBoxN * CG) * (kGgBoxN * CG);
+            const int npad = MODE == kGgDw ? Role::BN : (n + kGgBoxN * CG - 1) / (kGgBoxN * CG) * (kGgBoxN * CG);
             const uint32_t idesc = (EP >= kGgSym ? umma_idesc_f16(Cfg::BM, npad) : umma_idesc_bf16(Cfg::BM, npad)) | (MODE != kGgFwd ? 1u << 15 : 0u) |
                                    (MODE == kGgDw ? 1u << 16 : 0u);
             uint32_t acc = 0, tacc = 0;
@@ -1040,7 +1044,7 @@ __global__ void __launch_bounds__((GgRole<MODE, CG, F32, EP>::kThreads), 1) gg_k
             for (int k0 = 0; k0 < nk; k0 += Role::KSUB) {
                 if (room == 0) {
                     if (!gg_wait(&sh->acc_empty[buf], free_ph, &sh->abort)) return false;
-                    tacc = tmem + (uint32_t)(buf * Cfg::BN);
+                    tacc = tmem + (uint32_t)(buf * Role::BN);
                     acc = 0;
                     room = Role::kPart;
                 }
@@ -1178,7 +1182,7 @@ __global__ void __launch_bounds__((GgRole<MODE, CG, F32, EP>::kThreads), 1) gg_k
                 return true;
             }
             if constexpr (Role::kIn) {
-                const uint32_t taddr = tmem + (uint32_t)(buf * Cfg::BN + c0) + ((uint32_t)((warp & 3) * 32) << 16);
+                const uint32_t taddr = tmem + (uint32_t)(buf * Role::BN + c0) + ((uint32_t)((warp & 3) * 32) << 16);
                 const int h = warp >> 2;
                 if (!gg_wait_warp(&sh->acc_full[buf], full_ph, &sh->abort)) return false;
                 tc_fence_after();
@@ -1202,7 +1206,7 @@ __global__ void __launch_bounds__((GgRole<MODE, CG, F32, EP>::kThreads), 1) gg_k
                         if (!wait()) return false;
                         const int rows = min(In::kRows, mine - c - i);
                         if constexpr (EP == kGgGluBack) glu_back_rows<In::kRows>(p, d + i, at(), row0 + c + i, rows, m, lane);
-                        if constexpr (EP == kGgSym) ns_sym_rows<In::kRows>(p, d + i, at(), e, r0 + i, m, lane, n0 > m0);
+                        if constexpr (EP == kGgSym) ns_sym_rows<In::kRows>(p, d + i, at(), e, r0 + i, m, lane, kMirror && n0 > m0);
                         if constexpr (EP == kGgAxpy) ns_axpy_rows<In::kRows>(p, d + i, at(), e, r0 + i, rows, m, lane);
                         if constexpr (EP == kGgResult) ns_result_rows<In::kRows>(p, d + i, at(), e, r0 + i, rows, m, lane);
                         done();
@@ -1219,32 +1223,33 @@ __global__ void __launch_bounds__((GgRole<MODE, CG, F32, EP>::kThreads), 1) gg_k
                 buf ^= 1;
                 if (buf == 0) full_ph ^= 1u;
                 return true;
-            }
-            uint32_t sum[Role::COLS / 32][32];  // the parts' sum
-            for (int k = 0; k < nk; k += kGgPartSteps) {
-                if (!gg_wait_warp(&sh->acc_full[buf], full_ph, &sh->abort)) return false;
-                tc_fence_after();
-                const uint32_t taddr = tmem + (uint32_t)(buf * Cfg::BN + c0) + ((uint32_t)((warp & 3) * 32) << 16);
-                if (mine > 0) gg_gather<Role::COLS>(taddr, sum, mine, k == 0);
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) {
-                    if (CG == 1)
-                        mbar_arrive(&sh->acc_empty[buf]);
-                    else
-                        mbar_arrive_cluster(&sh->acc_empty[buf], 0);
+            } else {
+                uint32_t sum[Role::COLS / 32][32];  // the parts' sum
+                for (int k = 0; k < nk; k += kGgPartSteps) {
+                    if (!gg_wait_warp(&sh->acc_full[buf], full_ph, &sh->abort)) return false;
+                    tc_fence_after();
+                    const uint32_t taddr = tmem + (uint32_t)(buf * Role::BN + c0) + ((uint32_t)((warp & 3) * 32) << 16);
+                    if (mine > 0) gg_gather<Role::COLS>(taddr, sum, mine, k == 0);
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) {
+                        if (CG == 1)
+                            mbar_arrive(&sh->acc_empty[buf]);
+                        else
+                            mbar_arrive_cluster(&sh->acc_empty[buf], 0);
+                    }
+                    buf ^= 1;
+                    if (buf == 0) full_ph ^= 1u;
                 }
-                buf ^= 1;
-                if (buf == 0) full_ph ^= 1u;
-            }
-            if constexpr (EP == kGgGlu) {
-                glu_store<Role::COLS, F32>(p, sum, row0, mine, m0 + (int)rank * MW + (warp & 3) * 16, lane);
+                if constexpr (EP == kGgGlu) {
+                    glu_store<Role::COLS, F32>(p, sum, row0, mine, m0 + (int)rank * MW + (warp & 3) * 16, lane);
+                } else {
+#pragma unroll
+                    for (int i = 0; i < Role::COLS / 32; ++i)
+                        if (32 * i < mine) gg_store32(sum[i], p.out, F32, row0 + 32 * i, min(32, mine - 32 * i), m, p.M);
+                }
                 return true;
             }
-#pragma unroll
-            for (int i = 0; i < Role::COLS / 32; ++i)
-                if (32 * i < mine) gg_store32(sum[i], p.out, F32, row0 + 32 * i, min(32, mine - 32 * i), m, p.M);
-            return true;
         });
     }
     __syncthreads();
