@@ -153,7 +153,7 @@ static int ns_plan(int E, int N, int K, int sms, NsPlan* q) {
     q->x = align_up(sizeof(uint16_t) * (size_t)q->group * q->m * q->n, 256);
     q->a = align_up(sizeof(uint16_t) * (size_t)q->group * q->m * q->m, 256);
     q->p = align_up(sizeof(float) * 3 * (size_t)q->group * q->parts, 256);
-    q->bytes = 3 * q->x + 2 * q->a + q->p;
+    q->bytes = 3 * q->x + 2 * q->a + q->p + 256;  // (the parts are aligned to 256)
     return MOE_OK;
 }
 
@@ -469,7 +469,7 @@ int moe_orthogonalize(const void* g, int g_dtype, int E, int N, int K, int steps
     MOE_REQ(workspace);
     if (sms < 2) return MOE_ERR_CUDA;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    unsigned char* ws = static_cast<unsigned char*>(workspace);
+    unsigned char* ws = reinterpret_cast<unsigned char*>(align_up(reinterpret_cast<uintptr_t>(workspace), 256));
     uint16_t* x[2] = {reinterpret_cast<uint16_t*>(ws), reinterpret_cast<uint16_t*>(ws + q.x)};
     uint16_t* low = reinterpret_cast<uint16_t*>(ws + 2 * q.x);
     void *A = ws + 3 * q.x, *B = ws + 3 * q.x + q.a;
@@ -485,6 +485,7 @@ int moe_orthogonalize(const void* g, int g_dtype, int E, int N, int K, int steps
         s.last[i].res_rows = N;
         s.last[i].res_cols = K;
         s.last[i].res_trans = trans;
+        s.last[i].res_sectors = K % 16 == 0 && aligned32(out);
     }
     if (!ok) return MOE_ERR_UNSUPPORTED;
     s.aa.status = dev_status;

@@ -77,6 +77,7 @@ struct GgParams {
     int early;       // the kernel behind this one touches nothing before its grid_dep_wait
     int rows;        // of every segment (offsets is then not read)
     int res_rows, res_cols, res_trans;  // the result's matrices: [E, res_rows, res_cols], transposed or not
+    int res_sectors;  // every sixteenth column of it lies on 32 bytes
     CUtensorMap zero[4];  // dw: boxes of 64 columns x 8, 4, 2 and 1 rows, for rows of zeros from behind x's end
     int32_t* status;
 };
@@ -122,8 +123,8 @@ template <int EP, bool NARROW = false>
 struct GgIn {
     static constexpr bool kOn = EP >= kGgGluBack;
     static constexpr int kParts = EP == kGgGluBack || NARROW ? 2 : 4, kRows = 16, kSlots = EP == kGgGluBack ? 3 : 2;
-    static constexpr int kPlane = kRows * 256;  // bytes
-    static constexpr int kBytes = kOn ? kParts * kSlots * 2 * kPlane : 0;
+    static constexpr int kPlane = kRows * 256, kSlot = kPlane * (EP == kGgSym ? 1 : 2);  // bytes
+    static constexpr int kBytes = kOn ? kParts * kSlots * kSlot : 0;
 };
 
 // Roles and limits by epilogue, over GgCfg's.  NARROW tiles of 32 columns are
@@ -736,6 +737,13 @@ __device__ __forceinline__ uint32_t gg_pack_f16(float first, float second) {
     return *reinterpret_cast<const uint32_t*>(&h);
 }
 
+// 32 bytes, a whole sector, in one store (32-byte aligned)
+__device__ __forceinline__ void st_v8(void* to, const uint32_t (&w)[8]) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(to), "r"(w[0]), "r"(w[1]), "r"(w[2]),
+                 "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+                 : "memory");
+}
+
 __device__ __forceinline__ float2 f16x2_to_f2(uint32_t u) { return __half22float2(*reinterpret_cast<const __half2*>(&u)); }
 
 // out = alpha product + beta in for ROWS rows of this lane's m, from row r of
@@ -765,7 +773,7 @@ __device__ __forceinline__ void ns_axpy_rows(const P& p, const float* d, const u
 // The same without the low parts of a symmetric product, less shift on the
 // diagonal, into rows of p.M fp16 values (a multiple of 16, as are the rows);
 // of a tile below the diagonal also into its mirror image, where a lane's
-// values lie side by side.
+// values lie side by side, 32 bytes.
 template <int ROWS, typename P>
 __device__ __forceinline__ void ns_sym_rows(const P& p, const float* d, const uint16_t* ins, int e, int r, int m, int lane,
                                             bool mirror) {
@@ -790,9 +798,8 @@ __device__ __forceinline__ void ns_sym_rows(const P& p, const float* d, const ui
         gg_put(to, w[j / 2], sel, there);
     }
     if (mirror && there) {
-        uint4* at = reinterpret_cast<uint4*>(out + ((size_t)e * p.rows + m) * M + r);
-#pragma unroll
-        for (int j = 0; j < ROWS / 8; ++j) at[j] = make_uint4(w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]);
+        static_assert(ROWS == 16, "a sector");
+        st_v8(out + ((size_t)e * p.rows + m) * M + r, w);
     }
 }
 
@@ -815,6 +822,11 @@ __device__ __forceinline__ void ns_result_rows(const P& p, const float* d, const
         if (m >= p.res_rows) return;
         uint16_t* to = out + ((size_t)e * p.res_rows + m) * p.res_cols + r;
         const int k = min(n, p.res_cols - r);
+        static_assert(ROWS == 16, "a sector");
+        if (k == ROWS && p.res_sectors) {
+            st_v8(to, w);
+            return;
+        }
 #pragma unroll
         for (int j = 0; j < ROWS; j += 8) {
             if (j + 8 <= k && p.res_cols % 8 == 0) {
@@ -1109,7 +1121,7 @@ __global__ void __launch_bounds__((GgRole<MODE, CG, F32, EP, NARROW>::kThreads),
                         if (row >= n) break;
                         if (!gg_wait(&sh->in_empty[h][r[h].s], r[h].ph ^ 1u, &sh->abort)) return false;
                         uint64_t* bar = &sh->in_full[h][r[h].s];
-                        const uint32_t to = smem_u32(ins) + (h * In::kSlots + r[h].s) * 2 * In::kPlane;
+                        const uint32_t to = smem_u32(ins) + (h * In::kSlots + r[h].s) * In::kSlot;
                         mbar_arrive_expect_tx(bar, p.planes * In::kPlane);
                         for (int i = 0; i < p.planes; ++i)
                             gg_load2<1>(to + i * In::kPlane, &p.tin[i], p.tin_at[i] + m, q0 + row, smem_u32(bar));
@@ -1191,7 +1203,7 @@ __global__ void __launch_bounds__((GgRole<MODE, CG, F32, EP, NARROW>::kThreads),
                     tmem_ld16(taddr + c, d);
                     auto wait = [&]() -> bool { return !p.planes || gg_wait_warp(&sh->in_full[h][in.s], in.ph, &sh->abort); };
                     auto at = [&]() {
-                        return reinterpret_cast<const uint16_t*>(ins + (h * In::kSlots + in.s) * 2 * In::kPlane) + (warp & 3) * 32;
+                        return reinterpret_cast<const uint16_t*>(ins + (h * In::kSlots + in.s) * In::kSlot) + (warp & 3) * 32;
                     };
                     auto done = [&]() {
                         if (!p.planes) return;

@@ -89,8 +89,6 @@ static int check_nvfp4(int G, int rows, int cols, int dtype) {
     return MOE_OK;
 }
 
-static bool aligned32(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 31u) == 0; }
-
 }  // namespace moe
 
 using namespace moe;
