@@ -387,6 +387,16 @@ __global__ void __launch_bounds__(MT) join_back_kernel(JoinParams p) {
 #pragma unroll
             for (int j = 0; j < 6; ++j) s[j] = __shfl_sync(0xffffffffu, sum, 4 * j);
         }
+        // the next token's inputs on their way into L2 meanwhile, a lane a row
+        if (warp == 0 && t + (int)gridDim.x < p.T) {
+            const size_t sx = (size_t)p.H * (p.x_f32 ? 4 : 2), sn = (size_t)p.H * (p.n_f32 ? 4 : 2), so = (size_t)p.H * (OF32 ? 4 : 2);
+            const size_t next = (size_t)t + gridDim.x;
+            if (r_next >= 0 && r_next < p.R)
+                bulk_prefetch_l2(static_cast<const unsigned char*>(p.o) + r_next * so, (uint32_t)so);
+            if (lane == 29 && p.pre) bulk_prefetch_l2(static_cast<const unsigned char*>(p.x) + next * sx, (uint32_t)sx);
+            if (lane == 30 && p.pre) bulk_prefetch_l2(static_cast<const unsigned char*>(p.dn) + next * sn, (uint32_t)sn);
+            if (lane == 31 && p.dy) bulk_prefetch_l2(static_cast<const unsigned char*>(p.dy) + next * sx, (uint32_t)sx);
+        }
         if (t != (int)blockIdx.x) write_dw(t - gridDim.x, parity ^ 1);
         const float n = 1.0f / (float)p.H;
         const float ny = 1.0f / sqrtf(s[0] * n + p.eps), my = ny * ny * ny * (s[1] * n);
