@@ -11,7 +11,8 @@ namespace moe {
 // for up to kGgvTok rows of one segment at a time.  Block (b, r) takes the
 // outputs 8b .. 8b + 7 of the rows r .. of a segment when r starts a group of
 // kGgvTok there.  Bound by the weights' bytes and the latency of one chain
-// offsets -> weights.
+// offsets -> weights: two rows of 1536 x 2048 on two experts take 10 us a call,
+// most of it on the host.
 template <int J>
 __global__ void __launch_bounds__(256) glu_gemv_kernel(const uint16_t* x, const uint16_t* gate_up, const int32_t* offsets,
                                                        int R, int I, int H, int E, void* h, int h_f32, uint16_t* gu,
