@@ -128,7 +128,8 @@ struct NsPlan {
     int m, n;        // rows and columns of X, padded
     int group;       // matrices that go through all steps together
     int parts;       // blocks that sum a matrix's squares
-    bool pairs, narrow;  // tiles of CTA pairs, tiles of 32 columns
+    bool pairs;      // tiles of CTA pairs
+    int narrow;      // tiles of 32 columns, 2: and split products
     size_t x, a, p;  // bytes of a group's X, of its A, of the sums
     size_t bytes;
 };
@@ -144,7 +145,8 @@ static int ns_plan(int E, int N, int K, int sms, NsPlan* q) {
     // narrow tiles while they leave no SM a second one of the symmetric products.  Measured, a product of the
     // chain with tiles of 128 and of 32 columns: one matrix of 390 x 515 6.7 and 4.6 us, 512 x 2048 8.8 and 7.3,
     // 768 x 2048 9.8 and 9.2, 1024 x 1024 8.9 and 10.2; four of 390 x 515 6.8 and 6.6, eight 7.8 and 9.5
-    q->narrow = (int64_t)E * ceil_div(q->m, 32) * ceil_div(q->m, 128) <= sms;
+    // Up to kNsSplitRows rows the products whose contraction that is are split (moe_ortho.cuh).
+    q->narrow = q->m <= kNsSplitRows ? 2 : (int64_t)E * ceil_div(q->m, 32) * ceil_div(q->m, 128) <= sms;
     q->group = E;
     q->parts = ceil_div(8 * sms, q->group);
     const int most = (int)(((size_t)N * K + 2047) / 2048);
@@ -153,7 +155,7 @@ static int ns_plan(int E, int N, int K, int sms, NsPlan* q) {
     q->x = align_up(sizeof(uint16_t) * (size_t)q->group * q->m * q->n, 256);
     q->a = align_up(sizeof(uint16_t) * (size_t)q->group * q->m * q->m, 256);
     q->p = align_up(sizeof(float) * 3 * (size_t)q->group * q->parts, 256);
-    q->bytes = 3 * q->x + 2 * q->a + q->p + 256;  // (the parts are aligned to 256)
+    q->bytes = (q->narrow == 2 ? 4 * q->x + 4 * q->a : 3 * q->x + 2 * q->a) + q->p + 256;  // (the parts are aligned to 256)
     return MOE_OK;
 }
 
@@ -163,34 +165,42 @@ struct NsProducts {
     GgParams xx[2], aa, bx[2], last[2];
 };
 
-static bool ns_params(const NsPlan& q, const void* w, const void* x, int cols, const void* in, void* low, void* out,
-                      bool sym, GgParams* p) {
+// A value in two fp16 buffers; low is nullptr where it is held in one.
+struct NsHalves {
+    uint16_t *high, *low;
+};
+
+// in: what the epilogue reads beside the product; split: into the product of both operands' halves.
+static bool ns_params(const NsPlan& q, NsHalves w, NsHalves x, int cols, NsHalves in, NsHalves out, bool split, bool sym,
+                      GgParams* p) {
     memset(p, 0, sizeof *p);
     p->rows = q.m;
-    p->low = low;
-    p->out = out;
+    p->low = out.low;
+    p->halves = split;
+    p->out = out.high;
     const uint64_t G = (uint64_t)q.group, R = G * q.m;
     bool ok;
     if (sym) {  // x [G m, cols] times its own rows
         p->M = q.m;
         p->C = cols;
-        ok = encode_map(&p->ta, w, 2, cols, q.m, G, 128);
+        ok = encode_map(&p->ta, w.high, 2, cols, q.m, G, 128) && (!split || encode_map(&p->ta_lo, w.low, 2, cols, q.m, G, 128));
     } else {  // x = B [G m, m], w = X [G, m, n]
         p->M = q.n;
         p->C = q.m;
         p->a_blocked = 1;
-        ok = encode_blocked(&p->ta, w, q.n, q.m, G);
+        ok = encode_blocked(&p->ta, w.high, q.n, q.m, G) && (!split || encode_blocked(&p->ta_lo, w.low, q.n, q.m, G));
     }
-    ok = ok && encode_map(&p->tb, x, 2, p->C, R, 0, kGgBoxN) && encode_map(&p->tb_all, x, 2, p->C, R, 0, 128);
-    if (in) {
+    ok = ok && encode_map(&p->tb, x.high, 2, p->C, R, 0, kGgBoxN) && encode_map(&p->tb_all, x.high, 2, p->C, R, 0, 128) &&
+         (!split || encode_map(&p->tb_lo, x.low, 2, p->C, R, 0, kGgBoxN));
+    if (in.high) {
         constexpr int rows = GgIn<kGgSym>::kRows;  // (the other products' as well)
-        ok = ok && encode_input(&p->tin[0], in, p->M, R, rows) && (!low || encode_input(&p->tin[1], low, p->M, R, rows));
-        p->planes = low ? 2 : 1;
+        ok = ok && encode_input(&p->tin[0], in.high, p->M, R, rows) && (!in.low || encode_input(&p->tin[1], in.low, p->M, R, rows));
+        p->planes = in.low ? 2 : 1;
     }
     return ok;
 }
 
-template <int CG, bool NARROW>
+template <int CG, int NARROW>
 static int ns_allow() {
     int rc = allow_smem(gg_kernel<kGgFwd, CG, false, kGgSym, NARROW>, kGgSmem);
     if (!rc) rc = allow_smem(gg_kernel<kGgDx, CG, false, kGgAxpy, NARROW>, kGgSmem);
@@ -198,7 +208,7 @@ static int ns_allow() {
 }
 
 // One product of E matrices, on no more SMs than it has tiles.
-template <int EP, int CG, bool NARROW>
+template <int EP, int CG, int NARROW>
 static int run_ns(GgParams& p, int E, float alpha, float beta, float shift, bool early, int sms, cudaStream_t st) {
     constexpr int MODE = EP == kGgSym ? kGgFwd : kGgDx;
     p.E = E;
@@ -213,12 +223,12 @@ static int run_ns(GgParams& p, int E, float alpha, float beta, float shift, bool
                                tiles * CG < sms ? (int)tiles * CG : sms, st);
 }
 
-template <int CG, bool NARROW>
+template <int CG, int NARROW>
 static int run_ns_steps(NsProducts& s, int E, int steps, float a, float b, float c, bool more, int sms, cudaStream_t st) {
     const float up = (float)(1 << kNsScaleLog2), down = 1.0f / up;
     for (int i = 0; i < steps; ++i) {
         // a + b A + c A A of A = S + A': one + lin A' + c A' A'
-        const float S = steps - i <= kNsShifted ? kNsShift : 0.0f, lin = b + 2.0f * c * S, one = a + b * S + c * S * S;
+        const float S = NARROW < 2 && steps - i <= kNsShifted ? kNsShift : 0.0f, lin = b + 2.0f * c * S, one = a + b * S + c * S * S;
         int rc = run_ns<kGgSym, CG, NARROW>(s.xx[i & 1], E, down * down, 0.0f, S, true, sms, st);
         if (!rc) rc = run_ns<kGgSym, CG, NARROW>(s.aa, E, c, lin, 0.0f, true, sms, st);
         if (!rc)
@@ -470,16 +480,29 @@ int moe_orthogonalize(const void* g, int g_dtype, int E, int N, int K, int steps
     if (sms < 2) return MOE_ERR_CUDA;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     unsigned char* ws = reinterpret_cast<unsigned char*>(align_up(reinterpret_cast<uintptr_t>(workspace), 256));
-    uint16_t* x[2] = {reinterpret_cast<uint16_t*>(ws), reinterpret_cast<uint16_t*>(ws + q.x)};
-    uint16_t* low = reinterpret_cast<uint16_t*>(ws + 2 * q.x);
-    void *A = ws + 3 * q.x, *B = ws + 3 * q.x + q.a;
-    float* parts = reinterpret_cast<float*>(ws + 3 * q.x + 2 * q.a);
+    auto take = [&](size_t bytes) {
+        void* p = ws;
+        ws += bytes;
+        return p;
+    };
+    auto halves = [&](size_t bytes, bool both) {
+        NsHalves h;
+        h.high = static_cast<uint16_t*>(take(bytes));
+        h.low = both ? static_cast<uint16_t*>(take(bytes)) : nullptr;
+        return h;
+    };
+    // X's low half is read where it is written, but for split products, which read it all over
+    const bool split = q.narrow == 2;
+    NsHalves x[2] = {halves(q.x, true), halves(q.x, split)};
+    if (!split) x[1].low = x[0].low;
+    const NsHalves A = halves(q.a, split), B = halves(q.a, split), none = {nullptr, nullptr};
+    float* parts = static_cast<float*>(take(q.p));
     const int f32 = g_dtype == MOE_DT_F32, trans = N > K;
     NsProducts s;
-    bool ok = ns_params(q, A, A, q.m, A, nullptr, B, true, &s.aa);
+    bool ok = ns_params(q, A, A, q.m, A, B, split, true, &s.aa);
     for (int i = 0; i < 2 && ok; ++i) {
-        ok = ns_params(q, x[i], x[i], q.n, nullptr, nullptr, A, true, &s.xx[i]) &&
-             ns_params(q, x[i], B, 0, x[i], low, x[i ^ 1], false, &s.bx[i]);
+        ok = ns_params(q, x[i], x[i], q.n, none, A, false, true, &s.xx[i]) &&
+             ns_params(q, x[i], B, 0, x[i], x[i ^ 1], split, false, &s.bx[i]);
         s.xx[i].status = s.bx[i].status = dev_status;
         s.last[i] = s.bx[i];
         s.last[i].res_rows = N;
@@ -489,7 +512,8 @@ int moe_orthogonalize(const void* g, int g_dtype, int E, int N, int K, int steps
     }
     if (!ok) return MOE_ERR_UNSUPPORTED;
     s.aa.status = dev_status;
-    if ((rc = q.narrow ? ns_allow<1, true>() : q.pairs ? ns_allow<2, false>() : ns_allow<1, false>())) return rc;
+    rc = q.narrow == 2 ? ns_allow<1, 2>() : q.narrow ? ns_allow<1, 1>() : q.pairs ? ns_allow<2, 0>() : ns_allow<1, 0>();
+    if (rc) return rc;
     const size_t each = (size_t)N * K;
     for (int e = 0; e < E; e += q.group) {
         const int G = E - e < q.group ? E - e : q.group;
@@ -502,13 +526,15 @@ int moe_orthogonalize(const void* g, int g_dtype, int E, int N, int K, int steps
         const int64_t tiles = (int64_t)G * ceil_div(cols, 64) * ceil_div(rows, 64);
         const int strip = tiles >= 16 * sms ? 256 : 64;
         rc = launch_pdl(ns_convert_kernel, dim3((unsigned)ceil_div(cols, strip), (unsigned)ceil_div(rows, 64), (unsigned)G), 256,
-                        0, st, from, f32, N, K, (const float*)parts, q.parts, eps, trans, x[0], low, q.m, q.n, strip);
+                        0, st, from, f32, N, K, (const float*)parts, q.parts, eps, trans, x[0].high, x[0].low, q.m, q.n,
+                        strip);
         if (rc) return rc;
         s.last[(steps - 1) & 1].out = out + each * e;
         const bool more = e + G < E;
-        rc = q.narrow  ? run_ns_steps<1, true>(s, G, steps, a, b, c, more, sms, st)
-             : q.pairs ? run_ns_steps<2, false>(s, G, steps, a, b, c, more, sms, st)
-                       : run_ns_steps<1, false>(s, G, steps, a, b, c, more, sms, st);
+        rc = q.narrow == 2 ? run_ns_steps<1, 2>(s, G, steps, a, b, c, more, sms, st)
+             : q.narrow    ? run_ns_steps<1, 1>(s, G, steps, a, b, c, more, sms, st)
+             : q.pairs     ? run_ns_steps<2, 0>(s, G, steps, a, b, c, more, sms, st)
+                           : run_ns_steps<1, 0>(s, G, steps, a, b, c, more, sms, st);
         if (rc) return rc;
     }
     return MOE_OK;

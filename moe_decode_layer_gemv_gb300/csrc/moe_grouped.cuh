@@ -76,7 +76,9 @@ struct GgParams {
     int planes, tin_at[2];
     // orthogonalisation: out = alpha product + beta in - shift 1
     float alpha, beta, shift;
-    void* low;       // B X: replaced by what fp16 leaves of out
+    void* low;       // receives what fp16 leaves of out
+    CUtensorMap ta_lo, tb_lo;  // split products: what fp16 left of the operands
+    int halves;      // high high + high low + low high, three products in one sum
     int early;       // the kernel behind this one touches nothing before its grid_dep_wait
     int rows;        // of every segment (offsets is then not read)
     int res_rows, res_cols, res_trans;  // the result's matrices: [E, res_rows, res_cols], transposed or not
@@ -122,18 +124,19 @@ constexpr int kGgInMax = 4;  // parts of the columns, and slots each, at most
 // operands: the gated unit's gradient of 65536 rows takes 205 us with 24 KB of
 // them, 188 with 32 and 48, 205 with 64, 225 with 96; eight or sixteen
 // epilogue warps make no difference there, as it waits for L2 by then.
-template <int EP, bool NARROW = false>
+template <int EP, int NARROW = 0>
 struct GgIn {
     static constexpr bool kOn = EP >= kGgGluBack;
     static constexpr int kParts = EP == kGgGluBack || NARROW ? 2 : 4, kRows = 16, kSlots = EP == kGgGluBack ? 3 : 2;
-    static constexpr int kPlane = kRows * 256, kSlot = kPlane * (EP == kGgSym ? 1 : 2);  // bytes
+    static constexpr int kPlane = kRows * 256, kSlot = kPlane * (EP == kGgSym && NARROW != 2 ? 1 : 2);  // bytes
     static constexpr int kBytes = kOn ? kParts * kSlots * kSlot : 0;
 };
 
 // Roles and limits by epilogue, over GgCfg's.  NARROW tiles of 32 columns are
 // for products too small to fill the GPU: an SM takes in some 100 GB/s of
-// operands, so that it is the number of SMs that counts (orthogonalisation).
-template <int MODE, int CG, bool F32, int EP, bool NARROW = false>
+// operands, so that it is the number of SMs that counts (orthogonalisation);
+// with NARROW = 2 operands and results may be in two fp16 values.
+template <int MODE, int CG, bool F32, int EP, int NARROW = 0>
 struct GgRole {
     static constexpr bool kIn = GgIn<EP, NARROW>::kOn;
     static constexpr int kInBytes = GgIn<EP, NARROW>::kBytes;
@@ -778,11 +781,11 @@ __device__ __forceinline__ void ns_axpy_rows(const P& p, const float* d, const u
     }
 }
 
-// The same without the low parts of a symmetric product, less shift on the
+// The same without (unless SPLIT) the low parts, of a symmetric product less shift on the
 // diagonal, into rows of p.M fp16 values (a multiple of 16, as are the rows);
 // of a tile below the diagonal also into its mirror image, where a lane's
 // values lie side by side, 32 bytes.
-template <int ROWS, typename P>
+template <int ROWS, bool SPLIT, typename P>
 __device__ __forceinline__ void ns_sym_rows(const P& p, const float* d, const uint16_t* ins, int e, int r, int m, int lane,
                                             bool mirror) {
     const int M = p.M, odd = lane & 1;
@@ -790,13 +793,16 @@ __device__ __forceinline__ void ns_sym_rows(const P& p, const float* d, const ui
     const bool there = m < M;
     uint16_t* out = static_cast<uint16_t*>(p.out);
     uint16_t* to = out + ((size_t)e * p.rows + r + odd) * M + (m - odd);
+    uint16_t* tl = SPLIT ? static_cast<uint16_t*>(p.low) + (to - out) : nullptr;
     uint32_t w[ROWS / 2];  // rows j and j + 1 of this lane's m
 #pragma unroll
     for (int j = 0; j < ROWS; j += 2, to += 2 * (size_t)M) {
         float v0 = p.alpha * d[j], v1 = p.alpha * d[j + 1];
         if (p.planes) {
-            v0 = fmaf(p.beta, in_f16(ins + lane, j), v0);
-            v1 = fmaf(p.beta, in_f16(ins + lane, j + 1), v1);
+            float f0 = in_f16(ins + lane, j), f1 = in_f16(ins + lane, j + 1);
+            if (SPLIT) f0 += in_f16(ins + ROWS * 128 + lane, j), f1 += in_f16(ins + ROWS * 128 + lane, j + 1);
+            v0 = fmaf(p.beta, f0, v0);
+            v1 = fmaf(p.beta, f1, v1);
         }
         if (!mirror) {
             v0 -= r + j == m ? p.shift : 0.0f;
@@ -804,6 +810,11 @@ __device__ __forceinline__ void ns_sym_rows(const P& p, const float* d, const ui
         }
         w[j / 2] = gg_pack_f16(v0, v1);
         gg_put(to, w[j / 2], sel, there);
+        if (SPLIT) {
+            const float2 t = f16x2_to_f2(w[j / 2]);
+            gg_put(tl, gg_pack_f16(v0 - t.x, v1 - t.y), sel, there);
+            tl += 2 * (size_t)M;
+        }
     }
     if (mirror && there) {
         static_assert(ROWS == 16, "a sector");
@@ -876,7 +887,7 @@ __device__ __forceinline__ void ns_result_rows(const P& p, const float* d, const
 // tiles.  Three roles run through the same tile sequence, each at its own
 // pace: the producer fills the ring, the MMA issuer accumulates tile d into
 // tensor-memory buffer d mod 2, the epilogue warps read the other buffer out.
-template <int MODE, int CG, bool F32, int EP = kGgStore, bool NARROW = false>
+template <int MODE, int CG, bool F32, int EP = kGgStore, int NARROW = 0>
 __global__ void __launch_bounds__((GgRole<MODE, CG, F32, EP, NARROW>::kThreads), 1) gg_kernel(const __grid_constant__ GgParams p) {
     using Cfg = GgCfg<MODE, CG, F32>;
     extern __shared__ __align__(1024) unsigned char gg_smem_raw[];
@@ -990,15 +1001,15 @@ __global__ void __launch_bounds__((GgRole<MODE, CG, F32, EP, NARROW>::kThreads),
         const uint32_t bars = CG == 1 ? smem_u32(sh->full) : cluster_addr(sh->full, 0);
         if (gg_elect()) {
             walk([&](int e, int q0, int n, int n0, int m0, int len) -> bool {
-                const int nk = (len + 63) / 64;
+                const int nk = (len + 63) / 64, nks = NARROW == 2 && p.halves ? 3 * nk : nk;
                 // rows of B that this CTA holds (forward, dx), in whole boxes
                 const int rows = MODE == kGgDw ? 128 : (n + kGgBoxN * CG - 1) / (kGgBoxN * CG) * kGgBoxN;
                 const uint32_t bytes = CG * (kGgTile + (uint32_t)rows * 128u);
                 const int am = m0 + (int)rank * MW, bn = (MODE == kGgDw ? n0 : q0) + (int)rank * rows;
-                for (int k0 = 0; k0 < nk; k0 += Role::KSUB) {
+                for (int k0 = 0; k0 < nks; k0 += Role::KSUB) {
                     if (!gg_wait(&sh->empty[r.s], r.ph ^ 1u, &sh->abort)) return false;
                     const uint32_t st = ring_at + r.s * stage_bytes, bar = bars + r.s * 8u;
-                    const int ke = min(Role::KSUB, nk - k0);
+                    const int ke = min(Role::KSUB, nks - k0);
                     // dw: the stage that a segment ends in, if not with a whole MMA, lands on
                     // each CTA's own barrier and is cleared there before it counts as full
                     const bool tail = MODE == kGgDw && gg_ragged(len - k0 * 64);
@@ -1014,14 +1025,17 @@ __global__ void __launch_bounds__((GgRole<MODE, CG, F32, EP, NARROW>::kThreads),
                     for (int u = 0; u < Role::KSUB; ++u) {
                         if (u >= ke) break;
                         const uint32_t sa = st + u * kGgTile, sb = st + b_off + u * b_tile;
-                        const int c = (k0 + u) * 64;
+                        const int part = NARROW == 2 ? (k0 + u) / nk : 0;  // of a split product
+                        const int c = (k0 + u - part * nk) * 64;
+                        const CUtensorMap* const ta = part == 2 ? &p.ta_lo : &p.ta;
+                        const CUtensorMap* const tb = part == 1 ? &p.tb_lo : &p.tb;
                         if (EP == kGgGlu) {
                             gg_load5<CG>(sa, &p.ta, c, 0, 0, am >> 3, e, bar);
                         } else if (MODE == kGgFwd) {
-                            gg_load3<CG>(sa, &p.ta, c, am, e, bar);
+                            gg_load3<CG>(sa, ta, c, am, e, bar);
                         } else if (MODE == kGgDx) {
                             if (p.a_blocked) {
-                                gg_load4<CG>(sa, &p.ta, 0, c, am >> 6, e, bar);
+                                gg_load4<CG>(sa, ta, 0, c, am >> 6, e, bar);
                             } else {
                                 gg_load3<CG>(sa, &p.ta, am, c, e, bar);
                                 gg_load3<CG>(sa + 8192, &p.ta, am + 64, c, e, bar);
@@ -1037,7 +1051,7 @@ __global__ void __launch_bounds__((GgRole<MODE, CG, F32, EP, NARROW>::kThreads),
                         } else if (rows == 128) {
                             gg_load2<CG>(sb, &p.tb_all, c, bn, bar);
                         } else {
-                            for (int i = 0; i < rows; i += kGgBoxN) gg_load2<CG>(sb + i * 128, &p.tb, c, bn + i, bar);
+                            for (int i = 0; i < rows; i += kGgBoxN) gg_load2<CG>(sb + i * 128, tb, c, bn + i, bar);
                         }
                     }
                     r.next(S);
@@ -1055,7 +1069,7 @@ __global__ void __launch_bounds__((GgRole<MODE, CG, F32, EP, NARROW>::kThreads),
         uint32_t tails = 0;    // parity of each stage's next use as a segment's end
         const uint32_t ring_at = smem_u32(ring);
         if (rank == 0 && gg_elect()) walk([&](int e, int q0, int n, int n0, int m0, int len) -> bool {
-            const int nk = (len + 63) / 64;
+            const int nk = ((len + 63) / 64) * (NARROW == 2 && p.halves ? 3 : 1);
             const int npad = MODE == kGgDw ? Role::BN : (n + kGgBoxN * CG - 1) / (kGgBoxN * CG) * (kGgBoxN * CG);
             const uint32_t idesc = (EP >= kGgSym ? umma_idesc_f16(Cfg::BM, npad) : umma_idesc_bf16(Cfg::BM, npad)) | (MODE != kGgFwd ? 1u << 15 : 0u) |
                                    (MODE == kGgDw ? 1u << 16 : 0u);
@@ -1226,7 +1240,7 @@ __global__ void __launch_bounds__((GgRole<MODE, CG, F32, EP, NARROW>::kThreads),
                         if (!wait()) return false;
                         const int rows = min(In::kRows, mine - c - i);
                         if constexpr (EP == kGgGluBack) glu_back_rows<In::kRows>(p, d + i, at(), row0 + c + i, rows, m, lane);
-                        if constexpr (EP == kGgSym) ns_sym_rows<In::kRows>(p, d + i, at(), e, r0 + i, m, lane, kMirror && n0 > m0);
+                        if constexpr (EP == kGgSym) ns_sym_rows<In::kRows, NARROW == 2>(p, d + i, at(), e, r0 + i, m, lane, kMirror && n0 > m0);
                         if constexpr (EP == kGgAxpy) ns_axpy_rows<In::kRows>(p, d + i, at(), e, r0 + i, rows, m, lane);
                         if constexpr (EP == kGgResult) ns_result_rows<In::kRows>(p, d + i, at(), e, r0 + i, rows, m, lane);
                         done();

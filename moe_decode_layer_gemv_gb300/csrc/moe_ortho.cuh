@@ -16,7 +16,11 @@
 // since most eigenvalues of A are near 1 by then and b A + c A A several times
 // as large as what is left of it, and its roundings too (random 300 x 900
 // matrices: 1.7e-3 without, 1.0e-3 so; earlier it would undo the above).  The
-// bf16 result's own rounding is 1.7e-3.  X carries a factor of 2^8, which keeps the
+// bf16 result's own rounding is 1.7e-3.  Short sides average over few
+// roundings (20 x 300: 2.2e-3), and cost little: up to 96 rows A and B too are
+// held in two values, and the products that contract over them, A A and B X,
+// take three terms (high high + high low + low high) and no shift.  20 x 300
+// then end 3.8e-4 off, 16 x 16 1.1e-3, of X's rounding in X X^T alone.  X carries a factor of 2^8, which keeps the
 // entries of the largest matrices (2^-14 on average at 16384 x 16384) out of
 // fp16's subnormals; a single entry of 1 is still far from 65504.
 //
@@ -38,6 +42,7 @@ namespace moe {
 constexpr int kNsScaleLog2 = 8;
 constexpr float kNsShift = 0.5f;
 constexpr int kNsShifted = 2;  // last steps with the shift
+constexpr int kNsSplitRows = 96;
 constexpr int kNsParts = 64;  // blocks that sum one matrix's squares, at most
 
 __device__ __forceinline__ float ns_value(const void* g, bool f32, size_t i) {

@@ -35,9 +35,15 @@ def _recurrence(g, steps, coeffs, eps, half):
     tall = x.shape[-2] > x.shape[-1]
     x = x.mT if tall else x
     x = two(x / (x.flatten(-2).norm(dim=-1).view(*x.shape[:-2], 1, 1) + eps))
+    # (a short side's A and B are held in 22 bits, and X rounded for X X^T alone: exact here but for that)
+    short = x.shape[-2] <= 96
     for i in range(steps):
-        s = 0.5 if steps - i <= 2 else 0.0
+        s = 0.5 if steps - i <= 2 and not short else 0.0
         h = r(x, UP)
+        if half and short:
+            m = h @ h.mT
+            x = two(a * x + (b * m + c * (m @ m)) @ x)
+            continue
         m = r(h @ h.mT - s * torch.eye(x.shape[-2], dtype=torch.float64, device=DEV), 1.0)
         x = (a + b * s + c * s * s) * x + r((b + 2 * c * s) * m + c * (m @ m), 1.0) @ h
         x = two(x) if i + 1 < steps else x
