@@ -3,21 +3,22 @@
 
 Tolerance: the kernel rounds X (which it carries in two fp16 values), A' = X X^T
 (in the last two steps less 1/2) and B, what b A + c A A then comes to, to fp16
-for its products, half a step (2^-12) a value; how far that carries depends on the matrix, so the recurrence is also run in 64 bits with these
-roundings, and its distance from the exact one is counted twice (once for the
-roundings, once for those that the fp32 sums decide the other way).  It has to
-stay below 2^-6 of the result itself, what one value a matrix may come to, where
-nothing averages.  With X' / X at least 0.68, |A| at most 1.3, |B| at most 2.85
-(b^2 / 4c) and |A (b + 2 c A)| at most 0.85, 2^-12 of X count 2 * 0.85 / 0.68
-times through A and 2.85 / 0.68 times through B X, those of A 0.85 / 0.68 and
-those of B 2.85 / 0.68 times: 12.2 2^-12 a step, below 2^-8; four of five steps
-deal with values that large, each passing on what came before at most as it
-is.  Values of X
+for its products, half a step (2^-12) a value; with a short side of up to 96 it
+rounds X alone, and for X X^T alone.  How far that carries depends on the
+matrix, so the recurrence is also run in 64 bits with these roundings, and its
+distance from the exact one is counted twice (once for the roundings, once for
+those that the fp32 sums decide the other way).  It has to stay below 2^-6 of
+the result itself, what one value a matrix may come to, where nothing averages.
+With X' / X at least 0.68, |A| at most 1.3, |B| at most 2.85 (b^2 / 4c) and
+|A (b + 2 c A)| at most 0.85, 2^-12 of X count 2 * 0.85 / 0.68 times through A
+and 2.85 / 0.68 times through B X, those of A 0.85 / 0.68 and those of B 2.85 /
+0.68 times: 12.2 2^-12 a step, below 2^-8; four of five steps deal with values
+that large, each passing on what came before at most as it is.  Values of X
 below fp16's normal ones are off by up to 2^-25 absolutely, 2^-33 of X without
 its factor 2^8, and a step enlarges what is that small by |a| at most: sqrt(N K)
 2^-33 (1 + |a|)^steps of 2-norm beside the rest, which counts where eps is all
-that a matrix is divided by.  The result's own rounding to bf16 adds half a step, 2^-8
-of each value.  Distances are 2-norms of whole matrices."""
+that a matrix is divided by.  The result's own rounding to bf16 adds half a
+step, 2^-8 of each value.  Distances are 2-norms of whole matrices."""
 import pytest
 import torch
 
