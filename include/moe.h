@@ -392,7 +392,8 @@ int moe_grouped_glu(const uint16_t* x, const uint16_t* gate_up, const int32_t* o
  * dgu [R, 2I] and h [R, I] bf16.  The rest of the block's backward pass is
  * moe_grouped_gemm_dx(dgu, gate_up), moe_grouped_gemm_dw(dgu, x) and
  * moe_grouped_gemm_dw(dy, h): h is made again here, so that the forward pass
- * need not keep it.  dgu may not overlap gu (the same address is refused).  dh
+ * need not keep it.  dgu and h may not overlap gu or dy (dgu at gu's address is
+ * refused).  dh
  * is one fp32 sum, whose additions (one for 16 terms) truncate: a sum of one
  * sign loses up to 7.4e-5 at H = 16384, 2 % of a bf16 result's half step.
  * Otherwise as moe_grouped_glu.
