@@ -245,9 +245,9 @@ __global__ void __launch_bounds__(MT) join_kernel(JoinParams p) {
 
 // ---------------------------------------------------------------- backward
 // With d the gradient of y (a = dn pre):
-//   d  = dy + rms(y) a - y rms(y)^3 mean(a y)        dx = d
+//   d  = dy + rms(y) a - (y rms(y)) rms(y) (rms(y) mean(a y))        dx = d
 //   g  = scale d (the gradient of b);  with a norm behind the block, c = g post:
-//   dz = rms(z) c - z rms(z)^3 mean(c z), else g
+//   dz = rms(z) c - (z rms(z)) rms(z) (rms(z) mean(c z)), else g
 //   do[pos_j] = w_j dz,  dw_j = <dz, o[pos_j]>
 //   dpre = sum_t dn y rms(y),  dscale = sum_t d b,  dpost = sum_t g z rms(z)
 // With f = scale post, the sums of c z come from those of dy f z, a f z and y f z:
@@ -404,10 +404,11 @@ __global__ void __launch_bounds__(MT) join_back_kernel(JoinParams p) {
             if (lane == 31 && p.dy) bulk_prefetch_l2(static_cast<const unsigned char*>(p.dy) + next * sx, (uint32_t)sx);
         }
         if (t != (int)blockIdx.x) write_dw(t - gridDim.x, parity ^ 1);
+        // (factors in the order that keeps them within fp32's range wherever the rows and their squares' sums are)
         const float n = 1.0f / (float)p.H;
-        const float ny = 1.0f / sqrtf(s[0] * n + p.eps), my = ny * ny * ny * (s[1] * n);
+        const float ny = 1.0f / sqrtf(s[0] * n + p.eps), my = ny * (ny * (s[1] * n));
         const float nz = 1.0f / sqrtf(s[2] * n + p.eps);
-        const float mz = nz * nz * nz * ((s[3] + (p.pre ? ny * s[4] - my * s[5] : 0.0f)) * n);
+        const float mz = nz * (nz * ((s[3] + (p.pre ? ny * (s[4] - my * s[5]) : 0.0f)) * n));
         float dots[MOE_MAX_TOPK] = {};
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
@@ -427,8 +428,9 @@ __global__ void __launch_bounds__(MT) join_back_kernel(JoinParams p) {
                 vector8(p.pre, v, f);
 #pragma unroll
                 for (int c = 0; c < 8; ++c) {
+                    y[c] *= ny;
                     d[c] += ny * (a[c] * f[c]) - y[c] * my;
-                    f[c] = a[c] * y[c] * ny;
+                    f[c] = a[c] * y[c];
                 }
                 add8(c_pre, nvec, v, f);
             }
@@ -452,8 +454,9 @@ __global__ void __launch_bounds__(MT) join_back_kernel(JoinParams p) {
             if (p.post) {
 #pragma unroll
                 for (int c = 0; c < 8; ++c) {
-                    f[c] = d[c] * (z[i][c] * nz);
-                    d[c] = nz * (d[c] * q[c]) - z[i][c] * mz;
+                    const float hat = z[i][c] * nz;
+                    f[c] = d[c] * hat;
+                    d[c] = nz * (d[c] * q[c]) - hat * mz;
                 }
                 add8(c_post, nvec, v, f);
             }

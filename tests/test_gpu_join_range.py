@@ -1,0 +1,59 @@
+"""Where the join's gradients could leave fp32's range or precision although
+their results do not: rows of any magnitude, an eps next to nothing.
+
+Tolerances and formulas as in test_gpu_join.py, where not said otherwise."""
+import pytest
+import torch
+
+import test_gpu_join as join
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda"
+F32, BF16 = torch.float32, torch.bfloat16
+NAMES = ("dx", "do", "dw", "dpost", "dscale", "dpre")
+
+# a vector a thread with its rows kept, and several, read again; blocks of several warps and of one
+SHAPES = [(9, 3, 136), (70, 2, 2056), (5, 4, 8200)]
+
+
+@pytest.mark.parametrize("T,k,H", SHAPES)
+@pytest.mark.parametrize("p,q", [(47, 0), (-47, 0), (0, 47), (0, -47), (47, -47), (-47, 47), (40, 40), (-40, -40)])
+def test_rows_of_any_magnitude(cuda_lib, T, k, H, p, q):
+    """Without eps the gradients of rows 2^p (the stream) and 2^q (the block's)
+    times as large are the same bits times a power of two: all operations
+    scale, as long as nothing leaves fp32's range.  Sums of squares reach
+    2^(2 |p|) times e^8 H, below 2^120; a gradient 2^-(p + q) times a few
+    2^-30, above 2^-120."""
+    c = join._case(T, k, H, F32, F32, F32)
+    c["eps"], c["dy"] = 0.0, None
+    want = dict(zip(NAMES, join._call_back(cuda_lib, c)))
+    c["x"], c["o"] = c["x"] * 2.0 ** p, c["o"] * 2.0 ** q
+    got = dict(zip(NAMES, join._call_back(cuda_lib, c)))
+    # dx ~ 1 / y; do ~ dx / o, dw ~ dx, dpost and dscale ~ dx (the norm takes o's magnitude away), dpre ~ 1
+    for n, e in (("dx", -p), ("do", -p - q), ("dw", -p), ("dpost", -p), ("dscale", -p), ("dpre", 0)):
+        assert bool(torch.isfinite(want[n]).all()) and torch.equal(got[n], want[n] * 2.0 ** e), n
+
+
+@pytest.mark.parametrize("T,k,H", SHAPES)
+@pytest.mark.parametrize("p", [47, 30])
+def test_large_rows_match_64_bits(cuda_lib, T, k, H, p):
+    c = join._case(T, k, H, F32, F32, F32)
+    c["x"], c["o"] = c["x"] * 2.0 ** p, c["o"] * 2.0 ** p
+    join._check(join._call(cuda_lib, c), c)
+    c["dy"] = c["dy"] * 2.0 ** -p  # (as large as the norm's part)
+    join._check_back(join._call_back(cuda_lib, c), c)
+
+
+@pytest.mark.parametrize("T,k,H", SHAPES)
+@pytest.mark.parametrize("eps", [1e-20, 1e-30, 1e-36])
+def test_rows_of_zeros_beside_a_tiny_eps(cuda_lib, monkeypatch, T, k, H, eps):
+    """1 / sqrt(eps) is within fp32's range, its cube is not; where a row is
+    zero the cube counts for nothing.  dn is small, since dx is 1 / sqrt(eps)
+    times as large."""
+    monkeypatch.setattr(join, "EPS", float(torch.tensor(eps, dtype=F32)))
+    c = join._case(T, k, H, F32, F32, F32)
+    c["eps"], c["dn"] = eps, c["dn"] * eps ** 0.5
+    c["o"][c["pos"][1].long()] = 0
+    c["x"][2] = 0
+    join._check(join._call(cuda_lib, c), c)
+    join._check_back(join._call_back(cuda_lib, c), c)
