@@ -417,7 +417,9 @@ int moe_grouped_glu_backward(const uint16_t* dy, const uint16_t* down, const uin
  * [T, k] fp32 (NULL: ones), k <= MOE_MAX_TOPK; post, scale, pre [H] fp32
  * (scale NULL: the number scale_all); eps in [0, 1].  y [T, H] of x's type
  * (may alias x), n [T, H] (n_dtype).  o NULL: the norm of x alone (no y).
- * Sums in fp32; n is made from y before it is rounded.  A row outside
+ * Sums in fp32; n is made from y before it is rounded.  With eps = 0 the norm
+ * of a row whose squares' mean is 0 in fp32 is zeros, as is its gradient (a
+ * token without rows passes the stream on).  A row outside
  * [-1, R) counts as dropped and sets MOE_DEV_BAD_ROUTE.  H a multiple of 8 in
  * [8, MOE_MAX_DIM], T and R at most MOE_MAX_ROWS.
  */

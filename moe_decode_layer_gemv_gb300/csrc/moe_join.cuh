@@ -133,6 +133,11 @@ __device__ __forceinline__ void token_sum(float (&v)[N], float* buf) {
     for (int i = 0; i < N; ++i) v[i] = warp_sum(lane < warps ? mine[i * 32 + lane] : 0.0f);
 }
 
+// 1 / sqrt of a mean square with eps, and 0 where that is nothing (eps = 0 and
+// a row of zeros, a token's without rows for instance): the norm of zeros is
+// zeros, and so is its gradient.
+__device__ __forceinline__ float norm_factor(float v) { return v == 0.0f ? 0.0f : 1.0f / sqrtf(v); }
+
 // The rows and weights of a token's routes; a row of -1 is none.
 __device__ __forceinline__ void token_routes(const JoinParams& p, int t, bool valid, int (&row)[MOE_MAX_TOPK],
                                              float (&w)[MOE_MAX_TOPK]) {
@@ -202,7 +207,7 @@ __global__ void __launch_bounds__(MT) join_kernel(JoinParams p) {
     float r = 1.0f;
     if (p.post) {
         token_sum(s, buf[0]);
-        r = 1.0f / sqrtf(s[0] / (float)p.H + p.eps);
+        r = norm_factor(s[0] / (float)p.H + p.eps);
     }
     s[0] = 0.0f;
 #pragma unroll
@@ -230,7 +235,7 @@ __global__ void __launch_bounds__(MT) join_kernel(JoinParams p) {
     }
     if (!p.pre) return;
     token_sum(s, buf[1]);
-    r = 1.0f / sqrtf(s[0] / (float)p.H + p.eps);
+    r = norm_factor(s[0] / (float)p.H + p.eps);
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
         const int v = threadIdx.x + i * blockDim.x;
@@ -406,8 +411,8 @@ __global__ void __launch_bounds__(MT) join_back_kernel(JoinParams p) {
         if (t != (int)blockIdx.x) write_dw(t - gridDim.x, parity ^ 1);
         // (factors in the order that keeps them within fp32's range wherever the rows and their squares' sums are)
         const float n = 1.0f / (float)p.H;
-        const float ny = 1.0f / sqrtf(s[0] * n + p.eps), my = ny * (ny * (s[1] * n));
-        const float nz = 1.0f / sqrtf(s[2] * n + p.eps);
+        const float ny = norm_factor(s[0] * n + p.eps), my = ny * (ny * (s[1] * n));
+        const float nz = norm_factor(s[2] * n + p.eps);
         const float mz = nz * (nz * ((s[3] + (p.pre ? ny * (s[4] - my * s[5]) : 0.0f)) * n));
         float dots[MOE_MAX_TOPK] = {};
 #pragma unroll

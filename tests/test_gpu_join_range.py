@@ -1,5 +1,6 @@
 """Where the join's gradients could leave fp32's range or precision although
-their results do not: rows of any magnitude, an eps next to nothing.
+their results do not: rows of any magnitude, an eps next to nothing, an eps of
+nothing with rows of nothing.
 
 Tolerances and formulas as in test_gpu_join.py, where not said otherwise."""
 import pytest
@@ -57,3 +58,52 @@ def test_rows_of_zeros_beside_a_tiny_eps(cuda_lib, monkeypatch, T, k, H, eps):
     c["x"][2] = 0
     join._check(join._call(cuda_lib, c), c)
     join._check_back(join._call_back(cuda_lib, c), c)
+
+
+@pytest.mark.parametrize("T,k,H", SHAPES)
+def test_tokens_without_rows_and_without_eps(cuda_lib, monkeypatch, T, k, H):
+    """A token whose routes are all dropped passes the stream on and adds
+    nothing to the sums, with eps = 0 too (the norm of nothing is nothing)."""
+    monkeypatch.setattr(join, "EPS", 0.0)
+    c = join._case(T, k, H, F32, F32, F32)
+    c["eps"] = 0.0
+    c["pos"][1], c["pos"][T - 1] = -1, -1
+    keep = torch.ones(T, dtype=torch.bool, device=DEV)
+    keep[1] = keep[T - 1] = False
+    there = {n: c[n][keep].contiguous() for n in ("x", "dy", "dn", "pos", "w")}
+    y, n = join._call(cuda_lib, c)
+    assert torch.equal(y[~keep], c["x"][~keep])
+    alone = cuda_lib.combine_norm(c["x"][~keep].contiguous(), pre=c["pre"], eps=0.0, n_dtype=F32)[1]
+    assert torch.equal(n[~keep], alone)
+    sub = {**c, **there}
+    join._check((y[keep], n[keep]), sub)
+    got, want = dict(zip(NAMES, join._call_back(cuda_lib, c))), join._backward(sub)
+    for m in ("dpost", "dscale"):
+        join._near(got[m], *want[m])
+    join._near_rows(got["dx"][keep], *want["dx"])
+    assert bool((got["dw"][~keep] == 0).all())
+    stream = join._backward(dict(c, o=None))
+    join._near(got["dpre"], *stream["dpre"])
+    join._near_rows(got["dx"][~keep], *(t[~keep] for t in stream["dx"]))
+
+
+@pytest.mark.parametrize("T,k,H", SHAPES)
+def test_rows_of_zeros_without_eps(cuda_lib, T, k, H):
+    """0 / 0 counts as 0: the norm of a row of zeros is zeros, and so is its gradient."""
+    c = join._case(T, k, H, F32, F32, F32)
+    c["eps"] = 0.0
+    clean, back = join._call(cuda_lib, c), join._call_back(cuda_lib, c)
+    rows = c["pos"][1].long()
+    c["o"][rows] = 0
+    c["x"][2] = 0
+    c["x"][1] = 0
+    y, n = join._call(cuda_lib, c)
+    assert bool((y[1] == 0).all()) and bool((n[1] == 0).all()) and bool(torch.isfinite(n).all())
+    keep = torch.ones(T, dtype=torch.bool, device=DEV)
+    keep[1] = keep[2] = False
+    assert torch.equal(n[keep], clean[1][keep])
+    got = join._call_back(cuda_lib, c)
+    assert all(bool(torch.isfinite(t).all()) for t in got)
+    assert torch.equal(got[0][1], c["dy"][1]) and torch.equal(got[0][2], c["dy"][2])
+    assert bool((got[1][rows] == 0).all()) and bool((got[2][1] == 0).all())
+    assert torch.equal(got[0][keep], back[0][keep]) and torch.equal(got[2][keep], back[2][keep])
