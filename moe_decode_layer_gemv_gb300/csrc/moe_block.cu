@@ -106,11 +106,9 @@ static int join_back_grid(int T, int H, int sums, int sms) {
 
 template <bool OF32, int NV>
 static int launch_join_back(const JoinParams& p, int grid, cudaStream_t st) {
-    const size_t smem = (size_t)p.sums * p.H * 4;
     // (with the kernel's static part 48 KB are passed earlier)
-    const int rc = smem > 32 * 1024 ? to_status(cudaFuncSetAttribute(
-                                          join_back_kernel<OF32, NV, 512>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem))
-                                    : MOE_OK;
+    const size_t smem = (size_t)p.sums * p.H * 4;
+    const int rc = smem > 32 * 1024 ? allow_smem(join_back_kernel<OF32, NV, 512>, 3 * MOE_MAX_DIM * 4) : MOE_OK;
     return rc ? rc : launch_pdl(join_back_kernel<OF32, NV, 512>, (unsigned)grid, join_threads(p.H, NV), smem, st, p);
 }
 

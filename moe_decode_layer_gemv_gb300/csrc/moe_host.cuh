@@ -9,6 +9,7 @@
 #include <string.h>
 
 #include <atomic>
+#include <mutex>
 
 #include "moe.h"
 
@@ -64,10 +65,19 @@ inline int launch_pdl(K kernel, dim3 grid, dim3 block, size_t smem, cudaStream_t
     return launch_ex(cfg, kernel, args...);
 }
 
-// dynamic shared memory above 48 KB needs an opt-in per kernel and device
+// Dynamic shared memory above 48 KB needs an opt-in per kernel and device.  The
+// limit is raised and never lowered: another host thread may have raised it for
+// its own launch of the same kernel, which is yet to come (the query takes the
+// 0.2 us that the setting would).
 template <typename K>
 inline int allow_smem(K kernel, size_t bytes) {
     if (bytes <= 48 * 1024) return MOE_OK;
+    static std::mutex lock;  // (one for all kernels of a type)
+    std::lock_guard<std::mutex> hold(lock);
+    cudaFuncAttributes a;
+    const cudaError_t e = cudaFuncGetAttributes(&a, kernel);
+    if (e != cudaSuccess) return to_status(e);
+    if (a.maxDynamicSharedSizeBytes >= (int)bytes) return MOE_OK;
     return to_status(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes));
 }
 
