@@ -459,8 +459,8 @@ int moe_combine_norm_backward(const void* dy, const void* dn, int n_dtype, const
  * fp32 sums: A (in the last two steps A - 1/2, with what follows from it) and b
  * A + c A A are rounded to fp16 in between, within half a step, 2^-12, of each
  * value (where the shorter side is at most 96 to 22 bits); X is carried in 22
- * bits and rounded to fp16 for the products (up to 96: for X X^T).  The norm of any finite matrix is exact to
- * fp32's rounding, without overflow.  Values of X below 2^-33 are lost
+ * bits and rounded to fp16 for the products (up to 96: for X X^T).  The norm of any finite matrix is within
+ * 2^-19 of itself, without overflow.  Values of X below 2^-33 are lost
  * (a matrix far smaller than eps).  A matrix with a NaN or an infinity becomes
  * NaN, the others are not affected; a zero matrix stays zero (with eps > 0).  The coefficients lie in [-16, 16]; such as let X grow past
  * fp16's range overflow to infinities.  1 <= steps <= MOE_MAX_NS_STEPS, N and

@@ -55,21 +55,40 @@ __device__ __forceinline__ float ns_value(const void* g, bool f32, size_t i) {
 
 // Sums of squares that neither overflow nor underflow (Blue 1978): values
 // beyond 2^48 are summed times 2^-80, those below 2^-48 times 2^80.
-// parts [E, gridDim.x, 3].
+// parts [E, gridDim.x, 3].  A thread adds up 32 squares at a time and carries
+// what the addition of such a sum to the others rounds off (Knuth's two-sum):
+// 16384 one after the other, as many as there are in the largest matrices, would be off by
+// up to 2^-12 where the values are alike, 2.4e-4.  45 additions at most remain
+// (32, five within a warp and eight across the block), 2^-19 of the norm.
+struct NsSum {
+    float s[3] = {0.0f, 0.0f, 0.0f}, run[3] = {0.0f, 0.0f, 0.0f}, left[3] = {0.0f, 0.0f, 0.0f};
+    __device__ __forceinline__ void add(float x) {
+        const float a = fabsf(x);
+        const float big = a > 0x1p48f ? x * 0x1p-80f : 0.0f, tiny = a < 0x1p-48f ? x * 0x1p80f : 0.0f;
+        const float mid = a > 0x1p48f || a < 0x1p-48f ? 0.0f : x;  // (a NaN goes here)
+        run[0] = fmaf(big, big, run[0]);
+        run[1] = fmaf(mid, mid, run[1]);
+        run[2] = fmaf(tiny, tiny, run[2]);
+    }
+    __device__ __forceinline__ void put_aside() {
+#pragma unroll
+        for (int j = 0; j < 3; ++j) {
+            const float t = s[j] + run[j], b = t - s[j];
+            left[j] += (s[j] - (t - b)) + (run[j] - b);
+            s[j] = t;
+            run[j] = 0.0f;
+        }
+    }
+    // (an infinite sum leaves no number behind, and stands for itself)
+    __device__ __forceinline__ float total(int j) const { return isfinite(s[j]) ? s[j] + left[j] : s[j]; }
+};
+
 __global__ void __launch_bounds__(256) ns_norm_kernel(const void* g, int f32, size_t n, float* parts) {
     __shared__ float s_sum[3][8];
     grid_dep_launch();
     grid_dep_wait();
     const size_t base = blockIdx.y * n;
-    float s[3] = {0.0f, 0.0f, 0.0f};
-    auto add = [&](float x) {
-        const float a = fabsf(x);
-        const float big = a > 0x1p48f ? x * 0x1p-80f : 0.0f, tiny = a < 0x1p-48f ? x * 0x1p80f : 0.0f;
-        const float mid = a > 0x1p48f || a < 0x1p-48f ? 0.0f : x;  // (a NaN goes here)
-        s[0] = fmaf(big, big, s[0]);
-        s[1] = fmaf(mid, mid, s[1]);
-        s[2] = fmaf(tiny, tiny, s[2]);
-    };
+    NsSum sum;
     const size_t step = (size_t)gridDim.x * 256, first = (size_t)blockIdx.x * 256 + threadIdx.x;
     if (n % 8 == 0) {
         const size_t pieces = f32 ? n / 4 : n / 8;  // of 16 bytes, four in flight a thread
@@ -85,23 +104,28 @@ __global__ void __launch_bounds__(256) ns_norm_kernel(const void* g, int f32, si
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
                     if (f32) {
-                        add(__uint_as_float(u[j]));
+                        sum.add(__uint_as_float(u[j]));
                     } else {
                         const float2 f = bf16x2_to_f2(u[j]);
-                        add(f.x);
-                        add(f.y);
+                        sum.add(f.x);
+                        sum.add(f.y);
                     }
                 }
             }
+            sum.put_aside();
         }
     } else {
+        for (size_t i = first; i < n; i += 32 * step) {
 #pragma unroll 4
-        for (size_t i = first; i < n; i += step) add(ns_value(g, f32, base + i));
+            for (int k = 0; k < 32; ++k)
+                if (i + k * step < n) sum.add(ns_value(g, f32, base + i + k * step));
+            sum.put_aside();
+        }
     }
 #pragma unroll
     for (int j = 0; j < 3; ++j) {
-        s[j] = warp_sum(s[j]);
-        if ((threadIdx.x & 31) == 0) s_sum[j][threadIdx.x >> 5] = s[j];
+        const float s = warp_sum(sum.total(j));
+        if ((threadIdx.x & 31) == 0) s_sum[j][threadIdx.x >> 5] = s;
     }
     __syncthreads();
     if (threadIdx.x < 3) {
