@@ -437,6 +437,8 @@ int moe_combine_norm(const void* x, int x_dtype, const void* o, int o_dtype, con
  * does; rows that it does not name are left as they were in d_o, and dw is 0
  * for dropped routes.  dx may alias dy; d_o may not overlap o (the same address
  * is refused).  The column sums
+ * (over tokens, fp32) are off by at most 2^-15 of their terms' magnitudes' sum,
+ * however many there are, beside what the terms are; they
  * are joined in a fixed order (the same call gives the same bits) through the
  * workspace, of moe_combine_norm_backward_workspace_bytes() (host-only, for
  * the current device; sums: how many of post, scale and pre are given), used

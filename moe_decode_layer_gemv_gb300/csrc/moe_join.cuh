@@ -261,6 +261,9 @@ __global__ void __launch_bounds__(MT) join_kernel(JoinParams p) {
 // token's barrier.
 // A block walks tokens and keeps the column sums in shared memory, each column
 // by the thread that owns it; the blocks' sums are joined in a fixed order.
+// After kJoinRun tokens they are added to the block's part of the workspace: n
+// additions one after the other are off by up to n / 2 2^-24 of a sum of one
+// sign, and the most tokens are 27594 a block (4 to 9e-5 at 6900).
 //
 // Bound by HBM and, with 16 warps an SM, by the latency between a token's loads
 // and its stores.  With NV = 1 a thread keeps what it read of a token (its rows
@@ -271,6 +274,8 @@ __global__ void __launch_bounds__(MT) join_kernel(JoinParams p) {
 // the prefetch, 169 with one of two tokens; 222 with the rows read again and
 // three blocks an SM; 206 with a ring of bulk copies feeding two groups of 256
 // threads from shared memory, whose 52 KB a token leave it three or four deep).
+constexpr int kJoinRun = 256;
+
 template <bool OF32, int NV, int MT>
 __global__ void __launch_bounds__(MT) join_back_kernel(JoinParams p) {
     extern __shared__ __align__(16) float cols[];  // [sums][H]
@@ -305,9 +310,31 @@ __global__ void __launch_bounds__(MT) join_back_kernel(JoinParams p) {
         for (int i = 0; i < warps; ++i) sum += dbuf[parity][i][threadIdx.x];
         p.dw[(size_t)t * p.k + threadIdx.x] = sum;
     };
+    // The block's column sums into its part of the workspace, or added to what is there: each column by the thread
+    // that owns it.
+    bool first = true;
+    auto put_aside = [&]() {
+        float4* out = reinterpret_cast<float4*>(p.parts + (size_t)blockIdx.x * p.sums * p.H);
+        float4* in = reinterpret_cast<float4*>(cols);
+        for (int s = 0; s < p.sums; ++s)
+            for (int v = threadIdx.x; v < nvec; v += blockDim.x)
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    float4 &sum = in[2 * s * nvec + h * nvec + v], &to = out[2 * (s * nvec + v) + h];
+                    float4 a = sum;
+                    if (!first) a = make_float4(a.x + to.x, a.y + to.y, a.z + to.z, a.w + to.w);
+                    to = a;
+                    sum = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                }
+        first = false;
+    };
     routes(blockIdx.x);
-    int parity = 0, t = blockIdx.x;
+    int parity = 0, t = blockIdx.x, run = 0;
     for (; t < p.T; t += gridDim.x, parity ^= 1) {
+        if (++run > kJoinRun) {
+            put_aside();
+            run = 1;
+        }
         if (r_next < -1 || r_next >= p.R) {
             set_status(p.status, MOE_DEV_BAD_ROUTE);
             r_next = -1;
@@ -485,13 +512,7 @@ __global__ void __launch_bounds__(MT) join_back_kernel(JoinParams p) {
     }
     __syncthreads();
     write_dw(t - gridDim.x, parity ^ 1);
-    float4* out = reinterpret_cast<float4*>(p.parts + (size_t)blockIdx.x * p.sums * p.H);
-    const float4* in = reinterpret_cast<const float4*>(cols);
-    for (int s = 0; s < p.sums; ++s)
-        for (int v = threadIdx.x; v < nvec; v += blockDim.x) {
-            out[2 * (s * nvec + v)] = in[2 * s * nvec + v];
-            out[2 * (s * nvec + v) + 1] = in[2 * s * nvec + nvec + v];
-        }
+    put_aside();
 }
 
 // The blocks' column sums in a fixed order: a block takes 32 columns, its

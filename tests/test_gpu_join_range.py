@@ -1,6 +1,6 @@
 """Where the join's gradients could leave fp32's range or precision although
 their results do not: rows of any magnitude, an eps next to nothing, an eps of
-nothing with rows of nothing.
+nothing with rows of nothing, and column sums over many tokens.
 
 Tolerances and formulas as in test_gpu_join.py, where not said otherwise."""
 import pytest
@@ -107,3 +107,29 @@ def test_rows_of_zeros_without_eps(cuda_lib, T, k, H):
     assert torch.equal(got[0][1], c["dy"][1]) and torch.equal(got[0][2], c["dy"][2])
     assert bool((got[1][rows] == 0).all()) and bool((got[2][1] == 0).all())
     assert torch.equal(got[0][keep], back[0][keep]) and torch.equal(got[2][keep], back[2][keep])
+
+
+def test_column_sums_over_many_tokens(cuda_lib):
+    """2^20 tokens, all terms of a column alike and of one sign: a sum of n
+    fp32 additions one after the other is off by up to n / 2 2^-24.  A block
+    adds up 256 tokens at most before it puts them aside (2^20 / 152 / 256 = 27
+    times on 152 SMs, 108 times for the most tokens), and the blocks' sums take
+    28 more: (256 + 108 + 28) / 2 2^-24 < 2^-16.  The terms' own roundings,
+    2^-20, count on top."""
+    T, H = 1 << 20, 2056
+    g = torch.Generator(device=DEV)
+    g.manual_seed(0)
+    r = lambda: (0.5 + torch.rand(H, generator=g, device=DEV))  # noqa: E731
+    row = {n: r().to(BF16) for n in ("y", "dy", "dn", "o")}
+    post, scale, pre = r(), r(), r()
+    y, dy, dn, o = (row[n].expand(T, H).contiguous() for n in ("y", "dy", "dn", "o"))
+    got = cuda_lib.combine_norm_backward(dy, dn, y, o, post=post, scale=scale, pre=pre, eps=1e-6)
+    one = lambda t: t.double().view(1, H)  # noqa: E731
+    a, ny = one(row["dn"]) * one(pre), join._rms(one(row["y"]))
+    d = one(row["dy"]) + ny * a - one(row["y"]) * ny ** 3 * (a * one(row["y"])).mean()
+    hat = one(row["o"]) * join._rms(one(row["o"]))
+    want = (d * one(scale) * hat, d * hat * one(post), one(row["dn"]) * one(row["y"]) * ny)
+    for n, t, w in zip(("dpost", "dscale", "dpre"), got[3:], want):
+        off = float((t.double() / (T * w.flatten()) - 1).abs().max())
+        assert off <= 2.0 ** -16 + 2.0 ** -20, (n, off)
+    torch.cuda.empty_cache()
