@@ -223,20 +223,17 @@ static int run_ns(GgParams& p, int E, float alpha, float beta, float shift, bool
 
 template <int CG, int NARROW>
 static int run_ns_steps(NsProducts& s, int E, int steps, float a, float b, float c, bool more, int sms, cudaStream_t st) {
-    void* const low = s.bx[0].low;
     const float up = (float)(1 << kNsScaleLog2), down = 1.0f / up;
     for (int i = 0; i < steps; ++i) {
         // a + b A + c A A of A = S + A': one + lin A' + c A' A'
         const float S = NARROW < 2 && steps - i <= kNsShifted ? kNsShift : 0.0f, lin = b + 2.0f * c * S, one = a + b * S + c * S * S;
         int rc = run_ns<kGgSym, CG, NARROW>(s.xx[i & 1], E, down * down, 0.0f, S, true, sms, st);
         if (!rc) rc = run_ns<kGgSym, CG, NARROW>(s.aa, E, c, lin, 0.0f, true, sms, st);
-        if (NARROW < 2) s.bx[i & 1].low = i + 2 < steps ? low : nullptr;  // (what the last step does not read)
         if (!rc)
             rc = i + 1 < steps ? run_ns<kGgAxpy, CG, NARROW>(s.bx[i & 1], E, 1.0f, one, 0.0f, true, sms, st)
                                : run_ns<kGgResult, CG, NARROW>(s.last[i & 1], E, down, one * down, 0.0f, more, sms, st);
         if (rc) return rc;
     }
-    if (NARROW < 2) s.bx[0].low = s.bx[1].low = low;
     return MOE_OK;
 }
 
@@ -513,8 +510,6 @@ int moe_orthogonalize(const void* g, int g_dtype, int E, int N, int K, int steps
     }
     if (!ok) return MOE_ERR_UNSUPPORTED;
     s.aa.status = dev_status;
-    // the last step takes X's high half alone (unless X0 is all there is)
-    if (steps > 1 && !split) s.last[0].planes = s.last[1].planes = 1;
     rc = q.narrow == 2 ? ns_allow<1, 2>() : q.narrow ? ns_allow<1, 1>() : q.pairs ? ns_allow<2, 0>() : ns_allow<1, 0>();
     if (rc) return rc;
     const size_t each = (size_t)N * K;

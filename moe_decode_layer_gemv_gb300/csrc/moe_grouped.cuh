@@ -76,7 +76,7 @@ struct GgParams {
     int planes, tin_at[2];
     // orthogonalisation: out = alpha product + beta in - shift 1
     float alpha, beta, shift;
-    void* low;       // receives what fp16 leaves of out, if not nullptr
+    void* low;       // receives what fp16 leaves of out (but of a symmetric product that is not split)
     CUtensorMap ta_lo, tb_lo;  // split products: what fp16 left of the operands
     int halves;      // high high + high low + low high, three products in one sum
     int early;       // the kernel behind this one touches nothing before its grid_dep_wait
@@ -769,9 +769,9 @@ __device__ __forceinline__ void ns_axpy_rows(const P& p, const float* d, const u
     const int last = m < M ? n - odd : 0;  // rows r + odd + j, j < last
     const uint16_t *in = ins + (lane - odd) + odd * 128, *lo = in + ROWS * 128;
     const size_t pair = ((size_t)e * p.rows + r + odd) * M + (m - odd);
-    uint16_t *to = static_cast<uint16_t*>(p.out) + pair, *tl = p.low ? static_cast<uint16_t*>(p.low) + pair : nullptr;
+    uint16_t *to = static_cast<uint16_t*>(p.out) + pair, *tl = static_cast<uint16_t*>(p.low) + pair;
 #pragma unroll
-    for (int j = 0; j < ROWS; j += 2, to += 2 * (size_t)M, tl += p.low ? 2 * (size_t)M : 0) {
+    for (int j = 0; j < ROWS; j += 2, to += 2 * (size_t)M, tl += 2 * (size_t)M) {
         const float2 v = gg_swap(d[j], d[j + 1], odd), f = f16x2_to_f2(in_pair(in, j)), l = f16x2_to_f2(in_pair(lo, j));
         const float v0 = fmaf(p.beta, f.x + l.x, p.alpha * v.x), v1 = fmaf(p.beta, f.y + l.y, p.alpha * v.y);
         const uint32_t w = gg_pack_f16(v0, v1);
@@ -779,7 +779,7 @@ __device__ __forceinline__ void ns_axpy_rows(const P& p, const float* d, const u
         const uint32_t x = gg_pack_f16(v0 - t.x, v1 - t.y);
         if (j < last) {
             *reinterpret_cast<uint32_t*>(to) = w;
-            if (p.low) *reinterpret_cast<uint32_t*>(tl) = x;
+            *reinterpret_cast<uint32_t*>(tl) = x;
         }
     }
 }
@@ -836,9 +836,8 @@ __device__ __forceinline__ void ns_result_rows(const P& p, const float* d, const
     uint32_t w[ROWS / 2];  // rows j and j + 1 of this lane's m
 #pragma unroll
     for (int j = 0; j < ROWS; j += 2) {
-        float f0 = in_f16(in, j), f1 = in_f16(in, j + 1);
-        if (p.planes == 2) f0 += in_f16(lo, j), f1 += in_f16(lo, j + 1);
-        const float v0 = fmaf(p.beta, f0, p.alpha * d[j]), v1 = fmaf(p.beta, f1, p.alpha * d[j + 1]);
+        const float v0 = fmaf(p.beta, in_f16(in, j) + in_f16(lo, j), p.alpha * d[j]);
+        const float v1 = fmaf(p.beta, in_f16(in, j + 1) + in_f16(lo, j + 1), p.alpha * d[j + 1]);
         w[j / 2] = gg_pack(__float_as_uint(v0), __float_as_uint(v1));
     }
     if (p.res_trans) {

@@ -9,22 +9,25 @@
 // |X|_2 near 1, so that nothing overflows (bf16 operands would be off by 8
 // times as much).  X itself is carried in two fp16 values, 22 bits, from step
 // to step: whatever is rounded off it in directions that G does not have grows
-// by a factor of a in each step, and a gradient of few tokens has few
-// directions (256 x 256 of rank 24: 3.1e-2 of the result with X in fp16 alone,
-// 1.5e-3 so).  In the last two steps A' = A - 1/2 takes A's place,
+// by a factor of a in each step, the last one included, and a gradient of few
+// tokens has few directions (256 x 256 of rank 24: 3.1e-2 of the result with X
+// in fp16 alone, 1.5e-3 so; 1.6e-3 with the high half alone in the last step,
+// and 1.9e-3 instead of 1.7e-3 for 130 x 500 of rank 1).  In the last two steps
+// A' = A - 1/2 takes A's place,
 //   a + b A + c A A = (a + b/2 + c/4) + (b + c) A' + c A' A',
 // since most eigenvalues of A are near 1 by then and b A + c A A several times
 // as large as what is left of it, and its roundings too (random 300 x 900
-// matrices: 1.7e-3 without, 1.0e-3 so; earlier it would undo the above), and the
-// last step takes X's high half alone, whose roundings nothing enlarges any more
-// (3e-4; 0.4 GB of traffic less for 64 matrices of 2048 x 768).  The
-// bf16 result's own rounding is 1.7e-3.  Short sides average over few
+// matrices: 1.7e-3 without, 1.0e-3 so).  In the directions that G lacks it
+// costs some of the low half's good: B is 1.9 there instead of 0, more than half of a,
+// and multiplies X's high half alone; in earlier steps it would undo the above.  The bf16 result's own rounding is 1.7e-3, which adds to
+// all of these in squares.  Short sides average over few
 // roundings (20 x 300: 2.2e-3), and cost little: up to 96 rows A and B too are
 // held in two values, and the products that contract over them, A A and B X,
 // take three terms (high high + high low + low high) and no shift.  20 x 300
-// then end 3.8e-4 off, 16 x 16 1.1e-3, of X's rounding in X X^T alone.  X carries a factor of 2^8, which keeps the
-// entries of the largest matrices (2^-14 on average at 16384 x 16384) out of
-// fp16's subnormals; a single entry of 1 is still far from 65504.
+// then end 3.8e-4 off, 16 x 16 1.1e-3, of X's rounding in X X^T alone.  X
+// carries a factor of 2^8, which keeps the entries of the largest matrices
+// (2^-14 on average at 16384 x 16384) out of fp16's subnormals; a single entry
+// of 1 is still far from 65504.
 //
 // 64 matrices of 2048 x 768 in bf16, five steps: 1489 us.  Norm 52 and
 // conversion 136 (HBM), then a step: X X^T 75 and A A 41 (384 tiles on 76 pairs
