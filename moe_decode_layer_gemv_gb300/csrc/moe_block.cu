@@ -124,11 +124,10 @@ static int run_join_back(const JoinParams& p, int grid, cudaStream_t st) {
 // ---------------------------------------------------------- orthogonalisation
 struct NsPlan {
     int m, n;        // rows and columns of X, padded
-    int group;       // matrices that go through all steps together
     int parts;       // blocks that sum a matrix's squares
     bool pairs;      // tiles of CTA pairs
     int narrow;      // tiles of 32 columns, 2: and split products
-    size_t x, a, p;  // bytes of a group's X, of its A, of the sums
+    size_t x, a, p;  // bytes of X, of A, of the sums
     size_t bytes;
 };
 
@@ -145,14 +144,13 @@ static int ns_plan(int E, int N, int K, int sms, NsPlan* q) {
     // 768 x 2048 9.8 and 9.2, 1024 x 1024 8.9 and 10.2; four of 390 x 515 6.8 and 6.6, eight 7.8 and 9.5
     // Up to kNsSplitRows rows the products whose contraction that is are split (moe_ortho.cuh).
     q->narrow = q->m <= kNsSplitRows ? 2 : (int64_t)E * ceil_div(q->m, 32) * ceil_div(q->m, 128) <= sms;
-    q->group = E;
-    q->parts = ceil_div(8 * sms, q->group);
+    q->parts = ceil_div(8 * sms, E);
     const int most = (int)(((size_t)N * K + 2047) / 2048);
     if (q->parts > most) q->parts = most;
     if (q->parts > kNsParts) q->parts = kNsParts;
-    q->x = align_up(sizeof(uint16_t) * (size_t)q->group * q->m * q->n, 256);
-    q->a = align_up(sizeof(uint16_t) * (size_t)q->group * q->m * q->m, 256);
-    q->p = align_up(sizeof(float) * 3 * (size_t)q->group * q->parts, 256);
+    q->x = align_up(sizeof(uint16_t) * (size_t)E * q->m * q->n, 256);
+    q->a = align_up(sizeof(uint16_t) * (size_t)E * q->m * q->m, 256);
+    q->p = align_up(sizeof(float) * 3 * (size_t)E * q->parts, 256);
     q->bytes = (q->narrow == 2 ? 4 * q->x + 4 * q->a : 3 * q->x + 2 * q->a) + q->p + 256;  // (the parts are aligned to 256)
     return MOE_OK;
 }
@@ -169,24 +167,24 @@ struct NsHalves {
 };
 
 // in: what the epilogue reads beside the product; split: into the product of both operands' halves.
-static bool ns_params(const NsPlan& q, NsHalves w, NsHalves x, int cols, NsHalves in, NsHalves out, bool split, bool sym,
+static bool ns_params(const NsPlan& q, int E, NsHalves w, NsHalves x, int cols, NsHalves in, NsHalves out, bool split, bool sym,
                       GgParams* p) {
     memset(p, 0, sizeof *p);
     p->rows = q.m;
     p->low = out.low;
     p->halves = split;
     p->out = out.high;
-    const uint64_t G = (uint64_t)q.group, R = G * q.m;
+    const uint64_t R = (uint64_t)E * q.m;
     bool ok;
-    if (sym) {  // x [G m, cols] times its own rows
+    if (sym) {  // x [E m, cols] times its own rows
         p->M = q.m;
         p->C = cols;
-        ok = encode_map(&p->ta, w.high, 2, cols, q.m, G, 128) && (!split || encode_map(&p->ta_lo, w.low, 2, cols, q.m, G, 128));
-    } else {  // x = B [G m, m], w = X [G, m, n]
+        ok = encode_map(&p->ta, w.high, 2, cols, q.m, E, 128) && (!split || encode_map(&p->ta_lo, w.low, 2, cols, q.m, E, 128));
+    } else {  // x = B [E m, m], w = X [E, m, n]
         p->M = q.n;
         p->C = q.m;
         p->a_blocked = 1;
-        ok = encode_blocked(&p->ta, w.high, q.n, q.m, G) && (!split || encode_blocked(&p->ta_lo, w.low, q.n, q.m, G));
+        ok = encode_blocked(&p->ta, w.high, q.n, q.m, E) && (!split || encode_blocked(&p->ta_lo, w.low, q.n, q.m, E));
     }
     ok = ok && encode_map(&p->tb, x.high, 2, p->C, R, 0, kGgBoxN) && encode_map(&p->tb_all, x.high, 2, p->C, R, 0, 128) &&
          (!split || encode_map(&p->tb_lo, x.low, 2, p->C, R, 0, kGgBoxN));
@@ -207,14 +205,13 @@ static int ns_allow() {
 
 // One product of E matrices, on no more SMs than it has tiles.
 template <int EP, int CG, int NARROW>
-static int run_ns(GgParams& p, int E, float alpha, float beta, float shift, bool early, int sms, cudaStream_t st) {
+static int run_ns(GgParams& p, int E, float alpha, float beta, float shift, int sms, cudaStream_t st) {
     constexpr int MODE = EP == kGgSym ? kGgFwd : kGgDx;
     p.E = E;
     p.R = E * p.rows;
     p.alpha = alpha;
     p.beta = beta;
     p.shift = shift;
-    p.early = early;
     const int64_t t = ceil_div(p.rows, NARROW ? 32 : 128 * CG);
     const int64_t tiles = E * (EP == kGgSym && !NARROW ? t * (t + 1) / 2 : t * ceil_div(p.M, 128 * CG));
     return launch_clusters<CG>(gg_kernel<MODE, CG, false, EP, NARROW>, p, GgRole<MODE, CG, false, EP, NARROW>::kThreads,
@@ -222,16 +219,16 @@ static int run_ns(GgParams& p, int E, float alpha, float beta, float shift, bool
 }
 
 template <int CG, int NARROW>
-static int run_ns_steps(NsProducts& s, int E, int steps, float a, float b, float c, bool more, int sms, cudaStream_t st) {
+static int run_ns_steps(NsProducts& s, int E, int steps, float a, float b, float c, int sms, cudaStream_t st) {
     const float up = (float)(1 << kNsScaleLog2), down = 1.0f / up;
     for (int i = 0; i < steps; ++i) {
         // a + b A + c A A of A = S + A': one + lin A' + c A' A'
         const float S = NARROW < 2 && steps - i <= kNsShifted ? kNsShift : 0.0f, lin = b + 2.0f * c * S, one = a + b * S + c * S * S;
-        int rc = run_ns<kGgSym, CG, NARROW>(s.xx[i & 1], E, down * down, 0.0f, S, true, sms, st);
-        if (!rc) rc = run_ns<kGgSym, CG, NARROW>(s.aa, E, c, lin, 0.0f, true, sms, st);
+        int rc = run_ns<kGgSym, CG, NARROW>(s.xx[i & 1], E, down * down, 0.0f, S, sms, st);
+        if (!rc) rc = run_ns<kGgSym, CG, NARROW>(s.aa, E, c, lin, 0.0f, sms, st);
         if (!rc)
-            rc = i + 1 < steps ? run_ns<kGgAxpy, CG, NARROW>(s.bx[i & 1], E, 1.0f, one, 0.0f, true, sms, st)
-                               : run_ns<kGgResult, CG, NARROW>(s.last[i & 1], E, down, one * down, 0.0f, more, sms, st);
+            rc = i + 1 < steps ? run_ns<kGgAxpy, CG, NARROW>(s.bx[i & 1], E, 1.0f, one, 0.0f, sms, st)
+                               : run_ns<kGgResult, CG, NARROW>(s.last[i & 1], E, down, one * down, 0.0f, sms, st);
         if (rc) return rc;
     }
     return MOE_OK;
@@ -425,7 +422,6 @@ int moe_combine_norm_backward(const void* dy, const void* dn, int n_dtype, const
     p.w = w;
     p.post = post;
     p.scale = scale;
-    p.want_scale = scale != nullptr;
     p.pre = pre;
     p.y = dx;
     p.x_f32 = y_dtype == MOE_DT_F32;
@@ -497,10 +493,10 @@ int moe_orthogonalize(const void* g, int g_dtype, int E, int N, int K, int steps
     float* parts = static_cast<float*>(take(q.p));
     const int f32 = g_dtype == MOE_DT_F32, trans = N > K;
     NsProducts s;
-    bool ok = ns_params(q, A, A, q.m, A, B, split, true, &s.aa);
+    bool ok = ns_params(q, E, A, A, q.m, A, B, split, true, &s.aa);
     for (int i = 0; i < 2 && ok; ++i) {
-        ok = ns_params(q, x[i], x[i], q.n, none, A, false, true, &s.xx[i]) &&
-             ns_params(q, x[i], B, 0, x[i], x[i ^ 1], split, false, &s.bx[i]);
+        ok = ns_params(q, E, x[i], x[i], q.n, none, A, false, true, &s.xx[i]) &&
+             ns_params(q, E, x[i], B, 0, x[i], x[i ^ 1], split, false, &s.bx[i]);
         s.xx[i].status = s.bx[i].status = dev_status;
         s.last[i] = s.bx[i];
         s.last[i].res_rows = N;
@@ -512,30 +508,21 @@ int moe_orthogonalize(const void* g, int g_dtype, int E, int N, int K, int steps
     s.aa.status = dev_status;
     rc = q.narrow == 2 ? ns_allow<1, 2>() : q.narrow ? ns_allow<1, 1>() : q.pairs ? ns_allow<2, 0>() : ns_allow<1, 0>();
     if (rc) return rc;
-    const size_t each = (size_t)N * K;
-    for (int e = 0; e < E; e += q.group) {
-        const int G = E - e < q.group ? E - e : q.group;
-        const void* from = static_cast<const unsigned char*>(g) + each * e * (f32 ? 4 : 2);
-        rc = launch_pdl(ns_norm_kernel, dim3((unsigned)q.parts, (unsigned)G), 256, 0, st, from, f32, each, parts);
-        if (rc) return rc;
-        // (the blocks cover the padded X: its rows are G's columns where G is tall)
-        const int rows = trans ? q.n : q.m, cols = trans ? q.m : q.n;
-        // (a block finds the norm first: with many blocks one serves four tiles)
-        const int64_t tiles = (int64_t)G * ceil_div(cols, 64) * ceil_div(rows, 64);
-        const int strip = tiles >= 16 * sms ? 256 : 64;
-        rc = launch_pdl(ns_convert_kernel, dim3((unsigned)ceil_div(cols, strip), (unsigned)ceil_div(rows, 64), (unsigned)G), 256,
-                        0, st, from, f32, N, K, (const float*)parts, q.parts, eps, trans, x[0].high, x[0].low, q.m, q.n,
-                        strip);
-        if (rc) return rc;
-        s.last[(steps - 1) & 1].out = out + each * e;
-        const bool more = e + G < E;
-        rc = q.narrow == 2 ? run_ns_steps<1, 2>(s, G, steps, a, b, c, more, sms, st)
-             : q.narrow    ? run_ns_steps<1, 1>(s, G, steps, a, b, c, more, sms, st)
-             : q.pairs     ? run_ns_steps<2, 0>(s, G, steps, a, b, c, more, sms, st)
-                           : run_ns_steps<1, 0>(s, G, steps, a, b, c, more, sms, st);
-        if (rc) return rc;
-    }
-    return MOE_OK;
+    rc = launch_pdl(ns_norm_kernel, dim3((unsigned)q.parts, (unsigned)E), 256, 0, st, g, f32, (size_t)N * K, parts);
+    if (rc) return rc;
+    // (the blocks cover the padded X: its rows are G's columns where G is tall)
+    const int rows = trans ? q.n : q.m, cols = trans ? q.m : q.n;
+    // (a block finds the norm first: with many blocks one serves four tiles)
+    const int64_t tiles = (int64_t)E * ceil_div(cols, 64) * ceil_div(rows, 64);
+    const int strip = tiles >= 16 * sms ? 256 : 64;
+    rc = launch_pdl(ns_convert_kernel, dim3((unsigned)ceil_div(cols, strip), (unsigned)ceil_div(rows, 64), (unsigned)E), 256, 0,
+                    st, g, f32, N, K, (const float*)parts, q.parts, eps, trans, x[0].high, x[0].low, q.m, q.n, strip);
+    if (rc) return rc;
+    s.last[(steps - 1) & 1].out = out;
+    return q.narrow == 2 ? run_ns_steps<1, 2>(s, E, steps, a, b, c, sms, st)
+           : q.narrow    ? run_ns_steps<1, 1>(s, E, steps, a, b, c, sms, st)
+           : q.pairs     ? run_ns_steps<2, 0>(s, E, steps, a, b, c, sms, st)
+                         : run_ns_steps<1, 0>(s, E, steps, a, b, c, sms, st);
 }
 
 }  // extern "C"

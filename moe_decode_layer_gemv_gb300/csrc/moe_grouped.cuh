@@ -79,7 +79,6 @@ struct GgParams {
     void* low;       // receives what fp16 leaves of out (but of a symmetric product that is not split)
     CUtensorMap ta_lo, tb_lo;  // split products: what fp16 left of the operands
     int halves;      // high high + high low + low high, three products in one sum
-    int early;       // the kernel behind this one touches nothing before its grid_dep_wait
     int rows;        // of every segment (offsets is then not read)
     int res_rows, res_cols, res_trans;  // the result's matrices: [E, res_rows, res_cols], transposed or not
     int res_sectors;  // every sixteenth column of it lies on 32 bytes
@@ -930,7 +929,7 @@ __global__ void __launch_bounds__((GgRole<MODE, CG, F32, EP, NARROW>::kThreads),
         if (MODE != kGgDw) prefetch_map(&p.tb_all);
     }
     if (warp == Role::EPI + 1) gg_tmem_alloc<CG>(&sh->tmem_slot, kGgTmemCols);
-    if (EP >= kGgSym && p.early) grid_dep_launch();
+    if (EP == kGgSym || EP == kGgAxpy) grid_dep_launch();  // (what follows touches nothing before its grid_dep_wait)
     if (EP < kGgSym) grid_dep_wait();
     constexpr int MW = EP == kGgGlu ? 64 : 128, BMW = MW * CG;  // outputs that a CTA's 128 rows and a tile give
     const int mtiles = (p.M + BMW - 1) / BMW;
@@ -1223,30 +1222,22 @@ __global__ void __launch_bounds__((GgRole<MODE, CG, F32, EP, NARROW>::kThreads),
                 const int h = warp >> 2;
                 if (!gg_wait_warp(&sh->acc_full[buf], full_ph, &sh->abort)) return false;
                 tc_fence_after();
-                for (int c = 0; c < mine; c += 16) {
-                    float d[16];
+                static_assert(In::kRows == 16, "one load of tensor memory a slot");
+                for (int c = 0; c < mine; c += In::kRows) {
+                    float d[In::kRows];
                     tmem_ld16(taddr + c, d);
-                    auto wait = [&]() -> bool { return !p.planes || gg_wait_warp(&sh->in_full[h][in.s], in.ph, &sh->abort); };
-                    auto at = [&]() {
-                        return reinterpret_cast<const uint16_t*>(ins + (h * In::kSlots + in.s) * In::kSlot) + (warp & 3) * 32;
-                    };
-                    auto done = [&]() {
-                        if (!p.planes) return;
+                    if (p.planes && !gg_wait_warp(&sh->in_full[h][in.s], in.ph, &sh->abort)) return false;
+                    const uint16_t* at =
+                        reinterpret_cast<const uint16_t*>(ins + (h * In::kSlots + in.s) * In::kSlot) + (warp & 3) * 32;
+                    const int r = n0 + c0 + c, rows = min(In::kRows, mine - c);
+                    if constexpr (EP == kGgGluBack) glu_back_rows<In::kRows>(p, d, at, row0 + c, rows, m, lane);
+                    if constexpr (EP == kGgSym) ns_sym_rows<In::kRows, NARROW == 2>(p, d, at, e, r, m, lane, kMirror && n0 > m0);
+                    if constexpr (EP == kGgAxpy) ns_axpy_rows<In::kRows>(p, d, at, e, r, rows, m, lane);
+                    if constexpr (EP == kGgResult) ns_result_rows<In::kRows>(p, d, at, e, r, rows, m, lane);
+                    if (p.planes) {
                         __syncwarp();
                         if (lane == 0) mbar_arrive(&sh->in_empty[h][in.s]);
                         in.next();
-                    };
-                    const int r0 = n0 + c0 + c;
-#pragma unroll
-                    for (int i = 0; i < 16; i += In::kRows) {
-                        if (c + i >= mine) break;
-                        if (!wait()) return false;
-                        const int rows = min(In::kRows, mine - c - i);
-                        if constexpr (EP == kGgGluBack) glu_back_rows<In::kRows>(p, d + i, at(), row0 + c + i, rows, m, lane);
-                        if constexpr (EP == kGgSym) ns_sym_rows<In::kRows, NARROW == 2>(p, d + i, at(), e, r0 + i, m, lane, kMirror && n0 > m0);
-                        if constexpr (EP == kGgAxpy) ns_axpy_rows<In::kRows>(p, d + i, at(), e, r0 + i, rows, m, lane);
-                        if constexpr (EP == kGgResult) ns_result_rows<In::kRows>(p, d + i, at(), e, r0 + i, rows, m, lane);
-                        done();
                     }
                 }
                 tc_fence_before();

@@ -27,7 +27,7 @@ struct JoinParams {
     void* d_o;
     float* dw;
     float* parts;           // [gridDim.x][sums][H] column sums: of those wanted, dpost, dscale, dpre
-    int sums, want_scale;
+    int sums;
     int32_t* status;
 };
 
@@ -287,8 +287,8 @@ __global__ void __launch_bounds__(MT) join_back_kernel(JoinParams p) {
     float* at = cols;
     float* c_post = p.post ? at : nullptr;
     at += p.post ? p.H : 0;
-    float* c_scale = p.want_scale ? at : nullptr;
-    at += p.want_scale ? p.H : 0;
+    float* c_scale = p.scale ? at : nullptr;
+    at += p.scale ? p.H : 0;
     float* c_pre = at;
     grid_dep_wait();
     __syncthreads();
