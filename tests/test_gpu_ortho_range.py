@@ -1,5 +1,5 @@
-"""What orthogonalisation (moe_orthogonalize) loses where that would show
-most."""
+"""Orthogonalisation (moe_orthogonalize) at its largest sizes, and what it loses
+where that would show most."""
 import math
 
 import pytest
@@ -63,3 +63,41 @@ def test_few_directions_keep_both_halves(cuda_lib, N, K, rank):
     own, lost = (want.to(BF16).double() - want).norm(), (_both_halves(g) - want).norm()
     off = (cuda_lib.orthogonalize(g).double() - want).norm()
     assert float(off) <= 1.02 * math.hypot(float(own), float(lost)), float(off) / math.hypot(float(own), float(lost))
+
+
+@pytest.mark.parametrize("N,K", [(3100, 4097), (4100, 2800)])
+def test_long_short_sides_match_64_bits(cuda_lib, N, K):
+    g = ortho._g(1, N, K)
+    ortho._check(cuda_lib.orthogonalize(g), g)
+
+
+@pytest.mark.parametrize("a,b", [((128, 128), (128, 128)), ((128, 120), (128, 100)), ((90, 128), (100, 128))])
+def test_the_largest_matrices(cuda_lib, a, b):
+    """Kronecker products A x B: their singular vectors are those of A and B,
+    their singular values all products, so that the exact result follows from
+    the recurrence of a number.
+
+    Tolerance: at most 12.2 half steps of fp16 a step and four steps that count
+    (test_gpu_ortho.py), evenly spread, which over 10^8 values is 3^-1/2 of
+    that in 2-norm; and half a step of bf16, likewise."""
+    gen = torch.Generator(device=DEV)
+    gen.manual_seed(0)
+    A, B = (torch.randn(s, generator=gen, device=DEV, dtype=torch.float64) for s in (a, b))
+    g = torch.kron(A, B).float().contiguous()
+    (ua, sa, va), (ub, sb, vb) = (torch.linalg.svd(t, full_matrices=False) for t in (A, B))
+    s = sa.unsqueeze(1) * sb.unsqueeze(0)
+    s = s / (s.norm() + 1e-7)
+    c0, c1, c2 = ortho.NS
+    for _ in range(5):
+        s = s * (c0 + s * s * (c1 + c2 * s * s))
+    got = cuda_lib.orthogonalize(g)
+    del g
+    off = size = 0.0
+    for i in range(a[0]):  # the rows that A's i-th row makes
+        t = torch.einsum("p,qr,pr,pm->mqr", ua[i], ub, s, va)  # [A's columns, B's rows, B's directions]
+        want = (t @ vb).transpose(0, 1).reshape(b[0], -1)
+        off += float((got[i * b[0]:(i + 1) * b[0]].double() - want).square().sum())
+        size += float(want.square().sum())
+    tol = (4 * 12.2 * 2.0 ** -12 + 2.0 ** -8) / 3 ** 0.5
+    assert math.sqrt(off / size) <= tol, math.sqrt(off / size)
+    torch.cuda.empty_cache()
