@@ -375,7 +375,8 @@ int moe_grouped_gemm_dw(const uint16_t* dy, const uint16_t* x, const int32_t* of
  * x [R, H] bf16, gate_up [E, 2I, H] bf16 (rows [0, I) gate, [I, 2I) up),
  * h [R, I] fp32 or bf16 (h_dtype); gu [R, 2I] bf16 or NULL receives (g, u),
  * which moe_grouped_glu_backward starts from.  g and u are fp32 sums; h is
- * made from them before they are rounded.  moe_grouped_gemm with w = down
+ * made from them before they are rounded, and in fp32 loses no more of sums of
+ * one sign than a plain product does (2^-20).  moe_grouped_gemm with w = down
  * completes the block.  R, offsets, segments and dev_status as in
  * moe_grouped_gemm; H and I multiples of 8 in [8, MOE_MAX_DIM].  An infinite
  * g gives what the formula gives (NaN at -infinity).

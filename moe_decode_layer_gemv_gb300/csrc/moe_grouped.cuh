@@ -143,9 +143,9 @@ struct GgRole {
     static constexpr int BN = NARROW ? 32 : GgCfg<MODE, CG, F32>::BN;
     static constexpr int COLS = BN / (EPI / 4);
     static constexpr int kThreads = kIn ? 32 * (EPI + 3) : GgCfg<MODE, CG, F32>::kThreads;
-    // steps an accumulator takes; fewer for a gated unit in fp32, whose product of two sums doubles what they
-    // lose (1.9e-6 of the result with parts of 1024 terms, 6.5e-7 with 384, 4.5e-7 with 256; 65536 rows over 64
-    // experts of 1536 x 2048: 269, 368 and 384 us)
+    // steps an accumulator takes; fewer for a gated unit in fp32, which is a product of two sums and is to lose no
+    // more of sums of one sign than one product does (1.0e-6): 1.9e-6 of the result with parts of 1024 terms, 6.5e-7
+    // with 384, 4.5e-7 with 256; 65536 rows over 64 experts of 1536 x 2048: 269, 368 and 384 us
     static constexpr int kPart = kIn ? 1 << 30 : EP == kGgGlu && F32 ? 6 : kGgPartSteps;
     // (beside the inputs two steps a stage would leave room for two stages)
     static constexpr int KSUB = kIn ? 1 : GgCfg<MODE, CG, F32>::KSUB;
