@@ -104,6 +104,12 @@ inline int launch_persistent(K kernel, const P& p, int threads, int sms, cudaStr
 // 161; 256: 180 and 159; 1024: 425 and 300; of 2048 x 768, 192 rows: 82 and 88,
 // 256: 94 and 89).
 constexpr int kGgPairRows = 128, kGgPairRowsDw = 0, kGgPairRowsDwF32 = 256;
+// The gated unit and its gradient store more, and the unit in fp32 drains its accumulators more often.  64 experts of
+// 1536 x 2048 and 2048 x 768, at 128 / 144 / 192 / 512 rows, single and paired: to bf16 95 / 106 / 110 / 181 and 104 /
+// 106 / 107 / 151 us, the gradient 67 / 79 / 85 / 134 and 71 / 73 / 77 / 124; to fp32 at 384 / 512 / 1024 rows 165 /
+// 205 / 380 and 184 / 200 / 347.  (128 experts alike; of 16 the pairs' larger tiles leave some SMs without any until
+// 500 rows: at 192 34 and 36 us, gradient 30 and 32.)
+constexpr int kGgPairRowsGlu = 144, kGgPairRowsGluF32 = 512;
 
 inline bool gg_pairs(int R, int M, int E, int rows = kGgPairRows) { return M > 128 && (int64_t)R >= (int64_t)rows * E; }
 
