@@ -73,10 +73,9 @@ static int join_vectors(int H, int threads) {
 static unsigned join_threads(int H, int nv) { return (unsigned)ceil_div(ceil_div(H / 8, nv), 32) * 32; }
 
 template <bool OF32, int MT>
-static int run_join(const JoinParams& p, unsigned tokens, cudaStream_t st) {
+static int run_join(const JoinParams& p, cudaStream_t st) {
     const int nv = join_vectors(p.H, MT);
-    const unsigned x = join_threads(p.H, nv), y = tokens * x > MT ? MT / x : tokens;
-    const dim3 block(x, y), grid((unsigned)ceil_div(p.T, (int)y));
+    const unsigned block = join_threads(p.H, nv), grid = (unsigned)p.T;
     switch (nv) {
         case 1: return launch_pdl(join_kernel<OF32, 1, MT>, grid, block, 0, st, p);
         case 2: return launch_pdl(join_kernel<OF32, 2, MT>, grid, block, 0, st, p);
@@ -85,10 +84,13 @@ static int run_join(const JoinParams& p, unsigned tokens, cudaStream_t st) {
     }
 }
 
-// Few tokens: a block each, of as many threads as help; many: several a block.
+// A block a token, of up to 512 threads while there are few, else of 256: top-8, 4096 columns, by 512 and 256, 64
+// tokens 11.4 and 13.4 us, 152 12.3 and 13.4, 304 17.5 and 15.5, 2432 79 and 56 (up to 2048 columns both are the
+// same).  Several tokens a block are never faster: 65536 tokens, top-2, 64 to 1024 columns, one and eight: 57 and 59
+// us, 59 and 61, 65 and 67, 127 and 136, 248 and 262.
 template <bool OF32>
 static int run_join(const JoinParams& p, int sms, cudaStream_t st) {
-    return p.T < 2 * sms ? run_join<OF32, 512>(p, 1, st) : run_join<OF32, 256>(p, 8, st);
+    return p.T < 2 * sms ? run_join<OF32, 512>(p, st) : run_join<OF32, 256>(p, st);
 }
 
 // The backward pass: up to 512 threads a token of one vector each, beyond of

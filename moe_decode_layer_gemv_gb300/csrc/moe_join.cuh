@@ -114,23 +114,15 @@ __device__ __forceinline__ float warp_sum8(const float (&v)[8], int lane) {
     return c + __shfl_xor_sync(0xffffffffu, c, 1);
 }
 
-// Sums over the threads of one token (blockDim.x, whole warps) of N values;
-// every thread of the block takes part.  `buf`: blockDim.y * 32 * N floats,
-// free again after the next barrier of the block.
-template <int N>
-__device__ __forceinline__ void token_sum(float (&v)[N], float* buf) {
-#pragma unroll
-    for (int i = 0; i < N; ++i) v[i] = warp_sum(v[i]);
-    if (blockDim.x == 32) return;
+// The sum over a block (whole warps, every thread takes part).  `buf`: 32
+// floats, free again after the next barrier of the block.
+__device__ __forceinline__ float block_sum(float v, float* buf) {
+    v = warp_sum(v);
+    if (blockDim.x == 32) return v;
     const int warps = blockDim.x >> 5, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    float* mine = buf + threadIdx.y * 32 * N;
-    if (lane == 0) {
-#pragma unroll
-        for (int i = 0; i < N; ++i) mine[i * 32 + warp] = v[i];
-    }
+    if (lane == 0) buf[warp] = v;
     __syncthreads();
-#pragma unroll
-    for (int i = 0; i < N; ++i) v[i] = warp_sum(lane < warps ? mine[i * 32 + lane] : 0.0f);
+    return warp_sum(lane < warps ? buf[lane] : 0.0f);
 }
 
 // 1 / sqrt of a mean square with eps, and 0 where that is nothing (eps = 0 and
@@ -139,13 +131,13 @@ __device__ __forceinline__ void token_sum(float (&v)[N], float* buf) {
 __device__ __forceinline__ float norm_factor(float v) { return v == 0.0f ? 0.0f : 1.0f / sqrtf(v); }
 
 // The rows and weights of a token's routes; a row of -1 is none.
-__device__ __forceinline__ void token_routes(const JoinParams& p, int t, bool valid, int (&row)[MOE_MAX_TOPK],
+__device__ __forceinline__ void token_routes(const JoinParams& p, int t, int (&row)[MOE_MAX_TOPK],
                                              float (&w)[MOE_MAX_TOPK]) {
 #pragma unroll
     for (int j = 0; j < MOE_MAX_TOPK; ++j) {
         row[j] = -1;
         w[j] = 0.0f;
-        if (j < p.k && valid && p.o) {
+        if (j < p.k && p.o) {
             const size_t at = (size_t)t * p.k + j;
             row[j] = p.pos ? p.pos[at] : (int)at;
             w[j] = p.w ? p.w[at] : 1.0f;
@@ -181,39 +173,36 @@ __device__ __forceinline__ void gather8(const JoinParams& p, const int (&row)[MO
 }
 
 // ---------------------------------------------------------------- forward
-// A token per row of threads (blockDim.y tokens a block of up to MT threads); a
-// thread holds the columns of NV vectors of eight.  Bound by HBM: 8192 tokens,
-// top-8, 2048 columns, an fp32 stream: 79 us, 0.81 of the copy bandwidth.
+// A token a block of up to MT threads; a thread holds the columns of NV vectors
+// of eight.  Bound by HBM: 8192 tokens, top-8, 2048 columns, an fp32 stream: 79
+// us, 0.81 of the copy bandwidth.
 template <bool OF32, int NV, int MT>
 __global__ void __launch_bounds__(MT) join_kernel(JoinParams p) {
-    __shared__ float buf[2][MT];
+    __shared__ float buf[2][32];
     grid_dep_wait();
-    const int t = blockIdx.x * blockDim.y + threadIdx.y, nvec = p.H / 8;
-    const bool valid = t < p.T;
+    const int t = blockIdx.x, nvec = p.H / 8;
     int row[MOE_MAX_TOPK];
-    float w[MOE_MAX_TOPK], s[1] = {0.0f}, b[NV][8];
+    float w[MOE_MAX_TOPK], s = 0.0f, b[NV][8];
     Raw8 rx;  // (NV = 1: the stream's columns are on their way with the rows)
-    const bool ahead = NV == 1 && valid && (int)threadIdx.x < nvec;
-    if (ahead) rx = raw8(p.x, p.x_f32, t, p.H, threadIdx.x);
-    token_routes(p, t, valid, row, w);
+    if (NV == 1 && (int)threadIdx.x < nvec) rx = raw8(p.x, p.x_f32, t, p.H, threadIdx.x);
+    token_routes(p, t, row, w);
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
         const int v = threadIdx.x + i * blockDim.x;
-        if (!valid || v >= nvec) continue;
+        if (v >= nvec) continue;
         gather8<OF32, 8>(p, row, w, v, b[i]);
 #pragma unroll
-        for (int c = 0; c < 8; ++c) s[0] = fmaf(b[i][c], b[i][c], s[0]);
+        for (int c = 0; c < 8; ++c) s = fmaf(b[i][c], b[i][c], s);
     }
     float r = 1.0f;
     if (p.post) {
-        token_sum(s, buf[0]);
-        r = norm_factor(s[0] / (float)p.H + p.eps);
+        r = norm_factor(block_sum(s, buf[0]) / (float)p.H + p.eps);
     }
-    s[0] = 0.0f;
+    s = 0.0f;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
         const int v = threadIdx.x + i * blockDim.x;
-        if (!valid || v >= nvec) continue;
+        if (v >= nvec) continue;
         float f[8], x[8];
         if (p.post) {
             vector8(p.post, v, f);
@@ -231,15 +220,14 @@ __global__ void __launch_bounds__(MT) join_kernel(JoinParams p) {
         }
         if (p.y) put8(p.y, p.x_f32, t, p.H, v, b[i]);
 #pragma unroll
-        for (int c = 0; c < 8; ++c) s[0] = fmaf(b[i][c], b[i][c], s[0]);
+        for (int c = 0; c < 8; ++c) s = fmaf(b[i][c], b[i][c], s);
     }
     if (!p.pre) return;
-    token_sum(s, buf[1]);
-    r = norm_factor(s[0] / (float)p.H + p.eps);
+    r = norm_factor(block_sum(s, buf[1]) / (float)p.H + p.eps);
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
         const int v = threadIdx.x + i * blockDim.x;
-        if (!valid || v >= nvec) continue;
+        if (v >= nvec) continue;
         float f[8];
         vector8(p.pre, v, f);
 #pragma unroll
