@@ -378,8 +378,8 @@ int moe_grouped_gemm_dw(const uint16_t* dy, const uint16_t* x, const int32_t* of
  * made from them before they are rounded, and in fp32 loses no more of sums of
  * one sign than a plain product does (2^-20).  moe_grouped_gemm with w = down
  * completes the block.  R, offsets, segments and dev_status as in
- * moe_grouped_gemm; H and I multiples of 8 in [8, MOE_MAX_DIM].  An infinite
- * g gives what the formula gives (NaN at -infinity).
+ * moe_grouped_gemm; H and I multiples of 8 in [8, MOE_MAX_DIM].  h and gu may
+ * not overlap x or each other (refused).  An infinite g gives what the formula gives (NaN at -infinity).
  */
 int moe_grouped_glu(const uint16_t* x, const uint16_t* gate_up, const int32_t* offsets, int R, int H, int I, int E, int act,
                     void* h, int h_dtype, uint16_t* gu, int32_t* dev_status, void* stream);
@@ -393,9 +393,8 @@ int moe_grouped_glu(const uint16_t* x, const uint16_t* gate_up, const int32_t* o
  * dgu [R, 2I] and h [R, I] bf16.  The rest of the block's backward pass is
  * moe_grouped_gemm_dx(dgu, gate_up), moe_grouped_gemm_dw(dgu, x) and
  * moe_grouped_gemm_dw(dy, h): h is made again here, so that the forward pass
- * need not keep it.  dgu and h may not overlap gu or dy (dgu at gu's address is
- * refused).  dh
- * is one fp32 sum, whose additions (one for 16 terms) truncate: a sum of one
+ * need not keep it.  dgu and h may not overlap gu, dy or each other (refused).
+ * dh is one fp32 sum, whose additions (one for 16 terms) truncate: a sum of one
  * sign loses up to 7.4e-5 at H = 16384, 2 % of a bf16 result's half step.
  * Otherwise as moe_grouped_glu.
  */
@@ -416,8 +415,10 @@ int moe_grouped_glu_backward(const uint16_t* dy, const uint16_t* down, const uin
  * moe_group_by_expert sorts them; pos [T, k] int32 the row of each route
  * (pos[route_idx[i]] = i), -1 for one that was dropped; NULL: row t k + j.  w
  * [T, k] fp32 (NULL: ones), k <= MOE_MAX_TOPK; post, scale, pre [H] fp32
- * (scale NULL: the number scale_all); eps in [0, 1].  y [T, H] of x's type
- * (may alias x), n [T, H] (n_dtype).  o NULL: the norm of x alone (no y).
+ * (scale NULL: the number scale_all); eps in [0, 1].  y [T, H] of x's type, n
+ * [T, H] (n_dtype); one of them may be x itself (n only of x's type), other
+ * overlaps with x, o or each other are refused (but with o of the same type
+ * where pos is NULL and k = 1).  o NULL: the norm of x alone (no y).
  * Sums in fp32; n is made from y before it is rounded.  With eps = 0 the norm
  * of a row whose squares' mean is 0 in fp32 is zeros, as is its gradient (a
  * token without rows passes the stream on).  A row outside
@@ -436,8 +437,9 @@ int moe_combine_norm(const void* x, int x_dtype, const void* o, int o_dtype, con
  * (NULL: not wanted), dpost, dscale, dpre [H] fp32, each for the vector that
  * is given.  pos must name each row at most once, as a grouping's inverse
  * does; rows that it does not name are left as they were in d_o, and dw is 0
- * for dropped routes.  dx may alias dy; d_o may not overlap o (the same address
- * is refused).  The column sums
+ * for dropped routes.  dx may be dy itself (or y, or dn of y's type); other
+ * overlaps of dx and d_o with what is read or with each other are refused.  The
+ * column sums
  * (over tokens, fp32) are off by at most 2^-15 of their terms' magnitudes' sum,
  * however many there are, beside what the terms are; they
  * are joined in a fixed order (the same call gives the same bits) through the

@@ -934,7 +934,8 @@ def grouped_glu_backward(dy, down, gu, offsets, act="silu", dgu=None, h=None, st
 
     down [E,H,I] bf16, gu as grouped_glu kept it.  The block's other gradients
     are grouped_gemm_dx(dgu, gate_up, offsets), grouped_gemm_dw(dgu, x,
-    offsets) and grouped_gemm_dw(dy, h, offsets).  `dgu` may not overlap gu."""
+    offsets) and grouped_gemm_dw(dy, h, offsets).  `dgu` and `h` may not
+    overlap gu, dy or each other."""
     try:
         R, H = dy.shape
         E, _, I = down.shape
@@ -1035,7 +1036,7 @@ def combine_norm(x, o=None, pos=None, w=None, post=None, scale=1.0, pre=None, ep
     them; pos [T,k] int32, where the grouping put each route (route_idx's
     inverse), -1 for a dropped one, by default row t k + j; w [T,k] fp32,
     post and pre [H] fp32; scale a number or [H] fp32.  y and n are buffers to
-    be written (y may be x).  Without pre there is no n (None); without o it
+    be written (one of them may be x).  Without pre there is no n (None); without o it
     is x's norm alone, and y is x.  Detached."""
     xd = _x_dtype(x)
     i, T, H, R, k, vector, scale = _join_args(x, o, pos, w, post, scale, pre)
@@ -1085,7 +1086,7 @@ def combine_norm_backward(dy, dn, y, o=None, pos=None, w=None, post=None, scale=
     y is what combine_norm returned (x, without rows); the rest are its own
     arguments.  pos must name each row at most once, as a grouping's inverse
     does; rows it does not name are left as they were in `do` (undefined in a
-    new tensor).  dx may be dy.  workspace: uint8, allocated here by default."""
+    new tensor).  dx may be dy (or y).  workspace: uint8, allocated here by default."""
     _x_dtype(y)
     i, T, H, R, k, vector, scale = _join_args(y, o, pos, w, post, scale, pre)
     _is(y, "y", y.dtype, (T, H), i)

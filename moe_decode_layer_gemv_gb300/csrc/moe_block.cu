@@ -54,6 +54,12 @@ static int run_glu(GgParams& p, const void* gate_up, const void* x, int R, int I
                : launch_persistent<1>(gg_kernel<kGgFwd, 1, F32, kGgGlu>, p, GgCfg<kGgFwd, 1, F32>::kThreads, sms, st);
 }
 
+// What a token's row of `out` covers may be read for another token, unless `in` lies at the same place in the same type.
+static bool clash(const void* out, int out_dtype, const void* in, int in_dtype, size_t n) {
+    if (out == in && out_dtype == in_dtype) return false;
+    return overlap(out, n * (out_dtype == MOE_DT_F32 ? 4 : 2), in, n * (in_dtype == MOE_DT_F32 ? 4 : 2));
+}
+
 static int check_join(int T, int H, int R, int k, bool o, bool pre, int x_dtype, int o_dtype, int n_dtype, float eps) {
     if (T < 0 || T > MOE_MAX_ROWS || H < 8 || H > MOE_MAX_DIM || (H & 7)) return MOE_ERR_INVALID_ARG;
     if (!o && !pre) return MOE_ERR_INVALID_ARG;
@@ -257,6 +263,8 @@ int moe_grouped_glu(const uint16_t* x, const uint16_t* gate_up, const int32_t* o
     MOE_REQ(h);
     MOE_OPT(gu);
     MOE_OPT(dev_status);
+    const size_t rows = 2 * (size_t)R, hn = rows * I * (h_dtype == MOE_DT_F32 ? 2 : 1), gun = 2 * rows * I;
+    if (overlap(h, hn, gu, gun) || overlap(h, hn, x, rows * H) || overlap(gu, gun, x, rows * H)) return MOE_ERR_INVALID_ARG;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     const int sms = sm_count();
     if (sms < 2) return MOE_ERR_CUDA;
@@ -296,7 +304,11 @@ int moe_grouped_glu_backward(const uint16_t* dy, const uint16_t* down, const uin
     MOE_REQ(offsets);
     MOE_REQ(dgu);
     MOE_REQ(h);
-    if (dgu == gu) return MOE_ERR_INVALID_ARG;  // (gu is read ahead of what is written)
+    // (gu and dy are read ahead of what is written)
+    const size_t rows = 2 * (size_t)R, hn = rows * I, gun = 2 * hn;
+    if (overlap(dgu, gun, gu, gun) || overlap(dgu, gun, dy, rows * H) || overlap(h, hn, gu, gun) ||
+        overlap(h, hn, dy, rows * H) || overlap(h, hn, dgu, gun))
+        return MOE_ERR_INVALID_ARG;
     MOE_OPT(dev_status);
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     const int sms = sm_count();
@@ -329,6 +341,8 @@ int moe_combine_norm(const void* x, int x_dtype, const void* o, int o_dtype, con
     if (rc) return rc;
     if (o && !pos && (int64_t)T * k > R) return MOE_ERR_INVALID_ARG;
     if (T == 0) return MOE_OK;
+    JoinParams p;
+    memset(&p, 0, sizeof p);
     MOE_REQ(x);
     MOE_OPT(o);
     MOE_OPT(pos);
@@ -339,10 +353,18 @@ int moe_combine_norm(const void* x, int x_dtype, const void* o, int o_dtype, con
     if (o) MOE_REQ(y);
     if (pre) MOE_REQ(n);
     MOE_OPT(dev_status);
+    p.y = o ? y : nullptr;
+    p.n = pre ? n : nullptr;
+    const size_t th = (size_t)T * H, xn = th * (x_dtype == MOE_DT_F32 ? 4 : 2), nn = th * (n_dtype == MOE_DT_F32 ? 4 : 2);
+    const size_t on = (size_t)R * H * (o_dtype == MOE_DT_F32 ? 4 : 2);
+    if (clash(p.y, x_dtype, x, x_dtype, th) || clash(p.n, n_dtype, x, x_dtype, th) || overlap(p.y, xn, p.n, nn))
+        return MOE_ERR_INVALID_ARG;
+    const bool own = !pos && k == 1;  // (a token reads the row of its own place alone)
+    if ((!(own && p.y == o && x_dtype == o_dtype) && overlap(p.y, xn, o, on)) ||
+        (!(own && p.n == o && n_dtype == o_dtype) && overlap(p.n, nn, o, on)))
+        return MOE_ERR_INVALID_ARG;
     const int sms = sm_count();
     if (sms < 1) return MOE_ERR_CUDA;
-    JoinParams p;
-    memset(&p, 0, sizeof p);
     p.x = x;
     p.o = o;
     p.pos = pos;
@@ -350,8 +372,6 @@ int moe_combine_norm(const void* x, int x_dtype, const void* o, int o_dtype, con
     p.post = o ? post : nullptr;
     p.scale = o ? scale : nullptr;
     p.pre = pre;
-    p.y = o ? y : nullptr;
-    p.n = n;
     p.x_f32 = x_dtype == MOE_DT_F32;
     p.n_f32 = n_dtype == MOE_DT_F32;
     p.T = T;
@@ -408,7 +428,9 @@ int moe_combine_norm_backward(const void* dy, const void* dn, int n_dtype, const
     MOE_REQ(dx);
     MOE_OPT(o);
     if (o) MOE_REQ(d_o);
-    if (o && d_o == o && R > 0) return MOE_ERR_INVALID_ARG;  // (wide rows are read again behind the first writes)
+    const size_t th = (size_t)T * H, xn = th * (y_dtype == MOE_DT_F32 ? 4 : 2), nn = th * (n_dtype == MOE_DT_F32 ? 4 : 2);
+    const size_t on = (size_t)R * H * (o_dtype == MOE_DT_F32 ? 4 : 2);
+    if (overlap(d_o, on, o, on)) return MOE_ERR_INVALID_ARG;  // (wide rows are read again behind the first writes)
     MOE_OPT(pos);
     MOE_OPT(w);
     MOE_OPT(dw);
@@ -418,6 +440,13 @@ int moe_combine_norm_backward(const void* dy, const void* dn, int n_dtype, const
         if (!workspace || workspace_bytes < sizeof(float) * (size_t)grid * sums * H) return MOE_ERR_WORKSPACE;
         MOE_REQ(workspace);
     }
+    const void* const yr = pre ? y : nullptr;  // (what is read)
+    if (clash(dx, y_dtype, dy, y_dtype, th) || clash(dx, y_dtype, pre ? dn : nullptr, n_dtype, th) ||
+        clash(dx, y_dtype, yr, y_dtype, th) || overlap(dx, xn, o, on))
+        return MOE_ERR_INVALID_ARG;
+    if (o && (overlap(d_o, on, dy, xn) || overlap(d_o, on, pre ? dn : nullptr, nn) || overlap(d_o, on, yr, xn) ||
+              overlap(d_o, on, dx, xn)))
+        return MOE_ERR_INVALID_ARG;
     JoinParams p;
     memset(&p, 0, sizeof p);
     p.x = y;

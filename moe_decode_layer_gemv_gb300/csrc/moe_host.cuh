@@ -21,6 +21,12 @@ inline bool aligned32(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 
 
 inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
+// Whether a bytes at p and b bytes at q share any; tensors that are not there share none.
+inline bool overlap(const void* p, size_t a, const void* q, size_t b) {
+    const uintptr_t u = reinterpret_cast<uintptr_t>(p), v = reinterpret_cast<uintptr_t>(q);
+    return p && q && a && b && u < v + b && v < u + a;
+}
+
 #define MOE_REQ(p) \
     do {           \
         if (!(p) || !aligned16(p)) return MOE_ERR_INVALID_ARG; \
