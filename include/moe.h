@@ -64,7 +64,8 @@ typedef enum {
 #define MOE_DEV_BAD_EXPERT_ID 2  /* an expert id outside [0, E)              */
 #define MOE_DEV_DUP_EXPERT 4     /* one token lists the same expert twice    */
 #define MOE_DEV_NONFINITE 8      /* a router logit was NaN or infinite       */
-#define MOE_DEV_BAD_ROUTE 16     /* a route_idx entry outside [0, B*top_k)    */
+#define MOE_DEV_BAD_ROUTE 16     /* a route_idx entry outside [0, B*top_k), or */
+                                 /* a row (pos) outside [-1, R)                */
 #define MOE_DEV_RANGE 32         /* a router partial sum of the persistent     */
                                  /* decode kernel beyond +-2^21 (clamped: that */
                                  /* token's routing is not exact)              */
@@ -418,7 +419,8 @@ int moe_grouped_glu_backward(const uint16_t* dy, const uint16_t* down, const uin
  * (scale NULL: the number scale_all); eps in [0, 1].  y [T, H] of x's type, n
  * [T, H] (n_dtype); one of them may be x itself (n only of x's type), other
  * overlaps with x, o or each other are refused (but with o of the same type
- * where pos is NULL and k = 1).  o NULL: the norm of x alone (no y).
+ * where pos is NULL and k = 1).  o NULL: the norm of x alone (no y; pos, w,
+ * post and both scales are not read, in the backward pass neither).
  * Sums in fp32; n is made from y before it is rounded.  With eps = 0 the norm
  * of a row whose squares' mean is 0 in fp32 is zeros, as is its gradient (a
  * token without rows passes the stream on).  A row outside

@@ -970,8 +970,8 @@ def _join_args(x, o, pos, w, post, scale, pre):
     if o is None:
         if pre is None:
             raise ValueError("combine_norm needs rows (o), a norm (pre), or both")
-        if pos is not None or w is not None or post is not None:
-            raise ValueError("pos, w and post belong to rows: o is missing")
+        if pos is not None or w is not None or post is not None or isinstance(scale, torch.Tensor):
+            raise ValueError("pos, w, post and a vector of scales belong to rows: o is missing")
         R = k = 0
         scale = 1.0
     else:

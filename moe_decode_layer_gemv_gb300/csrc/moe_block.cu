@@ -378,7 +378,7 @@ int moe_combine_norm(const void* x, int x_dtype, const void* o, int o_dtype, con
     p.H = H;
     p.R = R;
     p.k = o ? k : 0;
-    p.scale_all = scale_all;
+    p.scale_all = o ? scale_all : 1.0f;
     p.eps = eps;
     p.status = dev_status;
     cudaStream_t st = static_cast<cudaStream_t>(stream);

@@ -51,3 +51,11 @@ def test_the_join(api):
                dict(dx=2 * MB + on - 16), dict(do=2 * MB), dict(do=2 * MB + 16), dict(do=2 * MB - on + 16), dict(do=MB),
                dict(do=3 * MB), dict(do=4 * MB), dict(do=5 * MB), dict(do=5 * MB + xn - 16)):
         assert back(**kw) == inv, kw
+
+
+def test_a_vector_of_scales_belongs_to_rows(api):
+    import torch
+    x, v = torch.zeros(4, 64), torch.zeros(64)
+    for call in (lambda **kw: api.combine_norm(x, pre=v, **kw), lambda **kw: api.combine_norm_backward(x, x, x, pre=v, **kw)):
+        with pytest.raises(ValueError, match="belong to rows"):
+            call(scale=v)

@@ -133,3 +133,15 @@ def test_column_sums_over_many_tokens(cuda_lib):
         off = float((t.double() / (T * w.flatten()) - 1).abs().max())
         assert off <= 2.0 ** -16 + 2.0 ** -20, (n, off)
     torch.cuda.empty_cache()
+
+
+def test_a_scale_without_rows_counts_for_nothing(cuda_lib):
+    """At the C entry, where the scale is a number beside the rows' pointer."""
+    x = torch.randn((5, 72), device=DEV)
+    pre = torch.ones(72, device=DEV)
+    want = cuda_lib.combine_norm(x, pre=pre, n_dtype=F32)[1]
+    n, st = torch.empty_like(x), torch.cuda.current_stream().cuda_stream
+    for s in (float("inf"), float("nan"), 2.0):
+        assert cuda_lib._lib.moe_combine_norm(x.data_ptr(), 0, None, 1, None, None, 5, 72, 0, 0, None, None, s, pre.data_ptr(),
+                                              1e-6, None, n.data_ptr(), 0, None, st) == 0
+        assert torch.equal(n, want)
