@@ -91,9 +91,10 @@ static int run_join(const JoinParams& p, cudaStream_t st) {
 }
 
 // A block a token, of up to 512 threads while there are few, else of 256: top-8, 4096 columns, by 512 and 256, 64
-// tokens 11.4 and 13.4 us, 152 12.3 and 13.4, 304 17.5 and 15.5, 2432 79 and 56 (up to 2048 columns both are the
-// same).  Several tokens a block are never faster: 65536 tokens, top-2, 64 to 1024 columns, one and eight: 57 and 59
-// us, 59 and 61, 65 and 67, 127 and 136, 248 and 262.
+// tokens 10.7 and 10.7 us, 152 10.7 and 12.8, 304 16.8 and 12.7, 2432 74 and 50 (up to 2048 columns both are the
+// same).  Several tokens a block gain next to nothing where rows are short and cost up to a tenth else: 65536 tokens,
+// top-2, 64 to 1024 columns, one and eight: 56 and 58 us, 58 and 58, 60 and 62, 123 and 134, 248 and 261 (16384 of 64
+// columns: 21 and 19).
 template <bool OF32>
 static int run_join(const JoinParams& p, int sms, cudaStream_t st) {
     return p.T < 2 * sms ? run_join<OF32, 512>(p, st) : run_join<OF32, 256>(p, st);
@@ -269,9 +270,9 @@ int moe_grouped_glu(const uint16_t* x, const uint16_t* gate_up, const int32_t* o
     const int sms = sm_count();
     if (sms < 2) return MOE_ERR_CUDA;
     const int f32 = h_dtype == MOE_DT_F32;
-    // a few rows.  Measured, by rows and by tiles, of 1536 x 2048 on experts of their own: 2 rows 11.4 and 16.5 us, 8
-    // 18.6 and 20.6, 12 22.7 and 26.8, 32 41 and 49; on one expert 2 rows 11.4 and 15.5, 12 14.5 and 14.5, 16 20.6 and
-    // 14.5; of 512 x 1024 on one expert 8 rows 11.4 and 12.4, 32 12.4 and 12.4
+    // a few rows.  Measured, by rows and by tiles, of 1536 x 2048 on experts of their own: 2 rows 10.8 and 14.8 us, 8
+    // 16.9 and 18.9, 12 21 and 23, 32 41 and 39; on one expert 2 rows 10.8 and 14.8, 12 14.8 and 14.8, 16 18.9 and
+    // 14.8; of 512 x 1024 on one expert 8 rows 10.8 and 12.8, 32 12.8 and 12.8
     if (R <= 32 && R * ceil_div(2 * I, 128) < sms) {
         const dim3 grid((unsigned)ceil_div(I, 8), (unsigned)R);
         return H <= 1024 ? launch_pdl(glu_gemv_kernel<4>, grid, 256, 0, st, x, gate_up, offsets, R, I, H, E, h, f32, gu, p.c0,
@@ -329,7 +330,7 @@ int moe_grouped_glu_backward(const uint16_t* dy, const uint16_t* down, const uin
     p.out = dgu;
     p.out2 = h;
     p.status = dev_status;
-    return gg_pairs(R, I, E, kGgPairRowsGlu)
+    return gg_pairs(R, I, E, kGgPairRowsGluBack)
                ? launch_persistent<2>(gg_kernel<kGgDx, 2, false, kGgGluBack>, p, GgRole<kGgDx, 2, false, kGgGluBack>::kThreads, sms, st)
                : launch_persistent<1>(gg_kernel<kGgDx, 1, false, kGgGluBack>, p, GgRole<kGgDx, 1, false, kGgGluBack>::kThreads, sms, st);
 }
@@ -546,8 +547,8 @@ int moe_orthogonalize(const void* g, int g_dtype, int E, int N, int K, int steps
     // (the blocks cover the padded X: its rows are G's columns where G is tall)
     const int rows = trans ? q.n : q.m, cols = trans ? q.m : q.n;
     // A block finds the norm first: with many blocks one serves four tiles.  Calls of one step, bf16 matrices of 2048 x
-    // 768, one tile a block and four: one matrix (384 tiles) 46 and 49 us, two 54 and 59, four 65 and 65, six 78 and
-    // 73, 16 161 and 146, 64 503 and 444
+    // 768, one tile a block and four: one matrix (384 tiles) 46 and 48 us, two 52 and 58, four 64 and 62, six 76 and
+    // 70, 16 158 and 142, 64 498 and 439
     const int64_t tiles = (int64_t)E * ceil_div(cols, 64) * ceil_div(rows, 64);
     const int strip = tiles >= 12 * sms ? 256 : 64;
     rc = launch_pdl(ns_convert_kernel, dim3((unsigned)ceil_div(cols, strip), (unsigned)ceil_div(rows, 64), (unsigned)E), 256, 0,

@@ -105,11 +105,12 @@ inline int launch_persistent(K kernel, const P& p, int threads, int sms, cudaStr
 // 256: 94 and 89).
 constexpr int kGgPairRows = 128, kGgPairRowsDw = 0, kGgPairRowsDwF32 = 256;
 // The gated unit and its gradient store more, and the unit in fp32 drains its accumulators more often.  64 experts of
-// 1536 x 2048 and 2048 x 768, at 128 / 144 / 192 / 512 rows, single and paired: to bf16 95 / 106 / 110 / 181 and 104 /
-// 106 / 107 / 151 us, the gradient 67 / 79 / 85 / 134 and 71 / 73 / 77 / 124; to fp32 at 384 / 512 / 1024 rows 165 /
-// 205 / 380 and 184 / 200 / 347.  (128 experts alike; of 16 the pairs' larger tiles leave some SMs without any until
-// 500 rows: at 192 34 and 36 us, gradient 30 and 32.)
-constexpr int kGgPairRowsGlu = 144, kGgPairRowsGluF32 = 512;
+// 1536 x 2048 and 2048 x 768, single and paired, at 128 / 192 / 256 / 512 rows: to bf16 85 / 99 / 107 / 177 and 99 / 103
+// / 107 / 150 us, to fp32 91 / 113 / 119 / 205 and 119 / 123 / 130 / 203 (1024 rows: 381 and 351), the gradient 56 / 76
+// / 80 / 130 and 60 / 66 / 72 / 117 (144 rows: 70 and 62).  128 experts are ahead a little earlier (144 rows to bf16:
+// 177 and 168), 16, whose larger tiles leave some SMs without any, later (512 rows to bf16: 58 and 56, uneven 58 and
+// 64; the gradient at 144 rows 33 and 31).
+constexpr int kGgPairRowsGlu = 256, kGgPairRowsGluF32 = 512, kGgPairRowsGluBack = 144;
 
 inline bool gg_pairs(int R, int M, int E, int rows = kGgPairRows) { return M > 128 && (int64_t)R >= (int64_t)rows * E; }
 

@@ -1,5 +1,6 @@
-"""The gated unit in fp32 where its tiles are those of CTA pairs (from 512 rows
-a segment on average), and one row to either side of where the pairs begin.
+"""The gated unit and its gradient where their tiles are those of CTA pairs (from
+256 rows a segment on average, 512 to fp32, 144 for the gradient), and one row
+to either side of where the pairs begin.
 Tolerances as in test_gpu_glu.py."""
 import pytest
 import torch
@@ -10,7 +11,7 @@ pytestmark = pytest.mark.gpu
 
 # ragged ends and empty segments, widths that end inside a tile, a contraction of several accumulators
 SHAPES = [([1500, 0, 700], 392, 1000), ([513, 600, 1201], 72, 264), ([1100, 1], 264, 4104), ([511], 136, 200), ([512], 136, 200),
-          ([143], 136, 200), ([144], 136, 200)]
+          ([143], 136, 200), ([144], 136, 200), ([255], 136, 200), ([256], 136, 200), ([200, 400, 0, 470], 392, 1000)]
 
 
 @pytest.mark.parametrize("act", glu.ACTS)
