@@ -174,7 +174,7 @@ __device__ __forceinline__ void gather8(const JoinParams& p, const int (&row)[MO
 
 // ---------------------------------------------------------------- forward
 // A token a block of up to MT threads; a thread holds the columns of NV vectors
-// of eight.  Bound by HBM: 8192 tokens, top-8, 2048 columns, an fp32 stream: 79
+// of eight.  Bound by HBM: 8192 tokens, top-8, 2048 columns, an fp32 stream: 78
 // us, 0.81 of the copy bandwidth.
 template <bool OF32, int NV, int MT>
 __global__ void __launch_bounds__(MT) join_kernel(JoinParams p) {
@@ -258,10 +258,12 @@ __global__ void __launch_bounds__(MT) join_kernel(JoinParams p) {
 // of o, two of the stream, dn) in registers to the token's end, all loads in
 // flight at once, and the next token's inputs are brought into L2 meanwhile.
 // Wider rows are read again, from L2.  8192 tokens, top-8, 2048 columns, norm
-// and scale behind the block: 162 us, 0.69 of the copy bandwidth (178 without
+// and scale behind the block: 161 us, 0.70 of the copy bandwidth (178 without
 // the prefetch, 169 with one of two tokens; 222 with the rows read again and
 // three blocks an SM; 206 with a ring of bulk copies feeding two groups of 256
 // threads from shared memory, whose 52 KB a token leave it three or four deep).
+// fp32 rows, eight of eight columns a thread, do not fit in the 128 registers
+// beside the rest (140 bytes of a thread are spilled): 281 us, 0.69 of it.
 constexpr int kJoinRun = 256;
 
 template <bool OF32, int NV, int MT>

@@ -29,12 +29,12 @@
 // (2^-14 on average at 16384 x 16384) out of fp16's subnormals; a single entry
 // of 1 is still far from 65504.
 //
-// 64 matrices of 2048 x 768 in bf16, five steps: 1489 us.  Norm 52 and
-// conversion 136 (HBM), then a step: X X^T 75 and A A 41 (384 tiles on 76 pairs
-// of CTAs: six rounds for five), B X 155 (1 GB of HBM traffic; the last two
-// less).  Groups of 6 to
-// 38 matrices, whose X stays in L2, take longer (3465 to 1908 us when all took
-// 1732): their products do not fill the GPU and cost 3 to 5 us each to start.
+// 64 matrices of 2048 x 768 in bf16, five steps: 1525 us.  Norm 53 and
+// conversion 136 (HBM), then a step: X X^T 76 and A A 40 (384 tiles on 76 pairs
+// of CTAs: six rounds for five), B X 155 (1 GB of HBM traffic; the last 136).
+// Groups of 6 to 38 matrices, whose X stays in L2, take longer (3465 to 1908 us
+// when all took 1732): their products do not fill the GPU and cost 3 to 5 us
+// each to start.
 #pragma once
 
 #include <math_constants.h>
